@@ -35,11 +35,16 @@ BD_ERR_TIMEOUT = 7
 BD_ERR_WORKSPACE = 8
 BD_ERR_DEVICE = 9
 BD_ERR_BOUNDS = 10
+BD_ERR_BAD_INDEX = 11
 
 BD_ALPHA_PER_MATRIX = 0
 BD_ALPHA_PER_ROW = 1
 BD_OUT_BF16 = 0
 BD_OUT_F32 = 1
+BD_OUT_E4M3 = 2
+BD_KV_BF16 = 0
+BD_KV_INT8 = 1
+BD_MAX_AXES = 4
 BD_MAX_VARIANTS = 64
 BD_NOALLOC_MAX_ROWS = 262144
 
@@ -55,6 +60,10 @@ EXPORTS = (
     "bd_cache_create", "bd_cache_destroy", "bd_cache_set_source", "bd_cache_step", "bd_cache_release",
     "bd_cache_get_stats", "bd_cache_query", "bd_cache_debug_fail_load", "bd_materialize",
     "bd_monosoup_workspace_size", "bd_monosoup_merge",
+    "bd_rms_norm_workspace_size", "bd_rms_norm",
+    "bd_rope_append_workspace_size", "bd_rope_append",
+    "bd_kv_read_workspace_size", "bd_kv_read",
+    "bd_attention_workspace_size", "bd_attention",
 )
 BD_CACHE_SERVED = 0
 BD_CACHE_BASE = 1
@@ -117,6 +126,17 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             "bd_monosoup_workspace_size": ([_i64, _i64, _i32, _i32, _i32], _sz),
             "bd_monosoup_merge": ([_vp, _vp, _i32, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _int, _vp, _sz, _vp],
                                   _int),
+            "bd_rms_norm_workspace_size": ([_i64, _i64], _sz),
+            "bd_rms_norm": ([_vp, _vp, _i64, _i64, _vp, _vp, _i32, _vp, ctypes.c_float, _vp, _vp, _int, _vp, _vp, _sz,
+                             _vp], _int),
+            "bd_rope_append_workspace_size": ([_i64], _sz),
+            "bd_rope_append": ([_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i32, _vp, _i32, _vp, _vp, _i64, _i32, _int,
+                                _vp, _vp, _vp, _i64, _vp, _sz, _vp], _int),
+            "bd_kv_read_workspace_size": ([_i64], _sz),
+            "bd_kv_read": ([_vp, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _sz, _vp], _int),
+            "bd_attention_workspace_size": ([_i64, _i64, _i32, _i32, _i32], _sz),
+            "bd_attention": ([_vp, _i64, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _i64, _vp, ctypes.c_float, _int, _vp,
+                              _vp, _vp, _sz, _vp], _int),
             "bd_cache_create": ([_vp, _sz, _sz, _i32, ctypes.c_double, _vp, ctypes.POINTER(_vp)], _int),
             "bd_cache_destroy": ([_vp], None),
             "bd_cache_set_source": ([_vp, _i32, _vp, _sz], _int),
@@ -280,6 +300,171 @@ def bd_monosoup_merge(w_base, w_ft_list, rank, l, power_iters, omega, w_merged, 
                                     _ptr(omega, "omega", (torch.float32,), allow_none=True),
                                     _ptr(w_merged, "w_merged", _BF16_LIKE + (torch.float32,)), out_dtype, wsp, wsn,
                                     _stream(stream)), "bd_monosoup_merge")
+
+
+def bd_rms_norm_workspace_size(T: int, d: int) -> int:
+    return int(load().bd_rms_norm_workspace_size(T, d))
+
+
+def bd_rms_norm(x, gain, eps, out, ws, residual=None, residual_out=None, scale=None, vid=None, gain_list=(),
+                stream=None) -> None:
+    """out = norm(x + residual) * gain (the gain of token t's variant, vid[t], out of gain_list); out bf16, fp32, or
+    e4m3 with scale [T]; residual_out (which may be residual itself) receives x + residual."""
+    T, d = x.shape
+    if tuple(gain.shape) != (d,) or tuple(out.shape) != (T, d):
+        raise ValueError("gain must have the shape [d] and out that of x")
+    for name, t in (("residual", residual), ("residual_out", residual_out)):
+        if t is not None and tuple(t.shape) != (T, d):
+            raise ValueError(f"{name} shape differs from x")
+    if scale is not None and scale.numel() != T:
+        raise ValueError("scale must have one value per row")
+    if vid is not None and vid.numel() != T:
+        raise ValueError("vid must have one id per row")
+    tab, V = None, 0
+    if vid is not None:
+        V = len(gain_list)
+        if any(tuple(t.shape) != (d,) for t in gain_list):
+            raise ValueError("every gain must have the shape [d]")
+        tab = (ctypes.c_void_p * max(V, 1))(*[_ptr(t, "gain", _BF16_LIKE) for t in gain_list])
+    out_dtype = _OUT_DTYPES.get(out.dtype)
+    if out_dtype is None:
+        raise ValueError(f"out has dtype {out.dtype}, expected bfloat16, float32 or float8_e4m3fn")
+    wsp, wsn = _ws(ws)
+    _check(load().bd_rms_norm(_ptr(x, "x", _BF16_LIKE), _ptr(residual, "residual", _BF16_LIKE, True), T, d,
+                              _ptr(gain, "gain", _BF16_LIKE), _ptr(vid, "vid", (torch.int32,), True), V,
+                              tab, float(eps), _ptr(residual_out, "residual_out", _BF16_LIKE, True),
+                              _ptr(out, "out"), out_dtype, _ptr(scale, "scale", (torch.float32,), True), wsp, wsn,
+                              _stream(stream)), "bd_rms_norm")
+
+
+_OUT_DTYPES = {torch.bfloat16: BD_OUT_BF16, torch.float32: BD_OUT_F32, torch.float8_e4m3fn: BD_OUT_E4M3}
+
+
+class _KvPages(ctypes.Structure):
+    """bd_kv_pages (include/bitdelta.h)."""
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("n_pages", _i64), ("page_size", _i32),
+                ("n_kv", _i32), ("head_dim", _i32), ("dtype", _i32)]
+
+
+class KvPages:
+    """One layer's paged KV cache: ``k`` and ``v`` [n_pages][n_kv][page_size][head_dim] as torch.bfloat16 or, with
+    ``k_scale`` and ``v_scale`` [n_pages][n_kv][page_size] fp32, as torch.int8 codes.  Keeps the tensors referenced."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+            raise ValueError("k and v must be [n_pages][n_kv][page_size][head_dim] of one dtype")
+        int8 = k.dtype == torch.int8
+        if int8 != (k_scale is not None) or int8 != (v_scale is not None):
+            raise ValueError("scales belong to an int8 cache, and to it alone")
+        dt = (torch.int8,) if int8 else _BF16_LIKE
+        for t in (k_scale, v_scale):
+            if t is not None and tuple(t.shape) != tuple(k.shape[:3]):
+                raise ValueError("scales must be [n_pages][n_kv][page_size]")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages, self.n_kv, self.page_size, self.head_dim = (int(n) for n in k.shape)
+        self._c = _KvPages(_ptr(k, "k", dt), _ptr(v, "v", dt), _ptr(k_scale, "k_scale", (torch.float32,), True),
+                           _ptr(v_scale, "v_scale", (torch.float32,), True), self.n_pages, self.page_size, self.n_kv,
+                           self.head_dim, BD_KV_INT8 if int8 else BD_KV_BF16)
+        self._addr = ctypes.addressof(self._c)
+
+
+def _heads(t, name: str, dim: int) -> tuple[int, int]:
+    """(pointer, row stride) of a bf16 [T][heads][dim] tensor whose rows may be apart."""
+    if t.dim() != 3 or t.shape[2] != dim or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name} must be [T][heads][{dim}] with contiguous rows")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    if t.dtype not in _BF16_LIKE:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected one of {_BF16_LIKE}")
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1] * dim)
+
+
+def bd_rope_append_workspace_size(T: int) -> int:
+    return int(load().bd_rope_append_workspace_size(T))
+
+
+def rope_table(n_pos: int, rot_dim: int, theta: float, device=None) -> torch.Tensor:
+    """[n_pos][rot_dim/2][2] fp32 (cos, sin) of p * theta^(-2i/rot_dim), formed in fp64."""
+    freq = theta ** (-torch.arange(rot_dim // 2, dtype=torch.float64) / (rot_dim // 2))
+    angle = torch.arange(n_pos, dtype=torch.float64)[:, None] * freq
+    return torch.stack([angle.cos(), angle.sin()], -1).float().contiguous().to(device or "cuda")
+
+
+def bd_rope_append(q, k, v, pos, rope_table, slot, cache: KvPages, q_out, ws, axis_of_pair=None,
+                   interleaved: bool = False, stream=None) -> None:
+    """Turns q -> q_out and k by their positions and writes k and v at ``slot`` of the cache.  q, k, v: [T][heads][dim],
+    rows may be apart (slices of one packed product); q = None skips q.  pos: [T] or [T][axes]; axis_of_pair: a host
+    sequence of rot_dim/2 axis numbers."""
+    T, n_kv, dim = k.shape
+    if n_kv != cache.n_kv or v.shape != k.shape or dim != cache.head_dim:
+        raise ValueError("k and v must be [T][n_kv][head_dim] of the cache")
+    kp, ks = _heads(k, "k", dim)
+    vp, vs = _heads(v, "v", dim)
+    qp = qs = op = os_ = n_q = 0
+    if q is not None:
+        n_q = q.shape[1]
+        if q.shape[0] != T or q_out.shape != q.shape:
+            raise ValueError("q and q_out must have T rows of the same heads")
+        qp, qs = _heads(q, "q", dim)
+        op, os_ = _heads(q_out, "q_out", dim)
+    n_axes = pos.shape[1] if pos is not None and pos.dim() == 2 else 1
+    if (pos is not None and pos.shape[0] != T) or slot.numel() != T:
+        raise ValueError("pos and slot must have one row per token")
+    n_pos, pairs = (rope_table.shape[0], rope_table.shape[1]) if rope_table is not None else (0, 0)
+    axes = None
+    if axis_of_pair is not None:
+        if len(axis_of_pair) != pairs:
+            raise ValueError("axis_of_pair must have rot_dim/2 entries")
+        axes = bytes(axis_of_pair)
+    if rope_table is not None and (rope_table.dim() != 3 or rope_table.shape[2] != 2):
+        raise ValueError("rope_table must be [n_pos][rot_dim/2][2]")
+    wsp, wsn = _ws(ws)
+    _check(load().bd_rope_append(qp, qs, kp, ks, vp, vs, T, n_q, _ptr(pos, "pos", (torch.int32,), True), n_axes, axes,
+                                 _ptr(rope_table, "rope_table", (torch.float32,), True), n_pos, 2 * pairs,
+                                 int(interleaved), _ptr(slot, "slot", (torch.int32,)), cache._addr, op, os_, wsp, wsn,
+                                 _stream(stream)), "bd_rope_append")
+
+
+def bd_kv_read_workspace_size(rows: int) -> int:
+    return int(load().bd_kv_read_workspace_size(rows))
+
+
+def bd_kv_read(cache: KvPages, page_table, kv_off, k_out, v_out, ws, stream=None) -> None:
+    """Gathers the sequences' tokens out of the pages into k_out, v_out [rows][n_kv][head_dim] bf16."""
+    n_seq, max_pages = page_table.shape
+    rows = k_out.shape[0]
+    if tuple(k_out.shape) != (rows, cache.n_kv, cache.head_dim) or v_out.shape != k_out.shape:
+        raise ValueError("k_out and v_out must be [rows][n_kv][head_dim]")
+    if kv_off.numel() != n_seq + 1:
+        raise ValueError("kv_off must have n_seq + 1 entries")
+    wsp, wsn = _ws(ws)
+    _check(load().bd_kv_read(cache._addr, _ptr(page_table, "page_table", (torch.int32,)), max_pages,
+                             _ptr(kv_off, "kv_off", (torch.int32,)), n_seq, rows, _ptr(k_out, "k_out", _BF16_LIKE),
+                             _ptr(v_out, "v_out", _BF16_LIKE), wsp, wsn, _stream(stream)), "bd_kv_read")
+
+
+def bd_attention_workspace_size(T: int, n_seq: int, n_q: int, n_kv: int, head_dim: int) -> int:
+    return int(load().bd_attention_workspace_size(T, n_seq, n_q, n_kv, head_dim))
+
+
+def bd_attention(q, q_off, cache: KvPages, page_table, kv_len, scale, max_new, out, ws, causal: bool = True, lse=None,
+                 stream=None) -> None:
+    """Attention of the new tokens q [T][n_q][head_dim] (rows may be apart) of n_seq sequences over the paged cache."""
+    T, n_q, dim = q.shape
+    n_seq, max_pages = page_table.shape
+    if dim != cache.head_dim or tuple(out.shape) != (T, n_q, dim):
+        raise ValueError("q and out must be [T][n_q][head_dim] of the cache")
+    if q_off.numel() != n_seq + 1 or kv_len.numel() != n_seq:
+        raise ValueError("q_off must have n_seq + 1 entries and kv_len n_seq")
+    if lse is not None and tuple(lse.shape) != (T, n_q):
+        raise ValueError("lse must be [T][n_q]")
+    qp, qs = _heads(q, "q", dim)
+    wsp, wsn = _ws(ws)
+    _check(load().bd_attention(qp, qs, _ptr(q_off, "q_off", (torch.int32,)), T, n_seq, int(max_new), n_q, cache._addr,
+                               _ptr(page_table, "page_table", (torch.int32,)), max_pages,
+                               _ptr(kv_len, "kv_len", (torch.int32,)), float(scale), int(causal),
+                               _ptr(out, "out", _BF16_LIKE), _ptr(lse, "lse", (torch.float32,), True), wsp, wsn,
+                               _stream(stream)), "bd_attention")
 
 
 def bd_route(vid, V, perm, seg_off, ws, stream=None) -> None:

@@ -98,6 +98,8 @@ const char* bd_status_string(bd_status s)
         case BD_ERR_WORKSPACE: return "BD_ERR_WORKSPACE: workspace missing or too small";
         case BD_ERR_DEVICE: return "BD_ERR_DEVICE: current device is not compute capability 10.3";
         case BD_ERR_BOUNDS: return "BD_ERR_BOUNDS: a kernel met an index outside its buffer (bounds-checked build)";
+        case BD_ERR_BAD_INDEX:
+            return "BD_ERR_BAD_INDEX: a position, slot, page, length or offset outside its range";
     }
     return "BD_ERR_UNKNOWN";
 }
@@ -460,13 +462,290 @@ bd_status bd_route(const int32_t* vid, int64_t T, int32_t V, int32_t* perm, int3
     return launched(bd::launch_route(vid, T, V, perm, seg_off, err_word(ws), static_cast<cudaStream_t>(stream)));
 }
 
+// ------------------------------------------------------------------ norm
+
+size_t bd_rms_norm_workspace_size(int64_t /*T*/, int64_t /*d*/) { return kWsHeader; }
+
+bd_status bd_rms_norm(const uint16_t* x, const uint16_t* residual, int64_t T, int64_t d, const uint16_t* gain,
+                      const int32_t* vid, int32_t V, const uint16_t* const* gain_tab, float eps,
+                      uint16_t* residual_out, void* out, int out_dtype, float* scale, void* ws, size_t ws_bytes,
+                      void* stream)
+{
+    BD_NVTX_RANGE("bd_rms_norm");
+    if (out_dtype != BD_OUT_BF16 && out_dtype != BD_OUT_F32 && out_dtype != BD_OUT_E4M3) return BD_ERR_INVALID_ARG;
+    if (V < 0 || V > BD_MAX_VARIANTS || !(eps >= 0.0f)) return BD_ERR_INVALID_ARG;
+    if (T < 0 || T > INT32_MAX || d <= 0 || d % 8 != 0) return BD_ERR_UNSUPPORTED_SHAPE;
+    if (bd_status s = check_ws(ws, ws_bytes, bd_rms_norm_workspace_size(T, d))) return s;
+    if (T == 0) return BD_OK;
+    if (!x || !gain || !out || (out_dtype == BD_OUT_E4M3) != (scale != nullptr)) return BD_ERR_INVALID_ARG;
+    if (vid && V > 0 && !gain_tab) return BD_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(residual_out, 16) || !aligned(gain, 16) ||
+        !aligned(out, 16) || !aligned(vid, 4) || !aligned(scale, 4))
+        return BD_ERR_MISALIGNED;
+    const size_t n = static_cast<size_t>(T) * static_cast<size_t>(d), g = static_cast<size_t>(d) * 2;
+    const size_t obytes = n * (out_dtype == BD_OUT_F32 ? 4 : out_dtype == BD_OUT_BF16 ? 2 : 1);
+    const size_t tbytes = static_cast<size_t>(T) * 4;
+    const auto written_over = [&](const void* in, size_t bytes) {  // by an output other than residual_out
+        return overlaps(out, obytes, in, bytes) || overlaps(scale, tbytes, in, bytes);
+    };
+    if (written_over(x, n * 2) || written_over(residual, n * 2) || written_over(residual_out, n * 2) ||
+        written_over(gain, g) || written_over(vid, tbytes) || written_over(ws, ws_bytes) ||
+        overlaps(out, obytes, scale, tbytes) || overlaps(residual_out, n * 2, gain, g) ||
+        overlaps(residual_out, n * 2, vid, tbytes) || overlaps(residual_out, n * 2, ws, ws_bytes) ||
+        (residual_out != x && overlaps(residual_out, n * 2, x, n * 2)) ||
+        (residual_out != residual && overlaps(residual_out, n * 2, residual, n * 2)))
+        return BD_ERR_INVALID_ARG;
+    bd::NormArgs a{};
+    if (vid) {
+        for (int32_t v = 0; v < V; ++v) {
+            if (!gain_tab[v]) return BD_ERR_INVALID_ARG;
+            if (!aligned(gain_tab[v], 16)) return BD_ERR_MISALIGNED;
+            if (written_over(gain_tab[v], g) || overlaps(residual_out, n * 2, gain_tab[v], g))
+                return BD_ERR_INVALID_ARG;
+            a.gains[v] = gain_tab[v];
+        }
+    }
+    int sms = 0;
+    if (bd_status s = device_info(&sms)) return s;
+    a.x = x;
+    a.residual = residual;
+    a.residual_out = residual_out;
+    a.gain = gain;
+    a.vid = vid;
+    a.V = V;
+    a.T = T;
+    a.d = d;
+    a.eps = eps;
+    a.out = out;
+    a.out_dtype = out_dtype;
+    a.scale = scale;
+    a.err = err_word(ws);
+    return launched(bd::launch_rms_norm(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ paged KV cache
+
+// A cache's shape, pointers and alignment; *out is what the kernels take.
+static bd_status check_kv_pages(const bd_kv_pages* c, bd::KvPages* out)
+{
+    if (!c) return BD_ERR_INVALID_ARG;
+    if (c->dtype != BD_KV_BF16 && c->dtype != BD_KV_INT8) return BD_ERR_INVALID_ARG;
+    int shift = 4;
+    while (shift < 7 && (1 << shift) < c->page_size) ++shift;
+    if ((1 << shift) != c->page_size || (c->head_dim != 64 && c->head_dim != 128) || c->n_kv < 1 || c->n_kv > 1024 ||
+        c->n_pages < 0 || c->n_pages > INT32_MAX / c->n_kv || c->n_pages > INT32_MAX / c->page_size)
+        return BD_ERR_UNSUPPORTED_SHAPE;
+    const bool int8 = c->dtype == BD_KV_INT8;
+    if (!c->k || !c->v || (int8 && (!c->k_scale || !c->v_scale))) return BD_ERR_INVALID_ARG;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || (int8 && (!aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))))
+        return BD_ERR_MISALIGNED;
+    *out = bd::KvPages{c->k, c->v, int8 ? c->k_scale : nullptr, int8 ? c->v_scale : nullptr, c->n_pages, c->page_size,
+                       shift, c->n_kv, c->head_dim, int8 ? 1 : 0};
+    return BD_OK;
+}
+
+static size_t kv_vectors(const bd::KvPages& c)
+{
+    return static_cast<size_t>(c.n_pages) * static_cast<size_t>(c.n_kv) * static_cast<size_t>(c.page);
+}
+
+// Whether [p, p + n) meets any buffer of the cache.
+static bool meets_cache(const bd::KvPages& c, const void* p, size_t n)
+{
+    const size_t vec = kv_vectors(c), bytes = vec * static_cast<size_t>(c.dim) * (c.int8 ? 1 : 2);
+    return overlaps(p, n, c.k, bytes) || overlaps(p, n, c.v, bytes) || overlaps(p, n, c.k_scale, vec * 4) ||
+           overlaps(p, n, c.v_scale, vec * 4);
+}
+
+// Bytes from the first to the last element of T strided rows.
+static size_t span_bytes(int64_t T, int64_t stride, int64_t row)
+{
+    return (static_cast<size_t>(T - 1) * static_cast<size_t>(stride) + static_cast<size_t>(row)) * 2;
+}
+
+size_t bd_rope_append_workspace_size(int64_t /*T*/) { return kWsHeader; }
+
+bd_status bd_rope_append(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                         int64_t v_stride, int64_t T, int32_t n_q, const int32_t* pos, int32_t n_axes,
+                         const uint8_t* axis_of_pair, const float* rope_tab, int64_t n_pos, int32_t rot_dim,
+                         int interleaved, const int32_t* slot, const bd_kv_pages* cache, uint16_t* q_out,
+                         int64_t q_out_stride, void* ws, size_t ws_bytes, void* stream)
+{
+    BD_NVTX_RANGE("bd_rope_append");
+    bd::RopeArgs a{};
+    if (bd_status s = check_kv_pages(cache, &a.cache)) return s;
+    const int64_t dim = a.cache.dim, kv_row = a.cache.n_kv * dim, q_row = n_q * dim;
+    if (T < 0 || T > INT32_MAX || n_q < 0 || n_q > 65536 || rot_dim < 0 || rot_dim % 16 != 0 || rot_dim > dim)
+        return BD_ERR_UNSUPPORTED_SHAPE;
+    if (k_stride < kv_row || v_stride < kv_row || k_stride % 8 || v_stride % 8 ||
+        (n_q > 0 && (q_stride < q_row || q_out_stride < q_row || q_stride % 8 || q_out_stride % 8)))
+        return BD_ERR_UNSUPPORTED_SHAPE;
+    if (n_axes < 1 || n_axes > BD_MAX_AXES) return BD_ERR_INVALID_ARG;
+    if (bd_status s = check_ws(ws, ws_bytes, bd_rope_append_workspace_size(T))) return s;
+    for (int i = 0; axis_of_pair && i < rot_dim / 2; ++i) {
+        if (axis_of_pair[i] >= n_axes) return BD_ERR_INVALID_ARG;
+        a.axis_of_pair[i] = axis_of_pair[i];
+    }
+    if (T == 0) return BD_OK;
+    if (!k || !v || !slot || (n_q > 0 && (!q || !q_out)) || (rot_dim > 0 && (!pos || !rope_tab || n_pos < 1)))
+        return BD_ERR_INVALID_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16) || (n_q > 0 && (!aligned(q, 16) || !aligned(q_out, 16))) ||
+        !aligned(rope_tab, 16) || !aligned(pos, 4) || !aligned(slot, 4))
+        return BD_ERR_MISALIGNED;
+    const size_t tbytes = static_cast<size_t>(T) * 4;
+    const size_t kb = span_bytes(T, k_stride, kv_row), vb = span_bytes(T, v_stride, kv_row);
+    const size_t pb = rot_dim > 0 ? tbytes * n_axes : 0;
+    const size_t rb = rot_dim > 0 ? static_cast<size_t>(n_pos) * rot_dim * 4 : 0;
+    if (meets_cache(a.cache, k, kb) || meets_cache(a.cache, v, vb) || meets_cache(a.cache, slot, tbytes) ||
+        meets_cache(a.cache, ws, ws_bytes) || meets_cache(a.cache, pos, pb) || meets_cache(a.cache, rope_tab, rb))
+        return BD_ERR_INVALID_ARG;
+    if (n_q > 0) {
+        const size_t qb = span_bytes(T, q_stride, q_row), ob = span_bytes(T, q_out_stride, q_row);
+        const bool in_place = q_out == q && q_out_stride == q_stride;
+        // in place, k and v may lie between q's rows (slices of one product): their columns are apart
+        const auto apart = [&](const uint16_t* p, int64_t stride) {
+            if (stride != q_out_stride) return false;
+            const int64_t d = reinterpret_cast<intptr_t>(p) - reinterpret_cast<intptr_t>(q_out);
+            const int64_t row = stride * 2, at = ((d % row) + row) % row;
+            return at >= q_row * 2 && at + kv_row * 2 <= row;
+        };
+        if (meets_cache(a.cache, q, qb) || meets_cache(a.cache, q_out, ob) || overlaps(q_out, ob, slot, tbytes) ||
+            overlaps(q_out, ob, ws, ws_bytes) || overlaps(q_out, ob, pos, pb) || overlaps(q_out, ob, rope_tab, rb) ||
+            (overlaps(q_out, ob, k, kb) && !apart(k, k_stride)) || (overlaps(q_out, ob, v, vb) && !apart(v, v_stride)) ||
+            (!in_place && overlaps(q_out, ob, q, qb)))
+            return BD_ERR_INVALID_ARG;
+    }
+    int sms = 0;
+    if (bd_status s = device_info(&sms)) return s;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_out_stride = q_out_stride;
+    a.T = T;
+    a.n_q = n_q;
+    a.pos = pos;
+    a.n_axes = n_axes;
+    a.tab = rope_tab;
+    a.n_pos = n_pos;
+    a.rot = rot_dim;
+    a.interleaved = interleaved != 0;
+    a.slot = slot;
+    a.q_out = q_out;
+    a.err = err_word(ws);
+    return launched(bd::launch_rope_append(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t bd_kv_read_workspace_size(int64_t /*rows*/) { return kWsHeader; }
+
+bd_status bd_kv_read(const bd_kv_pages* cache, const int32_t* page_table, int64_t max_pages, const int32_t* kv_off,
+                     int64_t n_seq, int64_t rows, uint16_t* k_out, uint16_t* v_out, void* ws, size_t ws_bytes,
+                     void* stream)
+{
+    BD_NVTX_RANGE("bd_kv_read");
+    bd::KvReadArgs a{};
+    if (bd_status s = check_kv_pages(cache, &a.cache)) return s;
+    if (n_seq < 0 || n_seq > INT32_MAX || rows < 0 || rows > INT32_MAX || max_pages < 0 ||
+        max_pages > INT32_MAX / a.cache.page)
+        return BD_ERR_UNSUPPORTED_SHAPE;
+    if (bd_status s = check_ws(ws, ws_bytes, bd_kv_read_workspace_size(rows))) return s;
+    if (n_seq == 0 || rows == 0) return BD_OK;
+    if (!page_table || !kv_off || !k_out || !v_out) return BD_ERR_INVALID_ARG;
+    if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(page_table, 4) || !aligned(kv_off, 4))
+        return BD_ERR_MISALIGNED;
+    const size_t ob = static_cast<size_t>(rows) * static_cast<size_t>(a.cache.n_kv) * a.cache.dim * 2;
+    const size_t pb = static_cast<size_t>(n_seq) * static_cast<size_t>(max_pages) * 4;
+    const size_t fb = static_cast<size_t>(n_seq + 1) * 4;
+    for (const void* o : {static_cast<const void*>(k_out), static_cast<const void*>(v_out)})
+        if (meets_cache(a.cache, o, ob) || overlaps(o, ob, page_table, pb) || overlaps(o, ob, kv_off, fb) ||
+            overlaps(o, ob, ws, ws_bytes))
+            return BD_ERR_INVALID_ARG;
+    if (overlaps(k_out, ob, v_out, ob)) return BD_ERR_INVALID_ARG;
+    int sms = 0;
+    if (bd_status s = device_info(&sms)) return s;
+    a.table = page_table;
+    a.max_pages = max_pages;
+    a.kv_off = kv_off;
+    a.n_seq = n_seq;
+    a.rows = rows;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.err = err_word(ws);
+    return launched(bd::launch_kv_read(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ attention
+
+size_t bd_attention_workspace_size(int64_t T, int64_t n_seq, int32_t n_q, int32_t n_kv, int32_t head_dim)
+{
+    if (T < 0 || n_seq < 0 || n_kv < 1 || n_q < n_kv || (head_dim != 64 && head_dim != 128)) return kWsHeader;
+    return bd::attention_workspace_size(T, n_seq, n_q, n_kv, head_dim);
+}
+
+bd_status bd_attention(const uint16_t* q, int64_t q_stride, const int32_t* q_off, int64_t T, int64_t n_seq,
+                       int64_t max_new, int32_t n_q, const bd_kv_pages* cache, const int32_t* page_table,
+                       int64_t max_pages, const int32_t* kv_len, float scale, int causal, uint16_t* out, float* lse,
+                       void* ws, size_t ws_bytes, void* stream)
+{
+    BD_NVTX_RANGE("bd_attention");
+    bd::AttentionArgs a{};
+    if (bd_status s = check_kv_pages(cache, &a.cache)) return s;
+    if (n_q < 1 || n_q % a.cache.n_kv != 0 || n_q > 65536 || T < 0 || n_seq < 0 || max_new < 0 || max_pages < 0 ||
+        n_seq > INT32_MAX / 2 || max_pages > INT32_MAX / a.cache.page || T > INT32_MAX / n_q)
+        return BD_ERR_UNSUPPORTED_SHAPE;
+    const int64_t row = static_cast<int64_t>(n_q) * a.cache.dim;
+    if (q_stride < row || q_stride % 8) return BD_ERR_UNSUPPORTED_SHAPE;
+    if (!(scale - scale == 0.0f)) return BD_ERR_INVALID_ARG;  // not finite
+    if (bd_status s = check_ws(ws, ws_bytes, bd_attention_workspace_size(T, n_seq, n_q, a.cache.n_kv, a.cache.dim)))
+        return s;
+    if (T == 0 || n_seq == 0) return BD_OK;
+    if (!q || !q_off || !kv_len || !out || (!page_table && max_pages > 0)) return BD_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(q_off, 4) || !aligned(kv_len, 4) || !aligned(page_table, 4) ||
+        !aligned(lse, 4))
+        return BD_ERR_MISALIGNED;
+    const size_t qb = span_bytes(T, q_stride, row);
+    const size_t ob = static_cast<size_t>(T) * static_cast<size_t>(row) * 2, lb = static_cast<size_t>(T) * n_q * 4;
+    const size_t pb = static_cast<size_t>(n_seq) * static_cast<size_t>(max_pages) * 4;
+    const size_t fb = static_cast<size_t>(n_seq + 1) * 4;
+    const auto written_over = [&](const void* in, size_t n) { return overlaps(out, ob, in, n) || overlaps(lse, lb, in, n); };
+    if (written_over(q, qb) || written_over(q_off, fb) || written_over(kv_len, fb - 4) || written_over(page_table, pb) ||
+        written_over(ws, ws_bytes) || meets_cache(a.cache, out, ob) || meets_cache(a.cache, lse, lb) ||
+        meets_cache(a.cache, ws, ws_bytes) || overlaps(out, ob, lse, lb) || overlaps(ws, ws_bytes, q, qb) ||
+        overlaps(ws, ws_bytes, q_off, fb) || overlaps(ws, ws_bytes, kv_len, fb - 4) ||
+        overlaps(ws, ws_bytes, page_table, pb))
+        return BD_ERR_INVALID_ARG;
+    int sms = 0;
+    if (bd_status s = device_info(&sms)) return s;
+    a.q = q;
+    a.q_stride = q_stride;
+    a.q_off = q_off;
+    a.T = T;
+    a.n_seq = n_seq;
+    a.max_new = max_new;
+    a.n_q = n_q;
+    a.table = page_table;
+    a.max_pages = max_pages;
+    a.kv_len = kv_len;
+    a.scale = scale;
+    a.causal = causal != 0;
+    a.out = out;
+    a.lse = lse;
+    a.ws = ws;
+    a.err = err_word(ws);
+    a.sm_count = sms;
+    return launched(bd::launch_attention(a, static_cast<cudaStream_t>(stream)));
+}
+
 // ------------------------------------------------------------------ async errors
 
 int bd_debug_bounds_check(uint32_t* kernels)
 {
     const uint32_t f = bd::bounds_take_compress() | bd::bounds_take_skinny() | bd::bounds_take_multi() |
                        bd::bounds_take_prefill() | bd::bounds_take_route() | bd::bounds_take_materialize() |
-                       bd::bounds_take_monosoup();
+                       bd::bounds_take_monosoup() | bd::bounds_take_norm() | bd::bounds_take_kv() |
+                       bd::bounds_take_attention();
     if (kernels) *kernels = f;
     if (f == ~0u) return BD_ERR_CUDA;
     return f ? BD_ERR_BOUNDS : BD_OK;
@@ -495,6 +774,7 @@ bd_status bd_check_async(void* ws, void* stream)
     if (const int cs_ = bd::cuda_status(cudaStreamSynchronize(st))) return static_cast<bd_status>(cs_);
     if (word & (1u << BD_ERR_TIMEOUT)) return BD_ERR_TIMEOUT;
     if (word & (1u << BD_ERR_BAD_VARIANT)) return BD_ERR_BAD_VARIANT;
+    if (word & (1u << BD_ERR_BAD_INDEX)) return BD_ERR_BAD_INDEX;
     if (word & (1u << BD_ERR_NONFINITE)) return BD_ERR_NONFINITE;
     return BD_ERR_CUDA;
 }

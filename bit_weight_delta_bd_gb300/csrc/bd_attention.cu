@@ -1,0 +1,771 @@
+// Attention over the paged KV cache: the plan, the kernel for few query rows
+// per sequence (decode steps), and the join of partial results.
+//
+//   o_r = sum_j p_rj v_j / sum_j p_rj,   p_rj = exp2(c q_r . k_j - m_r),  c = scale log2(e)
+//
+// in one pass over the keys with a running maximum m_r: where a tile raises
+// it, the sums so far are multiplied by exp2(m_old - m_new).
+//
+// The decode kernel is bound by the cache's bytes.  One thread of a producer
+// warp's tile keeps a ring of stages (64 keys: K, V, scales) filled by TMA,
+// one box per page; four consumer warps take 16 keys of each stage each, with
+// a running maximum, denominator and 16 x dim sum of their own, so that
+// nothing is exchanged between warps until an item ends.  Rows are the 16
+// rows of m16n8k16 (query heads that share a kv head), keys its columns.
+//
+// Int8.  Codes become bf16 exactly: with r the byte, 0x4300 | (r & 0x7f) is
+// 128 + (r & 0x7f) and 0x4300 | (r & 0x80) is 128 or 256, and their
+// difference is the code; one byte permute, two logic operations and one
+// packed subtraction for two codes.  K's scale multiplies the fp32 score, V's
+// the fp32 probability.
+#include "bd_attention.cuh"
+
+#include <climits>
+
+#include "bd_tma.h"
+
+namespace bd {
+namespace {
+
+// ------------------------------------------------------------------------------- plan
+
+constexpr int kPlanThreads = 1024;
+
+// Exclusive scan over the block; *total gets the sum.
+__device__ __forceinline__ int block_scan(int v, int* red, int* total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) red[warp] = x;
+    __syncthreads();
+    int w = lane < kPlanThreads / 32 ? red[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
+    }
+    *total = __shfl_sync(0xffffffffu, w, 31);
+    const int base = warp ? __shfl_sync(0xffffffffu, w, warp - 1) : 0;
+    return base + x - v;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_constant__ AttnParams p)
+{
+    __shared__ int red[32];
+    const AttentionArgs& a = p.a;
+    const int n_seq = static_cast<int>(a.n_seq);
+    grid_launch_dependents();
+    grid_dependency_wait();
+
+    int items = 0;
+    for (int s0 = 0; s0 < n_seq; s0 += kPlanThreads) {
+        const int s = s0 + threadIdx.x;
+        int n = 0;
+        if (s < n_seq) {
+            const AttnSeq q = attn_seq(a, s, true);
+            n = static_cast<int>((static_cast<int64_t>(q.n_new) * p.G + p.mb - 1) / p.mb);
+        }
+        int total;
+        const int off = block_scan(n, red, &total);
+        if (s < n_seq) p.item_off[s] = items + off;
+        items += total;
+    }
+    __syncthreads();
+    // offsets that run backwards in a bad q_off could make more items than there is room for
+    const int64_t room = (a.T * p.G + p.mb - 1) / p.mb + a.n_seq;
+    if (items > room) items = static_cast<int>(room);
+
+    int tiles = 0;
+    for (int i0 = 0; i0 < items; i0 += kPlanThreads) {
+        const int i = i0 + threadIdx.x;
+        AttnItem it{};
+        if (i < items) {
+            int lo = 0, hi = n_seq;  // the last s with item_off[s] <= i
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (p.item_off[mid] <= i) lo = mid;
+                else hi = mid;
+            }
+            const AttnSeq q = attn_seq(a, lo, false);
+            it.seq = lo;
+            it.row0 = (i - p.item_off[lo]) * p.mb;
+            int64_t last = static_cast<int64_t>(it.row0) + p.mb - 1;
+            const int64_t rows = static_cast<int64_t>(q.n_new) * p.G;
+            if (last >= rows) last = rows - 1;
+            const int end = attn_seen(q, static_cast<int>(last / p.G), a.causal);
+            it.tiles = end > 0 ? (end + p.tile - 1) / p.tile : 1;
+        }
+        int total;
+        it.before = tiles + block_scan(it.tiles, red, &total);
+        if (i < items && bd_in(kBkAttnPlan, i, room)) p.items[i] = it;
+        tiles += total;
+    }
+    if (threadIdx.x == 0) *p.head = AttnHeader{items, tiles};
+}
+
+// ------------------------------------------------------------------------------- decode kernel
+
+constexpr int kMmaTile = 64;     // keys of a stage
+constexpr int kMmaRows = 16;     // rows of an item
+constexpr int kMmaConsumers = 4;
+constexpr int kMmaThreads = 32 * (kMmaConsumers + 1);
+constexpr int kMmaMaxStages = 8;
+
+struct MmaParams {
+    CUtensorMap k_map, v_map;  // [n_pages * n_kv][page][dim], box (128 bytes or a row) x min(page, 64)
+    AttnParams p;
+    int stages;
+};
+
+template <int DIM, bool INT8>
+struct MmaShape {
+    static constexpr int kRowBytes = DIM * (INT8 ? 1 : 2);
+    static constexpr int kBoxBytes = kRowBytes < 128 ? kRowBytes : 128;  // bytes of a row in one box
+    static constexpr int kHalves = kRowBytes / kBoxBytes;
+    static constexpr int kHalfBytes = kMmaTile * kBoxBytes;
+    static constexpr int kTileBytes = kMmaTile * kRowBytes;               // K (or V) of a stage
+    static constexpr int kStageBytes = 2 * kTileBytes + (INT8 ? 1024 : 0);  // stages stay 1024-byte aligned
+    static constexpr int kBufBytes = kMmaRows * DIM * 4;                  // the block's sum of an item
+};
+
+struct MmaShared {
+    uint64_t full[kMmaMaxStages];
+    uint64_t empty[kMmaMaxStages];
+    float m[kMmaConsumers][kMmaRows];
+    float l[kMmaConsumers][kMmaRows];
+    volatile int abort;
+};
+
+__device__ __forceinline__ bool attn_wait(volatile int* abort_flag, uint64_t* bar, uint32_t parity, uint32_t* err)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort_flag) return false;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            *abort_flag = 1;
+            raise_error(err, kErrTimeout);
+            return false;
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// Two int8 codes, the bytes that `sel` picks from r, as a pair of bf16.
+__device__ __forceinline__ uint32_t codes_bf16x2(uint32_t r, uint32_t sel)
+{
+    const uint32_t x = __byte_perm(r, 0x43434343u, sel);
+    const uint32_t hi = x & 0xFF7FFF7Fu, lo = x & 0xFF80FF80u;
+    const __nv_bfloat162 d =
+        __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&hi), *reinterpret_cast<const __nv_bfloat162*>(&lo));
+    return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
+{
+    const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kMmaConsumers) : "memory"); }
+
+// Byte offset of 16-byte chunk c of row t in a box of 128- or 64-byte rows
+// (TMA's 128- or 64-byte swizzle).
+template <int BOX_BYTES>
+__device__ __forceinline__ uint32_t swizzled(int t, int c)
+{
+    if constexpr (BOX_BYTES == 128)
+        return static_cast<uint32_t>(t * 128 + ((c ^ (t & 7)) << 4));
+    else
+        return static_cast<uint32_t>(t * 64 + ((c ^ ((t >> 1) & 3)) << 4));
+}
+
+template <int DIM, bool INT8>
+__global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_constant__ MmaParams mp)
+{
+    using S = MmaShape<DIM, INT8>;
+    constexpr int kSteps = DIM / 16;  // MMA steps of q . k, and pairs of 8-dim tiles of the output
+    extern __shared__ uint8_t dyn_raw[];
+    __shared__ MmaShared sh;
+    uint8_t* ring = dyn_raw + ((1024u - (smem_u32(dyn_raw) & 1023u)) & 1023u);
+    float* buf = reinterpret_cast<float*>(ring + static_cast<size_t>(mp.stages) * S::kStageBytes);
+
+    const AttnParams& p = mp.p;
+    const AttentionArgs& a = p.a;
+    const KvPages& cache = a.cache;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    grid_launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < mp.stages; ++s) {
+            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.empty[s], kMmaConsumers);
+        }
+        sh.abort = 0;
+        fence_mbarrier_init();
+    }
+    __syncthreads();
+    grid_dependency_wait();
+
+    const AttnHeader head = *p.head;
+    const int n_kv = cache.n_kv;
+    const int64_t units = static_cast<int64_t>(head.tiles) * n_kv;
+    const int active = attn_active(units, p.blocks);
+    const int c = blockIdx.x;
+    if (c >= active) return;
+    const int64_t u_end = attn_first(units, active, c + 1);
+    int64_t u = attn_first(units, active, c);
+    int item = attn_find_item(p.items, head.n_items, n_kv, u);
+    int stage = 0;
+    uint32_t phase = 0;
+
+    if (warp == kMmaConsumers) {
+        // ------------------------------------------------------------ producer warp
+        const int box_rows = cache.page < kMmaTile ? cache.page : kMmaTile;
+        const int pages_per_tile = kMmaTile / box_rows;
+        while (u < u_end) {
+            const AttnItem it = p.items[item];
+            const int64_t rel = u - static_cast<int64_t>(it.before) * n_kv;
+            const int h = static_cast<int>(rel / it.tiles);
+            const int t0 = static_cast<int>(rel - static_cast<int64_t>(h) * it.tiles);
+            const int64_t left = u_end - u;
+            const int t1 = left < it.tiles - t0 ? t0 + static_cast<int>(left) : it.tiles;
+            const AttnSeq sq = attn_seq(a, it.seq, false);
+            const int32_t* table = a.table + static_cast<int64_t>(it.seq) * a.max_pages;
+            const int pages = (sq.len + cache.page - 1) >> cache.page_shift;  // that the sequence has
+            for (int t = t0; t < t1; ++t) {
+                // lane j looks after the j-th box of the tile
+                const int key = t * kMmaTile + lane * box_rows;
+                const int at = key >> cache.page_shift;
+                const bool mine = lane < pages_per_tile && at < pages;
+                int page = 0;
+                if (mine) {
+                    page = table[at];
+                    if (page < 0 || page >= cache.n_pages) {
+                        raise_error(a.err, kErrBadIndex);
+                        page = 0;
+                    }
+                }
+                const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
+                bool ok = true;
+                if (lane == 0) {
+                    ok = attn_wait(&sh.abort, &sh.empty[stage], phase ^ 1, a.err);
+                    if (ok)
+                        mbar_arrive_expect_tx(&sh.full[stage],
+                                              static_cast<uint32_t>(boxes * box_rows) *
+                                                  (2 * S::kRowBytes + (INT8 ? 8 : 0)));
+                }
+                if (!__shfl_sync(0xffffffffu, ok, 0)) {
+                    // given up: leave only when the copies in flight have landed (each stage's last
+                    // fill has this cycle's parity below `stage` and the one before's from there on)
+                    if (lane < mp.stages)
+                        mbar_wait_bounded(&sh.full[lane], lane < stage ? phase : phase ^ 1);
+                    return;
+                }
+                if (mine) {
+                    uint8_t* st = ring + static_cast<size_t>(stage) * S::kStageBytes;
+                    const int row = key & (cache.page - 1);
+                    const int outer = page * n_kv + h;
+#pragma unroll
+                    for (int half = 0; half < S::kHalves; ++half) {
+                        uint8_t* dst = st + half * S::kHalfBytes + lane * box_rows * S::kBoxBytes;
+                        const int col = half * (S::kBoxBytes / (INT8 ? 1 : 2));
+                        tma_load_3d(dst, &mp.k_map, col, row, outer, &sh.full[stage]);
+                        tma_load_3d(dst + S::kTileBytes, &mp.v_map, col, row, outer, &sh.full[stage]);
+                    }
+                    if constexpr (INT8) {
+                        const int64_t vec = (static_cast<int64_t>(outer) << cache.page_shift) + row;
+                        uint8_t* sc = st + 2 * S::kTileBytes + lane * box_rows * 4;
+                        bulk_g2s(sc, cache.k_scale + vec, box_rows * 4, &sh.full[stage]);
+                        bulk_g2s(sc + kMmaTile * 4, cache.v_scale + vec, box_rows * 4, &sh.full[stage]);
+                    }
+                }
+                if (++stage == mp.stages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+            u += t1 - t0;
+            if (t1 == it.tiles && h == n_kv - 1) ++item;
+        }
+        return;
+    }
+
+    // ---------------------------------------------------------------- consumer warps
+    const int g = lane >> 2, q4 = lane & 3;
+    const float c2 = a.scale * kLog2e;
+    while (u < u_end) {
+        const AttnItem it = p.items[item];
+        const int64_t rel = u - static_cast<int64_t>(it.before) * n_kv;
+        const int h = static_cast<int>(rel / it.tiles);
+        const int t0 = static_cast<int>(rel - static_cast<int64_t>(h) * it.tiles);
+        const int64_t left = u_end - u;
+        const int t1 = left < it.tiles - t0 ? t0 + static_cast<int>(left) : it.tiles;
+        const AttnSeq sq = attn_seq(a, it.seq, false);
+        const int rows = sq.n_new * p.G;
+
+        // the two rows of this thread: keys they see, and q as A fragments
+        int seen[2];
+        uint32_t qf[kSteps][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = it.row0 + g + 8 * i;
+            const bool live = r < rows;
+            const int tok = live ? r / p.G : 0;
+            seen[i] = live ? attn_seen(sq, tok, a.causal) : 0;
+            const uint16_t* src = a.q + (static_cast<int64_t>(sq.q0) + tok) * a.q_stride +
+                                  static_cast<int64_t>(h * p.G + (live ? r - tok * p.G : 0)) * DIM;
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+                // int8 keys: the byte order of a code fragment is a permutation of the 16 dims of a
+                // step, taken here for q as well
+                const int lo = INT8 ? 16 * k + 4 * q4 : 16 * k + 2 * q4;
+                const int hi = INT8 ? lo + 2 : lo + 8;
+                qf[k][i] = live ? *reinterpret_cast<const uint32_t*>(src + lo) : 0u;
+                qf[k][i + 2] = live ? *reinterpret_cast<const uint32_t*>(src + hi) : 0u;
+            }
+        }
+        // the keys that every live row sees: tiles below need no mask
+        const int first_row_tok = it.row0 / p.G;
+        const int all_seen = attn_seen(sq, first_row_tok, a.causal);
+
+        float o[2 * kSteps][4];
+#pragma unroll
+        for (int i = 0; i < 2 * kSteps; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+
+        for (int t = t0; t < t1; ++t) {
+            // on a timeout (reported) the warps still meet at the barriers below, item by item
+            if (!attn_wait(&sh.abort, &sh.full[stage], phase, a.err)) break;
+            const uint32_t st = smem_u32(ring) + static_cast<uint32_t>(stage) * S::kStageBytes;
+            const int slice = 16 * warp;            // this warp's keys of the stage
+            const int key0 = t * kMmaTile + slice;  // and in the sequence
+
+            // ---- scores of 16 rows x 16 keys: s[0] keys 0..7, s[1] keys 8..15
+            float s[2][4] = {};
+            const int mi = lane >> 3, mr = lane & 7;
+            if constexpr (INT8) {
+                const int row = slice + (mi & 1) * 8 + mr;
+#pragma unroll
+                for (int k = 0; k < kSteps; k += 2) {
+                    uint32_t r[4];
+                    ldsm_x4(st + swizzled<S::kBoxBytes>(row, k + (mi >> 1)), r);
+                    mma_bf16_16816(s[0], qf[k][0], qf[k][1], qf[k][2], qf[k][3], codes_bf16x2(r[0], 0x4140),
+                                   codes_bf16x2(r[0], 0x4342));
+                    mma_bf16_16816(s[1], qf[k][0], qf[k][1], qf[k][2], qf[k][3], codes_bf16x2(r[1], 0x4140),
+                                   codes_bf16x2(r[1], 0x4342));
+                    mma_bf16_16816(s[0], qf[k + 1][0], qf[k + 1][1], qf[k + 1][2], qf[k + 1][3],
+                                   codes_bf16x2(r[2], 0x4140), codes_bf16x2(r[2], 0x4342));
+                    mma_bf16_16816(s[1], qf[k + 1][0], qf[k + 1][1], qf[k + 1][2], qf[k + 1][3],
+                                   codes_bf16x2(r[3], 0x4140), codes_bf16x2(r[3], 0x4342));
+                }
+            } else {
+                const int row = slice + (mi >> 1) * 8 + mr;
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                    uint32_t r[4];
+                    const int chunk = 2 * k + (mi & 1);
+                    ldsm_x4(st + (chunk >> 3) * S::kHalfBytes + swizzled<S::kBoxBytes>(row, chunk & 7), r);
+                    mma_bf16_16816(s[0], qf[k][0], qf[k][1], qf[k][2], qf[k][3], r[0], r[1]);
+                    mma_bf16_16816(s[1], qf[k][0], qf[k][1], qf[k][2], qf[k][3], r[2], r[3]);
+                }
+            }
+
+            // ---- to units of log2, masked; the scales of this thread's keys 2 q4 + {0, 1, 8, 9}
+            float vs[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+            if constexpr (INT8) {
+                const float* sc = reinterpret_cast<const float*>(ring + static_cast<size_t>(stage) * S::kStageBytes +
+                                                                 2 * S::kTileBytes) +
+                                  slice + 2 * q4;
+                const float2 k0 = *reinterpret_cast<const float2*>(sc), k1 = *reinterpret_cast<const float2*>(sc + 8);
+                const float2 v0 = *reinterpret_cast<const float2*>(sc + kMmaTile),
+                             v1 = *reinterpret_cast<const float2*>(sc + kMmaTile + 8);
+                const float ks[4] = {k0.x, k0.y, k1.x, k1.y};
+                vs[0] = v0.x;
+                vs[1] = v0.y;
+                vs[2] = v1.x;
+                vs[3] = v1.y;
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[n][e] *= ks[2 * n + (e & 1)] * c2;
+            } else {
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[n][e] *= c2;
+            }
+            uint32_t vmask0 = 0xFFFFFFFFu, vmask1 = 0xFFFFFFFFu;
+            const bool tail = key0 + 16 > sq.len;
+            if (key0 + 16 > all_seen) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = key0 + 8 * n + 2 * q4 + (e & 1);
+                        if (key >= seen[e >> 1]) s[n][e] = -INFINITY;
+                    }
+                if (tail) {
+                    // what lies past the sequence may be anything, NaN included: zeros instead
+                    const int k = key0 + 2 * q4;
+                    vmask0 = (k < sq.len ? 0xFFFFu : 0u) | (k + 1 < sq.len ? 0xFFFF0000u : 0u);
+                    vmask1 = (k + 8 < sq.len ? 0xFFFFu : 0u) | (k + 9 < sq.len ? 0xFFFF0000u : 0u);
+                    if constexpr (INT8) {
+                        if (k >= sq.len) vs[0] = 0.0f;
+                        if (k + 1 >= sq.len) vs[1] = 0.0f;
+                        if (k + 8 >= sq.len) vs[2] = 0.0f;
+                        if (k + 9 >= sq.len) vs[3] = 0.0f;
+                    }
+                }
+            }
+
+            // ---- running maximum, probabilities
+            float mt[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float v = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                mt[i] = fmaxf(m[i], v);
+            }
+            if (__any_sync(0xffffffffu, mt[0] > m[0] || mt[1] > m[1])) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float f = mt[i] == -INFINITY ? 1.0f : exp2f(m[i] - mt[i]);
+                    m[i] = mt[i];
+                    l[i] *= f;
+#pragma unroll
+                    for (int n = 0; n < 2 * kSteps; ++n) {
+                        o[n][2 * i] *= f;
+                        o[n][2 * i + 1] *= f;
+                    }
+                }
+            }
+            uint32_t pa[4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float mu = m[i] == -INFINITY ? 0.0f : m[i];
+                const float p0 = exp2f(s[0][2 * i] - mu), p1 = exp2f(s[0][2 * i + 1] - mu);
+                const float p2 = exp2f(s[1][2 * i] - mu), p3 = exp2f(s[1][2 * i + 1] - mu);
+                l[i] += (p0 + p1) + (p2 + p3);
+                pa[i] = pack_bf16x2(p0 * vs[0], p1 * vs[1]);
+                pa[i + 2] = pack_bf16x2(p2 * vs[2], p3 * vs[3]);
+            }
+
+            // ---- sums: 16 rows x dim += P (16 x 16) V (16 x dim)
+            const uint32_t vt = st + S::kTileBytes;
+            if constexpr (INT8) {
+                // a b16 element is a pair of dims: the transposed fragment holds dims 2n, 2n + 1 of
+                // two keys, and the permutes pick the two keys of one dim; tile 2k holds the even
+                // dims of a chunk, tile 2k + 1 the odd ones
+                const int row = slice + (mi & 1) * 8 + mr;
+#pragma unroll
+                for (int k = 0; k < kSteps; k += 2) {
+                    uint32_t r[4];
+                    ldsm_x4_t(vt + swizzled<S::kBoxBytes>(row, k + (mi >> 1)), r);
+                    mma_bf16_16816(o[2 * k], pa[0], pa[1], pa[2], pa[3], codes_bf16x2(r[0], 0x4240),
+                                   codes_bf16x2(r[1], 0x4240));
+                    mma_bf16_16816(o[2 * k + 1], pa[0], pa[1], pa[2], pa[3], codes_bf16x2(r[0], 0x4341),
+                                   codes_bf16x2(r[1], 0x4341));
+                    mma_bf16_16816(o[2 * k + 2], pa[0], pa[1], pa[2], pa[3], codes_bf16x2(r[2], 0x4240),
+                                   codes_bf16x2(r[3], 0x4240));
+                    mma_bf16_16816(o[2 * k + 3], pa[0], pa[1], pa[2], pa[3], codes_bf16x2(r[2], 0x4341),
+                                   codes_bf16x2(r[3], 0x4341));
+                }
+            } else {
+                const int row = slice + (mi & 1) * 8 + mr;
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                    uint32_t r[4];
+                    const int chunk = 2 * k + (mi >> 1);
+                    ldsm_x4_t(vt + (chunk >> 3) * S::kHalfBytes + swizzled<S::kBoxBytes>(row, chunk & 7), r);
+                    if (tail) {
+                        r[0] &= vmask0;
+                        r[1] &= vmask1;
+                        r[2] &= vmask0;
+                        r[3] &= vmask1;
+                    }
+                    mma_bf16_16816(o[2 * k], pa[0], pa[1], pa[2], pa[3], r[0], r[1]);
+                    mma_bf16_16816(o[2 * k + 1], pa[0], pa[1], pa[2], pa[3], r[2], r[3]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.empty[stage]);
+            if (++stage == mp.stages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+
+        // ---- join the four warps, in warp order
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+            if (q4 == 0) {
+                sh.m[warp][g + 8 * i] = m[i];
+                sh.l[warp][g + 8 * i] = l[i];
+            }
+        }
+        consumers_sync();
+        float f[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float mm = sh.m[0][g + 8 * i];
+#pragma unroll
+            for (int w = 1; w < kMmaConsumers; ++w) mm = fmaxf(mm, sh.m[w][g + 8 * i]);
+            f[i] = attn_weight(m[i], l[i], mm);
+        }
+        for (int w = 0; w < kMmaConsumers; ++w) {
+            if (warp == w) {
+#pragma unroll
+                for (int n = 0; n < 2 * kSteps; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int r = g + 8 * (e >> 1);
+                        // bf16: tile n, column 2 q4 + (e & 1); int8: chunk n / 2, dims 4 q4 + {0, 2}
+                        // of the even tile and 4 q4 + {1, 3} of the odd one
+                        const int d = INT8 ? 16 * (n >> 1) + 4 * q4 + (n & 1) + 2 * (e & 1) : 8 * n + 2 * q4 + (e & 1);
+                        const float v = f[e >> 1] == 0.0f ? 0.0f : o[n][e] * f[e >> 1];
+                        float* b = buf + r * DIM + d;
+                        *b = w == 0 ? v : *b + v;
+                    }
+            }
+            consumers_sync();
+        }
+
+        const bool whole = t0 == 0 && t1 == it.tiles;
+        const int slot = attn_slot(c, t0 == 0);
+        const int live_rows = rows - it.row0 < kMmaRows ? rows - it.row0 : kMmaRows;
+        for (int i = threadIdx.x; i < live_rows * (DIM / 4); i += 32 * kMmaConsumers) {
+            const int r = i / (DIM / 4), d = 4 * (i % (DIM / 4));
+            float mm = sh.m[0][r];
+#pragma unroll
+            for (int w = 1; w < kMmaConsumers; ++w) mm = fmaxf(mm, sh.m[w][r]);
+            float ll = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kMmaConsumers; ++w) {
+                const float lw = sh.l[w][r];
+                ll += lw * attn_weight(sh.m[w][r], lw, mm);
+            }
+            const float4 v = *reinterpret_cast<const float4*>(buf + r * DIM + d);
+            if (whole) {
+                const int row = it.row0 + r, tok = row / p.G;
+                const int64_t at = (static_cast<int64_t>(sq.q0) + tok) * a.n_q + h * p.G + (row - tok * p.G);
+                const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+                if (bd_in(kBkAttn, at, a.T * a.n_q)) {
+                    *reinterpret_cast<uint2*>(a.out + at * DIM + d) =
+                        make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+                    if (d == 0 && a.lse) a.lse[at] = attn_lse(mm, ll);
+                }
+            } else {
+                const int64_t at = static_cast<int64_t>(slot) * kMmaRows + r;
+                if (bd_in(kBkAttn, at, 2ll * p.blocks * kMmaRows)) {
+                    *reinterpret_cast<float4*>(p.part_o + at * DIM + d) = v;
+                    if (d == 0) p.part_ml[at] = make_float2(mm, ll);
+                }
+            }
+        }
+        consumers_sync();  // the buffers are free for the next item
+        u += t1 - t0;
+        if (t1 == it.tiles && h == n_kv - 1) ++item;
+    }
+}
+
+// ------------------------------------------------------------------------------- join
+
+constexpr int kJoinThreads = 128;
+
+// Block (c, y): if block c of the main kernel is the second one of some
+// (item, head), joins the parts of that (item, head), rows 4 y .. 4 y + 3.
+template <int DIM>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnParams p)
+{
+    constexpr int kPer = DIM / 32;  // values of a lane
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const AttentionArgs& a = p.a;
+    const AttnHeader head = *p.head;
+    const int n_kv = a.cache.n_kv;
+    const int64_t units = static_cast<int64_t>(head.tiles) * n_kv;
+    const int active = attn_active(units, p.blocks);
+    const int c = blockIdx.x + 1;
+    if (c >= active) return;
+    const int lane = threadIdx.x & 31;
+    const int64_t u = attn_first(units, active, c);
+    const AttnItem it = p.items[attn_find_item(p.items, head.n_items, n_kv, u)];
+    const int64_t rel = u - static_cast<int64_t>(it.before) * n_kv;
+    const int h = static_cast<int>(rel / it.tiles);
+    const int64_t start = static_cast<int64_t>(it.before) * n_kv + static_cast<int64_t>(h) * it.tiles;
+    if (start == u || attn_owner(units, active, start) != c - 1) return;
+    const int last = attn_owner(units, active, start + it.tiles - 1);
+    const AttnSeq sq = attn_seq(a, it.seq, false);
+    const int rows = sq.n_new * p.G;
+    const int r = 4 * blockIdx.y + (threadIdx.x >> 5);
+    const int row = it.row0 + r;
+    if (r >= p.mb || row >= rows) return;
+
+    const int parts = last - c + 2;  // blocks c - 1 .. last
+    float mm = -INFINITY;
+    for (int i = lane; i < parts; i += 32)
+        mm = fmaxf(mm, p.part_ml[static_cast<int64_t>(attn_slot(c - 1 + i, i == 0)) * p.mb + r].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+    float acc[kPer] = {}, ll = 0.0f;
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+        float w = 0.0f, lw = 0.0f;
+        if (i0 + lane < parts) {
+            const float2 ml = p.part_ml[static_cast<int64_t>(attn_slot(c - 1 + i0 + lane, i0 + lane == 0)) * p.mb + r];
+            w = attn_weight(ml.x, ml.y, mm);
+            lw = ml.y;
+        }
+        const int n = parts - i0 < 32 ? parts - i0 : 32;
+        for (int i = 0; i < n; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, i), li = __shfl_sync(0xffffffffu, lw, i);
+            const float* src = p.part_o +
+                               (static_cast<int64_t>(attn_slot(c - 1 + i0 + i, i0 + i == 0)) * p.mb + r) * DIM + kPer * lane;
+            float v[kPer];
+            if constexpr (kPer == 4) {
+                const float4 x = *reinterpret_cast<const float4*>(src);
+                v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+            } else {
+                const float2 x = *reinterpret_cast<const float2*>(src);
+                v[0] = x.x, v[1] = x.y;
+            }
+            if (wi != 0.0f) {
+                ll += wi * li;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) acc[e] += wi * v[e];
+            }
+        }
+    }
+    const int tok = row / p.G;
+    const int64_t at = (static_cast<int64_t>(sq.q0) + tok) * a.n_q + h * p.G + (row - tok * p.G);
+    if (!bd_in(kBkAttnCombine, at, a.T * a.n_q)) return;
+    const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + at * DIM + kPer * lane);
+#pragma unroll
+    for (int e = 0; e < kPer; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0 && a.lse) a.lse[at] = attn_lse(mm, ll);
+}
+
+template <int DIM, bool INT8>
+cudaError_t launch_mma_shape(const AttnParams& p, cudaStream_t stream)
+{
+    using S = MmaShape<DIM, INT8>;
+    static std::atomic<size_t> smem_set[kHostMaxDevices];
+    const KvPages& kv = p.a.cache;
+    MmaParams mp{};
+    mp.p = p;
+    const uint32_t box_rows = kv.page < kMmaTile ? kv.page : kMmaTile;
+    const auto type = INT8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const auto swz = S::kBoxBytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    const uint64_t outer = static_cast<uint64_t>(kv.n_pages) * kv.n_kv;
+    for (int i = 0; i < 2; ++i)
+        if (!encode_tma_3d(i ? &mp.v_map : &mp.k_map, type, INT8 ? 1 : 2, i ? kv.v : kv.k, DIM, kv.page, outer,
+                           S::kBoxBytes / (INT8 ? 1 : 2), box_rows, swz))
+            return cudaErrorInvalidValue;
+    // two blocks per SM: 113 KB each, less the static part and the alignment of the ring
+    constexpr size_t kBudget = 111u * 1024u;
+    mp.stages = static_cast<int>((kBudget - S::kBufBytes) / S::kStageBytes);
+    if (mp.stages > kMmaMaxStages) mp.stages = kMmaMaxStages;
+    const size_t smem = 1024 + static_cast<size_t>(mp.stages) * S::kStageBytes + S::kBufBytes;
+    cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(attn_mma_kernel<DIM, INT8>), smem, smem_set);
+    launch_dep(err, attn_mma_kernel<DIM, INT8>, dim3(p.blocks), dim3(kMmaThreads), smem, stream, mp);
+    return err;
+}
+
+constexpr size_t align_up(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+struct AttnWs {
+    size_t head, item_off, items, ml, o, total;
+};
+
+AttnWs attn_layout(int64_t T, int64_t n_seq, int64_t G, int dim, int mb, int blocks)
+{
+    AttnWs w{};
+    w.head = 256;
+    w.item_off = w.head + 256;
+    w.items = w.item_off + align_up(static_cast<size_t>(n_seq + 1) * 4);
+    const size_t items = static_cast<size_t>((T * G + mb - 1) / mb + n_seq);
+    w.ml = w.items + align_up(items * sizeof(AttnItem));
+    w.o = w.ml + align_up(static_cast<size_t>(2 * blocks) * mb * 8);
+    w.total = w.o + align_up(static_cast<size_t>(2 * blocks) * mb * dim * 4);
+    return w;
+}
+
+}  // namespace
+
+cudaError_t launch_attention_mma(const AttnParams& p, cudaStream_t stream)
+{
+    if (p.a.cache.dim == 128)
+        return p.a.cache.int8 ? launch_mma_shape<128, true>(p, stream) : launch_mma_shape<128, false>(p, stream);
+    return p.a.cache.int8 ? launch_mma_shape<64, true>(p, stream) : launch_mma_shape<64, false>(p, stream);
+}
+
+size_t attention_workspace_size(int64_t T, int64_t n_seq, int n_q, int n_kv, int dim)
+{
+    return attn_layout(T, n_seq, n_q / n_kv, dim, kMmaRows, kAttnMaxBlocks).total;
+}
+
+cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream)
+{
+    if (a.T == 0 || a.n_seq == 0) return cudaSuccess;
+    AttnParams p{};
+    p.a = a;
+    p.G = a.n_q / a.cache.n_kv;
+    p.tile = kMmaTile;
+    p.mb = kMmaRows;
+    p.blocks = 2 * a.sm_count < kAttnMaxBlocks ? 2 * a.sm_count : kAttnMaxBlocks;
+    const AttnWs w = attn_layout(a.T, a.n_seq, p.G, a.cache.dim, p.mb, kAttnMaxBlocks);
+    char* ws = static_cast<char*>(a.ws);
+    p.head = reinterpret_cast<AttnHeader*>(ws + w.head);
+    p.item_off = reinterpret_cast<int32_t*>(ws + w.item_off);
+    p.items = reinterpret_cast<AttnItem*>(ws + w.items);
+    p.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+    p.part_o = reinterpret_cast<float*>(ws + w.o);
+    cudaError_t err = cudaSuccess;
+    launch_dep(err, attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
+    if (err == cudaSuccess) err = launch_attention_mma(p, stream);
+    const dim3 grid(static_cast<unsigned>(p.blocks > 1 ? p.blocks - 1 : 1), static_cast<unsigned>((p.mb + 3) / 4));
+    launch_dep(err, a.cache.dim == 128 ? attn_join_kernel<128> : attn_join_kernel<64>, grid, dim3(kJoinThreads), 0,
+               stream, p);
+    return err;
+}
+
+BD_BOUNDS_TAKE(bounds_take_attention)
+
+}  // namespace bd

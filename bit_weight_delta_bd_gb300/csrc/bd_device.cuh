@@ -16,6 +16,7 @@ namespace bd {
 constexpr uint32_t kErrBadVariant = 1u << 4;
 constexpr uint32_t kErrNonFinite = 1u << 5;
 constexpr uint32_t kErrTimeout = 1u << 7;
+constexpr uint32_t kErrBadIndex = 1u << 11;
 
 // Bounded waits give up after this many nanoseconds of %globaltimer.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
@@ -36,7 +37,8 @@ __device__ __forceinline__ void raise_error(uint32_t* err, uint32_t bits)
 enum BoundsKernel : uint32_t {
     kBkCompress = 0, kBkAlphaFinalize, kBkReconstruct, kBkSkinny, kBkMultiPrepare, kBkMulti, kBkPrefill,
     kBkPrefillPlan, kBkGather, kBkRoute, kBkMaterialize, kBkMsProd, kBkMsSplit, kBkMsSlices, kBkMsGram,
-    kBkMsGramSum, kBkMsChol, kBkMsEig, kBkMsTri, kBkMsApply, kBkMsMerge
+    kBkMsGramSum, kBkMsChol, kBkMsEig, kBkMsTri, kBkMsApply, kBkMsMerge,
+    kBkNorm, kBkRope, kBkKvRead, kBkAttnPlan, kBkAttn, kBkAttnCombine
 };
 #ifdef BD_DEBUG_BOUNDS
 namespace {

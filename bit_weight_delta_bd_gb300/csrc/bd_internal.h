@@ -190,6 +190,92 @@ struct MonoSoupArgs {
     int sm_count;                  // SMs of the current device
 };
 
+// ---- norm (bd_norm.cu) ------------------------------------------------------------------------
+
+struct NormArgs {
+    const uint16_t* x;         // [T][d] bf16 bits
+    const uint16_t* residual;  // [T][d] or null
+    uint16_t* residual_out;    // [T][d] or null
+    const uint16_t* gain;      // [d]: the base model's
+    const int32_t* vid;        // [T] or null
+    int V;
+    const uint16_t* gains[kMaxVariants];
+    int64_t T, d;
+    float eps;
+    void* out;                 // [T][d] bf16, fp32 or e4m3 (bd_out_dtype)
+    int out_dtype;
+    float* scale;              // [T] (e4m3)
+    uint32_t* err;
+};
+
+cudaError_t launch_rms_norm(const NormArgs& a, int sm_count, cudaStream_t stream);
+
+// ---- paged KV cache (bd_kv.cu) ----------------------------------------------------------------
+
+struct KvPages {
+    void *k, *v;               // [n_pages][n_kv][page][dim] bf16 or int8
+    float *k_scale, *v_scale;  // [n_pages][n_kv][page] (int8)
+    int64_t n_pages;
+    int page, page_shift, n_kv, dim, int8;
+};
+
+constexpr int kMaxAxes = 4;
+constexpr int kMaxPairs = 64;  // rotary pairs of a head
+
+struct RopeArgs {
+    const uint16_t *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride, q_out_stride, T;
+    int n_q;
+    const int32_t* pos;        // [T][n_axes]
+    int n_axes;
+    uint8_t axis_of_pair[kMaxPairs];
+    const float* tab;          // [n_pos][rot/2][2]
+    int64_t n_pos;
+    int rot, interleaved;
+    const int32_t* slot;       // [T]
+    KvPages cache;
+    uint16_t* q_out;
+    uint32_t* err;
+};
+
+cudaError_t launch_rope_append(const RopeArgs& a, int sm_count, cudaStream_t stream);
+
+struct KvReadArgs {
+    KvPages cache;
+    const int32_t* table;      // [n_seq][max_pages]
+    int64_t max_pages;
+    const int32_t* kv_off;     // [n_seq + 1]
+    int64_t n_seq, rows;
+    uint16_t *k_out, *v_out;   // [rows][n_kv][dim]
+    uint32_t* err;
+};
+
+cudaError_t launch_kv_read(const KvReadArgs& a, int sm_count, cudaStream_t stream);
+
+// ---- attention over the paged cache (bd_attention.cu, bd_attention_chunk.cu) -------------------
+
+struct AttentionArgs {
+    const uint16_t* q;         // [T] rows of n_q heads
+    int64_t q_stride;
+    const int32_t* q_off;      // [n_seq + 1]
+    int64_t T, n_seq, max_new;
+    int n_q;
+    KvPages cache;
+    const int32_t* table;      // [n_seq][max_pages]
+    int64_t max_pages;
+    const int32_t* kv_len;     // [n_seq]
+    float scale;
+    int causal;
+    uint16_t* out;             // [T][n_q][dim]
+    float* lse;                // [T][n_q] or null
+    void* ws;
+    uint32_t* err;
+    int sm_count;
+};
+
+size_t attention_workspace_size(int64_t T, int64_t n_seq, int n_q, int n_kv, int dim);
+cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream);
+
 // bounds-checked builds: the flag words of each translation unit, read and
 // cleared (0 in normal builds)
 uint32_t bounds_take_compress();
@@ -199,6 +285,9 @@ uint32_t bounds_take_prefill();
 uint32_t bounds_take_route();
 uint32_t bounds_take_materialize();
 uint32_t bounds_take_monosoup();
+uint32_t bounds_take_norm();
+uint32_t bounds_take_kv();
+uint32_t bounds_take_attention();
 
 int monosoup_max_l();
 size_t monosoup_workspace_size(int64_t d_out, int64_t d_in, int k, int r, int l);

@@ -1,0 +1,308 @@
+// The paged KV cache: rotary positions with the write into the cache, and
+// reading the cache back.  Both kernels only move data (a few operations per
+// element) and are bound by the bytes they read and write.
+//
+// Int8 codes.  Per (token, kv head): scale = max(max |x|, 1e-30) / 127 and
+// code = round-half-even(x / scale), both with IEEE divisions.  The rotation
+// rounds each product and each sum by itself (no contraction to fused
+// multiply-adds), so codes and scales are those of the formula evaluated
+// operation by operation in fp32, whatever computes them.
+#include "bd_device.cuh"
+
+namespace bd {
+namespace {
+
+constexpr int kRopeThreads = 128;
+constexpr int kUnit = 16;  // elements of a head that one thread handles
+
+__device__ __forceinline__ void unpack8(uint4 u, float* f)
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float* f)
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 r = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&r);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 8 codes of x / scale as 8 bytes (the first element lowest)
+__device__ __forceinline__ uint2 codes8(const float* x, float scale)
+{
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        int c = __float2int_rn(__fdiv_rn(x[i], scale));
+        c = c < -127 ? -127 : c > 127 ? 127 : c;
+        w[i / 4] |= (static_cast<uint32_t>(c) & 0xFFu) << (8 * (i % 4));
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+struct RopeParams {
+    RopeArgs a;
+};
+
+// A thread handles 16 elements of a head: the 8 pairs (i, i + rot/2) from
+// i = 8 u on, or elements 16 u .. 16 u + 15 (interleaved pairs, the part past
+// rot, and v).  Its unit u stays the same for all heads it visits, so the
+// cosines and sines are read once per token.  UPH = dim / 16 units per head;
+// a block is one token (grid x) and one part of its heads (grid y).
+template <int UPH, bool INT8>
+__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeParams p)
+{
+    constexpr int kDim = UPH * kUnit;
+    constexpr int kHeadsPerPass = kRopeThreads / UPH;
+    const RopeArgs& a = p.a;
+    const int u = threadIdx.x % UPH;
+    const int64_t t = blockIdx.x;
+    const int n_kv = a.cache.n_kv;
+    const int heads = a.n_q + 2 * n_kv;
+
+    grid_launch_dependents();
+    grid_dependency_wait();
+
+    // this unit's elements and whether they turn
+    const bool turns = 16 * u < a.rot;
+    const int first = turns && !a.interleaved ? 8 * u : 16 * u;
+    const int second = turns && !a.interleaved ? 8 * u + a.rot / 2 : 16 * u + 8;
+    float c[8], s[8];
+    if (turns) {
+        const int pair0 = 8 * u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            int64_t pos = a.pos[t * a.n_axes + a.axis_of_pair[pair0 + i]];
+            if (pos < 0 || pos >= a.n_pos) {
+                raise_error(a.err, kErrBadIndex);
+                pos = 0;
+            }
+            const float2 cs = __ldg(reinterpret_cast<const float2*>(a.tab) + pos * (a.rot / 2) + pair0 + i);
+            c[i] = cs.x;
+            s[i] = cs.y;
+        }
+    }
+    const int64_t slots = a.cache.n_pages * a.cache.page;
+    int64_t slot = a.slot ? a.slot[t] : -1;
+    if (slot < -1 || slot >= slots) {
+        if (threadIdx.x == 0) raise_error(a.err, kErrBadIndex);
+        slot = -1;
+    }
+    const int64_t page = slot >> a.cache.page_shift, place = slot & (a.cache.page - 1);
+
+    // every lane of a head's group takes the same way, and all lanes of a
+    // warp run the same number of passes (the reductions use the full warp)
+    for (int h0 = blockIdx.y * kHeadsPerPass; h0 < heads; h0 += gridDim.y * kHeadsPerPass) {
+        const int h = h0 + threadIdx.x / UPH;
+        const bool live = h < heads;
+        const bool is_q = h < a.n_q, is_v = h >= a.n_q + n_kv;
+        float x[16];
+        if (live) {
+            const uint16_t* src = is_q ? a.q + t * a.q_stride + static_cast<int64_t>(h) * kDim
+                                 : is_v ? a.v + t * a.v_stride + static_cast<int64_t>(h - a.n_q - n_kv) * kDim
+                                        : a.k + t * a.k_stride + static_cast<int64_t>(h - a.n_q) * kDim;
+            const int e0 = is_v ? 16 * u : first, e1 = is_v ? 16 * u + 8 : second;
+            unpack8(*reinterpret_cast<const uint4*>(src + e0), x);
+            unpack8(*reinterpret_cast<const uint4*>(src + e1), x + 8);
+            if (turns && !is_v) {
+                if (a.interleaved) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float p0 = x[2 * i], p1 = x[2 * i + 1];
+                        x[2 * i] = __fsub_rn(__fmul_rn(p0, c[i]), __fmul_rn(p1, s[i]));
+                        x[2 * i + 1] = __fadd_rn(__fmul_rn(p1, c[i]), __fmul_rn(p0, s[i]));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float p0 = x[i], p1 = x[8 + i];
+                        x[i] = __fsub_rn(__fmul_rn(p0, c[i]), __fmul_rn(p1, s[i]));
+                        x[8 + i] = __fadd_rn(__fmul_rn(p1, c[i]), __fmul_rn(p0, s[i]));
+                    }
+                }
+            }
+            if (is_q) {
+                uint16_t* dst = a.q_out + t * a.q_out_stride + static_cast<int64_t>(h) * kDim;
+                *reinterpret_cast<uint4*>(dst + e0) = pack8(x);
+                *reinterpret_cast<uint4*>(dst + e1) = pack8(x + 8);
+            }
+        }
+        if constexpr (INT8) {
+            float amax = 0.0f;
+            if (live && !is_q) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) amax = max_nan(amax, fabsf(x[i]));
+            }
+#pragma unroll
+            for (int o = 1; o < UPH; o <<= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            if (live && !is_q && slot >= 0) {
+                const float scale = __fdiv_rn(max_nan(amax, 1e-30f), 127.0f);
+                const int hk = is_v ? h - a.n_q - n_kv : h - a.n_q;
+                const int64_t vec = ((page * n_kv + hk) << a.cache.page_shift) + place;
+                if (bd_in(kBkRope, vec, slots * n_kv)) {
+                    uint8_t* dst = static_cast<uint8_t*>(is_v ? a.cache.v : a.cache.k) + vec * kDim;
+                    const int e0 = is_v ? 16 * u : first, e1 = is_v ? 16 * u + 8 : second;
+                    *reinterpret_cast<uint2*>(dst + e0) = codes8(x, scale);
+                    *reinterpret_cast<uint2*>(dst + e1) = codes8(x + 8, scale);
+                    if (u == 0) (is_v ? a.cache.v_scale : a.cache.k_scale)[vec] = scale;
+                }
+            }
+        } else {
+            if (live && !is_q && slot >= 0) {
+                const int hk = is_v ? h - a.n_q - n_kv : h - a.n_q;
+                const int64_t vec = ((page * n_kv + hk) << a.cache.page_shift) + place;
+                if (bd_in(kBkRope, vec, slots * n_kv)) {
+                    uint16_t* dst = static_cast<uint16_t*>(is_v ? a.cache.v : a.cache.k) + vec * kDim;
+                    const int e0 = is_v ? 16 * u : first, e1 = is_v ? 16 * u + 8 : second;
+                    *reinterpret_cast<uint4*>(dst + e0) = pack8(x);
+                    *reinterpret_cast<uint4*>(dst + e1) = pack8(x + 8);
+                }
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------- read
+
+constexpr int kReadThreads = 256;
+constexpr int kReadRows = 8;  // output rows of a block
+
+struct KvReadParams {
+    KvReadArgs a;
+};
+
+// A block gathers kReadRows consecutive output rows: their places in the
+// cache are looked up first (a binary search in kv_off per row), then all
+// threads copy units of 16 elements.
+template <int UPH, bool INT8>
+__global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const __grid_constant__ KvReadParams p)
+{
+    constexpr int kDim = UPH * kUnit;
+    __shared__ int64_t base[kReadRows];  // page * n_kv * page + place of the token; -1: zeros, -2: leave the row
+    const KvReadArgs& a = p.a;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kReadRows;
+
+    grid_launch_dependents();
+    grid_dependency_wait();
+
+    if (threadIdx.x < kReadRows) {
+        const int64_t r = row0 + threadIdx.x;
+        int64_t b = -2;
+        if (r < a.rows && r < a.kv_off[a.n_seq]) {
+            int64_t lo = 0, hi = a.n_seq;  // the last s with kv_off[s] <= r
+            while (hi - lo > 1) {
+                const int64_t mid = (lo + hi) / 2;
+                if (a.kv_off[mid] <= r) lo = mid;
+                else hi = mid;
+            }
+            const int64_t j = r - a.kv_off[lo];
+            b = -1;
+            const int64_t at = j >> a.cache.page_shift;
+            if (j >= 0 && at < a.max_pages) {
+                const int64_t pg = a.table[lo * a.max_pages + at];
+                if (pg >= 0 && pg < a.cache.n_pages)
+                    b = ((pg * a.cache.n_kv) << a.cache.page_shift) + (j & (a.cache.page - 1));
+            }
+            if (b < 0) raise_error(a.err, kErrBadIndex);
+        }
+        base[threadIdx.x] = b;
+    }
+    __syncthreads();
+
+    const int per_row = a.cache.n_kv * UPH;  // units of one row of k (or v)
+    const int64_t vecs = (a.cache.n_pages * a.cache.n_kv) << a.cache.page_shift;
+    const bool is_v = blockIdx.y != 0;
+    const void* pool = is_v ? a.cache.v : a.cache.k;
+    const float* scales = is_v ? a.cache.v_scale : a.cache.k_scale;
+    uint16_t* out = is_v ? a.v_out : a.k_out;
+    for (int i = threadIdx.x; i < kReadRows * per_row; i += kReadThreads) {
+        const int r = i / per_row, j = i - r * per_row;
+        const int64_t b = base[r];
+        if (b == -2) continue;
+        const int h = j / UPH, u = j % UPH;
+        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+        const int64_t vec = b + (static_cast<int64_t>(h) << a.cache.page_shift);
+        if (b >= 0 && bd_in(kBkKvRead, vec, vecs)) {
+            if constexpr (INT8) {
+                const uint4 w = ld_stream_v4(static_cast<const uint8_t*>(pool) + vec * kDim + 16 * u);
+                const float scale = __ldg(scales + vec);
+                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+                float f[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    f[e] = static_cast<float>(static_cast<int8_t>(ww[e / 4] >> (8 * (e % 4)))) * scale;
+                lo = pack8(f);
+                hi = pack8(f + 8);
+            } else {
+                const uint16_t* src = static_cast<const uint16_t*>(pool) + vec * kDim + 16 * u;
+                lo = ld_stream_v4(src);
+                hi = ld_stream_v4(src + 8);
+            }
+        }
+        uint16_t* dst = out + ((row0 + r) * a.cache.n_kv + h) * kDim + 16 * u;
+        if (bd_in_range(kBkKvRead, dst - out, 16, a.rows * a.cache.n_kv * kDim)) {
+            *reinterpret_cast<uint4*>(dst) = lo;
+            *reinterpret_cast<uint4*>(dst + 8) = hi;
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_rope_append(const RopeArgs& a, int sm_count, cudaStream_t stream)
+{
+    if (a.T == 0) return cudaSuccess;
+    RopeParams p{a};
+    const int per_pass = kRopeThreads / (a.cache.dim / kUnit);
+    const int heads = a.n_q + 2 * a.cache.n_kv;
+    const int passes = (heads + per_pass - 1) / per_pass;
+    // few tokens: the heads of a token are split over blocks until the GPU
+    // has about 8 blocks per SM
+    int64_t split = (8ll * sm_count + a.T - 1) / a.T;
+    if (split > passes) split = passes;
+    if (split < 1) split = 1;
+    const dim3 grid(static_cast<unsigned>(a.T), static_cast<unsigned>(split));
+    cudaError_t err = cudaSuccess;
+    if (a.cache.dim == 128)
+        launch_dep(err, a.cache.int8 ? rope_append_kernel<8, true> : rope_append_kernel<8, false>, grid,
+                   dim3(kRopeThreads), 0, stream, p);
+    else
+        launch_dep(err, a.cache.int8 ? rope_append_kernel<4, true> : rope_append_kernel<4, false>, grid,
+                   dim3(kRopeThreads), 0, stream, p);
+    return err;
+}
+
+cudaError_t launch_kv_read(const KvReadArgs& a, int /*sm_count*/, cudaStream_t stream)
+{
+    if (a.rows == 0) return cudaSuccess;
+    KvReadParams p{a};
+    const dim3 grid(static_cast<unsigned>((a.rows + kReadRows - 1) / kReadRows), 2);
+    cudaError_t err = cudaSuccess;
+    if (a.cache.dim == 128)
+        launch_dep(err, a.cache.int8 ? kv_read_kernel<8, true> : kv_read_kernel<8, false>, grid, dim3(kReadThreads),
+                   0, stream, p);
+    else
+        launch_dep(err, a.cache.int8 ? kv_read_kernel<4, true> : kv_read_kernel<4, false>, grid, dim3(kReadThreads),
+                   0, stream, p);
+    return err;
+}
+
+BD_BOUNDS_TAKE(bounds_take_kv)
+
+}  // namespace bd

@@ -32,10 +32,12 @@ struct MapKey {
     uint64_t cols, rows, row_bytes;
     uint32_t box_cols, box_rows;
     int dtype, swizzle;
+    uint64_t outer = 0;  // 0: a 2-D map
     bool operator==(const MapKey& o) const
     {
         return base == o.base && cols == o.cols && rows == o.rows && row_bytes == o.row_bytes &&
-               box_cols == o.box_cols && box_rows == o.box_rows && dtype == o.dtype && swizzle == o.swizzle;
+               box_cols == o.box_cols && box_rows == o.box_rows && dtype == o.dtype && swizzle == o.swizzle &&
+               outer == o.outer;
     }
 };
 
@@ -43,8 +45,8 @@ struct MapKeyHash {
     size_t operator()(const MapKey& k) const
     {
         uint64_t h = 1469598103934665603ull;
-        const uint64_t v[8] = {static_cast<uint64_t>(k.base), k.cols, k.rows, k.row_bytes, k.box_cols, k.box_rows,
-                               static_cast<uint64_t>(k.dtype), static_cast<uint64_t>(k.swizzle)};
+        const uint64_t v[9] = {static_cast<uint64_t>(k.base), k.cols, k.rows, k.row_bytes, k.box_cols, k.box_rows,
+                               static_cast<uint64_t>(k.dtype), static_cast<uint64_t>(k.swizzle), k.outer};
         for (uint64_t x : v) h = (h ^ x) * 1099511628211ull;
         return static_cast<size_t>(h);
     }
@@ -54,12 +56,12 @@ constexpr size_t kMapCacheMax = 4096;
 
 }  // namespace
 
-bool encode_tma_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t cols, uint64_t rows,
-                   uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle)
+namespace {
+
+// a 2-D map (outer == 0) or a 3-D map over contiguous slices
+bool encode(CUtensorMap* map, const MapKey& key)
 {
     thread_local std::unordered_map<MapKey, CUtensorMap, MapKeyHash> cache;
-    const MapKey key{reinterpret_cast<uintptr_t>(base), cols, rows, row_bytes, box_cols, box_rows,
-                     static_cast<int>(dtype), static_cast<int>(swizzle)};
     auto it = cache.find(key);
     if (it != cache.end()) {
         std::memcpy(map, &it->second, sizeof(CUtensorMap));
@@ -67,16 +69,33 @@ bool encode_tma_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base
     }
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
-    const cuuint64_t dims[2] = {cols, rows};
-    const cuuint64_t strides[1] = {row_bytes};
-    const cuuint32_t box[2] = {box_cols, box_rows};
-    const cuuint32_t elem[2] = {1, 1};
-    if (fn(map, dtype, 2, const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+    const cuuint64_t dims[3] = {key.cols, key.rows, key.outer};
+    const cuuint64_t strides[2] = {key.row_bytes, key.rows * key.row_bytes};
+    const cuuint32_t box[3] = {key.box_cols, key.box_rows, 1};
+    const cuuint32_t elem[3] = {1, 1, 1};
+    if (fn(map, static_cast<CUtensorMapDataType>(key.dtype), key.outer ? 3 : 2, reinterpret_cast<void*>(key.base),
+           dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, static_cast<CUtensorMapSwizzle>(key.swizzle),
            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return false;
     if (cache.size() >= kMapCacheMax) cache.clear();
     cache.emplace(key, *map);
     return true;
+}
+
+}  // namespace
+
+bool encode_tma_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t cols, uint64_t rows,
+                   uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle)
+{
+    return encode(map, MapKey{reinterpret_cast<uintptr_t>(base), cols, rows, row_bytes, box_cols, box_rows,
+                              static_cast<int>(dtype), static_cast<int>(swizzle)});
+}
+
+bool encode_tma_3d(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t elem_bytes, const void* base, uint64_t cols,
+                   uint64_t rows, uint64_t outer, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle)
+{
+    return encode(map, MapKey{reinterpret_cast<uintptr_t>(base), cols, rows, cols * elem_bytes, box_cols, box_rows,
+                              static_cast<int>(dtype), static_cast<int>(swizzle), outer});
 }
 
 cudaError_t ensure_dynamic_smem(const void* kernel, size_t bytes, std::atomic<size_t>* per_device)

@@ -19,6 +19,12 @@ namespace bd {
 bool encode_tma_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t cols, uint64_t rows,
                    uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle);
 
+// Encodes a 3-D tiled tensor map over a contiguous [outer][rows][cols] array
+// of elements of elem_bytes, with a box of box_cols x box_rows x 1.  Cached
+// like the 2-D maps.
+bool encode_tma_3d(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t elem_bytes, const void* base, uint64_t cols,
+                   uint64_t rows, uint64_t outer, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle);
+
 // Raises a kernel's dynamic shared-memory limit on the current device to at
 // least `bytes` and asks for the largest shared-memory carve-out, calling the
 // runtime only the first time per device (the attributes persist);

@@ -64,12 +64,14 @@ typedef enum bd_status {
     BD_ERR_TIMEOUT = 7,           /* (async) a bounded in-kernel wait gave up */
     BD_ERR_WORKSPACE = 8,         /* workspace null or smaller than required */
     BD_ERR_DEVICE = 9,            /* current device is not a compute capability 10.3 GPU */
-    BD_ERR_BOUNDS = 10            /* (bounds-checked builds) a kernel met an index outside its buffer */
+    BD_ERR_BOUNDS = 10,           /* (bounds-checked builds) a kernel met an index outside its buffer */
+    BD_ERR_BAD_INDEX = 11         /* (async) a position, slot, page, length or offset outside its range */
 } bd_status;
 
 typedef enum bd_alpha_mode { BD_ALPHA_PER_MATRIX = 0, BD_ALPHA_PER_ROW = 1 } bd_alpha_mode;
 
-typedef enum bd_out_dtype { BD_OUT_BF16 = 0, BD_OUT_F32 = 1 } bd_out_dtype;
+/* BD_OUT_E4M3 (8 bits with a scale per row) is taken by bd_rms_norm only. */
+typedef enum bd_out_dtype { BD_OUT_BF16 = 0, BD_OUT_F32 = 1, BD_OUT_E4M3 = 2 } bd_out_dtype;
 
 /* Largest number of variants one bd_linear_multi call can address. */
 #define BD_MAX_VARIANTS 64
@@ -278,6 +280,157 @@ bd_status bd_monosoup_merge(const uint16_t* w_base, const uint16_t* const* w_ft,
 
 bd_status bd_compress_noalloc(const uint16_t* w_base, const uint16_t* w_ft, int64_t d_out, int64_t d_in,
                               int alpha_mode, uint32_t* signs, float* alpha, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The operators between a decoder layer's linears: the norm, rotary
+ * positions with the write into the paged KV cache, reading the cache back,
+ * and attention over it.  The BitDelta post serves whole models (section
+ * "Sunum mimarisi", steps 3-5) but describes only their linears; these entry
+ * points have no counterpart on its pages.
+ *
+ * RMS norm with the residual's addition:
+ *   h[t] = x[t] + residual[t]                     (x[t] without a residual)
+ *   y[t] = h[t] * (mean_j h[t][j]^2 + eps)^(-1/2) * gain_{vid[t]}
+ * A variant's gains are not compressed: token t takes the gain of its own
+ * variant, as its linears take their delta; vid[t] == -1 (or vid == NULL)
+ * means the base model's gain.  h, the mean and y are fp32; y is rounded once.
+ *   x, residual   device bf16 [T][d]; residual may be NULL
+ *   residual_out  device bf16 [T][d] or NULL: h rounded to bf16; may be the
+ *                 residual's own buffer (or x's)
+ *   gain          device bf16 [d]; gain_tab: host array of V device pointers,
+ *                 each bf16 [d] (ignored without vid); vid: device int32 [T]
+ *   out           device [T][d]: bf16, fp32 or (BD_OUT_E4M3) 8-bit codes with
+ *                 scale[t] = max(max_j |y[t][j]|, 1e-30) / 448, code =
+ *                 RN_e4m3(y * (448 / max)); a row that is not finite has a
+ *                 scale that is not finite
+ *   scale         device fp32 [T], 4-byte aligned, written for BD_OUT_E4M3 (NULL otherwise)
+ * d: a positive multiple of 8 (BD_ERR_UNSUPPORTED_SHAPE); matrices and gains
+ * 16-byte aligned; out may not overlap an input.  0 <= V <= BD_MAX_VARIANTS.
+ * An id outside [-1, V) sets BD_ERR_BAD_VARIANT and takes the base gain.
+ * ------------------------------------------------------------------------ */
+size_t bd_rms_norm_workspace_size(int64_t T, int64_t d);
+
+bd_status bd_rms_norm(const uint16_t* x, const uint16_t* residual, int64_t T, int64_t d, const uint16_t* gain,
+                      const int32_t* vid, int32_t V, const uint16_t* const* gain_tab, float eps,
+                      uint16_t* residual_out, void* out, int out_dtype, float* scale, void* ws, size_t ws_bytes,
+                      void* stream);
+
+/* ------------------------------------------------------------------------
+ * A paged KV cache of one layer: fixed-size pages of page_size tokens, each
+ * holding the tokens' keys (and values) of every kv head, head by head:
+ *   k, v              device [n_pages][n_kv][page_size][head_dim], bf16 or
+ *                     int8 codes, 16-byte aligned
+ *   k_scale, v_scale  device fp32 [n_pages][n_kv][page_size] (int8), 16-byte
+ *                     aligned; NULL for bf16.  A value is code * scale.
+ * head_dim 64 or 128; page_size 16, 32, 64 or 128; n_kv 1..1024.  Other
+ * values give BD_ERR_UNSUPPORTED_SHAPE.  A host struct that each call reads.
+ * ------------------------------------------------------------------------ */
+typedef enum bd_kv_dtype { BD_KV_BF16 = 0, BD_KV_INT8 = 1 } bd_kv_dtype;
+
+typedef struct bd_kv_pages {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    int64_t n_pages;
+    int32_t page_size;
+    int32_t n_kv;
+    int32_t head_dim;
+    int32_t dtype;
+} bd_kv_pages;
+
+/* ------------------------------------------------------------------------
+ * Rotary positions, and the write into the cache.
+ * Pair i (0 <= i < rot_dim/2) of a q or k head of token t turns by the angle
+ * whose cosine and sine stand at rope_tab[p][i], p = pos[t][axis_of_pair[i]]:
+ *   (a, b) -> (a cos - b sin, b cos + a sin)
+ * with (a, b) = (x[i], x[i + rot_dim/2]), or (x[2i], x[2i+1]) if
+ * `interleaved`; elements from rot_dim on pass through.  q goes to q_out
+ * (rounded to bf16 once), k and v go to the cache at slot[t] (page *
+ * page_size + place in the page; -1 writes nothing): rounded to bf16, or as
+ * int8 codes with, per token and head,
+ *   scale = max(max |x|, 1e-30) / 127,  code = round-half-even(x / scale),
+ * formed from the unrounded fp32 values.  A vector that is not finite gets a
+ * scale that is not finite.  Products and sums are rounded one by one (no
+ * fused multiply-add), so the codes do not depend on the kernel.
+ *   q, k, v    device bf16 rows of n_q, n_kv, n_kv heads of head_dim, rows
+ *              *_stride elements apart (a multiple of 8, at least the row):
+ *              slices of one packed product can be passed as they are.  q
+ *              and q_out may be NULL with n_q = 0.
+ *   q_out      device bf16 [T] rows, q_out_stride apart; may be q itself with
+ *              its stride (in place), may not overlap an input otherwise
+ *   pos        device int32 [T][n_axes], 1 <= n_axes <= 4; rope_tab: device
+ *              fp32 [n_pos][rot_dim/2][2] (cos, sin), 16-byte aligned.  A
+ *              position outside [0, n_pos) sets BD_ERR_BAD_INDEX and is taken as 0.
+ *   axis_of_pair  HOST uint8 [rot_dim/2], values below n_axes; NULL = all 0
+ *   slot       device int32 [T]; outside [-1, n_pages * page_size) it sets
+ *              BD_ERR_BAD_INDEX and nothing is written.  Two tokens of one
+ *              call may not name the same slot.
+ * rot_dim: 0 or a multiple of 16 up to head_dim.
+ * ------------------------------------------------------------------------ */
+#define BD_MAX_AXES 4
+
+size_t bd_rope_append_workspace_size(int64_t T);
+
+bd_status bd_rope_append(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                         int64_t v_stride, int64_t T, int32_t n_q, const int32_t* pos, int32_t n_axes,
+                         const uint8_t* axis_of_pair, const float* rope_tab, int64_t n_pos, int32_t rot_dim,
+                         int interleaved, const int32_t* slot, const bd_kv_pages* cache, uint16_t* q_out,
+                         int64_t q_out_stride, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Reading the cache back: tokens 0 .. kv_off[s+1]-kv_off[s]-1 of sequence s
+ * are gathered into rows kv_off[s].. of k_out and v_out, as bf16 (code *
+ * scale rounded once).
+ *   page_table  device int32 [n_seq][max_pages]: token j of sequence s lies
+ *               on page page_table[s][j / page_size], at j % page_size
+ *   kv_off      device int32 [n_seq + 1], nondecreasing, kv_off[0] = 0;
+ *               rows from kv_off[n_seq] on stay as they are
+ *   k_out, v_out  device bf16 [rows][n_kv][head_dim], 16-byte aligned
+ * A page outside [0, n_pages) or a token past max_pages * page_size sets
+ * BD_ERR_BAD_INDEX; its row is written as zeros.
+ * ------------------------------------------------------------------------ */
+size_t bd_kv_read_workspace_size(int64_t rows);
+
+bd_status bd_kv_read(const bd_kv_pages* cache, const int32_t* page_table, int64_t max_pages, const int32_t* kv_off,
+                     int64_t n_seq, int64_t rows, uint16_t* k_out, uint16_t* v_out, void* ws, size_t ws_bytes,
+                     void* stream);
+
+/* ------------------------------------------------------------------------
+ * Attention of new tokens over the paged cache.  Sequence s has the new
+ * tokens q_off[s] .. q_off[s+1]-1 (n of them), which are the last n of its
+ * kv_len[s] tokens in the cache (bd_rope_append has written them).  New
+ * token i of sequence s and query head h, with kv head h / (n_q / n_kv):
+ *   out = sum_j softmax_j(scale * q . k_j) v_j
+ * over j < kv_len[s] and, if `causal`, j <= kv_len[s] - n + i.  A row that
+ * sees no key gives zeros (lse: -infinity).  One token per sequence is a
+ * decode step; any mixture of lengths may share a call.
+ *   q        device bf16 [T] rows of n_q heads, q_stride elements apart (a
+ *            multiple of 8); 16-byte aligned
+ *   q_off    device int32 [n_seq + 1], nondecreasing from 0 to T; tokens that
+ *            no sequence claims are left unwritten
+ *   max_new  the largest number of new tokens of a sequence as far as the
+ *            host knows it; it chooses the kernel, never the result's meaning
+ *   page_table, max_pages  as in bd_kv_read; pages past a sequence's length
+ *            are not looked at, and what the cache holds past the length
+ *            (NaN included) has no influence
+ *   kv_len   device int32 [n_seq]
+ *   out      device bf16 [T][n_q][head_dim], 16-byte aligned
+ *   lse      device fp32 [T][n_q] or NULL: log sum_j exp(scale * q . k_j)
+ * n_q: a positive multiple of n_kv.  The int8 codes enter the tensor cores
+ * as exact bf16 values and their scales multiply the fp32 scores and
+ * probabilities.  Scores, the softmax and all sums are fp32; probabilities
+ * are rounded to bf16 before their product with V.  Results do not depend on
+ * timing (no atomics).  A page outside [0, n_pages), a length outside
+ * [0, max_pages * page_size] or offsets out of order set BD_ERR_BAD_INDEX:
+ * the value is clamped and the sequence's result is undefined.
+ * ------------------------------------------------------------------------ */
+size_t bd_attention_workspace_size(int64_t T, int64_t n_seq, int32_t n_q, int32_t n_kv, int32_t head_dim);
+
+bd_status bd_attention(const uint16_t* q, int64_t q_stride, const int32_t* q_off, int64_t T, int64_t n_seq,
+                       int64_t max_new, int32_t n_q, const bd_kv_pages* cache, const int32_t* page_table,
+                       int64_t max_pages, const int32_t* kv_len, float scale, int causal, uint16_t* out, float* lse,
+                       void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
  * Delta cache -- section "Altyapı ayrıntıları": a variant's packed delta is
