@@ -745,7 +745,7 @@ int bd_debug_bounds_check(uint32_t* kernels)
     const uint32_t f = bd::bounds_take_compress() | bd::bounds_take_skinny() | bd::bounds_take_multi() |
                        bd::bounds_take_prefill() | bd::bounds_take_route() | bd::bounds_take_materialize() |
                        bd::bounds_take_monosoup() | bd::bounds_take_norm() | bd::bounds_take_kv() |
-                       bd::bounds_take_attention();
+                       bd::bounds_take_attention() | bd::bounds_take_attention_chunk();
     if (kernels) *kernels = f;
     if (f == ~0u) return BD_ERR_CUDA;
     return f ? BD_ERR_BOUNDS : BD_OK;

@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
             uint32_t pa[4];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const float mu = m[i] == -INFINITY ? 0.0f : m[i];
+                const float mu = m[i] == -INFINITY ? 0.0f : m[i] - attn_bias<INT8>();
                 const float p0 = exp2f(s[0][2 * i] - mu), p1 = exp2f(s[0][2 * i + 1] - mu);
                 const float p2 = exp2f(s[1][2 * i] - mu), p3 = exp2f(s[1][2 * i + 1] - mu);
                 l[i] += (p0 + p1) + (p2 + p3);
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
             if (q4 == 0) {
-                sh.m[warp][g + 8 * i] = m[i];
+                sh.m[warp][g + 8 * i] = m[i] - attn_bias<INT8>();
                 sh.l[warp][g + 8 * i] = l[i];
             }
         }
@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
             float mm = sh.m[0][g + 8 * i];
 #pragma unroll
             for (int w = 1; w < kMmaConsumers; ++w) mm = fmaxf(mm, sh.m[w][g + 8 * i]);
-            f[i] = attn_weight(m[i], l[i], mm);
+            f[i] = attn_weight(m[i] - attn_bias<INT8>(), l[i], mm);
         }
         for (int w = 0; w < kMmaConsumers; ++w) {
             if (warp == w) {
@@ -610,7 +610,8 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
 constexpr int kJoinThreads = 128;
 
 // Block (c, y): if block c of the main kernel is the second one of some
-// (item, head), joins the parts of that (item, head), rows 4 y .. 4 y + 3.
+// (item, head), joins the parts of that (item, head); a warp takes the rows
+// 4 y + w, 4 (y + gridDim.y) + w, ...
 template <int DIM>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnParams p)
 {
@@ -634,52 +635,53 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     const int last = attn_owner(units, active, start + it.tiles - 1);
     const AttnSeq sq = attn_seq(a, it.seq, false);
     const int rows = sq.n_new * p.G;
-    const int r = 4 * blockIdx.y + (threadIdx.x >> 5);
-    const int row = it.row0 + r;
-    if (r >= p.mb || row >= rows) return;
-
+    const int live = rows - it.row0 < p.mb ? rows - it.row0 : p.mb;
     const int parts = last - c + 2;  // blocks c - 1 .. last
-    float mm = -INFINITY;
-    for (int i = lane; i < parts; i += 32)
-        mm = fmaxf(mm, p.part_ml[static_cast<int64_t>(attn_slot(c - 1 + i, i == 0)) * p.mb + r].x);
+    for (int r = 4 * blockIdx.y + (threadIdx.x >> 5); r < live; r += 4 * gridDim.y) {
+        float mm = -INFINITY;
+        for (int i = lane; i < parts; i += 32)
+            mm = fmaxf(mm, p.part_ml[static_cast<int64_t>(attn_slot(c - 1 + i, i == 0)) * p.mb + r].x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-    float acc[kPer] = {}, ll = 0.0f;
-    for (int i0 = 0; i0 < parts; i0 += 32) {
-        float w = 0.0f, lw = 0.0f;
-        if (i0 + lane < parts) {
-            const float2 ml = p.part_ml[static_cast<int64_t>(attn_slot(c - 1 + i0 + lane, i0 + lane == 0)) * p.mb + r];
-            w = attn_weight(ml.x, ml.y, mm);
-            lw = ml.y;
-        }
-        const int n = parts - i0 < 32 ? parts - i0 : 32;
-        for (int i = 0; i < n; ++i) {
-            const float wi = __shfl_sync(0xffffffffu, w, i), li = __shfl_sync(0xffffffffu, lw, i);
-            const float* src = p.part_o +
-                               (static_cast<int64_t>(attn_slot(c - 1 + i0 + i, i0 + i == 0)) * p.mb + r) * DIM + kPer * lane;
-            float v[kPer];
-            if constexpr (kPer == 4) {
-                const float4 x = *reinterpret_cast<const float4*>(src);
-                v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-            } else {
-                const float2 x = *reinterpret_cast<const float2*>(src);
-                v[0] = x.x, v[1] = x.y;
+        for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+        float acc[kPer] = {}, ll = 0.0f;
+        for (int i0 = 0; i0 < parts; i0 += 32) {
+            float w = 0.0f, lw = 0.0f;
+            if (i0 + lane < parts) {
+                const float2 ml =
+                    p.part_ml[static_cast<int64_t>(attn_slot(c - 1 + i0 + lane, i0 + lane == 0)) * p.mb + r];
+                w = attn_weight(ml.x, ml.y, mm);
+                lw = ml.y;
             }
-            if (wi != 0.0f) {
-                ll += wi * li;
+            const int n = parts - i0 < 32 ? parts - i0 : 32;
+            for (int i = 0; i < n; ++i) {
+                const float wi = __shfl_sync(0xffffffffu, w, i), li = __shfl_sync(0xffffffffu, lw, i);
+                const float* src =
+                    p.part_o + (static_cast<int64_t>(attn_slot(c - 1 + i0 + i, i0 + i == 0)) * p.mb + r) * DIM +
+                    kPer * lane;
+                float v[kPer];
+                if constexpr (kPer == 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(src);
+                    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+                } else {
+                    const float2 x = *reinterpret_cast<const float2*>(src);
+                    v[0] = x.x, v[1] = x.y;
+                }
+                if (wi != 0.0f) {
+                    ll += wi * li;
 #pragma unroll
-                for (int e = 0; e < kPer; ++e) acc[e] += wi * v[e];
+                    for (int e = 0; e < kPer; ++e) acc[e] += wi * v[e];
+                }
             }
         }
+        const int row = it.row0 + r, tok = row / p.G;
+        const int64_t at = (static_cast<int64_t>(sq.q0) + tok) * a.n_q + h * p.G + (row - tok * p.G);
+        if (!bd_in(kBkAttnCombine, at, a.T * a.n_q)) continue;
+        const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + at * DIM + kPer * lane);
+#pragma unroll
+        for (int e = 0; e < kPer; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+        if (lane == 0 && a.lse) a.lse[at] = attn_lse(mm, ll);
     }
-    const int tok = row / p.G;
-    const int64_t at = (static_cast<int64_t>(sq.q0) + tok) * a.n_q + h * p.G + (row - tok * p.G);
-    if (!bd_in(kBkAttnCombine, at, a.T * a.n_q)) return;
-    const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + at * DIM + kPer * lane);
-#pragma unroll
-    for (int e = 0; e < kPer; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-    if (lane == 0 && a.lse) a.lse[at] = attn_lse(mm, ll);
 }
 
 template <int DIM, bool INT8>
@@ -738,7 +740,11 @@ cudaError_t launch_attention_mma(const AttnParams& p, cudaStream_t stream)
 
 size_t attention_workspace_size(int64_t T, int64_t n_seq, int n_q, int n_kv, int dim)
 {
-    return attn_layout(T, n_seq, n_q / n_kv, dim, kMmaRows, kAttnMaxBlocks).total;
+    // the host may learn how long the chunks are only with the call: room for either kernel
+    const int G = n_q / n_kv;
+    const size_t mma = attn_layout(T, n_seq, G, dim, kMmaRows, kAttnMaxBlocks).total;
+    const size_t chunk = attn_layout(T, n_seq, G, dim, kChunkRows, kAttnMaxBlocks / 2).total;
+    return mma > chunk ? mma : chunk;
 }
 
 cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream)
@@ -747,10 +753,13 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream)
     AttnParams p{};
     p.a = a;
     p.G = a.n_q / a.cache.n_kv;
-    p.tile = kMmaTile;
-    p.mb = kMmaRows;
-    p.blocks = 2 * a.sm_count < kAttnMaxBlocks ? 2 * a.sm_count : kAttnMaxBlocks;
-    const AttnWs w = attn_layout(a.T, a.n_seq, p.G, a.cache.dim, p.mb, kAttnMaxBlocks);
+    const bool chunk = a.max_new * p.G > kMmaRows;
+    p.tile = chunk ? kChunkTile : kMmaTile;
+    p.mb = chunk ? kChunkRows : kMmaRows;
+    const int most = chunk ? kAttnMaxBlocks / 2 : kAttnMaxBlocks;
+    p.blocks = chunk ? a.sm_count : 2 * a.sm_count;
+    if (p.blocks > most) p.blocks = most;
+    const AttnWs w = attn_layout(a.T, a.n_seq, p.G, a.cache.dim, p.mb, most);
     char* ws = static_cast<char*>(a.ws);
     p.head = reinterpret_cast<AttnHeader*>(ws + w.head);
     p.item_off = reinterpret_cast<int32_t*>(ws + w.item_off);
@@ -759,8 +768,8 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream)
     p.part_o = reinterpret_cast<float*>(ws + w.o);
     cudaError_t err = cudaSuccess;
     launch_dep(err, attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
-    if (err == cudaSuccess) err = launch_attention_mma(p, stream);
-    const dim3 grid(static_cast<unsigned>(p.blocks > 1 ? p.blocks - 1 : 1), static_cast<unsigned>((p.mb + 3) / 4));
+    if (err == cudaSuccess) err = chunk ? launch_attention_chunk(p, stream) : launch_attention_mma(p, stream);
+    const dim3 grid(static_cast<unsigned>(p.blocks > 1 ? p.blocks - 1 : 1), chunk ? 16 : 4);
     launch_dep(err, a.cache.dim == 128 ? attn_join_kernel<128> : attn_join_kernel<64>, grid, dim3(kJoinThreads), 0,
                stream, p);
     return err;

@@ -116,6 +116,17 @@ __device__ __forceinline__ int attn_find_item(const AttnItem* items, int n_items
 // first tile (its last segment) or later (its first segment).
 __device__ __forceinline__ int attn_slot(int c, bool from_start) { return 2 * c + (from_start ? 1 : 0); }
 
+// Probabilities are formed as exp2(score - maximum + bias): what is far below
+// the maximum stays a normal number when it is rounded to bf16, after the
+// product with an int8 value's scale too.  Numerator and denominator carry
+// the same factor; a stored maximum is the one less the bias.  (Sums overflow
+// only for values above 2^80.)
+template <bool INT8>
+__device__ __forceinline__ constexpr float attn_bias()
+{
+    return INT8 ? 24.0f : 8.0f;
+}
+
 // The factor of a partial sum with maximum m and denominator l when it joins
 // others under the maximum of all: 0 where it has seen no key.  (A maximum of
 // -infinity with a denominator other than 0 is a row of NaN scores, which
@@ -129,6 +140,10 @@ __device__ __forceinline__ float attn_weight(float m, float l, float m_all)
 // Log-sum-exp of a row; m is in units of log2, l == 0 marks a row that saw no key.
 __device__ __forceinline__ float attn_lse(float m, float l) { return l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2; }
 
+// Few rows per sequence (bd_attention.cu): 16 rows an item, 64 keys a tile.
 cudaError_t launch_attention_mma(const AttnParams& p, cudaStream_t stream);
+// Chunks (bd_attention_chunk.cu): 256 rows an item, 128 keys a tile.
+cudaError_t launch_attention_chunk(const AttnParams& p, cudaStream_t stream);
+constexpr int kChunkTile = 128, kChunkRows = 256;
 
 }  // namespace bd

@@ -288,6 +288,7 @@ uint32_t bounds_take_monosoup();
 uint32_t bounds_take_norm();
 uint32_t bounds_take_kv();
 uint32_t bounds_take_attention();
+uint32_t bounds_take_attention_chunk();
 
 int monosoup_max_l();
 size_t monosoup_workspace_size(int64_t d_out, int64_t d_in, int k, int r, int l);
