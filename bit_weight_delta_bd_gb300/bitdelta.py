@@ -97,6 +97,8 @@ _i64, _i32, _vp, _sz, _int = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ct
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libbitdelta.so (built by ``bit_weight_delta_bd_gb300.build``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -171,6 +173,10 @@ _BF16_LIKE = (torch.bfloat16, torch.uint16, torch.int16)
 
 
 def _ptr(t: torch.Tensor | None, name: str, dtypes=None, allow_none: bool = False) -> int | None:
+    # the usual case first: a call's checks cost more host time than a small kernel takes
+    if (t is not None and t.is_cuda and t.get_device() == _device() and (dtypes is None or t.dtype in dtypes)
+            and t.is_contiguous()):
+        return t.data_ptr()
     if t is None:
         if allow_none:
             return None
@@ -181,14 +187,17 @@ def _ptr(t: torch.Tensor | None, name: str, dtypes=None, allow_none: bool = Fals
         raise ValueError(f"{name} is on {t.device}, not the current device")
     if dtypes is not None and t.dtype not in dtypes:
         raise ValueError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
+
+
+# torch's own short ways to the current device and stream (the public ones
+# check the initialisation and build a Stream object on every call: 3 us)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _stream(stream) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    return _raw_stream(_device()) if stream is None else stream.cuda_stream
 
 
 def _ws(ws: torch.Tensor) -> tuple[int, int]:
@@ -311,10 +320,10 @@ def bd_rms_norm(x, gain, eps, out, ws, residual=None, residual_out=None, scale=N
     """out = norm(x + residual) * gain (the gain of token t's variant, vid[t], out of gain_list); out bf16, fp32, or
     e4m3 with scale [T]; residual_out (which may be residual itself) receives x + residual."""
     T, d = x.shape
-    if tuple(gain.shape) != (d,) or tuple(out.shape) != (T, d):
+    if gain.shape != (d,) or out.shape != x.shape:
         raise ValueError("gain must have the shape [d] and out that of x")
     for name, t in (("residual", residual), ("residual_out", residual_out)):
-        if t is not None and tuple(t.shape) != (T, d):
+        if t is not None and t.shape != x.shape:
             raise ValueError(f"{name} shape differs from x")
     if scale is not None and scale.numel() != T:
         raise ValueError("scale must have one value per row")
@@ -323,7 +332,7 @@ def bd_rms_norm(x, gain, eps, out, ws, residual=None, residual_out=None, scale=N
     tab, V = None, 0
     if vid is not None:
         V = len(gain_list)
-        if any(tuple(t.shape) != (d,) for t in gain_list):
+        if any(t.shape != gain.shape for t in gain_list):
             raise ValueError("every gain must have the shape [d]")
         tab = (ctypes.c_void_p * max(V, 1))(*[_ptr(t, "gain", _BF16_LIKE) for t in gain_list])
     out_dtype = _OUT_DTYPES.get(out.dtype)
@@ -370,13 +379,15 @@ class KvPages:
 
 def _heads(t, name: str, dim: int) -> tuple[int, int]:
     """(pointer, row stride) of a bf16 [T][heads][dim] tensor whose rows may be apart."""
-    if t.dim() != 3 or t.shape[2] != dim or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dim):
+    T, heads, d = t.shape
+    s0, s1, s2 = t.stride()
+    if d != dim or s2 != 1 or (heads > 1 and s1 != dim):
         raise ValueError(f"{name} must be [T][heads][{dim}] with contiguous rows")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if not t.is_cuda or t.get_device() != _device():
         raise ValueError(f"{name} must be on the current CUDA device")
     if t.dtype not in _BF16_LIKE:
         raise ValueError(f"{name} has dtype {t.dtype}, expected one of {_BF16_LIKE}")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1] * dim)
+    return t.data_ptr(), (s0 if T > 1 else heads * dim)
 
 
 def bd_rope_append_workspace_size(T: int) -> int:

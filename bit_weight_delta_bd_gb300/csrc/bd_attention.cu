@@ -140,7 +140,132 @@ struct MmaShared {
     float m[kMmaConsumers][kMmaRows];
     float l[kMmaConsumers][kMmaRows];
     volatile int abort;
+    int64_t scan[kMmaThreads / 32];
+    int seq, row0;      // the block's first item,
+    int64_t before;     // and the units before it
 };
+
+// Key tiles of one head of the item of sequence q that starts at row0.
+__device__ __forceinline__ int mma_tiles(const AttnParams& p, const AttnSeq& q, int row0)
+{
+    int last = row0 + kMmaRows - 1;
+    const int rows = q.n_new * p.G;
+    if (last >= rows) last = rows - 1;
+    const int end = attn_seen(q, last / p.G, p.a.causal);
+    return end > 0 ? (end + kMmaTile - 1) / kMmaTile : 1;
+}
+
+// What a block does next: key tiles [t0, t1) of one (item, kv head).
+struct MmaSegment {
+    AttnSeq sq;
+    int seq, row0, rows, tiles;
+    int h, t0, t1;
+};
+
+// A block's segments in order.  The lengths of the next sequence are loaded
+// while the present one is worked on.
+struct MmaWalk {
+    const AttnParams& p;
+    int64_t u, end, before;  // next unit, last one + 1, units before the present item
+    MmaSegment s;
+    AttnSeq ahead;
+
+    __device__ __forceinline__ MmaWalk(const AttnParams& pp, int64_t u0, int64_t u1, int seq, int row0, int64_t b)
+        : p(pp), u(u0), end(u1), before(b)
+    {
+        if (u >= end) return;
+        s.seq = seq;
+        s.row0 = row0;
+        s.sq = attn_seq(p.a, seq, false);
+        s.rows = s.sq.n_new * p.G;
+        s.tiles = mma_tiles(p, s.sq, row0);
+        look_ahead();
+    }
+    __device__ __forceinline__ void look_ahead()
+    {
+        if (s.seq + 1 < p.a.n_seq) ahead = attn_seq(p.a, s.seq + 1, false);
+    }
+    __device__ __forceinline__ bool next()
+    {
+        if (u >= end) return false;
+        const int n_kv = p.a.cache.n_kv;
+        while (u - before >= static_cast<int64_t>(s.tiles) * n_kv) {  // on to the next item
+            before += static_cast<int64_t>(s.tiles) * n_kv;
+            s.row0 += kMmaRows;
+            while (s.row0 >= s.rows && s.seq + 1 < p.a.n_seq) {
+                ++s.seq;
+                s.sq = ahead;
+                s.rows = s.sq.n_new * p.G;
+                s.row0 = 0;
+                look_ahead();
+            }
+            s.tiles = mma_tiles(p, s.sq, s.row0);
+        }
+        const int64_t rel = u - before;
+        s.h = static_cast<int>(rel / s.tiles);
+        s.t0 = static_cast<int>(rel - static_cast<int64_t>(s.h) * s.tiles);
+        const int64_t left = end - u;
+        s.t1 = left < s.tiles - s.t0 ? s.t0 + static_cast<int>(left) : s.tiles;
+        u += s.t1 - s.t0;
+        return true;
+    }
+};
+
+// The whole block: adds up the tiles of all sequences (each thread those of
+// consecutive ones) and finds the item of the block's first unit.  Returns
+// the units of the call.
+__device__ __forceinline__ int64_t mma_deal(const AttnParams& p, MmaShared& sh)
+{
+    const AttentionArgs& a = p.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int n_seq = static_cast<int>(a.n_seq);
+    const int per = (n_seq + kMmaThreads - 1) / kMmaThreads;
+    const int s0 = static_cast<int>(threadIdx.x) * per < n_seq ? threadIdx.x * per : n_seq;
+    const int s1 = s0 + per < n_seq ? s0 + per : n_seq;
+    int64_t mine = 0;
+    for (int s = s0; s < s1; ++s) {
+        const AttnSeq q = attn_seq(a, s, blockIdx.x == 0);
+        for (int row0 = 0; row0 < q.n_new * p.G; row0 += kMmaRows) mine += mma_tiles(p, q, row0);
+    }
+    int64_t x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) sh.scan[warp] = x;
+    __syncthreads();
+    int64_t total = 0, at = x - mine;
+#pragma unroll
+    for (int w = 0; w < kMmaThreads / 32; ++w) {
+        if (w < warp) at += sh.scan[w];
+        total += sh.scan[w];
+    }
+    const int n_kv = a.cache.n_kv;
+    const int64_t units = total * n_kv;
+    const int active = attn_active(units, p.blocks);
+    if (static_cast<int>(blockIdx.x) < active) {
+        const int64_t u = attn_first(units, active, blockIdx.x);
+        if (u >= at * n_kv && u < (at + mine) * n_kv) {
+            // this thread's sequences hold it
+            int64_t before = at * n_kv;
+            for (int s = s0; s < s1; ++s) {
+                const AttnSeq q = attn_seq(a, s, false);
+                for (int row0 = 0; row0 < q.n_new * p.G; row0 += kMmaRows) {
+                    const int64_t n = static_cast<int64_t>(mma_tiles(p, q, row0)) * n_kv;
+                    if (u >= before && u < before + n) {
+                        sh.seq = s;
+                        sh.row0 = row0;
+                        sh.before = before;
+                    }
+                    before += n;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    return units;
+}
 
 __device__ __forceinline__ bool attn_wait(volatile int* abort_flag, uint64_t* bar, uint32_t parity, uint32_t* err)
 {
@@ -238,15 +363,24 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
     __syncthreads();
     grid_dependency_wait();
 
-    const AttnHeader head = *p.head;
     const int n_kv = cache.n_kv;
-    const int64_t units = static_cast<int64_t>(head.tiles) * n_kv;
+    const int64_t units = mma_deal(p, sh);
     const int active = attn_active(units, p.blocks);
     const int c = blockIdx.x;
+    MmaWalk walk(p, c < active ? attn_first(units, active, c) : 0, c < active ? attn_first(units, active, c + 1) : 0,
+                 sh.seq, sh.row0, sh.before);
+    if (threadIdx.x == 0) {
+        AttnJoin j{0, 0, 0, 0};
+        if (c < active) {
+            const int64_t rel = walk.u - walk.before;
+            const int h = static_cast<int>(rel / walk.s.tiles);
+            j = attn_join_of(units, active, c, walk.u, walk.before + static_cast<int64_t>(h) * walk.s.tiles,
+                             walk.s.tiles, walk.s.seq, walk.s.row0, h);
+        }
+        p.joins[c] = j;
+    }
     if (c >= active) return;
-    const int64_t u_end = attn_first(units, active, c + 1);
-    int64_t u = attn_first(units, active, c);
-    int item = attn_find_item(p.items, head.n_items, n_kv, u);
+    const MmaSegment& sg = walk.s;
     int stage = 0;
     uint32_t phase = 0;
 
@@ -254,17 +388,11 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
         // ------------------------------------------------------------ producer warp
         const int box_rows = cache.page < kMmaTile ? cache.page : kMmaTile;
         const int pages_per_tile = kMmaTile / box_rows;
-        while (u < u_end) {
-            const AttnItem it = p.items[item];
-            const int64_t rel = u - static_cast<int64_t>(it.before) * n_kv;
-            const int h = static_cast<int>(rel / it.tiles);
-            const int t0 = static_cast<int>(rel - static_cast<int64_t>(h) * it.tiles);
-            const int64_t left = u_end - u;
-            const int t1 = left < it.tiles - t0 ? t0 + static_cast<int>(left) : it.tiles;
-            const AttnSeq sq = attn_seq(a, it.seq, false);
-            const int32_t* table = a.table + static_cast<int64_t>(it.seq) * a.max_pages;
-            const int pages = (sq.len + cache.page - 1) >> cache.page_shift;  // that the sequence has
-            for (int t = t0; t < t1; ++t) {
+        while (walk.next()) {
+            const int h = sg.h;
+            const int32_t* table = a.table + static_cast<int64_t>(sg.seq) * a.max_pages;
+            const int pages = (sg.sq.len + cache.page - 1) >> cache.page_shift;  // that the sequence has
+            for (int t = sg.t0; t < sg.t1; ++t) {
                 // lane j looks after the j-th box of the tile
                 const int key = t * kMmaTile + lane * box_rows;
                 const int at = key >> cache.page_shift;
@@ -316,8 +444,6 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
                     phase ^= 1;
                 }
             }
-            u += t1 - t0;
-            if (t1 == it.tiles && h == n_kv - 1) ++item;
         }
         return;
     }
@@ -325,22 +451,16 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
     // ---------------------------------------------------------------- consumer warps
     const int g = lane >> 2, q4 = lane & 3;
     const float c2 = a.scale * kLog2e;
-    while (u < u_end) {
-        const AttnItem it = p.items[item];
-        const int64_t rel = u - static_cast<int64_t>(it.before) * n_kv;
-        const int h = static_cast<int>(rel / it.tiles);
-        const int t0 = static_cast<int>(rel - static_cast<int64_t>(h) * it.tiles);
-        const int64_t left = u_end - u;
-        const int t1 = left < it.tiles - t0 ? t0 + static_cast<int>(left) : it.tiles;
-        const AttnSeq sq = attn_seq(a, it.seq, false);
-        const int rows = sq.n_new * p.G;
+    while (walk.next()) {
+        const AttnSeq sq = sg.sq;
+        const int h = sg.h, t0 = sg.t0, t1 = sg.t1, rows = sg.rows, row0 = sg.row0;
 
         // the two rows of this thread: keys they see, and q as A fragments
         int seen[2];
         uint32_t qf[kSteps][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int r = it.row0 + g + 8 * i;
+            const int r = row0 + g + 8 * i;
             const bool live = r < rows;
             const int tok = live ? r / p.G : 0;
             seen[i] = live ? attn_seen(sq, tok, a.causal) : 0;
@@ -357,7 +477,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
             }
         }
         // the keys that every live row sees: tiles below need no mask
-        const int first_row_tok = it.row0 / p.G;
+        const int first_row_tok = row0 / p.G;
         const int all_seen = attn_seen(sq, first_row_tok, a.causal);
 
         float o[2 * kSteps][4];
@@ -567,9 +687,9 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
             consumers_sync();
         }
 
-        const bool whole = t0 == 0 && t1 == it.tiles;
+        const bool whole = t0 == 0 && t1 == sg.tiles;
         const int slot = attn_slot(c, t0 == 0);
-        const int live_rows = rows - it.row0 < kMmaRows ? rows - it.row0 : kMmaRows;
+        const int live_rows = rows - row0 < kMmaRows ? rows - row0 : kMmaRows;
         for (int i = threadIdx.x; i < live_rows * (DIM / 4); i += 32 * kMmaConsumers) {
             const int r = i / (DIM / 4), d = 4 * (i % (DIM / 4));
             float mm = sh.m[0][r];
@@ -583,7 +703,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
             }
             const float4 v = *reinterpret_cast<const float4*>(buf + r * DIM + d);
             if (whole) {
-                const int row = it.row0 + r, tok = row / p.G;
+                const int row = row0 + r, tok = row / p.G;
                 const int64_t at = (static_cast<int64_t>(sq.q0) + tok) * a.n_q + h * p.G + (row - tok * p.G);
                 const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
                 if (bd_in(kBkAttn, at, a.T * a.n_q)) {
@@ -600,8 +720,6 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
             }
         }
         consumers_sync();  // the buffers are free for the next item
-        u += t1 - t0;
-        if (t1 == it.tiles && h == n_kv - 1) ++item;
     }
 }
 
@@ -609,8 +727,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
 
 constexpr int kJoinThreads = 128;
 
-// Block (c, y): if block c of the main kernel is the second one of some
-// (item, head), joins the parts of that (item, head); a warp takes the rows
+// Block (c, y): joins what block c of the main kernel noted down; a warp takes the rows
 // 4 y + w, 4 (y + gridDim.y) + w, ...
 template <int DIM>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnParams p)
@@ -619,24 +736,14 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     grid_launch_dependents();
     grid_dependency_wait();
     const AttentionArgs& a = p.a;
-    const AttnHeader head = *p.head;
-    const int n_kv = a.cache.n_kv;
-    const int64_t units = static_cast<int64_t>(head.tiles) * n_kv;
-    const int active = attn_active(units, p.blocks);
     const int c = blockIdx.x + 1;
-    if (c >= active) return;
+    const AttnJoin it = p.joins[c];
+    if (it.parts == 0) return;
     const int lane = threadIdx.x & 31;
-    const int64_t u = attn_first(units, active, c);
-    const AttnItem it = p.items[attn_find_item(p.items, head.n_items, n_kv, u)];
-    const int64_t rel = u - static_cast<int64_t>(it.before) * n_kv;
-    const int h = static_cast<int>(rel / it.tiles);
-    const int64_t start = static_cast<int64_t>(it.before) * n_kv + static_cast<int64_t>(h) * it.tiles;
-    if (start == u || attn_owner(units, active, start) != c - 1) return;
-    const int last = attn_owner(units, active, start + it.tiles - 1);
+    const int h = it.h, parts = it.parts;
     const AttnSeq sq = attn_seq(a, it.seq, false);
     const int rows = sq.n_new * p.G;
     const int live = rows - it.row0 < p.mb ? rows - it.row0 : p.mb;
-    const int parts = last - c + 2;  // blocks c - 1 .. last
     for (int r = 4 * blockIdx.y + (threadIdx.x >> 5); r < live; r += 4 * gridDim.y) {
         float mm = -INFINITY;
         for (int i = lane; i < parts; i += 32)
@@ -713,7 +820,7 @@ cudaError_t launch_mma_shape(const AttnParams& p, cudaStream_t stream)
 constexpr size_t align_up(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 struct AttnWs {
-    size_t head, item_off, items, ml, o, total;
+    size_t head, item_off, items, joins, ml, o, total;
 };
 
 AttnWs attn_layout(int64_t T, int64_t n_seq, int64_t G, int dim, int mb, int blocks)
@@ -723,7 +830,8 @@ AttnWs attn_layout(int64_t T, int64_t n_seq, int64_t G, int dim, int mb, int blo
     w.item_off = w.head + 256;
     w.items = w.item_off + align_up(static_cast<size_t>(n_seq + 1) * 4);
     const size_t items = static_cast<size_t>((T * G + mb - 1) / mb + n_seq);
-    w.ml = w.items + align_up(items * sizeof(AttnItem));
+    w.joins = w.items + align_up(items * sizeof(AttnItem));
+    w.ml = w.joins + align_up(static_cast<size_t>(blocks) * sizeof(AttnJoin));
     w.o = w.ml + align_up(static_cast<size_t>(2 * blocks) * mb * 8);
     w.total = w.o + align_up(static_cast<size_t>(2 * blocks) * mb * dim * 4);
     return w;
@@ -764,10 +872,11 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream)
     p.head = reinterpret_cast<AttnHeader*>(ws + w.head);
     p.item_off = reinterpret_cast<int32_t*>(ws + w.item_off);
     p.items = reinterpret_cast<AttnItem*>(ws + w.items);
+    p.joins = reinterpret_cast<AttnJoin*>(ws + w.joins);
     p.part_ml = reinterpret_cast<float2*>(ws + w.ml);
     p.part_o = reinterpret_cast<float*>(ws + w.o);
     cudaError_t err = cudaSuccess;
-    launch_dep(err, attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
+    if (chunk) launch_dep(err, attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
     if (err == cudaSuccess) err = chunk ? launch_attention_chunk(p, stream) : launch_attention_mma(p, stream);
     const dim3 grid(static_cast<unsigned>(p.blocks > 1 ? p.blocks - 1 : 1), chunk ? 16 : 4);
     launch_dep(err, a.cache.dim == 128 ? attn_join_kernel<128> : attn_join_kernel<64>, grid, dim3(kJoinThreads), 0,

@@ -12,8 +12,15 @@
 // the lengths are, a long sequence is split over many blocks, and a short
 // one shares its block with others.  A block that does not see all tiles of
 // an (item, head) leaves its unnormalised sum, maximum and denominator in the
-// workspace; at most its first and its last are of that kind, and the join
-// adds them in block order, so results do not depend on timing.
+// workspace; at most its first and its last are of that kind.  The second
+// block of such an (item, head) notes it down, and the join adds its parts in
+// block order, so results do not depend on timing.
+//
+// Finding its units.  The decode kernel's blocks work the deal out from the
+// lengths by themselves (one load per sequence and a scan: no launch before
+// theirs, which is what a small call's time would go into); for chunks, whose
+// items differ in length within a sequence, a one-block kernel lists the
+// items first.
 #pragma once
 
 #include "bd_device.cuh"
@@ -31,6 +38,12 @@ struct AttnItem {
     int before;  // tiles of one head of the items before this one
 };
 
+// The (item, head) whose parts the join adds at block c: parts of blocks
+// c - 1 .. c + parts - 2; parts == 0: none.
+struct AttnJoin {
+    int seq, row0, h, parts;
+};
+
 struct AttnHeader {
     int n_items;
     int tiles;  // of one head, over all items
@@ -44,6 +57,7 @@ struct AttnParams {
     AttnHeader* head;
     AttnItem* items;
     int32_t* item_off;    // [n_seq + 1] first item of a sequence
+    AttnJoin* joins;      // [N]
     float* part_o;        // [2 N][mb][dim]
     float2* part_ml;      // [2 N][mb] (maximum in log2 units, denominator)
 };
@@ -91,6 +105,16 @@ __device__ __forceinline__ int64_t attn_first(int64_t units, int n, int c) { ret
 __device__ __forceinline__ int attn_owner(int64_t units, int n, int64_t u)
 {
     return static_cast<int>(((u + 1) * n - 1) / units);
+}
+
+// What block c, whose first unit u lies in the (item, head) with units
+// [start, start + tiles), notes down for the join.
+__device__ __forceinline__ AttnJoin attn_join_of(int64_t units, int n, int c, int64_t u, int64_t start, int tiles,
+                                                 int seq, int row0, int h)
+{
+    AttnJoin j{seq, row0, h, 0};
+    if (start != u && attn_owner(units, n, start) == c - 1) j.parts = attn_owner(units, n, start + tiles - 1) - c + 2;
+    return j;
 }
 
 // The item that unit u belongs to: the last i with n_kv * before <= u.  All
