@@ -8,19 +8,26 @@
 //
 // The decode kernel is bound by the cache's bytes.  One thread of a producer
 // warp's tile keeps a ring of stages (64 keys: K, V, scales) filled by TMA,
-// one box per page; four consumer warps take 16 keys of each stage each, with
-// a running maximum, denominator and 16 x dim sum of their own, so that
-// nothing is exchanged between warps until an item ends.  Rows are the 16
-// rows of m16n8k16 (query heads that share a kv head), keys its columns.
+// one box per page; four consumer warps take turns, two of them 32 keys each
+// of every other stage, with a running maximum, denominator and 16 x dim sum
+// of their own, so that nothing is exchanged between warps until an item
+// ends.  Rows are the 16 rows of m16n8k16 (query heads that share a kv head),
+// keys its columns.
 //
-// Int8.  Codes become bf16 exactly: with r the byte, 0x4300 | (r & 0x7f) is
-// 128 + (r & 0x7f) and 0x4300 | (r & 0x80) is 128 or 256, and their
-// difference is the code; one byte permute, two logic operations and one
-// packed subtraction for two codes.  K's scale multiplies the fp32 score, V's
-// the fp32 probability.
+// Int8.  Both products run in fp16, which holds the codes exactly: with u =
+// code + 128 the bits 0x6400 | u are 1024 + u, and one logic operation and
+// one packed addition give two codes (bf16, whose 8 bits have no room for u,
+// takes twice as many).  q is scaled per row by the power of two that brings
+// its largest element to 2^14 .. 2^15: its bf16 values are then exact in fp16
+// down to 2^-29 of that element.  K's scale multiplies the fp32 score.  V's
+// scale multiplies the fp32 probability, and the product enters fp16 over a
+// power of two that follows the largest scale seen, so that it stays below
+// 2^15 and what is rounded away lies 2^-40 below the largest.  Probabilities
+// so keep 11 bits, where a bf16 cache's, rounded to bf16 like its values, keep 8.
+
 #include "bd_attention.cuh"
 
-#include <climits>
+#include <cuda_fp16.h>
 
 #include "bd_tma.h"
 
@@ -114,6 +121,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
 constexpr int kMmaTile = 64;     // keys of a stage
 constexpr int kMmaRows = 16;     // rows of an item
 constexpr int kMmaConsumers = 4;
+constexpr int kMmaKeys = 32;     // keys of a stage that one warp takes
 constexpr int kMmaThreads = 32 * (kMmaConsumers + 1);
 constexpr int kMmaMaxStages = 8;
 
@@ -131,7 +139,7 @@ struct MmaShape {
     static constexpr int kHalfBytes = kMmaTile * kBoxBytes;
     static constexpr int kTileBytes = kMmaTile * kRowBytes;               // K (or V) of a stage
     static constexpr int kStageBytes = 2 * kTileBytes + (INT8 ? 1024 : 0);  // stages stay 1024-byte aligned
-    static constexpr int kBufBytes = kMmaRows * DIM * 4;                  // the block's sum of an item
+    static constexpr int kBufBytes = 2 * kMmaRows * DIM * 4;              // sums of an item, two warps each
 };
 
 struct MmaShared {
@@ -202,7 +210,7 @@ struct MmaWalk {
             s.tiles = mma_tiles(p, s.sq, s.row0);
         }
         const int64_t rel = u - before;
-        s.h = static_cast<int>(rel / s.tiles);
+        s.h = attn_div(rel, s.tiles);
         s.t0 = static_cast<int>(rel - static_cast<int64_t>(s.h) * s.tiles);
         const int64_t left = end - u;
         s.t1 = left < s.tiles - s.t0 ? s.t0 + static_cast<int>(left) : s.tiles;
@@ -307,14 +315,42 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4])
                  : "memory");
 }
 
-// Two int8 codes, the bytes that `sel` picks from r, as a pair of bf16.
-__device__ __forceinline__ uint32_t codes_bf16x2(uint32_t r, uint32_t sel)
+// Two int8 codes, bytes 0 and 2 of r, as a pair of fp16.
+__device__ __forceinline__ uint32_t codes_f16x2(uint32_t r)
 {
-    const uint32_t x = __byte_perm(r, 0x43434343u, sel);
-    const uint32_t hi = x & 0xFF7FFF7Fu, lo = x & 0xFF80FF80u;
-    const __nv_bfloat162 d =
-        __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&hi), *reinterpret_cast<const __nv_bfloat162*>(&lo));
+    const uint32_t x = (r & 0x00FF00FFu) ^ 0x64806480u;  // 1024 + 128 + code
+    const uint32_t offset = 0xE480E480u;                 // -1152
+    const __half2 d = __hadd2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&offset));
     return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    const __half2 r = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 2^e with e the exponent of |x| (x normal), kept within 2^-100 .. 2^100
+__device__ __forceinline__ float pow2_of(float x)
+{
+    const float c = fminf(fmaxf(fabsf(x), 7.9e-31f), 1.2e30f);
+    return __uint_as_float(__float_as_uint(c) & 0x7F800000u);
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
@@ -341,10 +377,11 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
 {
     using S = MmaShape<DIM, INT8>;
     constexpr int kSteps = DIM / 16;  // MMA steps of q . k, and pairs of 8-dim tiles of the output
-    extern __shared__ uint8_t dyn_raw[];
-    __shared__ MmaShared sh;
-    uint8_t* ring = dyn_raw + ((1024u - (smem_u32(dyn_raw) & 1023u)) & 1023u);
+    // all of it dynamic: the ring starts on a 1024-byte boundary without padding
+    extern __shared__ __align__(1024) uint8_t dyn_raw[];
+    uint8_t* ring = dyn_raw;
     float* buf = reinterpret_cast<float*>(ring + static_cast<size_t>(mp.stages) * S::kStageBytes);
+    MmaShared& sh = *reinterpret_cast<MmaShared*>(reinterpret_cast<uint8_t*>(buf) + S::kBufBytes);
 
     const AttnParams& p = mp.p;
     const AttentionArgs& a = p.a;
@@ -353,6 +390,8 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
 
     grid_launch_dependents();
     if (threadIdx.x == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&mp.k_map)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&mp.v_map)) : "memory");
         for (int s = 0; s < mp.stages; ++s) {
             mbar_init(&sh.full[s], 1);
             mbar_init(&sh.empty[s], kMmaConsumers);
@@ -373,7 +412,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
         AttnJoin j{0, 0, 0, 0};
         if (c < active) {
             const int64_t rel = walk.u - walk.before;
-            const int h = static_cast<int>(rel / walk.s.tiles);
+            const int h = attn_div(rel, walk.s.tiles);
             j = attn_join_of(units, active, c, walk.u, walk.before + static_cast<int64_t>(h) * walk.s.tiles,
                              walk.s.tiles, walk.s.seq, walk.s.row0, h);
         }
@@ -451,12 +490,14 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
     // ---------------------------------------------------------------- consumer warps
     const int g = lane >> 2, q4 = lane & 3;
     const float c2 = a.scale * kLog2e;
+    int turn = 0;  // stages so far: this warp takes those of its parity
     while (walk.next()) {
         const AttnSeq sq = sg.sq;
         const int h = sg.h, t0 = sg.t0, t1 = sg.t1, rows = sg.rows, row0 = sg.row0;
 
-        // the two rows of this thread: keys they see, and q as A fragments
+        // the two rows of this thread: keys they see, q as A fragments, and the factor of their scores
         int seen[2];
+        float cr[2] = {c2, c2};
         uint32_t qf[kSteps][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -466,19 +507,40 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
             seen[i] = live ? attn_seen(sq, tok, a.causal) : 0;
             const uint16_t* src = a.q + (static_cast<int64_t>(sq.q0) + tok) * a.q_stride +
                                   static_cast<int64_t>(h * p.G + (live ? r - tok * p.G : 0)) * DIM;
+            if constexpr (INT8) {
+                // a code fragment holds dims 4 q4 + {0, 2} and 4 q4 + {1, 3} of a step's 16
+                float v[kSteps][4];
+                float big = 0.0f;
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-                // int8 keys: the byte order of a code fragment is a permutation of the 16 dims of a
-                // step, taken here for q as well
-                const int lo = INT8 ? 16 * k + 4 * q4 : 16 * k + 2 * q4;
-                const int hi = INT8 ? lo + 2 : lo + 8;
-                qf[k][i] = live ? *reinterpret_cast<const uint32_t*>(src + lo) : 0u;
-                qf[k][i + 2] = live ? *reinterpret_cast<const uint32_t*>(src + hi) : 0u;
+                for (int k = 0; k < kSteps; ++k) {
+                    const uint2 w = live ? *reinterpret_cast<const uint2*>(src + 16 * k + 4 * q4) : make_uint2(0, 0);
+                    v[k][0] = __uint_as_float(w.x << 16);
+                    v[k][1] = __uint_as_float(w.x & 0xFFFF0000u);
+                    v[k][2] = __uint_as_float(w.y << 16);
+                    v[k][3] = __uint_as_float(w.y & 0xFFFF0000u);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) big = fmaxf(big, fabsf(v[k][e]));
+                }
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                const float unit = pow2_of(big), f = 16384.0f / unit;
+                cr[i] = c2 * (unit / 16384.0f);
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                    qf[k][i] = pack_f16x2(v[k][0] * f, v[k][2] * f);
+                    qf[k][i + 2] = pack_f16x2(v[k][1] * f, v[k][3] * f);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                    const int d = 16 * k + 2 * q4;
+                    qf[k][i] = live ? *reinterpret_cast<const uint32_t*>(src + d) : 0u;
+                    qf[k][i + 2] = live ? *reinterpret_cast<const uint32_t*>(src + d + 8) : 0u;
+                }
             }
         }
-        // the keys that every live row sees: tiles below need no mask
-        const int first_row_tok = row0 / p.G;
-        const int all_seen = attn_seen(sq, first_row_tok, a.causal);
+        // the keys that every live row sees: below, no mask is needed
+        const int all_seen = attn_seen(sq, row0 / p.G, a.causal);
 
         float o[2 * kSteps][4];
 #pragma unroll
@@ -486,102 +548,115 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+        float v_unit = 0.0f;  // int8: power of two at or above every scale of V so far, times 2^(bias - 15)
 
-        for (int t = t0; t < t1; ++t) {
-            // on a timeout (reported) the warps still meet at the barriers below, item by item
-            if (!attn_wait(&sh.abort, &sh.full[stage], phase, a.err)) break;
+        for (int t = t0; t < t1; ++t, ++turn) {
+            // every warp waits for every stage and hands it back, the ones that are not its own at once:
+            // a warp that did neither could be two phases away from a barrier, which its parity cannot
+            // tell from none.  On a timeout (reported) the warps still meet at the barriers below.
+            if (!__all_sync(0xffffffffu, attn_wait(&sh.abort, &sh.full[stage], phase, a.err))) {
+                turn += t1 - t;
+                break;
+            }
+            if ((turn & 1) != (warp >> 1)) {
+                if (lane == 0) mbar_arrive(&sh.empty[stage]);
+                if (++stage == mp.stages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+                continue;
+            }
             const uint32_t st = smem_u32(ring) + static_cast<uint32_t>(stage) * S::kStageBytes;
-            const int slice = 16 * warp;            // this warp's keys of the stage
-            const int key0 = t * kMmaTile + slice;  // and in the sequence
-
-            // ---- scores of 16 rows x 16 keys: s[0] keys 0..7, s[1] keys 8..15
-            float s[2][4] = {};
+            const int slice = kMmaKeys * (warp & 1);  // this warp's keys of the stage
+            const int key0 = t * kMmaTile + slice;    // and in the sequence
             const int mi = lane >> 3, mr = lane & 7;
+
+            // ---- scores of 16 rows x 32 keys: s[n] keys 8 n .. 8 n + 7
+            float s[4][4] = {};
             if constexpr (INT8) {
-                const int row = slice + (mi & 1) * 8 + mr;
 #pragma unroll
-                for (int k = 0; k < kSteps; k += 2) {
-                    uint32_t r[4];
-                    ldsm_x4(st + swizzled<S::kBoxBytes>(row, k + (mi >> 1)), r);
-                    mma_bf16_16816(s[0], qf[k][0], qf[k][1], qf[k][2], qf[k][3], codes_bf16x2(r[0], 0x4140),
-                                   codes_bf16x2(r[0], 0x4342));
-                    mma_bf16_16816(s[1], qf[k][0], qf[k][1], qf[k][2], qf[k][3], codes_bf16x2(r[1], 0x4140),
-                                   codes_bf16x2(r[1], 0x4342));
-                    mma_bf16_16816(s[0], qf[k + 1][0], qf[k + 1][1], qf[k + 1][2], qf[k + 1][3],
-                                   codes_bf16x2(r[2], 0x4140), codes_bf16x2(r[2], 0x4342));
-                    mma_bf16_16816(s[1], qf[k + 1][0], qf[k + 1][1], qf[k + 1][2], qf[k + 1][3],
-                                   codes_bf16x2(r[3], 0x4140), codes_bf16x2(r[3], 0x4342));
-                }
+                for (int k = 0; k < kSteps; k += 2)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        uint32_t r[4];
+                        ldsm_x4(st + swizzled<S::kBoxBytes>(slice + 16 * b + (mi & 1) * 8 + mr, k + (mi >> 1)), r);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            mma_f16_16816(s[2 * b + (x & 1)], qf[k + (x >> 1)][0], qf[k + (x >> 1)][1],
+                                          qf[k + (x >> 1)][2], qf[k + (x >> 1)][3], codes_f16x2(r[x]),
+                                          codes_f16x2(r[x] >> 8));
+                    }
             } else {
-                const int row = slice + (mi >> 1) * 8 + mr;
 #pragma unroll
-                for (int k = 0; k < kSteps; ++k) {
-                    uint32_t r[4];
-                    const int chunk = 2 * k + (mi & 1);
-                    ldsm_x4(st + (chunk >> 3) * S::kHalfBytes + swizzled<S::kBoxBytes>(row, chunk & 7), r);
-                    mma_bf16_16816(s[0], qf[k][0], qf[k][1], qf[k][2], qf[k][3], r[0], r[1]);
-                    mma_bf16_16816(s[1], qf[k][0], qf[k][1], qf[k][2], qf[k][3], r[2], r[3]);
-                }
+                for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        uint32_t r[4];
+                        const int chunk = 2 * k + (mi & 1), row = slice + 16 * b + (mi >> 1) * 8 + mr;
+                        ldsm_x4(st + (chunk >> 3) * S::kHalfBytes + swizzled<S::kBoxBytes>(row, chunk & 7), r);
+                        mma_bf16_16816(s[2 * b], qf[k][0], qf[k][1], qf[k][2], qf[k][3], r[0], r[1]);
+                        mma_bf16_16816(s[2 * b + 1], qf[k][0], qf[k][1], qf[k][2], qf[k][3], r[2], r[3]);
+                    }
             }
 
-            // ---- to units of log2, masked; the scales of this thread's keys 2 q4 + {0, 1, 8, 9}
-            float vs[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+            // ---- to units of log2, masked; this thread's keys are 8 n + 2 q4 + {0, 1}
+            float vs[4][2];
             if constexpr (INT8) {
                 const float* sc = reinterpret_cast<const float*>(ring + static_cast<size_t>(stage) * S::kStageBytes +
                                                                  2 * S::kTileBytes) +
                                   slice + 2 * q4;
-                const float2 k0 = *reinterpret_cast<const float2*>(sc), k1 = *reinterpret_cast<const float2*>(sc + 8);
-                const float2 v0 = *reinterpret_cast<const float2*>(sc + kMmaTile),
-                             v1 = *reinterpret_cast<const float2*>(sc + kMmaTile + 8);
-                const float ks[4] = {k0.x, k0.y, k1.x, k1.y};
-                vs[0] = v0.x;
-                vs[1] = v0.y;
-                vs[2] = v1.x;
-                vs[3] = v1.y;
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[n][e] *= ks[2 * n + (e & 1)] * c2;
+                for (int n = 0; n < 4; ++n) {
+                    const float2 ks = *reinterpret_cast<const float2*>(sc + 8 * n);
+                    const float2 v = *reinterpret_cast<const float2*>(sc + kMmaTile + 8 * n);
+                    vs[n][0] = v.x;
+                    vs[n][1] = v.y;
+                    s[n][0] *= ks.x * cr[0];
+                    s[n][1] *= ks.y * cr[0];
+                    s[n][2] *= ks.x * cr[1];
+                    s[n][3] *= ks.y * cr[1];
+                }
             } else {
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < 4; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) s[n][e] *= c2;
             }
-            uint32_t vmask0 = 0xFFFFFFFFu, vmask1 = 0xFFFFFFFFu;
-            const bool tail = key0 + 16 > sq.len;
-            if (key0 + 16 > all_seen) {
+            const bool tail = key0 + kMmaKeys > sq.len;
+            if (key0 + kMmaKeys > all_seen) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < 4; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int key = key0 + 8 * n + 2 * q4 + (e & 1);
                         if (key >= seen[e >> 1]) s[n][e] = -INFINITY;
+                        // what lies past the sequence may be anything, NaN included: zeros instead
+                        if (INT8 && e < 2 && key >= sq.len) vs[n][e] = 0.0f;
                     }
-                if (tail) {
-                    // what lies past the sequence may be anything, NaN included: zeros instead
-                    const int k = key0 + 2 * q4;
-                    vmask0 = (k < sq.len ? 0xFFFFu : 0u) | (k + 1 < sq.len ? 0xFFFF0000u : 0u);
-                    vmask1 = (k + 8 < sq.len ? 0xFFFFu : 0u) | (k + 9 < sq.len ? 0xFFFF0000u : 0u);
-                    if constexpr (INT8) {
-                        if (k >= sq.len) vs[0] = 0.0f;
-                        if (k + 1 >= sq.len) vs[1] = 0.0f;
-                        if (k + 8 >= sq.len) vs[2] = 0.0f;
-                        if (k + 9 >= sq.len) vs[3] = 0.0f;
-                    }
-                }
             }
 
-            // ---- running maximum, probabilities
+            // ---- running maximum
             float mt[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 float v = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+                v = fmaxf(v, fmaxf(fmaxf(s[2][2 * i], s[2][2 * i + 1]), fmaxf(s[3][2 * i], s[3][2 * i + 1])));
                 v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
                 v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
                 mt[i] = fmaxf(m[i], v);
             }
-            if (__any_sync(0xffffffffu, mt[0] > m[0] || mt[1] > m[1])) {
+            float v_new = v_unit;
+            if constexpr (INT8) {
+                float v = fmaxf(fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1])),
+                                fmaxf(fmaxf(vs[2][0], vs[2][1]), fmaxf(vs[3][0], vs[3][1])));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                constexpr float kUnit = static_cast<float>(1u << (static_cast<int>(attn_bias<true>()) - 14));
+                if (v * (0.5f * kUnit) > 0.5f * v_unit) v_new = pow2_of(v) * kUnit;
+            }
+            if (__any_sync(0xffffffffu, mt[0] > m[0] || mt[1] > m[1] || v_new != v_unit)) {
+                const float fv = INT8 && v_new != v_unit ? v_unit / v_new : 1.0f;
+                v_unit = v_new;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const float f = mt[i] == -INFINITY ? 1.0f : exp2f(m[i] - mt[i]);
@@ -589,57 +664,75 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
                     l[i] *= f;
 #pragma unroll
                     for (int n = 0; n < 2 * kSteps; ++n) {
-                        o[n][2 * i] *= f;
-                        o[n][2 * i + 1] *= f;
+                        o[n][2 * i] *= f * fv;
+                        o[n][2 * i + 1] *= f * fv;
                     }
                 }
             }
-            uint32_t pa[4];
+
+            // ---- probabilities as A fragments of two steps of 16 keys
+            uint32_t pa[2][4];
+            const float v_inv = INT8 ? (v_unit > 0.0f ? 1.0f / v_unit : 0.0f) : 1.0f;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float mu = m[i] == -INFINITY ? 0.0f : m[i] - attn_bias<INT8>();
-                const float p0 = exp2f(s[0][2 * i] - mu), p1 = exp2f(s[0][2 * i + 1] - mu);
-                const float p2 = exp2f(s[1][2 * i] - mu), p3 = exp2f(s[1][2 * i + 1] - mu);
-                l[i] += (p0 + p1) + (p2 + p3);
-                pa[i] = pack_bf16x2(p0 * vs[0], p1 * vs[1]);
-                pa[i + 2] = pack_bf16x2(p2 * vs[2], p3 * vs[3]);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const float p0 = ex2(s[2 * b][2 * i] - mu), p1 = ex2(s[2 * b][2 * i + 1] - mu);
+                    const float p2 = ex2(s[2 * b + 1][2 * i] - mu), p3 = ex2(s[2 * b + 1][2 * i + 1] - mu);
+                    l[i] += (p0 + p1) + (p2 + p3);
+                    if constexpr (INT8) {
+                        pa[b][i] = pack_f16x2(p0 * (vs[2 * b][0] * v_inv), p1 * (vs[2 * b][1] * v_inv));
+                        pa[b][i + 2] = pack_f16x2(p2 * (vs[2 * b + 1][0] * v_inv), p3 * (vs[2 * b + 1][1] * v_inv));
+                    } else {
+                        pa[b][i] = pack_bf16x2(p0, p1);
+                        pa[b][i + 2] = pack_bf16x2(p2, p3);
+                    }
+                }
             }
 
-            // ---- sums: 16 rows x dim += P (16 x 16) V (16 x dim)
+            // ---- sums: 16 rows x dim += P (16 x 32) V (32 x dim)
             const uint32_t vt = st + S::kTileBytes;
-            if constexpr (INT8) {
-                // a b16 element is a pair of dims: the transposed fragment holds dims 2n, 2n + 1 of
-                // two keys, and the permutes pick the two keys of one dim; tile 2k holds the even
-                // dims of a chunk, tile 2k + 1 the odd ones
-                const int row = slice + (mi & 1) * 8 + mr;
 #pragma unroll
-                for (int k = 0; k < kSteps; k += 2) {
-                    uint32_t r[4];
-                    ldsm_x4_t(vt + swizzled<S::kBoxBytes>(row, k + (mi >> 1)), r);
-                    mma_bf16_16816(o[2 * k], pa[0], pa[1], pa[2], pa[3], codes_bf16x2(r[0], 0x4240),
-                                   codes_bf16x2(r[1], 0x4240));
-                    mma_bf16_16816(o[2 * k + 1], pa[0], pa[1], pa[2], pa[3], codes_bf16x2(r[0], 0x4341),
-                                   codes_bf16x2(r[1], 0x4341));
-                    mma_bf16_16816(o[2 * k + 2], pa[0], pa[1], pa[2], pa[3], codes_bf16x2(r[2], 0x4240),
-                                   codes_bf16x2(r[3], 0x4240));
-                    mma_bf16_16816(o[2 * k + 3], pa[0], pa[1], pa[2], pa[3], codes_bf16x2(r[2], 0x4341),
-                                   codes_bf16x2(r[3], 0x4341));
-                }
-            } else {
-                const int row = slice + (mi & 1) * 8 + mr;
+            for (int b = 0; b < 2; ++b) {
+                const int row = slice + 16 * b + (mi & 1) * 8 + mr;
+                if constexpr (INT8) {
+                    // a b16 element is a pair of dims: the transposed fragment holds dims 2n, 2n + 1 of
+                    // two keys; tile 2k takes the even dims of a chunk, tile 2k + 1 the odd ones
 #pragma unroll
-                for (int k = 0; k < kSteps; ++k) {
-                    uint32_t r[4];
-                    const int chunk = 2 * k + (mi >> 1);
-                    ldsm_x4_t(vt + (chunk >> 3) * S::kHalfBytes + swizzled<S::kBoxBytes>(row, chunk & 7), r);
-                    if (tail) {
-                        r[0] &= vmask0;
-                        r[1] &= vmask1;
-                        r[2] &= vmask0;
-                        r[3] &= vmask1;
+                    for (int k = 0; k < kSteps; k += 2) {
+                        uint32_t r[4];
+                        ldsm_x4_t(vt + swizzled<S::kBoxBytes>(row, k + (mi >> 1)), r);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            mma_f16_16816(o[2 * (k + x)], pa[b][0], pa[b][1], pa[b][2], pa[b][3],
+                                          codes_f16x2(r[2 * x]), codes_f16x2(r[2 * x + 1]));
+                            mma_f16_16816(o[2 * (k + x) + 1], pa[b][0], pa[b][1], pa[b][2], pa[b][3],
+                                          codes_f16x2(r[2 * x] >> 8), codes_f16x2(r[2 * x + 1] >> 8));
+                        }
                     }
-                    mma_bf16_16816(o[2 * k], pa[0], pa[1], pa[2], pa[3], r[0], r[1]);
-                    mma_bf16_16816(o[2 * k + 1], pa[0], pa[1], pa[2], pa[3], r[2], r[3]);
+                } else {
+                    uint32_t mask0 = 0xFFFFFFFFu, mask1 = 0xFFFFFFFFu;
+                    if (tail) {
+                        // zeros for what lies past the sequence
+                        const int k = key0 + 16 * b + 2 * q4;
+                        mask0 = (k < sq.len ? 0xFFFFu : 0u) | (k + 1 < sq.len ? 0xFFFF0000u : 0u);
+                        mask1 = (k + 8 < sq.len ? 0xFFFFu : 0u) | (k + 9 < sq.len ? 0xFFFF0000u : 0u);
+                    }
+#pragma unroll
+                    for (int k = 0; k < kSteps; ++k) {
+                        uint32_t r[4];
+                        const int chunk = 2 * k + (mi >> 1);
+                        ldsm_x4_t(vt + (chunk >> 3) * S::kHalfBytes + swizzled<S::kBoxBytes>(row, chunk & 7), r);
+                        if (tail) {
+                            r[0] &= mask0;
+                            r[1] &= mask1;
+                            r[2] &= mask0;
+                            r[3] &= mask1;
+                        }
+                        mma_bf16_16816(o[2 * k], pa[b][0], pa[b][1], pa[b][2], pa[b][3], r[0], r[1]);
+                        mma_bf16_16816(o[2 * k + 1], pa[b][0], pa[b][1], pa[b][2], pa[b][3], r[2], r[3]);
+                    }
                 }
             }
             __syncwarp();
@@ -650,7 +743,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
             }
         }
 
-        // ---- join the four warps, in warp order
+        // ---- join the four warps: (0 + 2) and (1 + 3) in the two buffers
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
@@ -668,20 +761,27 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
 #pragma unroll
             for (int w = 1; w < kMmaConsumers; ++w) mm = fmaxf(mm, sh.m[w][g + 8 * i]);
             f[i] = attn_weight(m[i] - attn_bias<INT8>(), l[i], mm);
+            if (INT8 && f[i] != 0.0f) f[i] *= v_unit;  // the sums are over the scales' unit
         }
-        for (int w = 0; w < kMmaConsumers; ++w) {
-            if (warp == w) {
+        for (int w = 0; w < 2; ++w) {
+            if ((warp >> 1) == w) {
+                float* mine = buf + (warp & 1) * kMmaRows * DIM;
 #pragma unroll
                 for (int n = 0; n < 2 * kSteps; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int r = g + 8 * (e >> 1);
-                        // bf16: tile n, column 2 q4 + (e & 1); int8: chunk n / 2, dims 4 q4 + {0, 2}
-                        // of the even tile and 4 q4 + {1, 3} of the odd one
-                        const int d = INT8 ? 16 * (n >> 1) + 4 * q4 + (n & 1) + 2 * (e & 1) : 8 * n + 2 * q4 + (e & 1);
-                        const float v = f[e >> 1] == 0.0f ? 0.0f : o[n][e] * f[e >> 1];
-                        float* b = buf + r * DIM + d;
-                        *b = w == 0 ? v : *b + v;
+                    for (int i = 0; i < 2; ++i) {
+                        // bf16: tile n, columns 2 q4 + {0, 1}; int8: chunk n / 2, dims 4 q4 + {0, 2} of
+                        // the even tile and 4 q4 + {1, 3} of the odd one, kept at places 2 (n & 1) + {0, 1}
+                        const int d = INT8 ? 16 * (n >> 1) + 4 * q4 + 2 * (n & 1) : 8 * n + 2 * q4;
+                        float2* b = reinterpret_cast<float2*>(mine + (g + 8 * i) * DIM + d);
+                        float2 v = make_float2(0.0f, 0.0f);
+                        if (f[i] != 0.0f) v = make_float2(o[n][2 * i] * f[i], o[n][2 * i + 1] * f[i]);
+                        if (w == 1) {
+                            const float2 x = *b;
+                            v.x += x.x;
+                            v.y += x.y;
+                        }
+                        *b = v;
                     }
             }
             consumers_sync();
@@ -701,7 +801,10 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
                 const float lw = sh.l[w][r];
                 ll += lw * attn_weight(sh.m[w][r], lw, mm);
             }
-            const float4 v = *reinterpret_cast<const float4*>(buf + r * DIM + d);
+            float4 v = *reinterpret_cast<const float4*>(buf + r * DIM + d);
+            const float4 v1 = *reinterpret_cast<const float4*>(buf + kMmaRows * DIM + r * DIM + d);
+            v = make_float4(v.x + v1.x, v.y + v1.y, v.z + v1.z, v.w + v1.w);
+            if constexpr (INT8) v = make_float4(v.x, v.z, v.y, v.w);  // from places to dims
             if (whole) {
                 const int row = row0 + r, tok = row / p.G;
                 const int64_t at = (static_cast<int64_t>(sq.q0) + tok) * a.n_q + h * p.G + (row - tok * p.G);
@@ -760,23 +863,29 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
                 lw = ml.y;
             }
             const int n = parts - i0 < 32 ? parts - i0 : 32;
-            for (int i = 0; i < n; ++i) {
-                const float wi = __shfl_sync(0xffffffffu, w, i), li = __shfl_sync(0xffffffffu, lw, i);
-                const float* src =
-                    p.part_o + (static_cast<int64_t>(attn_slot(c - 1 + i0 + i, i0 + i == 0)) * p.mb + r) * DIM +
-                    kPer * lane;
-                float v[kPer];
-                if constexpr (kPer == 4) {
-                    const float4 x = *reinterpret_cast<const float4*>(src);
-                    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-                } else {
-                    const float2 x = *reinterpret_cast<const float2*>(src);
-                    v[0] = x.x, v[1] = x.y;
-                }
-                if (wi != 0.0f) {
-                    ll += wi * li;
+            for (int j0 = 0; j0 < n; j0 += 8) {
+                float v[8][kPer];
 #pragma unroll
-                    for (int e = 0; e < kPer; ++e) acc[e] += wi * v[e];
+                for (int j = 0; j < 8; ++j) {
+                    const int i = i0 + (j0 + j < n ? j0 + j : n - 1);
+                    const float* src =
+                        p.part_o + (static_cast<int64_t>(attn_slot(c - 1 + i, i == 0)) * p.mb + r) * DIM + kPer * lane;
+                    if constexpr (kPer == 4) {
+                        const float4 x = *reinterpret_cast<const float4*>(src);
+                        v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
+                    } else {
+                        const float2 x = *reinterpret_cast<const float2*>(src);
+                        v[j][0] = x.x, v[j][1] = x.y;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float wi = __shfl_sync(0xffffffffu, w, j0 + j), li = __shfl_sync(0xffffffffu, lw, j0 + j);
+                    if (j0 + j < n && wi != 0.0f) {
+                        ll += wi * li;
+#pragma unroll
+                        for (int e = 0; e < kPer; ++e) acc[e] += wi * v[j][e];
+                    }
                 }
             }
         }
@@ -807,11 +916,11 @@ cudaError_t launch_mma_shape(const AttnParams& p, cudaStream_t stream)
         if (!encode_tma_3d(i ? &mp.v_map : &mp.k_map, type, INT8 ? 1 : 2, i ? kv.v : kv.k, DIM, kv.page, outer,
                            S::kBoxBytes / (INT8 ? 1 : 2), box_rows, swz))
             return cudaErrorInvalidValue;
-    // two blocks per SM: 113 KB each, less the static part and the alignment of the ring
-    constexpr size_t kBudget = 111u * 1024u;
-    mp.stages = static_cast<int>((kBudget - S::kBufBytes) / S::kStageBytes);
+    // two blocks per SM: 113 KB each
+    constexpr size_t kBudget = 113u * 1024u, kRest = S::kBufBytes + sizeof(MmaShared);
+    mp.stages = static_cast<int>((kBudget - kRest) / S::kStageBytes);
     if (mp.stages > kMmaMaxStages) mp.stages = kMmaMaxStages;
-    const size_t smem = 1024 + static_cast<size_t>(mp.stages) * S::kStageBytes + S::kBufBytes;
+    const size_t smem = static_cast<size_t>(mp.stages) * S::kStageBytes + kRest;
     cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(attn_mma_kernel<DIM, INT8>), smem, smem_set);
     launch_dep(err, attn_mma_kernel<DIM, INT8>, dim3(p.blocks), dim3(kMmaThreads), smem, stream, mp);
     return err;

@@ -95,16 +95,32 @@ __device__ __forceinline__ int attn_seen(const AttnSeq& s, int i, int causal)
     return e < 0 ? 0 : e > s.len ? s.len : static_cast<int>(e);
 }
 
-// Number of blocks that take part, and the first unit of block c.
+// Number of blocks that take part, and the first unit of block c.  (Few units,
+// the usual case: 32-bit divisions, which take a fraction of the time of
+// 64-bit ones, and a block makes several before it can start.)
 __device__ __forceinline__ int attn_active(int64_t units, int blocks)
 {
     return units < blocks ? static_cast<int>(units) : blocks;
 }
-__device__ __forceinline__ int64_t attn_first(int64_t units, int n, int c) { return units * c / n; }
+constexpr int64_t kAttnFewUnits = 0xFFFFFFFFll / (kAttnMaxBlocks + 1) - 1;
+__device__ __forceinline__ int64_t attn_first(int64_t units, int n, int c)
+{
+    if (units < kAttnFewUnits) return static_cast<uint32_t>(units) * static_cast<uint32_t>(c) / static_cast<uint32_t>(n);
+    return units * c / n;
+}
 // The block that takes unit u: the last c with attn_first(c) <= u.
 __device__ __forceinline__ int attn_owner(int64_t units, int n, int64_t u)
 {
+    if (units < kAttnFewUnits)
+        return static_cast<int>((static_cast<uint32_t>(u + 1) * static_cast<uint32_t>(n) - 1u) /
+                                static_cast<uint32_t>(units));
     return static_cast<int>(((u + 1) * n - 1) / units);
+}
+// rel / tiles for 0 <= rel < tiles * n_kv
+__device__ __forceinline__ int attn_div(int64_t rel, int tiles)
+{
+    return rel <= 0xFFFFFFFFll ? static_cast<int>(static_cast<uint32_t>(rel) / static_cast<uint32_t>(tiles))
+                               : static_cast<int>(rel / tiles);
 }
 
 // What block c, whose first unit u lies in the (item, head) with units

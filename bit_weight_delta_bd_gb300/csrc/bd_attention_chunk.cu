@@ -205,7 +205,7 @@ struct Walk {
         const int n_kv = p.a.cache.n_kv;
         s.it = p.items[item];
         const int64_t rel = u - static_cast<int64_t>(s.it.before) * n_kv;
-        s.h = static_cast<int>(rel / s.it.tiles);
+        s.h = attn_div(rel, s.it.tiles);
         s.t0 = static_cast<int>(rel - static_cast<int64_t>(s.h) * s.it.tiles);
         const int64_t left = end - u;
         s.t1 = left < s.it.tiles - s.t0 ? s.t0 + static_cast<int>(left) : s.it.tiles;
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
         if (c < active) {
             const AttnItem it = p.items[walk.item];
             const int64_t first = static_cast<int64_t>(it.before) * n_kv;
-            const int h = static_cast<int>((walk.u - first) / it.tiles);
+            const int h = attn_div(walk.u - first, it.tiles);
             j = attn_join_of(units, active, c, walk.u, first + static_cast<int64_t>(h) * it.tiles, it.tiles, it.seq,
                              it.row0, h);
         }
