@@ -170,17 +170,19 @@ def _check(status: int, where: str) -> None:
 
 
 _BF16_LIKE = (torch.bfloat16, torch.uint16, torch.int16)
+_F32, _I32 = (torch.float32,), (torch.int32,)
 
 
-def _ptr(t: torch.Tensor | None, name: str, dtypes=None, allow_none: bool = False) -> int | None:
-    # the usual case first: a call's checks cost more host time than a small kernel takes
-    if (t is not None and t.is_cuda and t.get_device() == _device() and (dtypes is None or t.dtype in dtypes)
-            and t.is_contiguous()):
-        return t.data_ptr()
+def _ptr(t: torch.Tensor | None, name: str, dtypes=None, allow_none: bool = False, dev: int | None = None) -> int | None:
+    # the usual case first: a call's checks cost more host time than a small
+    # kernel takes (a CPU tensor's get_device() is -1)
     if t is None:
         if allow_none:
             return None
         raise ValueError(f"{name} is required")
+    if (t.get_device() == (_device() if dev is None and t.is_cuda else dev) and (dtypes is None or t.dtype in dtypes)
+            and t.is_contiguous()):
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.device.index != torch.cuda.current_device():
@@ -196,14 +198,14 @@ _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _stream(stream) -> int:
-    return _raw_stream(_device()) if stream is None else stream.cuda_stream
+def _stream(stream, dev: int | None = None) -> int:
+    return _raw_stream(_device() if dev is None else dev) if stream is None else stream.cuda_stream
 
 
-def _ws(ws: torch.Tensor) -> tuple[int, int]:
+def _ws(ws: torch.Tensor, dev: int | None = None) -> tuple[int, int]:
     if ws.dtype != torch.uint8:
         raise ValueError("workspace must be a torch.uint8 tensor")
-    return _ptr(ws, "ws"), ws.numel()
+    return _ptr(ws, "ws", None, False, dev), ws.numel()
 
 
 def new_workspace(nbytes: int, device=None) -> torch.Tensor:
@@ -320,11 +322,12 @@ def bd_rms_norm(x, gain, eps, out, ws, residual=None, residual_out=None, scale=N
     """out = norm(x + residual) * gain (the gain of token t's variant, vid[t], out of gain_list); out bf16, fp32, or
     e4m3 with scale [T]; residual_out (which may be residual itself) receives x + residual."""
     T, d = x.shape
+    dev = _device()
     if gain.shape != (d,) or out.shape != x.shape:
         raise ValueError("gain must have the shape [d] and out that of x")
-    for name, t in (("residual", residual), ("residual_out", residual_out)):
-        if t is not None and t.shape != x.shape:
-            raise ValueError(f"{name} shape differs from x")
+    if (residual is not None and residual.shape != x.shape) or (
+            residual_out is not None and residual_out.shape != x.shape):
+        raise ValueError("the residual's shape differs from x")
     if scale is not None and scale.numel() != T:
         raise ValueError("scale must have one value per row")
     if vid is not None and vid.numel() != T:
@@ -332,18 +335,18 @@ def bd_rms_norm(x, gain, eps, out, ws, residual=None, residual_out=None, scale=N
     tab, V = None, 0
     if vid is not None:
         V = len(gain_list)
-        if any(t.shape != gain.shape for t in gain_list):
+        if any(t.numel() != d for t in gain_list):
             raise ValueError("every gain must have the shape [d]")
-        tab = (ctypes.c_void_p * max(V, 1))(*[_ptr(t, "gain", _BF16_LIKE) for t in gain_list])
+        tab = (ctypes.c_void_p * max(V, 1))(*[_ptr(t, "gain", _BF16_LIKE, False, dev) for t in gain_list])
     out_dtype = _OUT_DTYPES.get(out.dtype)
     if out_dtype is None:
         raise ValueError(f"out has dtype {out.dtype}, expected bfloat16, float32 or float8_e4m3fn")
-    wsp, wsn = _ws(ws)
-    _check(load().bd_rms_norm(_ptr(x, "x", _BF16_LIKE), _ptr(residual, "residual", _BF16_LIKE, True), T, d,
-                              _ptr(gain, "gain", _BF16_LIKE), _ptr(vid, "vid", (torch.int32,), True), V,
-                              tab, float(eps), _ptr(residual_out, "residual_out", _BF16_LIKE, True),
-                              _ptr(out, "out"), out_dtype, _ptr(scale, "scale", (torch.float32,), True), wsp, wsn,
-                              _stream(stream)), "bd_rms_norm")
+    wsp, wsn = _ws(ws, dev)
+    _check(load().bd_rms_norm(_ptr(x, "x", _BF16_LIKE, False, dev), _ptr(residual, "residual", _BF16_LIKE, True, dev),
+                              T, d, _ptr(gain, "gain", _BF16_LIKE, False, dev), _ptr(vid, "vid", _I32, True, dev), V,
+                              tab, eps, _ptr(residual_out, "residual_out", _BF16_LIKE, True, dev),
+                              _ptr(out, "out", None, False, dev), out_dtype, _ptr(scale, "scale", _F32, True, dev),
+                              wsp, wsn, _stream(stream, dev)), "bd_rms_norm")
 
 
 _OUT_DTYPES = {torch.bfloat16: BD_OUT_BF16, torch.float32: BD_OUT_F32, torch.float8_e4m3fn: BD_OUT_E4M3}
@@ -377,13 +380,13 @@ class KvPages:
         self._addr = ctypes.addressof(self._c)
 
 
-def _heads(t, name: str, dim: int) -> tuple[int, int]:
+def _heads(t, name: str, dim: int, dev: int) -> tuple[int, int]:
     """(pointer, row stride) of a bf16 [T][heads][dim] tensor whose rows may be apart."""
     T, heads, d = t.shape
     s0, s1, s2 = t.stride()
     if d != dim or s2 != 1 or (heads > 1 and s1 != dim):
         raise ValueError(f"{name} must be [T][heads][{dim}] with contiguous rows")
-    if not t.is_cuda or t.get_device() != _device():
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on the current CUDA device")
     if t.dtype not in _BF16_LIKE:
         raise ValueError(f"{name} has dtype {t.dtype}, expected one of {_BF16_LIKE}")
@@ -407,33 +410,36 @@ def bd_rope_append(q, k, v, pos, rope_table, slot, cache: KvPages, q_out, ws, ax
     rows may be apart (slices of one packed product); q = None skips q.  pos: [T] or [T][axes]; axis_of_pair: a host
     sequence of rot_dim/2 axis numbers."""
     T, n_kv, dim = k.shape
+    dev = _device()
     if n_kv != cache.n_kv or v.shape != k.shape or dim != cache.head_dim:
         raise ValueError("k and v must be [T][n_kv][head_dim] of the cache")
-    kp, ks = _heads(k, "k", dim)
-    vp, vs = _heads(v, "v", dim)
+    kp, ks = _heads(k, "k", dim, dev)
+    vp, vs = _heads(v, "v", dim, dev)
     qp = qs = op = os_ = n_q = 0
     if q is not None:
         n_q = q.shape[1]
         if q.shape[0] != T or q_out.shape != q.shape:
             raise ValueError("q and q_out must have T rows of the same heads")
-        qp, qs = _heads(q, "q", dim)
-        op, os_ = _heads(q_out, "q_out", dim)
+        qp, qs = _heads(q, "q", dim, dev)
+        op, os_ = _heads(q_out, "q_out", dim, dev)
     n_axes = pos.shape[1] if pos is not None and pos.dim() == 2 else 1
     if (pos is not None and pos.shape[0] != T) or slot.numel() != T:
         raise ValueError("pos and slot must have one row per token")
-    n_pos, pairs = (rope_table.shape[0], rope_table.shape[1]) if rope_table is not None else (0, 0)
+    n_pos = pairs = 0
+    if rope_table is not None:
+        if rope_table.dim() != 3 or rope_table.shape[2] != 2:
+            raise ValueError("rope_table must be [n_pos][rot_dim/2][2]")
+        n_pos, pairs, _ = rope_table.shape
     axes = None
     if axis_of_pair is not None:
         if len(axis_of_pair) != pairs:
             raise ValueError("axis_of_pair must have rot_dim/2 entries")
         axes = bytes(axis_of_pair)
-    if rope_table is not None and (rope_table.dim() != 3 or rope_table.shape[2] != 2):
-        raise ValueError("rope_table must be [n_pos][rot_dim/2][2]")
-    wsp, wsn = _ws(ws)
-    _check(load().bd_rope_append(qp, qs, kp, ks, vp, vs, T, n_q, _ptr(pos, "pos", (torch.int32,), True), n_axes, axes,
-                                 _ptr(rope_table, "rope_table", (torch.float32,), True), n_pos, 2 * pairs,
-                                 int(interleaved), _ptr(slot, "slot", (torch.int32,)), cache._addr, op, os_, wsp, wsn,
-                                 _stream(stream)), "bd_rope_append")
+    wsp, wsn = _ws(ws, dev)
+    _check(load().bd_rope_append(qp, qs, kp, ks, vp, vs, T, n_q, _ptr(pos, "pos", _I32, True, dev), n_axes, axes,
+                                 _ptr(rope_table, "rope_table", _F32, True, dev), n_pos, 2 * pairs, interleaved,
+                                 _ptr(slot, "slot", _I32, False, dev), cache._addr, op, os_, wsp, wsn,
+                                 _stream(stream, dev)), "bd_rope_append")
 
 
 def bd_kv_read_workspace_size(rows: int) -> int:
@@ -443,15 +449,17 @@ def bd_kv_read_workspace_size(rows: int) -> int:
 def bd_kv_read(cache: KvPages, page_table, kv_off, k_out, v_out, ws, stream=None) -> None:
     """Gathers the sequences' tokens out of the pages into k_out, v_out [rows][n_kv][head_dim] bf16."""
     n_seq, max_pages = page_table.shape
-    rows = k_out.shape[0]
-    if tuple(k_out.shape) != (rows, cache.n_kv, cache.head_dim) or v_out.shape != k_out.shape:
+    rows, heads, dim = k_out.shape
+    dev = _device()
+    if heads != cache.n_kv or dim != cache.head_dim or v_out.shape != k_out.shape:
         raise ValueError("k_out and v_out must be [rows][n_kv][head_dim]")
     if kv_off.numel() != n_seq + 1:
         raise ValueError("kv_off must have n_seq + 1 entries")
-    wsp, wsn = _ws(ws)
-    _check(load().bd_kv_read(cache._addr, _ptr(page_table, "page_table", (torch.int32,)), max_pages,
-                             _ptr(kv_off, "kv_off", (torch.int32,)), n_seq, rows, _ptr(k_out, "k_out", _BF16_LIKE),
-                             _ptr(v_out, "v_out", _BF16_LIKE), wsp, wsn, _stream(stream)), "bd_kv_read")
+    wsp, wsn = _ws(ws, dev)
+    _check(load().bd_kv_read(cache._addr, _ptr(page_table, "page_table", _I32, False, dev), max_pages,
+                             _ptr(kv_off, "kv_off", _I32, False, dev), n_seq, rows,
+                             _ptr(k_out, "k_out", _BF16_LIKE, False, dev), _ptr(v_out, "v_out", _BF16_LIKE, False, dev),
+                             wsp, wsn, _stream(stream, dev)), "bd_kv_read")
 
 
 def bd_attention_workspace_size(T: int, n_seq: int, n_q: int, n_kv: int, head_dim: int) -> int:
@@ -463,19 +471,20 @@ def bd_attention(q, q_off, cache: KvPages, page_table, kv_len, scale, max_new, o
     """Attention of the new tokens q [T][n_q][head_dim] (rows may be apart) of n_seq sequences over the paged cache."""
     T, n_q, dim = q.shape
     n_seq, max_pages = page_table.shape
-    if dim != cache.head_dim or tuple(out.shape) != (T, n_q, dim):
+    dev = _device()
+    if dim != cache.head_dim or out.shape != q.shape:
         raise ValueError("q and out must be [T][n_q][head_dim] of the cache")
     if q_off.numel() != n_seq + 1 or kv_len.numel() != n_seq:
         raise ValueError("q_off must have n_seq + 1 entries and kv_len n_seq")
-    if lse is not None and tuple(lse.shape) != (T, n_q):
+    if lse is not None and lse.shape != (T, n_q):
         raise ValueError("lse must be [T][n_q]")
-    qp, qs = _heads(q, "q", dim)
-    wsp, wsn = _ws(ws)
-    _check(load().bd_attention(qp, qs, _ptr(q_off, "q_off", (torch.int32,)), T, n_seq, int(max_new), n_q, cache._addr,
-                               _ptr(page_table, "page_table", (torch.int32,)), max_pages,
-                               _ptr(kv_len, "kv_len", (torch.int32,)), float(scale), int(causal),
-                               _ptr(out, "out", _BF16_LIKE), _ptr(lse, "lse", (torch.float32,), True), wsp, wsn,
-                               _stream(stream)), "bd_attention")
+    qp, qs = _heads(q, "q", dim, dev)
+    wsp, wsn = _ws(ws, dev)
+    _check(load().bd_attention(qp, qs, _ptr(q_off, "q_off", _I32, False, dev), T, n_seq, max_new, n_q, cache._addr,
+                               _ptr(page_table, "page_table", _I32, False, dev), max_pages,
+                               _ptr(kv_len, "kv_len", _I32, False, dev), scale, causal,
+                               _ptr(out, "out", _BF16_LIKE, False, dev), _ptr(lse, "lse", _F32, True, dev), wsp, wsn,
+                               _stream(stream, dev)), "bd_attention")
 
 
 def bd_route(vid, V, perm, seg_off, ws, stream=None) -> None:
