@@ -68,7 +68,7 @@ struct ChunkShared {
     uint64_t full[kMaxBufs], empty[kMaxBufs];    // bf16 tiles
     uint64_t raw_full[3], raw_empty[3];          // tiles of codes
     uint64_t sc_full[3], sc_empty[3];            // scales
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+    uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2];  // P in two halves of 64 keys
     uint64_t done;
     uint32_t tmem;
     volatile int abort;
@@ -164,6 +164,52 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t 
     return d;
 }
 
+// One lane of the warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// Two fp32 values in one 64-bit register, and their packed arithmetic.
+__device__ __forceinline__ uint64_t f32x2(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
@@ -211,9 +257,14 @@ struct Walk {
         s.t1 = left < s.it.tiles - s.t0 ? s.t0 + static_cast<int>(left) : s.it.tiles;
         s.sq = attn_seq(p.a, s.it.seq, false);
         s.rows = s.sq.n_new * p.G - s.it.row0;
-        s.q_tiles = s.rows > kQRows ? 2 : 1;
         u += s.t1 - s.t0;
         if (s.t1 == s.it.tiles && s.h == n_kv - 1) ++item;
+        // known for uniform
+        s.t0 = __shfl_sync(0xffffffffu, s.t0, 0);
+        s.t1 = __shfl_sync(0xffffffffu, s.t1, 0);
+        s.rows = __shfl_sync(0xffffffffu, s.rows, 0);
+        s.sq.len = __shfl_sync(0xffffffffu, s.sq.len, 0);
+        s.q_tiles = s.rows > kQRows ? 2 : 1;
         return true;
     }
 };
@@ -252,7 +303,9 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
     const AttnParams& p = cp.p;
     const AttentionArgs& a = p.a;
     const KvPages& cache = a.cache;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (taken from lane 0, so that the compiler knows it for uniform: the
+    // branches below, and the descriptors that the MMA warp forms in them)
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     grid_launch_dependents();
     if (threadIdx.x == 0) {
@@ -269,7 +322,8 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.q_full[i], 4);
             mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.p_full[i], 4);
+            mbar_init(&sh.p_full[i][0], 4);
+            mbar_init(&sh.p_full[i][1], 4);
             mbar_init(&sh.o_full[i], 1);
         }
         mbar_init(&sh.done, 1);
@@ -369,11 +423,12 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
                 if constexpr (INT8) {
 #pragma unroll
                     for (int j = 0; j < 128; j += 4) {
-                        const float4 f = *reinterpret_cast<const float4*>(ks + j);
-                        v[j] = __float_as_uint(__uint_as_float(v[j]) * f.x);
-                        v[j + 1] = __float_as_uint(__uint_as_float(v[j + 1]) * f.y);
-                        v[j + 2] = __float_as_uint(__uint_as_float(v[j + 2]) * f.z);
-                        v[j + 3] = __float_as_uint(__uint_as_float(v[j + 3]) * f.w);
+                        const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(ks + j);
+                        const float2 a0 = unpack2(mul2(f32x2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), f.x));
+                        const float2 a1 =
+                            unpack2(mul2(f32x2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])), f.y));
+                        v[j] = __float_as_uint(a0.x), v[j + 1] = __float_as_uint(a0.y);
+                        v[j + 2] = __float_as_uint(a1.x), v[j + 3] = __float_as_uint(a1.y);
                     }
                 }
                 const int left = seen - t * kTile;  // keys of the tile that this row sees
@@ -386,12 +441,13 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
                 __syncwarp();
                 float mx[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mx[k] = __uint_as_float(v[k]);
+                for (int k = 0; k < 4; ++k) mx[k] = fmaxf(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
 #pragma unroll
-                for (int j = 4; j < 128; j += 4)
+                for (int j = 8; j < 128; j += 8)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(v[j + k]));
-                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    for (int k = 0; k < 4; ++k)
+                        mx[k] = max3(mx[k], __uint_as_float(v[j + 2 * k]), __uint_as_float(v[j + 2 * k + 1]));
+                const float mt = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
                 if (t == cur.t0) {
                     m = mt;
                 } else {
@@ -413,7 +469,8 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
                     }
                 }
                 const float nm = m == -INFINITY ? 0.0f : fmaf(-m, c2, attn_bias<INT8>());
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                uint64_t sum[2] = {0, 0};  // pairs of zeros
+                const uint64_t c22 = f32x2(c2, c2), nm2 = f32x2(nm, nm);
                 const auto probabilities = [&](auto mask) {
                     constexpr bool kMask = decltype(mask)::value;
 #pragma unroll
@@ -421,32 +478,41 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
                         uint32_t pk[16];
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
-                            float pr[4];
+                            [[maybe_unused]] ulonglong2 f{};
+                            if constexpr (INT8) f = *reinterpret_cast<const ulonglong2*>(vs + j + e);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                pr[k] = ex2(fmaf(__uint_as_float(v[j + e + k]), c2, nm));
-                                if (kMask && j + e + k >= left) pr[k] = 0.0f;
-                                sum[k] += pr[k];
+                            for (int k = 0; k < 2; ++k) {
+                                const int at = j + e + 2 * k;
+                                float2 pr =
+                                    unpack2(fma2(f32x2(__uint_as_float(v[at]), __uint_as_float(v[at + 1])), c22, nm2));
+                                pr.x = ex2(pr.x);
+                                pr.y = ex2(pr.y);
+                                if (kMask && at >= left) pr.x = 0.0f;
+                                if (kMask && at + 1 >= left) pr.y = 0.0f;
+                                const uint64_t pp = f32x2(pr.x, pr.y);
+                                sum[k] = add2(sum[k], pp);
+                                if constexpr (INT8) {
+                                    pr = unpack2(mul2(pp, k ? f.y : f.x));
+                                    if (kMask && at >= left) pr.x = 0.0f;
+                                    if (kMask && at + 1 >= left) pr.y = 0.0f;
+                                }
+                                pk[e / 2 + k] = pack_bf16x2(pr.x, pr.y);
                             }
-                            if constexpr (INT8) {
-                                const float4 f = *reinterpret_cast<const float4*>(vs + j + e);
-                                const float fs[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) pr[k] = kMask && j + e + k >= left ? 0.0f : pr[k] * fs[k];
-                            }
-                            pk[e / 2] = pack_bf16x2(pr[0], pr[1]);
-                            pk[e / 2 + 1] = pack_bf16x2(pr[2], pr[3]);
                         }
                         tmem_st16_start(ts + j / 2, pk);
+                        if (j == 32 || j == 96) {
+                            // P V of this half may start
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sh.p_full[i][j == 96]);
+                        }
                     }
                 };
                 if (masked) probabilities(std::true_type{});
                 else probabilities(std::false_type{});
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_full[i]);
+                const float2 s2 = unpack2(add2(sum[0], sum[1]));
+                l += s2.x + s2.y;
                 if constexpr (INT8) {
                     if (lane == 0) mbar_arrive(&sh.sc_empty[sc]);
                     if (++sc == S::kScaleBufs) sc = 0, sc_phase ^= 1;
@@ -574,7 +640,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
             uint32_t phase = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
             bool ok = true;
             const auto product_s = [&](int i, int b) {
-                if (lane == 0) {
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < DIM / 16; ++k) {
                         const uint32_t off = (k >> 2) * S::kHalfBytes + (k & 3) * 32;
@@ -586,7 +652,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
                 __syncwarp();
             };
             const auto free_buf = [&](int b) {
-                if (lane == 0) mma_commit(&sh.empty[b]);
+                if (elect_one()) mma_commit(&sh.empty[b]);
                 __syncwarp();
             };
             const auto take = [&](int* b) {  // the next tile of the ring
@@ -626,18 +692,22 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
                     }
                     if (more && !take(&bk)) break;
                     for (int i = 0; i < s.q_tiles; ++i) {
-                        if (!(ok = warp_wait(&sh.abort, &sh.p_full[i], p_phase[i], a.err))) break;
-                        p_phase[i] ^= 1;
-                        tc_fence_after();
-                        if (lane == 0) {
 #pragma unroll
-                            for (int k = 0; k < kTile / 16; ++k)
-                                mma_ts(tmem + kTmemO + i * DIM, tmem + i * 128 + 8 * k,
-                                       smem_desc_mn_sw128(buf_addr + bv * S::kTileBytes + k * 2048, S::kHalfBytes),
-                                       kIdescO, t > s.t0 || k > 0);
-                            if (!more) mma_commit(&sh.o_full[i]);
+                        for (int half = 0; half < 2; ++half) {
+                            if (!(ok = ok && warp_wait(&sh.abort, &sh.p_full[i][half], p_phase[i], a.err))) continue;
+                            tc_fence_after();
+                            if (elect_one()) {
+#pragma unroll
+                                for (int k = 4 * half; k < 4 * half + 4; ++k)
+                                    mma_ts(tmem + kTmemO + i * DIM, tmem + i * 128 + 8 * k,
+                                           smem_desc_mn_sw128(buf_addr + bv * S::kTileBytes + k * 2048, S::kHalfBytes),
+                                           kIdescO, t > s.t0 || k > 0);
+                                if (half == 1 && !more) mma_commit(&sh.o_full[i]);
+                            }
+                            __syncwarp();
                         }
-                        __syncwarp();
+                        if (!ok) break;
+                        p_phase[i] ^= 1;
                         if (more) product_s(i, bk);
                     }
                     if (!ok) break;
@@ -646,7 +716,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
                 }
             }
             // nothing of this block's products is in flight when its tensor memory is given back
-            if (lane == 0) mma_commit(&sh.done);
+            if (elect_one()) mma_commit(&sh.done);
             __syncwarp();
             mbar_wait_bounded(&sh.done, 0);
         }
