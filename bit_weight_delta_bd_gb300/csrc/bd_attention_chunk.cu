@@ -2,25 +2,37 @@
 // tensor cores (the formulas and the dealing of the work: bd_attention.cuh).
 //
 // An item is 256 query rows (two tiles of 128) of one kv head; its keys are
-// read in tiles of 128 by TMA.  Per key tile and query tile
-//   S = Q K^T       128 x 128, operands in shared memory, fp32 in tensor memory
+// read in tiles of 128 by TMA and multiplied in steps of 64.  Per step and
+// query tile
+//   S = Q K^T       128 x 64, operands in shared memory, fp32 in tensor memory
 //   P = exp2(c S - m)   one thread per row: maximum, probabilities, denominator
 //   O += P V        P as bf16 in tensor memory (over S), V in shared memory
-// Two warpgroups, one per query tile, take turns with the tensor cores: while
-// one computes probabilities, the products of the other run.  The running
-// maximum that P is formed with lags behind the true one by at most 2^8 (a
-// row's sums are rescaled in tensor memory only when its maximum grew by more
-// than 8 in units of log2; the fp32 sums have room for that factor), so that
-// rescaling is rare after a row's first tiles.  A warp issues the products of
-// both tiles in order, which also orders them: the commit that announces S of
-// key tile t + 1 stands behind P V of tile t.
+// S has two places, so that S of step j + 1 is there before P of step j is
+// done and neither the tensor cores nor the exponentials wait for the other:
+// with one place of 128 keys a query tile's products and exponentials took
+// turns, 3350 cycles for 128 keys and 256 rows of which the tensor cores
+// worked 2300.  (A step of 64 reads Q from shared memory twice as often; the
+// product S is then bound by those reads, at 3/4 of its rate.)
+// The running maximum that P is formed with lags behind the true one by at
+// most 2^8 (a row's sums are rescaled in tensor memory only when its maximum
+// grew by more than 8 in units of log2; the fp32 sums have room for that
+// factor), so that rescaling is rare after a row's first steps.
+// A warp for each query tile issues its products, P V of step j and then S of
+// step j + 2.
 //
 // Int8 keys and values: TMA brings the codes, a fourth warpgroup turns them
-// into bf16 tiles (exactly, as in the decode kernel), once for both query
-// tiles; the scales multiply S and P in the softmax's registers.
+// into tiles of numbers (exactly: K to fp16 and V to bf16), once for both
+// query tiles; the scales multiply S and P in the softmax's registers.  Q
+// enters that product in fp16, scaled by a power of two per row, as in the
+// decode kernel; P stays bf16, whose range the sums of a row's smallest
+// probabilities need.  Within each group of four dims the tiles hold them in
+// the order 0, 2, 1, 3, in which the codes come out of a register.
 //
 // Warps: 0..3 and 4..7 softmax of query tiles 0 and 1 (and loading Q, and
-// writing O); 8 TMA; 9 MMA; 12..15 conversion (int8).
+// writing O); 8 TMA; 9 and 10 MMA of query tiles 0 and 1; 12..15 conversion
+// (int8).
+#include <cuda_fp16.h>
+
 #include <type_traits>
 
 #include "bd_attention.cuh"
@@ -32,6 +44,7 @@ namespace {
 
 constexpr int kTile = 128;       // keys of a tile
 constexpr int kQRows = 128;      // rows of a query tile
+constexpr int kStep = 64;        // keys of a step
 constexpr float kLag = 8.0f;     // how far (log2) a row's maximum may run ahead of the one in use
 
 struct ChunkParams {
@@ -56,10 +69,9 @@ struct ChunkShape {
     static constexpr int kBytes = kOffScale + kScaleBufs * 2 * kTile * 4;
     // registers of a softmax thread, and of the others: the sum over the
     // warpgroups is what the block was launched with
-    static constexpr int kSoftRegs = INT8 ? 184 : 216;
-    static constexpr int kOtherRegs = 72;
+    static constexpr int kSoftRegs = INT8 ? 168 : 208;
+    static constexpr int kOtherRegs = 88;
     static_assert(2 * kSoftRegs + (INT8 ? 2 : 1) * kOtherRegs <= (INT8 ? 4 * 128 : 3 * 168), "register split");
-    static_assert(kBytes + 1024 + 1024 <= 227 * 1024, "shared memory");
 };
 
 constexpr int kMaxBufs = 8;
@@ -68,31 +80,35 @@ struct ChunkShared {
     uint64_t full[kMaxBufs], empty[kMaxBufs];    // bf16 tiles
     uint64_t raw_full[3], raw_empty[3];          // tiles of codes
     uint64_t sc_full[3], sc_empty[3];            // scales
-    uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2];  // P in two halves of 64 keys
+    uint64_t q_full[2], o_full[2];
+    uint64_t s_full[2][2], p_full[2][2], pv_done[2];  // by query tile (and place)
     uint64_t done;
     uint32_t tmem;
     volatile int abort;
 };
 
-constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemO = 256;  // S tiles at 0 and 128, O tiles from 256 on
+// all of it dynamic: the tiles start on a 1024-byte boundary without padding
+template <typename Shape>
+constexpr size_t chunk_smem()
+{
+    static_assert(Shape::kBytes + sizeof(ChunkShared) <= 227 * 1024, "shared memory");
+    return Shape::kBytes + sizeof(ChunkShared);
+}
 
-// A wait of a whole warp; false (for all lanes) once the block has given up.
-__device__ __forceinline__ bool warp_wait(volatile int* abort_flag, uint64_t* bar, uint32_t parity, uint32_t* err)
+constexpr int kSoftWarps = 8, kTmaWarp = 8, kMmaWarp = 9, kConvertWarp = 12;
+
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemO = 256;  // S at 128 i + 64 b (query tile i, place b), O tiles from 256 on
+
+// A wait of a whole warp; false (for all lanes) once the block has given up,
+// which the end of the kernel reports.
+__device__ __forceinline__ bool warp_wait(volatile int* abort_flag, uint64_t* bar, uint32_t parity)
 {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    const uint64_t t0 = global_timer_ns();
-    for (;;) {
-        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-        const bool late = global_timer_ns() - t0 > kWaitLimitNs;
-        if (__any_sync(0xffffffffu, late || *abort_flag)) {
-            if (late && !*abort_flag) {
-                *abort_flag = 1;
-                raise_error(err, kErrTimeout);
-            }
-            return false;
-        }
-    }
+    if (*abort_flag) return false;
+    if (__all_sync(0xffffffffu, mbar_wait_sleeping(bar, parity))) return true;
+    *abort_flag = 1;
+    return false;
 }
 
 template <int N>
@@ -140,7 +156,21 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t* v)
                    "+r"(v[29]), "+r"(v[30]), "+r"(v[31])::"memory");
 }
 
-__device__ __forceinline__ void tmem_st16_start(uint32_t taddr, const uint32_t* v)
+__device__ __forceinline__ void tmem_ld16_wait(uint32_t taddr, uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr)
+        : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                   "+r"(v[15])::"memory");
+}
+
+__device__ __forceinline__ void tmem_st16_start(uint32_t taddr, const uint32_t (&v)[16])
 {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
@@ -223,14 +253,69 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// codes (byte picks 0..1 and 2..3 of r) as pairs of bf16: see bd_attention.cu
-__device__ __forceinline__ uint32_t codes_bf16x2(uint32_t r, uint32_t sel)
+// Two codes, bytes 0 and 2 of r, as a pair of fp16 (see bd_attention.cu).
+__device__ __forceinline__ uint32_t codes_f16x2(uint32_t r)
 {
-    const uint32_t x = __byte_perm(r, 0x43434343u, sel);
-    const uint32_t hi = x & 0xFF7FFF7Fu, lo = x & 0xFF80FF80u;
+    const uint32_t x = (r & 0x00FF00FFu) ^ 0x64806480u, offset = 0xE480E480u;  // 1152 + code, -1152
+    const __half2 d = __hadd2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&offset));
+    return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+// Two codes, bytes 0 and 2 of r, as a pair of bf16: with c the byte, 0x4300 |
+// (c & 0x7f) is 128 + (c & 0x7f), 0x4300 | (c & 0x80) is 128 or 256, and the
+// difference is the code.
+__device__ __forceinline__ uint32_t codes_bf16x2(uint32_t r)
+{
+    const uint32_t hi = (r & 0x007F007Fu) | 0x43004300u, lo = (r & 0x00800080u) | 0x43004300u;
     const __nv_bfloat162 d =
         __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&hi), *reinterpret_cast<const __nv_bfloat162*>(&lo));
     return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+template <bool HALF>
+__device__ __forceinline__ uint2 codes4(uint32_t r)  // in the order 0, 2, 1, 3
+{
+    if constexpr (HALF) return make_uint2(codes_f16x2(r), codes_f16x2(r >> 8));
+    return make_uint2(codes_bf16x2(r), codes_bf16x2(r >> 8));
+}
+
+// A tile of codes as a tile of numbers: 16-byte chunks of 16 codes, chunk x
+// by thread x % 128 of the warpgroup.
+template <int DIM, bool HALF>
+__device__ __forceinline__ void convert_tile(const uint8_t* src, uint8_t* dst, int tid)
+{
+    constexpr int kChunks = DIM / 16;  // of a key
+    constexpr int kMine = kTile * kChunks / 128;
+    constexpr int kHalfBytes = kTile * 128;
+    constexpr int kBatch = 2;  // chunks of an iteration (the loop is kept small: instruction fetch)
+    const int ch = tid % kChunks, key0 = tid / kChunks;  // 128 threads are whole keys
+    // lanes of the upper half store their odd chunk first: no two of eight
+    // neighbouring lanes meet in a bank
+    const int first = ch >= 4;
+    uint8_t* half = dst + (ch >> 2) * kHalfBytes;
+    uint4 w[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) w[j] = *reinterpret_cast<const uint4*>(src + (tid + 128 * j) * 16);
+#pragma unroll 1
+    for (int i0 = 0; i0 < kMine; i0 += kBatch) {
+      uint4 next[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (i0 + kBatch < kMine) next[j] = *reinterpret_cast<const uint4*>(src + (tid + 128 * (i0 + kBatch + j)) * 16);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = i0 + j;
+        const int key = key0 + i * (128 / kChunks);
+        const uint2 a = codes4<HALF>(w[j].x), b = codes4<HALF>(w[j].y);
+        const uint2 c = codes4<HALF>(w[j].z), d = codes4<HALF>(w[j].w);
+        const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(c.x, c.y, d.x, d.y);
+        uint8_t* row = half + key * 128;
+        *reinterpret_cast<uint4*>(row + (((2 * (ch & 3) + first) ^ (key & 7)) << 4)) = first ? hi : lo;
+        *reinterpret_cast<uint4*>(row + (((2 * (ch & 3) + 1 - first) ^ (key & 7)) << 4)) = first ? lo : hi;
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) w[j] = next[j];
+    }
 }
 
 // What a block does next: key tiles [t0, t1) of one (item, kv head).
@@ -269,27 +354,70 @@ struct Walk {
     }
 };
 
-// This thread's row of a segment's query tile i, in shared memory (K-major,
-// 128-byte swizzle, halves of 64 dims); rows past the item are zeros.  A
-// negative scale is taken into Q's sign.
+// Row `row` (of the item) of a segment's Q; null past the item's rows.
 template <int DIM>
-__device__ __forceinline__ void load_q_row(const AttnParams& p, const Segment& s, int i, int r, uint8_t* dst)
+__device__ __forceinline__ const uint4* q_row(const AttnParams& p, const Segment& s, int row)
 {
     const AttentionArgs& a = p.a;
-    const int row = i * kQRows + r;
-    const bool live = row < s.rows && row < p.mb;
-    const int abs_row = s.it.row0 + row, tok = live ? abs_row / p.G : 0;
-    const uint4* src = reinterpret_cast<const uint4*>(
-        a.q + (static_cast<int64_t>(s.sq.q0) + tok) * a.q_stride +
-        static_cast<int64_t>(s.h * p.G + (live ? abs_row - tok * p.G : 0)) * DIM);
-    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+    if (row >= s.rows || row >= p.mb) return nullptr;
+    const int abs_row = s.it.row0 + row, tok = abs_row / p.G;
+    return reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(s.sq.q0) + tok) * a.q_stride +
+                                          static_cast<int64_t>(s.h * p.G + (abs_row - tok * p.G)) * DIM);
+}
+
+__device__ __forceinline__ float abs_max8(float big, uint4 v)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
+    for (int e = 0; e < 4; ++e)
+        big = max3(big, fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u)));
+    return big;
+}
+
+// The power of two at or below |x|, kept within 2^-100 .. 2^100.
+__device__ __forceinline__ float unit_of(float x)
+{
+    return __uint_as_float(__float_as_uint(fminf(fmaxf(x, 7.9e-31f), 1.2e30f)) & 0x7F800000u);
+}
+
+// Row r of a segment's query tile i, in shared memory (K-major, 128-byte
+// swizzle, halves of 64 dims); rows past the item are zeros.  A negative scale
+// is taken into Q's sign; int8: fp16, over the row's power of two, dims in the
+// codes' order.  Returns what the row's products are to be multiplied by.
+template <int DIM, bool INT8>
+__device__ __forceinline__ float load_q(const AttnParams& p, const Segment& s, int i, int r, uint8_t* dst)
+{
+    const uint4* src = q_row<DIM>(p, s, i * kQRows + r);
+    const uint32_t flip = p.a.scale < 0.0f ? 0x80008000u : 0u;
+    float f = 1.0f, back = 1.0f;
+    if constexpr (INT8) {
+        float big = 0.0f;
+#pragma unroll 2
+        for (int c = 0; c < (src ? DIM / 8 : 0); ++c) big = abs_max8(big, src[c]);
+        f = 16384.0f / unit_of(big);
+        back = unit_of(big) / 16384.0f;
+    }
+#pragma unroll 2
     for (int c = 0; c < DIM / 8; ++c) {
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (live) v = src[c];
+        if (src) v = src[c];
         v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+        if constexpr (INT8) {
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                const float x0 = __uint_as_float(w[e] << 16) * f, x1 = __uint_as_float(w[e] & 0xFFFF0000u) * f;
+                const float x2 = __uint_as_float(w[e + 1] << 16) * f, x3 = __uint_as_float(w[e + 1] & 0xFFFF0000u) * f;
+                const __half2 even = __floats2half2_rn(x0, x2), odd = __floats2half2_rn(x1, x3);
+                o[e] = *reinterpret_cast<const uint32_t*>(&even);
+                o[e + 1] = *reinterpret_cast<const uint32_t*>(&odd);
+            }
+            v = make_uint4(o[0], o[1], o[2], o[3]);
+        }
         *reinterpret_cast<uint4*>(dst + (c >> 3) * (kQRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
     }
+    return back;
 }
 
 template <int DIM, bool INT8>
@@ -297,9 +425,8 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
     attn_chunk_kernel(const __grid_constant__ ChunkParams cp)
 {
     using S = ChunkShape<DIM, INT8>;
-    extern __shared__ uint8_t dyn_raw[];
-    __shared__ ChunkShared sh;
-    uint8_t* dyn = dyn_raw + ((1024u - (smem_u32(dyn_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t dyn[];
+    ChunkShared& sh = *reinterpret_cast<ChunkShared*>(dyn + S::kBytes);
     const AttnParams& p = cp.p;
     const AttentionArgs& a = p.a;
     const KvPages& cache = a.cache;
@@ -311,7 +438,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kBufs; ++i) {
             mbar_init(&sh.full[i], INT8 ? 4 : 1);
-            mbar_init(&sh.empty[i], 1);
+            mbar_init(&sh.empty[i], 2);
         }
         for (int i = 0; i < 3; ++i) {
             mbar_init(&sh.raw_full[i], 1);
@@ -321,16 +448,18 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.q_full[i], 4);
-            mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.p_full[i][0], 4);
-            mbar_init(&sh.p_full[i][1], 4);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&sh.s_full[i][b], 1);
+                mbar_init(&sh.p_full[i][b], 4);
+            }
+            mbar_init(&sh.pv_done[i], 1);
             mbar_init(&sh.o_full[i], 1);
         }
-        mbar_init(&sh.done, 1);
+        mbar_init(&sh.done, 2);
         sh.abort = 0;
         fence_mbarrier_init();
     }
-    if (warp == 9) tmem_alloc(&sh.tmem, kTmemCols);
+    if (warp == kMmaWarp) tmem_alloc(&sh.tmem, kTmemCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -362,209 +491,225 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
     __syncwarp();
     Segment s;
 
-    if (warp < 8) {
+    if (warp < kSoftWarps) {
         // -------------------------------------------------------- softmax of query tile i
         reg_inc<S::kSoftRegs>();
         const int i = warp >> 2;
-        const int r = (warp & 3) * 32 + lane;
-        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lane_base + i * 128, to = tmem + lane_base + kTmemO + i * DIM;
+        const int r = 32 * (warp & 3) + lane;  // this thread's row of the tile
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t ts = tmem + lanes + i * 128, to = tmem + lanes + kTmemO + i * DIM;
         uint8_t* q_smem = dyn + i * S::kQBytes;
-        const float c2 = fabsf(a.scale) * kLog2e;
-        uint32_t s_phase = 0, o_phase = 0, sc_phase = 0;
+        float unit = 1.0f;  // of this thread's row of the Q in shared memory
+        uint32_t s_phase = 0, o_phase = 0, pv_phase = 0, sc_phase = 0;
         int sc = 0;
-        bool have = walk.next(s);
-        bool ok = true;
-        const auto put_q = [&](const Segment& q) {
-            load_q_row<DIM>(p, q, i, r, q_smem);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.q_full[i]);
-        };
-        if (have && i < s.q_tiles) put_q(s);
-        while (have && ok) {
-            const Segment cur = s;
-            if (i >= cur.q_tiles) {
+        // After a timeout (reported) the waits return at once and the loops run out on what is there.
+        // (Each part of the loop stands once, and its rare parts are rolled: the code that runs has to
+        // fit the instruction cache, or the warps wait for their instructions.)
+        bool ran = false, whole = false, live = false;  // of the segment whose sums are still to be written
+        int64_t at = 0;
+        float m = -INFINITY, l = 0.0f, m2 = 0.0f;
+        for (;;) {
+            // the products with the last Q are done (S of its last tile stood behind them): the next
+            // one may come in while the last P V runs
+            const bool have = walk.next(s);
+            const bool runs = have && i < s.q_tiles;
+            if (runs) {
+                unit = load_q<DIM, INT8>(p, s, i, r, q_smem);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.q_full[i]);
+            }
+            if (ran) {
+                warp_wait(&sh.abort, &sh.o_full[i], o_phase);
+                o_phase ^= 1;
+                tc_fence_after();
+                live = live && bd_in(kBkAttn, at, whole ? a.T * a.n_q : 2ll * p.blocks * p.mb);
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+                for (int j = 0; j < DIM; j += 16) {
+                    uint32_t o[16];
+                    __syncwarp();
+                    tmem_ld16_wait(to + j, o);
+                    if constexpr (INT8) {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) {  // back from the order 0, 2, 1, 3
+                            const uint32_t x = o[e + 1];
+                            o[e + 1] = o[e + 2];
+                            o[e + 2] = x;
+                        }
+                    }
+                    if (live && whole) {
+                        uint4* dst = reinterpret_cast<uint4*>(a.out + at * DIM + j);
+#pragma unroll
+                        for (int e = 0; e < 16; e += 8) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                w[k] = pack_bf16x2(__uint_as_float(o[e + 2 * k]) * inv,
+                                                   __uint_as_float(o[e + 2 * k + 1]) * inv);
+                            if (l == 0.0f) w[0] = w[1] = w[2] = w[3] = 0u;
+                            dst[e / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else if (live) {
+                        uint4* dst = reinterpret_cast<uint4*>(p.part_o + at * DIM + j);
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) dst[e / 4] = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    }
+                }
+                if (live) {
+                    if (!whole)
+                        p.part_ml[at] = make_float2(m2, l);
+                    else if (a.lse)
+                        a.lse[at] = attn_lse(m2, l);
+                }
+                __syncwarp();
+                tc_fence_before();
+            }
+            if (!have) break;
+            ran = runs;
+            if (!runs) {
                 // no rows here: only the scales' slots have to be handed on
                 if constexpr (INT8) {
-                    for (int t = cur.t0; t < cur.t1 && ok; ++t) {
-                        ok = warp_wait(&sh.abort, &sh.sc_full[sc], sc_phase, a.err);
+                    for (int t = s.t0; t < s.t1; ++t) {
+                        if (!warp_wait(&sh.abort, &sh.sc_full[sc], sc_phase)) break;
                         if (lane == 0) mbar_arrive(&sh.sc_empty[sc]);
                         if (++sc == S::kScaleBufs) sc = 0, sc_phase ^= 1;
                     }
                 }
-                have = walk.next(s);
-                if (have && i < s.q_tiles) put_q(s);
                 continue;
             }
             const int row = i * kQRows + r;
-            const bool live = row < cur.rows && row < p.mb;
-            const int abs_row = cur.it.row0 + row, tok = live ? abs_row / p.G : 0;
-            const int seen = live ? attn_seen(cur.sq, tok, a.causal) : 0;
+            live = row < s.rows && row < p.mb;
+            int seen = 0;
+            {
+                const int abs_row = s.it.row0 + row, tok = live ? abs_row / p.G : 0;
+                if (live) seen = attn_seen(s.sq, tok, a.causal);
+                whole = s.t0 == 0 && s.t1 == s.it.tiles;
+                at = whole ? (static_cast<int64_t>(s.sq.q0) + tok) * a.n_q + s.h * p.G + (abs_row - tok * p.G)
+                           : static_cast<int64_t>(attn_slot(c, s.t0 == 0)) * p.mb + row;
+            }
             // what the tile's first row sees (the others see at least as much): below it no mask
-            const int all_seen = attn_seen(cur.sq, (cur.it.row0 + i * kQRows) / p.G, a.causal);
-            float m = -INFINITY, l = 0.0f;
-            for (int t = cur.t0; t < cur.t1; ++t) {
-                if (!(ok = warp_wait(&sh.abort, &sh.s_full[i], s_phase, a.err))) break;
-                s_phase ^= 1;
+            const int all_seen = attn_seen(s.sq, (s.it.row0 + i * kQRows) / p.G, a.causal);
+            // (a scale of 0 would make NaN of a masked score)
+            const float c2 = fmaxf(fabsf(a.scale) * kLog2e * unit, 1e-30f);
+            m = -INFINITY;
+            l = 0.0f;
+#pragma unroll 1
+            for (int j = 2 * s.t0; j < 2 * s.t1; ++j) {
+                const int b = j & 1;
+                warp_wait(&sh.abort, &sh.s_full[i][b], s_phase);
                 tc_fence_after();
-                uint32_t v[128];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) tmem_ld32_start(ts + 32 * j, v + 32 * j);
+                uint32_t v[64];
+                tmem_ld32_start(ts + 64 * b, v);
+                tmem_ld32_start(ts + 64 * b + 32, v + 32);
                 const float *ks = nullptr, *vs = nullptr;
                 if constexpr (INT8) {
-                    ok = warp_wait(&sh.abort, &sh.sc_full[sc], sc_phase, a.err);
-                    ks = reinterpret_cast<const float*>(dyn + S::kOffScale) + sc * 2 * kTile;
+                    if (b == 0) warp_wait(&sh.abort, &sh.sc_full[sc], sc_phase);
+                    ks = reinterpret_cast<const float*>(dyn + S::kOffScale) + sc * 2 * kTile + kStep * b;
                     vs = ks + kTile;
                 }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) tmem_ld_wait(v + 32 * j);
-                if (!ok) break;
+                tmem_ld_wait(v);
+                tmem_ld_wait(v + 32);
                 if constexpr (INT8) {
 #pragma unroll
-                    for (int j = 0; j < 128; j += 4) {
-                        const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(ks + j);
-                        const float2 a0 = unpack2(mul2(f32x2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), f.x));
-                        const float2 a1 =
-                            unpack2(mul2(f32x2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])), f.y));
-                        v[j] = __float_as_uint(a0.x), v[j + 1] = __float_as_uint(a0.y);
-                        v[j + 2] = __float_as_uint(a1.x), v[j + 3] = __float_as_uint(a1.y);
+                    for (int e = 0; e < 64; e += 4) {
+                        const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(ks + e);
+                        const float2 x = unpack2(mul2(f32x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), f.x));
+                        const float2 y =
+                            unpack2(mul2(f32x2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), f.y));
+                        v[e] = __float_as_uint(x.x), v[e + 1] = __float_as_uint(x.y);
+                        v[e + 2] = __float_as_uint(y.x), v[e + 3] = __float_as_uint(y.y);
                     }
                 }
-                const int left = seen - t * kTile;  // keys of the tile that this row sees
-                const bool masked = (t + 1) * kTile > all_seen;
-                if (masked) {
+                if ((j + 1) * kStep > all_seen) {
+                    const int left = seen - j * kStep;  // keys of the step that the row sees
 #pragma unroll
-                    for (int j = 0; j < 128; ++j)
-                        if (j >= left) v[j] = 0xFF800000u;  // -infinity
+                    for (int e = 0; e < 64; ++e)
+                        if (e >= left) v[e] = 0xFF800000u;  // -infinity
+                    if constexpr (INT8) {
+                        // scales past the sequence may be anything, NaN included: zeros instead (every
+                        // warp writes them, each before it reads)
+                        const int valid = s.sq.len - j * kStep;
+                        float* z = const_cast<float*>(vs);
+                        if (lane >= valid) z[lane] = 0.0f;
+                        if (lane + 32 >= valid) z[lane + 32] = 0.0f;
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
                 float mx[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) mx[k] = fmaxf(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
 #pragma unroll
-                for (int j = 8; j < 128; j += 8)
+                for (int e = 8; e < 64; e += 8)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mx[k] = max3(mx[k], __uint_as_float(v[j + 2 * k]), __uint_as_float(v[j + 2 * k + 1]));
+                        mx[k] = max3(mx[k], __uint_as_float(v[e + 2 * k]), __uint_as_float(v[e + 2 * k + 1]));
                 const float mt = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-                if (t == cur.t0) {
-                    m = mt;
-                } else {
-                    const bool grow = mt > m && (m == -INFINITY || (mt - m) * c2 > kLag);
-                    if (__any_sync(0xffffffffu, grow)) {
-                        const float f = !grow ? 1.0f : m == -INFINITY ? 0.0f : ex2((m - mt) * c2);
-                        if (grow) m = mt;
-                        l *= f;
+                // the first step sets the maximum; later it moves when it has grown by kLag
+                const bool grow = mt > m && (mt - m) * c2 > kLag;
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float f = !grow ? 1.0f : m == -INFINITY ? 0.0f : ex2((m - mt) * c2);
+                    if (grow) m = mt;
+                    l *= f;
+                    if (j > 2 * s.t0) {
+                        // P V of the step before has to be done (S of this step says it of the one before that)
+                        warp_wait(&sh.abort, &sh.pv_done[i], pv_phase ^ 1);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int d = 0; d < DIM; d += 16) {
+                            uint32_t o[16];
+                            tmem_ld16_wait(to + d, o);
 #pragma unroll
-                        for (int j = 0; j < DIM; j += 32) {
-                            uint32_t o[32];
-                            tmem_ld32_start(to + j, o);
-                            tmem_ld_wait(o);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_st16_start(to + j, o);
-                            tmem_st16_start(to + j + 16, o + 16);
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st16_start(to + d, o);
                         }
                     }
                 }
                 const float nm = m == -INFINITY ? 0.0f : fmaf(-m, c2, attn_bias<INT8>());
                 uint64_t sum[2] = {0, 0};  // pairs of zeros
                 const uint64_t c22 = f32x2(c2, c2), nm2 = f32x2(nm, nm);
-                const auto probabilities = [&](auto mask) {
-                    constexpr bool kMask = decltype(mask)::value;
 #pragma unroll
-                    for (int j = 0; j < 128; j += 32) {
-                        uint32_t pk[16];
+                for (int e0 = 0; e0 < 64; e0 += 32) {
+                    uint32_t pk[16];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            [[maybe_unused]] ulonglong2 f{};
-                            if constexpr (INT8) f = *reinterpret_cast<const ulonglong2*>(vs + j + e);
+                    for (int e = 0; e < 32; e += 4) {
+                        [[maybe_unused]] ulonglong2 f{};
+                        if constexpr (INT8) f = *reinterpret_cast<const ulonglong2*>(vs + e0 + e);
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const int at = j + e + 2 * k;
-                                float2 pr =
-                                    unpack2(fma2(f32x2(__uint_as_float(v[at]), __uint_as_float(v[at + 1])), c22, nm2));
-                                pr.x = ex2(pr.x);
-                                pr.y = ex2(pr.y);
-                                if (kMask && at >= left) pr.x = 0.0f;
-                                if (kMask && at + 1 >= left) pr.y = 0.0f;
-                                const uint64_t pp = f32x2(pr.x, pr.y);
-                                sum[k] = add2(sum[k], pp);
-                                if constexpr (INT8) {
-                                    pr = unpack2(mul2(pp, k ? f.y : f.x));
-                                    if (kMask && at >= left) pr.x = 0.0f;
-                                    if (kMask && at + 1 >= left) pr.y = 0.0f;
-                                }
-                                pk[e / 2 + k] = pack_bf16x2(pr.x, pr.y);
-                            }
-                        }
-                        tmem_st16_start(ts + j / 2, pk);
-                        if (j == 32 || j == 96) {
-                            // P V of this half may start
-                            tmem_wait_st();
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&sh.p_full[i][j == 96]);
+                        for (int k = 0; k < 2; ++k) {
+                            const int x = e0 + e + 2 * k;
+                            float2 pr =
+                                unpack2(fma2(f32x2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), c22, nm2));
+                            pr.x = ex2(pr.x);
+                            pr.y = ex2(pr.y);
+                            const uint64_t pp = f32x2(pr.x, pr.y);
+                            sum[k] = add2(sum[k], pp);
+                            if constexpr (INT8) pr = unpack2(mul2(pp, k ? f.y : f.x));
+                            pk[e / 2 + k] = pack_bf16x2(pr.x, pr.y);
                         }
                     }
-                };
-                if (masked) probabilities(std::true_type{});
-                else probabilities(std::false_type{});
+                    tmem_st16_start(ts + 64 * b + e0 / 2, pk);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sh.p_full[i][b]);
+                    if constexpr (INT8)
+                        if (b) mbar_arrive(&sh.sc_empty[sc]);
+                }
+                if (b) s_phase ^= 1;
+                pv_phase ^= 1;
+                if constexpr (INT8)
+                    if (b && ++sc == S::kScaleBufs) sc = 0, sc_phase ^= 1;
                 const float2 s2 = unpack2(add2(sum[0], sum[1]));
                 l += s2.x + s2.y;
-                if constexpr (INT8) {
-                    if (lane == 0) mbar_arrive(&sh.sc_empty[sc]);
-                    if (++sc == S::kScaleBufs) sc = 0, sc_phase ^= 1;
-                }
             }
-            if (!ok) break;
-            // the products with this Q are done (S of the last tile stood behind them): the next one
-            // may come in while the last P V runs
-            have = walk.next(s);
-            if (have && i < s.q_tiles) put_q(s);
-            if (!(ok = warp_wait(&sh.abort, &sh.o_full[i], o_phase, a.err))) break;
-            o_phase ^= 1;
-            tc_fence_after();
-            const bool whole = cur.t0 == 0 && cur.t1 == cur.it.tiles;
-            const int64_t at = (static_cast<int64_t>(cur.sq.q0) + tok) * a.n_q + cur.h * p.G + (abs_row - tok * p.G);
-            const int64_t part = static_cast<int64_t>(attn_slot(c, cur.t0 == 0)) * p.mb + row;
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            const float m2 = m == -INFINITY ? -INFINITY : fmaf(m, c2, -attn_bias<INT8>());
-#pragma unroll
-            for (int j = 0; j < DIM; j += 32) {
-                uint32_t o[32];
-                __syncwarp();
-                tmem_ld32_start(to + j, o);
-                tmem_ld_wait(o);
-                if (live && whole && bd_in(kBkAttn, at, a.T * a.n_q)) {
-                    uint4* dst = reinterpret_cast<uint4*>(a.out + at * DIM + j);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            w[k] = pack_bf16x2(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
-                        dst[e / 8] = l == 0.0f ? make_uint4(0, 0, 0, 0) : make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                } else if (live && !whole && bd_in(kBkAttn, part, 2ll * p.blocks * p.mb)) {
-                    uint4* dst = reinterpret_cast<uint4*>(p.part_o + part * DIM + j);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) dst[e / 4] = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                }
-            }
-            if (live) {
-                if (!whole)
-                    p.part_ml[part] = make_float2(m2, l);
-                else if (a.lse)
-                    a.lse[at] = attn_lse(m2, l);
-            }
-            __syncwarp();
-            tc_fence_before();
+            m2 = m == -INFINITY ? -INFINITY : fmaf(m, c2, -attn_bias<INT8>());
         }
-    } else if (warp < 12) {
+    } else if (warp < kConvertWarp) {
         reg_dec<S::kOtherRegs>();
-        if (warp == 8) {
+        if (warp == kTmaWarp) {
             // ---------------------------------------------------- TMA
             constexpr int kRing = INT8 ? S::kRaw : S::kBufs;
             uint64_t* full = INT8 ? sh.raw_full : sh.full;
@@ -592,7 +737,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
                     const int outer = page * n_kv + s.h;
                     const uint32_t rows = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, mine)) * box_rows);
                     if constexpr (INT8) {
-                        if (!(ok = warp_wait(&sh.abort, &sh.sc_empty[sc], sc_phase ^ 1, a.err))) break;
+                        if (!(ok = warp_wait(&sh.abort, &sh.sc_empty[sc], sc_phase ^ 1))) break;
                         if (lane == 0) mbar_arrive_expect_tx(&sh.sc_full[sc], rows * 8);
                         __syncwarp();
                         if (mine) {
@@ -604,7 +749,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
                         if (++sc == S::kScaleBufs) sc = 0, sc_phase ^= 1;
                     }
                     for (int kv = 0; kv < 2; ++kv) {
-                        if (!(ok = warp_wait(&sh.abort, &empty[buf], phase ^ 1, a.err))) break;
+                        if (!(ok = warp_wait(&sh.abort, &empty[buf], phase ^ 1))) break;
                         if (lane == 0) mbar_arrive_expect_tx(&full[buf], rows * DIM * (INT8 ? 1 : 2));
                         __syncwarp();
                         if (mine) {
@@ -631,91 +776,95 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
                     for (int b = 0; b < S::kScaleBufs; ++b)
                         mbar_wait_bounded(&sh.sc_full[b], b < sc ? sc_phase : sc_phase ^ 1);
             }
-        } else if (warp == 9) {
-            // ---------------------------------------------------- MMA
-            constexpr uint32_t kIdescS = idesc_bf16_f32(kQRows, kTile);
+        } else if (warp < kMmaWarp + 2) {
+            // ---------------------------------------------------- MMA of query tile i
+            constexpr uint32_t kIdescS = INT8 ? idesc_f16_f32(kQRows, kStep) : idesc_bf16_f32(kQRows, kStep);
             constexpr uint32_t kIdescO = idesc_bf16_f32(kQRows, DIM) | (1u << 16);  // V: rows along the contracted index
-            const uint32_t q_addr = smem_u32(dyn), buf_addr = smem_u32(dyn + S::kOffBufs);
+            const int i = warp - kMmaWarp;
+            const uint32_t q_addr = smem_u32(dyn + i * S::kQBytes), buf_addr = smem_u32(dyn + S::kOffBufs);
+            const uint32_t ts = tmem + i * 128, to = tmem + kTmemO + i * DIM;
             int buf = 0;
-            uint32_t phase = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
-            bool ok = true;
-            const auto product_s = [&](int i, int b) {
-                if (elect_one()) {
-#pragma unroll
-                    for (int k = 0; k < DIM / 16; ++k) {
-                        const uint32_t off = (k >> 2) * S::kHalfBytes + (k & 3) * 32;
-                        mma_ss(tmem + i * 128, smem_desc_sw128(q_addr + i * S::kQBytes + off),
-                               smem_desc_sw128(buf_addr + b * S::kTileBytes + off), kIdescS, k > 0);
-                    }
-                    mma_commit(&sh.s_full[i]);
-                }
-                __syncwarp();
-            };
-            const auto free_buf = [&](int b) {
-                if (elect_one()) mma_commit(&sh.empty[b]);
-                __syncwarp();
-            };
-            const auto take = [&](int* b) {  // the next tile of the ring
-                ok = warp_wait(&sh.abort, &sh.full[buf], phase, a.err);
-                tc_fence_after();
-                *b = buf;
+            uint32_t phase = 0, q_phase = 0, p_phase = 0;
+            const auto wait = [&](uint64_t* bar, uint32_t parity) { warp_wait(&sh.abort, bar, parity); };
+            const auto take = [&]() {  // the next tile of the ring
+                const int b = buf;
+                wait(&sh.full[b], phase);
                 if (++buf == S::kBufs) buf = 0, phase ^= 1;
-                return ok;
+                return b;
             };
-            while (ok && walk.next(s)) {
-                int bk = 0, bv = 0;
-                if (!take(&bk)) break;
-                for (int i = 0; i < s.q_tiles && ok; ++i) {
-                    if (!(ok = warp_wait(&sh.abort, &sh.q_full[i], q_phase[i], a.err))) break;
-                    q_phase[i] ^= 1;
-                    tc_fence_after();
-                    product_s(i, bk);
+            // (after a timeout, which is reported, the waits return at once and the loop runs out)
+            while (walk.next(s)) {
+                if (i >= s.q_tiles) {
+                    // nothing to multiply: the tiles are only handed on
+#pragma unroll 1
+                    for (int n = 2 * (s.t1 - s.t0); n > 0; --n) {
+                        const int b = take();
+                        if (lane == 0) mbar_arrive(&sh.empty[b]);
+                    }
+                    continue;
                 }
-                if (!ok) break;
-                free_buf(bk);
-                for (int t = s.t0; t < s.t1 && ok; ++t) {
-                    const bool more = t + 1 < s.t1;
-                    if (!take(&bv)) break;
-                    if constexpr (!INT8) {
-                        // what lies past the sequence may be anything, NaN included: zeros
-                        // instead, so that probabilities of 0 times it stay 0
-                        const int valid = s.sq.len - t * kTile;
-                        if (valid < kTile) {
-                            uint8_t* vt = dyn + S::kOffBufs + bv * S::kTileBytes;
-                            for (int x = (valid > 0 ? valid : 0) * 8 + lane; x < kTile * 8; x += 32)
+                wait(&sh.q_full[i], q_phase);
+                q_phase ^= 1;
+                int bv = 0, bk = 0;
+                // turn j: P V of step j - 2, then S of step j
+#pragma unroll 1
+                for (int j = 2 * s.t0; j < 2 * s.t1 + 2; ++j) {
+                    const int b = j & 1;
+                    const bool pv = j >= 2 * s.t0 + 2, qk = j < 2 * s.t1;
+                    if (pv && b == 0) {
+                        bv = take();
+                        if constexpr (!INT8) {
+                            // what lies past the sequence may be anything, NaN included: zeros
+                            // instead, so that probabilities of 0 times it stay 0 (both warps
+                            // write them, each before its own product)
+                            const int valid = s.sq.len - (j - 2) * kStep;
+                            if (valid < kTile) {
+                                uint8_t* vt = dyn + S::kOffBufs + bv * S::kTileBytes;
+#pragma unroll 1
+                                for (int x = (valid > 0 ? valid : 0) * 8 + lane; x < kTile * 8; x += 32)
 #pragma unroll
-                                for (int half = 0; half < S::kHalves; ++half)
-                                    *reinterpret_cast<uint4*>(vt + half * S::kHalfBytes + x * 16) = make_uint4(0, 0, 0, 0);
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                        }
-                    }
-                    if (more && !take(&bk)) break;
-                    for (int i = 0; i < s.q_tiles; ++i) {
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            if (!(ok = ok && warp_wait(&sh.abort, &sh.p_full[i][half], p_phase[i], a.err))) continue;
-                            tc_fence_after();
-                            if (elect_one()) {
-#pragma unroll
-                                for (int k = 4 * half; k < 4 * half + 4; ++k)
-                                    mma_ts(tmem + kTmemO + i * DIM, tmem + i * 128 + 8 * k,
-                                           smem_desc_mn_sw128(buf_addr + bv * S::kTileBytes + k * 2048, S::kHalfBytes),
-                                           kIdescO, t > s.t0 || k > 0);
-                                if (half == 1 && !more) mma_commit(&sh.o_full[i]);
+                                    for (int half = 0; half < S::kHalves; ++half)
+                                        *reinterpret_cast<uint4*>(vt + half * S::kHalfBytes + x * 16) =
+                                            make_uint4(0, 0, 0, 0);
+                                fence_proxy_async_smem();
+                                __syncwarp();
                             }
-                            __syncwarp();
                         }
-                        if (!ok) break;
-                        p_phase[i] ^= 1;
-                        if (more) product_s(i, bk);
                     }
-                    if (!ok) break;
-                    free_buf(bv);
-                    if (more) free_buf(bk);
+                    if (qk && b == 0) bk = take();
+                    if (pv) {
+                        wait(&sh.p_full[i][b], p_phase);
+                        if (b) p_phase ^= 1;
+                    }
+                    tc_fence_after();
+                    if (elect_one()) {
+                        if (pv) {
+                            const uint64_t v_desc =
+                                smem_desc_mn_sw128(buf_addr + bv * S::kTileBytes + b * kStep * 128, S::kHalfBytes);
+#pragma unroll
+                            for (int k = 0; k < kStep / 16; ++k)
+                                mma_ts(to, ts + 64 * b + 8 * k, v_desc + k * (2048 >> 4), kIdescO,
+                                       j > 2 * s.t0 + 2 || k > 0);
+                            mma_commit(&sh.pv_done[i]);
+                            if (b) mma_commit(&sh.empty[bv]);
+                            if (j == 2 * s.t1 + 1) mma_commit(&sh.o_full[i]);
+                        }
+                        if (qk) {
+                            const uint64_t q_desc = smem_desc_sw128(q_addr);
+                            const uint64_t k_desc = smem_desc_sw128(buf_addr + bk * S::kTileBytes + b * kStep * 128);
+#pragma unroll
+                            for (int k = 0; k < DIM / 16; ++k) {
+                                const uint32_t off = ((k >> 2) * S::kHalfBytes + (k & 3) * 32) >> 4;
+                                mma_ss(ts + 64 * b, q_desc + off, k_desc + off, kIdescS, k > 0);
+                            }
+                            mma_commit(&sh.s_full[i][b]);
+                            if (b) mma_commit(&sh.empty[bk]);
+                        }
+                    }
+                    __syncwarp();
                 }
             }
-            // nothing of this block's products is in flight when its tensor memory is given back
+            // nothing of this warp's products is in flight when the tensor memory is given back
             if (elect_one()) mma_commit(&sh.done);
             __syncwarp();
             mbar_wait_bounded(&sh.done, 0);
@@ -728,29 +877,14 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
             uint32_t raw_phase = 0, phase = 0;
             bool ok = true;
             const int tid = threadIdx.x & 127;
-            constexpr int kChunks = DIM / 16;  // 16-byte chunks of codes of a key
             while (ok && walk.next(s)) {
                 for (int n = 2 * (s.t1 - s.t0); n > 0; --n) {
-                    if (!(ok = warp_wait(&sh.abort, &sh.raw_full[raw], raw_phase, a.err))) break;
-                    if (!(ok = warp_wait(&sh.abort, &sh.empty[buf], phase ^ 1, a.err))) break;
+                    if (!(ok = warp_wait(&sh.abort, &sh.raw_full[raw], raw_phase))) break;
+                    if (!(ok = warp_wait(&sh.abort, &sh.empty[buf], phase ^ 1))) break;
                     const uint8_t* src = dyn + S::kOffRaw + raw * S::kRawBytes;
                     uint8_t* dst = dyn + S::kOffBufs + buf * S::kTileBytes;
-#pragma unroll 4
-                    for (int x = tid; x < kTile * kChunks; x += 128) {
-                        const int key = x / kChunks, ch = x % kChunks;
-                        const uint4 w = *reinterpret_cast<const uint4*>(src + x * 16);
-                        const uint4 lo = make_uint4(codes_bf16x2(w.x, 0x4140), codes_bf16x2(w.x, 0x4342),
-                                                    codes_bf16x2(w.y, 0x4140), codes_bf16x2(w.y, 0x4342));
-                        const uint4 hi = make_uint4(codes_bf16x2(w.z, 0x4140), codes_bf16x2(w.z, 0x4342),
-                                                    codes_bf16x2(w.w, 0x4140), codes_bf16x2(w.w, 0x4342));
-                        uint8_t* half = dst + (ch >> 2) * S::kHalfBytes + key * 128;
-                        const int e = ((2 * (ch & 3)) ^ (key & 7)) << 4, o = ((2 * (ch & 3) + 1) ^ (key & 7)) << 4;
-                        // lanes of the upper half store their odd chunk first: no two of eight
-                        // neighbouring lanes meet in a bank
-                        const bool odd_first = ch >= 4;
-                        *reinterpret_cast<uint4*>(half + (odd_first ? o : e)) = odd_first ? hi : lo;
-                        *reinterpret_cast<uint4*>(half + (odd_first ? e : o)) = odd_first ? lo : hi;
-                    }
+                    if (n & 1) convert_tile<DIM, false>(src, dst, tid);  // V
+                    else convert_tile<DIM, true>(src, dst, tid);         // K
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
@@ -766,7 +900,8 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 9) tmem_dealloc(tmem, kTmemCols);
+    if (threadIdx.x == 0 && sh.abort) raise_error(a.err, kErrTimeout);
+    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
 template <int DIM, bool INT8>
@@ -784,7 +919,7 @@ cudaError_t launch_chunk_shape(const AttnParams& p, cudaStream_t stream)
                            i ? kv.v : kv.k, DIM, kv.page, outer, INT8 ? DIM : 64, kv.page,
                            INT8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
-    const size_t smem = S::kBytes + 1024;
+    constexpr size_t smem = chunk_smem<S>();
     const void* kernel = reinterpret_cast<const void*>(attn_chunk_kernel<DIM, INT8>);
     cudaError_t err = ensure_dynamic_smem(kernel, smem, smem_set);
     if (err != cudaSuccess) return err;

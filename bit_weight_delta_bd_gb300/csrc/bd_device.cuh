@@ -116,6 +116,29 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity)
     return done != 0;
 }
 
+// Waits for the phase with the given parity to complete, asleep for up to
+// about 20 us at a time, in a few instructions (for loops whose code has to be
+// small); gives up after 2^17 sleeps and returns false.
+__device__ __forceinline__ bool mbar_wait_sleeping(uint64_t* bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, 0;\n"
+        "BD_WAIT_%=:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "@p bra BD_DONE_%=;\n\t"
+        "add.u32 n, n, 1;\n\t"
+        "setp.lt.u32 q, n, 131072;\n\t"
+        "@q bra BD_WAIT_%=;\n"
+        "BD_DONE_%=:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    return done != 0;
+}
+
 // Waits for the phase with the given parity to complete; gives up after
 // kWaitLimitNs and returns false (the caller reports kErrTimeout).
 __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity)
