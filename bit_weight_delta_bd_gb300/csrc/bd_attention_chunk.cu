@@ -279,42 +279,40 @@ __device__ __forceinline__ uint2 codes4(uint32_t r)  // in the order 0, 2, 1, 3
     return make_uint2(codes_bf16x2(r), codes_bf16x2(r >> 8));
 }
 
-// A tile of codes as a tile of numbers: 16-byte chunks of 16 codes, chunk x
-// by thread x % 128 of the warpgroup.
+// A tile of codes as a tile of numbers, 16-byte chunks of 16 codes, by the 128
+// threads of a warpgroup.  Eight neighbouring lanes take four chunks of two
+// keys whose numbers differ in the bits (5: the lowest and the third; 64-byte
+// rows: the lowest) that put both their reads from TMA's swizzled tile of
+// codes and their writes to the swizzled tile of numbers into different banks.
+// Later chunks of a thread lie 16 (32) keys on, at the same place of the swizzle.
 template <int DIM, bool HALF>
 __device__ __forceinline__ void convert_tile(const uint8_t* src, uint8_t* dst, int tid)
 {
-    constexpr int kChunks = DIM / 16;  // of a key
-    constexpr int kMine = kTile * kChunks / 128;
-    constexpr int kHalfBytes = kTile * 128;
-    constexpr int kBatch = 2;  // chunks of an iteration (the loop is kept small: instruction fetch)
-    const int ch = tid % kChunks, key0 = tid / kChunks;  // 128 threads are whole keys
-    // lanes of the upper half store their odd chunk first: no two of eight
-    // neighbouring lanes meet in a bank
-    const int first = ch >= 4;
-    uint8_t* half = dst + (ch >> 2) * kHalfBytes;
-    uint4 w[kBatch];
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) w[j] = *reinterpret_cast<const uint4*>(src + (tid + 128 * j) * 16);
-#pragma unroll 1
-    for (int i0 = 0; i0 < kMine; i0 += kBatch) {
-      uint4 next[kBatch];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-        if (i0 + kBatch < kMine) next[j] = *reinterpret_cast<const uint4*>(src + (tid + 128 * (i0 + kBatch + j)) * 16);
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int i = i0 + j;
-        const int key = key0 + i * (128 / kChunks);
-        const uint2 a = codes4<HALF>(w[j].x), b = codes4<HALF>(w[j].y);
-        const uint2 c = codes4<HALF>(w[j].z), d = codes4<HALF>(w[j].w);
-        const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(c.x, c.y, d.x, d.y);
-        uint8_t* row = half + key * 128;
-        *reinterpret_cast<uint4*>(row + (((2 * (ch & 3) + first) ^ (key & 7)) << 4)) = first ? hi : lo;
-        *reinterpret_cast<uint4*>(row + (((2 * (ch & 3) + 1 - first) ^ (key & 7)) << 4)) = first ? lo : hi;
-      }
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) w[j] = next[j];
+    constexpr int kKeys = 128 * 16 / DIM;  // keys of one round
+    constexpr int kRounds = kTile / kKeys;
+    const int warp = tid >> 5, c = tid & 3, odd = (tid >> 2) & 1, rest = (tid >> 3) & 3;
+    int key, ch;
+    if constexpr (DIM == 128) {
+        // the warp's 4 keys of 16: {b, b ^ 5}, b = 2 (warp & 1) + {0, 1}, in the 8 keys of warp >> 1
+        ch = c + 4 * (rest & 1);
+        key = 8 * (warp >> 1) + ((2 * (warp & 1) + (rest >> 1)) ^ (odd ? 5 : 0));
+    } else {
+        ch = c;
+        key = 8 * warp + 2 * rest + odd;
+    }
+    const uint8_t* from = src + key * DIM + ((DIM == 128 ? ch ^ (key & 7) : ch ^ ((key >> 1) & 3)) << 4);
+    uint8_t* row = dst + (ch >> 2) * (kTile * 128) + key * 128;
+    uint8_t* to_lo = row + (((2 * (ch & 3)) ^ (key & 7)) << 4);
+    uint8_t* to_hi = row + (((2 * (ch & 3) + 1) ^ (key & 7)) << 4);
+    uint4 w = *reinterpret_cast<const uint4*>(from);
+#pragma unroll 2
+    for (int i = 0; i < kRounds; ++i) {
+        uint4 next = w;
+        if (i + 1 < kRounds) next = *reinterpret_cast<const uint4*>(from + (i + 1) * kKeys * DIM);
+        const uint2 a = codes4<HALF>(w.x), b = codes4<HALF>(w.y), d = codes4<HALF>(w.z), e = codes4<HALF>(w.w);
+        *reinterpret_cast<uint4*>(to_lo + i * kKeys * 128) = make_uint4(a.x, a.y, b.x, b.y);
+        *reinterpret_cast<uint4*>(to_hi + i * kKeys * 128) = make_uint4(d.x, d.y, e.x, e.y);
+        w = next;
     }
 }
 
@@ -917,7 +915,7 @@ cudaError_t launch_chunk_shape(const AttnParams& p, cudaStream_t stream)
         if (!encode_tma_3d(i ? &cp.v_map : &cp.k_map,
                            INT8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, INT8 ? 1 : 2,
                            i ? kv.v : kv.k, DIM, kv.page, outer, INT8 ? DIM : 64, kv.page,
-                           INT8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B))
+                           INT8 && DIM == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
     constexpr size_t smem = chunk_smem<S>();
     const void* kernel = reinterpret_cast<const void*>(attn_chunk_kernel<DIM, INT8>);
