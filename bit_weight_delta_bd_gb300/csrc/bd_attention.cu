@@ -6,13 +6,16 @@
 // in one pass over the keys with a running maximum m_r: where a tile raises
 // it, the sums so far are multiplied by exp2(m_old - m_new).
 //
-// The decode kernel is bound by the cache's bytes.  One thread of a producer
-// warp's tile keeps a ring of stages (64 keys: K, V, scales) filled by TMA,
-// one box per page; four consumer warps take turns, two of them 32 keys each
-// of every other stage, with a running maximum, denominator and 16 x dim sum
-// of their own, so that nothing is exchanged between warps until an item
-// ends.  Rows are the 16 rows of m16n8k16 (query heads that share a kv head),
-// keys its columns.
+// The decode kernel is bound by the cache's bytes.  One warp keeps a ring of
+// stages (64 keys: K, V, scales) filled by TMA, one box per page; four
+// consumer warps take turns, two of them 32 keys each of every other stage,
+// with a running maximum, denominator and sum of their own, so that nothing is
+// exchanged between warps until an item ends.  Keys are the 16 rows of
+// m16n8k16, the query heads that share a kv head its 8 columns: S^T = K Q^T
+// and O^T += V^T P^T, so that 8 heads leave no row of the product empty (heads
+// as rows: twice the products, exponentials and registers).  K enters by
+// ldmatrix, V by its transposing form, and P by movmatrix, which turns an 8 x 8
+// block of the first product's result into the second's operand.
 //
 // Int8.  Both products run in fp16, which holds the codes exactly: with u =
 // code + 128 the bits 0x6400 | u are 1024 + u, and one logic operation and
@@ -28,6 +31,8 @@
 #include "bd_attention.cuh"
 
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "bd_tma.h"
 
@@ -119,34 +124,42 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
 // ------------------------------------------------------------------------------- decode kernel
 
 constexpr int kMmaTile = 64;     // keys of a stage
-constexpr int kMmaRows = 16;     // rows of an item
 constexpr int kMmaConsumers = 4;
+constexpr int kMmaWholeKeys = 1024;  // caches up to this long are not split over blocks
 constexpr int kMmaKeys = 32;     // keys of a stage that one warp takes
 constexpr int kMmaThreads = 32 * (kMmaConsumers + 1);
 constexpr int kMmaMaxStages = 8;
+constexpr int kMmaMaxRows = 16;  // rows of an item: 8, or 16
+
+// Blocks that an SM holds: 3 with items of 8 rows, whose threads need 128
+// registers or fewer, unless a stage takes 32 KB (three blocks then have room
+// for two stages each: 155 us for the batch of 32 caches of 4096 .. 8192 keys
+// against 132).
+constexpr int mma_blocks_per_sm(int rows, int dim, bool int8) { return rows == 8 && (int8 || dim == 64) ? 3 : 2; }
 
 struct MmaParams {
-    CUtensorMap k_map, v_map;  // [n_pages * n_kv][page][dim], box (128 bytes or a row) x min(page, 64)
+    CUtensorMap k_map, v_map;  // [n_pages * n_kv][page][dim], box a row (in halves of 128 bytes) x min(page, 64)
     AttnParams p;
     int stages;
 };
 
-template <int DIM, bool INT8>
+// NT: groups of 8 rows of an item.
+template <int DIM, bool INT8, int NT>
 struct MmaShape {
+    static constexpr int kRows = 8 * NT;
     static constexpr int kRowBytes = DIM * (INT8 ? 1 : 2);
     static constexpr int kBoxBytes = kRowBytes < 128 ? kRowBytes : 128;  // bytes of a row in one box
     static constexpr int kHalves = kRowBytes / kBoxBytes;
-    static constexpr int kHalfBytes = kMmaTile * kBoxBytes;
     static constexpr int kTileBytes = kMmaTile * kRowBytes;               // K (or V) of a stage
     static constexpr int kStageBytes = 2 * kTileBytes + (INT8 ? 1024 : 0);  // stages stay 1024-byte aligned
-    static constexpr int kBufBytes = 2 * kMmaRows * DIM * 4;              // sums of an item, two warps each
+    static constexpr int kBufBytes = 2 * kRows * DIM * 4;              // sums of an item, two warps each
 };
 
 struct MmaShared {
     uint64_t full[kMmaMaxStages];
     uint64_t empty[kMmaMaxStages];
-    float m[kMmaConsumers][kMmaRows];
-    float l[kMmaConsumers][kMmaRows];
+    float m[kMmaConsumers][kMmaMaxRows];
+    float l[kMmaConsumers][kMmaMaxRows];
     volatile int abort;
     int64_t scan[kMmaThreads / 32];
     int seq, row0;      // the block's first item,
@@ -156,7 +169,7 @@ struct MmaShared {
 // Key tiles of one head of the item of sequence q that starts at row0.
 __device__ __forceinline__ int mma_tiles(const AttnParams& p, const AttnSeq& q, int row0)
 {
-    int last = row0 + kMmaRows - 1;
+    int last = row0 + p.mb - 1;
     const int rows = q.n_new * p.G;
     if (last >= rows) last = rows - 1;
     const int end = attn_seen(q, last / p.G, p.a.causal);
@@ -199,7 +212,7 @@ struct MmaWalk {
         const int n_kv = p.a.cache.n_kv;
         while (u - before >= static_cast<int64_t>(s.tiles) * n_kv) {  // on to the next item
             before += static_cast<int64_t>(s.tiles) * n_kv;
-            s.row0 += kMmaRows;
+            s.row0 += p.mb;
             while (s.row0 >= s.rows && s.seq + 1 < p.a.n_seq) {
                 ++s.seq;
                 s.sq = ahead;
@@ -219,10 +232,34 @@ struct MmaWalk {
     }
 };
 
+// The segments of a block that has a (sequence, head) to itself: its items in
+// order (one, in a decode step), with all their tiles.
+struct WholeWalk {
+    const AttnParams& p;
+    MmaSegment s;
+
+    __device__ __forceinline__ explicit WholeWalk(const AttnParams& pp) : p(pp)
+    {
+        s.seq = static_cast<int>(blockIdx.x) / p.a.cache.n_kv;
+        s.h = static_cast<int>(blockIdx.x) - s.seq * p.a.cache.n_kv;
+        s.sq = attn_seq(p.a, s.seq, s.h == 0);
+        s.rows = s.sq.n_new * p.G;
+        s.row0 = -p.mb;
+        s.t0 = 0;
+    }
+    __device__ __forceinline__ bool next()
+    {
+        s.row0 += p.mb;
+        if (s.row0 >= s.rows) return false;
+        s.tiles = s.t1 = mma_tiles(p, s.sq, s.row0);
+        return true;
+    }
+};
+
 // The whole block: adds up the tiles of all sequences (each thread those of
-// consecutive ones) and finds the item of the block's first unit.  Returns
-// the units of the call.
-__device__ __forceinline__ int64_t mma_deal(const AttnParams& p, MmaShared& sh)
+// consecutive ones), finds the item of the block's first unit and notes down
+// what the join needs.  The block's segments.
+__device__ __forceinline__ MmaWalk mma_deal(const AttnParams& p, MmaShared& sh)
 {
     const AttentionArgs& a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -233,7 +270,7 @@ __device__ __forceinline__ int64_t mma_deal(const AttnParams& p, MmaShared& sh)
     int64_t mine = 0;
     for (int s = s0; s < s1; ++s) {
         const AttnSeq q = attn_seq(a, s, blockIdx.x == 0);
-        for (int row0 = 0; row0 < q.n_new * p.G; row0 += kMmaRows) mine += mma_tiles(p, q, row0);
+        for (int row0 = 0; row0 < q.n_new * p.G; row0 += p.mb) mine += mma_tiles(p, q, row0);
     }
     int64_t x = mine;
 #pragma unroll
@@ -259,7 +296,7 @@ __device__ __forceinline__ int64_t mma_deal(const AttnParams& p, MmaShared& sh)
             int64_t before = at * n_kv;
             for (int s = s0; s < s1; ++s) {
                 const AttnSeq q = attn_seq(a, s, false);
-                for (int row0 = 0; row0 < q.n_new * p.G; row0 += kMmaRows) {
+                for (int row0 = 0; row0 < q.n_new * p.G; row0 += p.mb) {
                     const int64_t n = static_cast<int64_t>(mma_tiles(p, q, row0)) * n_kv;
                     if (u >= before && u < before + n) {
                         sh.seq = s;
@@ -272,7 +309,27 @@ __device__ __forceinline__ int64_t mma_deal(const AttnParams& p, MmaShared& sh)
         }
     }
     __syncthreads();
-    return units;
+    const int c = blockIdx.x;
+    MmaWalk walk(p, c < active ? attn_first(units, active, c) : 0, c < active ? attn_first(units, active, c + 1) : 0,
+                 sh.seq, sh.row0, sh.before);
+    if (threadIdx.x == 0) {
+        AttnJoin j{0, 0, 0, 0};
+        if (c < active) {
+            const int64_t rel = walk.u - walk.before;
+            const int h = attn_div(rel, walk.s.tiles);
+            j = attn_join_of(units, active, c, walk.u, walk.before + static_cast<int64_t>(h) * walk.s.tiles,
+                             walk.s.tiles, walk.s.seq, walk.s.row0, h);
+        }
+        p.joins[c] = j;
+    }
+    return walk;
+}
+
+template <bool WHOLE>
+__device__ __forceinline__ auto mma_walk(const AttnParams& p, MmaShared& sh)
+{
+    if constexpr (WHOLE) return WholeWalk(p);
+    else return mma_deal(p, sh);
 }
 
 __device__ __forceinline__ bool attn_wait(volatile int* abort_flag, uint64_t* bar, uint32_t parity, uint32_t* err)
@@ -299,6 +356,16 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                            uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+        : "memory");
+}
+
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4])
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -315,6 +382,24 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4])
                  : "memory");
 }
 
+// The 8 x 8 block of b16 that the warp holds as an accumulator fragment, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+template <bool HALF>
+__device__ __forceinline__ uint32_t pack16x2(float lo, float hi);
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
+{
+    const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+
 // Two int8 codes, bytes 0 and 2 of r, as a pair of fp16.
 __device__ __forceinline__ uint32_t codes_f16x2(uint32_t r)
 {
@@ -328,6 +413,17 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
 {
     const __half2 r = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+template <>
+__device__ __forceinline__ uint32_t pack16x2<true>(float lo, float hi)
+{
+    return pack_f16x2(lo, hi);
+}
+template <>
+__device__ __forceinline__ uint32_t pack16x2<false>(float lo, float hi)
+{
+    return pack_bf16x2(lo, hi);
 }
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -353,12 +449,6 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
-{
-    const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
-
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kMmaConsumers) : "memory"); }
 
 // Byte offset of 16-byte chunk c of row t in a box of 128- or 64-byte rows
@@ -372,11 +462,12 @@ __device__ __forceinline__ uint32_t swizzled(int t, int c)
         return static_cast<uint32_t>(t * 64 + ((c ^ ((t >> 1) & 3)) << 4));
 }
 
-template <int DIM, bool INT8>
-__global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_constant__ MmaParams mp)
+template <int DIM, bool INT8, int NT, bool WHOLE>
+__global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, INT8))
+    attn_mma_kernel(const __grid_constant__ MmaParams mp)
 {
-    using S = MmaShape<DIM, INT8>;
-    constexpr int kSteps = DIM / 16;  // MMA steps of q . k, and pairs of 8-dim tiles of the output
+    using S = MmaShape<DIM, INT8, NT>;
+    constexpr int kSteps = DIM / 16;  // MMA steps of q . k, and 16-dim tiles of the output
     // all of it dynamic: the ring starts on a 1024-byte boundary without padding
     extern __shared__ __align__(1024) uint8_t dyn_raw[];
     uint8_t* ring = dyn_raw;
@@ -403,22 +494,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
     grid_dependency_wait();
 
     const int n_kv = cache.n_kv;
-    const int64_t units = mma_deal(p, sh);
-    const int active = attn_active(units, p.blocks);
-    const int c = blockIdx.x;
-    MmaWalk walk(p, c < active ? attn_first(units, active, c) : 0, c < active ? attn_first(units, active, c + 1) : 0,
-                 sh.seq, sh.row0, sh.before);
-    if (threadIdx.x == 0) {
-        AttnJoin j{0, 0, 0, 0};
-        if (c < active) {
-            const int64_t rel = walk.u - walk.before;
-            const int h = attn_div(rel, walk.s.tiles);
-            j = attn_join_of(units, active, c, walk.u, walk.before + static_cast<int64_t>(h) * walk.s.tiles,
-                             walk.s.tiles, walk.s.seq, walk.s.row0, h);
-        }
-        p.joins[c] = j;
-    }
-    if (c >= active) return;
+    auto walk = mma_walk<WHOLE>(p, sh);
     const MmaSegment& sg = walk.s;
     int stage = 0;
     uint32_t phase = 0;
@@ -427,22 +503,26 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
         // ------------------------------------------------------------ producer warp
         const int box_rows = cache.page < kMmaTile ? cache.page : kMmaTile;
         const int pages_per_tile = kMmaTile / box_rows;
+        // The page of this lane's box in a tile (lane j looks after the j-th box), looked up one tile
+        // ahead, whether the sequence reaches it or not.
+        const auto page_of = [&](int t) {
+            const int at = (t * kMmaTile + lane * box_rows) >> cache.page_shift;
+            return lane < pages_per_tile && at < a.max_pages
+                       ? a.table[static_cast<int64_t>(sg.seq) * a.max_pages + at]
+                       : 0;
+        };
         while (walk.next()) {
             const int h = sg.h;
-            const int32_t* table = a.table + static_cast<int64_t>(sg.seq) * a.max_pages;
             const int pages = (sg.sq.len + cache.page - 1) >> cache.page_shift;  // that the sequence has
+            int page_next = page_of(sg.t0);
             for (int t = sg.t0; t < sg.t1; ++t) {
-                // lane j looks after the j-th box of the tile
                 const int key = t * kMmaTile + lane * box_rows;
-                const int at = key >> cache.page_shift;
-                const bool mine = lane < pages_per_tile && at < pages;
-                int page = 0;
-                if (mine) {
-                    page = table[at];
-                    if (page < 0 || page >= cache.n_pages) {
-                        raise_error(a.err, kErrBadIndex);
-                        page = 0;
-                    }
+                const bool mine = lane < pages_per_tile && (key >> cache.page_shift) < pages;
+                int page = page_next;
+                if (t + 1 < sg.t1) page_next = page_of(t + 1);
+                if (mine && (page < 0 || page >= cache.n_pages)) {
+                    raise_error(a.err, kErrBadIndex);
+                    page = 0;
                 }
                 const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
                 bool ok = true;
@@ -464,12 +544,13 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
                     uint8_t* st = ring + static_cast<size_t>(stage) * S::kStageBytes;
                     const int row = key & (cache.page - 1);
                     const int outer = page * n_kv + h;
-#pragma unroll
-                    for (int half = 0; half < S::kHalves; ++half) {
-                        uint8_t* dst = st + half * S::kHalfBytes + lane * box_rows * S::kBoxBytes;
-                        const int col = half * (S::kBoxBytes / (INT8 ? 1 : 2));
-                        tma_load_3d(dst, &mp.k_map, col, row, outer, &sh.full[stage]);
-                        tma_load_3d(dst + S::kTileBytes, &mp.v_map, col, row, outer, &sh.full[stage]);
+                    uint8_t* dst = st + lane * box_rows * S::kRowBytes;
+                    if constexpr (S::kHalves == 2) {
+                        tma_load_4d(dst, &mp.k_map, 0, row, 0, outer, &sh.full[stage]);
+                        tma_load_4d(dst + S::kTileBytes, &mp.v_map, 0, row, 0, outer, &sh.full[stage]);
+                    } else {
+                        tma_load_3d(dst, &mp.k_map, 0, row, outer, &sh.full[stage]);
+                        tma_load_3d(dst + S::kTileBytes, &mp.v_map, 0, row, outer, &sh.full[stage]);
                     }
                     if constexpr (INT8) {
                         const int64_t vec = (static_cast<int64_t>(outer) << cache.page_shift) + row;
@@ -495,59 +576,82 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
         const AttnSeq sq = sg.sq;
         const int h = sg.h, t0 = sg.t0, t1 = sg.t1, rows = sg.rows, row0 = sg.row0;
 
-        // the two rows of this thread: keys they see, q as A fragments, and the factor of their scores
-        int seen[2];
-        float cr[2] = {c2, c2};
-        uint32_t qf[kSteps][4];
+        // Q as B fragments: this thread has dims of query row 8 n + g.  Its scores, sums and maxima are
+        // those of rows 8 n + 2 q4 + {0, 1}: keys they see, and the factor of their scores.
+        uint32_t qf[NT][kSteps][2];
+        int seen[NT][2];
+        float cr[NT][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = row0 + g + 8 * i;
+        for (int n = 0; n < NT; ++n) {
+            const int r = row0 + 8 * n + g;
             const bool live = r < rows;
             const int tok = live ? r / p.G : 0;
-            seen[i] = live ? attn_seen(sq, tok, a.causal) : 0;
             const uint16_t* src = a.q + (static_cast<int64_t>(sq.q0) + tok) * a.q_stride +
                                   static_cast<int64_t>(h * p.G + (live ? r - tok * p.G : 0)) * DIM;
+            const int sees = live ? attn_seen(sq, tok, a.causal) : 0;
+            float factor = c2;
             if constexpr (INT8) {
                 // a code fragment holds dims 4 q4 + {0, 2} and 4 q4 + {1, 3} of a step's 16
-                float v[kSteps][4];
+                uint2 w[kSteps];
                 float big = 0.0f;
 #pragma unroll
                 for (int k = 0; k < kSteps; ++k) {
-                    const uint2 w = live ? *reinterpret_cast<const uint2*>(src + 16 * k + 4 * q4) : make_uint2(0, 0);
-                    v[k][0] = __uint_as_float(w.x << 16);
-                    v[k][1] = __uint_as_float(w.x & 0xFFFF0000u);
-                    v[k][2] = __uint_as_float(w.y << 16);
-                    v[k][3] = __uint_as_float(w.y & 0xFFFF0000u);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) big = fmaxf(big, fabsf(v[k][e]));
+                    w[k] = live ? *reinterpret_cast<const uint2*>(src + 16 * k + 4 * q4) : make_uint2(0, 0);
+                    big = fmaxf(big, fmaxf(fabsf(__uint_as_float(w[k].x << 16)),
+                                           fabsf(__uint_as_float(w[k].x & 0xFFFF0000u))));
+                    big = fmaxf(big, fmaxf(fabsf(__uint_as_float(w[k].y << 16)),
+                                           fabsf(__uint_as_float(w[k].y & 0xFFFF0000u))));
                 }
                 big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
                 big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
                 const float unit = pow2_of(big), f = 16384.0f / unit;
-                cr[i] = c2 * (unit / 16384.0f);
+                factor = c2 * (unit / 16384.0f);
 #pragma unroll
                 for (int k = 0; k < kSteps; ++k) {
-                    qf[k][i] = pack_f16x2(v[k][0] * f, v[k][2] * f);
-                    qf[k][i + 2] = pack_f16x2(v[k][1] * f, v[k][3] * f);
+                    qf[n][k][0] = pack_f16x2(__uint_as_float(w[k].x << 16) * f, __uint_as_float(w[k].y << 16) * f);
+                    qf[n][k][1] = pack_f16x2(__uint_as_float(w[k].x & 0xFFFF0000u) * f,
+                                             __uint_as_float(w[k].y & 0xFFFF0000u) * f);
                 }
             } else {
 #pragma unroll
                 for (int k = 0; k < kSteps; ++k) {
                     const int d = 16 * k + 2 * q4;
-                    qf[k][i] = live ? *reinterpret_cast<const uint32_t*>(src + d) : 0u;
-                    qf[k][i + 2] = live ? *reinterpret_cast<const uint32_t*>(src + d + 8) : 0u;
+                    qf[n][k][0] = live ? *reinterpret_cast<const uint32_t*>(src + d) : 0u;
+                    qf[n][k][1] = live ? *reinterpret_cast<const uint32_t*>(src + d + 8) : 0u;
                 }
             }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {  // from the lanes that loaded these rows
+                seen[n][i] = __shfl_sync(0xffffffffu, sees, 4 * (2 * q4 + i));
+                cr[n][i] = INT8 ? __shfl_sync(0xffffffffu, factor, 4 * (2 * q4 + i)) : c2;
+            }
         }
+        // a tile in shared memory: page boxes of box_rows keys, in each the halves of 128 bytes one
+        // after the other (rows of 128 bytes or less have one)
+        const int box_shift = cache.page < kMmaTile ? cache.page_shift : 6;
+        const auto chunk_at = [&](int row, int chunk) {
+            if constexpr (S::kHalves == 1) return swizzled<S::kBoxBytes>(row, chunk);
+            const int box = row >> box_shift, half = chunk >> 3;
+            return ((static_cast<uint32_t>(box) << box_shift) << 8) + ((static_cast<uint32_t>(half) << box_shift) << 7) +
+                   swizzled<128>(row & ((1 << box_shift) - 1), chunk & 7);
+        };
         // the keys that every live row sees: below, no mask is needed
         const int all_seen = attn_seen(sq, row0 / p.G, a.causal);
 
-        float o[2 * kSteps][4];
+        float o[NT][kSteps][4];  // dims of tile k (bf16: g, g + 8; int8: 2 g, 2 g + 1) x rows 8 n + 2 q4 + {0, 1}
+        float m[NT][2], l[NT][2];
 #pragma unroll
-        for (int i = 0; i < 2 * kSteps; ++i)
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+            for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n][k][e] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                m[n][i] = -INFINITY;
+                l[n][i] = 0.0f;
+            }
+        }
         float v_unit = 0.0f;  // int8: power of two at or above every scale of V so far, times 2^(bias - 15)
 
         for (int t = t0; t < t1; ++t, ++turn) {
@@ -571,144 +675,165 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
             const int key0 = t * kMmaTile + slice;    // and in the sequence
             const int mi = lane >> 3, mr = lane & 7;
 
-            // ---- scores of 16 rows x 32 keys: s[n] keys 8 n .. 8 n + 7
-            float s[4][4] = {};
-            if constexpr (INT8) {
-#pragma unroll
-                for (int k = 0; k < kSteps; k += 2)
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        uint32_t r[4];
-                        ldsm_x4(st + swizzled<S::kBoxBytes>(slice + 16 * b + (mi & 1) * 8 + mr, k + (mi >> 1)), r);
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            mma_f16_16816(s[2 * b + (x & 1)], qf[k + (x >> 1)][0], qf[k + (x >> 1)][1],
-                                          qf[k + (x >> 1)][2], qf[k + (x >> 1)][3], codes_f16x2(r[x]),
-                                          codes_f16x2(r[x] >> 8));
-                    }
-            } else {
-#pragma unroll
-                for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        uint32_t r[4];
-                        const int chunk = 2 * k + (mi & 1), row = slice + 16 * b + (mi >> 1) * 8 + mr;
-                        ldsm_x4(st + (chunk >> 3) * S::kHalfBytes + swizzled<S::kBoxBytes>(row, chunk & 7), r);
-                        mma_bf16_16816(s[2 * b], qf[k][0], qf[k][1], qf[k][2], qf[k][3], r[0], r[1]);
-                        mma_bf16_16816(s[2 * b + 1], qf[k][0], qf[k][1], qf[k][2], qf[k][3], r[2], r[3]);
-                    }
-            }
-
-            // ---- to units of log2, masked; this thread's keys are 8 n + 2 q4 + {0, 1}
-            float vs[4][2];
-            if constexpr (INT8) {
-                const float* sc = reinterpret_cast<const float*>(ring + static_cast<size_t>(stage) * S::kStageBytes +
-                                                                 2 * S::kTileBytes) +
-                                  slice + 2 * q4;
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const float2 ks = *reinterpret_cast<const float2*>(sc + 8 * n);
-                    const float2 v = *reinterpret_cast<const float2*>(sc + kMmaTile + 8 * n);
-                    vs[n][0] = v.x;
-                    vs[n][1] = v.y;
-                    s[n][0] *= ks.x * cr[0];
-                    s[n][1] *= ks.y * cr[0];
-                    s[n][2] *= ks.x * cr[1];
-                    s[n][3] *= ks.y * cr[1];
-                }
-            } else {
-#pragma unroll
-                for (int n = 0; n < 4; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[n][e] *= c2;
-            }
-            const bool tail = key0 + kMmaKeys > sq.len;
-            if (key0 + kMmaKeys > all_seen) {
-#pragma unroll
-                for (int n = 0; n < 4; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = key0 + 8 * n + 2 * q4 + (e & 1);
-                        if (key >= seen[e >> 1]) s[n][e] = -INFINITY;
-                        // what lies past the sequence may be anything, NaN included: zeros instead
-                        if (INT8 && e < 2 && key >= sq.len) vs[n][e] = 0.0f;
-                    }
-            }
-
-            // ---- running maximum
-            float mt[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float v = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
-                v = fmaxf(v, fmaxf(fmaxf(s[2][2 * i], s[2][2 * i + 1]), fmaxf(s[3][2 * i], s[3][2 * i + 1])));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-                mt[i] = fmaxf(m[i], v);
-            }
-            float v_new = v_unit;
-            if constexpr (INT8) {
-                float v = fmaxf(fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1])),
-                                fmaxf(fmaxf(vs[2][0], vs[2][1]), fmaxf(vs[3][0], vs[3][1])));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-                constexpr float kUnit = static_cast<float>(1u << (static_cast<int>(attn_bias<true>()) - 14));
-                if (v * (0.5f * kUnit) > 0.5f * v_unit) v_new = pow2_of(v) * kUnit;
-            }
-            if (__any_sync(0xffffffffu, mt[0] > m[0] || mt[1] > m[1] || v_new != v_unit)) {
-                const float fv = INT8 && v_new != v_unit ? v_unit / v_new : 1.0f;
-                v_unit = v_new;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float f = mt[i] == -INFINITY ? 1.0f : exp2f(m[i] - mt[i]);
-                    m[i] = mt[i];
-                    l[i] *= f;
-#pragma unroll
-                    for (int n = 0; n < 2 * kSteps; ++n) {
-                        o[n][2 * i] *= f * fv;
-                        o[n][2 * i + 1] *= f * fv;
-                    }
-                }
-            }
-
-            // ---- probabilities as A fragments of two steps of 16 keys
-            uint32_t pa[2][4];
-            const float v_inv = INT8 ? (v_unit > 0.0f ? 1.0f / v_unit : 0.0f) : 1.0f;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float mu = m[i] == -INFINITY ? 0.0f : m[i] - attn_bias<INT8>();
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const float p0 = ex2(s[2 * b][2 * i] - mu), p1 = ex2(s[2 * b][2 * i + 1] - mu);
-                    const float p2 = ex2(s[2 * b + 1][2 * i] - mu), p3 = ex2(s[2 * b + 1][2 * i + 1] - mu);
-                    l[i] += (p0 + p1) + (p2 + p3);
-                    if constexpr (INT8) {
-                        pa[b][i] = pack_f16x2(p0 * (vs[2 * b][0] * v_inv), p1 * (vs[2 * b][1] * v_inv));
-                        pa[b][i + 2] = pack_f16x2(p2 * (vs[2 * b + 1][0] * v_inv), p3 * (vs[2 * b + 1][1] * v_inv));
-                    } else {
-                        pa[b][i] = pack_bf16x2(p0, p1);
-                        pa[b][i + 2] = pack_bf16x2(p2, p3);
-                    }
-                }
-            }
-
-            // ---- sums: 16 rows x dim += P (16 x 32) V (32 x dim)
-            const uint32_t vt = st + S::kTileBytes;
+            // ---- scores of 32 keys x 8 NT rows: this thread's keys are 16 b + 8 j + g
+            float s[NT][2][4] = {};  // [row group][b][2 j + row]
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 const int row = slice + 16 * b + (mi & 1) * 8 + mr;
                 if constexpr (INT8) {
-                    // a b16 element is a pair of dims: the transposed fragment holds dims 2n, 2n + 1 of
-                    // two keys; tile 2k takes the even dims of a chunk, tile 2k + 1 the odd ones
+#pragma unroll
+                    for (int k = 0; k < kSteps; k += 2) {
+                        uint32_t r[4];
+                        ldsm_x4(st + swizzled<S::kBoxBytes>(row, k + (mi >> 1)), r);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const uint32_t a0 = codes_f16x2(r[2 * x]), a1 = codes_f16x2(r[2 * x + 1]);
+                            const uint32_t a2 = codes_f16x2(r[2 * x] >> 8), a3 = codes_f16x2(r[2 * x + 1] >> 8);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma_f16_16816(s[n][b], a0, a1, a2, a3, qf[n][k + x][0], qf[n][k + x][1]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kSteps; ++k) {
+                        uint32_t r[4];
+                        const int chunk = 2 * k + (mi >> 1);
+                        ldsm_x4(st + chunk_at(row, chunk), r);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma_bf16_16816(s[n][b], r[0], r[1], r[2], r[3], qf[n][k][0], qf[n][k][1]);
+                    }
+                }
+            }
+
+            // ---- to units of log2, masked
+            float vs[2][2];
+            if constexpr (INT8) {
+                const float* sc = reinterpret_cast<const float*>(ring + static_cast<size_t>(stage) * S::kStageBytes +
+                                                                 2 * S::kTileBytes) +
+                                  slice + g;
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float ks = sc[16 * b + 8 * j];
+                        vs[b][j] = sc[kMmaTile + 16 * b + 8 * j];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) s[n][b][2 * j + i] *= ks * cr[n][i];
+                    }
+            } else {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[n][b][e] *= c2;
+            }
+            const bool tail = key0 + kMmaKeys > sq.len;
+            if (key0 + kMmaKeys > all_seen) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int key = key0 + 16 * b + 8 * j + g;
+                        // what lies past the sequence may be anything, NaN included: zeros instead
+                        if (INT8 && key >= sq.len) vs[b][j] = 0.0f;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                if (key >= seen[n][i]) s[n][b][2 * j + i] = -INFINITY;
+                    }
+            }
+
+            // ---- running maxima, over this thread's keys and the 8 lanes of its rows
+            float mt[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    mt[n][i] = fmaxf(fmaxf(s[n][0][i], s[n][0][2 + i]), fmaxf(s[n][1][i], s[n][1][2 + i]));
+            float v_new = v_unit, v_max = 0.0f;
+            if constexpr (INT8) v_max = fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1]));
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) mt[n][i] = fmaxf(mt[n][i], __shfl_xor_sync(0xffffffffu, mt[n][i], x));
+                if constexpr (INT8) v_max = fmaxf(v_max, __shfl_xor_sync(0xffffffffu, v_max, x));
+            }
+            bool grow = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) grow = grow || mt[n][i] > m[n][i];
+            if constexpr (INT8) {
+                constexpr float kUnit = static_cast<float>(1u << (static_cast<int>(attn_bias<true>()) - 14));
+                if (v_max * (0.5f * kUnit) > 0.5f * v_unit) v_new = pow2_of(v_max) * kUnit;
+                grow = grow || v_new != v_unit;
+            }
+            if (__any_sync(0xffffffffu, grow)) {
+                const float fv = INT8 && v_new != v_unit ? v_unit / v_new : 1.0f;
+                v_unit = v_new;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float up = fmaxf(m[n][i], mt[n][i]);
+                        const float f = up == -INFINITY ? 1.0f : ex2(m[n][i] - up);
+                        m[n][i] = up;
+                        l[n][i] *= f;
+#pragma unroll
+                        for (int k = 0; k < kSteps; ++k) {
+                            o[n][k][i] *= f * fv;
+                            o[n][k][2 + i] *= f * fv;
+                        }
+                    }
+            }
+
+            // ---- probabilities, turned into B fragments: keys 16 b + 8 j + 2 q4 + {0, 1} of row 8 n + g
+            uint32_t pb[NT][2][2];
+            const float v_inv = INT8 ? (v_unit > 0.0f ? 1.0f / v_unit : 0.0f) : 1.0f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float mu[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) mu[i] = m[n][i] == -INFINITY ? 0.0f : m[n][i] - attn_bias<INT8>();
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float p0 = ex2(s[n][b][2 * j] - mu[0]), p1 = ex2(s[n][b][2 * j + 1] - mu[1]);
+                        l[n][0] += p0;
+                        l[n][1] += p1;
+                        const float w = INT8 ? vs[b][j] * v_inv : 1.0f;
+                        pb[n][b][j] = transpose8(INT8 ? pack16x2<INT8>(p0 * w, p1 * w) : pack16x2<INT8>(p0, p1));
+                    }
+            }
+
+            // ---- sums: dim x 8 NT rows += V^T (dim x 32) P^T (32 x 8 NT)
+            const uint32_t vt = st + S::kTileBytes;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                if constexpr (INT8) {
+                    // a b16 element is a pair of dims: the transposed fragment holds dims 2 g, 2 g + 1 of
+                    // two keys; the tile's rows 0..7 take the even dims of a chunk, rows 8..15 the odd ones
+                    const int row = slice + 16 * b + (mi & 1) * 8 + mr;
 #pragma unroll
                     for (int k = 0; k < kSteps; k += 2) {
                         uint32_t r[4];
                         ldsm_x4_t(vt + swizzled<S::kBoxBytes>(row, k + (mi >> 1)), r);
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            mma_f16_16816(o[2 * (k + x)], pa[b][0], pa[b][1], pa[b][2], pa[b][3],
-                                          codes_f16x2(r[2 * x]), codes_f16x2(r[2 * x + 1]));
-                            mma_f16_16816(o[2 * (k + x) + 1], pa[b][0], pa[b][1], pa[b][2], pa[b][3],
-                                          codes_f16x2(r[2 * x] >> 8), codes_f16x2(r[2 * x + 1] >> 8));
+                            const uint32_t a0 = codes_f16x2(r[2 * x]), a1 = codes_f16x2(r[2 * x] >> 8);
+                            const uint32_t a2 = codes_f16x2(r[2 * x + 1]), a3 = codes_f16x2(r[2 * x + 1] >> 8);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma_f16_16816(o[n][k + x], a0, a1, a2, a3, pb[n][b][0], pb[n][b][1]);
                         }
                     }
                 } else {
@@ -719,19 +844,21 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
                         mask0 = (k < sq.len ? 0xFFFFu : 0u) | (k + 1 < sq.len ? 0xFFFF0000u : 0u);
                         mask1 = (k + 8 < sq.len ? 0xFFFFu : 0u) | (k + 9 < sq.len ? 0xFFFF0000u : 0u);
                     }
+                    const int row = slice + 16 * b + (mi >> 1) * 8 + mr;
 #pragma unroll
                     for (int k = 0; k < kSteps; ++k) {
                         uint32_t r[4];
-                        const int chunk = 2 * k + (mi >> 1);
-                        ldsm_x4_t(vt + (chunk >> 3) * S::kHalfBytes + swizzled<S::kBoxBytes>(row, chunk & 7), r);
+                        const int chunk = 2 * k + (mi & 1);
+                        ldsm_x4_t(vt + chunk_at(row, chunk), r);
                         if (tail) {
                             r[0] &= mask0;
-                            r[1] &= mask1;
-                            r[2] &= mask0;
+                            r[1] &= mask0;
+                            r[2] &= mask1;
                             r[3] &= mask1;
                         }
-                        mma_bf16_16816(o[2 * k], pa[b][0], pa[b][1], pa[b][2], pa[b][3], r[0], r[1]);
-                        mma_bf16_16816(o[2 * k + 1], pa[b][0], pa[b][1], pa[b][2], pa[b][3], r[2], r[3]);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma_bf16_16816(o[n][k], r[0], r[1], r[2], r[3], pb[n][b][0], pb[n][b][1]);
                     }
                 }
             }
@@ -745,51 +872,63 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
 
         // ---- join the four warps: (0 + 2) and (1 + 3) in the two buffers
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-            if (q4 == 0) {
-                sh.m[warp][g + 8 * i] = m[i] - attn_bias<INT8>();
-                sh.l[warp][g + 8 * i] = l[i];
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], x);
+                m[n][i] -= attn_bias<INT8>();
+                if (g == 0) {
+                    sh.m[warp][8 * n + 2 * q4 + i] = m[n][i];
+                    sh.l[warp][8 * n + 2 * q4 + i] = l[n][i];
+                }
             }
-        }
         consumers_sync();
-        float f[2];
+        float f[NT][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float mm = sh.m[0][g + 8 * i];
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int w = 1; w < kMmaConsumers; ++w) mm = fmaxf(mm, sh.m[w][g + 8 * i]);
-            f[i] = attn_weight(m[i] - attn_bias<INT8>(), l[i], mm);
-            if (INT8 && f[i] != 0.0f) f[i] *= v_unit;  // the sums are over the scales' unit
-        }
+            for (int i = 0; i < 2; ++i) {
+                const int r = 8 * n + 2 * q4 + i;
+                float mm = sh.m[0][r];
+#pragma unroll
+                for (int w = 1; w < kMmaConsumers; ++w) mm = fmaxf(mm, sh.m[w][r]);
+                f[n][i] = attn_weight(m[n][i], l[n][i], mm);
+                if (INT8 && f[n][i] != 0.0f) f[n][i] *= v_unit;  // the sums are over the scales' unit
+            }
+#pragma unroll 1
         for (int w = 0; w < 2; ++w) {
             if ((warp >> 1) == w) {
-                float* mine = buf + (warp & 1) * kMmaRows * DIM;
+                float* mine = buf + (warp & 1) * S::kRows * DIM;
 #pragma unroll
-                for (int n = 0; n < 2 * kSteps; ++n)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        // bf16: tile n, columns 2 q4 + {0, 1}; int8: chunk n / 2, dims 4 q4 + {0, 2} of
-                        // the even tile and 4 q4 + {1, 3} of the odd one, kept at places 2 (n & 1) + {0, 1}
-                        const int d = INT8 ? 16 * (n >> 1) + 4 * q4 + 2 * (n & 1) : 8 * n + 2 * q4;
-                        float2* b = reinterpret_cast<float2*>(mine + (g + 8 * i) * DIM + d);
-                        float2 v = make_float2(0.0f, 0.0f);
-                        if (f[i] != 0.0f) v = make_float2(o[n][2 * i] * f[i], o[n][2 * i + 1] * f[i]);
-                        if (w == 1) {
-                            const float2 x = *b;
-                            v.x += x.x;
-                            v.y += x.y;
+                        float* line = mine + (8 * n + 2 * q4 + i) * DIM;
+#pragma unroll
+                        for (int k = 0; k < kSteps; ++k) {
+                            // (in an order of the row's own: the lanes' banks differ)
+                            const float x = f[n][i] == 0.0f ? 0.0f : o[n][k][i] * f[n][i];
+                            const float y = f[n][i] == 0.0f ? 0.0f : o[n][k][2 + i] * f[n][i];
+                            if constexpr (INT8) {
+                                float2* b = reinterpret_cast<float2*>(line + ((16 * k + 2 * g) ^ (q4 << 4)));
+                                const float2 old = w ? *b : make_float2(0.0f, 0.0f);
+                                *b = make_float2(old.x + x, old.y + y);
+                            } else {
+                                float* b0 = line + ((16 * k + g) ^ (q4 << 3));
+                                float* b1 = line + ((16 * k + 8 + g) ^ (q4 << 3));
+                                *b0 = w ? *b0 + x : x;
+                                *b1 = w ? *b1 + y : y;
+                            }
                         }
-                        *b = v;
                     }
             }
             consumers_sync();
         }
 
         const bool whole = t0 == 0 && t1 == sg.tiles;
-        const int slot = attn_slot(c, t0 == 0);
-        const int live_rows = rows - row0 < kMmaRows ? rows - row0 : kMmaRows;
+        const int slot = attn_slot(blockIdx.x, t0 == 0);
+        const int live_rows = rows - row0 < S::kRows ? rows - row0 : S::kRows;
         for (int i = threadIdx.x; i < live_rows * (DIM / 4); i += 32 * kMmaConsumers) {
             const int r = i / (DIM / 4), d = 4 * (i % (DIM / 4));
             float mm = sh.m[0][r];
@@ -801,10 +940,10 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
                 const float lw = sh.l[w][r];
                 ll += lw * attn_weight(sh.m[w][r], lw, mm);
             }
-            float4 v = *reinterpret_cast<const float4*>(buf + r * DIM + d);
-            const float4 v1 = *reinterpret_cast<const float4*>(buf + kMmaRows * DIM + r * DIM + d);
+            const int place = r * DIM + (d ^ (((r >> 1) & 3) << (INT8 ? 4 : 3)));
+            float4 v = *reinterpret_cast<const float4*>(buf + place);
+            const float4 v1 = *reinterpret_cast<const float4*>(buf + S::kRows * DIM + place);
             v = make_float4(v.x + v1.x, v.y + v1.y, v.z + v1.z, v.w + v1.w);
-            if constexpr (INT8) v = make_float4(v.x, v.z, v.y, v.w);  // from places to dims
             if (whole) {
                 const int row = row0 + r, tok = row / p.G;
                 const int64_t at = (static_cast<int64_t>(sq.q0) + tok) * a.n_q + h * p.G + (row - tok * p.G);
@@ -815,8 +954,8 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attn_mma_kernel(const __grid_c
                     if (d == 0 && a.lse) a.lse[at] = attn_lse(mm, ll);
                 }
             } else {
-                const int64_t at = static_cast<int64_t>(slot) * kMmaRows + r;
-                if (bd_in(kBkAttn, at, 2ll * p.blocks * kMmaRows)) {
+                const int64_t at = static_cast<int64_t>(slot) * S::kRows + r;
+                if (bd_in(kBkAttn, at, 2ll * p.blocks * S::kRows)) {
                     *reinterpret_cast<float4*>(p.part_o + at * DIM + d) = v;
                     if (d == 0) p.part_ml[at] = make_float2(mm, ll);
                 }
@@ -900,10 +1039,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     }
 }
 
-template <int DIM, bool INT8>
+template <int DIM, bool INT8, int NT, bool WHOLE>
 cudaError_t launch_mma_shape(const AttnParams& p, cudaStream_t stream)
 {
-    using S = MmaShape<DIM, INT8>;
+    using S = MmaShape<DIM, INT8, NT>;
     static std::atomic<size_t> smem_set[kHostMaxDevices];
     const KvPages& kv = p.a.cache;
     MmaParams mp{};
@@ -912,17 +1051,24 @@ cudaError_t launch_mma_shape(const AttnParams& p, cudaStream_t stream)
     const auto type = INT8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const auto swz = S::kBoxBytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
     const uint64_t outer = static_cast<uint64_t>(kv.n_pages) * kv.n_kv;
-    for (int i = 0; i < 2; ++i)
-        if (!encode_tma_3d(i ? &mp.v_map : &mp.k_map, type, INT8 ? 1 : 2, i ? kv.v : kv.k, DIM, kv.page, outer,
-                           S::kBoxBytes / (INT8 ? 1 : 2), box_rows, swz))
+    for (int i = 0; i < 2; ++i) {
+        CUtensorMap* map = i ? &mp.v_map : &mp.k_map;
+        const void* base = i ? kv.v : kv.k;
+        if (!(S::kHalves == 2 ? encode_tma_parts(map, type, 2, base, DIM, kv.page, outer, 2, box_rows, swz)
+                              : encode_tma_3d(map, type, INT8 ? 1 : 2, base, DIM, kv.page, outer, DIM, box_rows, swz)))
             return cudaErrorInvalidValue;
-    // two blocks per SM: 113 KB each
-    constexpr size_t kBudget = 113u * 1024u, kRest = S::kBufBytes + sizeof(MmaShared);
-    mp.stages = static_cast<int>((kBudget - kRest) / S::kStageBytes);
+    }
+    // the SM's shared memory shared by the blocks that it holds; all of it
+    // where there are no more blocks than SMs
+    constexpr size_t kRest = S::kBufBytes + sizeof(MmaShared);
+    const size_t budget = p.blocks <= p.a.sm_count ? 227u * 1024u
+                                                   : 228u * 1024u / mma_blocks_per_sm(8 * NT, DIM, INT8) - 1024u;
+    mp.stages = static_cast<int>((budget - kRest) / S::kStageBytes);
     if (mp.stages > kMmaMaxStages) mp.stages = kMmaMaxStages;
     const size_t smem = static_cast<size_t>(mp.stages) * S::kStageBytes + kRest;
-    cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(attn_mma_kernel<DIM, INT8>), smem, smem_set);
-    launch_dep(err, attn_mma_kernel<DIM, INT8>, dim3(p.blocks), dim3(kMmaThreads), smem, stream, mp);
+    const auto kernel = attn_mma_kernel<DIM, INT8, NT, WHOLE>;
+    cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem, smem_set);
+    launch_dep(err, kernel, dim3(p.blocks), dim3(kMmaThreads), smem, stream, mp);
     return err;
 }
 
@@ -950,17 +1096,28 @@ AttnWs attn_layout(int64_t T, int64_t n_seq, int64_t G, int dim, int mb, int blo
 
 cudaError_t launch_attention_mma(const AttnParams& p, cudaStream_t stream)
 {
+    const auto of = [&](auto dim, auto int8) {
+        constexpr int kDim = decltype(dim)::value;
+        constexpr bool kInt8 = decltype(int8)::value;
+        if (p.mb == 8)
+            return p.whole ? launch_mma_shape<kDim, kInt8, 1, true>(p, stream)
+                           : launch_mma_shape<kDim, kInt8, 1, false>(p, stream);
+        return p.whole ? launch_mma_shape<kDim, kInt8, 2, true>(p, stream)
+                       : launch_mma_shape<kDim, kInt8, 2, false>(p, stream);
+    };
+    using Yes = std::true_type;
+    using No = std::false_type;
     if (p.a.cache.dim == 128)
-        return p.a.cache.int8 ? launch_mma_shape<128, true>(p, stream) : launch_mma_shape<128, false>(p, stream);
-    return p.a.cache.int8 ? launch_mma_shape<64, true>(p, stream) : launch_mma_shape<64, false>(p, stream);
+        return p.a.cache.int8 ? of(std::integral_constant<int, 128>{}, Yes{}) : of(std::integral_constant<int, 128>{}, No{});
+    return p.a.cache.int8 ? of(std::integral_constant<int, 64>{}, Yes{}) : of(std::integral_constant<int, 64>{}, No{});
 }
 
 size_t attention_workspace_size(int64_t T, int64_t n_seq, int n_q, int n_kv, int dim)
 {
     // the host may learn how long the chunks are only with the call: room for either kernel
     const int G = n_q / n_kv;
-    const size_t mma = attn_layout(T, n_seq, G, dim, kMmaRows, kAttnMaxBlocks).total;
-    const size_t chunk = attn_layout(T, n_seq, G, dim, kChunkRows, kAttnMaxBlocks / 2).total;
+    const size_t mma = attn_layout(T, n_seq, G, dim, kMmaMaxRows, kAttnMaxBlocks).total;
+    const size_t chunk = attn_layout(T, n_seq, G, dim, kChunkRows, kAttnMaxChunkBlocks).total;
     return mma > chunk ? mma : chunk;
 }
 
@@ -970,12 +1127,17 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream)
     AttnParams p{};
     p.a = a;
     p.G = a.n_q / a.cache.n_kv;
-    const bool chunk = a.max_new * p.G > kMmaRows;
+    const int64_t rows = a.max_new * p.G;  // of a sequence, as far as the host knows
+    const bool chunk = rows > kMmaMaxRows;
     p.tile = chunk ? kChunkTile : kMmaTile;
-    p.mb = chunk ? kChunkRows : kMmaRows;
-    const int most = chunk ? kAttnMaxBlocks / 2 : kAttnMaxBlocks;
-    p.blocks = chunk ? a.sm_count : 2 * a.sm_count;
+    p.mb = chunk ? kChunkRows : rows > 8 ? kMmaMaxRows : 8;
+    const int most = chunk ? kAttnMaxChunkBlocks : kAttnMaxBlocks;
+    p.blocks = chunk ? a.sm_count : mma_blocks_per_sm(p.mb, a.cache.dim, a.cache.int8) * a.sm_count;
     if (p.blocks > most) p.blocks = most;
+    // Short caches, as far as the page table's width says: a block for each
+    // (sequence, head), which needs no deal and nothing to join.
+    p.whole = !chunk && a.max_pages * a.cache.page <= kMmaWholeKeys && a.n_seq * a.cache.n_kv <= INT32_MAX;
+    if (p.whole) p.blocks = static_cast<int>(a.n_seq * a.cache.n_kv);
     const AttnWs w = attn_layout(a.T, a.n_seq, p.G, a.cache.dim, p.mb, most);
     char* ws = static_cast<char*>(a.ws);
     p.head = reinterpret_cast<AttnHeader*>(ws + w.head);
@@ -987,7 +1149,8 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream)
     cudaError_t err = cudaSuccess;
     if (chunk) launch_dep(err, attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
     if (err == cudaSuccess) err = chunk ? launch_attention_chunk(p, stream) : launch_attention_mma(p, stream);
-    const dim3 grid(static_cast<unsigned>(p.blocks > 1 ? p.blocks - 1 : 1), chunk ? 16 : 4);
+    if (p.whole) return err;
+    const dim3 grid(static_cast<unsigned>(p.blocks > 1 ? p.blocks - 1 : 1), chunk ? 16 : p.mb / 4);
     launch_dep(err, a.cache.dim == 128 ? attn_join_kernel<128> : attn_join_kernel<64>, grid, dim3(kJoinThreads), 0,
                stream, p);
     return err;

@@ -27,7 +27,8 @@
 
 namespace bd {
 
-constexpr int kAttnMaxBlocks = 304;  // blocks of a launch at most: two for each of 152 SMs
+constexpr int kAttnMaxBlocks = 456;       // blocks of a launch at most: three for each of 152 SMs
+constexpr int kAttnMaxChunkBlocks = 152;  // chunks: one
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -54,6 +55,7 @@ struct AttnParams {
     int G;                // query heads of a kv head
     int tile, mb;         // keys per tile, rows per item
     int blocks;           // N
+    int whole;            // a block for each (sequence, head), and nothing to join (decode kernel)
     AttnHeader* head;
     AttnItem* items;
     int32_t* item_off;    // [n_seq + 1] first item of a sequence
@@ -180,7 +182,7 @@ __device__ __forceinline__ float attn_weight(float m, float l, float m_all)
 // Log-sum-exp of a row; m is in units of log2, l == 0 marks a row that saw no key.
 __device__ __forceinline__ float attn_lse(float m, float l) { return l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2; }
 
-// Few rows per sequence (bd_attention.cu): 16 rows an item, 64 keys a tile.
+// Few rows per sequence (bd_attention.cu): 8 or 16 rows an item, 64 keys a tile.
 cudaError_t launch_attention_mma(const AttnParams& p, cudaStream_t stream);
 // Chunks (bd_attention_chunk.cu): 256 rows an item, 128 keys a tile.
 cudaError_t launch_attention_chunk(const AttnParams& p, cudaStream_t stream);

@@ -25,6 +25,13 @@ bool encode_tma_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base
 bool encode_tma_3d(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t elem_bytes, const void* base, uint64_t cols,
                    uint64_t rows, uint64_t outer, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle);
 
+// Encodes a 4-D map over the same array whose rows are cut into `parts` equal
+// parts: coordinates (place in the part, row, part, outer), with a box of one
+// part's columns x box_rows x all parts x 1, so that one copy brings whole rows
+// with each part's pieces together.
+bool encode_tma_parts(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t elem_bytes, const void* base, uint64_t cols,
+                      uint64_t rows, uint64_t outer, uint32_t parts, uint32_t box_rows, CUtensorMapSwizzle swizzle);
+
 // Raises a kernel's dynamic shared-memory limit on the current device to at
 // least `bytes` and asks for the largest shared-memory carve-out, calling the
 // runtime only the first time per device (the attributes persist);
