@@ -317,6 +317,18 @@ def bd_rms_norm_workspace_size(T: int, d: int) -> int:
     return int(load().bd_rms_norm_workspace_size(T, d))
 
 
+def _row_ptrs(rows, n: int, name: str, dev: int) -> list[int]:
+    """Pointers of contiguous bf16 tensors of n elements."""
+    ptrs = []
+    for t in rows:
+        if (t.get_device() != dev or t.numel() != n or t.dtype not in _BF16_LIKE or not t.is_contiguous()):
+            if t.numel() != n:
+                raise ValueError(f"every {name} must have the shape [{n}]")
+            _ptr(t, name, _BF16_LIKE, False, dev)
+        ptrs.append(t.data_ptr())
+    return ptrs
+
+
 def bd_rms_norm(x, gain, eps, out, ws, residual=None, residual_out=None, scale=None, vid=None, gain_list=(),
                 stream=None) -> None:
     """out = norm(x + residual) * gain (the gain of token t's variant, vid[t], out of gain_list); out bf16, fp32, or
@@ -335,9 +347,7 @@ def bd_rms_norm(x, gain, eps, out, ws, residual=None, residual_out=None, scale=N
     tab, V = None, 0
     if vid is not None:
         V = len(gain_list)
-        if any(t.numel() != d for t in gain_list):
-            raise ValueError("every gain must have the shape [d]")
-        tab = (ctypes.c_void_p * max(V, 1))(*[_ptr(t, "gain", _BF16_LIKE, False, dev) for t in gain_list])
+        tab = (ctypes.c_void_p * max(V, 1))(*_row_ptrs(gain_list, d, "gain", dev))
     out_dtype = _OUT_DTYPES.get(out.dtype)
     if out_dtype is None:
         raise ValueError(f"out has dtype {out.dtype}, expected bfloat16, float32 or float8_e4m3fn")
@@ -382,8 +392,10 @@ class KvPages:
 
 def _heads(t, name: str, dim: int, dev: int) -> tuple[int, int]:
     """(pointer, row stride) of a bf16 [T][heads][dim] tensor whose rows may be apart."""
-    T, heads, d = t.shape
     s0, s1, s2 = t.stride()
+    if s1 == dim and s2 == 1 and s0 > dim and t.get_device() == dev and t.dtype in _BF16_LIKE:
+        return t.data_ptr(), s0
+    T, heads, d = t.shape
     if d != dim or s2 != 1 or (heads > 1 and s1 != dim):
         raise ValueError(f"{name} must be [T][heads][{dim}] with contiguous rows")
     if t.get_device() != dev:
@@ -418,7 +430,7 @@ def bd_rope_append(q, k, v, pos, rope_table, slot, cache: KvPages, q_out, ws, ax
     qp = qs = op = os_ = n_q = 0
     if q is not None:
         n_q = q.shape[1]
-        if q.shape[0] != T or q_out.shape != q.shape:
+        if q.shape != (T, n_q, dim) or q_out.shape != q.shape:
             raise ValueError("q and q_out must have T rows of the same heads")
         qp, qs = _heads(q, "q", dim, dev)
         op, os_ = _heads(q_out, "q_out", dim, dev)

@@ -631,6 +631,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
                         float* z = const_cast<float*>(vs);
                         if (lane >= valid) z[lane] = 0.0f;
                         if (lane + 32 >= valid) z[lane + 32] = 0.0f;
+                        fence_proxy_async_smem();  // before TMA's next scales in this place
                     }
                     __syncwarp();
                 }

@@ -12,7 +12,8 @@
 namespace bd {
 namespace {
 
-constexpr int kRopeThreads = 128;
+constexpr int kRopeThreads = 64;  // of a block at most
+constexpr int kRopeAhead = 2;     // heads that a thread loads before it works on the first
 constexpr int kUnit = 16;  // elements of a head that one thread handles
 
 __device__ __forceinline__ void unpack8(uint4 u, float* f)
@@ -64,86 +65,107 @@ struct RopeParams {
 // i = 8 u on, or elements 16 u .. 16 u + 15 (interleaved pairs, the part past
 // rot, and v).  Its unit u stays the same for all heads it visits, so the
 // cosines and sines are read once per token.  UPH = dim / 16 units per head;
-// a block is one token (grid x) and one part of its heads (grid y).
+// a block is one token (grid x) and one part of its heads (grid y), blockDim /
+// UPH heads a pass.  What bounds it is how many tokens an SM works on at a
+// time, since each waits for its position, then its table row, then its heads:
+// small blocks, and the heads of the first two passes loaded before the
+// position is there.  4096 tokens, 64/8 heads of 128, bf16: 30.5 us, 5.6 TB/s
+// (256 threads and three passes ahead 37.9, 128 threads and the position first
+// 33.2); int8 32.4 us.
 template <int UPH, bool INT8>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeParams p)
 {
     constexpr int kDim = UPH * kUnit;
-    constexpr int kHeadsPerPass = kRopeThreads / UPH;
     const RopeArgs& a = p.a;
     const int u = threadIdx.x % UPH;
     const int64_t t = blockIdx.x;
     const int n_kv = a.cache.n_kv;
     const int heads = a.n_q + 2 * n_kv;
+    const int per_pass = blockDim.x / UPH, step = gridDim.y * per_pass;
 
     grid_launch_dependents();
     grid_dependency_wait();
 
-    // this unit's elements and whether they turn
+    // this unit's elements, and whether they turn
     const bool turns = 16 * u < a.rot;
     const int first = turns && !a.interleaved ? 8 * u : 16 * u;
     const int second = turns && !a.interleaved ? 8 * u + a.rot / 2 : 16 * u + 8;
+
+    uint4 raw[kRopeAhead][2];
+    const auto load = [&](int h, uint4 (&to)[2]) {
+        if (h >= heads) return;
+        const bool is_v = h >= a.n_q + n_kv;
+        const uint16_t* src = h < a.n_q ? a.q + t * a.q_stride + static_cast<int64_t>(h) * kDim
+                              : is_v    ? a.v + t * a.v_stride + static_cast<int64_t>(h - a.n_q - n_kv) * kDim
+                                        : a.k + t * a.k_stride + static_cast<int64_t>(h - a.n_q) * kDim;
+        to[0] = *reinterpret_cast<const uint4*>(src + (is_v ? 16 * u : first));
+        to[1] = *reinterpret_cast<const uint4*>(src + (is_v ? 16 * u + 8 : second));
+    };
+    const int head0 = blockIdx.y * per_pass + threadIdx.x / UPH;
+#pragma unroll
+    for (int i = 0; i < kRopeAhead; ++i) load(head0 + i * step, raw[i]);
+
     float c[8], s[8];
     if (turns) {
         const int pair0 = 8 * u;
+        int64_t pos[kMaxAxes];
+#pragma unroll
+        for (int x = 0; x < kMaxAxes; ++x) {
+            pos[x] = x < a.n_axes ? a.pos[t * a.n_axes + x] : 0;
+            if (pos[x] < 0 || pos[x] >= a.n_pos) {
+                raise_error(a.err, kErrBadIndex);
+                pos[x] = 0;
+            }
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            int64_t pos = a.pos[t * a.n_axes + a.axis_of_pair[pair0 + i]];
-            if (pos < 0 || pos >= a.n_pos) {
-                raise_error(a.err, kErrBadIndex);
-                pos = 0;
-            }
-            const float2 cs = __ldg(reinterpret_cast<const float2*>(a.tab) + pos * (a.rot / 2) + pair0 + i);
+            const int x = a.axis_of_pair[pair0 + i];
+            const int64_t at = x == 0 ? pos[0] : x == 1 ? pos[1] : x == 2 ? pos[2] : pos[3];
+            const float2 cs = *(reinterpret_cast<const float2*>(a.tab) + at * (a.rot / 2) + pair0 + i);
             c[i] = cs.x;
             s[i] = cs.y;
         }
     }
     const int64_t slots = a.cache.n_pages * a.cache.page;
-    int64_t slot = a.slot ? a.slot[t] : -1;
+    int64_t slot = a.slot[t];
     if (slot < -1 || slot >= slots) {
         if (threadIdx.x == 0) raise_error(a.err, kErrBadIndex);
         slot = -1;
     }
     const int64_t page = slot >> a.cache.page_shift, place = slot & (a.cache.page - 1);
 
-    // every lane of a head's group takes the same way, and all lanes of a
-    // warp run the same number of passes (the reductions use the full warp)
-    for (int h0 = blockIdx.y * kHeadsPerPass; h0 < heads; h0 += gridDim.y * kHeadsPerPass) {
-        const int h = h0 + threadIdx.x / UPH;
+    // all lanes of a warp run the same number of passes (the reductions use the full warp)
+    const auto work = [&](int h, const uint4 (&from)[2]) {
         const bool live = h < heads;
         const bool is_q = h < a.n_q, is_v = h >= a.n_q + n_kv;
+        const int e0 = is_v ? 16 * u : first, e1 = is_v ? 16 * u + 8 : second;
         float x[16];
-        if (live) {
-            const uint16_t* src = is_q ? a.q + t * a.q_stride + static_cast<int64_t>(h) * kDim
-                                 : is_v ? a.v + t * a.v_stride + static_cast<int64_t>(h - a.n_q - n_kv) * kDim
-                                        : a.k + t * a.k_stride + static_cast<int64_t>(h - a.n_q) * kDim;
-            const int e0 = is_v ? 16 * u : first, e1 = is_v ? 16 * u + 8 : second;
-            unpack8(*reinterpret_cast<const uint4*>(src + e0), x);
-            unpack8(*reinterpret_cast<const uint4*>(src + e1), x + 8);
-            if (turns && !is_v) {
-                if (a.interleaved) {
+        unpack8(from[0], x);
+        unpack8(from[1], x + 8);
+        if (turns && !is_v) {
+            if (a.interleaved) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float p0 = x[2 * i], p1 = x[2 * i + 1];
-                        x[2 * i] = __fsub_rn(__fmul_rn(p0, c[i]), __fmul_rn(p1, s[i]));
-                        x[2 * i + 1] = __fadd_rn(__fmul_rn(p1, c[i]), __fmul_rn(p0, s[i]));
-                    }
-                } else {
+                for (int i = 0; i < 8; ++i) {
+                    const float p0 = x[2 * i], p1 = x[2 * i + 1];
+                    x[2 * i] = __fsub_rn(__fmul_rn(p0, c[i]), __fmul_rn(p1, s[i]));
+                    x[2 * i + 1] = __fadd_rn(__fmul_rn(p1, c[i]), __fmul_rn(p0, s[i]));
+                }
+            } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float p0 = x[i], p1 = x[8 + i];
-                        x[i] = __fsub_rn(__fmul_rn(p0, c[i]), __fmul_rn(p1, s[i]));
-                        x[8 + i] = __fadd_rn(__fmul_rn(p1, c[i]), __fmul_rn(p0, s[i]));
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    const float p0 = x[i], p1 = x[8 + i];
+                    x[i] = __fsub_rn(__fmul_rn(p0, c[i]), __fmul_rn(p1, s[i]));
+                    x[8 + i] = __fadd_rn(__fmul_rn(p1, c[i]), __fmul_rn(p0, s[i]));
                 }
             }
-            if (is_q) {
-                uint16_t* dst = a.q_out + t * a.q_out_stride + static_cast<int64_t>(h) * kDim;
-                *reinterpret_cast<uint4*>(dst + e0) = pack8(x);
-                *reinterpret_cast<uint4*>(dst + e1) = pack8(x + 8);
-            }
+        }
+        if (live && is_q) {
+            uint16_t* dst = a.q_out + t * a.q_out_stride + static_cast<int64_t>(h) * kDim;
+            *reinterpret_cast<uint4*>(dst + e0) = pack8(x);
+            *reinterpret_cast<uint4*>(dst + e1) = pack8(x + 8);
         }
         if constexpr (INT8) {
+            if (__all_sync(0xffffffffu, !live || is_q)) return;
             float amax = 0.0f;
             if (live && !is_q) {
 #pragma unroll
@@ -157,24 +179,30 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
                 const int64_t vec = ((page * n_kv + hk) << a.cache.page_shift) + place;
                 if (bd_in(kBkRope, vec, slots * n_kv)) {
                     uint8_t* dst = static_cast<uint8_t*>(is_v ? a.cache.v : a.cache.k) + vec * kDim;
-                    const int e0 = is_v ? 16 * u : first, e1 = is_v ? 16 * u + 8 : second;
                     *reinterpret_cast<uint2*>(dst + e0) = codes8(x, scale);
                     *reinterpret_cast<uint2*>(dst + e1) = codes8(x + 8, scale);
                     if (u == 0) (is_v ? a.cache.v_scale : a.cache.k_scale)[vec] = scale;
                 }
             }
-        } else {
-            if (live && !is_q && slot >= 0) {
-                const int hk = is_v ? h - a.n_q - n_kv : h - a.n_q;
-                const int64_t vec = ((page * n_kv + hk) << a.cache.page_shift) + place;
-                if (bd_in(kBkRope, vec, slots * n_kv)) {
-                    uint16_t* dst = static_cast<uint16_t*>(is_v ? a.cache.v : a.cache.k) + vec * kDim;
-                    const int e0 = is_v ? 16 * u : first, e1 = is_v ? 16 * u + 8 : second;
-                    *reinterpret_cast<uint4*>(dst + e0) = pack8(x);
-                    *reinterpret_cast<uint4*>(dst + e1) = pack8(x + 8);
-                }
+        } else if (live && !is_q && slot >= 0) {
+            const int hk = is_v ? h - a.n_q - n_kv : h - a.n_q;
+            const int64_t vec = ((page * n_kv + hk) << a.cache.page_shift) + place;
+            if (bd_in(kBkRope, vec, slots * n_kv)) {
+                uint16_t* dst = static_cast<uint16_t*>(is_v ? a.cache.v : a.cache.k) + vec * kDim;
+                *reinterpret_cast<uint4*>(dst + e0) = pack8(x);
+                *reinterpret_cast<uint4*>(dst + e1) = pack8(x + 8);
             }
         }
+    };
+    for (int h0 = blockIdx.y * per_pass; h0 < heads; h0 += kRopeAhead * step) {
+        const int h = h0 + threadIdx.x / UPH;
+        if (h0 != static_cast<int>(blockIdx.y) * per_pass) {
+#pragma unroll
+            for (int i = 0; i < kRopeAhead; ++i) load(h + i * step, raw[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kRopeAhead; ++i)
+            if (h0 + i * step < heads) work(h + i * step, raw[i]);
     }
 }
 
@@ -269,22 +297,24 @@ cudaError_t launch_rope_append(const RopeArgs& a, int sm_count, cudaStream_t str
 {
     if (a.T == 0) return cudaSuccess;
     RopeParams p{a};
-    const int per_pass = kRopeThreads / (a.cache.dim / kUnit);
-    const int heads = a.n_q + 2 * a.cache.n_kv;
-    const int passes = (heads + per_pass - 1) / per_pass;
-    // few tokens: the heads of a token are split over blocks until the GPU
-    // has about 8 blocks per SM
+    // as few passes as 64 threads allow, all about equally full
+    const int uph = a.cache.dim / kUnit, heads = a.n_q + 2 * a.cache.n_kv;
+    const int most = kRopeThreads / uph;
+    const int passes = (heads + most - 1) / most, per_pass = (heads + passes - 1) / passes;
+    const int threads = (per_pass * uph + 31) / 32 * 32;
+    // few tokens: the passes of a token are split over blocks until the GPU has about 8 blocks per SM
+    const int real = (heads + threads / uph - 1) / (threads / uph);
     int64_t split = (8ll * sm_count + a.T - 1) / a.T;
-    if (split > passes) split = passes;
+    if (split > real) split = real;
     if (split < 1) split = 1;
     const dim3 grid(static_cast<unsigned>(a.T), static_cast<unsigned>(split));
     cudaError_t err = cudaSuccess;
     if (a.cache.dim == 128)
         launch_dep(err, a.cache.int8 ? rope_append_kernel<8, true> : rope_append_kernel<8, false>, grid,
-                   dim3(kRopeThreads), 0, stream, p);
+                   dim3(threads), 0, stream, p);
     else
         launch_dep(err, a.cache.int8 ? rope_append_kernel<4, true> : rope_append_kernel<4, false>, grid,
-                   dim3(kRopeThreads), 0, stream, p);
+                   dim3(threads), 0, stream, p);
     return err;
 }
 
