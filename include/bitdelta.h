@@ -302,7 +302,8 @@ bd_status bd_compress_noalloc(const uint16_t* w_base, const uint16_t* w_ft, int6
  *   out           device [T][d]: bf16, fp32 or (BD_OUT_E4M3) 8-bit codes with
  *                 scale[t] = max(max_j |y[t][j]|, 1e-30) / 448, code =
  *                 RN_e4m3(y * (448 / max)); a row that is not finite has a
- *                 scale that is not finite
+ *                 scale that is not finite.  The maximum is that of |h * gain|
+ *                 times the row's factor: |y|'s up to fp32 rounding
  *   scale         device fp32 [T], 4-byte aligned, written for BD_OUT_E4M3 (NULL otherwise)
  * d: a positive multiple of 8 (BD_ERR_UNSUPPORTED_SHAPE); matrices and gains
  * 16-byte aligned; out may not overlap an input.  0 <= V <= BD_MAX_VARIANTS.
@@ -417,10 +418,14 @@ bd_status bd_kv_read(const bd_kv_pages* cache, const int32_t* page_table, int64_
  *   kv_len   device int32 [n_seq]
  *   out      device bf16 [T][n_q][head_dim], 16-byte aligned
  *   lse      device fp32 [T][n_q] or NULL: log sum_j exp(scale * q . k_j)
- * n_q: a positive multiple of n_kv.  The int8 codes enter the tensor cores
- * as exact bf16 values and their scales multiply the fp32 scores and
- * probabilities.  Scores, the softmax and all sums are fp32; probabilities
- * are rounded to bf16 before their product with V.  Results do not depend on
+ * n_q: a positive multiple of n_kv.  Scores, the softmax and all sums are
+ * fp32.  In a bf16 cache probabilities are rounded to bf16 before their
+ * product with V.  Int8 codes enter the tensor cores exactly (in fp16 with q,
+ * whose rows are scaled by a power of two so that bf16's 8 bits fit) and
+ * their scales multiply the fp32 scores and probabilities; probability times
+ * v_scale is then rounded once, to fp16 when max_new * (n_q / n_kv) <= 16 and
+ * to bf16 above.  Cached values up to 2^80 in magnitude give the formula's
+ * result; beyond that a product may overflow.  Results do not depend on
  * timing (no atomics).  A page outside [0, n_pages), a length outside
  * [0, max_pages * page_size] or offsets out of order set BD_ERR_BAD_INDEX:
  * the value is clamped and the sequence's result is undefined.
