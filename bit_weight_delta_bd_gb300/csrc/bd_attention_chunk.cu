@@ -363,6 +363,11 @@ __device__ __forceinline__ const uint4* q_row(const AttnParams& p, const Segment
                                           static_cast<int64_t>(s.h * p.G + (abs_row - tok * p.G)) * DIM);
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p)
+{
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 __device__ __forceinline__ float abs_max8(float big, uint4 v)
 {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -378,42 +383,60 @@ __device__ __forceinline__ float unit_of(float x)
     return __uint_as_float(__float_as_uint(fminf(fmaxf(x, 7.9e-31f), 1.2e30f)) & 0x7F800000u);
 }
 
-// Row r of a segment's query tile i, in shared memory (K-major, 128-byte
-// swizzle, halves of 64 dims); rows past the item are zeros.  A negative scale
-// is taken into Q's sign; int8: fp16, over the row's power of two, dims in the
-// codes' order.  Returns what the row's products are to be multiplied by.
+// A warp's 32 rows, from row r0 on, of a segment's query tile i, into shared
+// memory (K-major, 128-byte swizzle, halves of 64 dims); rows past the item
+// are zeros.  Neighbouring lanes take neighbouring 16 bytes, eight loads in
+// flight (a row per lane, two in flight, cost 6 us per item, and twice that
+// where int8 looked for the maximum first).  A negative scale is taken into
+// Q's sign; int8: fp16, over the row's power of two, dims in the codes' order.
+// Returns what the products of row r0 + lane are to be multiplied by.
 template <int DIM, bool INT8>
-__device__ __forceinline__ float load_q(const AttnParams& p, const Segment& s, int i, int r, uint8_t* dst)
+__device__ __forceinline__ float load_q(const AttnParams& p, const Segment& s, int i, int r0, int lane, uint8_t* dst)
 {
-    const uint4* src = q_row<DIM>(p, s, i * kQRows + r);
+    constexpr int kLanes = DIM / 8, kRowsAtOnce = 32 / kLanes, kBatch = 8;
+    const uint64_t own = reinterpret_cast<uint64_t>(q_row<DIM>(p, s, i * kQRows + r0 + lane));
     const uint32_t flip = p.a.scale < 0.0f ? 0x80008000u : 0u;
-    float f = 1.0f, back = 1.0f;
-    if constexpr (INT8) {
-        float big = 0.0f;
-#pragma unroll 2
-        for (int c = 0; c < (src ? DIM / 8 : 0); ++c) big = abs_max8(big, src[c]);
-        f = 16384.0f / unit_of(big);
-        back = unit_of(big) / 16384.0f;
-    }
-#pragma unroll 2
-    for (int c = 0; c < DIM / 8; ++c) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (src) v = src[c];
-        v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-        if constexpr (INT8) {
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint32_t o[4];
+    const int c = lane & (kLanes - 1), sub = lane / kLanes;
+    float back = 1.0f;
+#pragma unroll 1
+    for (int g = 0; g < 32; g += kBatch * kRowsAtOnce) {
+        uint4 v[kBatch];
 #pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-                const float x0 = __uint_as_float(w[e] << 16) * f, x1 = __uint_as_float(w[e] & 0xFFFF0000u) * f;
-                const float x2 = __uint_as_float(w[e + 1] << 16) * f, x3 = __uint_as_float(w[e + 1] & 0xFFFF0000u) * f;
-                const __half2 even = __floats2half2_rn(x0, x2), odd = __floats2half2_rn(x1, x3);
-                o[e] = *reinterpret_cast<const uint32_t*>(&even);
-                o[e + 1] = *reinterpret_cast<const uint32_t*>(&odd);
-            }
-            v = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int k = 0; k < kBatch; ++k) {
+            const uint64_t at = __shfl_sync(0xffffffffu, own, g + k * kRowsAtOnce + sub);
+            v[k] = make_uint4(0, 0, 0, 0);
+            if (at) v[k] = __ldg(reinterpret_cast<const uint4*>(at) + c);
         }
-        *reinterpret_cast<uint4*>(dst + (c >> 3) * (kQRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int r = r0 + g + k * kRowsAtOnce + sub;
+            uint4 x = v[k];
+            x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
+            if constexpr (INT8) {
+                float big = abs_max8(0.0f, x);
+#pragma unroll
+                for (int o = 1; o < kLanes; o *= 2) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+                const float unit = unit_of(big), f = 16384.0f / unit;
+#pragma unroll
+                for (int e = 0; e < kRowsAtOnce; ++e) {
+                    const float of = __shfl_sync(0xffffffffu, unit, e * kLanes);
+                    if (lane == g + k * kRowsAtOnce + e) back = of / 16384.0f;
+                }
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                uint32_t o[4];
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    const float x0 = __uint_as_float(w[e] << 16) * f, x1 = __uint_as_float(w[e] & 0xFFFF0000u) * f;
+                    const float x2 = __uint_as_float(w[e + 1] << 16) * f;
+                    const float x3 = __uint_as_float(w[e + 1] & 0xFFFF0000u) * f;
+                    const __half2 even = __floats2half2_rn(x0, x2), odd = __floats2half2_rn(x1, x3);
+                    o[e] = *reinterpret_cast<const uint32_t*>(&even);
+                    o[e + 1] = *reinterpret_cast<const uint32_t*>(&odd);
+                }
+                x = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            *reinterpret_cast<uint4*>(dst + (c >> 3) * (kQRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x;
+        }
     }
     return back;
 }
@@ -512,7 +535,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
             const bool have = walk.next(s);
             const bool runs = have && i < s.q_tiles;
             if (runs) {
-                unit = load_q<DIM, INT8>(p, s, i, r, q_smem);
+                unit = load_q<DIM, INT8>(p, s, i, r - lane, lane, q_smem);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.q_full[i]);
@@ -719,6 +742,14 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
             uint32_t phase = 0, sc_phase = 0;
             bool ok = true;
             while (ok && walk.next(s)) {
+                // the segment's Q on its way to the L2 cache while the tiles before it are worked on
+#pragma unroll 1
+                for (int r = lane; r < kChunkRows; r += 32)
+                    if (const uint4* q = q_row<DIM>(p, s, r)) {
+                        prefetch_l2(q);
+                        if constexpr (DIM == 128) prefetch_l2(q + 8);
+                    }
+                __syncwarp();
                 const int32_t* table = a.table + static_cast<int64_t>(s.it.seq) * a.max_pages;
                 const int pages = (s.sq.len + cache.page - 1) >> cache.page_shift;
                 for (int t = s.t0; t < s.t1 && ok; ++t) {
