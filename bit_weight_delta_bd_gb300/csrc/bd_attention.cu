@@ -17,6 +17,10 @@
 // ldmatrix, V by its transposing form, and P by movmatrix, which turns an 8 x 8
 // block of the first product's result into the second's operand.
 //
+// Short or few caches take no deal: a cluster of blocks has a (sequence, head)
+// to itself, each a share of its keys, and the blocks send one another the
+// parts of the rows that each joins, through distributed shared memory.
+//
 // Int8.  Both products run in fp16, which holds the codes exactly: with u =
 // code + 128 the bits 0x6400 | u are 1024 + u, and one logic operation and
 // one packed addition give two codes (bf16, whose 8 bits have no room for u,
@@ -152,13 +156,16 @@ struct MmaShape {
     static constexpr int kTileBytes = kMmaTile * kRowBytes;               // K (or V) of a stage
     static constexpr int kStageBytes = 2 * kTileBytes + (INT8 ? 1024 : 0);  // stages stay 1024-byte aligned
     static constexpr int kBufBytes = 2 * kRows * DIM * 4;              // sums of an item, two warps each
+    // what a block of a cluster gets of its rows from the others, for two items in turn
+    static constexpr int kRecvBytes = 2 * kRows * (DIM + 4) * 4;
 };
 
-struct MmaShared {
+struct alignas(16) MmaShared {
     uint64_t full[kMmaMaxStages];
     uint64_t empty[kMmaMaxStages];
     float m[kMmaConsumers][kMmaMaxRows];
     float l[kMmaConsumers][kMmaMaxRows];
+    uint64_t joined;    // the cluster's blocks have sent their parts of this block's rows
     volatile int abort;
     int64_t scan[kMmaThreads / 32];
     int seq, row0;      // the block's first item,
@@ -231,26 +238,31 @@ struct MmaWalk {
     }
 };
 
-// The segments of a block that has a (sequence, head) to itself: its items in
-// order (one, in a decode step), with all their tiles.
+// The segments of a block of a cluster that has a (sequence, head) to itself:
+// its items in order (one, in a decode step), with this block's share of their
+// tiles, which may be none.
 struct WholeWalk {
     const AttnParams& p;
     MmaSegment s;
+    int rank;  // of the block in its cluster
 
     __device__ __forceinline__ explicit WholeWalk(const AttnParams& pp) : p(pp)
     {
-        s.seq = static_cast<int>(blockIdx.x) / p.a.cache.n_kv;
-        s.h = static_cast<int>(blockIdx.x) - s.seq * p.a.cache.n_kv;
-        s.sq = attn_seq(p.a, s.seq, s.h == 0);
+        const int pair = static_cast<int>(blockIdx.x) / p.whole;
+        rank = static_cast<int>(blockIdx.x) - pair * p.whole;
+        s.seq = pair / p.a.cache.n_kv;
+        s.h = pair - s.seq * p.a.cache.n_kv;
+        s.sq = attn_seq(p.a, s.seq, s.h == 0 && rank == 0);
         s.rows = s.sq.n_new * p.G;
         s.row0 = -p.mb;
-        s.t0 = 0;
     }
     __device__ __forceinline__ bool next()
     {
         s.row0 += p.mb;
         if (s.row0 >= s.rows) return false;
-        s.tiles = s.t1 = mma_tiles(p, s.sq, s.row0);
+        s.tiles = mma_tiles(p, s.sq, s.row0);
+        s.t0 = static_cast<int>(static_cast<int64_t>(s.tiles) * rank / p.whole);
+        s.t1 = static_cast<int>(static_cast<int64_t>(s.tiles) * (rank + 1) / p.whole);
         return true;
     }
 };
@@ -344,6 +356,25 @@ __device__ __forceinline__ bool attn_wait(volatile int* abort_flag, uint64_t* ba
         }
     }
     return true;
+}
+
+// A wait for the other blocks of the cluster; false once given up.
+__device__ __forceinline__ bool mbar_wait_cluster_bounded(uint64_t* bar, uint32_t parity, uint32_t* err)
+{
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait_cluster(bar, parity))
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            raise_error(err, kErrTimeout);
+            return false;
+        }
+    return true;
+}
+
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, float4 v)
+{
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
 }
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar)
@@ -472,6 +503,13 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
     uint8_t* ring = dyn_raw;
     float* buf = reinterpret_cast<float*>(ring + static_cast<size_t>(mp.stages) * S::kStageBytes);
     MmaShared& sh = *reinterpret_cast<MmaShared*>(reinterpret_cast<uint8_t*>(buf) + S::kBufBytes);
+    // a cluster's parts: row k of those that this block joins, from rank w, for the item's parity; a
+    // block sends an item's parts only after it has all of the one before, so two places suffice
+    constexpr int kRecvStride = DIM + 4;  // the sum, its maximum and denominator
+    [[maybe_unused]] float* recv = reinterpret_cast<float*>(&sh + 1);
+    [[maybe_unused]] const auto recv_row = [&](uint32_t item, int w, int k) {
+        return static_cast<int>(item & 1) * S::kRows + w * (S::kRows / mp.p.whole) + k;
+    };
 
     const AttnParams& p = mp.p;
     const AttentionArgs& a = p.a;
@@ -486,15 +524,19 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
             mbar_init(&sh.full[s], 1);
             mbar_init(&sh.empty[s], kMmaConsumers);
         }
+        mbar_init(&sh.joined, WHOLE ? p.whole : 1);
         sh.abort = 0;
         fence_mbarrier_init();
     }
-    __syncthreads();
+    if (WHOLE && p.whole > 1) cluster_sync_all();  // the others' barriers are there before anything is sent
+    else __syncthreads();
     grid_dependency_wait();
 
     const int n_kv = cache.n_kv;
     auto walk = mma_walk<WHOLE>(p, sh);
     const MmaSegment& sg = walk.s;
+    int walk_rank = 0;
+    if constexpr (WHOLE) walk_rank = walk.rank;
     int stage = 0;
     uint32_t phase = 0;
 
@@ -570,6 +612,8 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
     // ---------------------------------------------------------------- consumer warps
     const int g = lane >> 2, q4 = lane & 3;
     const float c2 = a.scale * kLog2e;
+    [[maybe_unused]] uint32_t item = 0;  // of a cluster, so far
+    [[maybe_unused]] bool gave_up = false;
     int turn = 0;  // stages so far: this warp takes those of its parity
     while (walk.next()) {
         const AttnSeq sq = sg.sq;
@@ -925,6 +969,16 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
             consumers_sync();
         }
 
+        const auto write_row = [&](int r, int d, float4 v, float mm, float ll) {
+            const int row = row0 + r, tok = row / p.G;
+            const int64_t at = (static_cast<int64_t>(sq.q0) + tok) * a.n_q + h * p.G + (row - tok * p.G);
+            const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+            if (bd_in(kBkAttn, at, a.T * a.n_q)) {
+                *reinterpret_cast<uint2*>(a.out + at * DIM + d) =
+                    make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+                if (d == 0 && a.lse) a.lse[at] = attn_lse(mm, ll);
+            }
+        };
         const bool whole = t0 == 0 && t1 == sg.tiles;
         const int slot = attn_slot(blockIdx.x, t0 == 0);
         const int live_rows = rows - row0 < S::kRows ? rows - row0 : S::kRows;
@@ -943,15 +997,14 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
             float4 v = *reinterpret_cast<const float4*>(buf + place);
             const float4 v1 = *reinterpret_cast<const float4*>(buf + S::kRows * DIM + place);
             v = make_float4(v.x + v1.x, v.y + v1.y, v.z + v1.z, v.w + v1.w);
-            if (whole) {
-                const int row = row0 + r, tok = row / p.G;
-                const int64_t at = (static_cast<int64_t>(sq.q0) + tok) * a.n_q + h * p.G + (row - tok * p.G);
-                const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-                if (bd_in(kBkAttn, at, a.T * a.n_q)) {
-                    *reinterpret_cast<uint2*>(a.out + at * DIM + d) =
-                        make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
-                    if (d == 0 && a.lse) a.lse[at] = attn_lse(mm, ll);
-                }
+            if (WHOLE && p.whole > 1) {
+                // to the block of the cluster that joins this row: rank r mod the cluster's size
+                const int place_there = recv_row(item, walk_rank, r / p.whole);
+                const uint32_t there = cluster_address(recv + place_there * kRecvStride, r % p.whole);
+                st_cluster_v4(there + 4 * d, v);
+                if (d == 0) st_cluster_v4(there + 4 * DIM, make_float4(mm, ll, 0.0f, 0.0f));
+            } else if (whole) {
+                write_row(r, d, v, mm, ll);
             } else {
                 const int64_t at = static_cast<int64_t>(slot) * S::kRows + r;
                 if (bd_in(kBkAttn, at, 2ll * p.blocks * S::kRows)) {
@@ -961,7 +1014,35 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
             }
         }
         consumers_sync();  // the buffers are free for the next item
+        if constexpr (WHOLE) {
+            if (p.whole > 1) {
+                if (static_cast<int>(threadIdx.x) < p.whole) mbar_arrive_remote_release(&sh.joined, threadIdx.x);
+                // (given up, which is reported: what is there is joined)
+                if (!mbar_wait_cluster_bounded(&sh.joined, item & 1, a.err)) gave_up = true;
+                for (int i = threadIdx.x; i < S::kRows / p.whole * (DIM / 4); i += 32 * kMmaConsumers) {
+                    const int k = i / (DIM / 4), d = 4 * (i % (DIM / 4)), r = k * p.whole + walk_rank;
+                    if (r >= live_rows) break;
+                    float mm = -INFINITY, ll = 0.0f;
+                    for (int w = 0; w < p.whole; ++w) mm = fmaxf(mm, recv[recv_row(item, w, k) * kRecvStride + DIM]);
+                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    for (int w = 0; w < p.whole; ++w) {
+                        const float* part = recv + recv_row(item, w, k) * kRecvStride;
+                        const float lw = part[DIM + 1], f = attn_weight(part[DIM], lw, mm);
+                        if (f == 0.0f) continue;
+                        const float4 x = *reinterpret_cast<const float4*>(part + d);
+                        ll += lw * f;
+                        v = make_float4(v.x + x.x * f, v.y + x.y * f, v.z + x.z * f, v.w + x.w * f);
+                    }
+                    write_row(r, d, v, mm, ll);
+                }
+                ++item;
+            }
+        }
     }
+    // a block leaves when it has all that is sent to it, or else with the rest of its cluster: nothing
+    // is sent to one that has left (the barrier does not wait for threads that have)
+    if constexpr (WHOLE)
+        if (gave_up) asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // ------------------------------------------------------------------------------- join
@@ -1059,15 +1140,15 @@ cudaError_t launch_mma_shape(const AttnParams& p, cudaStream_t stream)
     }
     // the SM's shared memory shared by the blocks that it holds; all of it
     // where there are no more blocks than SMs
-    constexpr size_t kRest = S::kBufBytes + sizeof(MmaShared);
+    const size_t rest = S::kBufBytes + sizeof(MmaShared) + (p.whole > 1 ? S::kRecvBytes : 0);
     const size_t budget = p.blocks <= p.a.sm_count ? 227u * 1024u
                                                    : 228u * 1024u / mma_blocks_per_sm(8 * NT, DIM, INT8) - 1024u;
-    mp.stages = static_cast<int>((budget - kRest) / S::kStageBytes);
+    mp.stages = static_cast<int>((budget - rest) / S::kStageBytes);
     if (mp.stages > kMmaMaxStages) mp.stages = kMmaMaxStages;
-    const size_t smem = static_cast<size_t>(mp.stages) * S::kStageBytes + kRest;
+    const size_t smem = static_cast<size_t>(mp.stages) * S::kStageBytes + rest;
     const auto kernel = attn_mma_kernel<DIM, INT8, NT, WHOLE>;
     cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem, smem_set);
-    launch_dep(err, kernel, dim3(p.blocks), dim3(kMmaThreads), smem, stream, mp);
+    launch_dep_clusters(err, kernel, dim3(p.blocks), dim3(kMmaThreads), WHOLE ? p.whole : 1, smem, stream, mp);
     return err;
 }
 
@@ -1133,15 +1214,27 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream)
     const int most = chunk ? kAttnMaxChunkBlocks : kAttnMaxBlocks;
     p.blocks = chunk ? a.sm_count : mma_blocks_per_sm(p.mb, a.cache.dim, a.cache.int8) * a.sm_count;
     if (p.blocks > most) p.blocks = most;
-    // Short caches, as far as the page table's width says: a block for each
-    // (sequence, head), which needs no deal and nothing to join.  It takes
-    // 4.6 us at 100 keys and 1.15 us more for each 128, the split 8.5 us and
-    // little more for a few heads (64/8 heads, bf16, pages of 16: 8.2 against
-    // 9.0 us for one sequence at 511 keys, 12.8 against 9.8 at 1023), but
-    // 22.3 us against 14.9 for 16 sequences of 1023.
+    // Short caches, or few: a cluster of up to 8 blocks for each (sequence,
+    // head), which needs no deal and no second launch.  (cap is the longest
+    // cache as far as the page table's width says; 64/8 heads, bf16, pages of
+    // 16, us on the GPU, the deal and its join against clusters:
+    //   1 sequence    511 keys 8.7 / 6.7   2047 11.5 / 8.4   4000 13.0 / 10.7
+    //   4             511      8.9 / 7.0   2047 15.6 / 10.6  4000 21.7 / 16.6
+    //   16                                 1500 26.8 / 20.8  2047 31.7 / 25.5
+    // and 27.9 / 22.8 for 16 whose lengths lie below 2047 at random.)  A
+    // cluster is doubled while its blocks have more than 128 keys each and an
+    // SM to themselves, or more than 256 and half an SM: 16 sequences of 1023
+    // int8 keys take 20.0 with one block each and 17.0 with two, of 200 keys 8.0
+    // and 8.7.  Blocks of more than 1024 keys are too uneven for what they
+    // save; a block alone wins up to 512, or 1024 where there are many.
     const int64_t cap = a.max_pages * a.cache.page, pairs = a.n_seq * a.cache.n_kv;
-    p.whole = !chunk && (cap <= 512 || (cap <= 1024 && pairs >= 64)) && pairs <= INT32_MAX;
-    if (p.whole) p.blocks = static_cast<int>(pairs);
+    if (!chunk) {
+        int c = 1;
+        while (c < 8 && pairs * 2 * c <= 2 * a.sm_count && cap > (pairs * 2 * c <= a.sm_count ? 128 : 256) * c) c *= 2;
+        const int64_t most_keys = c > 1 || pairs >= 64 ? 1024 : 512;
+        if (cap <= most_keys * c && pairs * c <= INT32_MAX) p.whole = c;
+    }
+    if (p.whole) p.blocks = static_cast<int>(pairs) * p.whole;
     const AttnWs w = attn_layout(a.T, a.n_seq, p.G, a.cache.dim, p.mb, most);
     char* ws = static_cast<char*>(a.ws);
     p.head = reinterpret_cast<AttnHeader*>(ws + w.head);

@@ -16,6 +16,8 @@
 // block of such an (item, head) notes it down, and the join adds its parts in
 // block order, so results do not depend on timing.
 //
+// (The decode kernel does without where caches are short or few.)
+//
 // Finding its units.  The decode kernel's blocks work the deal out from the
 // lengths by themselves (one load per sequence and a scan: no launch before
 // theirs, which is what a small call's time would go into); for chunks, whose
@@ -55,7 +57,7 @@ struct AttnParams {
     int G;                // query heads of a kv head
     int tile, mb;         // keys per tile, rows per item
     int blocks;           // N
-    int whole;            // a block for each (sequence, head), and nothing to join (decode kernel)
+    int whole;            // a cluster of so many blocks for each (sequence, head), and no deal (decode kernel); or 0
     AttnHeader* head;
     AttnItem* items;
     int32_t* item_off;    // [n_seq + 1] first item of a sequence

@@ -222,6 +222,26 @@ __device__ __forceinline__ void mbar_arrive_remote(uint64_t* bar, uint32_t cta)
         : "memory");
 }
 
+// The same with release at cluster scope: the other CTA sees what this thread
+// has written, or seen written, before.
+__device__ __forceinline__ void mbar_arrive_remote_release(uint64_t* bar, uint32_t cta)
+{
+    asm volatile(
+        "{\n\t.reg .b32 ra;\n\t"
+        "mapa.shared::cluster.u32 ra, %0, %1;\n\t"
+        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [ra];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(cta)
+        : "memory");
+}
+
+// The address of `p`, in this CTA's shared memory, in that of the cluster's CTA of rank `cta`.
+__device__ __forceinline__ uint32_t cluster_address(const void* p, uint32_t cta)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(cta));
+    return r;
+}
+
 // try_wait with acquire at cluster scope: pairs with arrivals made by other
 // CTAs of the cluster (mbar_arrive_remote).
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity)

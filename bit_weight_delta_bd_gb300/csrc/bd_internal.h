@@ -23,8 +23,8 @@ constexpr int kMaxVariants = 64;
 // kernel of a chain.  The first error is kept in err and no later kernel is
 // launched.
 template <typename... KArgs, typename... Args>
-void launch_dep(cudaError_t& err, void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                Args&&... args)
+void launch_dep_clusters(cudaError_t& err, void (*kern)(KArgs...), dim3 grid, dim3 block, int cluster, size_t smem,
+                         cudaStream_t st, Args&&... args)
 {
     if (err != cudaSuccess) return;
     cudaLaunchConfig_t cfg{};
@@ -32,12 +32,23 @@ void launch_dep(cudaError_t& err, void (*kern)(KArgs...), dim3 grid, dim3 block,
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     err = cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+template <typename... KArgs, typename... Args>
+void launch_dep(cudaError_t& err, void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                Args&&... args)
+{
+    launch_dep_clusters(err, kern, grid, block, 1, smem, st, std::forward<Args>(args)...);
 }
 
 

@@ -13,6 +13,7 @@ import pytest
 import torch
 
 import layer_oracle as ref
+import test_layer_ops as ops
 from bit_weight_delta_bd_gb300 import bitdelta as bd
 
 pytestmark = pytest.mark.gpu
@@ -93,6 +94,23 @@ def test_cache_past_32_bits(dev, int8):
     if not int8:  # (an int8 cache's values are read back rounded, which attention does not do)
         bound = ref.attention_bounds(*want, max(lens))[0]
         assert bool(((runs[0][3].double().cpu() - want[0]).abs() <= bound).all())
+
+
+# ------------------------------------------------------------------------------- clusters, and the deal
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("n_new,kv_len,n_q,n_kv,dim,page,max_new", [
+    # clusters with several items each: more rows than max_new lets the host expect
+    ([5, 1, 9], [800, 33, 300], 16, 2, 128, 16, 1), ([3, 0, 40], [2000, 7, 500], 8, 1, 64, 64, 2),
+    # one row a head, 16 rows, rows that see nothing, blocks without a tile of their own
+    ([1], [900], 8, 8, 128, 32, 1), ([16], [1000], 8, 8, 64, 16, 16), ([4, 2], [2, 700], 8, 2, 128, 16, 4),
+    ([1, 1], [1, 1000], 8, 1, 64, 128, 1), ([1] * 19, [1023 - 50 * i for i in range(19)], 8, 8, 64, 16, 1),
+    ([1], [8192], 8, 1, 128, 64, 1), ([2], [4001], 7, 1, 64, 16, 2),
+    # dealt out: caches too long, or too many
+    ([1, 1], [20000, 3000], 8, 1, 128, 128, 1), ([1] * 40, [3000 - 70 * i for i in range(40)], 16, 8, 64, 16, 1),
+    ([2] * 30, [1500 - 51 * i for i in range(30)], 64, 8, 128, 32, 2), ([1], [9000], 12, 1, 64, 16, 1)])
+def test_attention_clusters_and_deal(dev, n_new, kv_len, n_q, n_kv, dim, page, max_new, int8):
+    ops.run_attention(dev, n_new, kv_len, n_q, n_kv, dim, page, int8, seed=sum(kv_len) % 97, max_new=max_new)
 
 
 # ------------------------------------------------------------------------------- one result
