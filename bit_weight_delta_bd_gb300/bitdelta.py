@@ -13,7 +13,9 @@ patterns.
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import operator
 import os
 import threading
 
@@ -170,6 +172,7 @@ def _check(status: int, where: str) -> None:
 
 
 _BF16_LIKE = (torch.bfloat16, torch.uint16, torch.int16)
+_BF16_SET = frozenset(_BF16_LIKE)
 _F32, _I32 = (torch.float32,), (torch.int32,)
 
 
@@ -317,28 +320,33 @@ def bd_rms_norm_workspace_size(T: int, d: int) -> int:
     return int(load().bd_rms_norm_workspace_size(T, d))
 
 
-def _row_ptrs(rows, n: int, name: str, dev: int) -> list[int]:
-    """Pointers of contiguous bf16 tensors of n elements."""
-    ptrs = []
-    for t in rows:
-        if (t.get_device() != dev or t.numel() != n or t.dtype not in _BF16_LIKE or not t.is_contiguous()):
+_dtype_of = operator.attrgetter("dtype")
+
+
+def _row_ptrs(rows, n: int, name: str, dev: int) -> array.array:
+    """Pointers of contiguous bf16 tensors of n elements.  (Checked a property at a time: a loop over 14 gains costs
+    twice the time of the norm's kernel.)"""
+    Tensor = torch.Tensor
+    if not (set(map(Tensor.get_device, rows)) <= {dev} and set(map(Tensor.numel, rows)) <= {n}
+            and set(map(_dtype_of, rows)) <= _BF16_SET and all(map(Tensor.is_contiguous, rows))):
+        for t in rows:
             if t.numel() != n:
                 raise ValueError(f"every {name} must have the shape [{n}]")
             _ptr(t, name, _BF16_LIKE, False, dev)
-        ptrs.append(t.data_ptr())
-    return ptrs
+    return array.array("Q", map(Tensor.data_ptr, rows))
 
 
 def bd_rms_norm(x, gain, eps, out, ws, residual=None, residual_out=None, scale=None, vid=None, gain_list=(),
                 stream=None) -> None:
     """out = norm(x + residual) * gain (the gain of token t's variant, vid[t], out of gain_list); out bf16, fp32, or
     e4m3 with scale [T]; residual_out (which may be residual itself) receives x + residual."""
-    T, d = x.shape
+    shape = x.shape
+    T, d = shape
     dev = _device()
-    if gain.shape != (d,) or out.shape != x.shape:
+    if gain.shape != (d,) or out.shape != shape:
         raise ValueError("gain must have the shape [d] and out that of x")
-    if (residual is not None and residual.shape != x.shape) or (
-            residual_out is not None and residual_out.shape != x.shape):
+    if (residual is not None and residual.shape != shape) or (
+            residual_out is not None and residual_out.shape != shape):
         raise ValueError("the residual's shape differs from x")
     if scale is not None and scale.numel() != T:
         raise ValueError("scale must have one value per row")
@@ -347,7 +355,8 @@ def bd_rms_norm(x, gain, eps, out, ws, residual=None, residual_out=None, scale=N
     tab, V = None, 0
     if vid is not None:
         V = len(gain_list)
-        tab = (ctypes.c_void_p * max(V, 1))(*_row_ptrs(gain_list, d, "gain", dev))
+        table = _row_ptrs(gain_list, d, "gain", dev)
+        tab = table.buffer_info()[0] if V else None
     out_dtype = _OUT_DTYPES.get(out.dtype)
     if out_dtype is None:
         raise ValueError(f"out has dtype {out.dtype}, expected bfloat16, float32 or float8_e4m3fn")
