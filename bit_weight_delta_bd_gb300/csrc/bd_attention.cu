@@ -324,12 +324,12 @@ __device__ __forceinline__ MmaWalk mma_deal(const AttnParams& p, MmaShared& sh)
     MmaWalk walk(p, c < active ? attn_first(units, active, c) : 0, c < active ? attn_first(units, active, c + 1) : 0,
                  sh.seq, sh.row0, sh.before);
     if (threadIdx.x == 0) {
-        AttnJoin j{0, 0, 0, 0};
+        AttnJoin j{};
         if (c < active) {
             const int64_t rel = walk.u - walk.before;
             const int h = attn_div(rel, walk.s.tiles);
             j = attn_join_of(units, active, c, walk.u, walk.before + static_cast<int64_t>(h) * walk.s.tiles,
-                             walk.s.tiles, walk.s.seq, walk.s.row0, h);
+                             walk.s.tiles, walk.s.sq, p.G, walk.s.row0, h);
         }
         p.joins[c] = j;
     }
@@ -1049,10 +1049,15 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
 
 constexpr int kJoinThreads = 128;
 
-// Block (c, y): joins what block c of the main kernel noted down; a warp takes the rows
-// 4 y + w, 4 (y + gridDim.y) + w, ...
-template <int DIM>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnParams p)
+// Block (c, y): joins what block c of the main kernel noted down, a row per
+// warp.  It has two latencies to wait for: what was noted down, then the parts
+// with their maxima, the first BATCH of them at once (in turn, with the
+// sequence's offsets before them, four: 27 us for the chunk of 4096 over 8192
+// keys, 64/8 heads, against 14).  A chunk's items have few parts and many
+// rows, which more warps at a time get through; a decode step's the reverse.
+template <int DIM, int BATCH>
+__global__ void __launch_bounds__(kJoinThreads, BATCH <= 4 ? 12 : 4)
+    attn_join_kernel(const __grid_constant__ AttnParams p)
 {
     constexpr int kPer = DIM / 32;  // values of a lane
     grid_launch_dependents();
@@ -1062,61 +1067,62 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     const AttnJoin it = p.joins[c];
     if (it.parts == 0) return;
     const int lane = threadIdx.x & 31;
-    const int h = it.h, parts = it.parts;
-    const AttnSeq sq = attn_seq(a, it.seq, false);
-    const int rows = sq.n_new * p.G;
-    const int live = rows - it.row0 < p.mb ? rows - it.row0 : p.mb;
-    for (int r = 4 * blockIdx.y + (threadIdx.x >> 5); r < live; r += 4 * gridDim.y) {
-        float mm = -INFINITY;
-        for (int i = lane; i < parts; i += 32)
-            mm = fmaxf(mm, p.part_ml[static_cast<int64_t>(attn_slot(c - 1 + i, i == 0)) * p.mb + r].x);
+    const int parts = it.parts;
+    const int live = it.rows - it.row0 < p.mb ? it.rows - it.row0 : p.mb;
+    const int r = kJoinThreads / 32 * blockIdx.y + (threadIdx.x >> 5);
+    if (r >= live) return;
+    const auto row_of = [&](int i) { return static_cast<int64_t>(attn_slot(c - 1 + i, i == 0)) * p.mb + r; };
+    float v[BATCH][kPer];
+    const auto load = [&](int i0) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-        float acc[kPer] = {}, ll = 0.0f;
-        for (int i0 = 0; i0 < parts; i0 += 32) {
-            float w = 0.0f, lw = 0.0f;
-            if (i0 + lane < parts) {
-                const float2 ml =
-                    p.part_ml[static_cast<int64_t>(attn_slot(c - 1 + i0 + lane, i0 + lane == 0)) * p.mb + r];
-                w = attn_weight(ml.x, ml.y, mm);
-                lw = ml.y;
-            }
-            const int n = parts - i0 < 32 ? parts - i0 : 32;
-            for (int j0 = 0; j0 < n; j0 += 8) {
-                float v[8][kPer];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int i = i0 + (j0 + j < n ? j0 + j : n - 1);
-                    const float* src =
-                        p.part_o + (static_cast<int64_t>(attn_slot(c - 1 + i, i == 0)) * p.mb + r) * DIM + kPer * lane;
-                    if constexpr (kPer == 4) {
-                        const float4 x = *reinterpret_cast<const float4*>(src);
-                        v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
-                    } else {
-                        const float2 x = *reinterpret_cast<const float2*>(src);
-                        v[j][0] = x.x, v[j][1] = x.y;
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float wi = __shfl_sync(0xffffffffu, w, j0 + j), li = __shfl_sync(0xffffffffu, lw, j0 + j);
-                    if (j0 + j < n && wi != 0.0f) {
-                        ll += wi * li;
-#pragma unroll
-                        for (int e = 0; e < kPer; ++e) acc[e] += wi * v[j][e];
-                    }
-                }
+        for (int j = 0; j < BATCH; ++j) {
+            const float* src = p.part_o + row_of(i0 + j < parts ? i0 + j : parts - 1) * DIM + kPer * lane;
+            if constexpr (kPer == 4) {
+                const float4 x = *reinterpret_cast<const float4*>(src);
+                v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
+            } else {
+                const float2 x = *reinterpret_cast<const float2*>(src);
+                v[j][0] = x.x, v[j][1] = x.y;
             }
         }
-        const int row = it.row0 + r, tok = row / p.G;
-        const int64_t at = (static_cast<int64_t>(sq.q0) + tok) * a.n_q + h * p.G + (row - tok * p.G);
-        if (!bd_in(kBkAttnCombine, at, a.T * a.n_q)) continue;
-        const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + at * DIM + kPer * lane);
+    };
+    load(0);
+    float2 ml = make_float2(-INFINITY, 0.0f);  // of part 32 n + lane
+    if (lane < parts) ml = p.part_ml[row_of(lane)];
+    float mm = ml.x;
+    for (int i = 32 + lane; i < parts; i += 32) mm = fmaxf(mm, p.part_ml[row_of(i)].x);
 #pragma unroll
-        for (int e = 0; e < kPer; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-        if (lane == 0 && a.lse) a.lse[at] = attn_lse(mm, ll);
+    for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+    float acc[kPer] = {}, ll = 0.0f, w = attn_weight(ml.x, ml.y, mm);
+    for (int i0 = 0; i0 < parts; i0 += BATCH) {
+        if (i0) load(i0);
+        if (i0 && (i0 & 31) == 0) {
+            ml = make_float2(-INFINITY, 0.0f);
+            if (i0 + lane < parts) ml = p.part_ml[row_of(i0 + lane)];
+            w = attn_weight(ml.x, ml.y, mm);
+        }
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            const float wj = __shfl_sync(0xffffffffu, w, (i0 + j) & 31);
+            const float lj = __shfl_sync(0xffffffffu, ml.y, (i0 + j) & 31);
+            if (i0 + j < parts && wj != 0.0f) {
+                ll += wj * lj;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) acc[e] += wj * v[j][e];
+            }
+        }
     }
+    const int row = it.row0 + r, tok = row / p.G;
+    const int64_t at = (static_cast<int64_t>(it.q0) + tok) * a.n_q + it.h * p.G + (row - tok * p.G);
+    if (!bd_in(kBkAttnCombine, at, a.T * a.n_q)) return;
+    const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+    uint32_t y[kPer / 2];
+#pragma unroll
+    for (int e = 0; e < kPer; e += 2) y[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    uint16_t* dst = a.out + at * DIM + kPer * lane;
+    if constexpr (kPer == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
+    else *reinterpret_cast<uint32_t*>(dst) = y[0];
+    if (lane == 0 && a.lse) a.lse[at] = attn_lse(mm, ll);
 }
 
 template <int DIM, bool INT8, int NT, bool WHOLE>
@@ -1247,9 +1253,10 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream)
     if (chunk) launch_dep(err, attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
     if (err == cudaSuccess) err = chunk ? launch_attention_chunk(p, stream) : launch_attention_mma(p, stream);
     if (p.whole) return err;
-    const dim3 grid(static_cast<unsigned>(p.blocks > 1 ? p.blocks - 1 : 1), chunk ? 16 : p.mb / 4);
-    launch_dep(err, a.cache.dim == 128 ? attn_join_kernel<128> : attn_join_kernel<64>, grid, dim3(kJoinThreads), 0,
-               stream, p);
+    const dim3 grid(static_cast<unsigned>(p.blocks > 1 ? p.blocks - 1 : 1), p.mb / (kJoinThreads / 32));
+    const auto join = a.cache.dim == 128 ? chunk ? attn_join_kernel<128, 4> : attn_join_kernel<128, 16>
+                                         : chunk ? attn_join_kernel<64, 4> : attn_join_kernel<64, 16>;
+    launch_dep(err, join, grid, dim3(kJoinThreads), 0, stream, p);
     return err;
 }
 

@@ -42,9 +42,11 @@ struct AttnItem {
 };
 
 // The (item, head) whose parts the join adds at block c: parts of blocks
-// c - 1 .. c + parts - 2; parts == 0: none.
+// c - 1 .. c + parts - 2; parts == 0: none.  With all that the join has to
+// know of the sequence, so that it need not look it up.
 struct AttnJoin {
-    int seq, row0, h, parts;
+    int q0, rows;  // of the sequence: its first token, and its rows
+    int row0, h, parts;
 };
 
 struct AttnHeader {
@@ -130,9 +132,9 @@ __device__ __forceinline__ int attn_div(int64_t rel, int tiles)
 // What block c, whose first unit u lies in the (item, head) with units
 // [start, start + tiles), notes down for the join.
 __device__ __forceinline__ AttnJoin attn_join_of(int64_t units, int n, int c, int64_t u, int64_t start, int tiles,
-                                                 int seq, int row0, int h)
+                                                 const AttnSeq& sq, int G, int row0, int h)
 {
-    AttnJoin j{seq, row0, h, 0};
+    AttnJoin j{sq.q0, sq.n_new * G, row0, h, 0};
     if (start != u && attn_owner(units, n, start) == c - 1) j.parts = attn_owner(units, n, start + tiles - 1) - c + 2;
     return j;
 }

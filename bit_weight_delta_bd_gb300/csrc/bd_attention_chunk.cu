@@ -499,13 +499,13 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
         walk.item = attn_find_item(p.items, head.n_items, n_kv, walk.u);
     }
     if (threadIdx.x == 0) {
-        AttnJoin j{0, 0, 0, 0};
+        AttnJoin j{};
         if (c < active) {
             const AttnItem it = p.items[walk.item];
             const int64_t first = static_cast<int64_t>(it.before) * n_kv;
             const int h = attn_div(walk.u - first, it.tiles);
-            j = attn_join_of(units, active, c, walk.u, first + static_cast<int64_t>(h) * it.tiles, it.tiles, it.seq,
-                             it.row0, h);
+            j = attn_join_of(units, active, c, walk.u, first + static_cast<int64_t>(h) * it.tiles, it.tiles,
+                             attn_seq(a, it.seq, false), p.G, it.row0, h);
         }
         p.joins[c] = j;
     }
