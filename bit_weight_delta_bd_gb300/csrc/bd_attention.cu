@@ -1203,7 +1203,7 @@ size_t attention_workspace_size(int64_t T, int64_t n_seq, int n_q, int n_kv, int
     // the host may learn how long the chunks are only with the call: room for either kernel
     const int G = n_q / n_kv;
     const size_t mma = attn_layout(T, n_seq, G, dim, kMmaMaxRows, kAttnMaxBlocks).total;
-    const size_t chunk = attn_layout(T, n_seq, G, dim, kChunkRows, kAttnMaxChunkBlocks).total;
+    const size_t chunk = attn_layout(T, n_seq, G, dim, chunk_rows(dim), kAttnMaxChunkBlocks * 256 / chunk_rows(dim)).total;
     return mma > chunk ? mma : chunk;
 }
 
@@ -1216,9 +1216,10 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream)
     const int64_t rows = a.max_new * p.G;  // of a sequence, as far as the host knows
     const bool chunk = rows > kMmaMaxRows;
     p.tile = chunk ? kChunkTile : kMmaTile;
-    p.mb = chunk ? kChunkRows : rows > 8 ? kMmaMaxRows : 8;
-    const int most = chunk ? kAttnMaxChunkBlocks : kAttnMaxBlocks;
-    p.blocks = chunk ? a.sm_count : mma_blocks_per_sm(p.mb, a.cache.dim, a.cache.int8) * a.sm_count;
+    p.mb = chunk ? chunk_rows(a.cache.dim) : rows > 8 ? kMmaMaxRows : 8;
+    const int ctas = p.mb / 256 > 1 ? 2 : 1;  // of a block of the deal
+    const int most = chunk ? kAttnMaxChunkBlocks / ctas : kAttnMaxBlocks;
+    p.blocks = chunk ? a.sm_count / ctas : mma_blocks_per_sm(p.mb, a.cache.dim, a.cache.int8) * a.sm_count;
     if (p.blocks > most) p.blocks = most;
     // Short caches, or few: a cluster of up to 8 blocks for each (sequence,
     // head), which needs no deal and no second launch.  (cap is the longest

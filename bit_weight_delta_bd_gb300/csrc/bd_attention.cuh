@@ -190,6 +190,7 @@ __device__ __forceinline__ float attn_lse(float m, float l) { return l == 0.0f ?
 cudaError_t launch_attention_mma(const AttnParams& p, cudaStream_t stream);
 // Chunks (bd_attention_chunk.cu): 256 rows an item, 128 keys a tile.
 cudaError_t launch_attention_chunk(const AttnParams& p, cudaStream_t stream);
-constexpr int kChunkTile = 128, kChunkRows = 256;
+constexpr int kChunkTile = 128;
+constexpr int chunk_rows(int dim) { return dim == 128 ? 512 : 256; }
 
 }  // namespace bd

@@ -54,14 +54,16 @@ struct ChunkParams {
 
 template <int DIM, bool INT8>
 struct ChunkShape {
+    static constexpr bool kPair = DIM == 128;
+    static constexpr int kCtas = kPair ? 2 : 1;
     static constexpr int kThreads = INT8 ? 512 : 384;
-    static constexpr int kBufs = INT8 ? 3 : (DIM == 128 ? 5 : 8);  // bf16 tiles in shared memory
-    static constexpr int kRaw = INT8 ? 3 : 0;                      // tiles of codes
-    static constexpr int kScaleBufs = INT8 ? 3 : 0;                // scales of a key tile, K and V
-    static constexpr int kHalves = DIM / 64;
-    static constexpr int kHalfBytes = kTile * 128;                 // 64 dims of 128 keys
-    static constexpr int kTileBytes = kHalves * kHalfBytes;
-    static constexpr int kRawBytes = kTile * DIM;
+    static constexpr int kBufs = INT8 ? (kPair ? 6 : 3) : 8;        // bf16 tiles in shared memory
+    static constexpr int kRaw = INT8 ? (kPair ? 6 : 3) : 0;         // tiles of codes
+    static constexpr int kScaleBufs = INT8 ? (kPair ? 4 : 3) : 0;   // scales of a key tile, K and V
+    // a CTA's part of a tile: in a pair half the keys of each step of K, half the dims of V
+    static constexpr int kKeysK = kTile / kCtas, kDimsV = DIM / kCtas;
+    static constexpr int kTileBytes = kTile * DIM * 2 / kCtas;
+    static constexpr int kRawBytes = kTile * DIM / kCtas;
     static constexpr int kQBytes = kQRows * DIM * 2;
     static constexpr int kOffBufs = 2 * kQBytes;
     static constexpr int kOffRaw = kOffBufs + kBufs * kTileBytes;
@@ -74,12 +76,13 @@ struct ChunkShape {
     static_assert(2 * kSoftRegs + (INT8 ? 2 : 1) * kOtherRegs <= (INT8 ? 4 * 128 : 3 * 168), "register split");
 };
 
-constexpr int kMaxBufs = 8;
+constexpr int kMaxBufs = 8, kMaxRaw = 6, kMaxScales = 4;
 
 struct ChunkShared {
-    uint64_t full[kMaxBufs], empty[kMaxBufs];    // bf16 tiles
-    uint64_t raw_full[3], raw_empty[3];          // tiles of codes
-    uint64_t sc_full[3], sc_empty[3];            // scales
+    uint64_t full[kMaxBufs], empty[kMaxBufs];    // bf16 tiles (full: of both CTAs, in the even one)
+    uint64_t landed[kMaxBufs];                   // this CTA's part of them (pairs, bf16)
+    uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];     // tiles of codes
+    uint64_t sc_full[kMaxScales], sc_empty[kMaxScales];  // scales
     uint64_t q_full[2], o_full[2];
     uint64_t s_full[2][2], p_full[2][2], pv_done[2];  // by query tile (and place)
     uint64_t done;
@@ -95,7 +98,7 @@ constexpr size_t chunk_smem()
     return Shape::kBytes + sizeof(ChunkShared);
 }
 
-constexpr int kSoftWarps = 8, kTmaWarp = 8, kMmaWarp = 9, kConvertWarp = 12;
+constexpr int kSoftWarps = 8, kTmaWarp = 8, kMmaWarp = 9, kPassWarp = 11, kConvertWarp = 12;
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;  // S at 128 i + 64 b (query tile i, place b), O tiles from 256 on
@@ -109,6 +112,39 @@ __device__ __forceinline__ bool warp_wait(volatile int* abort_flag, uint64_t* ba
     if (__all_sync(0xffffffffu, mbar_wait_sleeping(bar, parity))) return true;
     *abort_flag = 1;
     return false;
+}
+
+// Barriers of a pair: an arrival at the even CTA's, a wait for arrivals of
+// both, and the tensor cores' arrival at both.
+template <bool PAIR>
+__device__ __forceinline__ void arrive_even(uint64_t* bar)
+{
+    if constexpr (PAIR) mbar_arrive_remote(bar, 0);
+    else mbar_arrive(bar);
+}
+template <bool PAIR>
+__device__ __forceinline__ void wait_both(volatile int* abort_flag, uint64_t* bar, uint32_t parity)
+{
+    if (warp_wait(abort_flag, bar, parity) && PAIR) (void)mbar_try_wait_cluster(bar, parity);  // for its scope
+}
+template <bool PAIR>
+__device__ __forceinline__ void commit_both(uint64_t* bar)
+{
+    if constexpr (PAIR) mma_commit_pair(bar, 3);
+    else mma_commit(bar);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void mma_from_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    if constexpr (PAIR) mma_ts_pair(d, a, b, idesc, accumulate);
+    else mma_ts(d, a, b, idesc, accumulate);
+}
+template <bool PAIR>
+__device__ __forceinline__ void mma_from_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    if constexpr (PAIR) mma_ss_pair(d, a, b, idesc, accumulate);
+    else mma_ss(d, a, b, idesc, accumulate);
 }
 
 template <int N>
@@ -192,6 +228,19 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t 
     d |= static_cast<uint64_t>(1) << 46;
     d |= static_cast<uint64_t>(2) << 61;
     return d;
+}
+
+// What lies past the sequence in a tile of V may be anything, NaN included:
+// zeros from key `valid` on instead, so that probabilities of 0 times it stay
+// 0.  (64 dims, which is all of V that a CTA holds.)  By a warp.
+__device__ __forceinline__ void zero_past(uint8_t* v, int valid, int lane)
+{
+    if (valid >= kTile) return;
+#pragma unroll 1
+    for (int x = (valid > 0 ? valid : 0) * 8 + lane; x < kTile * 8; x += 32)
+        *reinterpret_cast<uint4*>(v + x * 16) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    __syncwarp();
 }
 
 // One lane of the warp.
@@ -285,11 +334,11 @@ __device__ __forceinline__ uint2 codes4(uint32_t r)  // in the order 0, 2, 1, 3
 // rows: the lowest) that put both their reads from TMA's swizzled tile of
 // codes and their writes to the swizzled tile of numbers into different banks.
 // Later chunks of a thread lie 16 (32) keys on, at the same place of the swizzle.
-template <int DIM, bool HALF>
+template <int DIM, int KEYS, bool HALF>
 __device__ __forceinline__ void convert_tile(const uint8_t* src, uint8_t* dst, int tid)
 {
     constexpr int kKeys = 128 * 16 / DIM;  // keys of one round
-    constexpr int kRounds = kTile / kKeys;
+    constexpr int kRounds = KEYS / kKeys;
     const int warp = tid >> 5, c = tid & 3, odd = (tid >> 2) & 1, rest = (tid >> 3) & 3;
     int key, ch;
     if constexpr (DIM == 128) {
@@ -301,7 +350,7 @@ __device__ __forceinline__ void convert_tile(const uint8_t* src, uint8_t* dst, i
         key = 8 * warp + 2 * rest + odd;
     }
     const uint8_t* from = src + key * DIM + ((DIM == 128 ? ch ^ (key & 7) : ch ^ ((key >> 1) & 3)) << 4);
-    uint8_t* row = dst + (ch >> 2) * (kTile * 128) + key * 128;
+    uint8_t* row = dst + (ch >> 2) * (KEYS * 128) + key * 128;
     uint8_t* to_lo = row + (((2 * (ch & 3)) ^ (key & 7)) << 4);
     uint8_t* to_hi = row + (((2 * (ch & 3) + 1) ^ (key & 7)) << 4);
     uint4 w = *reinterpret_cast<const uint4*>(from);
@@ -347,7 +396,7 @@ struct Walk {
         s.t1 = __shfl_sync(0xffffffffu, s.t1, 0);
         s.rows = __shfl_sync(0xffffffffu, s.rows, 0);
         s.sq.len = __shfl_sync(0xffffffffu, s.sq.len, 0);
-        s.q_tiles = s.rows > kQRows ? 2 : 1;
+        s.q_tiles = s.rows > p.mb / 2 ? 2 : 1;
         return true;
     }
 };
@@ -383,7 +432,7 @@ __device__ __forceinline__ float unit_of(float x)
     return __uint_as_float(__float_as_uint(fminf(fmaxf(x, 7.9e-31f), 1.2e30f)) & 0x7F800000u);
 }
 
-// A warp's 32 rows, from row r0 on, of a segment's query tile i, into shared
+// A warp's 32 rows, from row r0 on, of the query tile that starts at the item's row tile_row, into shared
 // memory (K-major, 128-byte swizzle, halves of 64 dims); rows past the item
 // are zeros.  Neighbouring lanes take neighbouring 16 bytes, eight loads in
 // flight (a row per lane, two in flight, cost 6 us per item, and twice that
@@ -391,10 +440,10 @@ __device__ __forceinline__ float unit_of(float x)
 // Q's sign; int8: fp16, over the row's power of two, dims in the codes' order.
 // Returns what the products of row r0 + lane are to be multiplied by.
 template <int DIM, bool INT8>
-__device__ __forceinline__ float load_q(const AttnParams& p, const Segment& s, int i, int r0, int lane, uint8_t* dst)
+__device__ __forceinline__ float load_q(const AttnParams& p, const Segment& s, int tile_row, int r0, int lane, uint8_t* dst)
 {
     constexpr int kLanes = DIM / 8, kRowsAtOnce = 32 / kLanes, kBatch = 8;
-    const uint64_t own = reinterpret_cast<uint64_t>(q_row<DIM>(p, s, i * kQRows + r0 + lane));
+    const uint64_t own = reinterpret_cast<uint64_t>(q_row<DIM>(p, s, tile_row + r0 + lane));
     const uint32_t flip = p.a.scale < 0.0f ? 0x80008000u : 0u;
     const int c = lane & (kLanes - 1), sub = lane / kLanes;
     float back = 1.0f;
@@ -446,6 +495,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
     attn_chunk_kernel(const __grid_constant__ ChunkParams cp)
 {
     using S = ChunkShape<DIM, INT8>;
+    constexpr bool kPair = S::kPair;
     extern __shared__ __align__(1024) uint8_t dyn[];
     ChunkShared& sh = *reinterpret_cast<ChunkShared*>(dyn + S::kBytes);
     const AttnParams& p = cp.p;
@@ -458,20 +508,23 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
     grid_launch_dependents();
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kBufs; ++i) {
-            mbar_init(&sh.full[i], INT8 ? 4 : 1);
+            mbar_init(&sh.full[i], (INT8 ? 4 : 1) * S::kCtas);
             mbar_init(&sh.empty[i], 2);
+            mbar_init(&sh.landed[i], 1);
         }
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < S::kRaw; ++i) {
             mbar_init(&sh.raw_full[i], 1);
             mbar_init(&sh.raw_empty[i], 4);
+        }
+        for (int i = 0; i < S::kScaleBufs; ++i) {
             mbar_init(&sh.sc_full[i], 1);
             mbar_init(&sh.sc_empty[i], 8);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.q_full[i], 4);
+            mbar_init(&sh.q_full[i], 4 * S::kCtas);
             for (int b = 0; b < 2; ++b) {
                 mbar_init(&sh.s_full[i][b], 1);
-                mbar_init(&sh.p_full[i][b], 4);
+                mbar_init(&sh.p_full[i][b], 4 * S::kCtas);
             }
             mbar_init(&sh.pv_done[i], 1);
             mbar_init(&sh.o_full[i], 1);
@@ -480,9 +533,13 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
         sh.abort = 0;
         fence_mbarrier_init();
     }
-    if (warp == kMmaWarp) tmem_alloc(&sh.tmem, kTmemCols);
+    if (warp == kMmaWarp) {
+        if constexpr (kPair) tmem_alloc_pair(&sh.tmem, kTmemCols);
+        else tmem_alloc(&sh.tmem, kTmemCols);
+    }
     tc_fence_before();
     __syncthreads();
+    if constexpr (kPair) cluster_sync_all();  // the other's barriers are there before anything arrives at them
     tc_fence_after();
     grid_dependency_wait();
 
@@ -491,14 +548,15 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
     const int n_kv = cache.n_kv;
     const int64_t units = static_cast<int64_t>(head.tiles) * n_kv;
     const int active = attn_active(units, p.blocks);
-    const int c = blockIdx.x;
+    const int rank = kPair ? __shfl_sync(0xffffffffu, static_cast<int>(cluster_ctarank()), 0) : 0;
+    const int c = blockIdx.x / S::kCtas;
     Walk walk{p, 0, 0, 0};
     if (c < active) {
         walk.u = attn_first(units, active, c);
         walk.end = attn_first(units, active, c + 1);
         walk.item = attn_find_item(p.items, head.n_items, n_kv, walk.u);
     }
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && rank == 0) {
         AttnJoin j{};
         if (c < active) {
             const AttnItem it = p.items[walk.item];
@@ -517,6 +575,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
         reg_inc<S::kSoftRegs>();
         const int i = warp >> 2;
         const int r = 32 * (warp & 3) + lane;  // this thread's row of the tile
+        const int tile_row = (i * S::kCtas + rank) * kQRows;  // the tile's first row of the item
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + lanes + i * 128, to = tmem + lanes + kTmemO + i * DIM;
         uint8_t* q_smem = dyn + i * S::kQBytes;
@@ -535,10 +594,10 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
             const bool have = walk.next(s);
             const bool runs = have && i < s.q_tiles;
             if (runs) {
-                unit = load_q<DIM, INT8>(p, s, i, r - lane, lane, q_smem);
+                unit = load_q<DIM, INT8>(p, s, tile_row, r - lane, lane, q_smem);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.q_full[i]);
+                if (lane == 0) arrive_even<kPair>(&sh.q_full[i]);
             }
             if (ran) {
                 warp_wait(&sh.abort, &sh.o_full[i], o_phase);
@@ -599,7 +658,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
                 }
                 continue;
             }
-            const int row = i * kQRows + r;
+            const int row = tile_row + r;
             live = row < s.rows && row < p.mb;
             int seen = 0;
             {
@@ -610,7 +669,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
                            : static_cast<int64_t>(attn_slot(c, s.t0 == 0)) * p.mb + row;
             }
             // what the tile's first row sees (the others see at least as much): below it no mask
-            const int all_seen = attn_seen(s.sq, (s.it.row0 + i * kQRows) / p.G, a.causal);
+            const int all_seen = attn_seen(s.sq, (s.it.row0 + tile_row) / p.G, a.causal);
             // (a scale of 0 would make NaN of a masked score)
             const float c2 = fmaxf(fabsf(a.scale) * kLog2e * unit, 1e-30f);
             m = -INFINITY;
@@ -716,7 +775,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&sh.p_full[i][b]);
+                    arrive_even<kPair>(&sh.p_full[i][b]);
                     if constexpr (INT8)
                         if (b) mbar_arrive(&sh.sc_empty[sc]);
                 }
@@ -734,18 +793,20 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
         if (warp == kTmaWarp) {
             // ---------------------------------------------------- TMA
             constexpr int kRing = INT8 ? S::kRaw : S::kBufs;
-            uint64_t* full = INT8 ? sh.raw_full : sh.full;
+            uint64_t* full = INT8 ? sh.raw_full : kPair ? sh.landed : sh.full;
             uint64_t* empty = INT8 ? sh.raw_empty : sh.empty;
-            const int box_rows = cache.page;  // at most 128
-            const int pages_per_tile = kTile / box_rows;
+            const int pages_per_tile = kTile / cache.page;  // (at most 128 keys a page)
+            // K of a pair: boxes of up to 32 keys, the CTA's half of each step of 64
+            const int box_k = kPair && cache.page > 32 ? 32 : cache.page;
+            const int boxes_k = S::kKeysK / box_k, boxes_step = kPair ? 32 / box_k : 0;
             int buf = 0, sc = 0;
             uint32_t phase = 0, sc_phase = 0;
             bool ok = true;
             while (ok && walk.next(s)) {
                 // the segment's Q on its way to the L2 cache while the tiles before it are worked on
 #pragma unroll 1
-                for (int r = lane; r < kChunkRows; r += 32)
-                    if (const uint4* q = q_row<DIM>(p, s, r)) {
+                for (int r = lane; r < 2 * kQRows; r += 32)
+                    if (const uint4* q = q_row<DIM>(p, s, ((r >> 7) * S::kCtas + rank) * kQRows + (r & 127))) {
                         prefetch_l2(q);
                         if constexpr (DIM == 128) prefetch_l2(q + 8);
                     }
@@ -753,7 +814,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
                 const int32_t* table = a.table + static_cast<int64_t>(s.it.seq) * a.max_pages;
                 const int pages = (s.sq.len + cache.page - 1) >> cache.page_shift;
                 for (int t = s.t0; t < s.t1 && ok; ++t) {
-                    // lane j looks after the j-th page of the tile
+                    // lane j looks after the j-th page of the tile, and the j-th box of K
                     const int at = t * pages_per_tile + lane;
                     const bool mine = lane < pages_per_tile && at < pages;
                     int page = 0;
@@ -765,35 +826,54 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
                         }
                     }
                     const int outer = page * n_kv + s.h;
-                    const uint32_t rows = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, mine)) * box_rows);
+                    const uint32_t rows =
+                        static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, mine)) * cache.page);
+                    int key_k = lane * cache.page;  // of the tile
+                    if constexpr (kPair) {
+                        const int step = lane / boxes_step;
+                        key_k = (step & 1) * kStep + 32 * rank + (lane - step * boxes_step) * box_k;
+                    }
+                    const int of = key_k >> cache.page_shift;  // the lane with the box's page
+                    const int outer_k = __shfl_sync(0xffffffffu, outer, of & 31);
+                    const bool mine_k = lane < boxes_k && t * pages_per_tile + of < pages;
+                    const uint32_t rows_k =
+                        static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, mine_k)) * box_k);
                     if constexpr (INT8) {
                         if (!(ok = warp_wait(&sh.abort, &sh.sc_empty[sc], sc_phase ^ 1))) break;
                         if (lane == 0) mbar_arrive_expect_tx(&sh.sc_full[sc], rows * 8);
                         __syncwarp();
                         if (mine) {
-                            uint8_t* dst = dyn + S::kOffScale + sc * 2 * kTile * 4 + lane * box_rows * 4;
+                            uint8_t* dst = dyn + S::kOffScale + sc * 2 * kTile * 4 + lane * cache.page * 4;
                             const int64_t vec = static_cast<int64_t>(outer) << cache.page_shift;
-                            bulk_g2s(dst, cache.k_scale + vec, box_rows * 4, &sh.sc_full[sc]);
-                            bulk_g2s(dst + kTile * 4, cache.v_scale + vec, box_rows * 4, &sh.sc_full[sc]);
+                            bulk_g2s(dst, cache.k_scale + vec, cache.page * 4, &sh.sc_full[sc]);
+                            bulk_g2s(dst + kTile * 4, cache.v_scale + vec, cache.page * 4, &sh.sc_full[sc]);
                         }
                         if (++sc == S::kScaleBufs) sc = 0, sc_phase ^= 1;
                     }
                     for (int kv = 0; kv < 2; ++kv) {
                         if (!(ok = warp_wait(&sh.abort, &empty[buf], phase ^ 1))) break;
-                        if (lane == 0) mbar_arrive_expect_tx(&full[buf], rows * DIM * (INT8 ? 1 : 2));
+                        constexpr int kBytes = INT8 ? 1 : 2;
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(&full[buf], (kv ? rows * S::kDimsV : rows_k * DIM) * kBytes);
                         __syncwarp();
-                        if (mine) {
-                            const CUtensorMap* map = kv ? &cp.v_map : &cp.k_map;
+                        uint8_t* dst = dyn + (INT8 ? S::kOffRaw + buf * S::kRawBytes : S::kOffBufs + buf * S::kTileBytes);
+                        if (kv == 0 && mine_k) {
+                            const int row = key_k & (cache.page - 1), to = lane * box_k;
                             if constexpr (INT8) {
-                                tma_load_3d(dyn + S::kOffRaw + buf * S::kRawBytes + lane * box_rows * DIM, map, 0, 0,
-                                            outer, &full[buf]);
+                                tma_load_3d(dst + to * DIM, &cp.k_map, 0, row, outer_k, &full[buf]);
                             } else {
 #pragma unroll
-                                for (int half = 0; half < S::kHalves; ++half)
-                                    tma_load_3d(dyn + S::kOffBufs + buf * S::kTileBytes + half * S::kHalfBytes +
-                                                    lane * box_rows * 128,
-                                                map, 64 * half, 0, outer, &full[buf]);
+                                for (int d = 0; d < DIM; d += 64)
+                                    tma_load_3d(dst + (d / 64) * S::kKeysK * 128 + to * 128, &cp.k_map, d, row, outer_k,
+                                                &full[buf]);
                             }
+                        }
+                        if (kv == 1 && mine) {
+                            const int to = lane * cache.page;
+                            if constexpr (INT8)
+                                tma_load_3d(dst + to * S::kDimsV, &cp.v_map, rank * S::kDimsV, 0, outer, &full[buf]);
+                            else
+                                tma_load_3d(dst + to * 128, &cp.v_map, rank * S::kDimsV, 0, outer, &full[buf]);
                         }
                         if (++buf == kRing) buf = 0, phase ^= 1;
                     }
@@ -806,16 +886,17 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
                     for (int b = 0; b < S::kScaleBufs; ++b)
                         mbar_wait_bounded(&sh.sc_full[b], b < sc ? sc_phase : sc_phase ^ 1);
             }
-        } else if (warp < kMmaWarp + 2) {
+        } else if (warp < kMmaWarp + 2 && rank == 0) {
             // ---------------------------------------------------- MMA of query tile i
-            constexpr uint32_t kIdescS = INT8 ? idesc_f16_f32(kQRows, kStep) : idesc_bf16_f32(kQRows, kStep);
-            constexpr uint32_t kIdescO = idesc_bf16_f32(kQRows, DIM) | (1u << 16);  // V: rows along the contracted index
+            constexpr int kRows = kQRows * S::kCtas;
+            constexpr uint32_t kIdescS = INT8 ? idesc_f16_f32(kRows, kStep) : idesc_bf16_f32(kRows, kStep);
+            constexpr uint32_t kIdescO = idesc_bf16_f32(kRows, DIM) | (1u << 16);  // V: rows along the contracted index
             const int i = warp - kMmaWarp;
             const uint32_t q_addr = smem_u32(dyn + i * S::kQBytes), buf_addr = smem_u32(dyn + S::kOffBufs);
             const uint32_t ts = tmem + i * 128, to = tmem + kTmemO + i * DIM;
             int buf = 0;
             uint32_t phase = 0, q_phase = 0, p_phase = 0;
-            const auto wait = [&](uint64_t* bar, uint32_t parity) { warp_wait(&sh.abort, bar, parity); };
+            const auto wait = [&](uint64_t* bar, uint32_t parity) { wait_both<kPair>(&sh.abort, bar, parity); };
             const auto take = [&]() {  // the next tile of the ring
                 const int b = buf;
                 wait(&sh.full[b], phase);
@@ -829,7 +910,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
 #pragma unroll 1
                     for (int n = 2 * (s.t1 - s.t0); n > 0; --n) {
                         const int b = take();
-                        if (lane == 0) mbar_arrive(&sh.empty[b]);
+                        if (lane < S::kCtas) mbar_arrive_remote(&sh.empty[b], lane);
                     }
                     continue;
                 }
@@ -843,23 +924,8 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
                     const bool pv = j >= 2 * s.t0 + 2, qk = j < 2 * s.t1;
                     if (pv && b == 0) {
                         bv = take();
-                        if constexpr (!INT8) {
-                            // what lies past the sequence may be anything, NaN included: zeros
-                            // instead, so that probabilities of 0 times it stay 0 (both warps
-                            // write them, each before its own product)
-                            const int valid = s.sq.len - (j - 2) * kStep;
-                            if (valid < kTile) {
-                                uint8_t* vt = dyn + S::kOffBufs + bv * S::kTileBytes;
-#pragma unroll 1
-                                for (int x = (valid > 0 ? valid : 0) * 8 + lane; x < kTile * 8; x += 32)
-#pragma unroll
-                                    for (int half = 0; half < S::kHalves; ++half)
-                                        *reinterpret_cast<uint4*>(vt + half * S::kHalfBytes + x * 16) =
-                                            make_uint4(0, 0, 0, 0);
-                                fence_proxy_async_smem();
-                                __syncwarp();
-                            }
-                        }
+                        if constexpr (!INT8 && !kPair) 
+                            zero_past(dyn + S::kOffBufs + bv * S::kTileBytes, s.sq.len - (j - 2) * kStep, lane);
                     }
                     if (qk && b == 0) bk = take();
                     if (pv) {
@@ -870,34 +936,50 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
                     if (elect_one()) {
                         if (pv) {
                             const uint64_t v_desc =
-                                smem_desc_mn_sw128(buf_addr + bv * S::kTileBytes + b * kStep * 128, S::kHalfBytes);
+                                smem_desc_mn_sw128(buf_addr + bv * S::kTileBytes + b * kStep * 128, kTile * 128);
 #pragma unroll
                             for (int k = 0; k < kStep / 16; ++k)
-                                mma_ts(to, ts + 64 * b + 8 * k, v_desc + k * (2048 >> 4), kIdescO,
-                                       j > 2 * s.t0 + 2 || k > 0);
-                            mma_commit(&sh.pv_done[i]);
-                            if (b) mma_commit(&sh.empty[bv]);
-                            if (j == 2 * s.t1 + 1) mma_commit(&sh.o_full[i]);
+                                mma_from_tmem<kPair>(to, ts + 64 * b + 8 * k, v_desc + k * (2048 >> 4), kIdescO,
+                                                     j > 2 * s.t0 + 2 || k > 0);
+                            commit_both<kPair>(&sh.pv_done[i]);
+                            if (b) commit_both<kPair>(&sh.empty[bv]);
+                            if (j == 2 * s.t1 + 1) commit_both<kPair>(&sh.o_full[i]);
                         }
                         if (qk) {
                             const uint64_t q_desc = smem_desc_sw128(q_addr);
-                            const uint64_t k_desc = smem_desc_sw128(buf_addr + bk * S::kTileBytes + b * kStep * 128);
+                            const uint64_t k_desc =
+                                smem_desc_sw128(buf_addr + bk * S::kTileBytes + b * (S::kKeysK / 2) * 128);
 #pragma unroll
                             for (int k = 0; k < DIM / 16; ++k) {
-                                const uint32_t off = ((k >> 2) * S::kHalfBytes + (k & 3) * 32) >> 4;
-                                mma_ss(ts + 64 * b, q_desc + off, k_desc + off, kIdescS, k > 0);
+                                const uint32_t in = (k & 3) * 32;
+                                mma_from_smem<kPair>(ts + 64 * b, q_desc + (((k >> 2) * kQRows * 128 + in) >> 4),
+                                                     k_desc + (((k >> 2) * S::kKeysK * 128 + in) >> 4), kIdescS, k > 0);
                             }
-                            mma_commit(&sh.s_full[i][b]);
-                            if (b) mma_commit(&sh.empty[bk]);
+                            commit_both<kPair>(&sh.s_full[i][b]);
+                            if (b) commit_both<kPair>(&sh.empty[bk]);
                         }
                     }
                     __syncwarp();
                 }
             }
             // nothing of this warp's products is in flight when the tensor memory is given back
-            if (elect_one()) mma_commit(&sh.done);
+            if (elect_one()) commit_both<kPair>(&sh.done);
             __syncwarp();
             mbar_wait_bounded(&sh.done, 0);
+        } else if (!INT8 && kPair && warp == kPassWarp) {
+            // ---------------------------------------------------- this CTA's parts are there
+            int buf = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            while (ok && walk.next(s)) {
+#pragma unroll 1
+                for (int n = 0; n < 2 * (s.t1 - s.t0); ++n) {  // K and V in turn
+                    if (!(ok = warp_wait(&sh.abort, &sh.landed[buf], phase))) break;
+                    if (n & 1) zero_past(dyn + S::kOffBufs + buf * S::kTileBytes, s.sq.len - (s.t0 + n / 2) * kTile, lane);
+                    if (lane == 0) arrive_even<kPair>(&sh.full[buf]);
+                    if (++buf == S::kBufs) buf = 0, phase ^= 1;
+                }
+            }
         }
     } else {
         reg_dec<S::kOtherRegs>();
@@ -913,12 +995,12 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
                     if (!(ok = warp_wait(&sh.abort, &sh.empty[buf], phase ^ 1))) break;
                     const uint8_t* src = dyn + S::kOffRaw + raw * S::kRawBytes;
                     uint8_t* dst = dyn + S::kOffBufs + buf * S::kTileBytes;
-                    if (n & 1) convert_tile<DIM, false>(src, dst, tid);  // V
-                    else convert_tile<DIM, true>(src, dst, tid);         // K
+                    if (n & 1) convert_tile<S::kDimsV, kTile, false>(src, dst, tid);  // V
+                    else convert_tile<DIM, S::kKeysK, true>(src, dst, tid);           // K
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(&sh.full[buf]);
+                        arrive_even<kPair>(&sh.full[buf]);
                         mbar_arrive(&sh.raw_empty[raw]);
                     }
                     if (++raw == S::kRaw) raw = 0, raw_phase ^= 1;
@@ -929,9 +1011,13 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (kPair) cluster_sync_all();  // the products read both CTAs' memory: neither ends before they have
     tc_fence_after();
     if (threadIdx.x == 0 && sh.abort) raise_error(a.err, kErrTimeout);
-    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+    if (warp == kMmaWarp) {
+        if constexpr (kPair) tmem_dealloc_pair(tmem, kTmemCols);
+        else tmem_dealloc(tmem, kTmemCols);
+    }
 }
 
 template <int DIM, bool INT8>
@@ -943,12 +1029,13 @@ cudaError_t launch_chunk_shape(const AttnParams& p, cudaStream_t stream)
     ChunkParams cp{};
     cp.p = p;
     const uint64_t outer = static_cast<uint64_t>(kv.n_pages) * kv.n_kv;
-    for (int i = 0; i < 2; ++i)
-        if (!encode_tma_3d(i ? &cp.v_map : &cp.k_map,
-                           INT8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, INT8 ? 1 : 2,
-                           i ? kv.v : kv.k, DIM, kv.page, outer, INT8 ? DIM : 64, kv.page,
-                           INT8 && DIM == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
-            return cudaErrorInvalidValue;
+    const auto type = INT8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const auto swizzle = [](int bytes) { return bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B; };
+    const int bytes = INT8 ? 1 : 2, cols_k = INT8 ? DIM : 64, cols_v = INT8 ? S::kDimsV : 64;
+    const int box_k = S::kPair && kv.page > 32 ? 32 : kv.page;
+    if (!encode_tma_3d(&cp.k_map, type, bytes, kv.k, DIM, kv.page, outer, cols_k, box_k, swizzle(cols_k * bytes)) ||
+        !encode_tma_3d(&cp.v_map, type, bytes, kv.v, DIM, kv.page, outer, cols_v, kv.page, swizzle(cols_v * bytes)))
+        return cudaErrorInvalidValue;
     constexpr size_t smem = chunk_smem<S>();
     const void* kernel = reinterpret_cast<const void*>(attn_chunk_kernel<DIM, INT8>);
     cudaError_t err = ensure_dynamic_smem(kernel, smem, smem_set);
@@ -965,7 +1052,8 @@ cudaError_t launch_chunk_shape(const AttnParams& p, cudaStream_t stream)
     }
     if (n * (S::kThreads / 128) < 2 * S::kSoftRegs + (S::kThreads / 128 - 2) * S::kOtherRegs)
         return cudaErrorInvalidConfiguration;
-    launch_dep(err, attn_chunk_kernel<DIM, INT8>, dim3(p.blocks), dim3(S::kThreads), smem, stream, cp);
+    launch_dep_clusters(err, attn_chunk_kernel<DIM, INT8>, dim3(p.blocks * S::kCtas), dim3(S::kThreads), S::kCtas, smem,
+                        stream, cp);
     return err;
 }
 

@@ -164,6 +164,18 @@ __device__ __forceinline__ void mma_ts_pair(uint32_t d_taddr, uint32_t a_taddr, 
         : "memory");
 }
 
+// The same with A from shared memory (each CTA's own 128 rows, at the same offset).
+__device__ __forceinline__ void mma_ss_pair(uint32_t d_taddr, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_taddr),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // Arrives once on the mbarrier at this shared-memory offset in every CTA of
 // cta_mask when all pair MMAs issued so far by this thread have completed.
 __device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint16_t cta_mask)
