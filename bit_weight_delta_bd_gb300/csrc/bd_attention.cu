@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
         const int s = s0 + threadIdx.x;
         int n = 0;
         if (s < n_seq) {
-            const AttnSeq q = attn_seq(a, s, true);
+            const AttnSeq q = attn_seq(p, s, true);
             n = static_cast<int>((static_cast<int64_t>(q.n_new) * p.G + p.mb - 1) / p.mb);
         }
         int total;
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
                 if (p.item_off[mid] <= i) lo = mid;
                 else hi = mid;
             }
-            const AttnSeq q = attn_seq(a, lo, false);
+            const AttnSeq q = attn_seq(p, lo, false);
             it.seq = lo;
             it.row0 = (i - p.item_off[lo]) * p.mb;
             int64_t last = static_cast<int64_t>(it.row0) + p.mb - 1;
@@ -203,14 +203,14 @@ struct MmaWalk {
         if (u >= end) return;
         s.seq = seq;
         s.row0 = row0;
-        s.sq = attn_seq(p.a, seq, false);
+        s.sq = attn_seq(p, seq, false);
         s.rows = s.sq.n_new * p.G;
         s.tiles = mma_tiles(p, s.sq, row0);
         look_ahead();
     }
     __device__ __forceinline__ void look_ahead()
     {
-        if (s.seq + 1 < p.a.n_seq) ahead = attn_seq(p.a, s.seq + 1, false);
+        if (s.seq + 1 < p.a.n_seq) ahead = attn_seq(p, s.seq + 1, false);
     }
     __device__ __forceinline__ bool next()
     {
@@ -252,7 +252,7 @@ struct WholeWalk {
         rank = static_cast<int>(blockIdx.x) - pair * p.whole;
         s.seq = pair / p.a.cache.n_kv;
         s.h = pair - s.seq * p.a.cache.n_kv;
-        s.sq = attn_seq(p.a, s.seq, s.h == 0 && rank == 0);
+        s.sq = attn_seq(p, s.seq, s.h == 0 && rank == 0);
         s.rows = s.sq.n_new * p.G;
         s.row0 = -p.mb;
     }
@@ -280,7 +280,7 @@ __device__ __forceinline__ MmaWalk mma_deal(const AttnParams& p, MmaShared& sh)
     const int s1 = s0 + per < n_seq ? s0 + per : n_seq;
     int64_t mine = 0;
     for (int s = s0; s < s1; ++s) {
-        const AttnSeq q = attn_seq(a, s, blockIdx.x == 0);
+        const AttnSeq q = attn_seq(p, s, blockIdx.x == 0);
         for (int row0 = 0; row0 < q.n_new * p.G; row0 += p.mb) mine += mma_tiles(p, q, row0);
     }
     int64_t x = mine;
@@ -306,7 +306,7 @@ __device__ __forceinline__ MmaWalk mma_deal(const AttnParams& p, MmaShared& sh)
             // this thread's sequences hold it
             int64_t before = at * n_kv;
             for (int s = s0; s < s1; ++s) {
-                const AttnSeq q = attn_seq(a, s, false);
+                const AttnSeq q = attn_seq(p, s, false);
                 for (int row0 = 0; row0 < q.n_new * p.G; row0 += p.mb) {
                     const int64_t n = static_cast<int64_t>(mma_tiles(p, q, row0)) * n_kv;
                     if (u >= before && u < before + n) {
@@ -1164,13 +1164,14 @@ struct AttnWs {
     size_t head, item_off, items, joins, ml, o, total;
 };
 
-AttnWs attn_layout(int64_t T, int64_t n_seq, int64_t G, int dim, int mb, int blocks)
+// rows: of all sequences, where the items are listed (chunks); else 0
+AttnWs attn_layout(int64_t rows, int64_t n_seq, int dim, int mb, int blocks)
 {
     AttnWs w{};
     w.head = 256;
     w.item_off = w.head + 256;
     w.items = w.item_off + align_up(static_cast<size_t>(n_seq + 1) * 4);
-    const size_t items = static_cast<size_t>((T * G + mb - 1) / mb + n_seq);
+    const size_t items = rows > 0 ? static_cast<size_t>((rows + mb - 1) / mb + n_seq) : 0;
     w.joins = w.items + align_up(items * sizeof(AttnItem));
     w.ml = w.joins + align_up(static_cast<size_t>(blocks) * sizeof(AttnJoin));
     w.o = w.ml + align_up(static_cast<size_t>(2 * blocks) * mb * 8);
@@ -1200,27 +1201,56 @@ cudaError_t launch_attention_mma(const AttnParams& p, cudaStream_t stream)
 
 size_t attention_workspace_size(int64_t T, int64_t n_seq, int n_q, int n_kv, int dim)
 {
-    // the host may learn how long the chunks are only with the call: room for either kernel
+    // the host may learn how long the chunks are only with the call: room for both kernels
     const int G = n_q / n_kv;
-    const size_t mma = attn_layout(T, n_seq, G, dim, kMmaMaxRows, kAttnMaxBlocks).total;
-    const size_t chunk = attn_layout(T, n_seq, G, dim, chunk_rows(dim), kAttnMaxChunkBlocks * 256 / chunk_rows(dim)).total;
-    return mma > chunk ? mma : chunk;
+    const size_t few = attn_layout(0, n_seq, dim, kMmaMaxRows, kAttnMaxBlocks).total;
+    const size_t chunk = attn_layout(T * G, n_seq, dim, chunk_rows(dim), chunk_max_blocks(dim)).total;
+    return few + chunk;
 }
 
-cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream)
+// Takes the workspace's next part (the first 256 bytes of it all are the error word's).
+static void attn_take_workspace(AttnParams& p, int64_t rows, int most_blocks, char*& ws)
 {
-    if (a.T == 0 || a.n_seq == 0) return cudaSuccess;
-    AttnParams p{};
-    p.a = a;
-    p.G = a.n_q / a.cache.n_kv;
-    const int64_t rows = a.max_new * p.G;  // of a sequence, as far as the host knows
-    const bool chunk = rows > kMmaMaxRows;
-    p.tile = chunk ? kChunkTile : kMmaTile;
-    p.mb = chunk ? chunk_rows(a.cache.dim) : rows > 8 ? kMmaMaxRows : 8;
-    const int ctas = p.mb / 256 > 1 ? 2 : 1;  // of a block of the deal
-    const int most = chunk ? kAttnMaxChunkBlocks / ctas : kAttnMaxBlocks;
-    p.blocks = chunk ? a.sm_count / ctas : mma_blocks_per_sm(p.mb, a.cache.dim, a.cache.int8) * a.sm_count;
+    const AttnWs w = attn_layout(rows, p.a.n_seq, p.a.cache.dim, p.mb, most_blocks);
+    p.head = reinterpret_cast<AttnHeader*>(ws + w.head);
+    p.item_off = reinterpret_cast<int32_t*>(ws + w.item_off);
+    p.items = reinterpret_cast<AttnItem*>(ws + w.items);
+    p.joins = reinterpret_cast<AttnJoin*>(ws + w.joins);
+    p.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+    p.part_o = reinterpret_cast<float*>(ws + w.o);
+    ws += w.total;
+}
+
+static void launch_join(cudaError_t& err, const AttnParams& p, bool chunk, cudaStream_t stream)
+{
+    const dim3 grid(static_cast<unsigned>(p.blocks > 1 ? p.blocks - 1 : 1), p.mb / (kJoinThreads / 32));
+    const auto join = p.a.cache.dim == 128 ? chunk ? attn_join_kernel<128, 4> : attn_join_kernel<128, 16>
+                                           : chunk ? attn_join_kernel<64, 4> : attn_join_kernel<64, 16>;
+    launch_dep(err, join, grid, dim3(kJoinThreads), 0, stream, p);
+}
+
+// Chunks: the items' list, the kernel, the join.
+static void launch_chunks(cudaError_t& err, AttnParams p, char*& ws, cudaStream_t stream)
+{
+    const int dim = p.a.cache.dim, most = chunk_max_blocks(dim);
+    p.tile = kChunkTile;
+    p.mb = chunk_rows(dim);
+    p.blocks = p.a.sm_count * 256 / p.mb;  // (a pair of CTAs for 512 rows)
     if (p.blocks > most) p.blocks = most;
+    attn_take_workspace(p, p.a.T * p.G, most, ws);
+    launch_dep(err, attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
+    if (err == cudaSuccess) err = launch_attention_chunk(p, stream);
+    launch_join(err, p, true, stream);
+}
+
+// Few rows a sequence.
+static void launch_few_rows(cudaError_t& err, AttnParams p, int rows, bool deal, char*& ws, cudaStream_t stream)
+{
+    const AttentionArgs& a = p.a;
+    p.tile = kMmaTile;
+    p.mb = rows > 8 ? kMmaMaxRows : 8;
+    p.blocks = mma_blocks_per_sm(p.mb, a.cache.dim, a.cache.int8) * a.sm_count;
+    if (p.blocks > kAttnMaxBlocks) p.blocks = kAttnMaxBlocks;
     // Short caches, or few: a cluster of up to 8 blocks for each (sequence,
     // head), which needs no deal and no second launch.  (cap is the longest
     // cache as far as the page table's width says; 64/8 heads, bf16, pages of
@@ -1235,29 +1265,48 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream)
     // and 8.7.  Blocks of more than 1024 keys are too uneven for what they
     // save; a block alone wins up to 512, or 1024 where there are many.
     const int64_t cap = a.max_pages * a.cache.page, pairs = a.n_seq * a.cache.n_kv;
-    if (!chunk) {
+    if (!deal) {
         int c = 1;
-        while (c < 8 && pairs * 2 * c <= 2 * a.sm_count && cap > (pairs * 2 * c <= a.sm_count ? 128 : 256) * c) c *= 2;
+        const auto keys = [&] { return pairs * 2 * c <= a.sm_count ? 128 : 256; };  // a block's, where doubling pays
+        while (c < 8 && pairs * 2 * c <= 2 * a.sm_count && cap > keys() * c) c *= 2;
         const int64_t most_keys = c > 1 || pairs >= 64 ? 1024 : 512;
         if (cap <= most_keys * c && pairs * c <= INT32_MAX) p.whole = c;
     }
     if (p.whole) p.blocks = static_cast<int>(pairs) * p.whole;
-    const AttnWs w = attn_layout(a.T, a.n_seq, p.G, a.cache.dim, p.mb, most);
+    attn_take_workspace(p, 0, kAttnMaxBlocks, ws);
+    if (err == cudaSuccess) err = launch_attention_mma(p, stream);
+    if (!p.whole) launch_join(err, p, false, stream);
+}
+
+cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream)
+{
+    if (a.T == 0 || a.n_seq == 0) return cudaSuccess;
+    AttnParams p{};
+    p.a = a;
+    p.G = a.n_q / a.cache.n_kv;
+    p.rows_upto = INT32_MAX;
     char* ws = static_cast<char*>(a.ws);
-    p.head = reinterpret_cast<AttnHeader*>(ws + w.head);
-    p.item_off = reinterpret_cast<int32_t*>(ws + w.item_off);
-    p.items = reinterpret_cast<AttnItem*>(ws + w.items);
-    p.joins = reinterpret_cast<AttnJoin*>(ws + w.joins);
-    p.part_ml = reinterpret_cast<float2*>(ws + w.ml);
-    p.part_o = reinterpret_cast<float*>(ws + w.o);
     cudaError_t err = cudaSuccess;
-    if (chunk) launch_dep(err, attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
-    if (err == cudaSuccess) err = chunk ? launch_attention_chunk(p, stream) : launch_attention_mma(p, stream);
-    if (p.whole) return err;
-    const dim3 grid(static_cast<unsigned>(p.blocks > 1 ? p.blocks - 1 : 1), p.mb / (kJoinThreads / 32));
-    const auto join = a.cache.dim == 128 ? chunk ? attn_join_kernel<128, 4> : attn_join_kernel<128, 16>
-                                         : chunk ? attn_join_kernel<64, 4> : attn_join_kernel<64, 16>;
-    launch_dep(err, join, grid, dim3(kJoinThreads), 0, stream, p);
+    const int64_t rows = a.max_new * p.G;  // of a sequence, as far as the host knows
+    if (rows <= kMmaMaxRows) {
+        launch_few_rows(err, p, static_cast<int>(rows), false, ws, stream);
+        return err;
+    }
+    // A batch that mixes chunks with decode steps: the sequences of up to 16
+    // rows take the kernel for few rows, in a launch of its own, since a tile
+    // of the other has 128 rows or more (a chunk of 512 tokens and m single
+    // ones over 4000 keys, 64/8 heads, us apart / together: bf16 m = 1 88 / 77,
+    // 7 108 / 108, 31 168 / 218; int8 109 / 101, 122 / 143, 157 / 302).  Not
+    // where the number of tokens says that all sequences have max_new, nor for
+    // few sequences, nor for chunks so small that the launch costs too much.
+    const bool split = rows >= 128 && a.n_seq >= 4 && a.T < a.n_seq * a.max_new;
+    if (split) p.rows_above = kMmaMaxRows;
+    launch_chunks(err, p, ws, stream);
+    if (split) {
+        p.rows_above = 0;
+        p.rows_upto = kMmaMaxRows;
+        launch_few_rows(err, p, p.G <= 8 ? 8 : kMmaMaxRows, true, ws, stream);
+    }
     return err;
 }
 

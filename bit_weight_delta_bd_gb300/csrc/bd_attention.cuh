@@ -30,7 +30,6 @@
 namespace bd {
 
 constexpr int kAttnMaxBlocks = 456;       // blocks of a launch at most: three for each of 152 SMs
-constexpr int kAttnMaxChunkBlocks = 152;  // chunks: one
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -59,6 +58,7 @@ struct AttnParams {
     int G;                // query heads of a kv head
     int tile, mb;         // keys per tile, rows per item
     int blocks;           // N
+    int rows_above, rows_upto;  // sequences with no more, or more, rows than these are another launch's
     int whole;            // a cluster of so many blocks for each (sequence, head), and no deal (decode kernel); or 0
     AttnHeader* head;
     AttnItem* items;
@@ -90,6 +90,15 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttentionArgs& a, int s, bool 
     r.q0 = static_cast<int>(q0);
     r.n_new = static_cast<int>(q1 - q0);
     r.len = static_cast<int>(len);
+    return r;
+}
+
+// The same, without new tokens where the sequence is another launch's.
+__device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int s, bool report)
+{
+    AttnSeq r = attn_seq(p.a, s, report);
+    const int64_t rows = static_cast<int64_t>(r.n_new) * p.G;
+    if (rows <= p.rows_above || rows > p.rows_upto) r.n_new = 0;
     return r;
 }
 
@@ -188,9 +197,11 @@ __device__ __forceinline__ float attn_lse(float m, float l) { return l == 0.0f ?
 
 // Few rows per sequence (bd_attention.cu): 8 or 16 rows an item, 64 keys a tile.
 cudaError_t launch_attention_mma(const AttnParams& p, cudaStream_t stream);
-// Chunks (bd_attention_chunk.cu): 256 rows an item, 128 keys a tile.
+// Chunks (bd_attention_chunk.cu): 256 or 512 rows an item, 128 keys a tile.
 cudaError_t launch_attention_chunk(const AttnParams& p, cudaStream_t stream);
 constexpr int kChunkTile = 128;
+// CTA pairs (512 rows an item) where a half of V's dims fills 128-byte rows
 constexpr int chunk_rows(int dim) { return dim == 128 ? 512 : 256; }
+constexpr int chunk_max_blocks(int dim) { return dim == 128 ? 76 : 152; }  // of the deal: pairs, or CTAs
 
 }  // namespace bd

@@ -387,7 +387,7 @@ struct Walk {
         s.t0 = static_cast<int>(rel - static_cast<int64_t>(s.h) * s.it.tiles);
         const int64_t left = end - u;
         s.t1 = left < s.it.tiles - s.t0 ? s.t0 + static_cast<int>(left) : s.it.tiles;
-        s.sq = attn_seq(p.a, s.it.seq, false);
+        s.sq = attn_seq(p, s.it.seq, false);
         s.rows = s.sq.n_new * p.G - s.it.row0;
         u += s.t1 - s.t0;
         if (s.t1 == s.it.tiles && s.h == n_kv - 1) ++item;
@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
             const int64_t first = static_cast<int64_t>(it.before) * n_kv;
             const int h = attn_div(walk.u - first, it.tiles);
             j = attn_join_of(units, active, c, walk.u, first + static_cast<int64_t>(h) * it.tiles, it.tiles,
-                             attn_seq(a, it.seq, false), p.G, it.row0, h);
+                             attn_seq(p, it.seq, false), p.G, it.row0, h);
         }
         p.joins[c] = j;
     }
