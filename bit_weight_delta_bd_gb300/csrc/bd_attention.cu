@@ -373,7 +373,8 @@ __device__ __forceinline__ bool mbar_wait_cluster_bounded(uint64_t* bar, uint32_
 
 __device__ __forceinline__ void st_cluster_v4(uint32_t addr, float4 v)
 {
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z),
+                 "f"(v.w)
                  : "memory");
 }
 
@@ -479,7 +480,10 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kMmaConsumers) : "memory"); }
+__device__ __forceinline__ void consumers_sync()
+{
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kMmaConsumers) : "memory");
+}
 
 // Byte offset of 16-byte chunk c of row t in a box of 128- or 64-byte rows
 // (TMA's 128- or 64-byte swizzle).
@@ -1192,11 +1196,13 @@ cudaError_t launch_attention_mma(const AttnParams& p, cudaStream_t stream)
         return p.whole ? launch_mma_shape<kDim, kInt8, 2, true>(p, stream)
                        : launch_mma_shape<kDim, kInt8, 2, false>(p, stream);
     };
+    using Dim64 = std::integral_constant<int, 64>;
+    using Dim128 = std::integral_constant<int, 128>;
     using Yes = std::true_type;
     using No = std::false_type;
     if (p.a.cache.dim == 128)
-        return p.a.cache.int8 ? of(std::integral_constant<int, 128>{}, Yes{}) : of(std::integral_constant<int, 128>{}, No{});
-    return p.a.cache.int8 ? of(std::integral_constant<int, 64>{}, Yes{}) : of(std::integral_constant<int, 64>{}, No{});
+        return p.a.cache.int8 ? of(Dim128{}, Yes{}) : of(Dim128{}, No{});
+    return p.a.cache.int8 ? of(Dim64{}, Yes{}) : of(Dim64{}, No{});
 }
 
 size_t attention_workspace_size(int64_t T, int64_t n_seq, int n_q, int n_kv, int dim)

@@ -120,7 +120,8 @@ __device__ __forceinline__ int attn_active(int64_t units, int blocks)
 constexpr int64_t kAttnFewUnits = 0xFFFFFFFFll / (kAttnMaxBlocks + 1) - 1;
 __device__ __forceinline__ int64_t attn_first(int64_t units, int n, int c)
 {
-    if (units < kAttnFewUnits) return static_cast<uint32_t>(units) * static_cast<uint32_t>(c) / static_cast<uint32_t>(n);
+    if (units < kAttnFewUnits)
+        return static_cast<uint32_t>(units) * static_cast<uint32_t>(c) / static_cast<uint32_t>(n);
     return units * c / n;
 }
 // The block that takes unit u: the last c with attn_first(c) <= u.
@@ -172,7 +173,7 @@ __device__ __forceinline__ int attn_find_item(const AttnItem* items, int n_items
 __device__ __forceinline__ int attn_slot(int c, bool from_start) { return 2 * c + (from_start ? 1 : 0); }
 
 // Probabilities are formed as exp2(score - maximum + bias): what is far below
-// the maximum stays a normal number when it is rounded to bf16, after the
+// the maximum stays a normal number when it is rounded to 16 bits, after the
 // product with an int8 value's scale too.  Numerator and denominator carry
 // the same factor; a stored maximum is the one less the bias.  (Sums overflow
 // only for values above 2^80.)

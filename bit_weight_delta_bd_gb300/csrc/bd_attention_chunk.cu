@@ -1,9 +1,9 @@
 // Attention over the paged KV cache for chunks of new tokens, on the tcgen05
 // tensor cores (the formulas and the dealing of the work: bd_attention.cuh).
 //
-// An item is 256 query rows (two tiles of 128) of one kv head; its keys are
-// read in tiles of 128 by TMA and multiplied in steps of 64.  Per step and
-// query tile
+// An item is 256 query rows of one kv head for each CTA (two query tiles of
+// 128); its keys are read in tiles of 128 by TMA and multiplied in steps of 64.
+// Per step and query tile
 //   S = Q K^T       128 x 64, operands in shared memory, fp32 in tensor memory
 //   P = exp2(c S - m)   one thread per row: maximum, probabilities, denominator
 //   O += P V        P as bf16 in tensor memory (over S), V in shared memory
@@ -11,8 +11,18 @@
 // done and neither the tensor cores nor the exponentials wait for the other:
 // with one place of 128 keys a query tile's products and exponentials took
 // turns, 3350 cycles for 128 keys and 256 rows of which the tensor cores
-// worked 2300.  (A step of 64 reads Q from shared memory twice as often; the
-// product S is then bound by those reads, at 3/4 of its rate.)
+// worked 2300.
+//
+// Pairs.  With head_dim 128 two CTAs work on an item of 512 rows: the even
+// one's products cover both (M = 256), and each holds half of the operand that
+// they share, 32 keys of each step of K and 64 dims of V.  What bounds a single
+// CTA is its shared memory (a step of 64 reads Q twice as often as one of 128
+// would, and the 64-key product then runs at 3/4 of its rate); a pair reads 3/4
+// of that, and int8 tiles are converted once for 512 rows.  A chunk of 4096
+// tokens over 8192 keys, 64/8 heads: bf16 885 -> 812 us, 1694 TFLOP/s; int8
+// 1245 -> 1110 us.  With head_dim 64 half of V's dims would leave 64-byte rows,
+// and the exponentials bound the kernel: single CTAs, 715 us for bf16.
+//
 // The running maximum that P is formed with lags behind the true one by at
 // most 2^8 (a row's sums are rescaled in tensor memory only when its maximum
 // grew by more than 8 in units of log2; the fp32 sums have room for that
@@ -21,15 +31,21 @@
 // step j + 2.
 //
 // Int8 keys and values: TMA brings the codes, a fourth warpgroup turns them
-// into tiles of numbers (exactly: K to fp16 and V to bf16), once for both
+// into tiles of numbers (exactly: K to fp16 and V to bf16), once for all
 // query tiles; the scales multiply S and P in the softmax's registers.  Q
 // enters that product in fp16, scaled by a power of two per row, as in the
 // decode kernel; P stays bf16, whose range the sums of a row's smallest
 // probabilities need.  Within each group of four dims the tiles hold them in
-// the order 0, 2, 1, 3, in which the codes come out of a register.
+// the order 0, 2, 1, 3, in which the codes come out of a register.  The
+// softmax bounds this kernel: without its reads of the scales (32 of 16 bytes
+// per step and warp, in the way of the products' operands) and the conversion
+// it would take 934 us, and without the softmax 757.  (Four lanes to a row, a
+// quarter of the scales each, shuffles for the maximum: 1260 us; two warpgroups
+// to a row: slower as well.)
 //
 // Warps: 0..3 and 4..7 softmax of query tiles 0 and 1 (and loading Q, and
-// writing O); 8 TMA; 9 and 10 MMA of query tiles 0 and 1; 12..15 conversion
+// writing O); 8 TMA; 9 and 10 MMA of query tiles 0 and 1 (of a pair: the even
+// CTA's); 11 passes on that a pair's bf16 tiles have landed; 12..15 conversion
 // (int8).
 #include <cuda_fp16.h>
 
@@ -48,7 +64,9 @@ constexpr int kStep = 64;        // keys of a step
 constexpr float kLag = 8.0f;     // how far (log2) a row's maximum may run ahead of the one in use
 
 struct ChunkParams {
-    CUtensorMap k_map, v_map;  // [n_pages * n_kv][page][dim]; bf16: box 64 x page rows, 128-byte swizzle; int8: box dim x page rows
+    // [n_pages * n_kv][page][dim]; boxes of 128 bytes (int8 V of a pair, and head_dim 64: 64) x page rows, K of a
+    // pair up to 32
+    CUtensorMap k_map, v_map;
     AttnParams p;
 };
 
@@ -334,6 +352,7 @@ __device__ __forceinline__ uint2 codes4(uint32_t r)  // in the order 0, 2, 1, 3
 // rows: the lowest) that put both their reads from TMA's swizzled tile of
 // codes and their writes to the swizzled tile of numbers into different banks.
 // Later chunks of a thread lie 16 (32) keys on, at the same place of the swizzle.
+// DIM: codes of a row; KEYS: rows of the tile.
 template <int DIM, int KEYS, bool HALF>
 __device__ __forceinline__ void convert_tile(const uint8_t* src, uint8_t* dst, int tid)
 {
@@ -432,9 +451,9 @@ __device__ __forceinline__ float unit_of(float x)
     return __uint_as_float(__float_as_uint(fminf(fmaxf(x, 7.9e-31f), 1.2e30f)) & 0x7F800000u);
 }
 
-// A warp's 32 rows, from row r0 on, of the query tile that starts at the item's row tile_row, into shared
-// memory (K-major, 128-byte swizzle, halves of 64 dims); rows past the item
-// are zeros.  Neighbouring lanes take neighbouring 16 bytes, eight loads in
+// A warp's 32 rows, from row r0 on, of the query tile that starts at the
+// item's row tile_row, into shared memory (K-major, 128-byte swizzle, halves
+// of 64 dims); rows past the item are zeros.  Neighbouring lanes take neighbouring 16 bytes, eight loads in
 // flight (a row per lane, two in flight, cost 6 us per item, and twice that
 // where int8 looked for the maximum first).  A negative scale is taken into
 // Q's sign; int8: fp16, over the row's power of two, dims in the codes' order.
@@ -890,7 +909,8 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
             // ---------------------------------------------------- MMA of query tile i
             constexpr int kRows = kQRows * S::kCtas;
             constexpr uint32_t kIdescS = INT8 ? idesc_f16_f32(kRows, kStep) : idesc_bf16_f32(kRows, kStep);
-            constexpr uint32_t kIdescO = idesc_bf16_f32(kRows, DIM) | (1u << 16);  // V: rows along the contracted index
+            // V: rows along the contracted index
+            constexpr uint32_t kIdescO = idesc_bf16_f32(kRows, DIM) | (1u << 16);
             const int i = warp - kMmaWarp;
             const uint32_t q_addr = smem_u32(dyn + i * S::kQBytes), buf_addr = smem_u32(dyn + S::kOffBufs);
             const uint32_t ts = tmem + i * 128, to = tmem + kTmemO + i * DIM;
