@@ -414,7 +414,9 @@ bd_status bd_kv_read(const bd_kv_pages* cache, const int32_t* page_table, int64_
  *            host knows it; it chooses the kernel, never the result's meaning
  *   page_table, max_pages  as in bd_kv_read; pages past a sequence's length
  *            are not looked at, and what the cache holds past the length
- *            (NaN included) has no influence
+ *            (NaN included) has no influence.  Of keys that a causal row does
+ *            not see, v has to be finite: products run over whole tiles, and
+ *            0 * NaN is NaN.
  *   kv_len   device int32 [n_seq]
  *   out      device bf16 [T][n_q][head_dim], 16-byte aligned
  *   lse      device fp32 [T][n_q] or NULL: log sum_j exp(scale * q . k_j)
