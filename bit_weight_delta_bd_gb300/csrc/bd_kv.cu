@@ -12,8 +12,7 @@
 namespace bd {
 namespace {
 
-constexpr int kRopeThreads = 64;  // of a block at most
-constexpr int kRopeAhead = 2;     // heads that a thread loads before it works on the first
+constexpr int rope_threads(bool int8) { return int8 ? 64 : 32; }  // of a block at most
 constexpr int kUnit = 16;  // elements of a head that one thread handles
 
 __device__ __forceinline__ void unpack8(uint4 u, float* f)
@@ -68,14 +67,19 @@ struct RopeParams {
 // a block is one token (grid x) and one part of its heads (grid y), blockDim /
 // UPH heads a pass.  What bounds it is how many tokens an SM works on at a
 // time, since each waits for its position, then its table row, then its heads:
-// small blocks, and the heads of the first two passes loaded before the
-// position is there.  4096 tokens, 64/8 heads of 128, bf16: 30.5 us, 5.6 TB/s
-// (256 threads and three passes ahead 37.9, 128 threads and the position first
-// 33.2); int8 32.4 us.
+// small blocks, a head's successor loaded before it is worked on, and the first
+// heads before the position is there.  One head ahead, or two where codes are
+// formed, since more registers leave fewer blocks.  4096 tokens, 64/8 heads of
+// 128: bf16 29.9 us, 5.7 TB/s, with 32 threads (64 threads 30.0, with two ahead
+// 34.0, three 38.5; 256 threads 37.9; the position first 33.2), and 5 ragged
+// prompts of up to 1201 tokens, 48 heads of 64, 11.6 us (64 threads 12.5);
+// int8 and read back 37.9 us with 64 threads (32 threads 45.6; one ahead 39.5;
+// loads only after the work on those before 40.5).
 template <int UPH, bool INT8>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeParams p)
+__global__ void __launch_bounds__(rope_threads(INT8)) rope_append_kernel(const __grid_constant__ RopeParams p)
 {
     constexpr int kDim = UPH * kUnit;
+    constexpr int kAhead = INT8 ? 2 : 1;  // heads that a thread has loaded, or is loading
     const RopeArgs& a = p.a;
     const int u = threadIdx.x % UPH;
     const int64_t t = blockIdx.x;
@@ -91,7 +95,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
     const int first = turns && !a.interleaved ? 8 * u : 16 * u;
     const int second = turns && !a.interleaved ? 8 * u + a.rot / 2 : 16 * u + 8;
 
-    uint4 raw[kRopeAhead][2];
+    uint4 raw[kAhead][2];
     const auto load = [&](int h, uint4 (&to)[2]) {
         if (h >= heads) return;
         const bool is_v = h >= a.n_q + n_kv;
@@ -103,7 +107,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
     };
     const int head0 = blockIdx.y * per_pass + threadIdx.x / UPH;
 #pragma unroll
-    for (int i = 0; i < kRopeAhead; ++i) load(head0 + i * step, raw[i]);
+    for (int i = 0; i < kAhead; ++i) load(head0 + i * step, raw[i]);
 
     float c[8], s[8];
     if (turns) {
@@ -194,15 +198,15 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
             }
         }
     };
-    for (int h0 = blockIdx.y * per_pass; h0 < heads; h0 += kRopeAhead * step) {
+    for (int h0 = blockIdx.y * per_pass; h0 < heads; h0 += kAhead * step) {
         const int h = h0 + threadIdx.x / UPH;
-        if (h0 != static_cast<int>(blockIdx.y) * per_pass) {
 #pragma unroll
-            for (int i = 0; i < kRopeAhead; ++i) load(h + i * step, raw[i]);
+        for (int i = 0; i < kAhead; ++i) {
+            if (h0 + i * step >= heads) break;
+            const uint4 now[2] = {raw[i][0], raw[i][1]};
+            load(h + (i + kAhead) * step, raw[i]);
+            work(h + i * step, now);
         }
-#pragma unroll
-        for (int i = 0; i < kRopeAhead; ++i)
-            if (h0 + i * step < heads) work(h + i * step, raw[i]);
     }
 }
 
@@ -217,7 +221,8 @@ struct KvReadParams {
 
 // A block gathers kReadRows consecutive output rows: their places in the
 // cache are looked up first (a binary search in kv_off per row), then all
-// threads copy units of 16 elements.
+// threads copy units of 16 elements, two at a time: 8 sequences of up to 8192
+// int8 tokens, 8 heads of 128, in 48.3 us, 6.1 TB/s (51.6 one at a time).
 template <int UPH, bool INT8>
 __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const __grid_constant__ KvReadParams p)
 {
@@ -259,34 +264,48 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const __grid_cons
     const void* pool = is_v ? a.cache.v : a.cache.k;
     const float* scales = is_v ? a.cache.v_scale : a.cache.k_scale;
     uint16_t* out = is_v ? a.v_out : a.k_out;
-    for (int i = threadIdx.x; i < kReadRows * per_row; i += kReadThreads) {
-        const int r = i / per_row, j = i - r * per_row;
-        const int64_t b = base[r];
-        if (b == -2) continue;
-        const int h = j / UPH, u = j % UPH;
-        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-        const int64_t vec = b + (static_cast<int64_t>(h) << a.cache.page_shift);
-        if (b >= 0 && bd_in(kBkKvRead, vec, vecs)) {
+    // two units at a time: both loads before either is converted
+    const int units = kReadRows * per_row;
+    for (int i0 = threadIdx.x; i0 < units; i0 += 2 * kReadThreads) {
+        uint4 lo[2], hi[2];
+        float scale[2];
+        int64_t to[2];  // of the output, or -1
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int i = i0 + k * kReadThreads;
+            const int r = i / per_row, j = i - r * per_row;
+            const int64_t b = i < units ? base[r] : -2;
+            const int h = j / UPH, u = j % UPH;
+            to[k] = b == -2 ? -1 : ((row0 + r) * a.cache.n_kv + h) * kDim + 16 * u;
+            lo[k] = hi[k] = make_uint4(0, 0, 0, 0);
+            scale[k] = 0.0f;
+            const int64_t vec = b + (static_cast<int64_t>(h) << a.cache.page_shift);
+            if (b >= 0 && bd_in(kBkKvRead, vec, vecs)) {
+                if constexpr (INT8) {
+                    lo[k] = ld_stream_v4(static_cast<const uint8_t*>(pool) + vec * kDim + 16 * u);
+                    scale[k] = __ldg(scales + vec);
+                } else {
+                    const uint16_t* src = static_cast<const uint16_t*>(pool) + vec * kDim + 16 * u;
+                    lo[k] = ld_stream_v4(src);
+                    hi[k] = ld_stream_v4(src + 8);
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (to[k] < 0 || !bd_in_range(kBkKvRead, to[k], 16, a.rows * a.cache.n_kv * kDim)) continue;
             if constexpr (INT8) {
-                const uint4 w = ld_stream_v4(static_cast<const uint8_t*>(pool) + vec * kDim + 16 * u);
-                const float scale = __ldg(scales + vec);
-                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+                const uint32_t ww[4] = {lo[k].x, lo[k].y, lo[k].z, lo[k].w};
                 float f[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    f[e] = static_cast<float>(static_cast<int8_t>(ww[e / 4] >> (8 * (e % 4)))) * scale;
-                lo = pack8(f);
-                hi = pack8(f + 8);
-            } else {
-                const uint16_t* src = static_cast<const uint16_t*>(pool) + vec * kDim + 16 * u;
-                lo = ld_stream_v4(src);
-                hi = ld_stream_v4(src + 8);
+                    f[e] = static_cast<float>(static_cast<int8_t>(ww[e / 4] >> (8 * (e % 4)))) * scale[k];
+                lo[k] = pack8(f);
+                hi[k] = pack8(f + 8);
             }
-        }
-        uint16_t* dst = out + ((row0 + r) * a.cache.n_kv + h) * kDim + 16 * u;
-        if (bd_in_range(kBkKvRead, dst - out, 16, a.rows * a.cache.n_kv * kDim)) {
-            *reinterpret_cast<uint4*>(dst) = lo;
-            *reinterpret_cast<uint4*>(dst + 8) = hi;
+            uint16_t* dst = out + to[k];
+            *reinterpret_cast<uint4*>(dst) = lo[k];
+            *reinterpret_cast<uint4*>(dst + 8) = hi[k];
         }
     }
 }
@@ -297,9 +316,9 @@ cudaError_t launch_rope_append(const RopeArgs& a, int sm_count, cudaStream_t str
 {
     if (a.T == 0) return cudaSuccess;
     RopeParams p{a};
-    // as few passes as 64 threads allow, all about equally full
+    // as few passes as so many threads allow, all about equally full
     const int uph = a.cache.dim / kUnit, heads = a.n_q + 2 * a.cache.n_kv;
-    const int most = kRopeThreads / uph;
+    const int most = rope_threads(a.cache.int8) / uph;
     const int passes = (heads + most - 1) / most, per_pass = (heads + passes - 1) / passes;
     const int threads = (per_pass * uph + 31) / 32 * 32;
     // few tokens: the passes of a token are split over blocks until the GPU has about 8 blocks per SM
