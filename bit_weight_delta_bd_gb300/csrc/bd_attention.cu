@@ -23,14 +23,18 @@
 //
 // Int8.  Both products run in fp16, which holds the codes exactly: with u =
 // code + 128 the bits 0x6400 | u are 1024 + u, and one logic operation and
-// one packed addition give two codes (bf16, whose 8 bits have no room for u,
-// takes twice as many).  q is scaled per row by the power of two that brings
-// its largest element to 2^14 .. 2^15: its bf16 values are then exact in fp16
-// down to 2^-29 of that element.  K's scale multiplies the fp32 score.  V's
-// scale multiplies the fp32 probability, and the product enters fp16 over a
-// power of two that follows the largest scale seen, so that it stays below
-// 2^15 and what is rounded away lies 2^-40 below the largest.  Probabilities
-// so keep 11 bits, where a bf16 cache's, rounded to bf16 like its values, keep 8.
+// one packed addition give two codes.  q is scaled per row by the power of two
+// that brings its largest element to 2^14 .. 2^15: its bf16 values are then
+// exact in fp16 down to 2^-29 of that element.  K's scale multiplies the fp32
+// score.  V's scale multiplies the fp32 probability, and the product enters
+// fp16 over a power of two that follows the largest scale seen, so that it
+// stays below 2^15, with 11 bits where a bf16 cache's probabilities, rounded
+// to bf16 like its values, have 8.  A step with a product below 2^-14, where
+// fp16 loses bits, runs P V in bf16 instead (a dim in which the likeliest keys'
+// codes are 0 takes its value from the others, however small they are); that
+// takes a logic operation more for two codes: 92.5 us where all steps do, 88.6
+// where none does (4 sequences of up to 65538 keys, 64/8 heads; 86.7 without
+// the test).
 
 #include "bd_attention.cuh"
 
@@ -421,9 +425,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x)
     return y;
 }
 
-template <bool HALF>
-__device__ __forceinline__ uint32_t pack16x2(float lo, float hi);
-
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
 {
     const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
@@ -446,15 +447,17 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-template <>
-__device__ __forceinline__ uint32_t pack16x2<true>(float lo, float hi)
+constexpr uint32_t kFp16Normal = 0x38800000u;  // the bits of 2^-14
+
+// Two int8 codes as a pair of bf16, which have no room for 128 + code: with c
+// the byte, 0x4300 | (c & 0x7f) is 128 + (c & 0x7f), 0x4300 | (c & 0x80) is 128
+// or 256, and the difference is the code.
+__device__ __forceinline__ uint32_t codes_bf16x2(uint32_t r)
 {
-    return pack_f16x2(lo, hi);
-}
-template <>
-__device__ __forceinline__ uint32_t pack16x2<false>(float lo, float hi)
-{
-    return pack_bf16x2(lo, hi);
+    const uint32_t hi = (r & 0x007F007Fu) | 0x43004300u, lo = (r & 0x00800080u) | 0x43004300u;
+    const __nv_bfloat162 d =
+        __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&hi), *reinterpret_cast<const __nv_bfloat162*>(&lo));
+    return *reinterpret_cast<const uint32_t*>(&d);
 }
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -844,6 +847,8 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
 
             // ---- probabilities, turned into B fragments: keys 16 b + 8 j + 2 q4 + {0, 1} of row 8 n + g
             uint32_t pb[NT][2][2];
+            [[maybe_unused]] float pw[NT][2][4];  // int8: what is to be rounded
+            [[maybe_unused]] uint32_t least = 0xFFFFFFFFu;  // the least of it that is not 0: its bits less 1
             const float v_inv = INT8 ? (v_unit > 0.0f ? 1.0f / v_unit : 0.0f) : 1.0f;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -857,18 +862,39 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
                         const float p0 = ex2(s[n][b][2 * j] - mu[0]), p1 = ex2(s[n][b][2 * j + 1] - mu[1]);
                         l[n][0] += p0;
                         l[n][1] += p1;
-                        const float w = INT8 ? vs[b][j] * v_inv : 1.0f;
-                        pb[n][b][j] = transpose8(INT8 ? pack16x2<INT8>(p0 * w, p1 * w) : pack16x2<INT8>(p0, p1));
+                        if constexpr (INT8) {
+                            const float w = vs[b][j] * v_inv;
+                            pw[n][b][2 * j] = p0 * w, pw[n][b][2 * j + 1] = p1 * w;
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                least = min(least, __float_as_uint(pw[n][b][2 * j + e]) - 1u);
+                        } else {
+                            pb[n][b][j] = transpose8(pack_bf16x2(p0, p1));
+                        }
                     }
+            }
+
+            [[maybe_unused]] bool low = false;  // some of it would lose bits in fp16
+            if constexpr (INT8) {
+                low = __any_sync(0xffffffffu, least < kFp16Normal);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float x = pw[n][b][2 * j], y = pw[n][b][2 * j + 1];
+                            pb[n][b][j] = transpose8(low ? pack_bf16x2(x, y) : pack_f16x2(x, y));
+                        }
             }
 
             // ---- sums: dim x 8 NT rows += V^T (dim x 32) P^T (32 x 8 NT)
             const uint32_t vt = st + S::kTileBytes;
+            // a b16 element is a pair of dims: the transposed fragment holds dims 2 g, 2 g + 1 of two keys;
+            // the tile's rows 0..7 take the even dims of a chunk, rows 8..15 the odd ones
+            [[maybe_unused]] const auto add_codes = [&](auto as_bf16) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                if constexpr (INT8) {
-                    // a b16 element is a pair of dims: the transposed fragment holds dims 2 g, 2 g + 1 of
-                    // two keys; the tile's rows 0..7 take the even dims of a chunk, rows 8..15 the odd ones
+                for (int b = 0; b < 2; ++b) {
                     const int row = slice + 16 * b + (mi & 1) * 8 + mr;
 #pragma unroll
                     for (int k = 0; k < kSteps; k += 2) {
@@ -876,14 +902,29 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
                         ldsm_x4_t(vt + swizzled<S::kBoxBytes>(row, k + (mi >> 1)), r);
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            const uint32_t a0 = codes_f16x2(r[2 * x]), a1 = codes_f16x2(r[2 * x] >> 8);
-                            const uint32_t a2 = codes_f16x2(r[2 * x + 1]), a3 = codes_f16x2(r[2 * x + 1] >> 8);
+                            if constexpr (decltype(as_bf16)::value) {
+                                const uint32_t a0 = codes_bf16x2(r[2 * x]), a1 = codes_bf16x2(r[2 * x] >> 8);
+                                const uint32_t a2 = codes_bf16x2(r[2 * x + 1]), a3 = codes_bf16x2(r[2 * x + 1] >> 8);
 #pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                mma_f16_16816(o[n][k + x], a0, a1, a2, a3, pb[n][b][0], pb[n][b][1]);
+                                for (int n = 0; n < NT; ++n)
+                                    mma_bf16_16816(o[n][k + x], a0, a1, a2, a3, pb[n][b][0], pb[n][b][1]);
+                            } else {
+                                const uint32_t a0 = codes_f16x2(r[2 * x]), a1 = codes_f16x2(r[2 * x] >> 8);
+                                const uint32_t a2 = codes_f16x2(r[2 * x + 1]), a3 = codes_f16x2(r[2 * x + 1] >> 8);
+#pragma unroll
+                                for (int n = 0; n < NT; ++n)
+                                    mma_f16_16816(o[n][k + x], a0, a1, a2, a3, pb[n][b][0], pb[n][b][1]);
+                            }
                         }
                     }
-                } else {
+                }
+            };
+            if constexpr (INT8) {
+                if (low) add_codes(std::true_type{});
+                else add_codes(std::false_type{});
+            } else {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
                     uint32_t mask0 = 0xFFFFFFFFu, mask1 = 0xFFFFFFFFu;
                     if (tail) {
                         // zeros for what lies past the sequence
@@ -1210,7 +1251,7 @@ size_t attention_workspace_size(int64_t T, int64_t n_seq, int n_q, int n_kv, int
     // the host may learn how long the chunks are only with the call: room for both kernels
     const int G = n_q / n_kv;
     const size_t few = attn_layout(0, n_seq, dim, kMmaMaxRows, kAttnMaxBlocks).total;
-    const size_t chunk = attn_layout(T * G, n_seq, dim, chunk_rows(dim), chunk_max_blocks(dim)).total;
+    const size_t chunk = attn_layout(T * G, n_seq, dim, kChunkRows, chunk_max_blocks(kChunkRows)).total;
     return few + chunk;
 }
 
@@ -1236,12 +1277,12 @@ static void launch_join(cudaError_t& err, const AttnParams& p, bool chunk, cudaS
 }
 
 // Chunks: the items' list, the kernel, the join.
-static void launch_chunks(cudaError_t& err, AttnParams p, char*& ws, cudaStream_t stream)
+static void launch_chunks(cudaError_t& err, AttnParams p, int64_t rows, char*& ws, cudaStream_t stream)
 {
-    const int dim = p.a.cache.dim, most = chunk_max_blocks(dim);
     p.tile = kChunkTile;
-    p.mb = chunk_rows(dim);
-    p.blocks = p.a.sm_count * 256 / p.mb;  // (a pair of CTAs for 512 rows)
+    p.mb = p.a.cache.dim == 128 && rows > kChunkRows ? kPairRows : kChunkRows;
+    const int most = chunk_max_blocks(p.mb);
+    p.blocks = p.a.sm_count * kChunkRows / p.mb;
     if (p.blocks > most) p.blocks = most;
     attn_take_workspace(p, p.a.T * p.G, most, ws);
     launch_dep(err, attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
@@ -1307,7 +1348,7 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream)
     // few sequences, nor for chunks so small that the launch costs too much.
     const bool split = rows >= 128 && a.n_seq >= 4 && a.T < a.n_seq * a.max_new;
     if (split) p.rows_above = kMmaMaxRows;
-    launch_chunks(err, p, ws, stream);
+    launch_chunks(err, p, rows, ws, stream);
     if (split) {
         p.rows_above = 0;
         p.rows_upto = kMmaMaxRows;

@@ -201,8 +201,8 @@ cudaError_t launch_attention_mma(const AttnParams& p, cudaStream_t stream);
 // Chunks (bd_attention_chunk.cu): 256 or 512 rows an item, 128 keys a tile.
 cudaError_t launch_attention_chunk(const AttnParams& p, cudaStream_t stream);
 constexpr int kChunkTile = 128;
-// CTA pairs (512 rows an item) where a half of V's dims fills 128-byte rows
-constexpr int chunk_rows(int dim) { return dim == 128 ? 512 : 256; }
-constexpr int chunk_max_blocks(int dim) { return dim == 128 ? 76 : 152; }  // of the deal: pairs, or CTAs
+// CTA pairs: 512 rows an item
+constexpr int kChunkRows = 256, kPairRows = 512;
+constexpr int chunk_max_blocks(int rows) { return 152 * kChunkRows / rows; }  // of the deal: CTAs, or pairs
 
 }  // namespace bd

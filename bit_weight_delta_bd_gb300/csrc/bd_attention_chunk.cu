@@ -13,15 +13,18 @@
 // turns, 3350 cycles for 128 keys and 256 rows of which the tensor cores
 // worked 2300.
 //
-// Pairs.  With head_dim 128 two CTAs work on an item of 512 rows: the even
+// Pairs.  With head_dim 128 and more than 256 rows two CTAs work on an item of 512: the even
 // one's products cover both (M = 256), and each holds half of the operand that
 // they share, 32 keys of each step of K and 64 dims of V.  What bounds a single
 // CTA is its shared memory (a step of 64 reads Q twice as often as one of 128
 // would, and the 64-key product then runs at 3/4 of its rate); a pair reads 3/4
 // of that, and int8 tiles are converted once for 512 rows.  A chunk of 4096
 // tokens over 8192 keys, 64/8 heads: bf16 885 -> 812 us, 1694 TFLOP/s; int8
-// 1245 -> 1110 us.  With head_dim 64 half of V's dims would leave 64-byte rows,
-// and the exponentials bound the kernel: single CTAs, 715 us for bf16.
+// 1245 -> 1110 us.  Sequences of up to 256 rows would fill a pair's first query
+// tile at most, which takes as long as both: 8 sequences of 4 tokens over 4000
+// keys take 48 us by single CTAs and 68 by pairs (int8).  With head_dim 64
+// half of V's dims would leave 64-byte rows, and the exponentials bound the
+// kernel: single CTAs, 715 us for bf16.
 //
 // The running maximum that P is formed with lags behind the true one by at
 // most 2^8 (a row's sums are rescaled in tensor memory only when its maximum
@@ -70,14 +73,15 @@ struct ChunkParams {
     AttnParams p;
 };
 
-template <int DIM, bool INT8>
+template <int DIM, bool INT8, bool PAIR>
 struct ChunkShape {
-    static constexpr bool kPair = DIM == 128;
+    static constexpr bool kPair = PAIR;
     static constexpr int kCtas = kPair ? 2 : 1;
     static constexpr int kThreads = INT8 ? 512 : 384;
-    static constexpr int kBufs = INT8 ? (kPair ? 6 : 3) : 8;        // bf16 tiles in shared memory
-    static constexpr int kRaw = INT8 ? (kPair ? 6 : 3) : 0;         // tiles of codes
-    static constexpr int kScaleBufs = INT8 ? (kPair ? 4 : 3) : 0;   // scales of a key tile, K and V
+    static constexpr bool kSmall = PAIR || DIM == 64;  // tiles of 16 KB
+    static constexpr int kBufs = INT8 ? (kSmall ? 6 : 3) : kSmall ? 8 : 5;  // bf16 tiles in shared memory
+    static constexpr int kRaw = INT8 ? (kSmall ? 6 : 3) : 0;                // tiles of codes
+    static constexpr int kScaleBufs = INT8 ? (kSmall ? 4 : 3) : 0;          // scales of a key tile, K and V
     // a CTA's part of a tile: in a pair half the keys of each step of K, half the dims of V
     static constexpr int kKeysK = kTile / kCtas, kDimsV = DIM / kCtas;
     static constexpr int kTileBytes = kTile * DIM * 2 / kCtas;
@@ -250,13 +254,16 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t 
 
 // What lies past the sequence in a tile of V may be anything, NaN included:
 // zeros from key `valid` on instead, so that probabilities of 0 times it stay
-// 0.  (64 dims, which is all of V that a CTA holds.)  By a warp.
+// 0.  DIMS: that the CTA holds.  By a warp.
+template <int DIMS>
 __device__ __forceinline__ void zero_past(uint8_t* v, int valid, int lane)
 {
     if (valid >= kTile) return;
 #pragma unroll 1
     for (int x = (valid > 0 ? valid : 0) * 8 + lane; x < kTile * 8; x += 32)
-        *reinterpret_cast<uint4*>(v + x * 16) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int d = 0; d < DIMS; d += 64)
+            *reinterpret_cast<uint4*>(v + (d / 64) * kTile * 128 + x * 16) = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     __syncwarp();
 }
@@ -509,12 +516,12 @@ __device__ __forceinline__ float load_q(const AttnParams& p, const Segment& s, i
     return back;
 }
 
-template <int DIM, bool INT8>
-__global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
+template <int DIM, bool INT8, bool PAIR>
+__global__ void __launch_bounds__(ChunkShape<DIM, INT8, PAIR>::kThreads, 1)
     attn_chunk_kernel(const __grid_constant__ ChunkParams cp)
 {
-    using S = ChunkShape<DIM, INT8>;
-    constexpr bool kPair = S::kPair;
+    using S = ChunkShape<DIM, INT8, PAIR>;
+    constexpr bool kPair = PAIR;
     extern __shared__ __align__(1024) uint8_t dyn[];
     ChunkShared& sh = *reinterpret_cast<ChunkShared*>(dyn + S::kBytes);
     const AttnParams& p = cp.p;
@@ -889,10 +896,14 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
                         }
                         if (kv == 1 && mine) {
                             const int to = lane * cache.page;
-                            if constexpr (INT8)
+                            if constexpr (INT8) {
                                 tma_load_3d(dst + to * S::kDimsV, &cp.v_map, rank * S::kDimsV, 0, outer, &full[buf]);
-                            else
-                                tma_load_3d(dst + to * 128, &cp.v_map, rank * S::kDimsV, 0, outer, &full[buf]);
+                            } else {
+#pragma unroll
+                                for (int d = 0; d < S::kDimsV; d += 64)
+                                    tma_load_3d(dst + (d / 64) * kTile * 128 + to * 128, &cp.v_map,
+                                                rank * S::kDimsV + d, 0, outer, &full[buf]);
+                            }
                         }
                         if (++buf == kRing) buf = 0, phase ^= 1;
                     }
@@ -945,7 +956,8 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
                     if (pv && b == 0) {
                         bv = take();
                         if constexpr (!INT8 && !kPair) 
-                            zero_past(dyn + S::kOffBufs + bv * S::kTileBytes, s.sq.len - (j - 2) * kStep, lane);
+                            zero_past<S::kDimsV>(dyn + S::kOffBufs + bv * S::kTileBytes,
+                                                 s.sq.len - (j - 2) * kStep, lane);
                     }
                     if (qk && b == 0) bk = take();
                     if (pv) {
@@ -995,7 +1007,9 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
 #pragma unroll 1
                 for (int n = 0; n < 2 * (s.t1 - s.t0); ++n) {  // K and V in turn
                     if (!(ok = warp_wait(&sh.abort, &sh.landed[buf], phase))) break;
-                    if (n & 1) zero_past(dyn + S::kOffBufs + buf * S::kTileBytes, s.sq.len - (s.t0 + n / 2) * kTile, lane);
+                    if (n & 1)
+                        zero_past<S::kDimsV>(dyn + S::kOffBufs + buf * S::kTileBytes,
+                                             s.sq.len - (s.t0 + n / 2) * kTile, lane);
                     if (lane == 0) arrive_even<kPair>(&sh.full[buf]);
                     if (++buf == S::kBufs) buf = 0, phase ^= 1;
                 }
@@ -1040,10 +1054,10 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8>::kThreads, 1)
     }
 }
 
-template <int DIM, bool INT8>
+template <int DIM, bool INT8, bool PAIR>
 cudaError_t launch_chunk_shape(const AttnParams& p, cudaStream_t stream)
 {
-    using S = ChunkShape<DIM, INT8>;
+    using S = ChunkShape<DIM, INT8, PAIR>;
     static std::atomic<size_t> smem_set[kHostMaxDevices];
     const KvPages& kv = p.a.cache;
     ChunkParams cp{};
@@ -1057,7 +1071,7 @@ cudaError_t launch_chunk_shape(const AttnParams& p, cudaStream_t stream)
         !encode_tma_3d(&cp.v_map, type, bytes, kv.v, DIM, kv.page, outer, cols_v, kv.page, swizzle(cols_v * bytes)))
         return cudaErrorInvalidValue;
     constexpr size_t smem = chunk_smem<S>();
-    const void* kernel = reinterpret_cast<const void*>(attn_chunk_kernel<DIM, INT8>);
+    const void* kernel = reinterpret_cast<const void*>(attn_chunk_kernel<DIM, INT8, PAIR>);
     cudaError_t err = ensure_dynamic_smem(kernel, smem, smem_set);
     if (err != cudaSuccess) return err;
     // the warpgroups' register split draws on what the block was launched
@@ -1072,7 +1086,7 @@ cudaError_t launch_chunk_shape(const AttnParams& p, cudaStream_t stream)
     }
     if (n * (S::kThreads / 128) < 2 * S::kSoftRegs + (S::kThreads / 128 - 2) * S::kOtherRegs)
         return cudaErrorInvalidConfiguration;
-    launch_dep_clusters(err, attn_chunk_kernel<DIM, INT8>, dim3(p.blocks * S::kCtas), dim3(S::kThreads), S::kCtas, smem,
+    launch_dep_clusters(err, attn_chunk_kernel<DIM, INT8, PAIR>, dim3(p.blocks * S::kCtas), dim3(S::kThreads), S::kCtas, smem,
                         stream, cp);
     return err;
 }
@@ -1083,9 +1097,13 @@ BD_BOUNDS_TAKE(bounds_take_attention_chunk)
 
 cudaError_t launch_attention_chunk(const AttnParams& p, cudaStream_t stream)
 {
+    const bool int8 = p.a.cache.int8 != 0;
+    if (p.mb == kPairRows) {
+        return int8 ? launch_chunk_shape<128, true, true>(p, stream) : launch_chunk_shape<128, false, true>(p, stream);
+    }
     if (p.a.cache.dim == 128)
-        return p.a.cache.int8 ? launch_chunk_shape<128, true>(p, stream) : launch_chunk_shape<128, false>(p, stream);
-    return p.a.cache.int8 ? launch_chunk_shape<64, true>(p, stream) : launch_chunk_shape<64, false>(p, stream);
+        return int8 ? launch_chunk_shape<128, true, false>(p, stream) : launch_chunk_shape<128, false, false>(p, stream);
+    return int8 ? launch_chunk_shape<64, true, false>(p, stream) : launch_chunk_shape<64, false, false>(p, stream);
 }
 
 }  // namespace bd

@@ -425,8 +425,8 @@ bd_status bd_kv_read(const bd_kv_pages* cache, const int32_t* page_table, int64_
  * product with V.  Int8 codes enter the tensor cores exactly (in fp16 with q,
  * whose rows are scaled by a power of two so that bf16's 8 bits fit) and
  * their scales multiply the fp32 scores and probabilities; probability times
- * v_scale is then rounded once, to fp16 when max_new * (n_q / n_kv) <= 16 and
- * to bf16 above.  Cached values up to 2^80 in magnitude give the formula's
+ * v_scale is then rounded once, to bf16, or to fp16 where its range allows.
+ * Cached values up to 2^80 in magnitude give the formula's
  * result; beyond that a product may overflow.  Results do not depend on
  * timing (no atomics).  A page outside [0, n_pages), a length outside
  * [0, max_pages * page_size] or offsets out of order set BD_ERR_BAD_INDEX:

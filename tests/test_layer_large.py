@@ -124,6 +124,36 @@ def test_attention_mixed_batch(dev, n_new, kv_len, n_q, n_kv, dim, page, max_new
     ops.run_attention(dev, n_new, kv_len, n_q, n_kv, dim, page, int8, seed=sum(kv_len) % 89, max_new=max_new)
 
 
+@pytest.mark.parametrize("n_new", [1, 40])
+@pytest.mark.parametrize("gap", [20, 30, 60])
+def test_attention_small_probabilities(dev, n_new, gap):
+    """One key has all the weight and a value of 0 in every dim but the first: the others hold what is left to the
+    keys `gap` (in units of the exponential) below it, to the same relative bound."""
+    dim, length, page = 64, 120, 16
+    g = torch.Generator().manual_seed(gap + n_new)
+    kc = torch.zeros(8, 1, page, dim, dtype=torch.int8)
+    vc = torch.randint(-127, 128, (8, 1, page, dim), generator=g).to(torch.int8)
+    kc[:, 0, :, 0] = torch.randint(-12, -8, (8, page), generator=g).to(torch.int8)
+    kc[0, 0, 3, 0] = 118
+    vc[0, 0, 3, 1:] = 0
+    ks, vs = torch.full((8, 1, page), 0.5), 0.01 + 0.01 * torch.rand(8, 1, page, generator=g)
+    q = torch.zeros(n_new, 1, dim)
+    q[:, :, 0] = gap / 64
+    q = q.to(torch.bfloat16)
+    cache = bd.KvPages(*(t.to(dev) for t in (kc, vc, ks, vs)))
+    table = torch.arange(8, dtype=torch.int32, device=dev).view(1, 8)
+    out = torch.empty(n_new, 1, dim, device=dev, dtype=torch.bfloat16)
+    ws = bd.new_workspace(bd.bd_attention_workspace_size(n_new, 1, 1, 1, dim), dev)
+    bd.bd_attention(q.to(dev), torch.tensor([0, n_new], dtype=torch.int32, device=dev), cache, table,
+                    torch.tensor([length], dtype=torch.int32, device=dev), 1.0, n_new, out, ws)
+    assert bd.bd_check_async(ws) == bd.BD_OK
+    k, v = ((c.double() * s.double()[..., None]).transpose(1, 2).reshape(128, 1, dim)[:length]
+            for c, s in ((kc, ks), (vc, vs)))
+    want = ref.attention(q, [0, n_new], [k], [v], [length], 1.0, True)
+    assert float(want[0][:, :, 1:].abs().max()) < 0.01 * 2.0 ** -(gap / 1.5)
+    ops.within(out, want[0], ref.attention_bounds(*want, length)[0], "attention")
+
+
 # ------------------------------------------------------------------------------- one result
 
 def test_results_do_not_depend_on_the_run(dev):
