@@ -1095,7 +1095,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
 constexpr int kJoinThreads = 128;
 
 // Block (c, y): joins what block c of the main kernel noted down, a row per
-// warp.  It has two latencies to wait for: what was noted down, then the parts
+// warp and more where sequences have more rows than the host expects.  It has two latencies to wait for: what was noted down, then the parts
 // with their maxima, the first BATCH of them at once (in turn, with the
 // sequence's offsets before them, four: 27 us for the chunk of 4096 over 8192
 // keys, 64/8 heads, against 14).  A chunk's items have few parts and many
@@ -1114,60 +1114,61 @@ __global__ void __launch_bounds__(kJoinThreads, BATCH <= 4 ? 12 : 4)
     const int lane = threadIdx.x & 31;
     const int parts = it.parts;
     const int live = it.rows - it.row0 < p.mb ? it.rows - it.row0 : p.mb;
-    const int r = kJoinThreads / 32 * blockIdx.y + (threadIdx.x >> 5);
-    if (r >= live) return;
-    const auto row_of = [&](int i) { return static_cast<int64_t>(attn_slot(c - 1 + i, i == 0)) * p.mb + r; };
-    float v[BATCH][kPer];
-    const auto load = [&](int i0) {
+    constexpr int kWarps = kJoinThreads / 32;
+    for (int r = kWarps * blockIdx.y + (threadIdx.x >> 5); r < live; r += kWarps * gridDim.y) {
+        const auto row_of = [&](int i) { return static_cast<int64_t>(attn_slot(c - 1 + i, i == 0)) * p.mb + r; };
+        float v[BATCH][kPer];
+        const auto load = [&](int i0) {
 #pragma unroll
-        for (int j = 0; j < BATCH; ++j) {
-            const float* src = p.part_o + row_of(i0 + j < parts ? i0 + j : parts - 1) * DIM + kPer * lane;
-            if constexpr (kPer == 4) {
-                const float4 x = *reinterpret_cast<const float4*>(src);
-                v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
-            } else {
-                const float2 x = *reinterpret_cast<const float2*>(src);
-                v[j][0] = x.x, v[j][1] = x.y;
+            for (int j = 0; j < BATCH; ++j) {
+                const float* src = p.part_o + row_of(i0 + j < parts ? i0 + j : parts - 1) * DIM + kPer * lane;
+                if constexpr (kPer == 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(src);
+                    v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
+                } else {
+                    const float2 x = *reinterpret_cast<const float2*>(src);
+                    v[j][0] = x.x, v[j][1] = x.y;
+                }
+            }
+        };
+        load(0);
+        float2 ml = make_float2(-INFINITY, 0.0f);  // of part 32 n + lane
+        if (lane < parts) ml = p.part_ml[row_of(lane)];
+        float mm = ml.x;
+        for (int i = 32 + lane; i < parts; i += 32) mm = fmaxf(mm, p.part_ml[row_of(i)].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+        float acc[kPer] = {}, ll = 0.0f, w = attn_weight(ml.x, ml.y, mm);
+        for (int i0 = 0; i0 < parts; i0 += BATCH) {
+            if (i0) load(i0);
+            if (i0 && (i0 & 31) == 0) {
+                ml = make_float2(-INFINITY, 0.0f);
+                if (i0 + lane < parts) ml = p.part_ml[row_of(i0 + lane)];
+                w = attn_weight(ml.x, ml.y, mm);
+            }
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) {
+                const float wj = __shfl_sync(0xffffffffu, w, (i0 + j) & 31);
+                const float lj = __shfl_sync(0xffffffffu, ml.y, (i0 + j) & 31);
+                if (i0 + j < parts && wj != 0.0f) {
+                    ll += wj * lj;
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e) acc[e] += wj * v[j][e];
+                }
             }
         }
-    };
-    load(0);
-    float2 ml = make_float2(-INFINITY, 0.0f);  // of part 32 n + lane
-    if (lane < parts) ml = p.part_ml[row_of(lane)];
-    float mm = ml.x;
-    for (int i = 32 + lane; i < parts; i += 32) mm = fmaxf(mm, p.part_ml[row_of(i)].x);
+        const int row = it.row0 + r, tok = row / p.G;
+        const int64_t at = (static_cast<int64_t>(it.q0) + tok) * a.n_q + it.h * p.G + (row - tok * p.G);
+        if (!bd_in(kBkAttnCombine, at, a.T * a.n_q)) continue;
+        const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+        uint32_t y[kPer / 2];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-    float acc[kPer] = {}, ll = 0.0f, w = attn_weight(ml.x, ml.y, mm);
-    for (int i0 = 0; i0 < parts; i0 += BATCH) {
-        if (i0) load(i0);
-        if (i0 && (i0 & 31) == 0) {
-            ml = make_float2(-INFINITY, 0.0f);
-            if (i0 + lane < parts) ml = p.part_ml[row_of(i0 + lane)];
-            w = attn_weight(ml.x, ml.y, mm);
-        }
-#pragma unroll
-        for (int j = 0; j < BATCH; ++j) {
-            const float wj = __shfl_sync(0xffffffffu, w, (i0 + j) & 31);
-            const float lj = __shfl_sync(0xffffffffu, ml.y, (i0 + j) & 31);
-            if (i0 + j < parts && wj != 0.0f) {
-                ll += wj * lj;
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) acc[e] += wj * v[j][e];
-            }
-        }
+        for (int e = 0; e < kPer; e += 2) y[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+        uint16_t* dst = a.out + at * DIM + kPer * lane;
+        if constexpr (kPer == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
+        else *reinterpret_cast<uint32_t*>(dst) = y[0];
+        if (lane == 0 && a.lse) a.lse[at] = attn_lse(mm, ll);
     }
-    const int row = it.row0 + r, tok = row / p.G;
-    const int64_t at = (static_cast<int64_t>(it.q0) + tok) * a.n_q + it.h * p.G + (row - tok * p.G);
-    if (!bd_in(kBkAttnCombine, at, a.T * a.n_q)) return;
-    const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-    uint32_t y[kPer / 2];
-#pragma unroll
-    for (int e = 0; e < kPer; e += 2) y[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-    uint16_t* dst = a.out + at * DIM + kPer * lane;
-    if constexpr (kPer == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
-    else *reinterpret_cast<uint32_t*>(dst) = y[0];
-    if (lane == 0 && a.lse) a.lse[at] = attn_lse(mm, ll);
 }
 
 template <int DIM, bool INT8, int NT, bool WHOLE>
@@ -1268,9 +1269,11 @@ static void attn_take_workspace(AttnParams& p, int64_t rows, int most_blocks, ch
     ws += w.total;
 }
 
-static void launch_join(cudaError_t& err, const AttnParams& p, bool chunk, cudaStream_t stream)
+static void launch_join(cudaError_t& err, const AttnParams& p, int64_t rows, bool chunk, cudaStream_t stream)
 {
-    const dim3 grid(static_cast<unsigned>(p.blocks > 1 ? p.blocks - 1 : 1), p.mb / (kJoinThreads / 32));
+    constexpr int kWarps = kJoinThreads / 32;
+    const int live = rows < p.mb ? static_cast<int>(rows) : p.mb;  // of an item, at most
+    const dim3 grid(static_cast<unsigned>(p.blocks > 1 ? p.blocks - 1 : 1), (live + kWarps - 1) / kWarps);
     const auto join = p.a.cache.dim == 128 ? chunk ? attn_join_kernel<128, 4> : attn_join_kernel<128, 16>
                                            : chunk ? attn_join_kernel<64, 4> : attn_join_kernel<64, 16>;
     launch_dep(err, join, grid, dim3(kJoinThreads), 0, stream, p);
@@ -1287,7 +1290,7 @@ static void launch_chunks(cudaError_t& err, AttnParams p, int64_t rows, char*& w
     attn_take_workspace(p, p.a.T * p.G, most, ws);
     launch_dep(err, attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
     if (err == cudaSuccess) err = launch_attention_chunk(p, stream);
-    launch_join(err, p, true, stream);
+    launch_join(err, p, rows, true, stream);
 }
 
 // Few rows a sequence.
@@ -1322,7 +1325,7 @@ static void launch_few_rows(cudaError_t& err, AttnParams p, int rows, bool deal,
     if (p.whole) p.blocks = static_cast<int>(pairs) * p.whole;
     attn_take_workspace(p, 0, kAttnMaxBlocks, ws);
     if (err == cudaSuccess) err = launch_attention_mma(p, stream);
-    if (!p.whole) launch_join(err, p, false, stream);
+    if (!p.whole) launch_join(err, p, p.mb, false, stream);
 }
 
 cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream)
