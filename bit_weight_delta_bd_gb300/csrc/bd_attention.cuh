@@ -15,8 +15,7 @@
 // workspace; at most its first and its last are of that kind.  The second
 // block of such an (item, head) notes it down, and the join adds its parts in
 // block order, so results do not depend on timing.
-//
-// (The decode kernel does without where caches are short or few.)
+// (The decode kernel does without a deal where caches are short or few.)
 //
 // Finding its units.  The decode kernel's blocks work the deal out from the
 // lengths by themselves (one load per sequence and a scan: no launch before

@@ -119,7 +119,7 @@ def test_attention_clusters_and_deal(dev, n_new, kv_len, n_q, n_kv, dim, page, m
     ([1, 300, 1, 1, 40, 2, 3], [900, 800, 33, 1, 400, 1500, 3], 16, 2, 128, 16, 300),
     ([16, 17, 200, 1], [200, 300, 200, 5000], 4, 4, 64, 64, 200), ([1] * 30 + [129], [40 * i for i in range(31)], 12, 1, 128, 32, 129),
     ([1, 1, 1], [700, 0, 64], 8, 1, 64, 16, 50),  # no chunk after all
-    ([0, 0, 150], [9, 0, 150], 8, 2, 128, 128, 150), ([600, 8, 1], [600, 1000, 2000], 2, 2, 128, 16, 9)])
+    ([0, 0, 150], [9, 0, 150], 8, 2, 128, 128, 150), ([1, 30, 2], [50, 30, 700], 8, 2, 128, 16, 2 ** 62), ([600, 8, 1], [600, 1000, 2000], 2, 2, 128, 16, 9)])
 def test_attention_mixed_batch(dev, n_new, kv_len, n_q, n_kv, dim, page, max_new, int8):
     ops.run_attention(dev, n_new, kv_len, n_q, n_kv, dim, page, int8, seed=sum(kv_len) % 89, max_new=max_new)
 
