@@ -32,7 +32,7 @@
 // to bf16 like its values, have 8.  A step with a product below 2^-14, where
 // fp16 loses bits, runs P V in bf16 instead (a dim in which the likeliest keys'
 // codes are 0 takes its value from the others, however small they are); that
-// takes a logic operation more for two codes: 92.5 us where all steps do, 88.6
+// takes a logic operation more for two codes: 92.5 us where all steps do, 88.0
 // where none does (4 sequences of up to 65538 keys, 64/8 heads; 86.7 without
 // the test).
 
@@ -874,27 +874,21 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
                     }
             }
 
-            [[maybe_unused]] bool low = false;  // some of it would lose bits in fp16
-            if constexpr (INT8) {
-                low = __any_sync(0xffffffffu, least < kFp16Normal);
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int b = 0; b < 2; ++b)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const float x = pw[n][b][2 * j], y = pw[n][b][2 * j + 1];
-                            pb[n][b][j] = transpose8(low ? pack_bf16x2(x, y) : pack_f16x2(x, y));
-                        }
-            }
-
             // ---- sums: dim x 8 NT rows += V^T (dim x 32) P^T (32 x 8 NT)
             const uint32_t vt = st + S::kTileBytes;
             // a b16 element is a pair of dims: the transposed fragment holds dims 2 g, 2 g + 1 of two keys;
             // the tile's rows 0..7 take the even dims of a chunk, rows 8..15 the odd ones
             [[maybe_unused]] const auto add_codes = [&](auto as_bf16) {
+                constexpr bool kBf16 = decltype(as_bf16)::value;
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float x = pw[n][b][2 * j], y = pw[n][b][2 * j + 1];
+                            pb[n][b][j] = transpose8(kBf16 ? pack_bf16x2(x, y) : pack_f16x2(x, y));
+                        }
                     const int row = slice + 16 * b + (mi & 1) * 8 + mr;
 #pragma unroll
                     for (int k = 0; k < kSteps; k += 2) {
@@ -902,7 +896,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
                         ldsm_x4_t(vt + swizzled<S::kBoxBytes>(row, k + (mi >> 1)), r);
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            if constexpr (decltype(as_bf16)::value) {
+                            if constexpr (kBf16) {
                                 const uint32_t a0 = codes_bf16x2(r[2 * x]), a1 = codes_bf16x2(r[2 * x] >> 8);
                                 const uint32_t a2 = codes_bf16x2(r[2 * x + 1]), a3 = codes_bf16x2(r[2 * x + 1] >> 8);
 #pragma unroll
@@ -920,7 +914,8 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
                 }
             };
             if constexpr (INT8) {
-                if (low) add_codes(std::true_type{});
+                // some of it would lose bits in fp16
+                if (__any_sync(0xffffffffu, least < kFp16Normal)) add_codes(std::true_type{});
                 else add_codes(std::false_type{});
             } else {
 #pragma unroll
