@@ -49,7 +49,7 @@ namespace {
 
 // ------------------------------------------------------------------------------- plan
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 256;
 
 // Exclusive scan over the block; *total gets the sum.
 __device__ __forceinline__ int block_scan(int v, int* red, int* total)

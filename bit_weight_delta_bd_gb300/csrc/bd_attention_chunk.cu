@@ -19,8 +19,9 @@
 // CTA is its shared memory (a step of 64 reads Q twice as often as one of 128
 // would, and the 64-key product then runs at 3/4 of its rate); a pair reads 3/4
 // of that, and int8 tiles are converted once for 512 rows.  A chunk of 4096
-// tokens over 8192 keys, 64/8 heads: bf16 885 -> 812 us, 1694 TFLOP/s; int8
-// 1245 -> 1110 us.  Sequences of up to 256 rows would fill a pair's first query
+// tokens over 8192 keys, 64/8 heads: bf16 885 -> 812 us, int8 1245 -> 1110 (and
+// 785 .. 810 us, up to 1750 TFLOP/s, with O written by whole sectors, a row per
+// thread: 5 us of any call).  Sequences of up to 256 rows would fill a pair's first query
 // tile at most, which takes as long as both: 8 sequences of 4 tokens over 4000
 // keys take 48 us by single CTAs and 68 by pairs (int8).  With head_dim 64
 // half of V's dims would leave 64-byte rows, and the exponentials bound the
@@ -606,6 +607,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8, PAIR>::kThreads, 1)
         const uint32_t ts = tmem + lanes + i * 128, to = tmem + lanes + kTmemO + i * DIM;
         uint8_t* q_smem = dyn + i * S::kQBytes;
         float unit = 1.0f;  // of this thread's row of the Q in shared memory
+        const bool out_sectors = on_sector(a.out);
         uint32_t s_phase = 0, o_phase = 0, pv_phase = 0, sc_phase = 0;
         int sc = 0;
         // After a timeout (reported) the waits return at once and the loops run out on what is there.
@@ -645,21 +647,26 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8, PAIR>::kThreads, 1)
                         }
                     }
                     if (live && whole) {
-                        uint4* dst = reinterpret_cast<uint4*>(a.out + at * DIM + j);
+                        uint32_t w[8];
 #pragma unroll
-                        for (int e = 0; e < 16; e += 8) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                w[k] = pack_bf16x2(__uint_as_float(o[e + 2 * k]) * inv,
-                                                   __uint_as_float(o[e + 2 * k + 1]) * inv);
-                            if (l == 0.0f) w[0] = w[1] = w[2] = w[3] = 0u;
-                            dst[e / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int k = 0; k < 8; ++k) {
+                            w[k] = pack_bf16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+                            if (l == 0.0f) w[k] = 0u;
+                        }
+                        uint16_t* dst = a.out + at * DIM + j;
+                        if (out_sectors) {
+                            store_32(dst, w);
+                        } else {
+                            reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                            reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
                         }
                     } else if (live) {
-                        uint4* dst = reinterpret_cast<uint4*>(p.part_o + at * DIM + j);
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4) dst[e / 4] = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        for (int e = 0; e < 16; e += 8) {
+                            const uint32_t w[8] = {o[e],     o[e + 1], o[e + 2], o[e + 3],
+                                                   o[e + 4], o[e + 5], o[e + 6], o[e + 7]};
+                            store_32(p.part_o + at * DIM + j + e, w);
+                        }
                     }
                 }
                 if (live) {

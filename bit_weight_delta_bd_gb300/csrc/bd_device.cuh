@@ -293,5 +293,25 @@ __device__ __forceinline__ uint4 ld_stream_v4(const void* p)
     return v;
 }
 
+// 32 bytes at once, a whole sector (two accesses of 16 bytes by threads whose
+// data lie 32 bytes apart touch each sector twice).
+__device__ __forceinline__ void store_32(void* p, const uint32_t (&v)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+__device__ __forceinline__ void store_32(void* p, uint4 lo, uint4 hi)
+{
+    const uint32_t v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    store_32(p, v);
+}
+__device__ __forceinline__ void load_32(const void* p, uint4& lo, uint4& hi)
+{
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(lo.x), "=r"(lo.y), "=r"(lo.z), "=r"(lo.w), "=r"(hi.x), "=r"(hi.y), "=r"(hi.z), "=r"(hi.w)
+                 : "l"(p));
+}
+__device__ __forceinline__ bool on_sector(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
 
 }  // namespace bd

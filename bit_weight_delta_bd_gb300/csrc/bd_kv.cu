@@ -222,7 +222,8 @@ struct KvReadParams {
 // A block gathers kReadRows consecutive output rows: their places in the
 // cache are looked up first (a binary search in kv_off per row), then all
 // threads copy units of 16 elements, two at a time: 8 sequences of up to 8192
-// int8 tokens, 8 heads of 128, in 48.3 us, 6.1 TB/s (51.6 one at a time).
+// int8 tokens, 8 heads of 128, in 48.4 us, 6.1 TB/s (51.6 one at a time); bf16
+// 59.4 us, 6.6 TB/s, by whole sectors (62.5 by halves of 16 bytes).
 template <int UPH, bool INT8>
 __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const __grid_constant__ KvReadParams p)
 {
@@ -264,6 +265,8 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const __grid_cons
     const void* pool = is_v ? a.cache.v : a.cache.k;
     const float* scales = is_v ? a.cache.v_scale : a.cache.k_scale;
     uint16_t* out = is_v ? a.v_out : a.k_out;
+    // (int8 has no registers to spare for eight at once: 50.5 us for 48.4)
+    [[maybe_unused]] const bool sectors = on_sector(pool) && on_sector(out);
     // two units at a time: both loads before either is converted
     const int units = kReadRows * per_row;
     for (int i0 = threadIdx.x; i0 < units; i0 += 2 * kReadThreads) {
@@ -286,8 +289,12 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const __grid_cons
                     scale[k] = __ldg(scales + vec);
                 } else {
                     const uint16_t* src = static_cast<const uint16_t*>(pool) + vec * kDim + 16 * u;
-                    lo[k] = ld_stream_v4(src);
-                    hi[k] = ld_stream_v4(src + 8);
+                    if (sectors) {
+                        load_32(src, lo[k], hi[k]);
+                    } else {
+                        lo[k] = ld_stream_v4(src);
+                        hi[k] = ld_stream_v4(src + 8);
+                    }
                 }
             }
         }
@@ -304,8 +311,12 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const __grid_cons
                 hi[k] = pack8(f + 8);
             }
             uint16_t* dst = out + to[k];
-            *reinterpret_cast<uint4*>(dst) = lo[k];
-            *reinterpret_cast<uint4*>(dst + 8) = hi[k];
+            if (!INT8 && sectors) {
+                store_32(dst, lo[k], hi[k]);
+            } else {
+                *reinterpret_cast<uint4*>(dst) = lo[k];
+                *reinterpret_cast<uint4*>(dst + 8) = hi[k];
+            }
         }
     }
 }

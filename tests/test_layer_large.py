@@ -154,6 +154,45 @@ def test_attention_small_probabilities(dev, n_new, gap):
     ops.within(out, want[0], ref.attention_bounds(*want, length)[0], "attention")
 
 
+@pytest.mark.parametrize("int8", [False, True])
+def test_buffers_on_16_byte_boundaries(dev, int8):
+    """Buffers 16 bytes off the start of a 32-byte sector give the same bits as ones on it."""
+    T, n_q, n_kv, dim, page = 300, 8, 2, 128, 16
+    g = torch.Generator(device=dev).manual_seed(6)
+
+    def rand(*shape, off=0):
+        n = int(np.prod(shape))
+        t = torch.empty(n + 8, device=dev, dtype=torch.bfloat16)
+        t[off: off + n].normal_(generator=g)
+        return t[off: off + n].view(shape)
+
+    def moved(t):
+        u = torch.empty(t.numel() + 16 // t.element_size(), device=dev, dtype=t.dtype)[16 // t.element_size():]
+        u.copy_(t.flatten())
+        assert u.data_ptr() % 32 == 16
+        return u.view(t.shape)
+
+    q, k, v = rand(T, n_q, dim), rand(T, n_kv, dim), rand(T, n_kv, dim)
+    shape = (20, n_kv, page, dim)
+    pos = torch.arange(T, dtype=torch.int32, device=dev)
+    table = torch.arange(20, dtype=torch.int32, device=dev).view(1, 20)
+    off = torch.tensor([0, T], dtype=torch.int32, device=dev)
+    tab = bd.rope_table(T, dim, 10000.0, dev)
+    ws = bd.new_workspace(bd.bd_attention_workspace_size(T, 1, n_q, n_kv, dim), dev)
+    for inter in (False, True):
+        runs = []
+        for place in (lambda t: t, moved):
+            kv = [place(torch.zeros(shape, dtype=torch.int8 if int8 else torch.bfloat16, device=dev)) for _ in range(2)]
+            cache = bd.KvPages(*kv, *([torch.zeros(shape[:3], device=dev) for _ in range(2)] if int8 else []))
+            qo, out, ko, vo = (place(torch.zeros_like(t)) for t in (q, q, k, v))
+            bd.bd_rope_append(place(q), place(k), place(v), pos, tab, pos, cache, qo, ws, interleaved=inter)
+            bd.bd_kv_read(cache, table, off, ko, vo, ws)
+            bd.bd_attention(qo, off, cache, table, off[1:], dim ** -0.5, T, out, ws)
+            assert bd.bd_check_async(ws) == bd.BD_OK
+            runs.append([*kv, qo, ko, vo, out])
+        assert all(torch.equal(a, b) for a, b in zip(*runs))
+
+
 # ------------------------------------------------------------------------------- one result
 
 def test_results_do_not_depend_on_the_run(dev):
