@@ -701,6 +701,8 @@ bd_status bd_attention(const uint16_t* q, int64_t q_stride, const int32_t* q_off
     if (bd_status s = check_ws(ws, ws_bytes, bd_attention_workspace_size(T, n_seq, n_q, a.cache.n_kv, a.cache.dim)))
         return s;
     if (T == 0 || n_seq == 0) return BD_OK;
+    // a bad page is replaced by page 0, and the tensor maps need an extent: there has to be one
+    if (a.cache.n_pages == 0) return BD_ERR_UNSUPPORTED_SHAPE;
     if (!q || !q_off || !kv_len || !out || (!page_table && max_pages > 0)) return BD_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(q_off, 4) || !aligned(kv_len, 4) || !aligned(page_table, 4) ||
         !aligned(lse, 4))

@@ -420,6 +420,7 @@ bd_status bd_kv_read(const bd_kv_pages* cache, const int32_t* page_table, int64_
  *   kv_len   device int32 [n_seq]
  *   out      device bf16 [T][n_q][head_dim], 16-byte aligned
  *   lse      device fp32 [T][n_q] or NULL: log sum_j exp(scale * q . k_j)
+ * The cache has at least one page (BD_ERR_UNSUPPORTED_SHAPE: new tokens are in it).
  * n_q: a positive multiple of n_kv.  Scores, the softmax and all sums are
  * fp32.  In a bf16 cache probabilities are rounded to bf16 before their
  * product with V.  Int8 codes enter the tensor cores exactly (in fp16 with q,
