@@ -169,7 +169,7 @@ struct alignas(16) MmaShared {
     uint64_t empty[kMmaMaxStages];
     float m[kMmaConsumers][kMmaMaxRows];
     float l[kMmaConsumers][kMmaMaxRows];
-    uint64_t joined;    // the cluster's blocks have sent their parts of this block's rows
+    uint64_t joined[2];  // the cluster's blocks have sent their parts of this block's rows, by the item's parity
     volatile int abort;
     int64_t scan[kMmaThreads / 32];
     int seq, row0;      // the block's first item,
@@ -510,8 +510,11 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
     uint8_t* ring = dyn_raw;
     float* buf = reinterpret_cast<float*>(ring + static_cast<size_t>(mp.stages) * S::kStageBytes);
     MmaShared& sh = *reinterpret_cast<MmaShared*>(reinterpret_cast<uint8_t*>(buf) + S::kBufBytes);
-    // a cluster's parts: row k of those that this block joins, from rank w, for the item's parity; a
-    // block sends an item's parts only after it has all of the one before, so two places suffice
+    // A cluster's parts: row k of those that this block joins, from rank w, for the item's parity.  A
+    // block sends an item's parts only after it has all of the one before, so two places suffice, and
+    // two barriers: one would take a block's arrival for the next item, which a third block's late one
+    // for this item does not hold back, for that.  Item i + 2, which shares item i's, is sent only
+    // after every block's arrival for i + 1, so after every block has had all of item i.
     constexpr int kRecvStride = DIM + 4;  // the sum, its maximum and denominator
     [[maybe_unused]] float* recv = reinterpret_cast<float*>(&sh + 1);
     [[maybe_unused]] const auto recv_row = [&](uint32_t item, int w, int k) {
@@ -531,7 +534,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
             mbar_init(&sh.full[s], 1);
             mbar_init(&sh.empty[s], kMmaConsumers);
         }
-        mbar_init(&sh.joined, WHOLE ? p.whole : 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&sh.joined[i], WHOLE ? p.whole : 1);
         sh.abort = 0;
         fence_mbarrier_init();
     }
@@ -1056,9 +1059,10 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
         consumers_sync();  // the buffers are free for the next item
         if constexpr (WHOLE) {
             if (p.whole > 1) {
-                if (static_cast<int>(threadIdx.x) < p.whole) mbar_arrive_remote_release(&sh.joined, threadIdx.x);
+                uint64_t* const joined = &sh.joined[item & 1];
+                if (static_cast<int>(threadIdx.x) < p.whole) mbar_arrive_remote_release(joined, threadIdx.x);
                 // (given up, which is reported: what is there is joined)
-                if (!mbar_wait_cluster_bounded(&sh.joined, item & 1, a.err)) gave_up = true;
+                if (!mbar_wait_cluster_bounded(joined, (item >> 1) & 1, a.err)) gave_up = true;
                 for (int i = threadIdx.x; i < S::kRows / p.whole * (DIM / 4); i += 32 * kMmaConsumers) {
                     const int k = i / (DIM / 4), d = 4 * (i % (DIM / 4)), r = k * p.whole + walk_rank;
                     if (r >= live_rows) break;

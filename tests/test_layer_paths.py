@@ -1,0 +1,46 @@
+"""The operators between a layer's linears on the paths that sizes and hints
+choose between: clusters with many items, CTA pairs over ragged chunks, norms
+of many rows and of every row length's kernel, attention without a causal mask
+in few rows, and scales of any sign -- against the 64-bit definitions of
+layer_oracle.py, with its bounds."""
+import numpy as np
+import pytest
+import torch
+
+import layer_oracle as ref
+import test_layer_ops as ops
+from bit_weight_delta_bd_gb300 import bitdelta as bd
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    import __graft_entry__
+
+    __graft_entry__.build()
+    torch.cuda.set_device(0)
+    return torch.device("cuda:0")
+
+
+def again(run, out, times):
+    """The call repeated: the same bits each time."""
+    outs = [torch.empty_like(out) for _ in range(times)]
+    for o in outs:
+        run(o)
+    assert all(torch.equal(out, o) for o in outs)
+
+
+# ------------------------------------------------------------------------------- clusters
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("n_new,kv_len,n_q,n_kv,dim,page", [
+    ([64], [1100], 8, 1, 64, 16), ([50, 3, 21], [500, 400, 30], 16, 1, 128, 16), ([33, 1], [260, 900], 7, 1, 128, 64)])
+def test_clusters_of_many_items(dev, n_new, kv_len, n_q, n_kv, dim, page, int8):
+    """A host that expects one token a sequence gets clusters, whose blocks join item after item."""
+    out, q, on, off, lens = ops.run_attention(dev, n_new, kv_len, n_q, n_kv, dim, page, int8, seed=sum(n_new), max_new=1)
+    cache = bd.KvPages(on["k"], on["v"], on["ks"], on["vs"])
+    ws = bd.new_workspace(bd.bd_attention_workspace_size(len(q), len(n_new), n_q, n_kv, dim), dev)
+    again(lambda o: bd.bd_attention(q, off, cache, on["table"], lens, dim ** -0.5, 1, o, ws), out, 50)
+    assert bd.bd_check_async(ws) == bd.BD_OK
