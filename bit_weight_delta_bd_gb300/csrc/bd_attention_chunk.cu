@@ -49,8 +49,8 @@
 //
 // Warps: 0..3 and 4..7 softmax of query tiles 0 and 1 (and loading Q, and
 // writing O); 8 TMA; 9 and 10 MMA of query tiles 0 and 1 (of a pair: the even
-// CTA's); 11 passes on that a pair's bf16 tiles have landed; 12..15 conversion
-// (int8).
+// CTA's); 11 passes on that a pair's tiles are there (bf16: landed, int8: the
+// odd CTA's converted); 12..15 conversion (int8).
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -103,7 +103,7 @@ constexpr int kMaxBufs = 8, kMaxRaw = 6, kMaxScales = 4;
 
 struct ChunkShared {
     uint64_t full[kMaxBufs], empty[kMaxBufs];    // bf16 tiles (full: of both CTAs, in the even one)
-    uint64_t landed[kMaxBufs];                   // this CTA's part of them (pairs, bf16)
+    uint64_t landed[kMaxBufs];                   // this CTA's part of them (pairs; int8: the odd one's)
     uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];     // tiles of codes
     uint64_t sc_full[kMaxScales], sc_empty[kMaxScales];  // scales
     uint64_t q_full[2], o_full[2];
@@ -137,12 +137,22 @@ __device__ __forceinline__ bool warp_wait(volatile int* abort_flag, uint64_t* ba
     return false;
 }
 
-// Barriers of a pair: an arrival at the even CTA's, a wait for arrivals of
-// both, and the tensor cores' arrival at both.
+// Barriers of a pair: an arrival at the even CTA's (for tensor memory, and for
+// tiles that TMA has brought), a wait for arrivals of both, and the tensor
+// cores' arrival at both.
 template <bool PAIR>
 __device__ __forceinline__ void arrive_even(uint64_t* bar)
 {
     if constexpr (PAIR) mbar_arrive_remote(bar, 0);
+    else mbar_arrive(bar);
+}
+// The same for what this CTA's threads have written to its shared memory, which
+// the even CTA's products are to read: released at cluster scope by the odd
+// CTA, since an arrival of CTA scope orders none of it there.
+template <bool PAIR>
+__device__ __forceinline__ void arrive_even_written(uint64_t* bar, int rank)
+{
+    if (PAIR && rank != 0) mbar_arrive_remote_release(bar, 0);
     else mbar_arrive(bar);
 }
 template <bool PAIR>
@@ -255,11 +265,11 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t 
 
 // What lies past the sequence in a tile of V may be anything, NaN included:
 // zeros from key `valid` on instead, so that probabilities of 0 times it stay
-// 0.  DIMS: that the CTA holds.  By a warp.
+// 0.  DIMS: that the CTA holds.  By a warp.  Returns whether it wrote any.
 template <int DIMS>
-__device__ __forceinline__ void zero_past(uint8_t* v, int valid, int lane)
+__device__ __forceinline__ bool zero_past(uint8_t* v, int valid, int lane)
 {
-    if (valid >= kTile) return;
+    if (valid >= kTile) return false;
 #pragma unroll 1
     for (int x = (valid > 0 ? valid : 0) * 8 + lane; x < kTile * 8; x += 32)
 #pragma unroll
@@ -267,6 +277,7 @@ __device__ __forceinline__ void zero_past(uint8_t* v, int valid, int lane)
             *reinterpret_cast<uint4*>(v + (d / 64) * kTile * 128 + x * 16) = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     __syncwarp();
+    return true;
 }
 
 // One lane of the warp.
@@ -535,9 +546,10 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8, PAIR>::kThreads, 1)
     grid_launch_dependents();
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kBufs; ++i) {
-            mbar_init(&sh.full[i], (INT8 ? 4 : 1) * S::kCtas);
+            // (int8: four warps of the even CTA, and what the odd one passes on)
+            mbar_init(&sh.full[i], INT8 ? 3 + S::kCtas : S::kCtas);
             mbar_init(&sh.empty[i], 2);
-            mbar_init(&sh.landed[i], 1);
+            mbar_init(&sh.landed[i], INT8 ? 4 : 1);
         }
         for (int i = 0; i < S::kRaw; ++i) {
             mbar_init(&sh.raw_full[i], 1);
@@ -625,7 +637,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8, PAIR>::kThreads, 1)
                 unit = load_q<DIM, INT8>(p, s, tile_row, r - lane, lane, q_smem);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) arrive_even<kPair>(&sh.q_full[i]);
+                if (lane == 0) arrive_even_written<kPair>(&sh.q_full[i], rank);
             }
             if (ran) {
                 warp_wait(&sh.abort, &sh.o_full[i], o_phase);
@@ -962,7 +974,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8, PAIR>::kThreads, 1)
                     const bool pv = j >= 2 * s.t0 + 2, qk = j < 2 * s.t1;
                     if (pv && b == 0) {
                         bv = take();
-                        if constexpr (!INT8 && !kPair) 
+                        if constexpr (!INT8 && !kPair)
                             zero_past<S::kDimsV>(dyn + S::kOffBufs + bv * S::kTileBytes,
                                                  s.sq.len - (j - 2) * kStep, lane);
                     }
@@ -1005,8 +1017,11 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8, PAIR>::kThreads, 1)
             if (elect_one()) commit_both<kPair>(&sh.done);
             __syncwarp();
             mbar_wait_bounded(&sh.done, 0);
-        } else if (!INT8 && kPair && warp == kPassWarp) {
+        } else if (kPair && warp == kPassWarp && (!INT8 || rank != 0)) {
             // ---------------------------------------------------- this CTA's parts are there
+            // A release at cluster scope waits for the warp's writes on their way: by the converting
+            // warps themselves an int8 chunk of 4096 over 8192 keys takes 1211 us, by this warp, which
+            // writes next to nothing, 1112 (8 mixed chunks: 386 and 335).
             int buf = 0;
             uint32_t phase = 0;
             bool ok = true;
@@ -1014,10 +1029,14 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8, PAIR>::kThreads, 1)
 #pragma unroll 1
                 for (int n = 0; n < 2 * (s.t1 - s.t0); ++n) {  // K and V in turn
                     if (!(ok = warp_wait(&sh.abort, &sh.landed[buf], phase))) break;
-                    if (n & 1)
-                        zero_past<S::kDimsV>(dyn + S::kOffBufs + buf * S::kTileBytes,
-                                             s.sq.len - (s.t0 + n / 2) * kTile, lane);
-                    if (lane == 0) arrive_even<kPair>(&sh.full[buf]);
+                    bool written = INT8;
+                    if (!INT8 && (n & 1))
+                        written = zero_past<S::kDimsV>(dyn + S::kOffBufs + buf * S::kTileBytes,
+                                                       s.sq.len - (s.t0 + n / 2) * kTile, lane);
+                    if (lane == 0) {
+                        if (written) arrive_even_written<kPair>(&sh.full[buf], rank);
+                        else arrive_even<kPair>(&sh.full[buf]);
+                    }
                     if (++buf == S::kBufs) buf = 0, phase ^= 1;
                 }
             }
@@ -1041,7 +1060,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8, PAIR>::kThreads, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        arrive_even<kPair>(&sh.full[buf]);
+                        mbar_arrive(kPair && rank != 0 ? &sh.landed[buf] : &sh.full[buf]);
                         mbar_arrive(&sh.raw_empty[raw]);
                     }
                     if (++raw == S::kRaw) raw = 0, raw_phase ^= 1;

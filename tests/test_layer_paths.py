@@ -44,3 +44,20 @@ def test_clusters_of_many_items(dev, n_new, kv_len, n_q, n_kv, dim, page, int8):
     ws = bd.new_workspace(bd.bd_attention_workspace_size(len(q), len(n_new), n_q, n_kv, dim), dev)
     again(lambda o: bd.bd_attention(q, off, cache, on["table"], lens, dim ** -0.5, 1, o, ws), out, 50)
     assert bd.bd_check_async(ws) == bd.BD_OK
+
+
+# ------------------------------------------------------------------------------- pairs
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("n_new,kv_len,n_q,n_kv,page", [
+    # lengths that end inside a tile, in either half of its keys, on pages of every size; what lies past is NaN
+    ([300, 77, 513], [300, 1001, 1500], 8, 2, 16), ([257, 1, 400, 90], [257, 33, 830, 95], 8, 1, 64),
+    ([130, 600], [1111, 601], 4, 1, 128), ([80] * 9, [80 + 29 * i for i in range(9)], 32, 4, 32)])
+def test_pairs_over_ragged_chunks(dev, n_new, kv_len, n_q, n_kv, page, int8):
+    """Both CTAs' rows, values past the lengths and converted tiles reach the products: many short items, again and
+    again, with the same bits."""
+    out, q, on, off, lens = ops.run_attention(dev, n_new, kv_len, n_q, n_kv, 128, page, int8, seed=len(n_new))
+    cache = bd.KvPages(on["k"], on["v"], on["ks"], on["vs"])
+    ws = bd.new_workspace(bd.bd_attention_workspace_size(len(q), len(n_new), n_q, n_kv, 128), dev)
+    again(lambda o: bd.bd_attention(q, off, cache, on["table"], lens, 128 ** -0.5, max(n_new), o, ws), out, 100)
+    assert bd.bd_check_async(ws) == bd.BD_OK
