@@ -397,6 +397,13 @@ class KvPages:
                            _ptr(v_scale, "v_scale", (torch.float32,), True), self.n_pages, self.page_size, self.n_kv,
                            self.head_dim, BD_KV_INT8 if int8 else BD_KV_BF16)
         self._addr = ctypes.addressof(self._c)
+        self._dev = k.get_device()
+
+    def _on(self, dev: int) -> int:
+        """The address of the handle for a call on device dev, which the tensors have to be on."""
+        if self._dev != dev:
+            raise ValueError(f"cache is on cuda:{self._dev}, not the current device")
+        return self._addr
 
 
 def _heads(t, name: str, dim: int, dev: int) -> tuple[int, int]:
@@ -459,7 +466,7 @@ def bd_rope_append(q, k, v, pos, rope_table, slot, cache: KvPages, q_out, ws, ax
     wsp, wsn = _ws(ws, dev)
     _check(load().bd_rope_append(qp, qs, kp, ks, vp, vs, T, n_q, _ptr(pos, "pos", _I32, True, dev), n_axes, axes,
                                  _ptr(rope_table, "rope_table", _F32, True, dev), n_pos, 2 * pairs, interleaved,
-                                 _ptr(slot, "slot", _I32, False, dev), cache._addr, op, os_, wsp, wsn,
+                                 _ptr(slot, "slot", _I32, False, dev), cache._on(dev), op, os_, wsp, wsn,
                                  _stream(stream, dev)), "bd_rope_append")
 
 
@@ -477,7 +484,7 @@ def bd_kv_read(cache: KvPages, page_table, kv_off, k_out, v_out, ws, stream=None
     if kv_off.numel() != n_seq + 1:
         raise ValueError("kv_off must have n_seq + 1 entries")
     wsp, wsn = _ws(ws, dev)
-    _check(load().bd_kv_read(cache._addr, _ptr(page_table, "page_table", _I32, False, dev), max_pages,
+    _check(load().bd_kv_read(cache._on(dev), _ptr(page_table, "page_table", _I32, False, dev), max_pages,
                              _ptr(kv_off, "kv_off", _I32, False, dev), n_seq, rows,
                              _ptr(k_out, "k_out", _BF16_LIKE, False, dev), _ptr(v_out, "v_out", _BF16_LIKE, False, dev),
                              wsp, wsn, _stream(stream, dev)), "bd_kv_read")
@@ -501,7 +508,7 @@ def bd_attention(q, q_off, cache: KvPages, page_table, kv_len, scale, max_new, o
         raise ValueError("lse must be [T][n_q]")
     qp, qs = _heads(q, "q", dim, dev)
     wsp, wsn = _ws(ws, dev)
-    _check(load().bd_attention(qp, qs, _ptr(q_off, "q_off", _I32, False, dev), T, n_seq, max_new, n_q, cache._addr,
+    _check(load().bd_attention(qp, qs, _ptr(q_off, "q_off", _I32, False, dev), T, n_seq, max_new, n_q, cache._on(dev),
                                _ptr(page_table, "page_table", _I32, False, dev), max_pages,
                                _ptr(kv_len, "kv_len", _I32, False, dev), scale, causal,
                                _ptr(out, "out", _BF16_LIKE, False, dev), _ptr(lse, "lse", _F32, True, dev), wsp, wsn,
