@@ -257,6 +257,15 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const __grid_cons
         }
         base[threadIdx.x] = b;
     }
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x >= 32) {
+        // offsets out of order, or tokens that there are no rows for (by the warps that have nothing to look up)
+        bool bad = false;
+        for (int64_t s = threadIdx.x - 32; s < a.n_seq; s += kReadThreads - 32) {
+            const int32_t o = a.kv_off[s], e = a.kv_off[s + 1];
+            bad = bad || e < o || (s == 0 && o != 0) || e > a.rows;
+        }
+        if (bad) raise_error(a.err, kErrBadIndex);
+    }
     __syncthreads();
 
     const int per_row = a.cache.n_kv * UPH;  // units of one row of k (or v)

@@ -389,7 +389,8 @@ bd_status bd_rope_append(const uint16_t* q, int64_t q_stride, const uint16_t* k,
  *               rows from kv_off[n_seq] on stay as they are
  *   k_out, v_out  device bf16 [rows][n_kv][head_dim], 16-byte aligned
  * A page outside [0, n_pages) or a token past max_pages * page_size sets
- * BD_ERR_BAD_INDEX; its row is written as zeros.
+ * BD_ERR_BAD_INDEX; its row is written as zeros.  Offsets out of order, or past
+ * `rows`, set it too: rows that lie within the output are written.
  * ------------------------------------------------------------------------ */
 size_t bd_kv_read_workspace_size(int64_t rows);
 

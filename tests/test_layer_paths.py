@@ -61,3 +61,34 @@ def test_pairs_over_ragged_chunks(dev, n_new, kv_len, n_q, n_kv, page, int8):
     ws = bd.new_workspace(bd.bd_attention_workspace_size(len(q), len(n_new), n_q, n_kv, 128), dev)
     again(lambda o: bd.bd_attention(q, off, cache, on["table"], lens, 128 ** -0.5, max(n_new), o, ws), out, 100)
     assert bd.bd_check_async(ws) == bd.BD_OK
+
+
+# ------------------------------------------------------------------------------- offsets of a read
+
+@pytest.mark.parametrize("n_seq", [1, 3, 700])
+def test_kv_read_reports_bad_offsets(dev, n_seq):
+    """Offsets that run backwards, start past 0, or end past the output's rows; what has a place is read."""
+    pool = torch.arange(16, dtype=torch.float32, device=dev).view(1, 1, 16, 1).expand(2, 1, 16, 64)
+    pool = pool.to(torch.bfloat16).contiguous()
+    cache, ws = bd.KvPages(pool, pool.clone()), bd.new_workspace(256, dev)
+    table = torch.zeros(n_seq, 1, dtype=torch.int32, device=dev)
+    good = [min(5 * s, 12) for s in range(n_seq + 1)]
+    rows = good[-1]
+
+    def read(off, rows):
+        ko, vo = (torch.full((rows, 1, 64), 3.0, device=dev, dtype=torch.bfloat16) for _ in range(2))
+        bd.bd_kv_read(cache, table, torch.tensor(off, dtype=torch.int32, device=dev), ko, vo, ws)
+        return bd.bd_check_async(ws), ko
+
+    want = torch.tensor([r - max(o for o in good if o <= r) for r in range(rows)], dtype=torch.float32)
+    status, ko = read(good, rows)
+    assert status == bd.BD_OK and torch.equal(ko[:, 0, 0].float().cpu(), want)
+    status, ko = read(good, rows - 1)
+    assert status == bd.BD_ERR_BAD_INDEX and torch.equal(ko[:, 0, 0].float().cpu(), want[:-1])
+    assert read([1] + good[1:], rows)[0] == bd.BD_ERR_BAD_INDEX
+    assert read([-2] + good[1:], rows)[0] == bd.BD_ERR_BAD_INDEX
+    if n_seq > 1:
+        back = list(good)
+        back[n_seq // 2] = good[-1] + 1
+        assert read(back, rows)[0] == bd.BD_ERR_BAD_INDEX
+    assert read(good, rows)[0] == bd.BD_OK
