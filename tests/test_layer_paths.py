@@ -3,7 +3,10 @@ choose between: clusters with many items, CTA pairs over ragged chunks, norms
 of many rows and of every row length's kernel, attention without a causal mask
 in few rows, and scales of any sign -- against the 64-bit definitions of
 layer_oracle.py, with its bounds."""
-import numpy as np
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -92,3 +95,101 @@ def test_kv_read_reports_bad_offsets(dev, n_seq):
         back[n_seq // 2] = good[-1] + 1
         assert read(back, rows)[0] == bd.BD_ERR_BAD_INDEX
     assert read(good, rows)[0] == bd.BD_OK
+
+
+# ------------------------------------------------------------------------------- norms of every kernel
+
+OUT = [torch.bfloat16, torch.float32, torch.float8_e4m3fn]
+
+
+def check_norm(dev, T, d, V, out_dtype, seed, residual=True, in_place=False):
+    h, y, ho, out, scale = ops.run_norm(dev, T, d, V, out_dtype, residual, seed=seed, in_place=in_place)
+    if residual:
+        ops.within(ho, h, ref.half_ulp_bf16(h) + h.abs() * 2 * ref.U32, "residual")
+    bound = y.abs() * ref.norm_rel(d)
+    if out_dtype == torch.bfloat16:
+        bound = bound + ref.half_ulp_bf16(y.abs() + bound)
+    if out_dtype != torch.float8_e4m3fn:
+        return ops.within(out, y, bound, "norm")
+    # the scale is off by the norm's error; a code by half its step and by the scale's error
+    s = y.abs().amax(1).clamp_min(1e-30) / 448
+    rel = ref.norm_rel(d) + 4 * ref.U32
+    ops.within(scale, s, s * rel, "scale")
+    z = (y / s[:, None]).abs()
+    half_step = torch.pow(2.0, torch.floor(torch.log2(z.clamp_min(2.0 ** -6))) - 4)
+    ops.within(out.float().cpu().double() * scale.cpu().double()[:, None], y,
+               s[:, None] * half_step * (1 + 2.0 ** -10) + y.abs() * 4 * rel, "codes")
+
+
+@pytest.mark.parametrize("out_dtype", OUT)
+@pytest.mark.parametrize("T,d,V", [
+    # more rows than the GPU has places for: a warp a row up to 512, then one, two, four groups a thread, and
+    # rows that are read twice
+    (700, 8, 0), (1001, 248, 3), (700, 256, 0), (901, 264, 14), (701, 512, 64), (320, 520, 0), (1300, 4096, 5),
+    (4096, 8192, 14), (700, 16384, 0), (305, 16392, 2), (400, 20480, 3), (310, 32768, 0), (306, 33000, 1),
+    # few rows of the same lengths
+    (5, 16392, 2), (3, 20480, 0), (2, 32768, 1)])
+def test_norm_kernels(dev, T, d, V, out_dtype):
+    check_norm(dev, T, d, V, out_dtype, seed=T + d)
+
+
+@pytest.mark.parametrize("T,d", [(700, 504), (900, 8192), (400, 20480), (308, 32776)])
+def test_norm_many_rows_in_place(dev, T, d):
+    check_norm(dev, T, d, 2, torch.bfloat16, seed=T, in_place=True)
+    check_norm(dev, T, d, 0, torch.float32, seed=T + 1, residual=False)
+
+
+# ------------------------------------------------------------------------------- masks and scales of attention
+
+FEW = [  # clusters, and caches that are dealt out; 2 to 16 rows a head
+    ([2], [300], 1, 1, 64, 16), ([3, 1], [70, 900], 8, 2, 128, 16), ([16], [513], 4, 4, 64, 64),
+    ([2, 5], [9000, 40], 8, 8, 128, 128), ([1] * 20 + [2], [1200 - 50 * i for i in range(21)], 16, 8, 64, 32),
+    ([2, 2], [0, 1], 8, 1, 128, 32)]
+MANY = [([40, 7], [130, 7], 8, 2, 64, 16), ([300, 1, 33], [700, 90, 33], 8, 2, 128, 64), ([9], [400], 4, 1, 128, 16),
+        ([70, 70], [0, 1], 4, 1, 64, 32)]
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("n_new,kv_len,n_q,n_kv,dim,page", FEW)
+def test_few_rows_without_a_causal_mask(dev, n_new, kv_len, n_q, n_kv, dim, page, int8):
+    ops.run_attention(dev, n_new, kv_len, n_q, n_kv, dim, page, int8, causal=False, seed=len(n_new) + dim)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("scale", [-0.1, 0.0, -1.0])
+@pytest.mark.parametrize("n_new,kv_len,n_q,n_kv,dim,page", FEW + MANY)
+def test_scales_of_any_sign(dev, n_new, kv_len, n_q, n_kv, dim, page, scale, int8):
+    """Below zero the largest products weigh least; at zero every key that a row sees weighs the same."""
+    causal = sum(kv_len) % 3 != 0
+    ops.run_attention(dev, n_new, kv_len, n_q, n_kv, dim, page, int8, causal=causal, seed=sum(kv_len) % 83, scale=scale)
+
+
+@pytest.mark.parametrize("n_new", [[1, 1], [40, 1]])
+def test_nan_query_stays_in_its_rows_int8(dev, n_new):
+    out, qd, on, off, ln = ops.run_attention(dev, n_new, [90, 90], 4, 2, 128, 16, True, seed=3)
+    q = qd.clone()
+    q[0, 1] = float("nan")
+    out2 = torch.empty_like(out)
+    ws = bd.new_workspace(bd.bd_attention_workspace_size(len(q), 2, 4, 2, 128), dev)
+    cache = bd.KvPages(on["k"], on["v"], on["ks"], on["vs"])
+    bd.bd_attention(q, off, cache, on["table"], ln, 128 ** -0.5, max(n_new), out2, ws)
+    assert out2[0, 1].isnan().all()
+    # (the rows of an item share the type of a step's products: the others keep their bounds, not their bits)
+    c = ref.paged(n_new, [90, 90], 2, 128, 16, True, seed=3)
+    want = ref.attention(qd.cpu(), off.tolist(), c["vals"]["k"], c["vals"]["v"], [90, 90], 128 ** -0.5, True)
+    out2[0, 1] = out[0, 1]
+    ops.within(out2, want[0], ref.attention_bounds(*want, 90)[0], "attention")
+
+
+# ------------------------------------------------------------------------------- the bounds-checked build
+
+def test_bounds_checked_build_on_these_paths(dev):
+    """The same tests through the library that checks each access (conftest.py asks it after every test)."""
+    from bit_weight_delta_bd_gb300 import build
+
+    lib = build.build(debug_bounds=True)
+    p = subprocess.run([sys.executable, "-m", "pytest", os.path.abspath(__file__), "-m", "gpu", "-x", "-q", "-k",
+                        "norm_kernels or norm_many or many_items or ragged_chunks or bad_offsets"],
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                       env=dict(os.environ, BD_LIBRARY=lib), capture_output=True, text=True, timeout=600)
+    assert p.returncode == 0, p.stdout[-4000:] + p.stderr[-2000:]
