@@ -31,10 +31,12 @@
 // stays below 2^15, with 11 bits where a bf16 cache's probabilities, rounded
 // to bf16 like its values, have 8.  A step with a product below 2^-14, where
 // fp16 loses bits, runs P V in bf16 instead (a dim in which the likeliest keys'
-// codes are 0 takes its value from the others, however small they are); that
-// takes a logic operation more for two codes: 92.5 us where all steps do, 88.0
-// where none does (4 sequences of up to 65538 keys, 64/8 heads; 86.7 without
-// the test).
+// codes are 0 takes its value from the others, however small they are).  The
+// step's large products then have 8 bits as well, as in a bf16 cache: a step
+// has one type, and two products for each step would cost more than the bits
+// are worth.  A bf16 step takes a logic operation more for two codes: 92.5 us
+// where all steps do, 88.0 where none does (4 sequences of up to 65538 keys,
+// 64/8 heads; 86.7 without the test).
 
 #include "bd_attention.cuh"
 
@@ -1093,12 +1095,14 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
 
 constexpr int kJoinThreads = 128;
 
-// Block (c, y): joins what block c of the main kernel noted down, a row per
-// warp and more where sequences have more rows than the host expects.  It has two latencies to wait for: what was noted down, then the parts
-// with their maxima, the first BATCH of them at once (in turn, with the
-// sequence's offsets before them, four: 27 us for the chunk of 4096 over 8192
-// keys, 64/8 heads, against 14).  A chunk's items have few parts and many
-// rows, which more warps at a time get through; a decode step's the reverse.
+// Block (c - 1, y) joins what block c of the main kernel noted down: a row per
+// warp, and more where sequences have more rows than the host expects.  It
+// waits twice, for what was noted down and then for the parts with their
+// maxima, the first BATCH parts at once.  (Where it waited four times, for the
+// sequence's offsets and for one part after another too, the chunk of 4096 over
+// 8192 keys, 64/8 heads, took 27 us for its join instead of 14.)  A chunk's
+// items have few parts and many rows, for which more warps at a time are
+// better; a decode step's have many parts and few rows.
 template <int DIM, int BATCH>
 __global__ void __launch_bounds__(kJoinThreads, BATCH <= 4 ? 12 : 4)
     attn_join_kernel(const __grid_constant__ AttnParams p)

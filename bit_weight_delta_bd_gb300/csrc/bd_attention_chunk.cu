@@ -13,19 +13,22 @@
 // turns, 3350 cycles for 128 keys and 256 rows of which the tensor cores
 // worked 2300.
 //
-// Pairs.  With head_dim 128 and more than 256 rows two CTAs work on an item of 512: the even
-// one's products cover both (M = 256), and each holds half of the operand that
-// they share, 32 keys of each step of K and 64 dims of V.  What bounds a single
-// CTA is its shared memory (a step of 64 reads Q twice as often as one of 128
-// would, and the 64-key product then runs at 3/4 of its rate); a pair reads 3/4
-// of that, and int8 tiles are converted once for 512 rows.  A chunk of 4096
-// tokens over 8192 keys, 64/8 heads: bf16 885 -> 812 us, int8 1245 -> 1110 (and
-// 785 .. 810 us, up to 1750 TFLOP/s, with O written by whole sectors, a row per
-// thread: 5 us of any call).  Sequences of up to 256 rows would fill a pair's first query
-// tile at most, which takes as long as both: 8 sequences of 4 tokens over 4000
-// keys take 48 us by single CTAs and 68 by pairs (int8).  With head_dim 64
-// half of V's dims would leave 64-byte rows, and the exponentials bound the
-// kernel: single CTAs, 715 us for bf16.
+// Pairs.  With head_dim 128 and sequences of more than 256 rows two CTAs work
+// on an item of 512: the even one's products cover both (M = 256), and each
+// holds half of the operand that they share, 32 keys of each step of K and 64
+// dims of V.  What bounds a single CTA is its shared memory (a step of 64 reads
+// Q twice as often as one of 128 would, and the 64-key product then runs at 3/4
+// of its rate); a pair reads 3/4 of that, and int8 tiles are converted once for
+// 512 rows.  A chunk of 4096 tokens over 8192 keys, 64/8 heads: bf16 885 us by
+// single CTAs and 812 by pairs, int8 1245 and 1110.  (O written by whole
+// sectors, a row per thread, takes 5 us less of any call: 765 .. 820 us for the
+// bf16 chunk as the clocks allow, 1670 to 1800 TFLOP/s.)
+// Sequences of up to 256 rows would fill a pair's first query tile at most,
+// which takes as long as both: 8 sequences of 4 tokens over 4000 int8 keys take
+// 45 us by single CTAs and 68 by pairs.  With head_dim 64 half of V's dims
+// would leave 64-byte rows: single CTAs, 717 us for bf16 and 1122 for int8,
+// which by their number should be the exponentials' time (as many as with
+// head_dim 128, for half the products; no measurement sets them apart).
 //
 // The running maximum that P is formed with lags behind the true one by at
 // most 2^8 (a row's sums are rescaled in tensor memory only when its maximum

@@ -423,14 +423,19 @@ bd_status bd_kv_read(const bd_kv_pages* cache, const int32_t* page_table, int64_
  *   lse      device fp32 [T][n_q] or NULL: log sum_j exp(scale * q . k_j)
  * The cache has at least one page (BD_ERR_UNSUPPORTED_SHAPE: new tokens are in it).
  * n_q: a positive multiple of n_kv.  Scores, the softmax and all sums are
- * fp32.  In a bf16 cache probabilities are rounded to bf16 before their
- * product with V.  Int8 codes enter the tensor cores exactly (in fp16 with q,
- * whose rows are scaled by a power of two so that bf16's 8 bits fit) and
- * their scales multiply the fp32 scores and probabilities; probability times
- * v_scale is then rounded once, to bf16, or to fp16 where its range allows.
- * Cached values up to 2^80 in magnitude give the formula's
- * result; beyond that a product may overflow.  Results do not depend on
- * timing (no atomics).  A page outside [0, n_pages), a length outside
+ * fp32.  What is rounded to 16 bits before its product, beside q and a bf16
+ * cache that are so already:
+ *   - probabilities over a bf16 cache, to bf16;
+ *   - over an int8 cache, probability times v_scale: to bf16 in the kernel for
+ *     chunks; in the one for few rows (decode steps: up to 16 for each kv head
+ *     of a sequence) to fp16, of 11 bits, but where one of 32 keys' products is
+ *     too small for fp16's range all of theirs are rounded to bf16, of 8.
+ * Int8 codes enter the tensor cores exactly (K's in fp16 with q, whose rows are
+ * scaled by a power of two so that bf16's 8 bits fit), and their scales
+ * multiply the fp32 scores and probabilities.
+ * Cached values up to 2^80 in magnitude give the formula's result; beyond that
+ * a product may overflow.  Results do not depend on timing (no atomics).  A
+ * page outside [0, n_pages), a length outside
  * [0, max_pages * page_size] or offsets out of order set BD_ERR_BAD_INDEX:
  * the value is clamped and the sequence's result is undefined.
  * ------------------------------------------------------------------------ */
