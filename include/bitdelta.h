@@ -434,7 +434,7 @@ bd_status bd_kv_read(const bd_kv_pages* cache, const int32_t* page_table, int64_
  * scaled by a power of two so that bf16's 8 bits fit), and their scales
  * multiply the fp32 scores and probabilities.
  * Cached values up to 2^80 in magnitude give the formula's result; beyond that
- * a product may overflow.  Results do not depend on timing (no atomics).  A
+ * a product may overflow, and a result below 2^-125 may come out as 0.  Results do not depend on timing (no atomics).  A
  * page outside [0, n_pages), a length outside
  * [0, max_pages * page_size] or offsets out of order set BD_ERR_BAD_INDEX:
  * the value is clamped and the sequence's result is undefined.
