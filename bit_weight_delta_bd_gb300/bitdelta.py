@@ -46,6 +46,7 @@ BD_OUT_F32 = 1
 BD_OUT_E4M3 = 2
 BD_KV_BF16 = 0
 BD_KV_INT8 = 1
+BD_KV_INT4 = 2
 BD_MAX_AXES = 4
 BD_MAX_VARIANTS = 64
 BD_NOALLOC_MAX_ROWS = 262144
@@ -63,6 +64,7 @@ EXPORTS = (
     "bd_cache_get_stats", "bd_cache_query", "bd_cache_debug_fail_load", "bd_materialize",
     "bd_monosoup_workspace_size", "bd_monosoup_merge",
     "bd_rms_norm_workspace_size", "bd_rms_norm",
+    "bd_block_norm_workspace_size", "bd_block_norm",
     "bd_rope_append_workspace_size", "bd_rope_append",
     "bd_kv_read_workspace_size", "bd_kv_read",
     "bd_attention_workspace_size", "bd_attention",
@@ -133,6 +135,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             "bd_rms_norm_workspace_size": ([_i64, _i64], _sz),
             "bd_rms_norm": ([_vp, _vp, _i64, _i64, _vp, _vp, _i32, _vp, ctypes.c_float, _vp, _vp, _int, _vp, _vp, _sz,
                              _vp], _int),
+            "bd_block_norm_workspace_size": ([_i64, _i64], _sz),
+            "bd_block_norm": ([_vp, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp, ctypes.c_float, ctypes.c_float, _vp, _vp,
+                               _vp, _i32, ctypes.c_float, _vp, _vp, _int, _vp, _vp, _sz, _vp], _int),
             "bd_rope_append_workspace_size": ([_i64], _sz),
             "bd_rope_append": ([_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i32, _vp, _i32, _vp, _vp, _i64, _i32, _int,
                                 _vp, _vp, _vp, _i64, _vp, _sz, _vp], _int),
@@ -368,6 +373,62 @@ def bd_rms_norm(x, gain, eps, out, ws, residual=None, residual_out=None, scale=N
                               wsp, wsn, _stream(stream, dev)), "bd_rms_norm")
 
 
+def bd_block_norm_workspace_size(T: int, d: int) -> int:
+    return int(load().bd_block_norm_workspace_size(T, d))
+
+
+def bd_block_norm(x, residual, gain, eps, out, ws, residual_out=None, post_gain=None, gate=None, gate_idx=None,
+                  block_scale: float = 1.0, residual_scale: float = 1.0, scale=None, vid=None, gain_list=(),
+                  post_gain_list=(), stream=None) -> None:
+    """The norms around a block that gave x: h = residual_scale * residual + block_scale * gate * norm(x) * post_gain,
+    out = norm(h) * gain; residual_out (which may be residual itself) receives h.  post_gain None: x enters as it is.
+    gate: [d] or [rows][d], one row for all tokens, a row for each, or row gate_idx[t] for token t.  Token t takes the
+    gains of its variant, vid[t], out of gain_list and post_gain_list; out bf16, fp32, or e4m3 with scale [T]."""
+    shape = x.shape
+    T, d = shape
+    dev = _device()
+    if gain.shape != (d,) or out.shape != shape or residual.shape != shape:
+        raise ValueError("gain must have the shape [d], out and residual that of x")
+    if residual_out is not None and residual_out.shape != shape:
+        raise ValueError("residual_out's shape differs from x")
+    if post_gain is not None and post_gain.shape != (d,):
+        raise ValueError("post_gain must have the shape [d]")
+    if scale is not None and scale.numel() != T:
+        raise ValueError("scale must have one value per row")
+    if vid is not None and vid.numel() != T:
+        raise ValueError("vid must have one id per row")
+    gate_rows = 0
+    if gate is not None:
+        if gate.shape[-1] != d or gate.dim() > 2:
+            raise ValueError("gate must have the shape [d] or [rows][d]")
+        gate_rows = gate.shape[0] if gate.dim() == 2 else 1
+    if gate_idx is not None and (gate is None or gate_idx.numel() != T):
+        raise ValueError("gate_idx must have one row of gate per token")
+    tab = post_tab = None
+    V = 0
+    if vid is not None:
+        V = len(gain_list)
+        if post_gain is not None and len(post_gain_list) != V:
+            raise ValueError("gain_list and post_gain_list differ in length")
+        table = _row_ptrs(gain_list, d, "gain", dev)
+        tab = table.buffer_info()[0] if V else None
+        if post_gain is not None:
+            post_table = _row_ptrs(post_gain_list, d, "post_gain", dev)
+            post_tab = post_table.buffer_info()[0] if V else None
+    out_dtype = _OUT_DTYPES.get(out.dtype)
+    if out_dtype is None:
+        raise ValueError(f"out has dtype {out.dtype}, expected bfloat16, float32 or float8_e4m3fn")
+    wsp, wsn = _ws(ws, dev)
+    _check(load().bd_block_norm(_ptr(x, "x", _BF16_LIKE, False, dev), _ptr(residual, "residual", _BF16_LIKE, False, dev),
+                                T, d, _ptr(post_gain, "post_gain", _BF16_LIKE, True, dev), post_tab,
+                                _ptr(gate, "gate", _BF16_LIKE, True, dev), gate_rows,
+                                _ptr(gate_idx, "gate_idx", _I32, True, dev), block_scale, residual_scale,
+                                _ptr(gain, "gain", _BF16_LIKE, False, dev), tab, _ptr(vid, "vid", _I32, True, dev), V,
+                                eps, _ptr(residual_out, "residual_out", _BF16_LIKE, True, dev),
+                                _ptr(out, "out", None, False, dev), out_dtype, _ptr(scale, "scale", _F32, True, dev),
+                                wsp, wsn, _stream(stream, dev)), "bd_block_norm")
+
+
 _OUT_DTYPES = {torch.bfloat16: BD_OUT_BF16, torch.float32: BD_OUT_F32, torch.float8_e4m3fn: BD_OUT_E4M3}
 
 
@@ -379,23 +440,29 @@ class _KvPages(ctypes.Structure):
 
 class KvPages:
     """One layer's paged KV cache: ``k`` and ``v`` [n_pages][n_kv][page_size][head_dim] as torch.bfloat16 or, with
-    ``k_scale`` and ``v_scale`` [n_pages][n_kv][page_size] fp32, as torch.int8 codes.  Keeps the tensors referenced."""
+    ``k_scale`` and ``v_scale`` [n_pages][n_kv][page_size] fp32, as torch.int8 codes, or [..][head_dim / 2] as
+    torch.uint8, two 4-bit codes a byte, with scales [n_pages][n_kv][page_size][head_dim / 32][2] bf16: (scale, lowest
+    value) of each group of 32 elements.  Keeps the tensors referenced."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
             raise ValueError("k and v must be [n_pages][n_kv][page_size][head_dim] of one dtype")
-        int8 = k.dtype == torch.int8
-        if int8 != (k_scale is not None) or int8 != (v_scale is not None):
-            raise ValueError("scales belong to an int8 cache, and to it alone")
-        dt = (torch.int8,) if int8 else _BF16_LIKE
-        for t in (k_scale, v_scale):
-            if t is not None and tuple(t.shape) != tuple(k.shape[:3]):
-                raise ValueError("scales must be [n_pages][n_kv][page_size]")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        int8, int4 = k.dtype == torch.int8, k.dtype == torch.uint8
+        if (int8 or int4) != (k_scale is not None) or (int8 or int4) != (v_scale is not None):
+            raise ValueError("scales belong to an int8 or a 4-bit cache, and to them alone")
+        dt = (k.dtype,) if int8 or int4 else _BF16_LIKE
         self.n_pages, self.n_kv, self.page_size, self.head_dim = (int(n) for n in k.shape)
-        self._c = _KvPages(_ptr(k, "k", dt), _ptr(v, "v", dt), _ptr(k_scale, "k_scale", (torch.float32,), True),
-                           _ptr(v_scale, "v_scale", (torch.float32,), True), self.n_pages, self.page_size, self.n_kv,
-                           self.head_dim, BD_KV_INT8 if int8 else BD_KV_BF16)
+        per, st = tuple(k.shape[:3]), _F32
+        if int4:
+            self.head_dim *= 2
+            per, st = (*per, self.head_dim // 32, 2), _BF16_LIKE
+        for t in (k_scale, v_scale):
+            if t is not None and tuple(t.shape) != per:
+                raise ValueError("scales must be [n_pages][n_kv][page_size], of 4-bit codes [..][head_dim / 32][2]")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._c = _KvPages(_ptr(k, "k", dt), _ptr(v, "v", dt), _ptr(k_scale, "k_scale", st, True),
+                           _ptr(v_scale, "v_scale", st, True), self.n_pages, self.page_size, self.n_kv,
+                           self.head_dim, BD_KV_INT8 if int8 else BD_KV_INT4 if int4 else BD_KV_BF16)
         self._addr = ctypes.addressof(self._c)
         self._dev = k.get_device()
 

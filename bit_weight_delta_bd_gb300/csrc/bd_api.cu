@@ -523,24 +523,103 @@ bd_status bd_rms_norm(const uint16_t* x, const uint16_t* residual, int64_t T, in
     return launched(bd::launch_rms_norm(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
+// ------------------------------------------------------------------ norms around a block
+
+size_t bd_block_norm_workspace_size(int64_t /*T*/, int64_t /*d*/) { return kWsHeader; }
+
+bd_status bd_block_norm(const uint16_t* x, const uint16_t* residual, int64_t T, int64_t d, const uint16_t* post_gain,
+                        const uint16_t* const* post_gain_tab, const uint16_t* gate, int64_t gate_rows,
+                        const int32_t* gate_idx, float block_scale, float residual_scale, const uint16_t* gain,
+                        const uint16_t* const* gain_tab, const int32_t* vid, int32_t V, float eps,
+                        uint16_t* residual_out, void* out, int out_dtype, float* scale, void* ws, size_t ws_bytes,
+                        void* stream)
+{
+    BD_NVTX_RANGE("bd_block_norm");
+    if (out_dtype != BD_OUT_BF16 && out_dtype != BD_OUT_F32 && out_dtype != BD_OUT_E4M3) return BD_ERR_INVALID_ARG;
+    if (V < 0 || V > BD_MAX_VARIANTS || !(eps >= 0.0f)) return BD_ERR_INVALID_ARG;
+    if (!(block_scale - block_scale == 0.0f) || !(residual_scale - residual_scale == 0.0f))
+        return BD_ERR_INVALID_ARG;  // not finite
+    if (T < 0 || T > INT32_MAX || d <= 0 || d % 8 != 0 || gate_rows < 0 || gate_rows > INT32_MAX)
+        return BD_ERR_UNSUPPORTED_SHAPE;
+    if (bd_status s = check_ws(ws, ws_bytes, bd_block_norm_workspace_size(T, d))) return s;
+    if (T == 0) return BD_OK;
+    if (!x || !residual || !gain || !out || (out_dtype == BD_OUT_E4M3) != (scale != nullptr)) return BD_ERR_INVALID_ARG;
+    if (vid && V > 0 && (!gain_tab || (post_gain && !post_gain_tab))) return BD_ERR_INVALID_ARG;
+    // without gate_idx: one gate for all tokens, or each token's own
+    if (gate ? gate_rows < 1 || (!gate_idx && gate_rows != 1 && gate_rows != T) : gate_idx != nullptr)
+        return BD_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(residual_out, 16) || !aligned(gain, 16) ||
+        !aligned(post_gain, 16) || !aligned(gate, 16) || !aligned(gate_idx, 4) || !aligned(out, 16) ||
+        !aligned(vid, 4) || !aligned(scale, 4))
+        return BD_ERR_MISALIGNED;
+    const size_t n = static_cast<size_t>(T) * static_cast<size_t>(d), g = static_cast<size_t>(d) * 2;
+    const size_t obytes = n * (out_dtype == BD_OUT_F32 ? 4 : out_dtype == BD_OUT_BF16 ? 2 : 1);
+    const size_t tbytes = static_cast<size_t>(T) * 4, gbytes = static_cast<size_t>(gate_rows) * g;
+    const auto written_over = [&](const void* in, size_t bytes) {  // by an output other than residual_out
+        return overlaps(out, obytes, in, bytes) || overlaps(scale, tbytes, in, bytes);
+    };
+    const auto met = [&](const void* in, size_t bytes) {  // by any output
+        return written_over(in, bytes) || overlaps(residual_out, n * 2, in, bytes);
+    };
+    if (written_over(x, n * 2) || written_over(residual, n * 2) || written_over(residual_out, n * 2) || met(gain, g) ||
+        met(post_gain, g) || met(gate, gbytes) || met(gate_idx, tbytes) || met(vid, tbytes) || met(ws, ws_bytes) ||
+        overlaps(out, obytes, scale, tbytes) || (residual_out != x && overlaps(residual_out, n * 2, x, n * 2)) ||
+        (residual_out != residual && overlaps(residual_out, n * 2, residual, n * 2)))
+        return BD_ERR_INVALID_ARG;
+    bd::BlockNormArgs a{};
+    if (vid) {
+        for (int32_t v = 0; v < V; ++v) {
+            for (const uint16_t* w : {gain_tab[v], post_gain ? post_gain_tab[v] : gain_tab[v]}) {
+                if (!w) return BD_ERR_INVALID_ARG;
+                if (!aligned(w, 16)) return BD_ERR_MISALIGNED;
+                if (met(w, g)) return BD_ERR_INVALID_ARG;
+            }
+            a.gains[v] = gain_tab[v];
+            if (post_gain) a.post_gains[v] = post_gain_tab[v];
+        }
+    }
+    int sms = 0;
+    if (bd_status s = device_info(&sms)) return s;
+    a.x = x;
+    a.residual = residual;
+    a.residual_out = residual_out;
+    a.post_gain = post_gain;
+    a.gain = gain;
+    a.gate = gate;
+    a.gate_rows = gate_rows;
+    a.gate_idx = gate_idx;
+    a.vid = vid;
+    a.V = V;
+    a.block_scale = block_scale;
+    a.residual_scale = residual_scale;
+    a.T = T;
+    a.d = d;
+    a.eps = eps;
+    a.out = out;
+    a.out_dtype = out_dtype;
+    a.scale = scale;
+    a.err = err_word(ws);
+    return launched(bd::launch_block_norm(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
 // ------------------------------------------------------------------ paged KV cache
 
 // A cache's shape, pointers and alignment; *out is what the kernels take.
 static bd_status check_kv_pages(const bd_kv_pages* c, bd::KvPages* out)
 {
     if (!c) return BD_ERR_INVALID_ARG;
-    if (c->dtype != BD_KV_BF16 && c->dtype != BD_KV_INT8) return BD_ERR_INVALID_ARG;
+    if (c->dtype != BD_KV_BF16 && c->dtype != BD_KV_INT8 && c->dtype != BD_KV_INT4) return BD_ERR_INVALID_ARG;
     int shift = 4;
     while (shift < 7 && (1 << shift) < c->page_size) ++shift;
     if ((1 << shift) != c->page_size || (c->head_dim != 64 && c->head_dim != 128) || c->n_kv < 1 || c->n_kv > 1024 ||
         c->n_pages < 0 || c->n_pages > INT32_MAX / c->n_kv || c->n_pages > INT32_MAX / c->page_size)
         return BD_ERR_UNSUPPORTED_SHAPE;
-    const bool int8 = c->dtype == BD_KV_INT8;
-    if (!c->k || !c->v || (int8 && (!c->k_scale || !c->v_scale))) return BD_ERR_INVALID_ARG;
-    if (!aligned(c->k, 16) || !aligned(c->v, 16) || (int8 && (!aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))))
+    const bool codes = c->dtype != BD_KV_BF16;
+    if (!c->k || !c->v || (codes && (!c->k_scale || !c->v_scale))) return BD_ERR_INVALID_ARG;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || (codes && (!aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))))
         return BD_ERR_MISALIGNED;
-    *out = bd::KvPages{c->k, c->v, int8 ? c->k_scale : nullptr, int8 ? c->v_scale : nullptr, c->n_pages, c->page_size,
-                       shift, c->n_kv, c->head_dim, int8 ? 1 : 0};
+    *out = bd::KvPages{c->k, c->v, codes ? c->k_scale : nullptr, codes ? c->v_scale : nullptr, c->n_pages, c->page_size,
+                       shift, c->n_kv, c->head_dim, c->dtype == BD_KV_INT8, c->dtype == BD_KV_INT4};
     return BD_OK;
 }
 
@@ -552,9 +631,10 @@ static size_t kv_vectors(const bd::KvPages& c)
 // Whether [p, p + n) meets any buffer of the cache.
 static bool meets_cache(const bd::KvPages& c, const void* p, size_t n)
 {
-    const size_t vec = kv_vectors(c), bytes = vec * static_cast<size_t>(c.dim) * (c.int8 ? 1 : 2);
-    return overlaps(p, n, c.k, bytes) || overlaps(p, n, c.v, bytes) || overlaps(p, n, c.k_scale, vec * 4) ||
-           overlaps(p, n, c.v_scale, vec * 4);
+    const size_t vec = kv_vectors(c), dim = static_cast<size_t>(c.dim);
+    const size_t bytes = vec * (c.int4 ? dim / 2 : c.int8 ? dim : 2 * dim), sb = vec * (c.int4 ? dim / 32 : 1) * 4;
+    return overlaps(p, n, c.k, bytes) || overlaps(p, n, c.v, bytes) || overlaps(p, n, c.k_scale, sb) ||
+           overlaps(p, n, c.v_scale, sb);
 }
 
 // Bytes from the first to the last element of T strided rows.
@@ -746,7 +826,8 @@ int bd_debug_bounds_check(uint32_t* kernels)
 {
     const uint32_t f = bd::bounds_take_compress() | bd::bounds_take_skinny() | bd::bounds_take_multi() |
                        bd::bounds_take_prefill() | bd::bounds_take_route() | bd::bounds_take_materialize() |
-                       bd::bounds_take_monosoup() | bd::bounds_take_norm() | bd::bounds_take_kv() |
+                       bd::bounds_take_monosoup() | bd::bounds_take_norm() | bd::bounds_take_block_norm() |
+                       bd::bounds_take_kv() |
                        bd::bounds_take_attention() | bd::bounds_take_attention_chunk();
     if (kernels) *kernels = f;
     if (f == ~0u) return BD_ERR_CUDA;

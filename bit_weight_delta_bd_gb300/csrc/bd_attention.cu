@@ -1342,7 +1342,7 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream)
     cudaError_t err = cudaSuccess;
     // new tokens and rows of a sequence, as far as the host knows
     const int64_t max_new = a.max_new < a.T ? a.max_new : a.T, rows = max_new * p.G;
-    if (rows <= kMmaMaxRows) {
+    if (rows <= kMmaMaxRows && !a.cache.int4) {
         launch_few_rows(err, p, static_cast<int>(rows), false, ws, stream);
         return err;
     }
@@ -1353,7 +1353,7 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream)
     // 7 108 / 108, 31 168 / 218; int8 109 / 101, 122 / 143, 157 / 302).  Not
     // where the number of tokens says that all sequences have max_new, nor for
     // few sequences, nor for chunks so small that the launch costs too much.
-    const bool split = rows >= 128 && a.n_seq >= 4 && a.T < a.n_seq * max_new;
+    const bool split = !a.cache.int4 && rows >= 128 && a.n_seq >= 4 && a.T < a.n_seq * max_new;
     if (split) p.rows_above = kMmaMaxRows;
     launch_chunks(err, p, rows, ws, stream);
     if (split) {

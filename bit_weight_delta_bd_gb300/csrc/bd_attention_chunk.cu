@@ -53,7 +53,12 @@
 // Warps: 0..3 and 4..7 softmax of query tiles 0 and 1 (and loading Q, and
 // writing O); 8 TMA; 9 and 10 MMA of query tiles 0 and 1 (of a pair: the even
 // CTA's); 11 passes on that a pair's tiles are there (bf16: landed, int8: the
-// odd CTA's converted); 12..15 conversion (int8).
+// odd CTA's converted); 12..15 conversion (int8, 4 bits).
+//
+// 4-bit keys and values: TMA and bulk copies bring the codes with their groups'
+// scales and lowest values, and the fourth warpgroup forms code * scale + low,
+// rounded once to bf16: what a bf16 cache of the same values would hold.  All
+// that follows is as for bf16.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -65,6 +70,7 @@
 namespace bd {
 namespace {
 
+constexpr int kBf16 = 0, kInt8 = 1, kInt4 = 2;  // what the cache holds
 constexpr int kTile = 128;       // keys of a tile
 constexpr int kQRows = 128;      // rows of a query tile
 constexpr int kStep = 64;        // keys of a step
@@ -77,19 +83,24 @@ struct ChunkParams {
     AttnParams p;
 };
 
-template <int DIM, bool INT8, bool PAIR>
+template <int DIM, int KIND, bool PAIR>
 struct ChunkShape {
     static constexpr bool kPair = PAIR;
     static constexpr int kCtas = kPair ? 2 : 1;
-    static constexpr int kThreads = INT8 ? 512 : 384;
+    static constexpr bool INT8 = KIND == kInt8, INT4 = KIND == kInt4, kCodes = INT8 || INT4;
+    static constexpr int kThreads = kCodes ? 512 : 384;
     static constexpr bool kSmall = PAIR || DIM == 64;  // tiles of 16 KB
-    static constexpr int kBufs = INT8 ? (kSmall ? 6 : 3) : kSmall ? 8 : 5;  // bf16 tiles in shared memory
-    static constexpr int kRaw = INT8 ? (kSmall ? 6 : 3) : 0;                // tiles of codes
+    // bf16 tiles in shared memory, and tiles of codes
+    static constexpr int kBufs = INT8 ? (kSmall ? 6 : 3) : INT4 ? (kSmall ? 8 : 4) : kSmall ? 8 : 5;
+    static constexpr int kRaw = INT8 ? (kSmall ? 6 : 3) : INT4 ? (kSmall ? 5 : 3) : 0;
     static constexpr int kScaleBufs = INT8 ? (kSmall ? 4 : 3) : 0;          // scales of a key tile, K and V
     // a CTA's part of a tile: in a pair half the keys of each step of K, half the dims of V
     static constexpr int kKeysK = kTile / kCtas, kDimsV = DIM / kCtas;
     static constexpr int kTileBytes = kTile * DIM * 2 / kCtas;
-    static constexpr int kRawBytes = kTile * DIM / kCtas;
+    // 4 bits: codes, then the groups' scales and lowest values, whole rows of them
+    static constexpr int kPairBytes = DIM / 8;  // of a row
+    static constexpr int kCodeBytes = kTile * DIM / kCtas / (INT4 ? 2 : 1);
+    static constexpr int kRawBytes = kCodeBytes + (INT4 ? kTile * kPairBytes : 0);
     static constexpr int kQBytes = kQRows * DIM * 2;
     static constexpr int kOffBufs = 2 * kQBytes;
     static constexpr int kOffRaw = kOffBufs + kBufs * kTileBytes;
@@ -97,9 +108,9 @@ struct ChunkShape {
     static constexpr int kBytes = kOffScale + kScaleBufs * 2 * kTile * 4;
     // registers of a softmax thread, and of the others: the sum over the
     // warpgroups is what the block was launched with
-    static constexpr int kSoftRegs = INT8 ? 168 : 208;
+    static constexpr int kSoftRegs = kCodes ? 168 : 208;
     static constexpr int kOtherRegs = 88;
-    static_assert(2 * kSoftRegs + (INT8 ? 2 : 1) * kOtherRegs <= (INT8 ? 4 * 128 : 3 * 168), "register split");
+    static_assert(2 * kSoftRegs + (kCodes ? 2 : 1) * kOtherRegs <= (kCodes ? 4 * 128 : 3 * 168), "register split");
 };
 
 constexpr int kMaxBufs = 8, kMaxRaw = 6, kMaxScales = 4;
@@ -406,6 +417,59 @@ __device__ __forceinline__ void convert_tile(const uint8_t* src, uint8_t* dst, i
     }
 }
 
+// Byte offset of 16-byte chunk c of row t in a tile of 64- or 32-byte rows
+// (TMA's swizzles).
+template <int ROW_BYTES>
+__device__ __forceinline__ int swizzled_codes(int t, int c)
+{
+    return ROW_BYTES == 64 ? t * 64 + ((c ^ ((t >> 1) & 3)) << 4) : t * 32 + ((c ^ ((t >> 2) & 1)) << 4);
+}
+
+// 8 4-bit codes as 8 bf16 values code * scale + low: 0x4300 | code is 128 + code.
+__device__ __forceinline__ uint4 values4(uint32_t w, __nv_bfloat162 scale, __nv_bfloat162 low)
+{
+    const __nv_bfloat162 offset = __float2bfloat162_rn(128.0f);
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t x = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+        const __nv_bfloat162 v = __hfma2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), offset), scale, low);
+        r[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// A tile of 4-bit codes with their scales and lowest values as a tile of bf16
+// values, a group of 32 a thread, by the 128 threads of a warpgroup.  Eight
+// neighbouring lanes take the same group of 8 keys in a row: reads and writes
+// of 16 bytes meet in no bank.  DIM: values of a row; KEYS: rows of the tile;
+// PAIRS: words of scales of a row, of which this tile's are the DIM / 32 from
+// first on.  Rows from `valid` on become zeros (what lies there may be anything).
+template <int DIM, int KEYS, int PAIRS>
+__device__ __forceinline__ void convert_tile4(const uint8_t* src, const uint8_t* pairs, int first, int valid,
+                                              uint8_t* dst, int tid)
+{
+    constexpr int kGroups = DIM / 32, kKeys = 128 / kGroups;  // of a round
+    const int g = (tid >> 3) & (kGroups - 1), key0 = (tid & 7) + 8 * (tid / (8 * kGroups));
+    uint8_t* half = dst + (g >> 1) * (KEYS * 128);
+#pragma unroll 2
+    for (int i = 0; i < KEYS / kKeys; ++i) {
+        const int key = key0 + i * kKeys;
+        const uint4 c = *reinterpret_cast<const uint4*>(src + swizzled_codes<DIM / 2>(key, g));
+        const uint32_t pair = *reinterpret_cast<const uint32_t*>(pairs + (key * PAIRS + first + g) * 4);
+        const uint32_t s2 = __byte_perm(pair, 0, 0x1010), l2 = __byte_perm(pair, 0, 0x3232);
+        const __nv_bfloat162 scale = *reinterpret_cast<const __nv_bfloat162*>(&s2);
+        const __nv_bfloat162 low = *reinterpret_cast<const __nv_bfloat162*>(&l2);
+        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint4 v = values4(w[j], scale, low);
+            if (key >= valid) v = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(half + key * 128 + (((4 * (g & 1) + j) ^ (key & 7)) << 4)) = v;
+        }
+    }
+}
+
 // What a block does next: key tiles [t0, t1) of one (item, kv head).
 struct Segment {
     AttnItem it;
@@ -531,12 +595,12 @@ __device__ __forceinline__ float load_q(const AttnParams& p, const Segment& s, i
     return back;
 }
 
-template <int DIM, bool INT8, bool PAIR>
-__global__ void __launch_bounds__(ChunkShape<DIM, INT8, PAIR>::kThreads, 1)
+template <int DIM, int KIND, bool PAIR>
+__global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
     attn_chunk_kernel(const __grid_constant__ ChunkParams cp)
 {
-    using S = ChunkShape<DIM, INT8, PAIR>;
-    constexpr bool kPair = PAIR;
+    using S = ChunkShape<DIM, KIND, PAIR>;
+    constexpr bool kPair = PAIR, INT8 = S::INT8, INT4 = S::INT4, kCodes = S::kCodes;
     extern __shared__ __align__(1024) uint8_t dyn[];
     ChunkShared& sh = *reinterpret_cast<ChunkShared*>(dyn + S::kBytes);
     const AttnParams& p = cp.p;
@@ -549,10 +613,10 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8, PAIR>::kThreads, 1)
     grid_launch_dependents();
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kBufs; ++i) {
-            // (int8: four warps of the even CTA, and what the odd one passes on)
-            mbar_init(&sh.full[i], INT8 ? 3 + S::kCtas : S::kCtas);
+            // (codes: four warps of the even CTA, and what the odd one passes on)
+            mbar_init(&sh.full[i], kCodes ? 3 + S::kCtas : S::kCtas);
             mbar_init(&sh.empty[i], 2);
-            mbar_init(&sh.landed[i], INT8 ? 4 : 1);
+            mbar_init(&sh.landed[i], kCodes ? 4 : 1);
         }
         for (int i = 0; i < S::kRaw; ++i) {
             mbar_init(&sh.raw_full[i], 1);
@@ -840,9 +904,9 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8, PAIR>::kThreads, 1)
         reg_dec<S::kOtherRegs>();
         if (warp == kTmaWarp) {
             // ---------------------------------------------------- TMA
-            constexpr int kRing = INT8 ? S::kRaw : S::kBufs;
-            uint64_t* full = INT8 ? sh.raw_full : kPair ? sh.landed : sh.full;
-            uint64_t* empty = INT8 ? sh.raw_empty : sh.empty;
+            constexpr int kRing = kCodes ? S::kRaw : S::kBufs;
+            uint64_t* full = kCodes ? sh.raw_full : kPair ? sh.landed : sh.full;
+            uint64_t* empty = kCodes ? sh.raw_empty : sh.empty;
             const int pages_per_tile = kTile / cache.page;  // (at most 128 keys a page)
             // K of a pair: boxes of up to 32 keys, the CTA's half of each step of 64
             const int box_k = kPair && cache.page > 32 ? 32 : cache.page;
@@ -900,14 +964,23 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8, PAIR>::kThreads, 1)
                     }
                     for (int kv = 0; kv < 2; ++kv) {
                         if (!(ok = warp_wait(&sh.abort, &empty[buf], phase ^ 1))) break;
-                        constexpr int kBytes = INT8 ? 1 : 2;
-                        if (lane == 0)
-                            mbar_arrive_expect_tx(&full[buf], (kv ? rows * S::kDimsV : rows_k * DIM) * kBytes);
+                        // bytes of a row of K and of V
+                        constexpr uint32_t kRowK = INT4 ? DIM / 2 + S::kPairBytes : INT8 ? DIM : 2 * DIM;
+                        constexpr uint32_t kRowV = INT4   ? S::kDimsV / 2 + S::kPairBytes
+                                                   : INT8 ? S::kDimsV : 2 * S::kDimsV;
+                        if (lane == 0) mbar_arrive_expect_tx(&full[buf], kv ? rows * kRowV : rows_k * kRowK);
                         __syncwarp();
-                        uint8_t* dst = dyn + (INT8 ? S::kOffRaw + buf * S::kRawBytes : S::kOffBufs + buf * S::kTileBytes);
+                        uint8_t* dst =
+                            dyn + (kCodes ? S::kOffRaw + buf * S::kRawBytes : S::kOffBufs + buf * S::kTileBytes);
                         if (kv == 0 && mine_k) {
                             const int row = key_k & (cache.page - 1), to = lane * box_k;
-                            if constexpr (INT8) {
+                            if constexpr (INT4) {
+                                tma_load_3d(dst + to * (DIM / 2), &cp.k_map, 0, row, outer_k, &full[buf]);
+                                const int64_t vec = (static_cast<int64_t>(outer_k) << cache.page_shift) + row;
+                                bulk_g2s(dst + S::kCodeBytes + to * S::kPairBytes,
+                                         reinterpret_cast<const uint8_t*>(cache.k_scale) + vec * S::kPairBytes,
+                                         box_k * S::kPairBytes, &full[buf]);
+                            } else if constexpr (INT8) {
                                 tma_load_3d(dst + to * DIM, &cp.k_map, 0, row, outer_k, &full[buf]);
                             } else {
 #pragma unroll
@@ -918,7 +991,14 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8, PAIR>::kThreads, 1)
                         }
                         if (kv == 1 && mine) {
                             const int to = lane * cache.page;
-                            if constexpr (INT8) {
+                            if constexpr (INT4) {
+                                tma_load_3d(dst + to * (S::kDimsV / 2), &cp.v_map, rank * (S::kDimsV / 2), 0, outer,
+                                            &full[buf]);
+                                const int64_t vec = static_cast<int64_t>(outer) << cache.page_shift;
+                                bulk_g2s(dst + S::kCodeBytes + to * S::kPairBytes,
+                                         reinterpret_cast<const uint8_t*>(cache.v_scale) + vec * S::kPairBytes,
+                                         cache.page * S::kPairBytes, &full[buf]);
+                            } else if constexpr (INT8) {
                                 tma_load_3d(dst + to * S::kDimsV, &cp.v_map, rank * S::kDimsV, 0, outer, &full[buf]);
                             } else {
 #pragma unroll
@@ -977,7 +1057,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8, PAIR>::kThreads, 1)
                     const bool pv = j >= 2 * s.t0 + 2, qk = j < 2 * s.t1;
                     if (pv && b == 0) {
                         bv = take();
-                        if constexpr (!INT8 && !kPair)
+                        if constexpr (!kCodes && !kPair)
                             zero_past<S::kDimsV>(dyn + S::kOffBufs + bv * S::kTileBytes,
                                                  s.sq.len - (j - 2) * kStep, lane);
                     }
@@ -1020,7 +1100,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8, PAIR>::kThreads, 1)
             if (elect_one()) commit_both<kPair>(&sh.done);
             __syncwarp();
             mbar_wait_bounded(&sh.done, 0);
-        } else if (kPair && warp == kPassWarp && (!INT8 || rank != 0)) {
+        } else if (kPair && warp == kPassWarp && (!kCodes || rank != 0)) {
             // ---------------------------------------------------- this CTA's parts are there
             // A release at cluster scope waits for the warp's writes on their way: by the converting
             // warps themselves an int8 chunk of 4096 over 8192 keys takes 1211 us, by this warp, which
@@ -1032,8 +1112,8 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8, PAIR>::kThreads, 1)
 #pragma unroll 1
                 for (int n = 0; n < 2 * (s.t1 - s.t0); ++n) {  // K and V in turn
                     if (!(ok = warp_wait(&sh.abort, &sh.landed[buf], phase))) break;
-                    bool written = INT8;
-                    if (!INT8 && (n & 1))
+                    bool written = kCodes;
+                    if (!kCodes && (n & 1))
                         written = zero_past<S::kDimsV>(dyn + S::kOffBufs + buf * S::kTileBytes,
                                                        s.sq.len - (s.t0 + n / 2) * kTile, lane);
                     if (lane == 0) {
@@ -1046,8 +1126,8 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8, PAIR>::kThreads, 1)
         }
     } else {
         reg_dec<S::kOtherRegs>();
-        if constexpr (INT8) {
-            // -------------------------------------------------------- codes to bf16 tiles
+        if constexpr (kCodes) {
+            // -------------------------------------------------------- codes to tiles of numbers
             int raw = 0, buf = 0;
             uint32_t raw_phase = 0, phase = 0;
             bool ok = true;
@@ -1058,8 +1138,17 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8, PAIR>::kThreads, 1)
                     if (!(ok = warp_wait(&sh.abort, &sh.empty[buf], phase ^ 1))) break;
                     const uint8_t* src = dyn + S::kOffRaw + raw * S::kRawBytes;
                     uint8_t* dst = dyn + S::kOffBufs + buf * S::kTileBytes;
-                    if (n & 1) convert_tile<S::kDimsV, kTile, false>(src, dst, tid);  // V
-                    else convert_tile<DIM, S::kKeysK, true>(src, dst, tid);           // K
+                    if constexpr (INT4) {
+                        // (n counts down: the tile is t1 - (n + 1) / 2)
+                        if (n & 1)
+                            convert_tile4<S::kDimsV, kTile, DIM / 32>(src, src + S::kCodeBytes, rank * (S::kDimsV / 32),
+                                                                      s.sq.len - (s.t1 - (n + 1) / 2) * kTile, dst, tid);
+                        else
+                            convert_tile4<DIM, S::kKeysK, DIM / 32>(src, src + S::kCodeBytes, 0, kTile, dst, tid);
+                    } else {
+                        if (n & 1) convert_tile<S::kDimsV, kTile, false>(src, dst, tid);  // V
+                        else convert_tile<DIM, S::kKeysK, true>(src, dst, tid);           // K
+                    }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
@@ -1083,24 +1172,28 @@ __global__ void __launch_bounds__(ChunkShape<DIM, INT8, PAIR>::kThreads, 1)
     }
 }
 
-template <int DIM, bool INT8, bool PAIR>
+template <int DIM, int KIND, bool PAIR>
 cudaError_t launch_chunk_shape(const AttnParams& p, cudaStream_t stream)
 {
-    using S = ChunkShape<DIM, INT8, PAIR>;
+    using S = ChunkShape<DIM, KIND, PAIR>;
     static std::atomic<size_t> smem_set[kHostMaxDevices];
     const KvPages& kv = p.a.cache;
     ChunkParams cp{};
     cp.p = p;
     const uint64_t outer = static_cast<uint64_t>(kv.n_pages) * kv.n_kv;
-    const auto type = INT8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    const auto swizzle = [](int bytes) { return bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B; };
-    const int bytes = INT8 ? 1 : 2, cols_k = INT8 ? DIM : 64, cols_v = INT8 ? S::kDimsV : 64;
+    const auto type = S::kCodes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const auto swizzle = [](int bytes) {
+        return bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B : bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+    };
+    // (4 bits: two elements a byte)
+    const int bytes = S::kCodes ? 1 : 2, cols = S::INT4 ? DIM / 2 : DIM;
+    const int cols_k = S::kCodes ? cols : 64, cols_v = S::INT4 ? S::kDimsV / 2 : S::INT8 ? S::kDimsV : 64;
     const int box_k = S::kPair && kv.page > 32 ? 32 : kv.page;
-    if (!encode_tma_3d(&cp.k_map, type, bytes, kv.k, DIM, kv.page, outer, cols_k, box_k, swizzle(cols_k * bytes)) ||
-        !encode_tma_3d(&cp.v_map, type, bytes, kv.v, DIM, kv.page, outer, cols_v, kv.page, swizzle(cols_v * bytes)))
+    if (!encode_tma_3d(&cp.k_map, type, bytes, kv.k, cols, kv.page, outer, cols_k, box_k, swizzle(cols_k * bytes)) ||
+        !encode_tma_3d(&cp.v_map, type, bytes, kv.v, cols, kv.page, outer, cols_v, kv.page, swizzle(cols_v * bytes)))
         return cudaErrorInvalidValue;
     constexpr size_t smem = chunk_smem<S>();
-    const void* kernel = reinterpret_cast<const void*>(attn_chunk_kernel<DIM, INT8, PAIR>);
+    const void* kernel = reinterpret_cast<const void*>(attn_chunk_kernel<DIM, KIND, PAIR>);
     cudaError_t err = ensure_dynamic_smem(kernel, smem, smem_set);
     if (err != cudaSuccess) return err;
     // the warpgroups' register split draws on what the block was launched
@@ -1115,7 +1208,7 @@ cudaError_t launch_chunk_shape(const AttnParams& p, cudaStream_t stream)
     }
     if (n * (S::kThreads / 128) < 2 * S::kSoftRegs + (S::kThreads / 128 - 2) * S::kOtherRegs)
         return cudaErrorInvalidConfiguration;
-    launch_dep_clusters(err, attn_chunk_kernel<DIM, INT8, PAIR>, dim3(p.blocks * S::kCtas), dim3(S::kThreads), S::kCtas, smem,
+    launch_dep_clusters(err, attn_chunk_kernel<DIM, KIND, PAIR>, dim3(p.blocks * S::kCtas), dim3(S::kThreads), S::kCtas, smem,
                         stream, cp);
     return err;
 }
@@ -1126,13 +1219,14 @@ BD_BOUNDS_TAKE(bounds_take_attention_chunk)
 
 cudaError_t launch_attention_chunk(const AttnParams& p, cudaStream_t stream)
 {
-    const bool int8 = p.a.cache.int8 != 0;
-    if (p.mb == kPairRows) {
-        return int8 ? launch_chunk_shape<128, true, true>(p, stream) : launch_chunk_shape<128, false, true>(p, stream);
-    }
-    if (p.a.cache.dim == 128)
-        return int8 ? launch_chunk_shape<128, true, false>(p, stream) : launch_chunk_shape<128, false, false>(p, stream);
-    return int8 ? launch_chunk_shape<64, true, false>(p, stream) : launch_chunk_shape<64, false, false>(p, stream);
+    const auto of = [&](auto kind) {
+        constexpr int kKind = decltype(kind)::value;
+        if (p.mb == kPairRows) return launch_chunk_shape<128, kKind, true>(p, stream);
+        if (p.a.cache.dim == 128) return launch_chunk_shape<128, kKind, false>(p, stream);
+        return launch_chunk_shape<64, kKind, false>(p, stream);
+    };
+    if (p.a.cache.int4) return of(std::integral_constant<int, kInt4>{});
+    return p.a.cache.int8 ? of(std::integral_constant<int, kInt8>{}) : of(std::integral_constant<int, kBf16>{});
 }
 
 }  // namespace bd

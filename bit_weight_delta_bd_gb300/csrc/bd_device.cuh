@@ -38,7 +38,7 @@ enum BoundsKernel : uint32_t {
     kBkCompress = 0, kBkAlphaFinalize, kBkReconstruct, kBkSkinny, kBkMultiPrepare, kBkMulti, kBkPrefill,
     kBkPrefillPlan, kBkGather, kBkRoute, kBkMaterialize, kBkMsProd, kBkMsSplit, kBkMsSlices, kBkMsGram,
     kBkMsGramSum, kBkMsChol, kBkMsEig, kBkMsTri, kBkMsApply, kBkMsMerge,
-    kBkNorm, kBkRope, kBkKvRead, kBkAttnPlan, kBkAttn, kBkAttnCombine
+    kBkNorm, kBkRope, kBkKvRead, kBkAttnPlan, kBkAttn, kBkAttnCombine, kBkBlockNorm
 };
 #ifdef BD_DEBUG_BOUNDS
 namespace {

@@ -221,13 +221,39 @@ struct NormArgs {
 
 cudaError_t launch_rms_norm(const NormArgs& a, int sm_count, cudaStream_t stream);
 
+// ---- the norms around a block (bd_block_norm.cu) ----------------------------------------------
+
+struct BlockNormArgs {
+    const uint16_t* x;          // [T][d] bf16 bits: the block's output
+    const uint16_t* residual;   // [T][d]
+    uint16_t* residual_out;     // [T][d] or null
+    const uint16_t* post_gain;  // [d]: the base model's; null: no norm after the block
+    const uint16_t* gain;       // [d]: the base model's
+    const uint16_t* gate;       // [gate_rows][d] or null
+    int64_t gate_rows;
+    const int32_t* gate_idx;    // [T] or null
+    const int32_t* vid;         // [T] or null
+    int V;
+    const uint16_t* post_gains[kMaxVariants];
+    const uint16_t* gains[kMaxVariants];
+    float block_scale, residual_scale;
+    int64_t T, d;
+    float eps;
+    void* out;                  // [T][d] bf16, fp32 or e4m3 (bd_out_dtype)
+    int out_dtype;
+    float* scale;               // [T] (e4m3)
+    uint32_t* err;
+};
+
+cudaError_t launch_block_norm(const BlockNormArgs& a, int sm_count, cudaStream_t stream);
+
 // ---- paged KV cache (bd_kv.cu) ----------------------------------------------------------------
 
 struct KvPages {
-    void *k, *v;               // [n_pages][n_kv][page][dim] bf16 or int8
-    float *k_scale, *v_scale;  // [n_pages][n_kv][page] (int8)
+    void *k, *v;               // [n_pages][n_kv][page][dim] bf16, int8 or 4-bit codes
+    float *k_scale, *v_scale;  // [n_pages][n_kv][page] (int8), [n_pages][n_kv][page][dim / 32] words (int4)
     int64_t n_pages;
-    int page, page_shift, n_kv, dim, int8;
+    int page, page_shift, n_kv, dim, int8, int4;
 };
 
 constexpr int kMaxAxes = 4;
@@ -297,6 +323,7 @@ uint32_t bounds_take_route();
 uint32_t bounds_take_materialize();
 uint32_t bounds_take_monosoup();
 uint32_t bounds_take_norm();
+uint32_t bounds_take_block_norm();
 uint32_t bounds_take_kv();
 uint32_t bounds_take_attention();
 uint32_t bounds_take_attention_chunk();

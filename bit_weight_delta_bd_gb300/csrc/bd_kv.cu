@@ -7,12 +7,22 @@
 // rounds each product and each sum by itself (no contraction to fused
 // multiply-adds), so codes and scales are those of the formula evaluated
 // operation by operation in fp32, whatever computes them.
+//
+// 4-bit codes.  Per (token, kv head, group of 32 elements): low = bf16(min x),
+// scale = bf16(max(max x - min x, 1e-30) / 15), code = round-half-even((x -
+// low) / scale) within 0 .. 15, formed in the same way.  The codes are found
+// for the rounded scale and lowest value, so that their 8 bits cost next to
+// nothing: the largest element lies within 15.06 steps, and the lowest is off
+// by no more than a bf16 cache would have it.
 #include "bd_device.cuh"
 
 namespace bd {
 namespace {
 
-constexpr int rope_threads(bool int8) { return int8 ? 64 : 32; }  // of a block at most
+constexpr int kBf16 = 0, kInt8 = 1, kInt4 = 2;  // what the cache holds
+int kind_of(const KvPages& c) { return c.int4 ? kInt4 : c.int8 ? kInt8 : kBf16; }
+
+constexpr int rope_threads(int kind) { return kind == kBf16 ? 32 : 64; }  // of a block at most
 constexpr int kUnit = 16;  // elements of a head that one thread handles
 
 __device__ __forceinline__ void unpack8(uint4 u, float* f)
@@ -56,6 +66,88 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
+__device__ __forceinline__ float min_nan(float a, float b)
+{
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// 8 elements' 4-bit codes in a word, and their group's scale and lowest value in
+// another, out of the group's smallest and largest element.
+__device__ __forceinline__ uint2 codes4(const float* x, float lo, float hi)
+{
+    const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(max_nan(__fsub_rn(hi, lo), 1e-30f), 15.0f));
+    const __nv_bfloat16 lb = __float2bfloat16_rn(lo);
+    const float scale = __bfloat162float(sb), low = __bfloat162float(lb);
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        int c = __float2int_rn(__fdiv_rn(__fsub_rn(x[i], low), scale));
+        c = c < 0 ? 0 : c > 15 ? 15 : c;
+        w |= static_cast<uint32_t>(c) << (16 * (i % 2) + 4 * (i / 2));
+    }
+    const uint32_t pair = static_cast<uint32_t>(__bfloat16_as_ushort(sb)) |
+                          static_cast<uint32_t>(__bfloat16_as_ushort(lb)) << 16;
+    return make_uint2(w, pair);
+}
+
+// The smallest and largest element of the groups of 32 that a thread's chunks
+// of 8, elements e[0].. and e[1].., belong to; lo and hi hold the chunks' own.
+// UPH threads of a head call it together.  WIDE: the head turns in pairs (i, i +
+// rot / 2) and rot is a multiple of 64 (or nothing turns so), so that a group's
+// chunks are in the same place of 4 neighbouring threads, or (`alone`: a head, or
+// part of one, that does not turn) both places of 2.  Otherwise the threads
+// exchange all groups.
+template <int UPH, bool WIDE>
+__device__ __forceinline__ void group_range(const int (&e)[2], bool alone, float (&lo)[2], float (&hi)[2])
+{
+    if constexpr (WIDE) {
+        if (alone) {
+            lo[0] = lo[1] = min_nan(lo[0], lo[1]);
+            hi[0] = hi[1] = max_nan(hi[0], hi[1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            lo[i] = min_nan(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], 1));
+            hi[i] = max_nan(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], 1));
+            const float l = __shfl_xor_sync(0xffffffffu, lo[i], 2), h = __shfl_xor_sync(0xffffffffu, hi[i], 2);
+            if (!alone) {
+                lo[i] = min_nan(lo[i], l);
+                hi[i] = max_nan(hi[i], h);
+            }
+        }
+    } else {
+        float found[2][2] = {};
+#pragma unroll
+        for (int g = 0; g < UPH / 2; ++g) {
+            float l = INFINITY, h = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (e[i] / 32 == g) {
+                    l = min_nan(l, lo[i]);
+                    h = max_nan(h, hi[i]);
+                }
+#pragma unroll
+            for (int o = 1; o < UPH; o <<= 1) {
+                l = min_nan(l, __shfl_xor_sync(0xffffffffu, l, o));
+                h = max_nan(h, __shfl_xor_sync(0xffffffffu, h, o));
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (e[i] / 32 == g) {
+                    found[i][0] = l;
+                    found[i][1] = h;
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            lo[i] = found[i][0];
+            hi[i] = found[i][1];
+        }
+    }
+}
+
 struct RopeParams {
     RopeArgs a;
 };
@@ -75,11 +167,11 @@ struct RopeParams {
 // prompts of up to 1201 tokens, 48 heads of 64, 11.6 us (64 threads 12.5);
 // int8 and read back 37.9 us with 64 threads (32 threads 45.6; one ahead 39.5;
 // loads only after the work on those before 40.5).
-template <int UPH, bool INT8>
-__global__ void __launch_bounds__(rope_threads(INT8)) rope_append_kernel(const __grid_constant__ RopeParams p)
+template <int UPH, int KIND, bool WIDE>
+__global__ void __launch_bounds__(rope_threads(KIND)) rope_append_kernel(const __grid_constant__ RopeParams p)
 {
     constexpr int kDim = UPH * kUnit;
-    constexpr int kAhead = INT8 ? 2 : 1;  // heads that a thread has loaded, or is loading
+    constexpr int kAhead = KIND == kBf16 ? 1 : 2;  // heads that a thread has loaded, or is loading
     const RopeArgs& a = p.a;
     const int u = threadIdx.x % UPH;
     const int64_t t = blockIdx.x;
@@ -168,7 +260,36 @@ __global__ void __launch_bounds__(rope_threads(INT8)) rope_append_kernel(const _
             *reinterpret_cast<uint4*>(dst + e0) = pack8(x);
             *reinterpret_cast<uint4*>(dst + e1) = pack8(x + 8);
         }
-        if constexpr (INT8) {
+        if constexpr (KIND == kInt4) {
+            if (__all_sync(0xffffffffu, !live || is_q)) return;
+            const int e[2] = {e0, e1};
+            float lo[2], hi[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                lo[i] = hi[i] = x[8 * i];
+#pragma unroll
+                for (int j = 1; j < 8; ++j) {
+                    lo[i] = min_nan(lo[i], x[8 * i + j]);
+                    hi[i] = max_nan(hi[i], x[8 * i + j]);
+                }
+            }
+            group_range<UPH, WIDE>(e, is_v || !turns || a.interleaved, lo, hi);
+            if (live && !is_q && slot >= 0) {
+                const int hk = is_v ? h - a.n_q - n_kv : h - a.n_q;
+                const int64_t vec = ((page * n_kv + hk) << a.cache.page_shift) + place;
+                if (bd_in(kBkRope, vec, slots * n_kv)) {
+                    uint32_t* dst = static_cast<uint32_t*>(is_v ? a.cache.v : a.cache.k) + vec * (kDim / 8);
+                    uint32_t* sc = reinterpret_cast<uint32_t*>(is_v ? a.cache.v_scale : a.cache.k_scale) +
+                                   vec * (kDim / 32);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint2 w = codes4(x + 8 * i, lo[i], hi[i]);
+                        dst[e[i] / 8] = w.x;
+                        if (e[i] % 32 == 0) sc[e[i] / 32] = w.y;
+                    }
+                }
+            }
+        } else if constexpr (KIND == kInt8) {
             if (__all_sync(0xffffffffu, !live || is_q)) return;
             float amax = 0.0f;
             if (live && !is_q) {
@@ -219,23 +340,12 @@ struct KvReadParams {
     KvReadArgs a;
 };
 
-// A block gathers kReadRows consecutive output rows: their places in the
-// cache are looked up first (a binary search in kv_off per row), then all
-// threads copy units of 16 elements, two at a time: 8 sequences of up to 8192
-// int8 tokens, 8 heads of 128, in 48.4 us, 6.1 TB/s (51.6 one at a time); bf16
-// 59.4 us, 6.6 TB/s, by whole sectors (62.5 by halves of 16 bytes).
-template <int UPH, bool INT8>
-__global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const __grid_constant__ KvReadParams p)
+// Where rows row0 .. row0 + rows - 1 of the output lie in the cache: page * n_kv
+// * page + place of the token; -1: zeros, -2: leave the row.  By the whole block,
+// which meets afterwards; rows is at most the block's threads.
+__device__ __forceinline__ void read_bases(const KvReadArgs& a, int64_t row0, int rows, int64_t* base)
 {
-    constexpr int kDim = UPH * kUnit;
-    __shared__ int64_t base[kReadRows];  // page * n_kv * page + place of the token; -1: zeros, -2: leave the row
-    const KvReadArgs& a = p.a;
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kReadRows;
-
-    grid_launch_dependents();
-    grid_dependency_wait();
-
-    if (threadIdx.x < kReadRows) {
+    if (static_cast<int>(threadIdx.x) < rows) {
         const int64_t r = row0 + threadIdx.x;
         int64_t b = -2;
         if (r < a.rows && r < a.kv_off[a.n_seq]) {
@@ -257,7 +367,7 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const __grid_cons
         }
         base[threadIdx.x] = b;
     }
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x >= 32) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && static_cast<int>(threadIdx.x) >= 32) {
         // offsets out of order, or tokens that there are no rows for (by the warps that have nothing to look up)
         bool bad = false;
         for (int64_t s = threadIdx.x - 32; s < a.n_seq; s += kReadThreads - 32) {
@@ -266,6 +376,25 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const __grid_cons
         }
         if (bad) raise_error(a.err, kErrBadIndex);
     }
+}
+
+// A block gathers kReadRows consecutive output rows: their places in the
+// cache are looked up first (a binary search in kv_off per row), then all
+// threads copy units of 16 elements, two at a time: 8 sequences of up to 8192
+// int8 tokens, 8 heads of 128, in 48.4 us, 6.1 TB/s (51.6 one at a time); bf16
+// 59.4 us, 6.6 TB/s, by whole sectors (62.5 by halves of 16 bytes).
+template <int UPH, bool INT8>
+__global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const __grid_constant__ KvReadParams p)
+{
+    constexpr int kDim = UPH * kUnit;
+    __shared__ int64_t base[kReadRows];
+    const KvReadArgs& a = p.a;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kReadRows;
+
+    grid_launch_dependents();
+    grid_dependency_wait();
+
+    read_bases(a, row0, kReadRows, base);
     __syncthreads();
 
     const int per_row = a.cache.n_kv * UPH;  // units of one row of k (or v)
@@ -330,6 +459,96 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const __grid_cons
     }
 }
 
+// 4-bit codes: a unit is a group of 32 elements, 16 bytes of codes and 4 of its
+// scale and lowest value, which become 64 bytes.  The rows of a block are
+// chosen so that it has two units for each thread where that still leaves a
+// block for every SM.
+constexpr int kRead4MaxRows = 128;
+
+struct KvRead4Params {
+    KvReadArgs a;
+    int rows;  // of a block
+};
+
+template <int GROUPS>
+__global__ void __launch_bounds__(kReadThreads) kv_read4_kernel(const __grid_constant__ KvRead4Params p)
+{
+    __shared__ int64_t base[kRead4MaxRows];
+    const KvReadArgs& a = p.a;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.rows;
+
+    grid_launch_dependents();
+    grid_dependency_wait();
+
+    read_bases(a, row0, p.rows, base);
+    __syncthreads();
+
+    const int per_row = a.cache.n_kv * GROUPS;  // units of one row of k (or v)
+    const int64_t vecs = (a.cache.n_pages * a.cache.n_kv) << a.cache.page_shift;
+    const bool is_v = blockIdx.y != 0;
+    const uint4* pool = static_cast<const uint4*>(is_v ? a.cache.v : a.cache.k);
+    const uint32_t* scales = reinterpret_cast<const uint32_t*>(is_v ? a.cache.v_scale : a.cache.k_scale);
+    uint16_t* out = is_v ? a.v_out : a.k_out;
+    const bool sectors = on_sector(out);
+    const int units = p.rows * per_row;
+    for (int i0 = threadIdx.x; i0 < units; i0 += 2 * kReadThreads) {
+        uint4 code[2];
+        uint32_t pair[2];
+        int64_t to[2];  // of the output, or -1
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int i = i0 + k * kReadThreads;
+            const int r = i / per_row, j = i - r * per_row;
+            const int64_t b = i < units ? base[r] : -2;
+            const int h = j / GROUPS, g = j % GROUPS;
+            to[k] = b == -2 ? -1 : (((row0 + r) * a.cache.n_kv + h) * GROUPS + g) * 32;
+            code[k] = make_uint4(0, 0, 0, 0);
+            pair[k] = 0;
+            const int64_t vec = b + (static_cast<int64_t>(h) << a.cache.page_shift);
+            if (b >= 0 && bd_in(kBkKvRead, vec, vecs)) {
+                code[k] = ld_stream_v4(pool + vec * GROUPS + g);
+                pair[k] = __ldg(scales + vec * GROUPS + g);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (to[k] < 0 || !bd_in_range(kBkKvRead, to[k], 32, a.rows * a.cache.n_kv * GROUPS * 32)) continue;
+            const float scale = __uint_as_float(pair[k] << 16), low = __uint_as_float(pair[k] & 0xFFFF0000u);
+            const uint32_t w[4] = {code[k].x, code[k].y, code[k].z, code[k].w};
+            uint16_t* dst = out + to[k];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float f[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const uint32_t c = (w[2 * half + e / 8] >> (16 * (e % 2) + 4 * (e % 8 / 2))) & 15u;
+                    f[e] = fmaf(static_cast<float>(c), scale, low);  // (the product is exact)
+                }
+                const uint4 lo = pack8(f), hi = pack8(f + 8);
+                if (sectors) {
+                    store_32(dst + 16 * half, lo, hi);
+                } else {
+                    *reinterpret_cast<uint4*>(dst + 16 * half) = lo;
+                    *reinterpret_cast<uint4*>(dst + 16 * half + 8) = hi;
+                }
+            }
+        }
+    }
+}
+
+template <int UPH>
+void launch_rope_kind(cudaError_t& err, const RopeParams& p, dim3 grid, int threads, cudaStream_t stream)
+{
+    const int kind = kind_of(p.a.cache);
+    const bool wide = p.a.interleaved || p.a.rot % 64 == 0;
+    launch_dep(err,
+               kind == kBf16   ? rope_append_kernel<UPH, kBf16, true>
+               : kind == kInt8 ? rope_append_kernel<UPH, kInt8, true>
+               : wide          ? rope_append_kernel<UPH, kInt4, true>
+                               : rope_append_kernel<UPH, kInt4, false>,
+               grid, dim3(threads), 0, stream, p);
+}
+
 }  // namespace
 
 cudaError_t launch_rope_append(const RopeArgs& a, int sm_count, cudaStream_t stream)
@@ -338,7 +557,7 @@ cudaError_t launch_rope_append(const RopeArgs& a, int sm_count, cudaStream_t str
     RopeParams p{a};
     // as few passes as so many threads allow, all about equally full
     const int uph = a.cache.dim / kUnit, heads = a.n_q + 2 * a.cache.n_kv;
-    const int most = rope_threads(a.cache.int8) / uph;
+    const int most = rope_threads(kind_of(a.cache)) / uph;
     const int passes = (heads + most - 1) / most, per_pass = (heads + passes - 1) / passes;
     const int threads = (per_pass * uph + 31) / 32 * 32;
     // few tokens: the passes of a token are split over blocks until the GPU has about 8 blocks per SM
@@ -348,18 +567,26 @@ cudaError_t launch_rope_append(const RopeArgs& a, int sm_count, cudaStream_t str
     if (split < 1) split = 1;
     const dim3 grid(static_cast<unsigned>(a.T), static_cast<unsigned>(split));
     cudaError_t err = cudaSuccess;
-    if (a.cache.dim == 128)
-        launch_dep(err, a.cache.int8 ? rope_append_kernel<8, true> : rope_append_kernel<8, false>, grid,
-                   dim3(threads), 0, stream, p);
-    else
-        launch_dep(err, a.cache.int8 ? rope_append_kernel<4, true> : rope_append_kernel<4, false>, grid,
-                   dim3(threads), 0, stream, p);
+    if (a.cache.dim == 128) launch_rope_kind<8>(err, p, grid, threads, stream);
+    else launch_rope_kind<4>(err, p, grid, threads, stream);
     return err;
 }
 
-cudaError_t launch_kv_read(const KvReadArgs& a, int /*sm_count*/, cudaStream_t stream)
+cudaError_t launch_kv_read(const KvReadArgs& a, int sm_count, cudaStream_t stream)
 {
     if (a.rows == 0) return cudaSuccess;
+    if (a.cache.int4) {
+        const int groups = a.cache.dim / 32;
+        int rows = 2 * kReadThreads / (a.cache.n_kv * groups);
+        rows = rows < 1 ? 1 : rows > kRead4MaxRows ? kRead4MaxRows : rows;
+        while (rows > 1 && (a.rows + rows - 1) / rows < sm_count / 2) rows /= 2;
+        const KvRead4Params p4{a, rows};
+        const dim3 grid4(static_cast<unsigned>((a.rows + rows - 1) / rows), 2);
+        cudaError_t err = cudaSuccess;
+        launch_dep(err, a.cache.dim == 128 ? kv_read4_kernel<4> : kv_read4_kernel<2>, grid4, dim3(kReadThreads), 0,
+                   stream, p4);
+        return err;
+    }
     KvReadParams p{a};
     const dim3 grid(static_cast<unsigned>((a.rows + kReadRows - 1) / kReadRows), 2);
     cudaError_t err = cudaSuccess;

@@ -70,7 +70,7 @@ typedef enum bd_status {
 
 typedef enum bd_alpha_mode { BD_ALPHA_PER_MATRIX = 0, BD_ALPHA_PER_ROW = 1 } bd_alpha_mode;
 
-/* BD_OUT_E4M3 (8 bits with a scale per row) is taken by bd_rms_norm only. */
+/* BD_OUT_E4M3 (8 bits with a scale per row) is taken by bd_rms_norm and bd_block_norm only. */
 typedef enum bd_out_dtype { BD_OUT_BF16 = 0, BD_OUT_F32 = 1, BD_OUT_E4M3 = 2 } bd_out_dtype;
 
 /* Largest number of variants one bd_linear_multi call can address. */
@@ -317,16 +317,56 @@ bd_status bd_rms_norm(const uint16_t* x, const uint16_t* residual, int64_t T, in
                       void* stream);
 
 /* ------------------------------------------------------------------------
+ * The norms around a block (attention, feed-forward), with its gate:
+ *   n[t] = x[t] * (mean_j x[t][j]^2 + eps)^(-1/2) * post_gain_{vid[t]}
+ *   h[t] = residual_scale * residual[t] + block_scale * gate_t * n[t]
+ *   y[t] = h[t] * (mean_j h[t][j]^2 + eps)^(-1/2) * gain_{vid[t]}
+ * x is what the block gives; n = x without post_gain, and h has no factor gate
+ * without gate.  All of it is fp32; h and y are rounded once.
+ *   x, residual   device bf16 [T][d]
+ *   post_gain, gain   device bf16 [d]: the base model's; post_gain may be NULL
+ *   post_gain_tab, gain_tab   host arrays of V device pointers, each bf16 [d]
+ *                 (ignored without vid; post_gain_tab without post_gain)
+ *   vid           device int32 [T] or NULL; -1: the base model's gains
+ *   gate          device bf16 [gate_rows][d] or NULL (gate_rows 0, gate_idx
+ *                 NULL).  Token t takes row gate_idx[t] (device int32 [T]): a
+ *                 sequence's, a variant's; without gate_idx the one row of
+ *                 gate_rows == 1, or row t of gate_rows == T.  An index outside
+ *                 [0, gate_rows) sets BD_ERR_BAD_INDEX and takes row 0
+ *   block_scale, residual_scale   finite
+ *   residual_out, out, out_dtype, scale, d, eps, V and ids out of range as in
+ *                 bd_rms_norm; residual_out may be the residual's own buffer
+ *                 (or x's)
+ * Matrices, gains and gates 16-byte aligned; out may not overlap an input.
+ * ------------------------------------------------------------------------ */
+size_t bd_block_norm_workspace_size(int64_t T, int64_t d);
+
+bd_status bd_block_norm(const uint16_t* x, const uint16_t* residual, int64_t T, int64_t d, const uint16_t* post_gain,
+                        const uint16_t* const* post_gain_tab, const uint16_t* gate, int64_t gate_rows,
+                        const int32_t* gate_idx, float block_scale, float residual_scale, const uint16_t* gain,
+                        const uint16_t* const* gain_tab, const int32_t* vid, int32_t V, float eps,
+                        uint16_t* residual_out, void* out, int out_dtype, float* scale, void* ws, size_t ws_bytes,
+                        void* stream);
+
+/* ------------------------------------------------------------------------
  * A paged KV cache of one layer: fixed-size pages of page_size tokens, each
  * holding the tokens' keys (and values) of every kv head, head by head:
- *   k, v              device [n_pages][n_kv][page_size][head_dim], bf16 or
- *                     int8 codes, 16-byte aligned
+ *   k, v              device [n_pages][n_kv][page_size][head_dim], bf16, int8
+ *                     codes or 4-bit codes (two a byte), 16-byte aligned
  *   k_scale, v_scale  device fp32 [n_pages][n_kv][page_size] (int8), 16-byte
  *                     aligned; NULL for bf16.  A value is code * scale.
+ *                     4 bits: [n_pages][n_kv][page_size][head_dim / 32] words,
+ *                     16-byte aligned, for each group of 32 neighbouring
+ *                     elements a bf16 scale (low half, not negative) and a
+ *                     bf16 lowest value `low` (high half).  A value is code *
+ *                     scale + low, code 0 .. 15.
+ * 4-bit codes: element 8 w + 2 i of a head stands in bits 4 i .. 4 i + 3 of its
+ * 32-bit word w, element 8 w + 2 i + 1 in bits 16 + 4 i .. 19 + 4 i, so that one
+ * mask takes two neighbours out of a word.
  * head_dim 64 or 128; page_size 16, 32, 64 or 128; n_kv 1..1024.  Other
  * values give BD_ERR_UNSUPPORTED_SHAPE.  A host struct that each call reads.
  * ------------------------------------------------------------------------ */
-typedef enum bd_kv_dtype { BD_KV_BF16 = 0, BD_KV_INT8 = 1 } bd_kv_dtype;
+typedef enum bd_kv_dtype { BD_KV_BF16 = 0, BD_KV_INT8 = 1, BD_KV_INT4 = 2 } bd_kv_dtype;
 
 typedef struct bd_kv_pages {
     void* k;
@@ -351,9 +391,13 @@ typedef struct bd_kv_pages {
  * page_size + place in the page; -1 writes nothing): rounded to bf16, or as
  * int8 codes with, per token and head,
  *   scale = max(max |x|, 1e-30) / 127,  code = round-half-even(x / scale),
- * formed from the unrounded fp32 values.  A vector that is not finite gets a
- * scale that is not finite.  Products and sums are rounded one by one (no
- * fused multiply-add), so the codes do not depend on the kernel.
+ * or as 4-bit codes with, per token, head and group of 32 elements,
+ *   low = bf16(min x),  scale = bf16(max(max x - min x, 1e-30) / 15),
+ *   code = round-half-even((x - low) / scale), kept within 0 .. 15,
+ * formed from the unrounded fp32 values.  A vector (4 bits: group) that is not
+ * finite, or a group whose max - min is not, gets a scale that is not finite.
+ * Products, sums and quotients are rounded one by one (no fused multiply-add),
+ * so the codes do not depend on the kernel.
  *   q, k, v    device bf16 rows of n_q, n_kv, n_kv heads of head_dim, rows
  *              *_stride elements apart (a multiple of 8, at least the row):
  *              slices of one packed product can be passed as they are.  q
@@ -382,7 +426,7 @@ bd_status bd_rope_append(const uint16_t* q, int64_t q_stride, const uint16_t* k,
 /* ------------------------------------------------------------------------
  * Reading the cache back: tokens 0 .. kv_off[s+1]-kv_off[s]-1 of sequence s
  * are gathered into rows kv_off[s].. of k_out and v_out, as bf16 (code *
- * scale rounded once).
+ * scale rounded once; 4 bits: code * scale + low, formed in fp32, rounded).
  *   page_table  device int32 [n_seq][max_pages]: token j of sequence s lies
  *               on page page_table[s][j / page_size], at j % page_size
  *   kv_off      device int32 [n_seq + 1], nondecreasing, kv_off[0] = 0;
