@@ -56,9 +56,23 @@
 // odd CTA's converted); 12..15 conversion (int8, 4 bits).
 //
 // 4-bit keys and values: TMA and bulk copies bring the codes with their groups'
-// scales and lowest values, and the fourth warpgroup forms code * scale + low,
-// rounded once to bf16: what a bf16 cache of the same values would hold.  All
-// that follows is as for bf16.
+// scales and lowest values, and the fourth warpgroup forms tiles of numbers.
+//   V: code * scale + low, rounded once to bf16: what a bf16 cache of the same
+// values would hold.
+//   K is kept exact, since its rounding would show in the scores (by 2^-12 of the
+// sum of their products' magnitudes, where fp32 sums leave 2^-20: the
+// log-sum-exp of a row that sees few keys was off by 1e-4 to 1e-3).  A key is
+//   (code - 8) scale + (low + 8 scale)
+// whose first term has 3 + 8 bits, so fp16 holds it, and whose second is the
+// same for the 32 dims of a group: S gets 16 more columns of Q, the sums of q
+// over each group in two pieces of 11 bits, against low and 8 scale (a ninth
+// product step for the eight of head_dim 128).  fp16's range: q is scaled per
+// row by a power of two, as for int8, and a tile of K by one that brings its
+// largest value to 2^14; the softmax, which multiplies by a factor anyway, takes
+// it back.  Where the keys of a tile are more than 2^10 apart, each is scaled by
+// its own power, and the softmax multiplies key by key (such a tile is not to
+// let a large key, which a causal row may not even see, flush the others).
+// Within a key, what lies 2^-27 below its largest element may lose bits.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -91,21 +105,26 @@ struct ChunkShape {
     static constexpr int kThreads = kCodes ? 512 : 384;
     static constexpr bool kSmall = PAIR || DIM == 64;  // tiles of 16 KB
     // bf16 tiles in shared memory, and tiles of codes
-    static constexpr int kBufs = INT8 ? (kSmall ? 6 : 3) : INT4 ? (kSmall ? 8 : 4) : kSmall ? 8 : 5;
+    static constexpr int kBufs = kCodes ? (kSmall ? 6 : 3) : kSmall ? 8 : 5;
     static constexpr int kRaw = INT8 ? (kSmall ? 6 : 3) : INT4 ? (kSmall ? 5 : 3) : 0;
-    static constexpr int kScaleBufs = INT8 ? (kSmall ? 4 : 3) : 0;          // scales of a key tile, K and V
+    static constexpr int kScaleBufs = INT4 ? 4 : INT8 ? (kSmall ? 4 : 3) : 0;  // scales of a key tile, K and V
+    // 4 bits: a tile's factor, and its keys'; the columns of Q and K past the dims, rows of 32 bytes
+    static constexpr int kScaleBytes = INT4 ? (4 + kTile) * 4 : 2 * kTile * 4;
+    static constexpr int kExtRow = INT4 ? 32 : 0;
     // a CTA's part of a tile: in a pair half the keys of each step of K, half the dims of V
     static constexpr int kKeysK = kTile / kCtas, kDimsV = DIM / kCtas;
-    static constexpr int kTileBytes = kTile * DIM * 2 / kCtas;
+    static constexpr int kExtK = kKeysK * kExtRow;                      // behind a tile
+    static constexpr int kTileBytes = kTile * DIM * 2 / kCtas + kExtK;
     // 4 bits: codes, then the groups' scales and lowest values, whole rows of them
     static constexpr int kPairBytes = DIM / 8;  // of a row
     static constexpr int kCodeBytes = kTile * DIM / kCtas / (INT4 ? 2 : 1);
     static constexpr int kRawBytes = kCodeBytes + (INT4 ? kTile * kPairBytes : 0);
     static constexpr int kQBytes = kQRows * DIM * 2;
-    static constexpr int kOffBufs = 2 * kQBytes;
+    static constexpr int kOffExtQ = 2 * kQBytes;  // of both query tiles
+    static constexpr int kOffBufs = kOffExtQ + 2 * kQRows * kExtRow;
     static constexpr int kOffRaw = kOffBufs + kBufs * kTileBytes;
     static constexpr int kOffScale = kOffRaw + kRaw * kRawBytes;
-    static constexpr int kBytes = kOffScale + kScaleBufs * 2 * kTile * 4;
+    static constexpr int kBytes = kOffScale + kScaleBufs * kScaleBytes;
     // registers of a softmax thread, and of the others: the sum over the
     // warpgroups is what the block was launched with
     static constexpr int kSoftRegs = kCodes ? 168 : 208;
@@ -123,6 +142,8 @@ struct ChunkShared {
     uint64_t q_full[2], o_full[2];
     uint64_t s_full[2][2], p_full[2][2], pv_done[2];  // by query tile (and place)
     uint64_t done;
+    uint64_t ranged;    // the converting warps have each said how large the keys of their part are (4 bits)
+    uint2 range[2][4];  // the bits of the largest and of the smallest, by the tile's parity
     uint32_t tmem;
     volatile int abort;
 };
@@ -277,6 +298,19 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t 
     return d;
 }
 
+// Shared-memory descriptor of a K-major operand of 16 columns: rows of 32 bytes
+// (32-byte swizzle), groups of 8 rows 256 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_sw32(uint32_t saddr)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(1) << 16;
+    d |= static_cast<uint64_t>(256 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(6) << 61;
+    return d;
+}
+
 // What lies past the sequence in a tile of V may be anything, NaN included:
 // zeros from key `valid` on instead, so that probabilities of 0 times it stay
 // 0.  DIMS: that the CTA holds.  By a warp.  Returns whether it wrote any.
@@ -426,40 +460,57 @@ __device__ __forceinline__ int swizzled_codes(int t, int c)
 }
 
 // 8 4-bit codes as 8 bf16 values code * scale + low: 0x4300 | code is 128 + code.
-__device__ __forceinline__ uint4 values4(uint32_t w, __nv_bfloat162 scale, __nv_bfloat162 low)
+__device__ __forceinline__ uint4 values4(uint32_t w, uint32_t scale, uint32_t low)
 {
     const __nv_bfloat162 offset = __float2bfloat162_rn(128.0f);
     uint32_t r[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t x = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-        const __nv_bfloat162 v = __hfma2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), offset), scale, low);
+        const __nv_bfloat162 v = __hfma2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), offset),
+                                         *reinterpret_cast<const __nv_bfloat162*>(&scale),
+                                         *reinterpret_cast<const __nv_bfloat162*>(&low));
         r[i] = *reinterpret_cast<const uint32_t*>(&v);
     }
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// A tile of 4-bit codes with their scales and lowest values as a tile of bf16
+// 8 4-bit codes as 8 fp16 values (code - 8) * scale, which are exact: 0x6400 |
+// code is 1024 + code, 0x6400 | 16 code is 1024 + 16 code.
+__device__ __forceinline__ uint4 centred4(uint32_t w, __half2 scale)
+{
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t x = ((i < 2 ? w : w >> 8) & (i % 2 ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
+        const __half2 c = i % 2 ? __hfma2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(1.0f / 16),
+                                          __float2half2_rn(-72.0f))
+                                : __hadd2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(-1032.0f));
+        const __half2 v = __hmul2(c, scale);
+        r[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// A tile of V's 4-bit codes with their scales and lowest values as a tile of bf16
 // values, a group of 32 a thread, by the 128 threads of a warpgroup.  Eight
 // neighbouring lanes take the same group of 8 keys in a row: reads and writes
-// of 16 bytes meet in no bank.  DIM: values of a row; KEYS: rows of the tile;
-// PAIRS: words of scales of a row, of which this tile's are the DIM / 32 from
-// first on.  Rows from `valid` on become zeros (what lies there may be anything).
-template <int DIM, int KEYS, int PAIRS>
-__device__ __forceinline__ void convert_tile4(const uint8_t* src, const uint8_t* pairs, int first, int valid,
-                                              uint8_t* dst, int tid)
+// of 16 bytes meet in no bank.  DIM: values of a row; PAIRS: words of scales of a
+// row, of which this tile's are the DIM / 32 from first on.  Rows from `valid`
+// on become zeros (what lies there may be anything).
+template <int DIM, int PAIRS>
+__device__ __forceinline__ void convert_v4(const uint8_t* src, const uint8_t* pairs, int first, int valid, uint8_t* dst,
+                                           int tid)
 {
     constexpr int kGroups = DIM / 32, kKeys = 128 / kGroups;  // of a round
     const int g = (tid >> 3) & (kGroups - 1), key0 = (tid & 7) + 8 * (tid / (8 * kGroups));
-    uint8_t* half = dst + (g >> 1) * (KEYS * 128);
+    uint8_t* half = dst + (g >> 1) * (kTile * 128);
 #pragma unroll 2
-    for (int i = 0; i < KEYS / kKeys; ++i) {
+    for (int i = 0; i < kTile / kKeys; ++i) {
         const int key = key0 + i * kKeys;
         const uint4 c = *reinterpret_cast<const uint4*>(src + swizzled_codes<DIM / 2>(key, g));
         const uint32_t pair = *reinterpret_cast<const uint32_t*>(pairs + (key * PAIRS + first + g) * 4);
-        const uint32_t s2 = __byte_perm(pair, 0, 0x1010), l2 = __byte_perm(pair, 0, 0x3232);
-        const __nv_bfloat162 scale = *reinterpret_cast<const __nv_bfloat162*>(&s2);
-        const __nv_bfloat162 low = *reinterpret_cast<const __nv_bfloat162*>(&l2);
+        const uint32_t scale = __byte_perm(pair, 0, 0x1010), low = __byte_perm(pair, 0, 0x3232);
         const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -467,6 +518,68 @@ __device__ __forceinline__ void convert_tile4(const uint8_t* src, const uint8_t*
             if (key >= valid) v = make_uint4(0, 0, 0, 0);
             *reinterpret_cast<uint4*>(half + key * 128 + (((4 * (g & 1) + j) ^ (key & 7)) << 4)) = v;
         }
+    }
+}
+
+// The largest element that a key may have, by its groups' scales and lowest
+// values: 0 where that is not finite.
+template <int PAIRS>
+__device__ __forceinline__ float key_range(const uint8_t* pairs, int key)
+{
+    float big = 0.0f;
+#pragma unroll
+    for (int g = 0; g < PAIRS; ++g) {
+        const uint32_t pair = *reinterpret_cast<const uint32_t*>(pairs + (key * PAIRS + g) * 4);
+        const float s = __uint_as_float(pair << 16), low = __uint_as_float(pair & 0xFFFF0000u);
+        const float a = fmaf(15.0f, s, low);
+        // (NaN in, NaN out: the maximum of two would drop it)
+        const float m = fmaxf(fmaxf(fabsf(low), fabsf(a)), 8.0f * fabsf(s));
+        big = a - a == 0.0f && low - low == 0.0f ? fmaxf(big, m) : INFINITY;
+    }
+    return big < INFINITY ? big : 0.0f;
+}
+
+// What K's values of that size are multiplied by to lie below 2^14 .. 2^15, and
+// its inverse; 0 (no key says anything) counts as 1.
+__device__ __forceinline__ float key_factor(float big, float& back)
+{
+    const float u = big > 0.0f ? __uint_as_float(__float_as_uint(fminf(fmaxf(big, 7.9e-31f), 1.2e30f)) & 0x7F800000u) : 1.0f;
+    back = u / 16384.0f;
+    return 16384.0f / u;
+}
+
+// A tile of K's 4-bit codes: (code - 8) scale in fp16, over the factor of the key,
+// and behind the tile the 16 columns for the lowest values, for each group (low,
+// 8 scale) twice.  KEYS: rows of the tile, which are keys key_of(row) of the
+// whole tile of 128 whose scales and lowest values `pairs` holds.  f: the factor
+// of all keys, or 0 where by_key has each key's inverse.
+template <int DIM, int KEYS, typename KeyOf>
+__device__ __forceinline__ void convert_k4(const uint8_t* src, const uint8_t* pairs, float f, const float* by_key,
+                                           uint8_t* dst, int tid, KeyOf key_of)
+{
+    constexpr int kGroups = DIM / 32, kKeys = 128 / kGroups;  // of a round
+    const int g = (tid >> 3) & (kGroups - 1), row0 = (tid & 7) + 8 * (tid / (8 * kGroups));
+    uint8_t* half = dst + (g >> 1) * (KEYS * 128);
+    uint8_t* ext = dst + KEYS * DIM * 2;
+#pragma unroll 2
+    for (int i = 0; i < KEYS / kKeys; ++i) {
+        const int row = row0 + i * kKeys, key = key_of(row);
+        const uint4 c = *reinterpret_cast<const uint4*>(src + swizzled_codes<DIM / 2>(row, g));
+        const uint32_t pair = *reinterpret_cast<const uint32_t*>(pairs + (key * kGroups + g) * 4);
+        const float fk = f != 0.0f ? f : 1.0f / by_key[key];
+        const float s = __uint_as_float(pair << 16) * fk, low = __uint_as_float(pair & 0xFFFF0000u) * fk;
+        const __half2 scale = __float2half2_rn(s);
+        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(half + row * 128 + (((4 * (g & 1) + j) ^ (row & 7)) << 4)) = centred4(w[j], scale);
+        const __half2 e = __floats2half2_rn(low, 8.0f * s);
+        const uint32_t ee = *reinterpret_cast<const uint32_t*>(&e);
+        uint8_t* x = ext + row * 32;
+        const int sw = (row >> 2) & 1;
+        *reinterpret_cast<uint2*>(x + (((g >> 1) ^ sw) << 4) + 8 * (g & 1)) = make_uint2(ee, ee);
+        if constexpr (kGroups == 2)  // the columns of no group
+            *reinterpret_cast<uint2*>(x + ((1 ^ sw) << 4) + 8 * g) = make_uint2(0, 0);
     }
 }
 
@@ -542,11 +655,16 @@ __device__ __forceinline__ float unit_of(float x)
 // of 64 dims); rows past the item are zeros.  Neighbouring lanes take neighbouring 16 bytes, eight loads in
 // flight (a row per lane, two in flight, cost 6 us per item, and twice that
 // where int8 looked for the maximum first).  A negative scale is taken into
-// Q's sign; int8: fp16, over the row's power of two, dims in the codes' order.
+// Q's sign; int8: fp16, over the row's power of two, dims in the codes' order; 4
+// bits: the same in the dims' own order, and in ext the 16 columns of the sums
+// over the groups of 32, each as two pieces twice.
 // Returns what the products of row r0 + lane are to be multiplied by.
-template <int DIM, bool INT8>
-__device__ __forceinline__ float load_q(const AttnParams& p, const Segment& s, int tile_row, int r0, int lane, uint8_t* dst)
+template <int DIM, int KIND>
+__device__ __forceinline__ float load_q(const AttnParams& p, const Segment& s, int tile_row, int r0, int lane, uint8_t* dst,
+                                        [[maybe_unused]] uint8_t* ext)
 {
+    constexpr bool INT4 = KIND == kInt4;
+    constexpr float kTop = INT4 ? 512.0f : 16384.0f;  // (the sums of 32 have to lie in fp16's range too)
     constexpr int kLanes = DIM / 8, kRowsAtOnce = 32 / kLanes, kBatch = 8;
     const uint64_t own = reinterpret_cast<uint64_t>(q_row<DIM>(p, s, tile_row + r0 + lane));
     const uint32_t flip = p.a.scale < 0.0f ? 0x80008000u : 0u;
@@ -566,28 +684,46 @@ __device__ __forceinline__ float load_q(const AttnParams& p, const Segment& s, i
             const int r = r0 + g + k * kRowsAtOnce + sub;
             uint4 x = v[k];
             x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
-            if constexpr (INT8) {
+            if constexpr (KIND != kBf16) {
                 float big = abs_max8(0.0f, x);
 #pragma unroll
                 for (int o = 1; o < kLanes; o *= 2) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-                const float unit = unit_of(big), f = 16384.0f / unit;
+                const float unit = unit_of(big), f = kTop / unit;
 #pragma unroll
                 for (int e = 0; e < kRowsAtOnce; ++e) {
                     const float of = __shfl_sync(0xffffffffu, unit, e * kLanes);
-                    if (lane == g + k * kRowsAtOnce + e) back = of / 16384.0f;
+                    if (lane == g + k * kRowsAtOnce + e) back = of / kTop;
                 }
                 const uint32_t w[4] = {x.x, x.y, x.z, x.w};
                 uint32_t o[4];
+                [[maybe_unused]] float sum = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 4; e += 2) {
                     const float x0 = __uint_as_float(w[e] << 16) * f, x1 = __uint_as_float(w[e] & 0xFFFF0000u) * f;
                     const float x2 = __uint_as_float(w[e + 1] << 16) * f;
                     const float x3 = __uint_as_float(w[e + 1] & 0xFFFF0000u) * f;
-                    const __half2 even = __floats2half2_rn(x0, x2), odd = __floats2half2_rn(x1, x3);
+                    const __half2 even = __floats2half2_rn(x0, INT4 ? x1 : x2);
+                    const __half2 odd = __floats2half2_rn(INT4 ? x2 : x1, x3);
+                    if constexpr (INT4) sum += (x0 + x1) + (x2 + x3);
                     o[e] = *reinterpret_cast<const uint32_t*>(&even);
                     o[e + 1] = *reinterpret_cast<const uint32_t*>(&odd);
                 }
                 x = make_uint4(o[0], o[1], o[2], o[3]);
+                if constexpr (INT4) {
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                    const int gr = c >> 2;
+                    if ((c & 3) == 0) {
+                        const __half hi = __float2half_rn(sum), lo = __float2half_rn(sum - __half2float(hi));
+                        const __half2 hh = __half2half2(hi), ll = __half2half2(lo);
+                        uint8_t* q = ext + r * 32;
+                        const int sw = (r >> 2) & 1;
+                        *reinterpret_cast<uint2*>(q + (((gr >> 1) ^ sw) << 4) + 8 * (gr & 1)) =
+                            make_uint2(*reinterpret_cast<const uint32_t*>(&hh), *reinterpret_cast<const uint32_t*>(&ll));
+                        if constexpr (DIM == 64)
+                            *reinterpret_cast<uint2*>(q + ((1 ^ sw) << 4) + 8 * gr) = make_uint2(0, 0);
+                    }
+                }
             }
             *reinterpret_cast<uint4*>(dst + (c >> 3) * (kQRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x;
         }
@@ -623,7 +759,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
             mbar_init(&sh.raw_empty[i], 4);
         }
         for (int i = 0; i < S::kScaleBufs; ++i) {
-            mbar_init(&sh.sc_full[i], 1);
+            mbar_init(&sh.sc_full[i], INT4 ? 4 : 1);
             mbar_init(&sh.sc_empty[i], 8);
         }
         for (int i = 0; i < 2; ++i) {
@@ -636,6 +772,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
             mbar_init(&sh.o_full[i], 1);
         }
         mbar_init(&sh.done, 2);
+        mbar_init(&sh.ranged, 4);
         sh.abort = 0;
         fence_mbarrier_init();
     }
@@ -701,7 +838,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
             const bool have = walk.next(s);
             const bool runs = have && i < s.q_tiles;
             if (runs) {
-                unit = load_q<DIM, INT8>(p, s, tile_row, r - lane, lane, q_smem);
+                unit = load_q<DIM, KIND>(p, s, tile_row, r - lane, lane, q_smem, dyn + S::kOffExtQ + i * kQRows * S::kExtRow);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) arrive_even_written<kPair>(&sh.q_full[i], rank);
@@ -761,7 +898,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
             ran = runs;
             if (!runs) {
                 // no rows here: only the scales' slots have to be handed on
-                if constexpr (INT8) {
+                if constexpr (kCodes) {
                     for (int t = s.t0; t < s.t1; ++t) {
                         if (!warp_wait(&sh.abort, &sh.sc_full[sc], sc_phase)) break;
                         if (lane == 0) mbar_arrive(&sh.sc_empty[sc]);
@@ -784,6 +921,11 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
             const int all_seen = attn_seen(s.sq, (s.it.row0 + tile_row) / p.G, a.causal);
             // (a scale of 0 would make NaN of a masked score)
             const float c2 = fmaxf(fabsf(a.scale) * kLog2e * unit, 1e-30f);
+            // what a step's scores, and the maximum, are multiplied by to be in units of log2: with 4-bit codes the
+            // scores are over their tile's factor, and the maximum is kept in those units
+            float cs = c2;
+            const float cm = INT4 ? 1.0f : c2;
+            [[maybe_unused]] bool by_key = false;
             m = -INFINITY;
             l = 0.0f;
 #pragma unroll 1
@@ -795,6 +937,17 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
                 tmem_ld32_start(ts + 64 * b, v);
                 tmem_ld32_start(ts + 64 * b + 32, v + 32);
                 const float *ks = nullptr, *vs = nullptr;
+                if constexpr (INT4) {
+                    ks = reinterpret_cast<const float*>(dyn + S::kOffScale + sc * S::kScaleBytes);
+                    if (b == 0) {
+                        warp_wait(&sh.abort, &sh.sc_full[sc], sc_phase);
+                        const float back = ks[0];  // 0: by key
+                        by_key = back == 0.0f;
+                        const float c = fabsf(a.scale) * kLog2e * unit;
+                        cs = fmaxf(by_key ? c : c * back, 1e-30f);
+                    }
+                    ks += 4 + kStep * b;
+                }
                 if constexpr (INT8) {
                     if (b == 0) warp_wait(&sh.abort, &sh.sc_full[sc], sc_phase);
                     ks = reinterpret_cast<const float*>(dyn + S::kOffScale) + sc * 2 * kTile + kStep * b;
@@ -802,7 +955,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
                 }
                 tmem_ld_wait(v);
                 tmem_ld_wait(v + 32);
-                if constexpr (INT8) {
+                if (INT8 || (INT4 && by_key)) {
 #pragma unroll
                     for (int e = 0; e < 64; e += 4) {
                         const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(ks + e);
@@ -838,11 +991,12 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
                     for (int k = 0; k < 4; ++k)
                         mx[k] = max3(mx[k], __uint_as_float(v[e + 2 * k]), __uint_as_float(v[e + 2 * k + 1]));
                 const float mt = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+                const float mu = INT4 ? mt * cs : mt;
                 // the first step sets the maximum; later it moves when it has grown by kLag
-                const bool grow = mt > m && (mt - m) * c2 > kLag;
+                const bool grow = mu > m && (mu - m) * cm > kLag;
                 if (__any_sync(0xffffffffu, grow)) {
-                    const float f = !grow ? 1.0f : m == -INFINITY ? 0.0f : ex2((m - mt) * c2);
-                    if (grow) m = mt;
+                    const float f = !grow ? 1.0f : m == -INFINITY ? 0.0f : ex2((m - mu) * cm);
+                    if (grow) m = mu;
                     l *= f;
                     if (j > 2 * s.t0) {
                         // P V of the step before has to be done (S of this step says it of the one before that)
@@ -858,9 +1012,9 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
                         }
                     }
                 }
-                const float nm = m == -INFINITY ? 0.0f : fmaf(-m, c2, attn_bias<INT8>());
+                const float nm = m == -INFINITY ? 0.0f : fmaf(-m, cm, attn_bias<INT8>());
                 uint64_t sum[2] = {0, 0};  // pairs of zeros
-                const uint64_t c22 = f32x2(c2, c2), nm2 = f32x2(nm, nm);
+                const uint64_t c22 = f32x2(cs, cs), nm2 = f32x2(nm, nm);
 #pragma unroll
                 for (int e0 = 0; e0 < 64; e0 += 32) {
                     uint32_t pk[16];
@@ -888,17 +1042,17 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
                 __syncwarp();
                 if (lane == 0) {
                     arrive_even<kPair>(&sh.p_full[i][b]);
-                    if constexpr (INT8)
+                    if constexpr (kCodes)
                         if (b) mbar_arrive(&sh.sc_empty[sc]);
                 }
                 if (b) s_phase ^= 1;
                 pv_phase ^= 1;
-                if constexpr (INT8)
+                if constexpr (kCodes)
                     if (b && ++sc == S::kScaleBufs) sc = 0, sc_phase ^= 1;
                 const float2 s2 = unpack2(add2(sum[0], sum[1]));
                 l += s2.x + s2.y;
             }
-            m2 = m == -INFINITY ? -INFINITY : fmaf(m, c2, -attn_bias<INT8>());
+            m2 = m == -INFINITY ? -INFINITY : fmaf(m, cm, -attn_bias<INT8>());
         }
     } else if (warp < kConvertWarp) {
         reg_dec<S::kOtherRegs>();
@@ -965,10 +1119,11 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
                     for (int kv = 0; kv < 2; ++kv) {
                         if (!(ok = warp_wait(&sh.abort, &empty[buf], phase ^ 1))) break;
                         // bytes of a row of K and of V
-                        constexpr uint32_t kRowK = INT4 ? DIM / 2 + S::kPairBytes : INT8 ? DIM : 2 * DIM;
-                        constexpr uint32_t kRowV = INT4   ? S::kDimsV / 2 + S::kPairBytes
-                                                   : INT8 ? S::kDimsV : 2 * S::kDimsV;
-                        if (lane == 0) mbar_arrive_expect_tx(&full[buf], kv ? rows * kRowV : rows_k * kRowK);
+                        constexpr uint32_t kRowK = INT4 ? DIM / 2 : INT8 ? DIM : 2 * DIM;
+                        constexpr uint32_t kRowV = INT4 ? S::kDimsV / 2 : INT8 ? S::kDimsV : 2 * S::kDimsV;
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(&full[buf], (kv ? rows * kRowV : rows_k * kRowK) +
+                                                                  (INT4 ? rows * S::kPairBytes : 0u));
                         __syncwarp();
                         uint8_t* dst =
                             dyn + (kCodes ? S::kOffRaw + buf * S::kRawBytes : S::kOffBufs + buf * S::kTileBytes);
@@ -976,10 +1131,6 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
                             const int row = key_k & (cache.page - 1), to = lane * box_k;
                             if constexpr (INT4) {
                                 tma_load_3d(dst + to * (DIM / 2), &cp.k_map, 0, row, outer_k, &full[buf]);
-                                const int64_t vec = (static_cast<int64_t>(outer_k) << cache.page_shift) + row;
-                                bulk_g2s(dst + S::kCodeBytes + to * S::kPairBytes,
-                                         reinterpret_cast<const uint8_t*>(cache.k_scale) + vec * S::kPairBytes,
-                                         box_k * S::kPairBytes, &full[buf]);
                             } else if constexpr (INT8) {
                                 tma_load_3d(dst + to * DIM, &cp.k_map, 0, row, outer_k, &full[buf]);
                             } else {
@@ -994,10 +1145,6 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
                             if constexpr (INT4) {
                                 tma_load_3d(dst + to * (S::kDimsV / 2), &cp.v_map, rank * (S::kDimsV / 2), 0, outer,
                                             &full[buf]);
-                                const int64_t vec = static_cast<int64_t>(outer) << cache.page_shift;
-                                bulk_g2s(dst + S::kCodeBytes + to * S::kPairBytes,
-                                         reinterpret_cast<const uint8_t*>(cache.v_scale) + vec * S::kPairBytes,
-                                         cache.page * S::kPairBytes, &full[buf]);
                             } else if constexpr (INT8) {
                                 tma_load_3d(dst + to * S::kDimsV, &cp.v_map, rank * S::kDimsV, 0, outer, &full[buf]);
                             } else {
@@ -1005,6 +1152,16 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
                                 for (int d = 0; d < S::kDimsV; d += 64)
                                     tma_load_3d(dst + (d / 64) * kTile * 128 + to * 128, &cp.v_map,
                                                 rank * S::kDimsV + d, 0, outer, &full[buf]);
+                            }
+                        }
+                        if constexpr (INT4) {
+                            // the scales and lowest values of the whole tile (of K too, whose factor is that of
+                            // both CTAs' keys)
+                            if (mine) {
+                                const int64_t vec = static_cast<int64_t>(outer) << cache.page_shift;
+                                const float* pairs = kv ? cache.v_scale : cache.k_scale;
+                                bulk_g2s(dst + S::kCodeBytes + lane * cache.page * S::kPairBytes,
+                                         pairs + vec * (S::kPairBytes / 4), cache.page * S::kPairBytes, &full[buf]);
                             }
                         }
                         if (++buf == kRing) buf = 0, phase ^= 1;
@@ -1021,7 +1178,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
         } else if (warp < kMmaWarp + 2 && rank == 0) {
             // ---------------------------------------------------- MMA of query tile i
             constexpr int kRows = kQRows * S::kCtas;
-            constexpr uint32_t kIdescS = INT8 ? idesc_f16_f32(kRows, kStep) : idesc_bf16_f32(kRows, kStep);
+            constexpr uint32_t kIdescS = kCodes ? idesc_f16_f32(kRows, kStep) : idesc_bf16_f32(kRows, kStep);
             // V: rows along the contracted index
             constexpr uint32_t kIdescO = idesc_bf16_f32(kRows, DIM) | (1u << 16);
             const int i = warp - kMmaWarp;
@@ -1089,6 +1246,13 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
                                 mma_from_smem<kPair>(ts + 64 * b, q_desc + (((k >> 2) * kQRows * 128 + in) >> 4),
                                                      k_desc + (((k >> 2) * S::kKeysK * 128 + in) >> 4), kIdescS, k > 0);
                             }
+                            if constexpr (INT4)
+                                mma_from_smem<kPair>(
+                                    ts + 64 * b,
+                                    smem_desc_sw32(smem_u32(dyn + S::kOffExtQ + i * kQRows * S::kExtRow)),
+                                    smem_desc_sw32(buf_addr + bk * S::kTileBytes + S::kKeysK * DIM * 2 +
+                                                   b * (S::kKeysK / 2) * S::kExtRow),
+                                    kIdescS, 1);
                             commit_both<kPair>(&sh.s_full[i][b]);
                             if (b) commit_both<kPair>(&sh.empty[bk]);
                         }
@@ -1132,6 +1296,9 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
             uint32_t raw_phase = 0, phase = 0;
             bool ok = true;
             const int tid = threadIdx.x & 127;
+            // 4 bits: the factors' slot, and the meetings of the four warps over a tile's range, so far
+            [[maybe_unused]] int sc = 0, ranges = 0;
+            [[maybe_unused]] uint32_t sc_phase = 0, met = 0;
             while (ok && walk.next(s)) {
                 for (int n = 2 * (s.t1 - s.t0); n > 0; --n) {
                     if (!(ok = warp_wait(&sh.abort, &sh.raw_full[raw], raw_phase))) break;
@@ -1139,12 +1306,50 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
                     const uint8_t* src = dyn + S::kOffRaw + raw * S::kRawBytes;
                     uint8_t* dst = dyn + S::kOffBufs + buf * S::kTileBytes;
                     if constexpr (INT4) {
+                        const uint8_t* pairs = src + S::kCodeBytes;
                         // (n counts down: the tile is t1 - (n + 1) / 2)
-                        if (n & 1)
-                            convert_tile4<S::kDimsV, kTile, DIM / 32>(src, src + S::kCodeBytes, rank * (S::kDimsV / 32),
-                                                                      s.sq.len - (s.t1 - (n + 1) / 2) * kTile, dst, tid);
-                        else
-                            convert_tile4<DIM, S::kKeysK, DIM / 32>(src, src + S::kCodeBytes, 0, kTile, dst, tid);
+                        const int valid = s.sq.len - (s.t1 - (n + 1) / 2) * kTile;
+                        if (n & 1) {
+                            convert_v4<S::kDimsV, DIM / 32>(src, pairs, rank * (S::kDimsV / 32), valid, dst, tid);
+                        } else {
+                            if (!(ok = warp_wait(&sh.abort, &sh.sc_empty[sc], sc_phase ^ 1))) break;
+                            // how large the tile's keys are, and how far apart: a key a thread
+                            const float big = tid < valid ? key_range<DIM / 32>(pairs, tid) : 0.0f;
+                            const uint32_t bits = __float_as_uint(big);
+                            uint32_t most = __reduce_max_sync(0xffffffffu, bits);
+                            uint32_t least = __reduce_min_sync(0xffffffffu, bits ? bits : 0x7F800000u);
+                            const auto meet = [&]() {
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(&sh.ranged);
+                                ok = warp_wait(&sh.abort, &sh.ranged, met);
+                                met ^= 1;
+                                return ok;
+                            };
+                            if (lane == 0) sh.range[ranges][warp - kConvertWarp] = make_uint2(most, least);
+                            if (!meet()) break;
+#pragma unroll
+                            for (int w = 0; w < 4; ++w) {
+                                most = max(most, sh.range[ranges][w].x);
+                                least = min(least, sh.range[ranges][w].y);
+                            }
+                            ranges ^= 1;
+                            float* slot = reinterpret_cast<float*>(dyn + S::kOffScale + sc * S::kScaleBytes);
+                            float back;
+                            float f = key_factor(__uint_as_float(most), back);
+                            if (most != 0 && (least >> 23) + 10 < (most >> 23)) {
+                                (void)key_factor(big, back);
+                                slot[4 + tid] = back;
+                                back = f = 0.0f;
+                            }
+                            if (tid == 0) slot[0] = back;
+                            if (f == 0.0f && !meet()) break;  // the others' keys' factors are there
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sh.sc_full[sc]);
+                            if (++sc == S::kScaleBufs) sc = 0, sc_phase ^= 1;
+                            convert_k4<DIM, S::kKeysK>(src, pairs, f, slot + 4, dst, tid, [&](int row) {
+                                return kPair ? (row >> 5) * kStep + 32 * rank + (row & 31) : row;
+                            });
+                        }
                     } else {
                         if (n & 1) convert_tile<S::kDimsV, kTile, false>(src, dst, tid);  // V
                         else convert_tile<DIM, S::kKeysK, true>(src, dst, tid);           // K
