@@ -37,6 +37,20 @@
 // are worth.  A bf16 step takes a logic operation more for two codes: 92.5 us
 // where all steps do, 88.0 where none does (4 sequences of up to 65538 keys,
 // 64/8 heads; 86.7 without the test).
+//
+// 4-bit codes.  A masked nibble in the low bits of a half is an fp16 number as
+// it stands, code 2^-24 (below the normal ones, which the tensor cores take in
+// their stride) or, from bits 4 to 7, code 2^-20: five logic operations make
+// eight codes of a word into operands, half of what int8's take, and what the
+// odd places have too much is taken out of q (2^-4) or of the finished sums.
+// The word holds neighbouring dims 16 bits apart, so that one mask makes a pair.
+//   q . k = sum_g scale_g (q_g . code_g) + low_g (sum of q_g)
+// takes an accumulator and a fused multiply-add for each group of 32 dims; the
+// second term is one more product step for all groups, of the lowest values
+// against the sums of q in three bf16 pieces (24 bits).
+//   sum_j p_j v_j = sum_j (p_j scale_jg) code_j + sum_j p_j low_jg
+// takes p once for each group, times its scale, in fp16 (11 bits; bf16 where that
+// has too little range, as for int8), and fp32 sums for the second term.
 
 #include "bd_attention.cuh"
 
@@ -144,23 +158,30 @@ constexpr int kMmaMaxRows = 16;  // rows of an item: 8, or 16
 // registers or fewer, unless a stage takes 32 KB (three blocks then have room
 // for two stages each: 155 us for the batch of 32 caches of 4096 .. 8192 keys
 // against 132).
-constexpr int mma_blocks_per_sm(int rows, int dim, bool int8) { return rows == 8 && (int8 || dim == 64) ? 3 : 2; }
+constexpr int mma_blocks_per_sm(int rows, int dim, bool codes) { return rows == 8 && (codes || dim == 64) ? 3 : 2; }
+
+constexpr int kBf16 = 0, kInt8 = 1, kInt4 = 2;  // what the cache holds
 
 struct MmaParams {
-    CUtensorMap k_map, v_map;  // [n_pages * n_kv][page][dim], box a row (in halves of 128 bytes) x min(page, 64)
+    // [n_pages * n_kv][page][dim], box a row (in halves of 128 bytes) x min(page, 64); 4 bits: rows of 128 bytes,
+    // which hold 2 or 4 keys
+    CUtensorMap k_map, v_map;
     AttnParams p;
     int stages;
 };
 
 // NT: groups of 8 rows of an item.
-template <int DIM, bool INT8, int NT>
+template <int DIM, int KIND, int NT>
 struct MmaShape {
+    static constexpr bool INT8 = KIND == kInt8, INT4 = KIND == kInt4;
     static constexpr int kRows = 8 * NT;
-    static constexpr int kRowBytes = DIM * (INT8 ? 1 : 2);
+    static constexpr int kRowBytes = INT4 ? DIM / 2 : DIM * (INT8 ? 1 : 2);
+    static constexpr int kPairBytes = INT4 ? DIM / 8 : INT8 ? 4 : 0;  // scales of a key (and its lowest values)
     static constexpr int kBoxBytes = kRowBytes < 128 ? kRowBytes : 128;  // bytes of a row in one box
     static constexpr int kHalves = kRowBytes / kBoxBytes;
     static constexpr int kTileBytes = kMmaTile * kRowBytes;               // K (or V) of a stage
-    static constexpr int kStageBytes = 2 * kTileBytes + (INT8 ? 1024 : 0);  // stages stay 1024-byte aligned
+    // stages stay 1024-byte aligned
+    static constexpr int kStageBytes = 2 * kTileBytes + (INT4 ? 2 * kMmaTile * kPairBytes : INT8 ? 1024 : 0);
     static constexpr int kBufBytes = 2 * kRows * DIM * 4;              // sums of an item, two warps each
     // what a block of a cluster gets of its rows from the others, for two items in turn
     static constexpr int kRecvBytes = 2 * kRows * (DIM + 4) * 4;
@@ -490,6 +511,17 @@ __device__ __forceinline__ void consumers_sync()
     asm volatile("bar.sync 1, %0;" ::"n"(32 * kMmaConsumers) : "memory");
 }
 
+// Byte offset of the codes of key t's group c of 32 dims in a tile of 4-bit keys:
+// 256 / DIM of them to a row of 128 bytes (TMA's 128-byte swizzle).  Eight
+// neighbouring keys' chunks lie in different banks.
+template <int DIM>
+__device__ __forceinline__ uint32_t codes_at(int t, int c)
+{
+    constexpr int kPer = 256 / DIM, kShift = DIM == 128 ? 1 : 2;
+    const int row = t >> kShift;
+    return static_cast<uint32_t>(row * 128 + ((((t & (kPer - 1)) * (DIM / 32) + c) ^ (row & 7)) << 4));
+}
+
 // Byte offset of 16-byte chunk c of row t in a box of 128- or 64-byte rows
 // (TMA's 128- or 64-byte swizzle).
 template <int BOX_BYTES>
@@ -501,11 +533,51 @@ __device__ __forceinline__ uint32_t swizzled(int t, int c)
         return static_cast<uint32_t>(t * 64 + ((c ^ ((t >> 1) & 3)) << 4));
 }
 
-template <int DIM, bool INT8, int NT, bool WHOLE>
-__global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, INT8))
+// A lane's pairs (scale, lowest value) of a key's groups out of shared memory.
+template <int GROUPS>
+__device__ __forceinline__ void load_pairs(const uint8_t* p, uint32_t (&w)[GROUPS])
+{
+    if constexpr (GROUPS == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        w[0] = v.x, w[1] = v.y;
+    }
+}
+__device__ __forceinline__ float pair_scale(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float pair_low(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b)
+{
+    const __nv_bfloat162 r =
+        __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b)
+{
+    const __nv_bfloat162 r =
+        __hmin2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Nibbles 0 and 4 of r as a pair of bf16 numbers `times` (a power of two) their value.
+__device__ __forceinline__ uint32_t nibbles_bf16x2(uint32_t r, float times)
+{
+    const uint32_t x = (r & 0x000F000Fu) | 0x43004300u;  // 128 + code
+    const __nv_bfloat162 d = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x), __float2bfloat162_rn(times),
+                                     __float2bfloat162_rn(-128.0f * times));
+    return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+template <int DIM, int KIND, int NT, bool WHOLE>
+__global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KIND != kBf16))
     attn_mma_kernel(const __grid_constant__ MmaParams mp)
 {
-    using S = MmaShape<DIM, INT8, NT>;
+    using S = MmaShape<DIM, KIND, NT>;
+    constexpr bool INT8 = S::INT8, INT4 = S::INT4;
+    [[maybe_unused]] constexpr int kGroups = DIM / 32;  // of a head, with 4-bit codes
+    constexpr float kBias = attn_bias<INT8 || INT4>();
     constexpr int kSteps = DIM / 16;  // MMA steps of q . k, and 16-dim tiles of the output
     // all of it dynamic: the ring starts on a 1024-byte boundary without padding
     extern __shared__ __align__(1024) uint8_t dyn_raw[];
@@ -584,7 +656,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
                     if (ok)
                         mbar_arrive_expect_tx(&sh.full[stage],
                                               static_cast<uint32_t>(boxes * box_rows) *
-                                                  (2 * S::kRowBytes + (INT8 ? 8 : 0)));
+                                                  (2 * (S::kRowBytes + S::kPairBytes)));
                 }
                 if (!__shfl_sync(0xffffffffu, ok, 0)) {
                     // given up: leave only when the copies in flight have landed (each stage's last
@@ -598,18 +670,23 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
                     const int row = key & (cache.page - 1);
                     const int outer = page * n_kv + h;
                     uint8_t* dst = st + lane * box_rows * S::kRowBytes;
-                    if constexpr (S::kHalves == 2) {
+                    if constexpr (INT4) {
+                        const int line = row * S::kRowBytes / 128;
+                        tma_load_3d(dst, &mp.k_map, 0, line, outer, &sh.full[stage]);
+                        tma_load_3d(dst + S::kTileBytes, &mp.v_map, 0, line, outer, &sh.full[stage]);
+                    } else if constexpr (S::kHalves == 2) {
                         tma_load_4d(dst, &mp.k_map, 0, row, 0, outer, &sh.full[stage]);
                         tma_load_4d(dst + S::kTileBytes, &mp.v_map, 0, row, 0, outer, &sh.full[stage]);
                     } else {
                         tma_load_3d(dst, &mp.k_map, 0, row, outer, &sh.full[stage]);
                         tma_load_3d(dst + S::kTileBytes, &mp.v_map, 0, row, outer, &sh.full[stage]);
                     }
-                    if constexpr (INT8) {
-                        const int64_t vec = (static_cast<int64_t>(outer) << cache.page_shift) + row;
-                        uint8_t* sc = st + 2 * S::kTileBytes + lane * box_rows * 4;
-                        bulk_g2s(sc, cache.k_scale + vec, box_rows * 4, &sh.full[stage]);
-                        bulk_g2s(sc + kMmaTile * 4, cache.v_scale + vec, box_rows * 4, &sh.full[stage]);
+                    if constexpr (INT8 || INT4) {
+                        const int64_t vec = ((static_cast<int64_t>(outer) << cache.page_shift) + row) * (S::kPairBytes / 4);
+                        uint8_t* sc = st + 2 * S::kTileBytes + lane * box_rows * S::kPairBytes;
+                        bulk_g2s(sc, cache.k_scale + vec, box_rows * S::kPairBytes, &sh.full[stage]);
+                        bulk_g2s(sc + kMmaTile * S::kPairBytes, cache.v_scale + vec, box_rows * S::kPairBytes,
+                                 &sh.full[stage]);
                     }
                 }
                 if (++stage == mp.stages) {
@@ -634,6 +711,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
         // Q as B fragments: this thread has dims of query row 8 n + g.  Its scores, sums and maxima are
         // those of rows 8 n + 2 q4 + {0, 1}: keys they see, and the factor of their scores.
         uint32_t qf[NT][kSteps][2];
+        [[maybe_unused]] uint32_t qs[NT][2];  // 4 bits: the sum of q over group q4, in three pieces
         int seen[NT][2];
         float cr[NT][2];
 #pragma unroll
@@ -645,7 +723,46 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
                                   static_cast<int64_t>(h * p.G + (live ? r - tok * p.G : 0)) * DIM;
             const int sees = live ? attn_seen(sq, tok, a.causal) : 0;
             float factor = c2;
-            if constexpr (INT8) {
+            if constexpr (INT4) {
+                // word q4 of a group holds its dims 8 q4 .. 8 q4 + 7: two steps of 16, whose second pair is 2^4
+                // too large; a negative scale is taken into q's sign
+                uint4 w[kGroups];
+                float big = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kGroups; ++k) {
+                    w[k] = live ? *reinterpret_cast<const uint4*>(src + 32 * k + 8 * q4) : make_uint4(0, 0, 0, 0);
+                    const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        big = fmaxf(big, fmaxf(fabsf(__uint_as_float(u[e] << 16)),
+                                               fabsf(__uint_as_float(u[e] & 0xFFFF0000u))));
+                }
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                const float unit = pow2_of(big), f = a.scale < 0.0f ? -16384.0f / unit : 16384.0f / unit;
+                // (a scale of 0 would make NaN of a masked score)
+                factor = fmaxf(fabsf(c2) * (unit / 16384.0f) * 16777216.0f, 1e-37f);
+                float mine = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kGroups; ++k) {
+                    const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float x = __uint_as_float(u[e] << 16) * f, y = __uint_as_float(u[e] & 0xFFFF0000u) * f;
+                        qf[n][2 * k + e / 2][e & 1] = e & 1 ? pack_f16x2(x * 0.0625f, y * 0.0625f) : pack_f16x2(x, y);
+                        sum += x + y;
+                    }
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                    if (q4 == k) mine = sum;
+                }
+                mine *= 1.0f / 16777216.0f;
+                const float hi = __bfloat162float(__float2bfloat16_rn(mine));
+                const float mid = __bfloat162float(__float2bfloat16_rn(mine - hi));
+                qs[n][0] = pack_bf16x2(hi, mid);
+                qs[n][1] = pack_bf16x2(mine - hi - mid, 0.0f);
+            } else if constexpr (INT8) {
                 // a code fragment holds dims 4 q4 + {0, 2} and 4 q4 + {1, 3} of a step's 16
                 uint2 w[kSteps];
                 float big = 0.0f;
@@ -678,7 +795,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
 #pragma unroll
             for (int i = 0; i < 2; ++i) {  // from the lanes that loaded these rows
                 seen[n][i] = __shfl_sync(0xffffffffu, sees, 4 * (2 * q4 + i));
-                cr[n][i] = INT8 ? __shfl_sync(0xffffffffu, factor, 4 * (2 * q4 + i)) : c2;
+                cr[n][i] = INT8 || INT4 ? __shfl_sync(0xffffffffu, factor, 4 * (2 * q4 + i)) : c2;
             }
         }
         // a tile in shared memory: page boxes of box_rows keys, in each the halves of 128 bytes one
@@ -693,7 +810,10 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
         // the keys that every live row sees: below, no mask is needed
         const int all_seen = attn_seen(sq, row0 / p.G, a.causal);
 
-        float o[NT][kSteps][4];  // dims of tile k (bf16: g, g + 8; int8: 2 g, 2 g + 1) x rows 8 n + 2 q4 + {0, 1}
+        // dims of tile k (bf16: g, g + 8; int8: 2 g, 2 g + 1; 4 bits: 32 (k / 2) + 8 (g / 2) + g % 2 + 4 (k % 2) + {0, 2},
+        // over 2^24 and 2^20) x rows 8 n + 2 q4 + {0, 1}
+        float o[NT][kSteps][4];
+        [[maybe_unused]] float low[NT][INT4 ? kGroups : 1][2] = {};  // 4 bits: sums of p times the lowest values
         float m[NT][2], l[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -707,7 +827,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
                 l[n][i] = 0.0f;
             }
         }
-        float v_unit = 0.0f;  // int8: power of two at or above every scale of V so far, times 2^(bias - 15)
+        float v_unit = 0.0f;  // int8, 4 bits: power of two at or above every scale of V so far, times 2^(bias - 15)
 
         for (int t = t0; t < t1; ++t, ++turn) {
             // every warp waits for every stage and hands it back, the ones that are not its own at once:
@@ -730,223 +850,428 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
             const int key0 = t * kMmaTile + slice;    // and in the sequence
             const int mi = lane >> 3, mr = lane & 7;
 
-            // ---- scores of 32 keys x 8 NT rows: this thread's keys are 16 b + 8 j + g
-            float s[NT][2][4] = {};  // [row group][b][2 j + row]
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int row = slice + 16 * b + (mi & 1) * 8 + mr;
-                if constexpr (INT8) {
-#pragma unroll
-                    for (int k = 0; k < kSteps; k += 2) {
-                        uint32_t r[4];
-                        ldsm_x4(st + swizzled<S::kBoxBytes>(row, k + (mi >> 1)), r);
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const uint32_t a0 = codes_f16x2(r[2 * x]), a1 = codes_f16x2(r[2 * x + 1]);
-                            const uint32_t a2 = codes_f16x2(r[2 * x] >> 8), a3 = codes_f16x2(r[2 * x + 1] >> 8);
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                mma_f16_16816(s[n][b], a0, a1, a2, a3, qf[n][k + x][0], qf[n][k + x][1]);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < kSteps; ++k) {
-                        uint32_t r[4];
-                        const int chunk = 2 * k + (mi >> 1);
-                        ldsm_x4(st + chunk_at(row, chunk), r);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            mma_bf16_16816(s[n][b], r[0], r[1], r[2], r[3], qf[n][k][0], qf[n][k][1]);
-                    }
-                }
-            }
-
-            // ---- to units of log2, masked
-            float vs[2][2];
-            if constexpr (INT8) {
-                const float* sc = reinterpret_cast<const float*>(ring + static_cast<size_t>(stage) * S::kStageBytes +
-                                                                 2 * S::kTileBytes) +
-                                  slice + g;
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float ks = sc[16 * b + 8 * j];
-                        vs[b][j] = sc[kMmaTile + 16 * b + 8 * j];
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) s[n][b][2 * j + i] *= ks * cr[n][i];
-                    }
-            } else {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int b = 0; b < 2; ++b)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s[n][b][e] *= c2;
-            }
-            const bool tail = key0 + kMmaKeys > sq.len;
-            if (key0 + kMmaKeys > all_seen) {
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int key = key0 + 16 * b + 8 * j + g;
-                        // what lies past the sequence may be anything, NaN included: zeros instead
-                        if (INT8 && key >= sq.len) vs[b][j] = 0.0f;
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i)
-                                if (key >= seen[n][i]) s[n][b][2 * j + i] = -INFINITY;
-                    }
-            }
-
-            // ---- running maxima, over this thread's keys and the 8 lanes of its rows
-            float mt[NT][2];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    mt[n][i] = fmaxf(fmaxf(s[n][0][i], s[n][0][2 + i]), fmaxf(s[n][1][i], s[n][1][2 + i]));
-            float v_new = v_unit, v_max = 0.0f;
-            if constexpr (INT8) v_max = fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1]));
-#pragma unroll
-            for (int x = 4; x < 32; x <<= 1) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) mt[n][i] = fmaxf(mt[n][i], __shfl_xor_sync(0xffffffffu, mt[n][i], x));
-                if constexpr (INT8) v_max = fmaxf(v_max, __shfl_xor_sync(0xffffffffu, v_max, x));
-            }
-            bool grow = false;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) grow = grow || mt[n][i] > m[n][i];
-            if constexpr (INT8) {
-                constexpr float kUnit = static_cast<float>(1u << (static_cast<int>(attn_bias<true>()) - 14));
-                if (v_max * (0.5f * kUnit) > 0.5f * v_unit) v_new = pow2_of(v_max) * kUnit;
-                grow = grow || v_new != v_unit;
-            }
-            if (__any_sync(0xffffffffu, grow)) {
-                const float fv = INT8 && v_new != v_unit ? v_unit / v_new : 1.0f;
-                v_unit = v_new;
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float up = fmaxf(m[n][i], mt[n][i]);
-                        const float f = up == -INFINITY ? 1.0f : ex2(m[n][i] - up);
-                        m[n][i] = up;
-                        l[n][i] *= f;
-#pragma unroll
-                        for (int k = 0; k < kSteps; ++k) {
-                            o[n][k][i] *= f * fv;
-                            o[n][k][2 + i] *= f * fv;
-                        }
-                    }
-            }
-
-            // ---- probabilities, turned into B fragments: keys 16 b + 8 j + 2 q4 + {0, 1} of row 8 n + g
-            uint32_t pb[NT][2][2];
-            [[maybe_unused]] float pw[NT][2][4];  // int8: what is to be rounded
-            [[maybe_unused]] uint32_t least = 0xFFFFFFFFu;  // the least of it that is not 0: its bits less 1
-            const float v_inv = INT8 ? (v_unit > 0.0f ? 1.0f / v_unit : 0.0f) : 1.0f;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float mu[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) mu[i] = m[n][i] == -INFINITY ? 0.0f : m[n][i] - attn_bias<INT8>();
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float p0 = ex2(s[n][b][2 * j] - mu[0]), p1 = ex2(s[n][b][2 * j + 1] - mu[1]);
-                        l[n][0] += p0;
-                        l[n][1] += p1;
-                        if constexpr (INT8) {
-                            const float w = vs[b][j] * v_inv;
-                            pw[n][b][2 * j] = p0 * w, pw[n][b][2 * j + 1] = p1 * w;
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                least = min(least, __float_as_uint(pw[n][b][2 * j + e]) - 1u);
-                        } else {
-                            pb[n][b][j] = transpose8(pack_bf16x2(p0, p1));
-                        }
-                    }
-            }
-
-            // ---- sums: dim x 8 NT rows += V^T (dim x 32) P^T (32 x 8 NT)
-            const uint32_t vt = st + S::kTileBytes;
-            // a b16 element is a pair of dims: the transposed fragment holds dims 2 g, 2 g + 1 of two keys;
-            // the tile's rows 0..7 take the even dims of a chunk, rows 8..15 the odd ones
-            [[maybe_unused]] const auto add_codes = [&](auto as_bf16) {
-                constexpr bool kBf16 = decltype(as_bf16)::value;
+            if constexpr (INT4) {
+                const uint8_t* pairs = ring + static_cast<size_t>(stage) * S::kStageBytes + 2 * S::kTileBytes;
+                // ---- scores of 32 keys x 8 NT rows: this thread's keys are 16 b + 8 j + g
+                float s[NT][2][4] = {};  // [row group][b][2 j + row]
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
+                    const uint8_t* kp = pairs + (slice + 16 * b + g) * S::kPairBytes;
+                    const uint32_t w0 = *reinterpret_cast<const uint32_t*>(kp + 4 * (q4 & (kGroups - 1)));
+                    const uint32_t w1 =
+                        *reinterpret_cast<const uint32_t*>(kp + 8 * S::kPairBytes + 4 * (q4 & (kGroups - 1)));
+                    const uint32_t l0 = __byte_perm(w0, 0, 0x3232), l1 = __byte_perm(w1, 0, 0x3232);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const float x = pw[n][b][2 * j], y = pw[n][b][2 * j + 1];
-                            pb[n][b][j] = transpose8(kBf16 ? pack_bf16x2(x, y) : pack_f16x2(x, y));
-                        }
+                    for (int n = 0; n < NT; ++n) mma_bf16_16816(s[n][b], l0, l1, l0, l1, qs[n][0], qs[n][1]);
+                    uint32_t sc0[kGroups], sc1[kGroups];
+                    load_pairs<kGroups>(kp, sc0);
+                    load_pairs<kGroups>(kp + 8 * S::kPairBytes, sc1);
                     const int row = slice + 16 * b + (mi & 1) * 8 + mr;
 #pragma unroll
-                    for (int k = 0; k < kSteps; k += 2) {
+                    for (int k = 0; k < kGroups; k += 2) {
                         uint32_t r[4];
-                        ldsm_x4_t(vt + swizzled<S::kBoxBytes>(row, k + (mi >> 1)), r);
+                        ldsm_x4(st + codes_at<DIM>(row, k + (mi >> 1)), r);
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            if constexpr (kBf16) {
-                                const uint32_t a0 = codes_bf16x2(r[2 * x]), a1 = codes_bf16x2(r[2 * x] >> 8);
-                                const uint32_t a2 = codes_bf16x2(r[2 * x + 1]), a3 = codes_bf16x2(r[2 * x + 1] >> 8);
+                            const uint32_t u0 = r[2 * x], u1 = r[2 * x + 1], h0 = u0 >> 8, h1 = u1 >> 8;
 #pragma unroll
-                                for (int n = 0; n < NT; ++n)
-                                    mma_bf16_16816(o[n][k + x], a0, a1, a2, a3, pb[n][b][0], pb[n][b][1]);
-                            } else {
-                                const uint32_t a0 = codes_f16x2(r[2 * x]), a1 = codes_f16x2(r[2 * x] >> 8);
-                                const uint32_t a2 = codes_f16x2(r[2 * x + 1]), a3 = codes_f16x2(r[2 * x + 1] >> 8);
+                            for (int n = 0; n < NT; ++n) {
+                                float d[4] = {};
+                                mma_f16_16816(d, u0 & 0x000F000Fu, u1 & 0x000F000Fu, u0 & 0x00F000F0u, u1 & 0x00F000F0u,
+                                              qf[n][2 * (k + x)][0], qf[n][2 * (k + x)][1]);
+                                mma_f16_16816(d, h0 & 0x000F000Fu, h1 & 0x000F000Fu, h0 & 0x00F000F0u, h1 & 0x00F000F0u,
+                                              qf[n][2 * (k + x) + 1][0], qf[n][2 * (k + x) + 1][1]);
 #pragma unroll
-                                for (int n = 0; n < NT; ++n)
-                                    mma_f16_16816(o[n][k + x], a0, a1, a2, a3, pb[n][b][0], pb[n][b][1]);
+                                for (int e = 0; e < 4; ++e)
+                                    s[n][b][e] = fmaf(d[e], pair_scale(e < 2 ? sc0[k + x] : sc1[k + x]), s[n][b][e]);
                             }
                         }
                     }
                 }
-            };
-            if constexpr (INT8) {
+                uint32_t vw[2][2][kGroups];  // of V's keys
+                uint32_t v_most, v_least;
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        load_pairs<kGroups>(pairs + (kMmaTile + slice + 16 * b + 8 * j + g) * S::kPairBytes, vw[b][j]);
+                const bool tail = key0 + kMmaKeys > sq.len;
+                const auto past = [&](uint32_t value) {  // what stands for the pairs past the sequence
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+#pragma unroll
+                            for (int k = 0; k < kGroups; ++k)
+                                if (key0 + 16 * b + 8 * j + g >= sq.len) vw[b][j][k] = value;
+                };
+                // (what lies there may be anything, NaN included: NaN, which no maximum or minimum takes, and then zeros)
+                if (tail) past(0x7FFF7FFFu);
+                v_most = v_least = vw[0][0][0];
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int k = 0; k < kGroups; ++k) {
+                            v_most = max_bf16x2(v_most, vw[b][j][k]);
+                            v_least = min_bf16x2(v_least, vw[b][j][k]);
+                        }
+                if (tail) past(0u);
+                if (key0 + kMmaKeys > all_seen) {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i)
+                                    if (key0 + 16 * b + 8 * j + g >= seen[n][i]) s[n][b][2 * j + i] = -INFINITY;
+                }
+
+                // ---- running maxima (units of log2), over this thread's keys and the 8 lanes of its rows
+                float mt[NT][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        mt[n][i] = fmaxf(fmaxf(s[n][0][i], s[n][0][2 + i]), fmaxf(s[n][1][i], s[n][1][2 + i]));
+                float v_max = fmaxf(0.0f, pair_scale(v_most));
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) mt[n][i] = fmaxf(mt[n][i], __shfl_xor_sync(0xffffffffu, mt[n][i], x));
+                    v_max = fmaxf(v_max, __shfl_xor_sync(0xffffffffu, v_max, x));
+                }
+                float v_new = v_unit;
+                constexpr float kUnit = static_cast<float>(1u << (static_cast<int>(kBias) - 14));
+                if (v_max * (0.5f * kUnit) > 0.5f * v_unit) v_new = pow2_of(v_max) * kUnit;
+                bool grow = v_new != v_unit;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        mt[n][i] *= cr[n][i];
+                        grow = grow || mt[n][i] > m[n][i];
+                    }
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float fv = v_new != v_unit ? v_unit / v_new : 1.0f;
+                    v_unit = v_new;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float up = fmaxf(m[n][i], mt[n][i]);
+                            const float f = up == -INFINITY ? 1.0f : ex2(m[n][i] - up);
+                            m[n][i] = up;
+                            l[n][i] *= f;
+#pragma unroll
+                            for (int k = 0; k < kGroups; ++k) low[n][k][i] *= f;
+#pragma unroll
+                            for (int k = 0; k < kSteps; ++k) {
+                                o[n][k][i] *= f * fv;
+                                o[n][k][2 + i] *= f * fv;
+                            }
+                        }
+                }
+
+                // ---- probabilities; s becomes them over the scales' unit
+                const float v_inv = v_unit > 0.0f ? 1.0f / v_unit : 0.0f;
+                uint32_t least = 0xFFFFFFFFu;  // the least of it that is not 0: its bits less 1
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float mu = m[n][i] == -INFINITY ? 0.0f : m[n][i] - kBias;
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const float p = ex2(fmaf(s[n][b][2 * j + i], cr[n][i], -mu));
+                                l[n][i] += p;
+#pragma unroll
+                                for (int k = 0; k < kGroups; ++k)
+                                    low[n][k][i] = fmaf(p, pair_low(vw[b][j][k]), low[n][k][i]);
+                                s[n][b][2 * j + i] = p * v_inv;
+                                least = min(least, __float_as_uint(p * v_inv) - 1u);
+                            }
+                    }
+
+                // ---- sums: dim x 8 NT rows += V^T (dim x 32) P^T (32 x 8 NT), group by group.  A b16 element is four
+                // dims: the transposed fragment holds dims 8 (g / 2) + g % 2 + 2 i of two keys in its nibbles i
+                const uint32_t vt = st + S::kTileBytes;
+                const auto add_codes = [&](auto as_bf16) {
+                    constexpr bool kAsBf16 = decltype(as_bf16)::value;
+                    constexpr float kTimes = kAsBf16 ? 1.0f / 16777216.0f : 1.0f;
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const int row = slice + 16 * b + (mi & 1) * 8 + mr;
+#pragma unroll
+                        for (int k = 0; k < kGroups; k += 2) {
+                            uint32_t r[4];
+                            ldsm_x4_t(vt + codes_at<DIM>(row, k + (mi >> 1)), r);
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const uint32_t u0 = r[2 * x], u1 = r[2 * x + 1];
+                                uint32_t pb[NT][2];
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    const float sc = pair_scale(vw[b][j][k + x]) * kTimes;
+#pragma unroll
+                                    for (int n = 0; n < NT; ++n) {
+                                        const float y0 = s[n][b][2 * j] * sc, y1 = s[n][b][2 * j + 1] * sc;
+                                        pb[n][j] = transpose8(kAsBf16 ? pack_bf16x2(y0, y1) : pack_f16x2(y0, y1));
+                                    }
+                                }
+#pragma unroll
+                                for (int y = 0; y < 2; ++y) {
+                                    uint32_t a0, a1, a2, a3;
+                                    if constexpr (kAsBf16) {
+                                        a0 = nibbles_bf16x2(u0 >> (8 * y), 1.0f), a1 = nibbles_bf16x2(u0 >> (8 * y + 4), 16.0f);
+                                        a2 = nibbles_bf16x2(u1 >> (8 * y), 1.0f), a3 = nibbles_bf16x2(u1 >> (8 * y + 4), 16.0f);
+                                    } else {
+                                        const uint32_t t0 = u0 >> (8 * y), t1 = u1 >> (8 * y);
+                                        a0 = t0 & 0x000F000Fu, a1 = t0 & 0x00F000F0u;
+                                        a2 = t1 & 0x000F000Fu, a3 = t1 & 0x00F000F0u;
+                                    }
+#pragma unroll
+                                    for (int n = 0; n < NT; ++n) {
+                                        float (&d)[4] = o[n][2 * (k + x) + y];
+                                        if constexpr (kAsBf16) mma_bf16_16816(d, a0, a1, a2, a3, pb[n][0], pb[n][1]);
+                                        else mma_f16_16816(d, a0, a1, a2, a3, pb[n][0], pb[n][1]);
+                                    }
+                                }
+                            }
+                        }
+                    }
+                };
                 // some of it would lose bits in fp16
-                if (__any_sync(0xffffffffu, least < kFp16Normal)) add_codes(std::true_type{});
-                else add_codes(std::false_type{});
+                if (__any_sync(0xffffffffu, __uint_as_float(least) * pair_scale(v_least) < __uint_as_float(kFp16Normal)))
+                    add_codes(std::true_type{});
+                else
+                    add_codes(std::false_type{});
             } else {
+                // ---- scores of 32 keys x 8 NT rows: this thread's keys are 16 b + 8 j + g
+                float s[NT][2][4] = {};  // [row group][b][2 j + row]
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    uint32_t mask0 = 0xFFFFFFFFu, mask1 = 0xFFFFFFFFu;
-                    if (tail) {
-                        // zeros for what lies past the sequence
-                        const int k = key0 + 16 * b + 2 * q4;
-                        mask0 = (k < sq.len ? 0xFFFFu : 0u) | (k + 1 < sq.len ? 0xFFFF0000u : 0u);
-                        mask1 = (k + 8 < sq.len ? 0xFFFFu : 0u) | (k + 9 < sq.len ? 0xFFFF0000u : 0u);
-                    }
-                    const int row = slice + 16 * b + (mi >> 1) * 8 + mr;
+                    const int row = slice + 16 * b + (mi & 1) * 8 + mr;
+                    if constexpr (INT8) {
 #pragma unroll
-                    for (int k = 0; k < kSteps; ++k) {
-                        uint32_t r[4];
-                        const int chunk = 2 * k + (mi & 1);
-                        ldsm_x4_t(vt + chunk_at(row, chunk), r);
-                        if (tail) {
-                            r[0] &= mask0;
-                            r[1] &= mask0;
-                            r[2] &= mask1;
-                            r[3] &= mask1;
+                        for (int k = 0; k < kSteps; k += 2) {
+                            uint32_t r[4];
+                            ldsm_x4(st + swizzled<S::kBoxBytes>(row, k + (mi >> 1)), r);
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const uint32_t a0 = codes_f16x2(r[2 * x]), a1 = codes_f16x2(r[2 * x + 1]);
+                                const uint32_t a2 = codes_f16x2(r[2 * x] >> 8), a3 = codes_f16x2(r[2 * x + 1] >> 8);
+#pragma unroll
+                                for (int n = 0; n < NT; ++n)
+                                    mma_f16_16816(s[n][b], a0, a1, a2, a3, qf[n][k + x][0], qf[n][k + x][1]);
+                            }
                         }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < kSteps; ++k) {
+                            uint32_t r[4];
+                            const int chunk = 2 * k + (mi >> 1);
+                            ldsm_x4(st + chunk_at(row, chunk), r);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma_bf16_16816(s[n][b], r[0], r[1], r[2], r[3], qf[n][k][0], qf[n][k][1]);
+                        }
+                    }
+                }
+
+                // ---- to units of log2, masked
+                float vs[2][2];
+                if constexpr (INT8) {
+                    const float* sc = reinterpret_cast<const float*>(ring + static_cast<size_t>(stage) * S::kStageBytes +
+                                                                     2 * S::kTileBytes) +
+                                      slice + g;
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float ks = sc[16 * b + 8 * j];
+                            vs[b][j] = sc[kMmaTile + 16 * b + 8 * j];
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) s[n][b][2 * j + i] *= ks * cr[n][i];
+                        }
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) s[n][b][e] *= c2;
+                }
+                const bool tail = key0 + kMmaKeys > sq.len;
+                if (key0 + kMmaKeys > all_seen) {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int key = key0 + 16 * b + 8 * j + g;
+                            // what lies past the sequence may be anything, NaN included: zeros instead
+                            if (INT8 && key >= sq.len) vs[b][j] = 0.0f;
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i)
+                                    if (key >= seen[n][i]) s[n][b][2 * j + i] = -INFINITY;
+                        }
+                }
+
+                // ---- running maxima, over this thread's keys and the 8 lanes of its rows
+                float mt[NT][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        mt[n][i] = fmaxf(fmaxf(s[n][0][i], s[n][0][2 + i]), fmaxf(s[n][1][i], s[n][1][2 + i]));
+                float v_new = v_unit, v_max = 0.0f;
+                if constexpr (INT8) v_max = fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1]));
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) mt[n][i] = fmaxf(mt[n][i], __shfl_xor_sync(0xffffffffu, mt[n][i], x));
+                    if constexpr (INT8) v_max = fmaxf(v_max, __shfl_xor_sync(0xffffffffu, v_max, x));
+                }
+                bool grow = false;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) grow = grow || mt[n][i] > m[n][i];
+                if constexpr (INT8) {
+                    constexpr float kUnit = static_cast<float>(1u << (static_cast<int>(attn_bias<true>()) - 14));
+                    if (v_max * (0.5f * kUnit) > 0.5f * v_unit) v_new = pow2_of(v_max) * kUnit;
+                    grow = grow || v_new != v_unit;
+                }
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float fv = INT8 && v_new != v_unit ? v_unit / v_new : 1.0f;
+                    v_unit = v_new;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float up = fmaxf(m[n][i], mt[n][i]);
+                            const float f = up == -INFINITY ? 1.0f : ex2(m[n][i] - up);
+                            m[n][i] = up;
+                            l[n][i] *= f;
+#pragma unroll
+                            for (int k = 0; k < kSteps; ++k) {
+                                o[n][k][i] *= f * fv;
+                                o[n][k][2 + i] *= f * fv;
+                            }
+                        }
+                }
+
+                // ---- probabilities, turned into B fragments: keys 16 b + 8 j + 2 q4 + {0, 1} of row 8 n + g
+                uint32_t pb[NT][2][2];
+                [[maybe_unused]] float pw[NT][2][4];  // int8: what is to be rounded
+                [[maybe_unused]] uint32_t least = 0xFFFFFFFFu;  // the least of it that is not 0: its bits less 1
+                const float v_inv = INT8 ? (v_unit > 0.0f ? 1.0f / v_unit : 0.0f) : 1.0f;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float mu[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) mu[i] = m[n][i] == -INFINITY ? 0.0f : m[n][i] - attn_bias<INT8>();
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float p0 = ex2(s[n][b][2 * j] - mu[0]), p1 = ex2(s[n][b][2 * j + 1] - mu[1]);
+                            l[n][0] += p0;
+                            l[n][1] += p1;
+                            if constexpr (INT8) {
+                                const float w = vs[b][j] * v_inv;
+                                pw[n][b][2 * j] = p0 * w, pw[n][b][2 * j + 1] = p1 * w;
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    least = min(least, __float_as_uint(pw[n][b][2 * j + e]) - 1u);
+                            } else {
+                                pb[n][b][j] = transpose8(pack_bf16x2(p0, p1));
+                            }
+                        }
+                }
+
+                // ---- sums: dim x 8 NT rows += V^T (dim x 32) P^T (32 x 8 NT)
+                const uint32_t vt = st + S::kTileBytes;
+                // a b16 element is a pair of dims: the transposed fragment holds dims 2 g, 2 g + 1 of two keys;
+                // the tile's rows 0..7 take the even dims of a chunk, rows 8..15 the odd ones
+                [[maybe_unused]] const auto add_codes = [&](auto as_bf16) {
+                    constexpr bool kBf16 = decltype(as_bf16)::value;
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
-                            mma_bf16_16816(o[n][k], r[0], r[1], r[2], r[3], pb[n][b][0], pb[n][b][1]);
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const float x = pw[n][b][2 * j], y = pw[n][b][2 * j + 1];
+                                pb[n][b][j] = transpose8(kBf16 ? pack_bf16x2(x, y) : pack_f16x2(x, y));
+                            }
+                        const int row = slice + 16 * b + (mi & 1) * 8 + mr;
+#pragma unroll
+                        for (int k = 0; k < kSteps; k += 2) {
+                            uint32_t r[4];
+                            ldsm_x4_t(vt + swizzled<S::kBoxBytes>(row, k + (mi >> 1)), r);
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                if constexpr (kBf16) {
+                                    const uint32_t a0 = codes_bf16x2(r[2 * x]), a1 = codes_bf16x2(r[2 * x] >> 8);
+                                    const uint32_t a2 = codes_bf16x2(r[2 * x + 1]), a3 = codes_bf16x2(r[2 * x + 1] >> 8);
+#pragma unroll
+                                    for (int n = 0; n < NT; ++n)
+                                        mma_bf16_16816(o[n][k + x], a0, a1, a2, a3, pb[n][b][0], pb[n][b][1]);
+                                } else {
+                                    const uint32_t a0 = codes_f16x2(r[2 * x]), a1 = codes_f16x2(r[2 * x] >> 8);
+                                    const uint32_t a2 = codes_f16x2(r[2 * x + 1]), a3 = codes_f16x2(r[2 * x + 1] >> 8);
+#pragma unroll
+                                    for (int n = 0; n < NT; ++n)
+                                        mma_f16_16816(o[n][k + x], a0, a1, a2, a3, pb[n][b][0], pb[n][b][1]);
+                                }
+                            }
+                        }
+                    }
+                };
+                if constexpr (INT8) {
+                    // some of it would lose bits in fp16
+                    if (__any_sync(0xffffffffu, least < kFp16Normal)) add_codes(std::true_type{});
+                    else add_codes(std::false_type{});
+                } else {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        uint32_t mask0 = 0xFFFFFFFFu, mask1 = 0xFFFFFFFFu;
+                        if (tail) {
+                            // zeros for what lies past the sequence
+                            const int k = key0 + 16 * b + 2 * q4;
+                            mask0 = (k < sq.len ? 0xFFFFu : 0u) | (k + 1 < sq.len ? 0xFFFF0000u : 0u);
+                            mask1 = (k + 8 < sq.len ? 0xFFFFu : 0u) | (k + 9 < sq.len ? 0xFFFF0000u : 0u);
+                        }
+                        const int row = slice + 16 * b + (mi >> 1) * 8 + mr;
+#pragma unroll
+                        for (int k = 0; k < kSteps; ++k) {
+                            uint32_t r[4];
+                            const int chunk = 2 * k + (mi & 1);
+                            ldsm_x4_t(vt + chunk_at(row, chunk), r);
+                            if (tail) {
+                                r[0] &= mask0;
+                                r[1] &= mask0;
+                                r[2] &= mask1;
+                                r[3] &= mask1;
+                            }
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma_bf16_16816(o[n][k], r[0], r[1], r[2], r[3], pb[n][b][0], pb[n][b][1]);
+                        }
                     }
                 }
             }
@@ -965,7 +1290,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
             for (int i = 0; i < 2; ++i) {
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], x);
-                m[n][i] -= attn_bias<INT8>();
+                m[n][i] -= kBias;
                 if (g == 0) {
                     sh.m[warp][8 * n + 2 * q4 + i] = m[n][i];
                     sh.l[warp][8 * n + 2 * q4 + i] = l[n][i];
@@ -983,6 +1308,12 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
                 for (int w = 1; w < kMmaConsumers; ++w) mm = fmaxf(mm, sh.m[w][r]);
                 f[n][i] = attn_weight(m[n][i], l[n][i], mm);
                 if (INT8 && f[n][i] != 0.0f) f[n][i] *= v_unit;  // the sums are over the scales' unit
+                if constexpr (INT4) {
+#pragma unroll
+                    for (int k = 0; k < kGroups; ++k)
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1) low[n][k][i] += __shfl_xor_sync(0xffffffffu, low[n][k][i], x);
+                }
             }
 #pragma unroll 1
         for (int w = 0; w < 2; ++w) {
@@ -993,8 +1324,21 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         float* line = mine + (8 * n + 2 * q4 + i) * DIM;
+                        [[maybe_unused]] const int swap = (q4 & 1) << 2;
 #pragma unroll
                         for (int k = 0; k < kSteps; ++k) {
+                            if constexpr (INT4) {
+                                const float unit = v_unit * 16777216.0f, lw = low[n][k / 2][i];
+                                const float x = f[n][i] == 0.0f ? 0.0f : fmaf(o[n][k][i], unit, lw) * f[n][i];
+                                const float y =
+                                    f[n][i] == 0.0f ? 0.0f : fmaf(o[n][k][2 + i], unit * 0.0625f, lw) * f[n][i];
+                                const int d = 32 * (k / 2) + 8 * (g >> 1) + (g & 1) + 4 * (k & 1);
+                                float* b0 = line + (d ^ swap);
+                                float* b1 = line + ((d + 2) ^ swap);
+                                *b0 = w ? *b0 + x : x;
+                                *b1 = w ? *b1 + y : y;
+                                continue;
+                            }
                             // (in an order of the row's own: the lanes' banks differ)
                             const float x = f[n][i] == 0.0f ? 0.0f : o[n][k][i] * f[n][i];
                             const float y = f[n][i] == 0.0f ? 0.0f : o[n][k][2 + i] * f[n][i];
@@ -1038,7 +1382,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, IN
                 const float lw = sh.l[w][r];
                 ll += lw * attn_weight(sh.m[w][r], lw, mm);
             }
-            const int place = r * DIM + (d ^ (((r >> 1) & 3) << (INT8 ? 4 : 3)));
+            const int place = r * DIM + (d ^ (INT4 ? ((r >> 1) & 1) << 2 : ((r >> 1) & 3) << (INT8 ? 4 : 3)));
             float4 v = *reinterpret_cast<const float4*>(buf + place);
             const float4 v1 = *reinterpret_cast<const float4*>(buf + S::kRows * DIM + place);
             v = make_float4(v.x + v1.x, v.y + v1.y, v.z + v1.z, v.w + v1.w);
@@ -1174,34 +1518,38 @@ __global__ void __launch_bounds__(kJoinThreads, BATCH <= 4 ? 12 : 4)
     }
 }
 
-template <int DIM, bool INT8, int NT, bool WHOLE>
+template <int DIM, int KIND, int NT, bool WHOLE>
 cudaError_t launch_mma_shape(const AttnParams& p, cudaStream_t stream)
 {
-    using S = MmaShape<DIM, INT8, NT>;
+    using S = MmaShape<DIM, KIND, NT>;
+    constexpr bool kCodes = KIND != kBf16;
     static std::atomic<size_t> smem_set[kHostMaxDevices];
     const KvPages& kv = p.a.cache;
     MmaParams mp{};
     mp.p = p;
     const uint32_t box_rows = kv.page < kMmaTile ? kv.page : kMmaTile;
-    const auto type = INT8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const auto type = kCodes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const auto swz = S::kBoxBytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
     const uint64_t outer = static_cast<uint64_t>(kv.n_pages) * kv.n_kv;
     for (int i = 0; i < 2; ++i) {
         CUtensorMap* map = i ? &mp.v_map : &mp.k_map;
         const void* base = i ? kv.v : kv.k;
-        if (!(S::kHalves == 2 ? encode_tma_parts(map, type, 2, base, DIM, kv.page, outer, 2, box_rows, swz)
-                              : encode_tma_3d(map, type, INT8 ? 1 : 2, base, DIM, kv.page, outer, DIM, box_rows, swz)))
+        if (!(S::INT4 ? encode_tma_3d(map, type, 1, base, 128, kv.page * S::kRowBytes / 128, outer, 128,
+                                      box_rows * S::kRowBytes / 128, CU_TENSOR_MAP_SWIZZLE_128B)
+              : S::kHalves == 2
+                  ? encode_tma_parts(map, type, 2, base, DIM, kv.page, outer, 2, box_rows, swz)
+                  : encode_tma_3d(map, type, kCodes ? 1 : 2, base, DIM, kv.page, outer, DIM, box_rows, swz)))
             return cudaErrorInvalidValue;
     }
     // the SM's shared memory shared by the blocks that it holds; all of it
     // where there are no more blocks than SMs
     const size_t rest = S::kBufBytes + sizeof(MmaShared) + (p.whole > 1 ? S::kRecvBytes : 0);
     const size_t budget = p.blocks <= p.a.sm_count ? 227u * 1024u
-                                                   : 228u * 1024u / mma_blocks_per_sm(8 * NT, DIM, INT8) - 1024u;
+                                                   : 228u * 1024u / mma_blocks_per_sm(8 * NT, DIM, kCodes) - 1024u;
     mp.stages = static_cast<int>((budget - rest) / S::kStageBytes);
     if (mp.stages > kMmaMaxStages) mp.stages = kMmaMaxStages;
     const size_t smem = static_cast<size_t>(mp.stages) * S::kStageBytes + rest;
-    const auto kernel = attn_mma_kernel<DIM, INT8, NT, WHOLE>;
+    const auto kernel = attn_mma_kernel<DIM, KIND, NT, WHOLE>;
     cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem, smem_set);
     launch_dep_clusters(err, kernel, dim3(p.blocks), dim3(kMmaThreads), WHOLE ? p.whole : 1, smem, stream, mp);
     return err;
@@ -1232,22 +1580,20 @@ AttnWs attn_layout(int64_t rows, int64_t n_seq, int dim, int mb, int blocks)
 
 cudaError_t launch_attention_mma(const AttnParams& p, cudaStream_t stream)
 {
-    const auto of = [&](auto dim, auto int8) {
-        constexpr int kDim = decltype(dim)::value;
-        constexpr bool kInt8 = decltype(int8)::value;
+    const auto of = [&](auto dim, auto kind) {
+        constexpr int kDim = decltype(dim)::value, kKind = decltype(kind)::value;
         if (p.mb == 8)
-            return p.whole ? launch_mma_shape<kDim, kInt8, 1, true>(p, stream)
-                           : launch_mma_shape<kDim, kInt8, 1, false>(p, stream);
-        return p.whole ? launch_mma_shape<kDim, kInt8, 2, true>(p, stream)
-                       : launch_mma_shape<kDim, kInt8, 2, false>(p, stream);
+            return p.whole ? launch_mma_shape<kDim, kKind, 1, true>(p, stream)
+                           : launch_mma_shape<kDim, kKind, 1, false>(p, stream);
+        return p.whole ? launch_mma_shape<kDim, kKind, 2, true>(p, stream)
+                       : launch_mma_shape<kDim, kKind, 2, false>(p, stream);
     };
-    using Dim64 = std::integral_constant<int, 64>;
-    using Dim128 = std::integral_constant<int, 128>;
-    using Yes = std::true_type;
-    using No = std::false_type;
-    if (p.a.cache.dim == 128)
-        return p.a.cache.int8 ? of(Dim128{}, Yes{}) : of(Dim128{}, No{});
-    return p.a.cache.int8 ? of(Dim64{}, Yes{}) : of(Dim64{}, No{});
+    const auto of_kind = [&](auto dim) {
+        if (p.a.cache.int4) return of(dim, std::integral_constant<int, kInt4>{});
+        return p.a.cache.int8 ? of(dim, std::integral_constant<int, kInt8>{})
+                              : of(dim, std::integral_constant<int, kBf16>{});
+    };
+    return p.a.cache.dim == 128 ? of_kind(std::integral_constant<int, 128>{}) : of_kind(std::integral_constant<int, 64>{});
 }
 
 size_t attention_workspace_size(int64_t T, int64_t n_seq, int n_q, int n_kv, int dim)
@@ -1302,7 +1648,7 @@ static void launch_few_rows(cudaError_t& err, AttnParams p, int rows, bool deal,
     const AttentionArgs& a = p.a;
     p.tile = kMmaTile;
     p.mb = rows > 8 ? kMmaMaxRows : 8;
-    p.blocks = mma_blocks_per_sm(p.mb, a.cache.dim, a.cache.int8) * a.sm_count;
+    p.blocks = mma_blocks_per_sm(p.mb, a.cache.dim, a.cache.int8 || a.cache.int4) * a.sm_count;
     if (p.blocks > kAttnMaxBlocks) p.blocks = kAttnMaxBlocks;
     // Short caches, or few: a cluster of up to 8 blocks for each (sequence,
     // head), which needs no deal and no second launch.  (cap is the longest
@@ -1342,7 +1688,7 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream)
     cudaError_t err = cudaSuccess;
     // new tokens and rows of a sequence, as far as the host knows
     const int64_t max_new = a.max_new < a.T ? a.max_new : a.T, rows = max_new * p.G;
-    if (rows <= kMmaMaxRows && !a.cache.int4) {
+    if (rows <= kMmaMaxRows) {
         launch_few_rows(err, p, static_cast<int>(rows), false, ws, stream);
         return err;
     }
@@ -1353,7 +1699,7 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream)
     // 7 108 / 108, 31 168 / 218; int8 109 / 101, 122 / 143, 157 / 302).  Not
     // where the number of tokens says that all sequences have max_new, nor for
     // few sequences, nor for chunks so small that the launch costs too much.
-    const bool split = !a.cache.int4 && rows >= 128 && a.n_seq >= 4 && a.T < a.n_seq * max_new;
+    const bool split = rows >= 128 && a.n_seq >= 4 && a.T < a.n_seq * max_new;
     if (split) p.rows_above = kMmaMaxRows;
     launch_chunks(err, p, rows, ws, stream);
     if (split) {
