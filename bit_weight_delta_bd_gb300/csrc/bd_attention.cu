@@ -147,9 +147,14 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
 
 // ------------------------------------------------------------------------------- decode kernel
 
-constexpr int kMmaTile = 64;     // keys of a stage
+constexpr int kBf16 = 0, kInt8 = 1, kInt4 = 2;  // what the cache holds
+// Keys of a stage: 64, of which two warps take half each and two none; 4-bit
+// codes 128, of which every warp takes a quarter (what a warp does for a stage
+// beside its keys weighs more where these take less).
+constexpr int mma_tile(int kind) { return kind == kInt4 ? 128 : 64; }
 constexpr int kMmaConsumers = 4;
 constexpr int kMmaKeys = 32;     // keys of a stage that one warp takes
+constexpr float kMmaLag = 4.0f;  // how far (log2) a row's maximum may run ahead of the one in use (4-bit codes)
 constexpr int kMmaThreads = 32 * (kMmaConsumers + 1);
 constexpr int kMmaMaxStages = 8;
 constexpr int kMmaMaxRows = 16;  // rows of an item: 8, or 16
@@ -160,10 +165,8 @@ constexpr int kMmaMaxRows = 16;  // rows of an item: 8, or 16
 // against 132).
 constexpr int mma_blocks_per_sm(int rows, int dim, bool codes) { return rows == 8 && (codes || dim == 64) ? 3 : 2; }
 
-constexpr int kBf16 = 0, kInt8 = 1, kInt4 = 2;  // what the cache holds
-
 struct MmaParams {
-    // [n_pages * n_kv][page][dim], box a row (in halves of 128 bytes) x min(page, 64); 4 bits: rows of 128 bytes,
+    // [n_pages * n_kv][page][dim], box a row (in halves of 128 bytes) x min(page, tile); 4 bits: rows of 128 bytes,
     // which hold 2 or 4 keys
     CUtensorMap k_map, v_map;
     AttnParams p;
@@ -179,9 +182,10 @@ struct MmaShape {
     static constexpr int kPairBytes = INT4 ? DIM / 8 : INT8 ? 4 : 0;  // scales of a key (and its lowest values)
     static constexpr int kBoxBytes = kRowBytes < 128 ? kRowBytes : 128;  // bytes of a row in one box
     static constexpr int kHalves = kRowBytes / kBoxBytes;
-    static constexpr int kTileBytes = kMmaTile * kRowBytes;               // K (or V) of a stage
+    static constexpr int kTile = mma_tile(KIND);
+    static constexpr int kTileBytes = kTile * kRowBytes;                  // K (or V) of a stage
     // stages stay 1024-byte aligned
-    static constexpr int kStageBytes = 2 * kTileBytes + (INT4 ? 2 * kMmaTile * kPairBytes : INT8 ? 1024 : 0);
+    static constexpr int kStageBytes = 2 * kTileBytes + (INT4 ? 2 * kTile * kPairBytes : INT8 ? 1024 : 0);
     static constexpr int kBufBytes = 2 * kRows * DIM * 4;              // sums of an item, two warps each
     // what a block of a cluster gets of its rows from the others, for two items in turn
     static constexpr int kRecvBytes = 2 * kRows * (DIM + 4) * 4;
@@ -200,13 +204,14 @@ struct alignas(16) MmaShared {
 };
 
 // Key tiles of one head of the item of sequence q that starts at row0.
+template <int TILE>
 __device__ __forceinline__ int mma_tiles(const AttnParams& p, const AttnSeq& q, int row0)
 {
     int last = row0 + p.mb - 1;
     const int rows = q.n_new * p.G;
     if (last >= rows) last = rows - 1;
     const int end = attn_seen(q, last / p.G, p.a.causal);
-    return end > 0 ? (end + kMmaTile - 1) / kMmaTile : 1;
+    return end > 0 ? (end + TILE - 1) / TILE : 1;
 }
 
 // What a block does next: key tiles [t0, t1) of one (item, kv head).
@@ -218,6 +223,7 @@ struct MmaSegment {
 
 // A block's segments in order.  The lengths of the next sequence are loaded
 // while the present one is worked on.
+template <int TILE>
 struct MmaWalk {
     const AttnParams& p;
     int64_t u, end, before;  // next unit, last one + 1, units before the present item
@@ -232,7 +238,7 @@ struct MmaWalk {
         s.row0 = row0;
         s.sq = attn_seq(p, seq, false);
         s.rows = s.sq.n_new * p.G;
-        s.tiles = mma_tiles(p, s.sq, row0);
+        s.tiles = mma_tiles<TILE>(p, s.sq, row0);
         look_ahead();
     }
     __device__ __forceinline__ void look_ahead()
@@ -253,7 +259,7 @@ struct MmaWalk {
                 s.row0 = 0;
                 look_ahead();
             }
-            s.tiles = mma_tiles(p, s.sq, s.row0);
+            s.tiles = mma_tiles<TILE>(p, s.sq, s.row0);
         }
         const int64_t rel = u - before;
         s.h = attn_div(rel, s.tiles);
@@ -268,6 +274,7 @@ struct MmaWalk {
 // The segments of a block of a cluster that has a (sequence, head) to itself:
 // its items in order (one, in a decode step), with this block's share of their
 // tiles, which may be none.
+template <int TILE>
 struct WholeWalk {
     const AttnParams& p;
     MmaSegment s;
@@ -287,7 +294,7 @@ struct WholeWalk {
     {
         s.row0 += p.mb;
         if (s.row0 >= s.rows) return false;
-        s.tiles = mma_tiles(p, s.sq, s.row0);
+        s.tiles = mma_tiles<TILE>(p, s.sq, s.row0);
         s.t0 = static_cast<int>(static_cast<int64_t>(s.tiles) * rank / p.whole);
         s.t1 = static_cast<int>(static_cast<int64_t>(s.tiles) * (rank + 1) / p.whole);
         return true;
@@ -297,7 +304,8 @@ struct WholeWalk {
 // The whole block: adds up the tiles of all sequences (each thread those of
 // consecutive ones), finds the item of the block's first unit and notes down
 // what the join needs.  The block's segments.
-__device__ __forceinline__ MmaWalk mma_deal(const AttnParams& p, MmaShared& sh)
+template <int TILE>
+__device__ __forceinline__ MmaWalk<TILE> mma_deal(const AttnParams& p, MmaShared& sh)
 {
     const AttentionArgs& a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -308,7 +316,7 @@ __device__ __forceinline__ MmaWalk mma_deal(const AttnParams& p, MmaShared& sh)
     int64_t mine = 0;
     for (int s = s0; s < s1; ++s) {
         const AttnSeq q = attn_seq(p, s, blockIdx.x == 0);
-        for (int row0 = 0; row0 < q.n_new * p.G; row0 += p.mb) mine += mma_tiles(p, q, row0);
+        for (int row0 = 0; row0 < q.n_new * p.G; row0 += p.mb) mine += mma_tiles<TILE>(p, q, row0);
     }
     int64_t x = mine;
 #pragma unroll
@@ -335,7 +343,7 @@ __device__ __forceinline__ MmaWalk mma_deal(const AttnParams& p, MmaShared& sh)
             for (int s = s0; s < s1; ++s) {
                 const AttnSeq q = attn_seq(p, s, false);
                 for (int row0 = 0; row0 < q.n_new * p.G; row0 += p.mb) {
-                    const int64_t n = static_cast<int64_t>(mma_tiles(p, q, row0)) * n_kv;
+                    const int64_t n = static_cast<int64_t>(mma_tiles<TILE>(p, q, row0)) * n_kv;
                     if (u >= before && u < before + n) {
                         sh.seq = s;
                         sh.row0 = row0;
@@ -348,7 +356,7 @@ __device__ __forceinline__ MmaWalk mma_deal(const AttnParams& p, MmaShared& sh)
     }
     __syncthreads();
     const int c = blockIdx.x;
-    MmaWalk walk(p, c < active ? attn_first(units, active, c) : 0, c < active ? attn_first(units, active, c + 1) : 0,
+    MmaWalk<TILE> walk(p, c < active ? attn_first(units, active, c) : 0, c < active ? attn_first(units, active, c + 1) : 0,
                  sh.seq, sh.row0, sh.before);
     if (threadIdx.x == 0) {
         AttnJoin j{};
@@ -363,11 +371,11 @@ __device__ __forceinline__ MmaWalk mma_deal(const AttnParams& p, MmaShared& sh)
     return walk;
 }
 
-template <bool WHOLE>
+template <bool WHOLE, int TILE>
 __device__ __forceinline__ auto mma_walk(const AttnParams& p, MmaShared& sh)
 {
-    if constexpr (WHOLE) return WholeWalk(p);
-    else return mma_deal(p, sh);
+    if constexpr (WHOLE) return WholeWalk<TILE>(p);
+    else return mma_deal<TILE>(p, sh);
 }
 
 __device__ __forceinline__ bool attn_wait(volatile int* abort_flag, uint64_t* bar, uint32_t parity, uint32_t* err)
@@ -492,6 +500,16 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same with sums of zero before it.
+__device__ __forceinline__ void mma_f16_16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                    uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 // 2^e with e the exponent of |x| (x normal), kept within 2^-100 .. 2^100
 __device__ __forceinline__ float pow2_of(float x)
 {
@@ -548,17 +566,17 @@ __device__ __forceinline__ void load_pairs(const uint8_t* p, uint32_t (&w)[GROUP
 __device__ __forceinline__ float pair_scale(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float pair_low(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b)
+__device__ __forceinline__ float max3(float a, float b, float c)
 {
-    const __nv_bfloat162 r =
-        __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
-__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b)
+__device__ __forceinline__ float min3(float a, float b, float c)
 {
-    const __nv_bfloat162 r =
-        __hmin2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
+    float r;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 // Nibbles 0 and 4 of r as a pair of bf16 numbers `times` (a power of two) their value.
@@ -617,7 +635,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
     grid_dependency_wait();
 
     const int n_kv = cache.n_kv;
-    auto walk = mma_walk<WHOLE>(p, sh);
+    auto walk = mma_walk<WHOLE, S::kTile>(p, sh);
     const MmaSegment& sg = walk.s;
     int walk_rank = 0;
     if constexpr (WHOLE) walk_rank = walk.rank;
@@ -626,12 +644,12 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
 
     if (warp == kMmaConsumers) {
         // ------------------------------------------------------------ producer warp
-        const int box_rows = cache.page < kMmaTile ? cache.page : kMmaTile;
-        const int pages_per_tile = kMmaTile / box_rows;
+        const int box_rows = cache.page < S::kTile ? cache.page : S::kTile;
+        const int pages_per_tile = S::kTile / box_rows;
         // The page of this lane's box in a tile (lane j looks after the j-th box), looked up one tile
         // ahead, whether the sequence reaches it or not.
         const auto page_of = [&](int t) {
-            const int at = (t * kMmaTile + lane * box_rows) >> cache.page_shift;
+            const int at = (t * S::kTile + lane * box_rows) >> cache.page_shift;
             return lane < pages_per_tile && at < a.max_pages
                        ? a.table[static_cast<int64_t>(sg.seq) * a.max_pages + at]
                        : 0;
@@ -641,7 +659,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
             const int pages = (sg.sq.len + cache.page - 1) >> cache.page_shift;  // that the sequence has
             int page_next = page_of(sg.t0);
             for (int t = sg.t0; t < sg.t1; ++t) {
-                const int key = t * kMmaTile + lane * box_rows;
+                const int key = t * S::kTile + lane * box_rows;
                 const bool mine = lane < pages_per_tile && (key >> cache.page_shift) < pages;
                 int page = page_next;
                 if (t + 1 < sg.t1) page_next = page_of(t + 1);
@@ -685,7 +703,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
                         const int64_t vec = ((static_cast<int64_t>(outer) << cache.page_shift) + row) * (S::kPairBytes / 4);
                         uint8_t* sc = st + 2 * S::kTileBytes + lane * box_rows * S::kPairBytes;
                         bulk_g2s(sc, cache.k_scale + vec, box_rows * S::kPairBytes, &sh.full[stage]);
-                        bulk_g2s(sc + kMmaTile * S::kPairBytes, cache.v_scale + vec, box_rows * S::kPairBytes,
+                        bulk_g2s(sc + S::kTile * S::kPairBytes, cache.v_scale + vec, box_rows * S::kPairBytes,
                                  &sh.full[stage]);
                     }
                 }
@@ -704,6 +722,11 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
     [[maybe_unused]] uint32_t item = 0;  // of a cluster, so far
     [[maybe_unused]] bool gave_up = false;
     int turn = 0;  // stages so far: this warp takes those of its parity
+    // 4 bits: where in a tile of codes this lane's rows of the fragments of groups 0 and 1 begin; those of
+    // groups 2 and 3 differ in the bit of 2 << 4.  16 keys on lie 8 DIM bytes on, with heads of 64 (four rows of
+    // 128 bytes) in the other half of the swizzle
+    constexpr uint32_t kStep16 = DIM == 64 ? 64 : 0;
+    [[maybe_unused]] const uint32_t code_base = codes_at<DIM>(kMmaKeys * warp + (lane >> 3 & 1) * 8 + (lane & 7), lane >> 4);
     while (walk.next()) {
         const AttnSeq sq = sg.sq;
         const int h = sg.h, t0 = sg.t0, t1 = sg.t1, rows = sg.rows, row0 = sg.row0;
@@ -800,7 +823,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
         }
         // a tile in shared memory: page boxes of box_rows keys, in each the halves of 128 bytes one
         // after the other (rows of 128 bytes or less have one)
-        const int box_shift = cache.page < kMmaTile ? cache.page_shift : 6;
+        const int box_shift = cache.page < S::kTile ? cache.page_shift : 6;
         const auto chunk_at = [&](int row, int chunk) {
             if constexpr (S::kHalves == 1) return swizzled<S::kBoxBytes>(row, chunk);
             const int box = row >> box_shift, half = chunk >> 3;
@@ -837,7 +860,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
                 turn += t1 - t;
                 break;
             }
-            if ((turn & 1) != (warp >> 1)) {
+            if (!INT4 && (turn & 1) != (warp >> 1)) {
                 if (lane == 0) mbar_arrive(&sh.empty[stage]);
                 if (++stage == mp.stages) {
                     stage = 0;
@@ -846,11 +869,13 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
                 continue;
             }
             const uint32_t st = smem_u32(ring) + static_cast<uint32_t>(stage) * S::kStageBytes;
-            const int slice = kMmaKeys * (warp & 1);  // this warp's keys of the stage
-            const int key0 = t * kMmaTile + slice;    // and in the sequence
+            const int slice = kMmaKeys * (INT4 ? warp : warp & 1);  // this warp's keys of the stage
+            const int key0 = t * S::kTile + slice;                  // and in the sequence
             const int mi = lane >> 3, mr = lane & 7;
 
-            if constexpr (INT4) {
+            if (INT4 && key0 >= sq.len && key0 != 0) {
+                // nothing of the sequence here
+            } else if constexpr (INT4) {
                 const uint8_t* pairs = ring + static_cast<size_t>(stage) * S::kStageBytes + 2 * S::kTileBytes;
                 // ---- scores of 32 keys x 8 NT rows: this thread's keys are 16 b + 8 j + g
                 float s[NT][2][4] = {};  // [row group][b][2 j + row]
@@ -866,19 +891,18 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
                     uint32_t sc0[kGroups], sc1[kGroups];
                     load_pairs<kGroups>(kp, sc0);
                     load_pairs<kGroups>(kp + 8 * S::kPairBytes, sc1);
-                    const int row = slice + 16 * b + (mi & 1) * 8 + mr;
 #pragma unroll
                     for (int k = 0; k < kGroups; k += 2) {
                         uint32_t r[4];
-                        ldsm_x4(st + codes_at<DIM>(row, k + (mi >> 1)), r);
+                        ldsm_x4((st + 8 * b * DIM + code_base) ^ (kStep16 * b | k << 4), r);
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             const uint32_t u0 = r[2 * x], u1 = r[2 * x + 1], h0 = u0 >> 8, h1 = u1 >> 8;
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
-                                float d[4] = {};
-                                mma_f16_16816(d, u0 & 0x000F000Fu, u1 & 0x000F000Fu, u0 & 0x00F000F0u, u1 & 0x00F000F0u,
-                                              qf[n][2 * (k + x)][0], qf[n][2 * (k + x)][1]);
+                                float d[4];
+                                mma_f16_16816_first(d, u0 & 0x000F000Fu, u1 & 0x000F000Fu, u0 & 0x00F000F0u, u1 & 0x00F000F0u,
+                                                    qf[n][2 * (k + x)][0], qf[n][2 * (k + x)][1]);
                                 mma_f16_16816(d, h0 & 0x000F000Fu, h1 & 0x000F000Fu, h0 & 0x00F000F0u, h1 & 0x00F000F0u,
                                               qf[n][2 * (k + x) + 1][0], qf[n][2 * (k + x) + 1][1]);
 #pragma unroll
@@ -889,12 +913,11 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
                     }
                 }
                 uint32_t vw[2][2][kGroups];  // of V's keys
-                uint32_t v_most, v_least;
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        load_pairs<kGroups>(pairs + (kMmaTile + slice + 16 * b + 8 * j + g) * S::kPairBytes, vw[b][j]);
+                        load_pairs<kGroups>(pairs + (S::kTile + slice + 16 * b + 8 * j + g) * S::kPairBytes, vw[b][j]);
                 const bool tail = key0 + kMmaKeys > sq.len;
                 const auto past = [&](uint32_t value) {  // what stands for the pairs past the sequence
 #pragma unroll
@@ -907,15 +930,15 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
                 };
                 // (what lies there may be anything, NaN included: NaN, which no maximum or minimum takes, and then zeros)
                 if (tail) past(0x7FFF7FFFu);
-                v_most = v_least = vw[0][0][0];
+                float v_max = 0.0f, v_least = INFINITY;
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
 #pragma unroll
-                        for (int k = 0; k < kGroups; ++k) {
-                            v_most = max_bf16x2(v_most, vw[b][j][k]);
-                            v_least = min_bf16x2(v_least, vw[b][j][k]);
+                        for (int k = 0; k < kGroups; k += 2) {
+                            v_max = max3(v_max, pair_scale(vw[b][j][k]), pair_scale(vw[b][j][k + 1]));
+                            v_least = min3(v_least, pair_scale(vw[b][j][k]), pair_scale(vw[b][j][k + 1]));
                         }
                 if (tail) past(0u);
                 if (key0 + kMmaKeys > all_seen) {
@@ -937,7 +960,6 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
                         mt[n][i] = fmaxf(fmaxf(s[n][0][i], s[n][0][2 + i]), fmaxf(s[n][1][i], s[n][1][2 + i]));
-                float v_max = fmaxf(0.0f, pair_scale(v_most));
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) {
 #pragma unroll
@@ -947,7 +969,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
                     v_max = fmaxf(v_max, __shfl_xor_sync(0xffffffffu, v_max, x));
                 }
                 float v_new = v_unit;
-                constexpr float kUnit = static_cast<float>(1u << (static_cast<int>(kBias) - 14));
+                constexpr float kUnit = static_cast<float>(1u << (static_cast<int>(kBias + kMmaLag) - 14));
                 if (v_max * (0.5f * kUnit) > 0.5f * v_unit) v_new = pow2_of(v_max) * kUnit;
                 bool grow = v_new != v_unit;
 #pragma unroll
@@ -955,7 +977,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         mt[n][i] *= cr[n][i];
-                        grow = grow || mt[n][i] > m[n][i];
+                        grow = grow || mt[n][i] > m[n][i] + kMmaLag;
                     }
                 if (__any_sync(0xffffffffu, grow)) {
                     const float fv = v_new != v_unit ? v_unit / v_new : 1.0f;
@@ -979,8 +1001,9 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
                 }
 
                 // ---- probabilities; s becomes them over the scales' unit
-                const float v_inv = v_unit > 0.0f ? 1.0f / v_unit : 0.0f;
-                uint32_t least = 0xFFFFFFFFu;  // the least of it that is not 0: its bits less 1
+                // (the unit is a power of two: its inverse has the exponent's mirror image)
+                const float v_inv = v_unit > 0.0f ? __uint_as_float(0x7F000000u - __float_as_uint(v_unit)) : 0.0f;
+                float least = INFINITY;  // of it (a masked one's 0 is not looked at)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -996,9 +1019,25 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
                                 for (int k = 0; k < kGroups; ++k)
                                     low[n][k][i] = fmaf(p, pair_low(vw[b][j][k]), low[n][k][i]);
                                 s[n][b][2 * j + i] = p * v_inv;
-                                least = min(least, __float_as_uint(p * v_inv) - 1u);
                             }
                     }
+                if (key0 + kMmaKeys > all_seen) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (s[n][b][e] > 0.0f) least = fminf(least, s[n][b][e]);
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            least = min3(least, s[n][b][0], s[n][b][1]);
+                            least = min3(least, s[n][b][2], s[n][b][3]);
+                        }
+                }
 
                 // ---- sums: dim x 8 NT rows += V^T (dim x 32) P^T (32 x 8 NT), group by group.  A b16 element is four
                 // dims: the transposed fragment holds dims 8 (g / 2) + g % 2 + 2 i of two keys in its nibbles i
@@ -1008,11 +1047,10 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
                     constexpr float kTimes = kAsBf16 ? 1.0f / 16777216.0f : 1.0f;
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
-                        const int row = slice + 16 * b + (mi & 1) * 8 + mr;
 #pragma unroll
                         for (int k = 0; k < kGroups; k += 2) {
                             uint32_t r[4];
-                            ldsm_x4_t(vt + codes_at<DIM>(row, k + (mi >> 1)), r);
+                            ldsm_x4_t((vt + 8 * b * DIM + code_base) ^ (kStep16 * b | k << 4), r);
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
                                 const uint32_t u0 = r[2 * x], u1 = r[2 * x + 1];
@@ -1049,7 +1087,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
                     }
                 };
                 // some of it would lose bits in fp16
-                if (__any_sync(0xffffffffu, __uint_as_float(least) * pair_scale(v_least) < __uint_as_float(kFp16Normal)))
+                if (__any_sync(0xffffffffu, least * v_least < __uint_as_float(kFp16Normal)))
                     add_codes(std::true_type{});
                 else
                     add_codes(std::false_type{});
@@ -1097,7 +1135,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             const float ks = sc[16 * b + 8 * j];
-                            vs[b][j] = sc[kMmaTile + 16 * b + 8 * j];
+                            vs[b][j] = sc[S::kTile + 16 * b + 8 * j];
 #pragma unroll
                             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -1527,7 +1565,7 @@ cudaError_t launch_mma_shape(const AttnParams& p, cudaStream_t stream)
     const KvPages& kv = p.a.cache;
     MmaParams mp{};
     mp.p = p;
-    const uint32_t box_rows = kv.page < kMmaTile ? kv.page : kMmaTile;
+    const uint32_t box_rows = kv.page < S::kTile ? kv.page : S::kTile;
     const auto type = kCodes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const auto swz = S::kBoxBytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
     const uint64_t outer = static_cast<uint64_t>(kv.n_pages) * kv.n_kv;
@@ -1646,7 +1684,7 @@ static void launch_chunks(cudaError_t& err, AttnParams p, int64_t rows, char*& w
 static void launch_few_rows(cudaError_t& err, AttnParams p, int rows, bool deal, char*& ws, cudaStream_t stream)
 {
     const AttentionArgs& a = p.a;
-    p.tile = kMmaTile;
+    p.tile = mma_tile(a.cache.int4 ? kInt4 : a.cache.int8 ? kInt8 : kBf16);
     p.mb = rows > 8 ? kMmaMaxRows : 8;
     p.blocks = mma_blocks_per_sm(p.mb, a.cache.dim, a.cache.int8 || a.cache.int4) * a.sm_count;
     if (p.blocks > kAttnMaxBlocks) p.blocks = kAttnMaxBlocks;
