@@ -393,6 +393,18 @@ __device__ __forceinline__ bool attn_wait(volatile int* abort_flag, uint64_t* ba
     return true;
 }
 
+// The same asleep, in a few instructions (a wait that asks again and again takes
+// the others' turns to issue).
+__device__ __forceinline__ bool attn_wait_asleep(volatile int* abort_flag, uint64_t* bar, uint32_t parity, uint32_t* err)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (mbar_wait_sleeping(bar, parity)) return true;
+    *abort_flag = 1;
+    raise_error(err, kErrTimeout);
+    return false;
+}
+
 // A wait for the other blocks of the cluster; false once given up.
 __device__ __forceinline__ bool mbar_wait_cluster_bounded(uint64_t* bar, uint32_t parity, uint32_t* err)
 {
@@ -670,7 +682,8 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
                 const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
                 bool ok = true;
                 if (lane == 0) {
-                    ok = attn_wait(&sh.abort, &sh.empty[stage], phase ^ 1, a.err);
+                    ok = INT4 ? attn_wait_asleep(&sh.abort, &sh.empty[stage], phase ^ 1, a.err)
+                              : attn_wait(&sh.abort, &sh.empty[stage], phase ^ 1, a.err);
                     if (ok)
                         mbar_arrive_expect_tx(&sh.full[stage],
                                               static_cast<uint32_t>(boxes * box_rows) *
@@ -838,6 +851,9 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
         float o[NT][kSteps][4];
         [[maybe_unused]] float low[NT][INT4 ? kGroups : 1][2] = {};  // 4 bits: sums of p times the lowest values
         float m[NT][2], l[NT][2];
+        // 4 bits: what is added to a row's scores (the bias less its maximum, in units of log2), and the score from
+        // which the maximum moves (-infinity: no key yet), not in those units
+        [[maybe_unused]] float nm[NT][2] = {}, lim[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -848,15 +864,20 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
             for (int i = 0; i < 2; ++i) {
                 m[n][i] = -INFINITY;
                 l[n][i] = 0.0f;
+                lim[n][i] = -INFINITY;
             }
         }
+        [[maybe_unused]] float v_inv = 0.0f;
+        // scales that raise the unit: 2^15 is left for the largest product of a probability
+        [[maybe_unused]] constexpr float kUnit = INT4 ? static_cast<float>(1u << ((static_cast<int>(kBias + kMmaLag) - 14) & 31)) : 1.0f;
         float v_unit = 0.0f;  // int8, 4 bits: power of two at or above every scale of V so far, times 2^(bias - 15)
 
         for (int t = t0; t < t1; ++t, ++turn) {
             // every warp waits for every stage and hands it back, the ones that are not its own at once:
             // a warp that did neither could be two phases away from a barrier, which its parity cannot
             // tell from none.  On a timeout (reported) the warps still meet at the barriers below.
-            if (!__all_sync(0xffffffffu, attn_wait(&sh.abort, &sh.full[stage], phase, a.err))) {
+            if (!__all_sync(0xffffffffu, INT4 ? attn_wait_asleep(&sh.abort, &sh.full[stage], phase, a.err)
+                                              : attn_wait(&sh.abort, &sh.full[stage], phase, a.err))) {
                 turn += t1 - t;
                 break;
             }
@@ -953,42 +974,49 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
                                     if (key0 + 16 * b + 8 * j + g >= seen[n][i]) s[n][b][2 * j + i] = -INFINITY;
                 }
 
-                // ---- running maxima (units of log2), over this thread's keys and the 8 lanes of its rows
-                float mt[NT][2];
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        mt[n][i] = fmaxf(fmaxf(s[n][0][i], s[n][0][2 + i]), fmaxf(s[n][1][i], s[n][1][2 + i]));
-#pragma unroll
-                for (int x = 4; x < 32; x <<= 1) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) mt[n][i] = fmaxf(mt[n][i], __shfl_xor_sync(0xffffffffu, mt[n][i], x));
-                    v_max = fmaxf(v_max, __shfl_xor_sync(0xffffffffu, v_max, x));
-                }
-                float v_new = v_unit;
-                constexpr float kUnit = static_cast<float>(1u << (static_cast<int>(kBias + kMmaLag) - 14));
-                if (v_max * (0.5f * kUnit) > 0.5f * v_unit) v_new = pow2_of(v_max) * kUnit;
-                bool grow = v_new != v_unit;
+                // ---- running maxima.  They lag: a row's moves when one of its scores lies kMmaLag above it, which
+                // after the first keys is rare, so that the lanes need not tell one another their scores
+                bool grow = v_max * (0.5f * kUnit) >= v_unit && v_max > 0.0f;  // by a power of two or more
+                float mt[NT][2];  // of this thread's keys, not yet in units of log2
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        mt[n][i] *= cr[n][i];
-                        grow = grow || mt[n][i] > m[n][i] + kMmaLag;
+                        mt[n][i] = max3(fmaxf(s[n][0][i], s[n][0][2 + i]), s[n][1][i], s[n][1][2 + i]);
+                        grow = grow || mt[n][i] > lim[n][i];
                     }
                 if (__any_sync(0xffffffffu, grow)) {
-                    const float fv = v_new != v_unit ? v_unit / v_new : 1.0f;
-                    v_unit = v_new;
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                mt[n][i] = fmaxf(mt[n][i], __shfl_xor_sync(0xffffffffu, mt[n][i], x));
+                        v_max = fmaxf(v_max, __shfl_xor_sync(0xffffffffu, v_max, x));
+                    }
+                    float fv = 1.0f;
+                    if (v_max * (0.5f * kUnit) >= v_unit && v_max > 0.0f) {
+                        const float v_new = pow2_of(v_max) * kUnit;
+                        fv = v_unit / v_new;
+                        v_unit = v_new;
+                        // (a power of two: its inverse has the exponent's mirror image)
+                        v_inv = __uint_as_float(0x7F000000u - __float_as_uint(v_unit));
+                    }
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const float up = fmaxf(m[n][i], mt[n][i]);
-                            const float f = up == -INFINITY ? 1.0f : ex2(m[n][i] - up);
-                            m[n][i] = up;
+                            float f = 1.0f;
+                            if (mt[n][i] > -INFINITY) {
+                                float to = kBias - mt[n][i] * cr[n][i];
+                                if (lim[n][i] > -INFINITY) {
+                                    to = fminf(to, nm[n][i]);
+                                    f = ex2(to - nm[n][i]);
+                                }
+                                nm[n][i] = to;
+                                lim[n][i] = (kBias + kMmaLag - to) / cr[n][i];
+                            }
                             l[n][i] *= f;
 #pragma unroll
                             for (int k = 0; k < kGroups; ++k) low[n][k][i] *= f;
@@ -1001,26 +1029,22 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
                 }
 
                 // ---- probabilities; s becomes them over the scales' unit
-                // (the unit is a power of two: its inverse has the exponent's mirror image)
-                const float v_inv = v_unit > 0.0f ? __uint_as_float(0x7F000000u - __float_as_uint(v_unit)) : 0.0f;
                 float least = INFINITY;  // of it (a masked one's 0 is not looked at)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float mu = m[n][i] == -INFINITY ? 0.0f : m[n][i] - kBias;
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
                         for (int b = 0; b < 2; ++b)
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
-                                const float p = ex2(fmaf(s[n][b][2 * j + i], cr[n][i], -mu));
+                                const float p = ex2(fmaf(s[n][b][2 * j + i], cr[n][i], nm[n][i]));
                                 l[n][i] += p;
 #pragma unroll
                                 for (int k = 0; k < kGroups; ++k)
                                     low[n][k][i] = fmaf(p, pair_low(vw[b][j][k]), low[n][k][i]);
                                 s[n][b][2 * j + i] = p * v_inv;
                             }
-                    }
                 if (key0 + kMmaKeys > all_seen) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
@@ -1087,7 +1111,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
                     }
                 };
                 // some of it would lose bits in fp16
-                if (__any_sync(0xffffffffu, least * v_least < __uint_as_float(kFp16Normal)))
+                if (__builtin_expect(__any_sync(0xffffffffu, least * v_least < __uint_as_float(kFp16Normal)), 0))
                     add_codes(std::true_type{});
                 else
                     add_codes(std::false_type{});
@@ -1328,7 +1352,8 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
             for (int i = 0; i < 2; ++i) {
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], x);
-                m[n][i] -= kBias;
+                if constexpr (INT4) m[n][i] = lim[n][i] > -INFINITY ? -nm[n][i] : -INFINITY;
+                else m[n][i] -= kBias;
                 if (g == 0) {
                     sh.m[warp][8 * n + 2 * q4 + i] = m[n][i];
                     sh.l[warp][8 * n + 2 * q4 + i] = l[n][i];
