@@ -49,8 +49,13 @@
 // second term is one more product step for all groups, of the lowest values
 // against the sums of q in three bf16 pieces (24 bits).
 //   sum_j p_j v_j = sum_j (p_j scale_jg) code_j + sum_j p_j low_jg
-// takes p once for each group, times its scale, in fp16 (11 bits; bf16 where that
-// has too little range, as for int8), and fp32 sums for the second term.
+// takes p once for each group, times its scale, in fp16 (11 bits), and fp32 sums
+// for the second term.  fp16's range: p is formed over a reference of the row
+// that brings the largest product of a probability with its key's scales and
+// lowest values to 2^11, so that what is rounded to a multiple of 2^-24 is below
+// 2^-35 of what makes up the row's largest values.  (With products of less than
+// 2^-14 in bf16, as for int8, the second form of the loop cost 11% of the time by
+// its registers alone.)
 
 #include "bd_attention.cuh"
 
@@ -154,7 +159,7 @@ constexpr int kBf16 = 0, kInt8 = 1, kInt4 = 2;  // what the cache holds
 constexpr int mma_tile(int kind) { return kind == kInt4 ? 128 : 64; }
 constexpr int kMmaConsumers = 4;
 constexpr int kMmaKeys = 32;     // keys of a stage that one warp takes
-constexpr float kMmaLag = 4.0f;  // how far (log2) a row's maximum may run ahead of the one in use (4-bit codes)
+constexpr float kMmaLag = 4.0f;  // how far (log2) a row's products may grow before its reference moves (4-bit codes)
 constexpr int kMmaThreads = 32 * (kMmaConsumers + 1);
 constexpr int kMmaMaxStages = 8;
 constexpr int kMmaMaxRows = 16;  // rows of an item: 8, or 16
@@ -584,22 +589,6 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-__device__ __forceinline__ float min3(float a, float b, float c)
-{
-    float r;
-    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
-// Nibbles 0 and 4 of r as a pair of bf16 numbers `times` (a power of two) their value.
-__device__ __forceinline__ uint32_t nibbles_bf16x2(uint32_t r, float times)
-{
-    const uint32_t x = (r & 0x000F000Fu) | 0x43004300u;  // 128 + code
-    const __nv_bfloat162 d = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x), __float2bfloat162_rn(times),
-                                     __float2bfloat162_rn(-128.0f * times));
-    return *reinterpret_cast<const uint32_t*>(&d);
-}
-
 template <int DIM, int KIND, int NT, bool WHOLE>
 __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KIND != kBf16))
     attn_mma_kernel(const __grid_constant__ MmaParams mp)
@@ -607,7 +596,6 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
     using S = MmaShape<DIM, KIND, NT>;
     constexpr bool INT8 = S::INT8, INT4 = S::INT4;
     [[maybe_unused]] constexpr int kGroups = DIM / 32;  // of a head, with 4-bit codes
-    constexpr float kBias = attn_bias<INT8 || INT4>();
     constexpr int kSteps = DIM / 16;  // MMA steps of q . k, and 16-dim tiles of the output
     // all of it dynamic: the ring starts on a 1024-byte boundary without padding
     extern __shared__ __align__(1024) uint8_t dyn_raw[];
@@ -851,9 +839,10 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
         float o[NT][kSteps][4];
         [[maybe_unused]] float low[NT][INT4 ? kGroups : 1][2] = {};  // 4 bits: sums of p times the lowest values
         float m[NT][2], l[NT][2];
-        // 4 bits: what is added to a row's scores (the bias less its maximum, in units of log2), and the score from
-        // which the maximum moves (-infinity: no key yet), not in those units
-        [[maybe_unused]] float nm[NT][2] = {}, lim[NT][2];
+        // 4 bits: what is added to a row's scores in units of log2 (its reference, negated); as long as it has seen no
+        // key, so much that the first one passes every limit
+        constexpr float kNoKey = 1e30f;
+        [[maybe_unused]] float nm[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -864,13 +853,10 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
             for (int i = 0; i < 2; ++i) {
                 m[n][i] = -INFINITY;
                 l[n][i] = 0.0f;
-                lim[n][i] = -INFINITY;
+                nm[n][i] = kNoKey;
             }
         }
-        [[maybe_unused]] float v_inv = 0.0f;
-        // scales that raise the unit: 2^15 is left for the largest product of a probability
-        [[maybe_unused]] constexpr float kUnit = INT4 ? static_cast<float>(1u << ((static_cast<int>(kBias + kMmaLag) - 14) & 31)) : 1.0f;
-        float v_unit = 0.0f;  // int8, 4 bits: power of two at or above every scale of V so far, times 2^(bias - 15)
+        float v_unit = 0.0f;  // int8: power of two at or above every scale of V so far, times 2^(bias - 15)
 
         for (int t = t0; t < t1; ++t, ++turn) {
             // every warp waits for every stage and hands it back, the ones that are not its own at once:
@@ -897,7 +883,19 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
             if (INT4 && key0 >= sq.len && key0 != 0) {
                 // nothing of the sequence here
             } else if constexpr (INT4) {
-                const uint8_t* pairs = ring + static_cast<size_t>(stage) * S::kStageBytes + 2 * S::kTileBytes;
+                uint8_t* pairs = ring + static_cast<size_t>(stage) * S::kStageBytes + 2 * S::kTileBytes;
+                if (key0 + kMmaKeys > sq.len) {
+                    // what lies past the sequence may be anything, NaN included: its probabilities are 0, and the
+                    // scales and lowest values of the slice's first key stand in (or 0 where it has none)
+                    uint8_t* first = pairs + (S::kTile + slice) * S::kPairBytes;
+#pragma unroll
+                    for (int k = 0; k < kGroups; ++k) {
+                        const uint32_t w = key0 < sq.len ? reinterpret_cast<const uint32_t*>(first)[k] : 0u;
+                        if (key0 + lane >= sq.len) reinterpret_cast<uint32_t*>(first + lane * S::kPairBytes)[k] = w;
+                    }
+                    fence_proxy_async_smem();  // before TMA's next in this place
+                    __syncwarp();
+                }
                 // ---- scores of 32 keys x 8 NT rows: this thread's keys are 16 b + 8 j + g
                 float s[NT][2][4] = {};  // [row group][b][2 j + row]
 #pragma unroll
@@ -933,35 +931,6 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
                         }
                     }
                 }
-                uint32_t vw[2][2][kGroups];  // of V's keys
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        load_pairs<kGroups>(pairs + (S::kTile + slice + 16 * b + 8 * j + g) * S::kPairBytes, vw[b][j]);
-                const bool tail = key0 + kMmaKeys > sq.len;
-                const auto past = [&](uint32_t value) {  // what stands for the pairs past the sequence
-#pragma unroll
-                    for (int b = 0; b < 2; ++b)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-#pragma unroll
-                            for (int k = 0; k < kGroups; ++k)
-                                if (key0 + 16 * b + 8 * j + g >= sq.len) vw[b][j][k] = value;
-                };
-                // (what lies there may be anything, NaN included: NaN, which no maximum or minimum takes, and then zeros)
-                if (tail) past(0x7FFF7FFFu);
-                float v_max = 0.0f, v_least = INFINITY;
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int k = 0; k < kGroups; k += 2) {
-                            v_max = max3(v_max, pair_scale(vw[b][j][k]), pair_scale(vw[b][j][k + 1]));
-                            v_least = min3(v_least, pair_scale(vw[b][j][k]), pair_scale(vw[b][j][k + 1]));
-                        }
-                if (tail) past(0u);
                 if (key0 + kMmaKeys > all_seen) {
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
@@ -974,62 +943,89 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
                                     if (key0 + 16 * b + 8 * j + g >= seen[n][i]) s[n][b][2 * j + i] = -INFINITY;
                 }
 
-                // ---- running maxima.  They lag: a row's moves when one of its scores lies kMmaLag above it, which
-                // after the first keys is rare, so that the lanes need not tell one another their scores
-                bool grow = v_max * (0.5f * kUnit) >= v_unit && v_max > 0.0f;  // by a power of two or more
-                float mt[NT][2];  // of this thread's keys, not yet in units of log2
+                // ---- probabilities over the row's reference, which follows the largest of them times what the key's
+                // values may amount to.  It lags: it moves when that passes 2^15, which after the first keys is rare, so
+                // that the lanes need not tell one another their scores
+                uint32_t vw[2][2][kGroups];  // the pairs of V's keys 16 b + 8 j + g
+                float size[2][2];            // at or above the scales and lowest values, and 2^-65
+                float p[NT][2][4];
+                bool grow = false;
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        load_pairs<kGroups>(pairs + (S::kTile + slice + 16 * b + 8 * j + g) * S::kPairBytes, vw[b][j]);
+                        size[b][j] = 2.7e-20f;
+#pragma unroll
+                        for (int k = 0; k < kGroups; ++k)  // (the scale's bits under the lowest value's add little)
+                            size[b][j] = max3(size[b][j], fabsf(pair_scale(vw[b][j][k])),
+                                              fabsf(__uint_as_float(vw[b][j][k])));
+                    }
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        mt[n][i] = max3(fmaxf(s[n][0][i], s[n][0][2 + i]), s[n][1][i], s[n][1][2 + i]);
-                        grow = grow || mt[n][i] > lim[n][i];
+                        float most = 0.0f;
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                p[n][b][2 * j + i] = ex2(fmaf(s[n][b][2 * j + i], cr[n][i], nm[n][i]));
+                            most = max3(most, p[n][b][i] * size[b][0], p[n][b][2 + i] * size[b][1]);
+                        }
+                        grow = grow || most > 32768.0f;
                     }
                 if (__any_sync(0xffffffffu, grow)) {
+                    // (values that are not finite say nothing of the others of their key: those are looked at here)
 #pragma unroll
-                    for (int x = 4; x < 32; x <<= 1) {
+                    for (int b = 0; b < 2; ++b)
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
+                        for (int j = 0; j < 2; ++j) {
+                            float big = 2.7e-20f;
 #pragma unroll
-                            for (int i = 0; i < 2; ++i)
-                                mt[n][i] = fmaxf(mt[n][i], __shfl_xor_sync(0xffffffffu, mt[n][i], x));
-                        v_max = fmaxf(v_max, __shfl_xor_sync(0xffffffffu, v_max, x));
-                    }
-                    float fv = 1.0f;
-                    if (v_max * (0.5f * kUnit) >= v_unit && v_max > 0.0f) {
-                        const float v_new = pow2_of(v_max) * kUnit;
-                        fv = v_unit / v_new;
-                        v_unit = v_new;
-                        // (a power of two: its inverse has the exponent's mirror image)
-                        v_inv = __uint_as_float(0x7F000000u - __float_as_uint(v_unit));
-                    }
+                            for (int k = 0; k < kGroups; ++k) {
+                                const float x = fabsf(pair_scale(vw[b][j][k])), y = fabsf(__uint_as_float(vw[b][j][k]));
+                                if (x < INFINITY) big = fmaxf(big, x);
+                                if (y < INFINITY) big = fmaxf(big, y);
+                            }
+                            size[b][j] = log2f(big);
+                        }
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
+                            float to = -INFINITY;
+#pragma unroll
+                            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                                for (int j = 0; j < 2; ++j)
+                                    to = fmaxf(to, fmaf(s[n][b][2 * j + i], cr[n][i], size[b][j]));
+#pragma unroll
+                            for (int x = 4; x < 32; x <<= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, x));
                             float f = 1.0f;
-                            if (mt[n][i] > -INFINITY) {
-                                float to = kBias - mt[n][i] * cr[n][i];
-                                if (lim[n][i] > -INFINITY) {
+                            if (to > -INFINITY && to < INFINITY) {
+                                to = 15.0f - kMmaLag - to;
+                                if (nm[n][i] != kNoKey) {
                                     to = fminf(to, nm[n][i]);
                                     f = ex2(to - nm[n][i]);
                                 }
                                 nm[n][i] = to;
-                                lim[n][i] = (kBias + kMmaLag - to) / cr[n][i];
                             }
                             l[n][i] *= f;
 #pragma unroll
                             for (int k = 0; k < kGroups; ++k) low[n][k][i] *= f;
 #pragma unroll
                             for (int k = 0; k < kSteps; ++k) {
-                                o[n][k][i] *= f * fv;
-                                o[n][k][2 + i] *= f * fv;
+                                o[n][k][i] *= f;
+                                o[n][k][2 + i] *= f;
                             }
+#pragma unroll
+                            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                                for (int j = 0; j < 2; ++j)
+                                    p[n][b][2 * j + i] = ex2(fmaf(s[n][b][2 * j + i], cr[n][i], nm[n][i]));
                         }
                 }
-
-                // ---- probabilities; s becomes them over the scales' unit
-                float least = INFINITY;  // of it (a masked one's 0 is not looked at)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -1038,83 +1034,42 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
                         for (int b = 0; b < 2; ++b)
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
-                                const float p = ex2(fmaf(s[n][b][2 * j + i], cr[n][i], nm[n][i]));
-                                l[n][i] += p;
+                                const float x = p[n][b][2 * j + i];
+                                l[n][i] += x;
 #pragma unroll
                                 for (int k = 0; k < kGroups; ++k)
-                                    low[n][k][i] = fmaf(p, pair_low(vw[b][j][k]), low[n][k][i]);
-                                s[n][b][2 * j + i] = p * v_inv;
+                                    low[n][k][i] = fmaf(x, pair_low(vw[b][j][k]), low[n][k][i]);
                             }
-                if (key0 + kMmaKeys > all_seen) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int b = 0; b < 2; ++b)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (s[n][b][e] > 0.0f) least = fminf(least, s[n][b][e]);
-                } else {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            least = min3(least, s[n][b][0], s[n][b][1]);
-                            least = min3(least, s[n][b][2], s[n][b][3]);
-                        }
-                }
 
                 // ---- sums: dim x 8 NT rows += V^T (dim x 32) P^T (32 x 8 NT), group by group.  A b16 element is four
                 // dims: the transposed fragment holds dims 8 (g / 2) + g % 2 + 2 i of two keys in its nibbles i
                 const uint32_t vt = st + S::kTileBytes;
-                const auto add_codes = [&](auto as_bf16) {
-                    constexpr bool kAsBf16 = decltype(as_bf16)::value;
-                    constexpr float kTimes = kAsBf16 ? 1.0f / 16777216.0f : 1.0f;
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
-                        for (int k = 0; k < kGroups; k += 2) {
-                            uint32_t r[4];
-                            ldsm_x4_t((vt + 8 * b * DIM + code_base) ^ (kStep16 * b | k << 4), r);
+                    for (int k = 0; k < kGroups; k += 2) {
+                        uint32_t r[4];
+                        ldsm_x4_t((vt + 8 * b * DIM + code_base) ^ (kStep16 * b | k << 4), r);
 #pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const uint32_t u0 = r[2 * x], u1 = r[2 * x + 1];
-                                uint32_t pb[NT][2];
+                        for (int x = 0; x < 2; ++x) {
+                            uint32_t pb[NT][2];
 #pragma unroll
-                                for (int j = 0; j < 2; ++j) {
-                                    const float sc = pair_scale(vw[b][j][k + x]) * kTimes;
+                            for (int j = 0; j < 2; ++j) {
+                                const float sc = pair_scale(vw[b][j][k + x]);
 #pragma unroll
-                                    for (int n = 0; n < NT; ++n) {
-                                        const float y0 = s[n][b][2 * j] * sc, y1 = s[n][b][2 * j + 1] * sc;
-                                        pb[n][j] = transpose8(kAsBf16 ? pack_bf16x2(y0, y1) : pack_f16x2(y0, y1));
-                                    }
-                                }
+                                for (int n = 0; n < NT; ++n)
+                                    pb[n][j] = transpose8(pack_f16x2(p[n][b][2 * j] * sc, p[n][b][2 * j + 1] * sc));
+                            }
 #pragma unroll
-                                for (int y = 0; y < 2; ++y) {
-                                    uint32_t a0, a1, a2, a3;
-                                    if constexpr (kAsBf16) {
-                                        a0 = nibbles_bf16x2(u0 >> (8 * y), 1.0f), a1 = nibbles_bf16x2(u0 >> (8 * y + 4), 16.0f);
-                                        a2 = nibbles_bf16x2(u1 >> (8 * y), 1.0f), a3 = nibbles_bf16x2(u1 >> (8 * y + 4), 16.0f);
-                                    } else {
-                                        const uint32_t t0 = u0 >> (8 * y), t1 = u1 >> (8 * y);
-                                        a0 = t0 & 0x000F000Fu, a1 = t0 & 0x00F000F0u;
-                                        a2 = t1 & 0x000F000Fu, a3 = t1 & 0x00F000F0u;
-                                    }
+                            for (int y = 0; y < 2; ++y) {
+                                const uint32_t t0 = r[2 * x] >> (8 * y), t1 = r[2 * x + 1] >> (8 * y);
 #pragma unroll
-                                    for (int n = 0; n < NT; ++n) {
-                                        float (&d)[4] = o[n][2 * (k + x) + y];
-                                        if constexpr (kAsBf16) mma_bf16_16816(d, a0, a1, a2, a3, pb[n][0], pb[n][1]);
-                                        else mma_f16_16816(d, a0, a1, a2, a3, pb[n][0], pb[n][1]);
-                                    }
-                                }
+                                for (int n = 0; n < NT; ++n)
+                                    mma_f16_16816(o[n][2 * (k + x) + y], t0 & 0x000F000Fu, t0 & 0x00F000F0u,
+                                                  t1 & 0x000F000Fu, t1 & 0x00F000F0u, pb[n][0], pb[n][1]);
                             }
                         }
                     }
-                };
-                // some of it would lose bits in fp16
-                if (__builtin_expect(__any_sync(0xffffffffu, least * v_least < __uint_as_float(kFp16Normal)), 0))
-                    add_codes(std::true_type{});
-                else
-                    add_codes(std::false_type{});
             } else {
                 // ---- scores of 32 keys x 8 NT rows: this thread's keys are 16 b + 8 j + g
                 float s[NT][2][4] = {};  // [row group][b][2 j + row]
@@ -1352,8 +1307,8 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
             for (int i = 0; i < 2; ++i) {
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], x);
-                if constexpr (INT4) m[n][i] = lim[n][i] > -INFINITY ? -nm[n][i] : -INFINITY;
-                else m[n][i] -= kBias;
+                if constexpr (INT4) m[n][i] = nm[n][i] != kNoKey ? -nm[n][i] : -INFINITY;
+                else m[n][i] -= attn_bias<INT8>();
                 if (g == 0) {
                     sh.m[warp][8 * n + 2 * q4 + i] = m[n][i];
                     sh.l[warp][8 * n + 2 * q4 + i] = l[n][i];
@@ -1391,7 +1346,8 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
 #pragma unroll
                         for (int k = 0; k < kSteps; ++k) {
                             if constexpr (INT4) {
-                                const float unit = v_unit * 16777216.0f, lw = low[n][k / 2][i];
+                                constexpr float unit = 16777216.0f;
+                                const float lw = low[n][k / 2][i];
                                 const float x = f[n][i] == 0.0f ? 0.0f : fmaf(o[n][k][i], unit, lw) * f[n][i];
                                 const float y =
                                     f[n][i] == 0.0f ? 0.0f : fmaf(o[n][k][2 + i], unit * 0.0625f, lw) * f[n][i];
