@@ -946,20 +946,18 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
                 // ---- probabilities over the row's reference, which follows the largest of them times what the key's
                 // values may amount to.  It lags: it moves when that passes 2^15, which after the first keys is rare, so
                 // that the lanes need not tell one another their scores
-                uint32_t vw[2][2][kGroups];  // the pairs of V's keys 16 b + 8 j + g
-                float size[2][2];            // at or above the scales and lowest values, and 2^-65
+                const uint8_t* v_pairs = pairs + (S::kTile + slice + g) * S::kPairBytes;  // keys 16 b + 8 j + g from here on
+                float size[2][2];  // at or above scale and lowest value of this lane's group, and 2^-65
                 float p[NT][2][4];
                 bool grow = false;
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        load_pairs<kGroups>(pairs + (S::kTile + slice + 16 * b + 8 * j + g) * S::kPairBytes, vw[b][j]);
-                        size[b][j] = 2.7e-20f;
-#pragma unroll
-                        for (int k = 0; k < kGroups; ++k)  // (the scale's bits under the lowest value's add little)
-                            size[b][j] = max3(size[b][j], fabsf(pair_scale(vw[b][j][k])),
-                                              fabsf(__uint_as_float(vw[b][j][k])));
+                        const uint32_t w = *reinterpret_cast<const uint32_t*>(v_pairs + (16 * b + 8 * j) * S::kPairBytes +
+                                                                              4 * (q4 & (kGroups - 1)));
+                        // (the scale's bits under the lowest value's add little)
+                        size[b][j] = max3(2.7e-20f, fabsf(pair_scale(w)), fabsf(__uint_as_float(w)));
                     }
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -982,9 +980,11 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             float big = 2.7e-20f;
+                            uint32_t w[kGroups];
+                            load_pairs<kGroups>(v_pairs + (16 * b + 8 * j) * S::kPairBytes, w);
 #pragma unroll
                             for (int k = 0; k < kGroups; ++k) {
-                                const float x = fabsf(pair_scale(vw[b][j][k])), y = fabsf(__uint_as_float(vw[b][j][k]));
+                                const float x = fabsf(pair_scale(w[k])), y = fabsf(__uint_as_float(w[k]));
                                 if (x < INFINITY) big = fmaxf(big, x);
                                 if (y < INFINITY) big = fmaxf(big, y);
                             }
@@ -1026,26 +1026,25 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
                                     p[n][b][2 * j + i] = ex2(fmaf(s[n][b][2 * j + i], cr[n][i], nm[n][i]));
                         }
                 }
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int b = 0; b < 2; ++b)
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const float x = p[n][b][2 * j + i];
-                                l[n][i] += x;
-#pragma unroll
-                                for (int k = 0; k < kGroups; ++k)
-                                    low[n][k][i] = fmaf(x, pair_low(vw[b][j][k]), low[n][k][i]);
-                            }
-
                 // ---- sums: dim x 8 NT rows += V^T (dim x 32) P^T (32 x 8 NT), group by group.  A b16 element is four
                 // dims: the transposed fragment holds dims 8 (g / 2) + g % 2 + 2 i of two keys in its nibbles i
                 const uint32_t vt = st + S::kTileBytes;
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
+                for (int b = 0; b < 2; ++b) {
+                    uint32_t w[2][kGroups];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        load_pairs<kGroups>(v_pairs + (16 * b + 8 * j) * S::kPairBytes, w[j]);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                l[n][i] += p[n][b][2 * j + i];
+#pragma unroll
+                                for (int k = 0; k < kGroups; ++k)
+                                    low[n][k][i] = fmaf(p[n][b][2 * j + i], pair_low(w[j][k]), low[n][k][i]);
+                            }
+                    }
 #pragma unroll
                     for (int k = 0; k < kGroups; k += 2) {
                         uint32_t r[4];
@@ -1055,7 +1054,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
                             uint32_t pb[NT][2];
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
-                                const float sc = pair_scale(vw[b][j][k + x]);
+                                const float sc = pair_scale(w[j][k + x]);
 #pragma unroll
                                 for (int n = 0; n < NT; ++n)
                                     pb[n][j] = transpose8(pack_f16x2(p[n][b][2 * j] * sc, p[n][b][2 * j + 1] * sc));
@@ -1070,6 +1069,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
                             }
                         }
                     }
+                }
             } else {
                 // ---- scores of 32 keys x 8 NT rows: this thread's keys are 16 b + 8 j + g
                 float s[NT][2][4] = {};  // [row group][b][2 j + row]
