@@ -308,13 +308,61 @@ struct WholeWalk {
 
 // The whole block: adds up the tiles of all sequences (each thread those of
 // consecutive ones), finds the item of the block's first unit and notes down
-// what the join needs.  The block's segments.
-template <int TILE>
+// what the join needs.  The block's segments.  BY_WARP: up to 64 sequences of an
+// item each are added up by every warp for itself, two a lane (2 us of a call,
+// which is what a few loads one after another and two meetings of the block take).
+template <int TILE, bool BY_WARP>
 __device__ __forceinline__ MmaWalk<TILE> mma_deal(const AttnParams& p, MmaShared& sh)
 {
     const AttentionArgs& a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n_seq = static_cast<int>(a.n_seq);
+    const int n_kv = a.cache.n_kv, c = blockIdx.x;
+    // the walk from unit u on, which lies in the item of sequence `seq` at row0 with `before` units before it
+    const auto start = [&](int64_t units, int active, int seq, int row0, int64_t before) {
+        MmaWalk<TILE> walk(p, c < active ? attn_first(units, active, c) : 0,
+                           c < active ? attn_first(units, active, c + 1) : 0, seq, row0, before);
+        if (threadIdx.x == 0) {
+            AttnJoin j{};
+            if (c < active) {
+                const int64_t rel = walk.u - walk.before;
+                const int h = attn_div(rel, walk.s.tiles);
+                j = attn_join_of(units, active, c, walk.u, walk.before + static_cast<int64_t>(h) * walk.s.tiles,
+                                 walk.s.tiles, walk.s.sq, p.G, walk.s.row0, h);
+            }
+            p.joins[c] = j;
+        }
+        return walk;
+    };
+    if (BY_WARP && n_seq <= 64) {
+        int tiles[2] = {0, 0};
+        bool several = false;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (2 * lane + k < n_seq) {
+                const AttnSeq q = attn_seq(p, 2 * lane + k, c == 0 && warp == 0);
+                if (q.n_new > 0) tiles[k] = mma_tiles<TILE>(p, q, 0);
+                several = several || q.n_new * p.G > p.mb;
+            }
+        if (!__any_sync(0xffffffffu, several)) {
+            int x = tiles[0] + tiles[1];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            const int64_t units = static_cast<int64_t>(__shfl_sync(0xffffffffu, x, 31)) * n_kv;
+            const int active = attn_active(units, p.blocks);
+            const int64_t u = c < active ? attn_first(units, active, c) : 0;
+            const int first = x - tiles[0] - tiles[1];
+            const unsigned mine = __ballot_sync(0xffffffffu, u >= static_cast<int64_t>(first) * n_kv &&
+                                                                 u < static_cast<int64_t>(x) * n_kv);
+            const int at = mine ? __ffs(mine) - 1 : 0;
+            const int f = __shfl_sync(0xffffffffu, first, at), t0 = __shfl_sync(0xffffffffu, tiles[0], at);
+            const bool second = u >= static_cast<int64_t>(f + t0) * n_kv;
+            return start(units, active, 2 * at + second, 0, static_cast<int64_t>(second ? f + t0 : f) * n_kv);
+        }
+    }
     const int per = (n_seq + kMmaThreads - 1) / kMmaThreads;
     const int s0 = static_cast<int>(threadIdx.x) * per < n_seq ? threadIdx.x * per : n_seq;
     const int s1 = s0 + per < n_seq ? s0 + per : n_seq;
@@ -337,7 +385,6 @@ __device__ __forceinline__ MmaWalk<TILE> mma_deal(const AttnParams& p, MmaShared
         if (w < warp) at += sh.scan[w];
         total += sh.scan[w];
     }
-    const int n_kv = a.cache.n_kv;
     const int64_t units = total * n_kv;
     const int active = attn_active(units, p.blocks);
     if (static_cast<int>(blockIdx.x) < active) {
@@ -360,27 +407,14 @@ __device__ __forceinline__ MmaWalk<TILE> mma_deal(const AttnParams& p, MmaShared
         }
     }
     __syncthreads();
-    const int c = blockIdx.x;
-    MmaWalk<TILE> walk(p, c < active ? attn_first(units, active, c) : 0, c < active ? attn_first(units, active, c + 1) : 0,
-                 sh.seq, sh.row0, sh.before);
-    if (threadIdx.x == 0) {
-        AttnJoin j{};
-        if (c < active) {
-            const int64_t rel = walk.u - walk.before;
-            const int h = attn_div(rel, walk.s.tiles);
-            j = attn_join_of(units, active, c, walk.u, walk.before + static_cast<int64_t>(h) * walk.s.tiles,
-                             walk.s.tiles, walk.s.sq, p.G, walk.s.row0, h);
-        }
-        p.joins[c] = j;
-    }
-    return walk;
+    return start(units, active, sh.seq, sh.row0, sh.before);
 }
 
-template <bool WHOLE, int TILE>
+template <bool WHOLE, int TILE, bool BY_WARP>
 __device__ __forceinline__ auto mma_walk(const AttnParams& p, MmaShared& sh)
 {
     if constexpr (WHOLE) return WholeWalk<TILE>(p);
-    else return mma_deal<TILE>(p, sh);
+    else return mma_deal<TILE, BY_WARP>(p, sh);
 }
 
 __device__ __forceinline__ bool attn_wait(volatile int* abort_flag, uint64_t* bar, uint32_t parity, uint32_t* err)
@@ -589,6 +623,28 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
+// Brings what a call looks up before its first key (lengths, pages, queries) to
+// the L2 cache, a line a thread, while the kernel before still runs: where it has
+// to come from memory, one look-up waits for another 1 us each time.  (Nothing is
+// read: the L2 cache is where that kernel's writes arrive too.)
+template <int DIM>
+__device__ __forceinline__ void prefetch_lookups(const AttentionArgs& a)
+{
+    constexpr int kLine = 128;
+    int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    const auto take = [&](const void* base, int64_t bytes) {  // whether the thread's line was one of these
+        const int64_t lines = (bytes + kLine - 1) / kLine;
+        if (i < lines) asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(base) + i * kLine));
+        i -= lines;
+        return i < 0;
+    };
+    if (take(a.kv_len, a.n_seq * 4) || take(a.q_off, (a.n_seq + 1) * 4) || take(a.table, a.n_seq * a.max_pages * 4)) return;
+    const int64_t row = static_cast<int64_t>(a.n_q) * DIM * 2 / kLine, t = i / row;
+    if (t < a.T)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(a.q + t * a.q_stride) +
+                                                      (i - t * row) * kLine));
+}
+
 template <int DIM, int KIND, int NT, bool WHOLE>
 __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KIND != kBf16))
     attn_mma_kernel(const __grid_constant__ MmaParams mp)
@@ -630,12 +686,13 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
         sh.abort = 0;
         fence_mbarrier_init();
     }
+    if constexpr (INT4) prefetch_lookups<DIM>(a);
     if (WHOLE && p.whole > 1) cluster_sync_all();  // the others' barriers are there before anything is sent
     else __syncthreads();
     grid_dependency_wait();
 
     const int n_kv = cache.n_kv;
-    auto walk = mma_walk<WHOLE, S::kTile>(p, sh);
+    auto walk = mma_walk<WHOLE, S::kTile, INT4>(p, sh);
     const MmaSegment& sg = walk.s;
     int walk_rank = 0;
     if constexpr (WHOLE) walk_rank = walk.rank;

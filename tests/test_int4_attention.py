@@ -96,6 +96,19 @@ def test_attention_decode(dev, n_new, kv_len, n_q, n_kv, dim, page, offset):
     run_attention(dev, n_new, kv_len, n_q, n_kv, dim, page, seed=len(n_new), packed=len(n_new) % 2 == 1, offset=offset)
 
 
+@pytest.mark.parametrize("n_q,n_kv,dim,page", [(16, 2, 128, 16), (16, 1, 64, 32), (32, 2, 128, 64), (3, 3, 64, 128)])
+def test_attention_many_short_and_one_long(dev, n_q, n_kv, dim, page):
+    """Sequences of one tile, of two, and of none beside a long one, which makes the batch one that is dealt out: a
+    block's segments are shorter than its teams are many."""
+    lens = [(i * 97) % 300 for i in range(150)] + [5000] + [1, 0, 128, 129, 256, 257] * 5
+    for n_new in ([1] * len(lens), [1, 0, 2] * (len(lens) // 3)):
+        run_attention(dev, n_new + [1] * (len(lens) - len(n_new)), lens, n_q, n_kv, dim, page, seed=21)
+    small = [1, 5000, 64, 300]  # 64 sequences or fewer: another way to deal
+    for n_new in ([1, 1, 1, 1], [2, 1, 0, 1]):
+        run_attention(dev, n_new, small, n_q, n_kv, dim, page, seed=22)
+    run_attention(dev, [1] * 61, [5000] + [(i * 97) % 300 for i in range(60)], n_q, n_kv, dim, page, seed=23)
+
+
 CHUNK = [
     ([5], [5], 8, 2, 64, 16, True), ([6, 3, 1], [6, 300, 77], 8, 1, 128, 16, True),
     ([130], [130], 8, 8, 64, 32, True), ([65, 1, 200, 0], [65, 700, 333, 9], 16, 4, 128, 64, True),
