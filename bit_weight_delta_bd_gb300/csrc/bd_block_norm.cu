@@ -15,7 +15,10 @@
 // largest times the row's factor, so it comes with the second sum.
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "bd_device.cuh"
+#include "bd_tma.h"
 
 namespace bd {
 namespace {
@@ -23,7 +26,6 @@ namespace {
 constexpr int kOutBf16 = 0, kOutF32 = 1, kOutE4m3 = 2;
 constexpr int kMaxThreads = 1024;
 constexpr int kThreads = 512;
-constexpr int kWarpRows = 8;  // rows of a block where a row is a warp's
 
 struct BlockNormParams {
     BlockNormArgs a;
@@ -168,21 +170,44 @@ __device__ __forceinline__ void form_h(const BlockNormArgs& a, const Raw& w, con
     for (int e = 0; e < 8; ++e) h[e] = fmaf(a.block_scale, h[e], a.residual_scale * r[e]);
 }
 
+// 8 elements of h, from element `at` of the matrix on, and of the norm's output.
+template <int OUT>
+__device__ __forceinline__ void put_group(const BlockNormArgs& a, int64_t at, const uint16_t* gain, const float (&z)[8],
+                                          float mult, float code)
+{
+    if (!bd_in_range(kBkBlockNorm, at, 8, a.T * a.d)) return;
+    if (a.residual_out) store_bf16(a.residual_out + at, z);
+    float y[8];
+    unpack8(*reinterpret_cast<const uint4*>(gain), y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = z[e] * mult * y[e];
+    if constexpr (OUT == kOutBf16) {
+        store_bf16(static_cast<uint16_t*>(a.out) + at, y);
+    } else if constexpr (OUT == kOutF32) {
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
+        o[0] = make_float4(y[0], y[1], y[2], y[3]);
+        o[1] = make_float4(y[4], y[5], y[6], y[7]);
+    } else {
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + at) =
+            make_uint2(e4m3x4(y[0] * code, y[1] * code, y[2] * code, y[3] * code),
+                       e4m3x4(y[4] * code, y[5] * code, y[6] * code, y[7] * code));
+    }
+}
+
 // NG: groups of 8 elements that a thread keeps (0: the row is longer than the
 // block can keep, and h is formed again from its terms in each pass).
-template <int NG, int OUT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxThreads, WARP ? 2 : 1)
-    block_norm_kernel(const __grid_constant__ BlockNormParams p)
+template <int NG, int OUT>
+__global__ void __launch_bounds__(kMaxThreads, 1) block_norm_kernel(const __grid_constant__ BlockNormParams p)
 {
     // the first sum's, and the second's by turns: a warp may still read the last row's
     __shared__ float2 red[3][32];
     const BlockNormArgs& a = p.a;
     const int64_t groups = a.d / 8;
-    const int first = WARP ? threadIdx.x & 31 : threadIdx.x, step = WARP ? 32 : blockDim.x;
-    const int64_t rows_step = static_cast<int64_t>(gridDim.x) * (WARP ? kWarpRows : 1);
-    int64_t t = WARP ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+    const int first = threadIdx.x, step = blockDim.x;
+    const int64_t rows_step = gridDim.x;
+    int64_t t = blockIdx.x;
     constexpr int kKeep = NG > 0 ? NG : 1;
-    constexpr bool kAhead = !WARP && NG > 0 && NG <= 2;  // the next row is loaded early (with four groups, registers are short)
+    constexpr bool kAhead = NG > 0 && NG <= 2;  // the next row is loaded early (with four groups, registers are short)
     Raw raw[kKeep];
     Rows rows{}, next{};
     const auto load_row = [&](int64_t r, Rows& w) {
@@ -215,7 +240,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxThreads, WARP ? 2 
                     if (bd_in_range(kBkBlockNorm, row + 8 * g, 8, a.T * a.d))
                         ss = add_squares(ss, *reinterpret_cast<const uint4*>(a.x + row + 8 * g));
             }
-            rstd = rsqrtf(row_reduce<WARP, false>(ss, 0.0f, red[0]).x / static_cast<float>(a.d) + a.eps);
+            rstd = rsqrtf(row_reduce<false, false>(ss, 0.0f, red[0]).x / static_cast<float>(a.d) + a.eps);
         }
 
         // ---- h, the sum of its squares, and the largest |h gain|
@@ -251,7 +276,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxThreads, WARP ? 2 
                 add_up(g, h[0]);
             }
         }
-        const float2 both = row_reduce<WARP, OUT == kOutE4m3>(ss, amax, red[1 + turn]);
+        const float2 both = row_reduce<false, OUT == kOutE4m3>(ss, amax, red[1 + turn]);
         const float mult = rsqrtf(both.x / static_cast<float>(a.d) + a.eps);
         float code = 1.0f;
         if constexpr (OUT == kOutE4m3) {
@@ -262,24 +287,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxThreads, WARP ? 2 
 
         // ---- out
         const auto put = [&](int64_t g, const float (&z)[8]) {
-            const int64_t at = row + 8 * g;
-            if (!bd_in_range(kBkBlockNorm, at, 8, a.T * a.d)) return;
-            if (a.residual_out) store_bf16(a.residual_out + at, z);
-            float y[8];
-            unpack8(*reinterpret_cast<const uint4*>(rows.gain + 8 * g), y);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = z[e] * mult * y[e];
-            if constexpr (OUT == kOutBf16) {
-                store_bf16(static_cast<uint16_t*>(a.out) + at, y);
-            } else if constexpr (OUT == kOutF32) {
-                float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
-                o[0] = make_float4(y[0], y[1], y[2], y[3]);
-                o[1] = make_float4(y[4], y[5], y[6], y[7]);
-            } else {
-                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + at) =
-                    make_uint2(e4m3x4(y[0] * code, y[1] * code, y[2] * code, y[3] * code),
-                               e4m3x4(y[4] * code, y[5] * code, y[6] * code, y[7] * code));
-            }
+            put_group<OUT>(a, row + 8 * g, rows.gain + 8 * g, z, mult, code);
         };
         if constexpr (NG > 0) {
 #pragma unroll
@@ -299,20 +307,279 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxThreads, WARP ? 2 
     }
 }
 
-template <int NG, bool WARP>
+// Two fp32 values in one 64-bit register, and their packed arithmetic.
+__device__ __forceinline__ uint64_t f32x2(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// a pair of bf16
+__device__ __forceinline__ uint64_t pair(uint32_t w)
+{
+    return f32x2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// Many rows: x, r and gates of a token's own come as bulk copies into a ring in
+// shared memory, a few rows ahead of the one that is worked on, so that neither
+// the meetings nor the registers say how much is on its way.  A row is a block's,
+// or of up to 128 groups a warp's, with a ring of its own and no meeting; a stage
+// is free again when the sum of the row's h^2 is there, which all have put their
+// parts into.  What is kept of a row from there on is h gain.
+constexpr int kRingMaxStages = 8;
+constexpr int kRingWarps = 8;  // rows of a block where a row is a warp's
+
+// Blocks of an SM that the registers allow for, of up to `block` threads.
+constexpr int ring_blocks(int ng, int block, bool warp) { return warp ? 6 - ng : 1024 / block; }
+
+struct RingParams {
+    BlockNormArgs a;
+    int stages, row_bytes;  // of a row's ring; bytes of a row of x
+};
+
+template <int NG, int OUT, int BLOCK, bool WARP>
+__global__ void __launch_bounds__(BLOCK, ring_blocks(NG, BLOCK, WARP)) block_norm_ring_kernel(const __grid_constant__ RingParams p)
+{
+    constexpr int kRows = WARP ? kRingWarps : 1;  // of the block at a time
+    extern __shared__ __align__(128) uint8_t ring_all[];
+    __shared__ float2 red[3][32];
+    __shared__ uint64_t full_all[kRows][kRingMaxStages];
+    __shared__ int given_up;
+    const BlockNormArgs& a = p.a;
+    const int which = WARP ? threadIdx.x >> 5 : 0;
+    const int first = WARP ? threadIdx.x & 31 : threadIdx.x, step = WARP ? 32 : blockDim.x;
+    const int groups = static_cast<int>(a.d / 8);
+    const bool own_gates = a.gate && a.gate_rows > 1;
+    const int stage_bytes = p.row_bytes * (own_gates ? 3 : 2);
+    uint8_t* const ring = ring_all + static_cast<size_t>(which) * p.stages * stage_bytes;
+    uint64_t* const full = full_all[which];
+    const int64_t rows_step = static_cast<int64_t>(gridDim.x) * kRows;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows + which;
+
+    grid_launch_dependents();
+    if (first == 0) {
+        for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
+        if (which == 0) given_up = 0;
+        fence_mbarrier_init();
+    }
+    __syncthreads();
+    grid_dependency_wait();
+
+    // the row of a gate that token t takes
+    const auto gate_row = [&](int64_t t) {
+        if (t >= a.T) return static_cast<int64_t>(0);
+        int64_t i = a.gate_idx ? a.gate_idx[t] : t;
+        if (i < 0 || i >= a.gate_rows) {
+            raise_error(a.err, kErrBadIndex);
+            i = 0;
+        }
+        return i;
+    };
+    // by the row's first thread: row t into stage s
+    const auto fill = [&](int64_t t, int s, int64_t gate_at) {
+        if (t >= a.T) return;
+        uint8_t* dst = ring + static_cast<size_t>(s) * stage_bytes;
+        mbar_arrive_expect_tx(&full[s], stage_bytes);
+        bulk_g2s(dst, a.x + t * a.d, p.row_bytes, &full[s]);
+        bulk_g2s(dst + p.row_bytes, a.residual + t * a.d, p.row_bytes, &full[s]);
+        if (own_gates) bulk_g2s(dst + 2 * p.row_bytes, a.gate + gate_at * a.d, p.row_bytes, &full[s]);
+    };
+    int64_t gate_next = 0;  // of the row that the next refill brings
+    if (first == 0) {
+        for (int s = 0; s < p.stages; ++s) fill(t0 + s * rows_step, s, own_gates ? gate_row(t0 + s * rows_step) : 0);
+        if (own_gates) gate_next = gate_row(t0 + p.stages * rows_step);
+    }
+    int vid_next = a.vid && t0 < a.T ? a.vid[t0] : -1;
+    int stage = 0, turn = 0;
+    uint32_t phase = 0;
+    for (int64_t t = t0; t < a.T; t += rows_step, turn ^= 1) {
+        const uint16_t *post = a.post_gain, *gain = a.gain;
+        if (a.vid) {
+            const int v = vid_next;
+            if (v >= 0 && v < a.V) {
+                gain = a.gains[v];
+                if (post) post = a.post_gains[v];
+            } else if (v != -1 && first == 0) {
+                raise_error(a.err, kErrBadVariant);
+            }
+            if (t + rows_step < a.T) vid_next = a.vid[t + rows_step];
+        }
+        if (first == 0 && a.gate_idx && !own_gates && a.gate_idx[t] != 0) raise_error(a.err, kErrBadIndex);
+        uint4 pg[NG];  // the gain of the norm after the block, on its way while the sum is formed
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+            pg[i] = make_uint4(0, 0, 0, 0);
+            if (post && first + i * step < groups) pg[i] = *(reinterpret_cast<const uint4*>(post) + first + i * step);
+        }
+        // (given up, which is reported: what is there is worked on)
+        if (!mbar_try_wait(&full[stage], phase) && !given_up && !mbar_wait_sleeping(&full[stage], phase)) {
+            given_up = 1;
+            raise_error(a.err, kErrTimeout);
+        }
+        const uint4* xs = reinterpret_cast<const uint4*>(ring + static_cast<size_t>(stage) * stage_bytes);
+        const uint4* rs = xs + groups;
+        const uint4* gs = own_gates ? rs + groups : reinterpret_cast<const uint4*>(a.gate);
+        uint4 x[NG];
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (first + i * step < groups) x[i] = xs[first + i * step];
+        }
+        float c = a.block_scale;
+        if (post) {
+            uint64_t ss = 0;  // a pair of zeros
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint64_t f = pair(w[e]);
+                    ss = fma2(f, f, ss);
+                }
+            }
+            const float2 s = unpack2(ss);
+            const float sum = row_reduce<WARP, false>(s.x + s.y, 0.0f, red[0]).x;
+            c *= rsqrtf(sum / static_cast<float>(a.d) + a.eps);
+        }
+        const uint64_t c2 = f32x2(c, c), rs2 = f32x2(a.residual_scale, a.residual_scale);
+        uint64_t ss = 0, z[NG][4];  // h gain
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+            const int g = first + i * step;
+            if (g >= groups) continue;
+            const uint4 r = rs[g], wg = *(reinterpret_cast<const uint4*>(gain) + g);
+            uint4 gate = make_uint4(0, 0, 0, 0);
+            if (a.gate) gate = gs[g];
+            const uint32_t xw[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, rw[4] = {r.x, r.y, r.z, r.w};
+            const uint32_t pw[4] = {pg[i].x, pg[i].y, pg[i].z, pg[i].w}, gw[4] = {gate.x, gate.y, gate.z, gate.w};
+            const uint32_t ww[4] = {wg.x, wg.y, wg.z, wg.w};
+            uint32_t hw[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint64_t n = mul2(pair(xw[e]), c2);
+                if (post) n = mul2(n, pair(pw[e]));
+                const uint64_t rr = mul2(pair(rw[e]), rs2);
+                // (a gate multiplies, and joins the residual, in one rounding)
+                const uint64_t h = a.gate ? fma2(n, pair(gw[e]), rr) : fma2(n, f32x2(1.0f, 1.0f), rr);
+                ss = fma2(h, h, ss);
+                z[i][e] = mul2(h, pair(ww[e]));
+                const float2 hf = unpack2(h);
+                hw[e] = f32_bf16x2(hf.x, hf.y);
+                if constexpr (OUT == kOutE4m3) {
+                    const float2 zf = unpack2(z[i][e]);
+                    amax = max_nan(amax, max_nan(fabsf(zf.x), fabsf(zf.y)));
+                }
+            }
+            if (a.residual_out && bd_in_range(kBkBlockNorm, t * a.d + 8 * g, 8, a.T * a.d))
+                *reinterpret_cast<uint4*>(a.residual_out + t * a.d + 8 * g) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+        }
+        const float2 s = unpack2(ss);
+        const float2 both = row_reduce<WARP, OUT == kOutE4m3>(s.x + s.y, amax, red[1 + turn]);
+        if (first == 0) {  // all threads have read their part of the row
+            fill(t + p.stages * rows_step, stage, gate_next);
+            if (own_gates) gate_next = gate_row(t + (p.stages + 1) * rows_step);
+        }
+        float mult = rsqrtf(both.x / static_cast<float>(a.d) + a.eps);
+        if constexpr (OUT == kOutE4m3) {
+            amax = max_nan(both.y * mult, 1e-30f);
+            if (first == 0) a.scale[t] = amax / 448.0f;
+        }
+        const uint64_t m2 = f32x2(mult, mult);
+        const float code = OUT == kOutE4m3 ? 448.0f / amax : 1.0f;
+        [[maybe_unused]] const uint64_t k2 = f32x2(code, code);
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+            const int g = first + i * step;
+            if (g >= groups) continue;
+            const int64_t at = t * a.d + 8 * g;
+            if (!bd_in_range(kBkBlockNorm, at, 8, a.T * a.d)) continue;
+            float2 y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint64_t v = mul2(z[i][e], m2);
+                if constexpr (OUT == kOutE4m3) v = mul2(v, k2);
+                y[e] = unpack2(v);
+            }
+            if constexpr (OUT == kOutBf16) {
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at) =
+                    make_uint4(f32_bf16x2(y[0].x, y[0].y), f32_bf16x2(y[1].x, y[1].y), f32_bf16x2(y[2].x, y[2].y),
+                               f32_bf16x2(y[3].x, y[3].y));
+            } else if constexpr (OUT == kOutF32) {
+                float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
+                o[0] = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
+                o[1] = make_float4(y[2].x, y[2].y, y[3].x, y[3].y);
+            } else {
+                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + at) = make_uint2(
+                    e4m3x4(y[0].x, y[0].y, y[1].x, y[1].y), e4m3x4(y[2].x, y[2].y, y[3].x, y[3].y));
+            }
+        }
+        if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+    // given up: leave only when the copies in flight have landed
+    if (given_up && first < p.stages) mbar_wait_bounded(&full[first], first < stage ? phase : phase ^ 1);
+}
+
+template <int NG, int BLOCK, bool WARP>
+cudaError_t launch_ring(const BlockNormArgs& a, int threads, int sm_count, cudaStream_t stream)
+{
+    static std::atomic<size_t> smem_set[3][kHostMaxDevices];
+    RingParams p{a, 0, static_cast<int>(a.d) * 2};
+    // blocks of an SM: by its threads, and by the registers of a block that may have up to BLOCK of them
+    const int by_registers = ring_blocks(NG, BLOCK, WARP) * (BLOCK / threads);
+    const int per_sm = 2048 / threads < by_registers ? 2048 / threads : by_registers;
+    const int rows = WARP ? kRingWarps : 1;
+    const size_t stage = static_cast<size_t>(p.row_bytes) * (a.gate && a.gate_rows > 1 ? 3 : 2) * rows;
+    const size_t room = (228u * 1024u) / per_sm - 3072u;
+    p.stages = static_cast<int>(room / stage);
+    if (p.stages > kRingMaxStages) p.stages = kRingMaxStages;
+    if (p.stages < 2) return cudaErrorInvalidConfiguration;  // (rows that long do not come here)
+    const size_t smem = stage * p.stages;
+    const int64_t blocks = (a.T + rows - 1) / rows, resident = static_cast<int64_t>(sm_count) * per_sm;
+    const dim3 grid(static_cast<unsigned>(blocks < resident ? blocks : resident));
+    const auto go = [&](auto kernel, std::atomic<size_t>* set) {
+        cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem, set);
+        launch_dep(err, kernel, grid, dim3(threads), smem, stream, p);
+        return err;
+    };
+    if (a.out_dtype == kOutBf16) return go(block_norm_ring_kernel<NG, kOutBf16, BLOCK, WARP>, smem_set[0]);
+    if (a.out_dtype == kOutF32) return go(block_norm_ring_kernel<NG, kOutF32, BLOCK, WARP>, smem_set[1]);
+    return go(block_norm_ring_kernel<NG, kOutE4m3, BLOCK, WARP>, smem_set[2]);
+}
+
+template <int NG>
 cudaError_t launch_groups(const BlockNormParams& p, int threads, int sm_count, cudaStream_t stream)
 {
     cudaError_t err = cudaSuccess;
-    // 2048 threads for each SM; rows that are a warp's, all at once
-    const int64_t blocks = WARP ? (p.a.T + kWarpRows - 1) / kWarpRows : p.a.T;
-    const int64_t resident = WARP ? blocks : static_cast<int64_t>(sm_count) * (2048 / threads);
-    const dim3 grid(static_cast<unsigned>(blocks < resident ? blocks : resident));
+    const int64_t resident = static_cast<int64_t>(sm_count) * (2048 / threads);  // 2048 threads for each SM
+    const dim3 grid(static_cast<unsigned>(p.a.T < resident ? p.a.T : resident));
     if (p.a.out_dtype == kOutBf16)
-        launch_dep(err, block_norm_kernel<NG, kOutBf16, WARP>, grid, dim3(threads), 0, stream, p);
+        launch_dep(err, block_norm_kernel<NG, kOutBf16>, grid, dim3(threads), 0, stream, p);
     else if (p.a.out_dtype == kOutF32)
-        launch_dep(err, block_norm_kernel<NG, kOutF32, WARP>, grid, dim3(threads), 0, stream, p);
+        launch_dep(err, block_norm_kernel<NG, kOutF32>, grid, dim3(threads), 0, stream, p);
     else
-        launch_dep(err, block_norm_kernel<NG, kOutE4m3, WARP>, grid, dim3(threads), 0, stream, p);
+        launch_dep(err, block_norm_kernel<NG, kOutE4m3>, grid, dim3(threads), 0, stream, p);
     return err;
 }
 
@@ -330,12 +597,15 @@ cudaError_t launch_block_norm(const BlockNormArgs& a, int sm_count, cudaStream_t
     // Few rows: as many threads on a row as it has groups, for its latency.
     // Many: a warp for short rows, else two groups a thread.
     const bool few = a.T <= 2 * sm_count;
-    if (!few && groups <= 32) return launch_groups<1, true>(p, 32 * kWarpRows, sm_count, stream);
-    if (!few && groups <= 64) return launch_groups<2, true>(p, 32 * kWarpRows, sm_count, stream);
-    if (groups <= (few ? kMaxThreads : kThreads)) return launch_groups<1, false>(p, threads_for(1), sm_count, stream);
-    if (groups <= 2 * kMaxThreads) return launch_groups<2, false>(p, threads_for(2), sm_count, stream);
-    if (groups <= 4 * kMaxThreads) return launch_groups<4, false>(p, threads_for(4), sm_count, stream);
-    return launch_groups<0, false>(p, kMaxThreads, sm_count, stream);
+    if (!few && groups <= 32) return launch_ring<1, 32 * kRingWarps, true>(a, 32 * kRingWarps, sm_count, stream);
+    if (!few && groups <= 64) return launch_ring<2, 32 * kRingWarps, true>(a, 32 * kRingWarps, sm_count, stream);
+    if (!few && groups <= 128) return launch_ring<4, 32 * kRingWarps, true>(a, 32 * kRingWarps, sm_count, stream);
+    if (!few && groups <= 1024) return launch_ring<2, 512, false>(a, threads_for(2), sm_count, stream);
+    if (!few && groups <= 2048) return launch_ring<2, 1024, false>(a, threads_for(2), sm_count, stream);
+    if (groups <= (few ? kMaxThreads : kThreads)) return launch_groups<1>(p, threads_for(1), sm_count, stream);
+    if (groups <= 2 * kMaxThreads) return launch_groups<2>(p, threads_for(2), sm_count, stream);
+    if (groups <= 4 * kMaxThreads) return launch_groups<4>(p, threads_for(4), sm_count, stream);
+    return launch_groups<0>(p, kMaxThreads, sm_count, stream);
 }
 
 BD_BOUNDS_TAKE(bounds_take_block_norm)
