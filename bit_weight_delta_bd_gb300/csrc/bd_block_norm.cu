@@ -343,12 +343,43 @@ __device__ __forceinline__ uint64_t pair(uint32_t w)
 // the meetings nor the registers say how much is on its way.  A row is a block's,
 // or of up to 128 groups a warp's, with a ring of its own and no meeting; a stage
 // is free again when the sum of the row's h^2 is there, which all have put their
-// parts into.  What is kept of a row from there on is h gain.
+// parts into.  What is kept of a row from there on is h gain.  With three stages
+// or more the sum of the next row's x^2 is formed in the same meeting, one for each
+// row; with two the next row would have to be there before the one after it is
+// asked for (4096 x 8192 gated e4m3: 59.5 us with one meeting, 57.5 with two; bf16
+// with one gate and three stages 51.7 and 54.0).
 constexpr int kRingMaxStages = 8;
 constexpr int kRingWarps = 8;  // rows of a block where a row is a warp's
 
 // Blocks of an SM that the registers allow for, of up to `block` threads.
 constexpr int ring_blocks(int ng, int block, bool warp) { return warp ? 6 - ng : 1024 / block; }
+
+// Sums of a and b, and the largest m, over the row's threads.  (m is the bits of a
+// magnitude, whose order is that of the numbers, with NaN above all.)
+template <bool WARP, bool MAX>
+__device__ __forceinline__ float3 ring_reduce(float a, float b, uint32_t m, float4* red)
+{
+    const auto warp_reduce = [&]() {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            a += __shfl_xor_sync(0xffffffffu, a, o);
+            b += __shfl_xor_sync(0xffffffffu, b, o);
+        }
+        if constexpr (MAX) m = __reduce_max_sync(0xffffffffu, m);
+    };
+    warp_reduce();
+    if constexpr (!WARP) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+        if (lane == 0) red[warp] = make_float4(a, b, __uint_as_float(m), 0.0f);
+        __syncthreads();
+        const float4 v = lane < warps ? red[lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        a = v.x;
+        b = v.y;
+        m = __float_as_uint(v.z);
+        warp_reduce();
+    }
+    return make_float3(a, b, __uint_as_float(m));
+}
 
 struct RingParams {
     BlockNormArgs a;
@@ -360,7 +391,8 @@ __global__ void __launch_bounds__(BLOCK, ring_blocks(NG, BLOCK, WARP)) block_nor
 {
     constexpr int kRows = WARP ? kRingWarps : 1;  // of the block at a time
     extern __shared__ __align__(128) uint8_t ring_all[];
-    __shared__ float2 red[3][32];
+    // by turns: a warp may still read the last row's; and the one of a meeting that the other lies between
+    __shared__ float4 red[3][32];
     __shared__ uint64_t full_all[kRows][kRingMaxStages];
     __shared__ int given_up;
     const BlockNormArgs& a = p.a;
@@ -410,6 +442,33 @@ __global__ void __launch_bounds__(BLOCK, ring_blocks(NG, BLOCK, WARP)) block_nor
     int vid_next = a.vid && t0 < a.T ? a.vid[t0] : -1;
     int stage = 0, turn = 0;
     uint32_t phase = 0;
+    // waits for row t, and returns this thread's part of the sum of its x^2
+    const auto squares = [&](int s, uint32_t ph) {
+        // (given up, which is reported: what is there is worked on)
+        if (!mbar_try_wait(&full[s], ph) && !given_up && !mbar_wait_sleeping(&full[s], ph)) {
+            given_up = 1;
+            raise_error(a.err, kErrTimeout);
+        }
+        if (!a.post_gain) return 0.0f;
+        const uint4* xs = reinterpret_cast<const uint4*>(ring + static_cast<size_t>(s) * stage_bytes);
+        uint64_t ss = 0;  // a pair of zeros
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+            if (first + i * step >= groups) continue;
+            const uint4 x = xs[first + i * step];
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint64_t f = pair(w[e]);
+                ss = fma2(f, f, ss);
+            }
+        }
+        const float2 s2 = unpack2(ss);
+        return s2.x + s2.y;
+    };
+    const bool ahead = p.stages >= 3;
+    float x_sum = 0.0f;
+    if (ahead && t0 < a.T) x_sum = ring_reduce<WARP, false>(0.0f, squares(0, 0), 0u, red[1]).y;
     for (int64_t t = t0; t < a.T; t += rows_step, turn ^= 1) {
         const uint16_t *post = a.post_gain, *gain = a.gain;
         if (a.vid) {
@@ -423,54 +482,34 @@ __global__ void __launch_bounds__(BLOCK, ring_blocks(NG, BLOCK, WARP)) block_nor
             if (t + rows_step < a.T) vid_next = a.vid[t + rows_step];
         }
         if (first == 0 && a.gate_idx && !own_gates && a.gate_idx[t] != 0) raise_error(a.err, kErrBadIndex);
-        uint4 pg[NG];  // the gain of the norm after the block, on its way while the sum is formed
-#pragma unroll
-        for (int i = 0; i < NG; ++i) {
-            pg[i] = make_uint4(0, 0, 0, 0);
-            if (post && first + i * step < groups) pg[i] = *(reinterpret_cast<const uint4*>(post) + first + i * step);
-        }
-        // (given up, which is reported: what is there is worked on)
-        if (!mbar_try_wait(&full[stage], phase) && !given_up && !mbar_wait_sleeping(&full[stage], phase)) {
-            given_up = 1;
-            raise_error(a.err, kErrTimeout);
-        }
         const uint4* xs = reinterpret_cast<const uint4*>(ring + static_cast<size_t>(stage) * stage_bytes);
         const uint4* rs = xs + groups;
         const uint4* gs = own_gates ? rs + groups : reinterpret_cast<const uint4*>(a.gate);
-        uint4 x[NG];
+        uint4 post_gain[NG];  // on its way while the row is waited for
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-            x[i] = make_uint4(0, 0, 0, 0);
-            if (first + i * step < groups) x[i] = xs[first + i * step];
+            post_gain[i] = make_uint4(0, 0, 0, 0);
+            if (post && first + i * step < groups)
+                post_gain[i] = *(reinterpret_cast<const uint4*>(post) + first + i * step);
         }
-        float c = a.block_scale;
-        if (post) {
-            uint64_t ss = 0;  // a pair of zeros
-#pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint64_t f = pair(w[e]);
-                    ss = fma2(f, f, ss);
-                }
-            }
-            const float2 s = unpack2(ss);
-            const float sum = row_reduce<WARP, false>(s.x + s.y, 0.0f, red[0]).x;
-            c *= rsqrtf(sum / static_cast<float>(a.d) + a.eps);
+        if (!ahead) {
+            x_sum = squares(stage, phase);
+            if (post) x_sum = ring_reduce<WARP, false>(0.0f, x_sum, 0u, red[2]).y;
         }
+        const float c = post ? a.block_scale * rsqrtf(x_sum / static_cast<float>(a.d) + a.eps) : a.block_scale;
         const uint64_t c2 = f32x2(c, c), rs2 = f32x2(a.residual_scale, a.residual_scale);
         uint64_t ss = 0, z[NG][4];  // h gain
-        float amax = 0.0f;
+        uint32_t most = 0;  // the bits of the largest |h gain|
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
             const int g = first + i * step;
             if (g >= groups) continue;
-            const uint4 r = rs[g], wg = *(reinterpret_cast<const uint4*>(gain) + g);
+            const uint4 x = xs[g], r = rs[g], wg = *(reinterpret_cast<const uint4*>(gain) + g);
+            const uint4 pg = post_gain[i];
             uint4 gate = make_uint4(0, 0, 0, 0);
             if (a.gate) gate = gs[g];
-            const uint32_t xw[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, rw[4] = {r.x, r.y, r.z, r.w};
-            const uint32_t pw[4] = {pg[i].x, pg[i].y, pg[i].z, pg[i].w}, gw[4] = {gate.x, gate.y, gate.z, gate.w};
+            const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, rw[4] = {r.x, r.y, r.z, r.w};
+            const uint32_t pw[4] = {pg.x, pg.y, pg.z, pg.w}, gw[4] = {gate.x, gate.y, gate.z, gate.w};
             const uint32_t ww[4] = {wg.x, wg.y, wg.z, wg.w};
             uint32_t hw[4];
 #pragma unroll
@@ -486,21 +525,25 @@ __global__ void __launch_bounds__(BLOCK, ring_blocks(NG, BLOCK, WARP)) block_nor
                 hw[e] = f32_bf16x2(hf.x, hf.y);
                 if constexpr (OUT == kOutE4m3) {
                     const float2 zf = unpack2(z[i][e]);
-                    amax = max_nan(amax, max_nan(fabsf(zf.x), fabsf(zf.y)));
+                    most = max(most, max(__float_as_uint(fabsf(zf.x)), __float_as_uint(fabsf(zf.y))));
                 }
             }
             if (a.residual_out && bd_in_range(kBkBlockNorm, t * a.d + 8 * g, 8, a.T * a.d))
                 *reinterpret_cast<uint4*>(a.residual_out + t * a.d + 8 * g) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
         }
         const float2 s = unpack2(ss);
-        const float2 both = row_reduce<WARP, OUT == kOutE4m3>(s.x + s.y, amax, red[1 + turn]);
+        const int following = stage + 1 == p.stages ? 0 : stage + 1;
+        const float x_part = ahead && t + rows_step < a.T ? squares(following, following ? phase : phase ^ 1) : 0.0f;
+        const float3 both = ring_reduce<WARP, OUT == kOutE4m3>(s.x + s.y, x_part, most, red[turn]);
+        x_sum = both.y;
         if (first == 0) {  // all threads have read their part of the row
             fill(t + p.stages * rows_step, stage, gate_next);
             if (own_gates) gate_next = gate_row(t + (p.stages + 1) * rows_step);
         }
-        float mult = rsqrtf(both.x / static_cast<float>(a.d) + a.eps);
+        const float mult = rsqrtf(both.x / static_cast<float>(a.d) + a.eps);
+        [[maybe_unused]] float amax = 0.0f;
         if constexpr (OUT == kOutE4m3) {
-            amax = max_nan(both.y * mult, 1e-30f);
+            amax = max_nan(both.z * mult, 1e-30f);
             if (first == 0) a.scale[t] = amax / 448.0f;
         }
         const uint64_t m2 = f32x2(mult, mult);
@@ -524,9 +567,17 @@ __global__ void __launch_bounds__(BLOCK, ring_blocks(NG, BLOCK, WARP)) block_nor
                     make_uint4(f32_bf16x2(y[0].x, y[0].y), f32_bf16x2(y[1].x, y[1].y), f32_bf16x2(y[2].x, y[2].y),
                                f32_bf16x2(y[3].x, y[3].y));
             } else if constexpr (OUT == kOutF32) {
-                float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
-                o[0] = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
-                o[1] = make_float4(y[2].x, y[2].y, y[3].x, y[3].y);
+                float* o = static_cast<float*>(a.out) + at;
+                const uint4 lo = make_uint4(__float_as_uint(y[0].x), __float_as_uint(y[0].y), __float_as_uint(y[1].x),
+                                            __float_as_uint(y[1].y));
+                const uint4 hi = make_uint4(__float_as_uint(y[2].x), __float_as_uint(y[2].y), __float_as_uint(y[3].x),
+                                            __float_as_uint(y[3].y));
+                if (on_sector(a.out)) {
+                    store_32(o, lo, hi);
+                } else {
+                    reinterpret_cast<uint4*>(o)[0] = lo;
+                    reinterpret_cast<uint4*>(o)[1] = hi;
+                }
             } else {
                 *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + at) = make_uint2(
                     e4m3x4(y[0].x, y[0].y, y[1].x, y[1].y), e4m3x4(y[2].x, y[2].y, y[3].x, y[3].y));
