@@ -22,7 +22,7 @@ namespace {
 constexpr int kBf16 = 0, kInt8 = 1, kInt4 = 2;  // what the cache holds
 int kind_of(const KvPages& c) { return c.int4 ? kInt4 : c.int8 ? kInt8 : kBf16; }
 
-constexpr int rope_threads(int kind) { return kind == kBf16 ? 32 : 64; }  // of a block at most
+constexpr int rope_threads(int kind) { return kind == kInt8 ? 64 : 32; }  // of a block at most
 constexpr int kUnit = 16;  // elements of a head that one thread handles
 
 __device__ __forceinline__ void unpack8(uint4 u, float* f)
@@ -73,19 +73,31 @@ __device__ __forceinline__ float min_nan(float a, float b)
     return r;
 }
 
+// a / b rounded to nearest, where inverse is 1 / b so rounded: with q = a inverse,
+// which is off by an ulp at most, the remainder a - b q is exact, and q +
+// remainder * inverse rounds to the quotient (Markstein, IBM J. Res. Dev. 34,
+// 1990).  For a / b in 2^-20 .. 2^20 and normal results; below, it is as small.
+__device__ __forceinline__ float quotient(float a, float b, float inverse)
+{
+    const float q = __fmul_rn(a, inverse);
+    return __fmaf_rn(__fmaf_rn(-q, b, a), inverse, q);
+}
+
 // 8 elements' 4-bit codes in a word, and their group's scale and lowest value in
-// another, out of the group's smallest and largest element.
+// another, out of the group's smallest and largest element.  (With divisions, 16
+// a thread, 4096 tokens take 38 us instead of 31.)
 __device__ __forceinline__ uint2 codes4(const float* x, float lo, float hi)
 {
     const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(max_nan(__fsub_rn(hi, lo), 1e-30f), 15.0f));
     const __nv_bfloat16 lb = __float2bfloat16_rn(lo);
-    const float scale = __bfloat162float(sb), low = __bfloat162float(lb);
+    const float scale = __bfloat162float(sb), low = __bfloat162float(lb), inverse = __frcp_rn(scale), top = 15.0f * scale;
     uint32_t w = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        int c = __float2int_rn(__fdiv_rn(__fsub_rn(x[i], low), scale));
-        c = c < 0 ? 0 : c > 15 ? 15 : c;
-        w |= static_cast<uint32_t>(c) << (16 * (i % 2) + 4 * (i / 2));
+        // within 0 .. 15 steps, which bounds the code; adding 1.5 2^23 rounds to a whole number, half to even
+        const float a = fminf(fmaxf(__fsub_rn(x[i], low), 0.0f), top);
+        const uint32_t c = __float_as_uint(__fadd_rn(quotient(a, scale, inverse), 12582912.0f)) & 15u;
+        w |= c << (16 * (i % 2) + 4 * (i / 2));
     }
     const uint32_t pair = static_cast<uint32_t>(__bfloat16_as_ushort(sb)) |
                           static_cast<uint32_t>(__bfloat16_as_ushort(lb)) << 16;
@@ -160,18 +172,19 @@ struct RopeParams {
 // UPH heads a pass.  What bounds it is how many tokens an SM works on at a
 // time, since each waits for its position, then its table row, then its heads:
 // small blocks, a head's successor loaded before it is worked on, and the first
-// heads before the position is there.  One head ahead, or two where codes are
+// heads before the position is there.  One head ahead, or two where int8 codes are
 // formed, since more registers leave fewer blocks.  4096 tokens, 64/8 heads of
 // 128: bf16 29.9 us, 5.7 TB/s, with 32 threads (64 threads 30.0, with two ahead
 // 34.0, three 38.5; 256 threads 37.9; the position first 33.2), and 5 ragged
 // prompts of up to 1201 tokens, 48 heads of 64, 11.6 us (64 threads 12.5);
 // int8 and read back 37.9 us with 64 threads (32 threads 45.6; one ahead 39.5;
-// loads only after the work on those before 40.5).
+// loads only after the work on those before 40.5).  4 bits, without reading back:
+// 30.2 us with 32 threads (64 threads 30.8, with two ahead 31.8; 128 threads 32.9).
 template <int UPH, int KIND, bool WIDE>
 __global__ void __launch_bounds__(rope_threads(KIND)) rope_append_kernel(const __grid_constant__ RopeParams p)
 {
     constexpr int kDim = UPH * kUnit;
-    constexpr int kAhead = KIND == kBf16 ? 1 : 2;  // heads that a thread has loaded, or is loading
+    constexpr int kAhead = KIND == kInt8 ? 2 : 1;  // heads that a thread has loaded, or is loading
     const RopeArgs& a = p.a;
     const int u = threadIdx.x % UPH;
     const int64_t t = blockIdx.x;
