@@ -69,10 +69,16 @@
 // product step for the eight of head_dim 128).  fp16's range: q is scaled per
 // row by a power of two, as for int8, and a tile of K by one that brings its
 // largest value to 2^14; the softmax, which multiplies by a factor anyway, takes
-// it back.  Where the keys of a tile are more than 2^10 apart, each is scaled by
+// it back.  Where the keys of a tile are more than 2^16 apart, each is scaled by
 // its own power, and the softmax multiplies key by key (such a tile is not to
 // let a large key, which a causal row may not even see, flush the others).
 // Within a key, what lies 2^-27 below its largest element may lose bits.
+// A chunk of 4096 tokens over 8192 keys, 64/8 heads, takes 1087 us (bf16 of the
+// same values 773, int8 1110), 4096 over 8192 with heads of 64 1020 (718, 1119):
+// as for int8, what the conversion adds to a kernel that the softmax bounds.
+// The factors' tests and the second form for tiles of distant keys stay out of
+// the softmax's common path: a branch to it there cost 20 us of the 300 that
+// chunks of 8 sequences with heads of 64 took.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -142,8 +148,6 @@ struct ChunkShared {
     uint64_t q_full[2], o_full[2];
     uint64_t s_full[2][2], p_full[2][2], pv_done[2];  // by query tile (and place)
     uint64_t done;
-    uint64_t ranged;    // the converting warps have each said how large the keys of their part are (4 bits)
-    uint2 range[2][4];  // the bits of the largest and of the smallest, by the tile's parity
     uint32_t tmem;
     volatile int abort;
 };
@@ -758,8 +762,8 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
             mbar_init(&sh.raw_full[i], 1);
             mbar_init(&sh.raw_empty[i], 4);
         }
-        for (int i = 0; i < S::kScaleBufs; ++i) {
-            mbar_init(&sh.sc_full[i], INT4 ? 4 : 1);
+        for (int i = 0; i < (INT8 ? S::kScaleBufs : 0); ++i) {
+            mbar_init(&sh.sc_full[i], 1);
             mbar_init(&sh.sc_empty[i], 8);
         }
         for (int i = 0; i < 2; ++i) {
@@ -772,7 +776,6 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
             mbar_init(&sh.o_full[i], 1);
         }
         mbar_init(&sh.done, 2);
-        mbar_init(&sh.ranged, 4);
         sh.abort = 0;
         fence_mbarrier_init();
     }
@@ -898,7 +901,8 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
             ran = runs;
             if (!runs) {
                 // no rows here: only the scales' slots have to be handed on
-                if constexpr (kCodes) {
+                if constexpr (INT4) sc = (sc + s.t1 - s.t0) % S::kScaleBufs;
+                if constexpr (INT8) {
                     for (int t = s.t0; t < s.t1; ++t) {
                         if (!warp_wait(&sh.abort, &sh.sc_full[sc], sc_phase)) break;
                         if (lane == 0) mbar_arrive(&sh.sc_empty[sc]);
@@ -931,23 +935,35 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
 #pragma unroll 1
             for (int j = 2 * s.t0; j < 2 * s.t1; ++j) {
                 const int b = j & 1;
+                const float *ks = nullptr, *vs = nullptr;
                 warp_wait(&sh.abort, &sh.s_full[i][b], s_phase);
                 tc_fence_after();
-                uint32_t v[64];
-                tmem_ld32_start(ts + 64 * b, v);
-                tmem_ld32_start(ts + 64 * b + 32, v + 32);
-                const float *ks = nullptr, *vs = nullptr;
                 if constexpr (INT4) {
+                    // (S is there, and so is what its keys were converted with)
                     ks = reinterpret_cast<const float*>(dyn + S::kOffScale + sc * S::kScaleBytes);
                     if (b == 0) {
-                        warp_wait(&sh.abort, &sh.sc_full[sc], sc_phase);
-                        const float back = ks[0];  // 0: by key
+                        const float back = *const_cast<const volatile float*>(ks);  // 0: by key
                         by_key = back == 0.0f;
                         const float c = fabsf(a.scale) * kLog2e * unit;
                         cs = fmaxf(by_key ? c : c * back, 1e-30f);
                     }
-                    ks += 4 + kStep * b;
                 }
+                if (INT4 && by_key) {
+                    // (rare, and a pass of its own through tensor memory, so that the usual one has no second form)
+#pragma unroll 1
+                    for (int e0 = 0; e0 < kStep; e0 += 16) {
+                        uint32_t x[16];
+                        tmem_ld16_wait(ts + 64 * b + e0, x);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            x[e] = __float_as_uint(__uint_as_float(x[e]) * ks[4 + kStep * b + e0 + e]);
+                        tmem_st16_start(ts + 64 * b + e0, x);
+                    }
+                    tmem_wait_st();
+                }
+                uint32_t v[64];
+                tmem_ld32_start(ts + 64 * b, v);
+                tmem_ld32_start(ts + 64 * b + 32, v + 32);
                 if constexpr (INT8) {
                     if (b == 0) warp_wait(&sh.abort, &sh.sc_full[sc], sc_phase);
                     ks = reinterpret_cast<const float*>(dyn + S::kOffScale) + sc * 2 * kTile + kStep * b;
@@ -955,7 +971,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
                 }
                 tmem_ld_wait(v);
                 tmem_ld_wait(v + 32);
-                if (INT8 || (INT4 && by_key)) {
+                if constexpr (INT8) {
 #pragma unroll
                     for (int e = 0; e < 64; e += 4) {
                         const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(ks + e);
@@ -1042,7 +1058,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
                 __syncwarp();
                 if (lane == 0) {
                     arrive_even<kPair>(&sh.p_full[i][b]);
-                    if constexpr (kCodes)
+                    if constexpr (INT8)
                         if (b) mbar_arrive(&sh.sc_empty[sc]);
                 }
                 if (b) s_phase ^= 1;
@@ -1296,9 +1312,10 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
             uint32_t raw_phase = 0, phase = 0;
             bool ok = true;
             const int tid = threadIdx.x & 127;
-            // 4 bits: the factors' slot, and the meetings of the four warps over a tile's range, so far
-            [[maybe_unused]] int sc = 0, ranges = 0;
-            [[maybe_unused]] uint32_t sc_phase = 0, met = 0;
+            // 4 bits: the factors' slot.  A slot has been read when it is written again, four tiles of K later: the buffer
+            // that tile goes to held K of at most three tiles before it, which has been multiplied, so that the softmax
+            // was done with S of the tile before that one, whose place that product took.
+            [[maybe_unused]] int sc = 0;
             while (ok && walk.next(s)) {
                 for (int n = 2 * (s.t1 - s.t0); n > 0; --n) {
                     if (!(ok = warp_wait(&sh.abort, &sh.raw_full[raw], raw_phase))) break;
@@ -1312,40 +1329,35 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
                         if (n & 1) {
                             convert_v4<S::kDimsV, DIM / 32>(src, pairs, rank * (S::kDimsV / 32), valid, dst, tid);
                         } else {
-                            if (!(ok = warp_wait(&sh.abort, &sh.sc_empty[sc], sc_phase ^ 1))) break;
-                            // how large the tile's keys are, and how far apart: a key a thread
-                            const float big = tid < valid ? key_range<DIM / 32>(pairs, tid) : 0.0f;
-                            const uint32_t bits = __float_as_uint(big);
-                            uint32_t most = __reduce_max_sync(0xffffffffu, bits);
-                            uint32_t least = __reduce_min_sync(0xffffffffu, bits ? bits : 0x7F800000u);
-                            const auto meet = [&]() {
-                                __syncwarp();
-                                if (lane == 0) mbar_arrive(&sh.ranged);
-                                ok = warp_wait(&sh.abort, &sh.ranged, met);
-                                met ^= 1;
-                                return ok;
-                            };
-                            if (lane == 0) sh.range[ranges][warp - kConvertWarp] = make_uint2(most, least);
-                            if (!meet()) break;
+                            // how large the tile's keys are, and how far apart: by each warp for itself, four keys a
+                            // lane (a meeting of the warps cost 30 us of the chunk of 4096 over 8192 keys, and a ring of
+                            // barriers for the factors 100)
+                            float big[4];
+                            uint32_t most = 0, least = 0x7F800000u;
 #pragma unroll
-                            for (int w = 0; w < 4; ++w) {
-                                most = max(most, sh.range[ranges][w].x);
-                                least = min(least, sh.range[ranges][w].y);
+                            for (int k = 0; k < 4; ++k) {
+                                const int key = 32 * k + lane;
+                                big[k] = key < valid ? key_range<DIM / 32>(pairs, key) : 0.0f;
+                                const uint32_t bits = __float_as_uint(big[k]);
+                                most = max(most, bits);
+                                least = min(least, bits ? bits : 0x7F800000u);
                             }
-                            ranges ^= 1;
+                            most = __reduce_max_sync(0xffffffffu, most);
+                            least = __reduce_min_sync(0xffffffffu, least);
                             float* slot = reinterpret_cast<float*>(dyn + S::kOffScale + sc * S::kScaleBytes);
                             float back;
                             float f = key_factor(__uint_as_float(most), back);
-                            if (most != 0 && (least >> 23) + 10 < (most >> 23)) {
-                                (void)key_factor(big, back);
-                                slot[4 + tid] = back;
+                            if (most != 0 && (least >> 23) + 16 < (most >> 23)) {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    (void)key_factor(big[k], back);
+                                    slot[4 + 32 * k + lane] = back;
+                                }
                                 back = f = 0.0f;
                             }
-                            if (tid == 0) slot[0] = back;
-                            if (f == 0.0f && !meet()) break;  // the others' keys' factors are there
+                            if (lane == 0) slot[0] = back;
                             __syncwarp();
-                            if (lane == 0) mbar_arrive(&sh.sc_full[sc]);
-                            if (++sc == S::kScaleBufs) sc = 0, sc_phase ^= 1;
+                            if (++sc == S::kScaleBufs) sc = 0;
                             convert_k4<DIM, S::kKeysK>(src, pairs, f, slot + 4, dst, tid, [&](int row) {
                                 return kPair ? (row >> 5) * kStep + 32 * rank + (row & 31) : row;
                             });
