@@ -399,7 +399,7 @@ def bd_block_norm(x, residual, gain, eps, out, ws, residual_out=None, post_gain=
         raise ValueError("vid must have one id per row")
     gate_rows = 0
     if gate is not None:
-        if gate.shape[-1] != d or gate.dim() > 2:
+        if gate.dim() not in (1, 2) or gate.shape[-1] != d:
             raise ValueError("gate must have the shape [d] or [rows][d]")
         gate_rows = gate.shape[0] if gate.dim() == 2 else 1
     if gate_idx is not None and (gate is None or gate_idx.numel() != T):

@@ -25,7 +25,6 @@ namespace {
 
 constexpr int kOutBf16 = 0, kOutF32 = 1, kOutE4m3 = 2;
 constexpr int kMaxThreads = 1024;
-constexpr int kThreads = 512;
 
 struct BlockNormParams {
     BlockNormArgs a;
@@ -653,7 +652,7 @@ cudaError_t launch_block_norm(const BlockNormArgs& a, int sm_count, cudaStream_t
     if (!few && groups <= 128) return launch_ring<4, 32 * kRingWarps, true>(a, 32 * kRingWarps, sm_count, stream);
     if (!few && groups <= 1024) return launch_ring<2, 512, false>(a, threads_for(2), sm_count, stream);
     if (!few && groups <= 2048) return launch_ring<2, 1024, false>(a, threads_for(2), sm_count, stream);
-    if (groups <= (few ? kMaxThreads : kThreads)) return launch_groups<1>(p, threads_for(1), sm_count, stream);
+    if (groups <= kMaxThreads) return launch_groups<1>(p, threads_for(1), sm_count, stream);
     if (groups <= 2 * kMaxThreads) return launch_groups<2>(p, threads_for(2), sm_count, stream);
     if (groups <= 4 * kMaxThreads) return launch_groups<4>(p, threads_for(4), sm_count, stream);
     return launch_groups<0>(p, kMaxThreads, sm_count, stream);

@@ -4,8 +4,10 @@ the write into the cache -> attention -> output product -> norm with the
 residual's addition.  Every step is an entry point of the library; a batch
 holds prompts and single tokens of any mixture of variants, and what a variant
 has of its own (the gains and the deltas of its linears) is picked per token.
+With --post-norm the block's output is normed with a gain of its own and weighted
+by its variant's gate before it is added.
 
-    python examples/decoder_block.py [--hidden 8192] [--kv int8] [--steps 32]
+    python examples/decoder_block.py [--hidden 8192] [--kv int8] [--post-norm] [--steps 32]
 
 The weights are random.  The first call takes the sequences' prompts in one
 batch, the others one token of each sequence, replayed as a CUDA graph."""
@@ -26,7 +28,7 @@ class DecoderBlock:
     """Weights, cache and workspaces of one layer's attention half.  Sequence s owns the pages page_table[s]."""
 
     def __init__(self, hidden=8192, n_q=64, n_kv=8, head_dim=128, variants=14, n_seq=16, max_len=1024, page=64,
-                 int8=True, max_tokens=4096, theta=10000.0, seed=0, device="cuda"):
+                 int8=True, max_tokens=4096, theta=10000.0, seed=0, device="cuda", int4=False, post_norm=False):
         self.hidden, self.n_q, self.n_kv, self.dim, self.page = hidden, n_q, n_kv, head_dim, page
         self.n_seq, self.eps = n_seq, 1e-5
         g = torch.Generator(device=device).manual_seed(seed)
@@ -42,9 +44,19 @@ class DecoderBlock:
             self.deltas[name] = (signs, alpha)
         self.gains = [[(1 + 0.1 * torch.randn(hidden, generator=g, device=device)).to(torch.bfloat16)
                        for _ in range(variants + 1)] for _ in range(2)]  # two norms; the base's gain first
+        self.post_gains = self.gates = None
+        if post_norm:  # the base's first
+            self.post_gains = [(1 + 0.1 * torch.randn(hidden, generator=g, device=device)).to(torch.bfloat16)
+                               for _ in range(variants + 1)]
+            self.gates = torch.rand(variants + 1, hidden, generator=g, device=device).to(torch.bfloat16)
         self.max_pages = -(-max_len // page)
         shape = (n_seq * self.max_pages, n_kv, page, head_dim)
-        if int8:
+        if int4:  # two codes a byte, and a pair of scale and lowest value for each group of 32
+            self.cache = bd.KvPages(*(torch.zeros(*shape[:3], head_dim // 2, dtype=torch.uint8, device=device)
+                                      for _ in range(2)),
+                                    *(torch.zeros(*shape[:3], head_dim // 32, 2, dtype=torch.bfloat16, device=device)
+                                      for _ in range(2)))
+        elif int8:
             self.cache = bd.KvPages(*(torch.zeros(shape, dtype=torch.int8, device=device) for _ in range(2)),
                                     *(torch.zeros(shape[:3], device=device) for _ in range(2)))
         else:
@@ -54,7 +66,8 @@ class DecoderBlock:
         self.rope = bd.rope_table(max_len, head_dim, theta, device)
         T, V = max_tokens, variants
         self.ws = bd.new_workspace(max(
-            bd.bd_rms_norm_workspace_size(T, hidden), bd.bd_linear_multi_workspace_size(T, V, rows, hidden),
+            bd.bd_rms_norm_workspace_size(T, hidden), bd.bd_block_norm_workspace_size(T, hidden),
+            bd.bd_linear_multi_workspace_size(T, V, rows, hidden),
             bd.bd_linear_multi_workspace_size(T, V, hidden, n_q * head_dim), bd.bd_rope_append_workspace_size(T),
             bd.bd_attention_workspace_size(T, n_seq, n_q, n_kv, head_dim)), device)
 
@@ -84,8 +97,13 @@ class DecoderBlock:
         bd.bd_attention(q, q_off, self.cache, self.page_table, kv_len, self.dim ** -0.5, max_new, b["att"], ws)
         bd.bd_linear_multi(b["att"].view(x.shape[0], -1), vid, *self.deltas["o"], bd.BD_ALPHA_PER_ROW, self.w_o,
                            b["y"], ws)
-        bd.bd_rms_norm(b["y"], second[0], self.eps, b["n"], ws, residual=x, residual_out=x, vid=vid,
-                       gain_list=second[1:])
+        if self.post_gains is None:
+            bd.bd_rms_norm(b["y"], second[0], self.eps, b["n"], ws, residual=x, residual_out=x, vid=vid,
+                           gain_list=second[1:])
+        else:
+            bd.bd_block_norm(b["y"], x, second[0], self.eps, b["n"], ws, residual_out=x, post_gain=self.post_gains[0],
+                             gate=self.gates, gate_idx=vid + 1, vid=vid, gain_list=second[1:],
+                             post_gain_list=self.post_gains[1:])
         return b["n"]
 
 
@@ -105,14 +123,15 @@ def main() -> None:
     ap.add_argument("--heads", type=int, default=64)
     ap.add_argument("--kv-heads", type=int, default=8)
     ap.add_argument("--sequences", type=int, default=16)
-    ap.add_argument("--kv", choices=("int8", "bf16"), default="int8")
+    ap.add_argument("--kv", choices=("int8", "int4", "bf16"), default="int8")
+    ap.add_argument("--post-norm", action="store_true")
     ap.add_argument("--steps", type=int, default=32)
     a = ap.parse_args()
     dev = torch.device("cuda:0")
     torch.cuda.set_device(dev)
     V, S = 14, a.sequences
     block = DecoderBlock(hidden=a.hidden, n_q=a.heads, n_kv=a.kv_heads, variants=V, n_seq=S, int8=a.kv == "int8",
-                         max_len=300 + a.steps, max_tokens=300 * S, device=dev)
+                         int4=a.kv == "int4", post_norm=a.post_norm, max_len=300 + a.steps, max_tokens=300 * S, device=dev)
     g = torch.Generator().manual_seed(1)
     prompts = torch.randint(1, 300, (S,), generator=g).tolist()
     variant = torch.randint(-1, V, (S,), generator=g, dtype=torch.int32).to(dev)

@@ -461,7 +461,7 @@ bd_status bd_kv_read(const bd_kv_pages* cache, const int32_t* page_table, int64_
  *            are not looked at, and what the cache holds past the length
  *            (NaN included) has no influence.  Of keys that a causal row does
  *            not see, v has to be finite: products run over whole tiles, and
- *            0 * NaN is NaN.
+ *            0 * NaN is NaN (4 bits: v's scales and lowest values).
  *   kv_len   device int32 [n_seq]
  *   out      device bf16 [T][n_q][head_dim], 16-byte aligned
  *   lse      device fp32 [T][n_q] or NULL: log sum_j exp(scale * q . k_j)
@@ -474,9 +474,17 @@ bd_status bd_kv_read(const bd_kv_pages* cache, const int32_t* page_table, int64_
  *     chunks; in the one for few rows (decode steps: up to 16 for each kv head
  *     of a sequence) to fp16, of 11 bits, but where one of 32 keys' products is
  *     too small for fp16's range all of theirs are rounded to bf16, of 8.
+ *   - over a 4-bit cache, in the kernel for few rows: probability times the
+ *     scale of its key's group, to fp16, over a power of two near the largest
+ *     product of a probability of the row with a scale or lowest value (2^-25 of
+ *     it still has all 11 bits, less than 2^-36 counts as 0); lowest values
+ *     multiply fp32 probabilities.  In the kernel for chunks: probabilities to
+ *     bf16, and v (code * scale + low) to bf16.
  * Int8 codes enter the tensor cores exactly (K's in fp16 with q, whose rows are
  * scaled by a power of two so that bf16's 8 bits fit), and their scales
- * multiply the fp32 scores and probabilities.
+ * multiply the fp32 scores and probabilities.  4-bit codes of K enter exactly
+ * too, with scales and lowest values in fp32 terms; in chunks, what lies 2^-27
+ * and more below the largest element of its key may be lost.
  * Cached values up to 2^80 in magnitude give the formula's result; beyond that
  * a product may overflow, and a result below 2^-125 may come out as 0.  Results do not depend on timing (no atomics).  A
  * page outside [0, n_pages), a length outside
