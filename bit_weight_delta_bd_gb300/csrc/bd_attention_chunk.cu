@@ -56,9 +56,11 @@
 // odd CTA's converted); 12..15 conversion (int8, 4 bits).
 //
 // 4-bit keys and values: TMA and bulk copies bring the codes with their groups'
-// scales and lowest values, and the fourth warpgroup forms tiles of numbers.
-//   V: code * scale + low, rounded once to bf16: what a bf16 cache of the same
-// values would hold.
+// scales and lowest values, and the fourth warpgroup forms tiles of fp16 numbers,
+// two warps K's and two V's (by four warps one tile after the other, what a tile
+// waits for is waited for twice as often: 1140 us for 1066, 4096 tokens over 8192
+// keys; a warp takes one group at a time, since with two or four in flight its
+// reads and writes get into the products' way: 1079 and 1167).
 //   K is kept exact, since its rounding would show in the scores (by 2^-12 of the
 // sum of their products' magnitudes, where fp32 sums leave 2^-20: the
 // log-sum-exp of a row that sees few keys was off by 1e-4 to 1e-3).  A key is
@@ -66,19 +68,24 @@
 // whose first term has 3 + 8 bits, so fp16 holds it, and whose second is the
 // same for the 32 dims of a group: S gets 16 more columns of Q, the sums of q
 // over each group in two pieces of 11 bits, against low and 8 scale (a ninth
-// product step for the eight of head_dim 128).  fp16's range: q is scaled per
-// row by a power of two, as for int8, and a tile of K by one that brings its
-// largest value to 2^14; the softmax, which multiplies by a factor anyway, takes
-// it back.  Where the keys of a tile are more than 2^16 apart, each is scaled by
-// its own power, and the softmax multiplies key by key (such a tile is not to
-// let a large key, which a causal row may not even see, flush the others).
-// Within a key, what lies 2^-27 below its largest element may lose bits.
-// A chunk of 4096 tokens over 8192 keys, 64/8 heads, takes 1087 us (bf16 of the
-// same values 773, int8 1110), 4096 over 8192 with heads of 64 1020 (718, 1119):
-// as for int8, what the conversion adds to a kernel that the softmax bounds.
-// The factors' tests and the second form for tiles of distant keys stay out of
-// the softmax's common path: a branch to it there cost 20 us of the 300 that
-// chunks of 8 sequences with heads of 64 took.
+// product step for the eight of head_dim 128).
+//   V: code * scale + low, rounded once to 11 bits, as are the probabilities (in
+// bf16, with 8, the result's error was 0.0028 of its norm for 0.0017, which is
+// what its own rounding to bf16 makes).
+//   fp16's range.  q is scaled per row by a power of two, as for int8; a tile of K
+// and a tile of V by one that brings its largest values near 2^14.  The softmax,
+// which multiplies by a factor anyway, takes K's back.  V's goes into P: a row's
+// reference follows the largest product of a probability with its tile's size, so
+// that P is at most 2^15 and what is rounded to a multiple of 2^-24 lies 2^-35 to
+// 2^-39 below the largest; the denominator takes it out again.  Where the keys or
+// the values of a tile are more than 2^16 apart each has its own power, and the
+// softmax goes through the scores once more (such a tile is not to let a large
+// one, which a causal row may not even see, flush the others).  Within a key or a
+// value, what lies 2^-27 below its largest element may lose bits.
+// A chunk of 4096 tokens over 8192 keys, 64/8 heads, takes 1066 us (bf16 of the
+// same values 773, int8 1110), 4096 over 8192 with heads of 64 999 (718, 1119).
+// What the conversion adds to a kernel that the softmax bounds: without it 1009
+// and 935.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -94,7 +101,6 @@ constexpr int kBf16 = 0, kInt8 = 1, kInt4 = 2;  // what the cache holds
 constexpr int kTile = 128;       // keys of a tile
 constexpr int kQRows = 128;      // rows of a query tile
 constexpr int kStep = 64;        // keys of a step
-constexpr float kLag = 8.0f;     // how far (log2) a row's maximum may run ahead of the one in use
 
 struct ChunkParams {
     // [n_pages * n_kv][page][dim]; boxes of 128 bytes (int8 V of a pair, and head_dim 64: 64) x page rows, K of a
@@ -109,13 +115,14 @@ struct ChunkShape {
     static constexpr int kCtas = kPair ? 2 : 1;
     static constexpr bool INT8 = KIND == kInt8, INT4 = KIND == kInt4, kCodes = INT8 || INT4;
     static constexpr int kThreads = kCodes ? 512 : 384;
+    static constexpr int kConverters = INT4 ? 2 : 4;  // warps that convert a tile of codes
     static constexpr bool kSmall = PAIR || DIM == 64;  // tiles of 16 KB
     // bf16 tiles in shared memory, and tiles of codes
     static constexpr int kBufs = kCodes ? (kSmall ? 6 : 3) : kSmall ? 8 : 5;
     static constexpr int kRaw = INT8 ? (kSmall ? 6 : 3) : INT4 ? (kSmall ? 5 : 3) : 0;
     static constexpr int kScaleBufs = INT4 ? 4 : INT8 ? (kSmall ? 4 : 3) : 0;  // scales of a key tile, K and V
-    // 4 bits: a tile's factor, and its keys'; the columns of Q and K past the dims, rows of 32 bytes
-    static constexpr int kScaleBytes = INT4 ? (4 + kTile) * 4 : 2 * kTile * 4;
+    // 4 bits: a tile's factors, and its keys'; the columns of Q and K past the dims, rows of 32 bytes
+    static constexpr int kScaleBytes = INT4 ? (4 + 2 * kTile) * 4 : 2 * kTile * 4;
     static constexpr int kExtRow = INT4 ? 32 : 0;
     // a CTA's part of a tile: in a pair half the keys of each step of K, half the dims of V
     static constexpr int kKeysK = kTile / kCtas, kDimsV = DIM / kCtas;
@@ -131,6 +138,9 @@ struct ChunkShape {
     static constexpr int kOffRaw = kOffBufs + kBufs * kTileBytes;
     static constexpr int kOffScale = kOffRaw + kRaw * kRawBytes;
     static constexpr int kBytes = kOffScale + kScaleBufs * kScaleBytes;
+    // how far (log2) a row's maximum may run ahead of the one in use, and what a probability is times 2 to the power of:
+    // the two together end below fp16's range for 4 bits
+    static constexpr float kLag = INT4 ? 4.0f : 8.0f, kBias = INT4 ? 11.0f : attn_bias<INT8>();
     // registers of a softmax thread, and of the others: the sum over the
     // warpgroups is what the block was launched with
     static constexpr int kSoftRegs = kCodes ? 168 : 208;
@@ -391,6 +401,12 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    const __half2 r = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 // Two codes, bytes 0 and 2 of r, as a pair of fp16 (see bd_attention.cu).
 __device__ __forceinline__ uint32_t codes_f16x2(uint32_t r)
 {
@@ -463,17 +479,14 @@ __device__ __forceinline__ int swizzled_codes(int t, int c)
     return ROW_BYTES == 64 ? t * 64 + ((c ^ ((t >> 1) & 3)) << 4) : t * 32 + ((c ^ ((t >> 2) & 1)) << 4);
 }
 
-// 8 4-bit codes as 8 bf16 values code * scale + low: 0x4300 | code is 128 + code.
-__device__ __forceinline__ uint4 values4(uint32_t w, uint32_t scale, uint32_t low)
+// 8 4-bit codes as 8 fp16 values code * scale + low: 0x6400 | code is 1024 + code.
+__device__ __forceinline__ uint4 values4(uint32_t w, __half2 scale, __half2 low)
 {
-    const __nv_bfloat162 offset = __float2bfloat162_rn(128.0f);
     uint32_t r[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t x = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-        const __nv_bfloat162 v = __hfma2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), offset),
-                                         *reinterpret_cast<const __nv_bfloat162*>(&scale),
-                                         *reinterpret_cast<const __nv_bfloat162*>(&low));
+        const uint32_t x = ((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u;
+        const __half2 v = __hfma2(__hadd2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(-1024.0f)), scale, low);
         r[i] = *reinterpret_cast<const uint32_t*>(&v);
     }
     return make_uint4(r[0], r[1], r[2], r[3]);
@@ -496,25 +509,62 @@ __device__ __forceinline__ uint4 centred4(uint32_t w, __half2 scale)
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// A tile of V's 4-bit codes with their scales and lowest values as a tile of bf16
-// values, a group of 32 a thread, by the 128 threads of a warpgroup.  Eight
-// neighbouring lanes take the same group of 8 keys in a row: reads and writes
-// of 16 bytes meet in no bank.  DIM: values of a row; PAIRS: words of scales of a
-// row, of which this tile's are the DIM / 32 from first on.  Rows from `valid`
-// on become zeros (what lies there may be anything).
-template <int DIM, int PAIRS>
-__device__ __forceinline__ void convert_v4(const uint8_t* src, const uint8_t* pairs, int first, int valid, uint8_t* dst,
-                                           int tid)
+// The size of a key or value: of its groups' 16 scale and |lowest value| the
+// largest, as the bits of a bf16 number whose exponent e bounds its elements by
+// 2^(e + 2).  One that is not finite, or below 2^-98 (a vector of zeros has scales
+// of 2^-104), has no say: 0.
+template <int PAIRS>
+__device__ __forceinline__ uint32_t pairs_size(const uint8_t* pairs, int key)
 {
-    constexpr int kGroups = DIM / 32, kKeys = 128 / kGroups;  // of a round
+    uint32_t most;  // of the scales, and of the lowest values
+    if constexpr (PAIRS == 4) {
+        const uint4 w = *reinterpret_cast<const uint4*>(pairs + key * 16);
+        most = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu), __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+    } else {
+        const uint2 w = *reinterpret_cast<const uint2*>(pairs + key * 8);
+        most = __vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu);
+    }
+    const uint32_t size = max((most & 0xFFFFu) + (4u << 7), most >> 16);
+    constexpr uint32_t kFrom = (127 - 98) << 7;
+    return size - kFrom < 0x7F80u - kFrom ? size : 0u;
+}
+
+// What converted values of a size with exponent e are multiplied by is 2^(kTopExp
+// - e), which leaves them below 2^15.  Sizes further than 2^kFar apart do not share
+// a factor.
+constexpr int kTopExp = 13, kFar = 16;
+constexpr int kLeastK = -98;
+constexpr int kLeastV = -66;  // smaller sizes count as this: the sum of the probabilities over them stays in fp32's range
+
+__device__ __forceinline__ float exp2_int(int e) { return __int_as_float((127 + e) << 23); }
+
+__device__ __forceinline__ int size_exp(uint32_t size, int from)
+{
+    return size ? min(max(static_cast<int>(size >> 7) - 127, from), 100) : 0;
+}
+
+// A tile of V's 4-bit codes with their scales and lowest values as a tile of fp16
+// values times a factor, a group of 32 a thread at a time, by 64 threads.  Eight
+// neighbouring lanes take the same group of 8 keys in a row: reads and writes of 16
+// bytes meet in no bank.  DIM: values of a row; PAIRS: words of scales of a row, of
+// which this tile's are the DIM / 32 from first on.  Rows from `valid` on become
+// zeros (what lies there may be anything).  f: the factor of all, or 0 where by_key
+// has the exponent of each.
+template <int DIM, int PAIRS>
+__device__ __forceinline__ void convert_v4(const uint8_t* src, const uint8_t* pairs, int first, float f, const float* by_key,
+                                           int valid, uint8_t* dst, int tid)
+{
+    constexpr int kGroups = DIM / 32, kKeys = 64 / kGroups;  // of a round
     const int g = (tid >> 3) & (kGroups - 1), key0 = (tid & 7) + 8 * (tid / (8 * kGroups));
     uint8_t* half = dst + (g >> 1) * (kTile * 128);
-#pragma unroll 2
+#pragma unroll 1
     for (int i = 0; i < kTile / kKeys; ++i) {
         const int key = key0 + i * kKeys;
         const uint4 c = *reinterpret_cast<const uint4*>(src + swizzled_codes<DIM / 2>(key, g));
         const uint32_t pair = *reinterpret_cast<const uint32_t*>(pairs + (key * PAIRS + first + g) * 4);
-        const uint32_t scale = __byte_perm(pair, 0, 0x1010), low = __byte_perm(pair, 0, 0x3232);
+        const float fk = f != 0.0f ? f : exp2_int(kTopExp - static_cast<int>(by_key[key]));
+        const __half2 scale = __float2half2_rn(__uint_as_float(pair << 16) * fk);
+        const __half2 low = __float2half2_rn(__uint_as_float(pair & 0xFFFF0000u) * fk);
         const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -525,52 +575,25 @@ __device__ __forceinline__ void convert_v4(const uint8_t* src, const uint8_t* pa
     }
 }
 
-// The largest element that a key may have, by its groups' scales and lowest
-// values: 0 where that is not finite.
-template <int PAIRS>
-__device__ __forceinline__ float key_range(const uint8_t* pairs, int key)
-{
-    float big = 0.0f;
-#pragma unroll
-    for (int g = 0; g < PAIRS; ++g) {
-        const uint32_t pair = *reinterpret_cast<const uint32_t*>(pairs + (key * PAIRS + g) * 4);
-        const float s = __uint_as_float(pair << 16), low = __uint_as_float(pair & 0xFFFF0000u);
-        const float a = fmaf(15.0f, s, low);
-        // (NaN in, NaN out: the maximum of two would drop it)
-        const float m = fmaxf(fmaxf(fabsf(low), fabsf(a)), 8.0f * fabsf(s));
-        big = a - a == 0.0f && low - low == 0.0f ? fmaxf(big, m) : INFINITY;
-    }
-    return big < INFINITY ? big : 0.0f;
-}
-
-// What K's values of that size are multiplied by to lie below 2^14 .. 2^15, and
-// its inverse; 0 (no key says anything) counts as 1.
-__device__ __forceinline__ float key_factor(float big, float& back)
-{
-    const float u = big > 0.0f ? __uint_as_float(__float_as_uint(fminf(fmaxf(big, 7.9e-31f), 1.2e30f)) & 0x7F800000u) : 1.0f;
-    back = u / 16384.0f;
-    return 16384.0f / u;
-}
-
 // A tile of K's 4-bit codes: (code - 8) scale in fp16, over the factor of the key,
 // and behind the tile the 16 columns for the lowest values, for each group (low,
 // 8 scale) twice.  KEYS: rows of the tile, which are keys key_of(row) of the
 // whole tile of 128 whose scales and lowest values `pairs` holds.  f: the factor
-// of all keys, or 0 where by_key has each key's inverse.
+// of all keys, or 0 where by_key has the exponent of each.
 template <int DIM, int KEYS, typename KeyOf>
 __device__ __forceinline__ void convert_k4(const uint8_t* src, const uint8_t* pairs, float f, const float* by_key,
                                            uint8_t* dst, int tid, KeyOf key_of)
 {
-    constexpr int kGroups = DIM / 32, kKeys = 128 / kGroups;  // of a round
+    constexpr int kGroups = DIM / 32, kKeys = 64 / kGroups;  // of a round
     const int g = (tid >> 3) & (kGroups - 1), row0 = (tid & 7) + 8 * (tid / (8 * kGroups));
     uint8_t* half = dst + (g >> 1) * (KEYS * 128);
     uint8_t* ext = dst + KEYS * DIM * 2;
-#pragma unroll 2
+#pragma unroll 1
     for (int i = 0; i < KEYS / kKeys; ++i) {
         const int row = row0 + i * kKeys, key = key_of(row);
         const uint4 c = *reinterpret_cast<const uint4*>(src + swizzled_codes<DIM / 2>(row, g));
         const uint32_t pair = *reinterpret_cast<const uint32_t*>(pairs + (key * kGroups + g) * 4);
-        const float fk = f != 0.0f ? f : 1.0f / by_key[key];
+        const float fk = f != 0.0f ? f : exp2_int(kTopExp - static_cast<int>(by_key[key]));
         const float s = __uint_as_float(pair << 16) * fk, low = __uint_as_float(pair & 0xFFFF0000u) * fk;
         const __half2 scale = __float2half2_rn(s);
         const uint32_t w[4] = {c.x, c.y, c.z, c.w};
@@ -753,17 +776,17 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
     grid_launch_dependents();
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kBufs; ++i) {
-            // (codes: four warps of the even CTA, and what the odd one passes on)
-            mbar_init(&sh.full[i], kCodes ? 3 + S::kCtas : S::kCtas);
+            // (codes: the converting warps of the even CTA, and what the odd one passes on)
+            mbar_init(&sh.full[i], kCodes ? S::kConverters - 1 + S::kCtas : S::kCtas);
             mbar_init(&sh.empty[i], 2);
-            mbar_init(&sh.landed[i], kCodes ? 4 : 1);
+            mbar_init(&sh.landed[i], kCodes ? S::kConverters : 1);
         }
         for (int i = 0; i < S::kRaw; ++i) {
             mbar_init(&sh.raw_full[i], 1);
-            mbar_init(&sh.raw_empty[i], 4);
+            mbar_init(&sh.raw_empty[i], S::kConverters);
         }
-        for (int i = 0; i < (INT8 ? S::kScaleBufs : 0); ++i) {
-            mbar_init(&sh.sc_full[i], 1);
+        for (int i = 0; i < S::kScaleBufs; ++i) {
+            mbar_init(&sh.sc_full[i], INT4 ? S::kConverters : 1);
             mbar_init(&sh.sc_empty[i], 8);
         }
         for (int i = 0; i < 2; ++i) {
@@ -929,34 +952,41 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
             // scores are over their tile's factor, and the maximum is kept in those units
             float cs = c2;
             const float cm = INT4 ? 1.0f : c2;
-            [[maybe_unused]] bool by_key = false;
             m = -INFINITY;
             l = 0.0f;
 #pragma unroll 1
             for (int j = 2 * s.t0; j < 2 * s.t1; ++j) {
                 const int b = j & 1;
                 const float *ks = nullptr, *vs = nullptr;
+                [[maybe_unused]] float back = 0.0f, v_exp = 0.0f;  // 4 bits, of the tile
+                [[maybe_unused]] bool far_v = false;
                 warp_wait(&sh.abort, &sh.s_full[i][b], s_phase);
                 tc_fence_after();
                 if constexpr (INT4) {
                     // (S is there, and so is what its keys were converted with)
                     ks = reinterpret_cast<const float*>(dyn + S::kOffScale + sc * S::kScaleBytes);
-                    if (b == 0) {
-                        const float back = *const_cast<const volatile float*>(ks);  // 0: by key
-                        by_key = back == 0.0f;
-                        const float c = fabsf(a.scale) * kLog2e * unit;
-                        cs = fmaxf(by_key ? c : c * back, 1e-30f);
-                    }
+                    back = ks[0];
+                    v_exp = ks[1];
+                    const float c = fabsf(a.scale) * kLog2e * unit;
+                    far_v = ks[2] == 0.0f;
+                    cs = far_v ? 1.0f : fmaxf(back == 0.0f ? c : c * back, 1e-30f);
                 }
-                if (INT4 && by_key) {
-                    // (rare, and a pass of its own through tensor memory, so that the usual one has no second form)
+                if (INT4 && (back == 0.0f || far_v)) {
+                    // keys or values far apart (rare, and a pass of its own through tensor memory, so that the usual one
+                    // has no second form): each key's factor; with the values', the scores are in units of log2
+                    const float c = fabsf(a.scale) * kLog2e * unit;
 #pragma unroll 1
                     for (int e0 = 0; e0 < kStep; e0 += 16) {
                         uint32_t x[16];
                         tmem_ld16_wait(ts + 64 * b + e0, x);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            x[e] = __float_as_uint(__uint_as_float(x[e]) * ks[4 + kStep * b + e0 + e]);
+                        for (int e = 0; e < 16; ++e) {
+                            const int key = kStep * b + e0 + e;
+                            float y = __uint_as_float(x[e]) *
+                                      (back == 0.0f ? exp2_int(static_cast<int>(ks[4 + key]) - kTopExp) : back);
+                            if (far_v) y = fmaf(y, c, ks[4 + kTile + key]);
+                            x[e] = __float_as_uint(y);
+                        }
                         tmem_st16_start(ts + 64 * b + e0, x);
                     }
                     tmem_wait_st();
@@ -1007,10 +1037,10 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
                     for (int k = 0; k < 4; ++k)
                         mx[k] = max3(mx[k], __uint_as_float(v[e + 2 * k]), __uint_as_float(v[e + 2 * k + 1]));
                 const float mt = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-                const float mu = INT4 ? mt * cs : mt;
+                const float mu = INT4 ? fmaf(mt, cs, v_exp) : mt;
                 // the first step sets the maximum; later it moves when it has grown by kLag
-                const bool grow = mu > m && (mu - m) * cm > kLag;
-                if (__any_sync(0xffffffffu, grow)) {
+                const bool grow = mu > m && (mu - m) * cm > S::kLag;
+                if (__any_sync(0xffffffffu, grow || (INT4 && far_v))) {
                     const float f = !grow ? 1.0f : m == -INFINITY ? 0.0f : ex2((m - mu) * cm);
                     if (grow) m = mu;
                     l *= f;
@@ -1027,8 +1057,22 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
                             tmem_st16_start(to + d, o);
                         }
                     }
+                    if (INT4 && far_v) {
+                        // the probabilities' sum, out of the values' factors
+                        const int left = seen - j * kStep;
+                        const float to_p = m == -INFINITY ? 0.0f : S::kBias + kTopExp - m;
+#pragma unroll 1
+                        for (int e0 = 0; e0 < kStep; e0 += 16) {
+                            uint32_t x[16];
+                            tmem_ld16_wait(ts + 64 * b + e0, x);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if (e0 + e < left)
+                                    l += ex2(__uint_as_float(x[e]) - ks[4 + kTile + kStep * b + e0 + e] + to_p);
+                        }
+                    }
                 }
-                const float nm = m == -INFINITY ? 0.0f : fmaf(-m, cm, attn_bias<INT8>());
+                const float nm = m == -INFINITY ? 0.0f : INT4 ? S::kBias + v_exp - m : fmaf(-m, cm, S::kBias);
                 uint64_t sum[2] = {0, 0};  // pairs of zeros
                 const uint64_t c22 = f32x2(cs, cs), nm2 = f32x2(nm, nm);
 #pragma unroll
@@ -1048,11 +1092,13 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
                             const uint64_t pp = f32x2(pr.x, pr.y);
                             sum[k] = add2(sum[k], pp);
                             if constexpr (INT8) pr = unpack2(mul2(pp, k ? f.y : f.x));
-                            pk[e / 2 + k] = pack_bf16x2(pr.x, pr.y);
+                            pk[e / 2 + k] = INT4 ? pack_f16x2(pr.x, pr.y) : pack_bf16x2(pr.x, pr.y);
                         }
                     }
                     tmem_st16_start(ts + 64 * b + e0 / 2, pk);
                 }
+                [[maybe_unused]] float to_sum = 0.0f;
+                if constexpr (INT4) to_sum = ks[2];  // (the slot may be another tile's after P is handed on)
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -1066,9 +1112,10 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
                 if constexpr (kCodes)
                     if (b && ++sc == S::kScaleBufs) sc = 0, sc_phase ^= 1;
                 const float2 s2 = unpack2(add2(sum[0], sum[1]));
-                l += s2.x + s2.y;
+                if constexpr (INT4) l = fmaf(s2.x + s2.y, to_sum, l);
+                else l += s2.x + s2.y;
             }
-            m2 = m == -INFINITY ? -INFINITY : fmaf(m, cm, -attn_bias<INT8>());
+            m2 = m == -INFINITY ? -INFINITY : fmaf(m, cm, -S::kBias - (INT4 ? kTopExp : 0));
         }
     } else if (warp < kConvertWarp) {
         reg_dec<S::kOtherRegs>();
@@ -1196,7 +1243,8 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
             constexpr int kRows = kQRows * S::kCtas;
             constexpr uint32_t kIdescS = kCodes ? idesc_f16_f32(kRows, kStep) : idesc_bf16_f32(kRows, kStep);
             // V: rows along the contracted index
-            constexpr uint32_t kIdescO = idesc_bf16_f32(kRows, DIM) | (1u << 16);
+            constexpr uint32_t kIdescO =
+                (INT4 ? idesc_f16_f32(kRows, DIM) : idesc_bf16_f32(kRows, DIM)) | (1u << 16);
             const int i = warp - kMmaWarp;
             const uint32_t q_addr = smem_u32(dyn + i * S::kQBytes), buf_addr = smem_u32(dyn + S::kOffBufs);
             const uint32_t ts = tmem + i * 128, to = tmem + kTmemO + i * DIM;
@@ -1306,66 +1354,94 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
         }
     } else {
         reg_dec<S::kOtherRegs>();
-        if constexpr (kCodes) {
+        if constexpr (INT4) {
+            // ------------------------------------- 4-bit codes to tiles of numbers: two warps for K's, two for V's
+            const bool is_v = warp >= kConvertWarp + 2;
+            const int tid = threadIdx.x & 63;
+            int raw = is_v, buf = is_v, sc = 0;
+            uint32_t raw_phase = 0, phase = 0, sc_phase = 0;
+            bool ok = true;
+            const auto hand_on = [&]() {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(kPair && rank != 0 ? &sh.landed[buf] : &sh.full[buf]);
+                    mbar_arrive(&sh.raw_empty[raw]);
+                }
+                if ((raw += 2) >= S::kRaw) raw -= S::kRaw, raw_phase ^= 1;
+                if ((buf += 2) >= S::kBufs) buf -= S::kBufs, phase ^= 1;
+                if (++sc == S::kScaleBufs) sc = 0, sc_phase ^= 1;
+            };
+            // the place of the tile's K, which its V's is next to
+            const auto k_place = [&]() { return is_v ? (buf == 0 ? S::kBufs - 1 : buf - 1) : buf; };
+            while (ok && walk.next(s)) {
+                for (int t = s.t0; t < s.t1; ++t) {
+                    const int valid = s.sq.len - t * kTile;
+                    const uint8_t* src = dyn + S::kOffRaw + raw * S::kRawBytes;
+                    const uint8_t* pairs = src + S::kCodeBytes;
+                    uint8_t* dst = dyn + S::kOffBufs + buf * S::kTileBytes;
+                    float* slot = reinterpret_cast<float*>(dyn + S::kOffScale + sc * S::kScaleBytes);
+                    float* by_key = slot + 4 + (is_v ? kTile : 0);
+                    if (!(ok = warp_wait(&sh.abort, &sh.raw_full[raw], raw_phase))) break;
+                    // the sizes of the tile's keys (values), by each of the two warps for itself, four keys a lane (by a
+                    // warp that has no other work, which is late then, the chunk of 4096 over 8192 keys takes 100 us more)
+                    uint32_t size[4], most = 0, least = 0xFFFFu;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int key = 32 * k + lane;
+                        size[k] = key < valid ? pairs_size<DIM / 32>(pairs, key) : 0u;
+                        most = max(most, size[k]);
+                        least = min(least, size[k] ? size[k] : 0xFFFFu);
+                    }
+                    most = __reduce_max_sync(0xffffffffu, most);
+                    least = __reduce_min_sync(0xffffffffu, least);
+                    const int from = is_v ? kLeastV : kLeastK;
+                    const bool far = most != 0 && (least >> 7) + kFar < (most >> 7);
+                    const int e = size_exp(most, from);
+                    // The factors' slot has been read when it is written again, four tiles later: the place that the
+                    // tile's K goes to held K of at most three tiles before it (or a later V), which has been multiplied,
+                    // after P of the tile before that one.
+                    if (!(ok = warp_wait(&sh.abort, &sh.empty[k_place()], (is_v && buf == 0 ? phase : phase ^ 1)))) break;
+                    if (far) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) by_key[32 * k + lane] = static_cast<float>(size_exp(size[k], from));
+                    }
+                    // what takes K's factor back (0: by key); V's exponent, which P gets, and what takes it out of the sum
+                    // of P (0: by key)
+                    if (lane == 0) {
+                        if (is_v) slot[1] = far ? 0.0f : static_cast<float>(e), slot[2] = far ? 0.0f : exp2_int(kTopExp - e);
+                        else slot[0] = far ? 0.0f : exp2_int(e - kTopExp);
+                    }
+                    __syncwarp();
+                    const float f = far ? 0.0f : exp2_int(kTopExp - e);
+                    if (is_v) {
+                        if (lane == 0) mbar_arrive(&sh.sc_full[sc]);
+                        if (!(ok = warp_wait(&sh.abort, &sh.empty[buf], phase ^ 1))) break;
+                        convert_v4<S::kDimsV, DIM / 32>(src, pairs, rank * (S::kDimsV / 32), f, by_key, valid, dst, tid);
+                    } else {
+                        convert_k4<DIM, S::kKeysK>(src, pairs, f, by_key, dst, tid, [&](int row) {
+                            return kPair ? (row >> 5) * kStep + 32 * rank + (row & 31) : row;
+                        });
+                        // (with K the factors are handed on)
+                        if (!(ok = warp_wait(&sh.abort, &sh.sc_full[sc], sc_phase))) break;
+                    }
+                    hand_on();
+                }
+            }
+        } else if constexpr (INT8) {
             // -------------------------------------------------------- codes to tiles of numbers
             int raw = 0, buf = 0;
             uint32_t raw_phase = 0, phase = 0;
             bool ok = true;
             const int tid = threadIdx.x & 127;
-            // 4 bits: the factors' slot.  A slot has been read when it is written again, four tiles of K later: the buffer
-            // that tile goes to held K of at most three tiles before it, which has been multiplied, so that the softmax
-            // was done with S of the tile before that one, whose place that product took.
-            [[maybe_unused]] int sc = 0;
             while (ok && walk.next(s)) {
                 for (int n = 2 * (s.t1 - s.t0); n > 0; --n) {
                     if (!(ok = warp_wait(&sh.abort, &sh.raw_full[raw], raw_phase))) break;
                     if (!(ok = warp_wait(&sh.abort, &sh.empty[buf], phase ^ 1))) break;
                     const uint8_t* src = dyn + S::kOffRaw + raw * S::kRawBytes;
                     uint8_t* dst = dyn + S::kOffBufs + buf * S::kTileBytes;
-                    if constexpr (INT4) {
-                        const uint8_t* pairs = src + S::kCodeBytes;
-                        // (n counts down: the tile is t1 - (n + 1) / 2)
-                        const int valid = s.sq.len - (s.t1 - (n + 1) / 2) * kTile;
-                        if (n & 1) {
-                            convert_v4<S::kDimsV, DIM / 32>(src, pairs, rank * (S::kDimsV / 32), valid, dst, tid);
-                        } else {
-                            // how large the tile's keys are, and how far apart: by each warp for itself, four keys a
-                            // lane (a meeting of the warps cost 30 us of the chunk of 4096 over 8192 keys, and a ring of
-                            // barriers for the factors 100)
-                            float big[4];
-                            uint32_t most = 0, least = 0x7F800000u;
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const int key = 32 * k + lane;
-                                big[k] = key < valid ? key_range<DIM / 32>(pairs, key) : 0.0f;
-                                const uint32_t bits = __float_as_uint(big[k]);
-                                most = max(most, bits);
-                                least = min(least, bits ? bits : 0x7F800000u);
-                            }
-                            most = __reduce_max_sync(0xffffffffu, most);
-                            least = __reduce_min_sync(0xffffffffu, least);
-                            float* slot = reinterpret_cast<float*>(dyn + S::kOffScale + sc * S::kScaleBytes);
-                            float back;
-                            float f = key_factor(__uint_as_float(most), back);
-                            if (most != 0 && (least >> 23) + 16 < (most >> 23)) {
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    (void)key_factor(big[k], back);
-                                    slot[4 + 32 * k + lane] = back;
-                                }
-                                back = f = 0.0f;
-                            }
-                            if (lane == 0) slot[0] = back;
-                            __syncwarp();
-                            if (++sc == S::kScaleBufs) sc = 0;
-                            convert_k4<DIM, S::kKeysK>(src, pairs, f, slot + 4, dst, tid, [&](int row) {
-                                return kPair ? (row >> 5) * kStep + 32 * rank + (row & 31) : row;
-                            });
-                        }
-                    } else {
-                        if (n & 1) convert_tile<S::kDimsV, kTile, false>(src, dst, tid);  // V
-                        else convert_tile<DIM, S::kKeysK, true>(src, dst, tid);           // K
-                    }
+                    if (n & 1) convert_tile<S::kDimsV, kTile, false>(src, dst, tid);  // V
+                    else convert_tile<DIM, S::kKeysK, true>(src, dst, tid);           // K
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {

@@ -545,9 +545,13 @@ __global__ void __launch_bounds__(BLOCK, ring_blocks(NG, BLOCK, WARP)) block_nor
             amax = max_nan(both.z * mult, 1e-30f);
             if (first == 0) a.scale[t] = amax / 448.0f;
         }
-        const uint64_t m2 = f32x2(mult, mult);
-        const float code = OUT == kOutE4m3 ? 448.0f / amax : 1.0f;
-        [[maybe_unused]] const uint64_t k2 = f32x2(code, code);
+        // 8 bits: y 448 / max |y| in one factor.  (A row whose largest |y| counts as 1e-30 may have one past fp32's range.)
+        float to_out = mult;
+        if constexpr (OUT == kOutE4m3) {
+            to_out = amax > 1e-30f ? 448.0f / both.z : mult * (448.0f / amax);
+            if (to_out == INFINITY) to_out = 3e38f;
+        }
+        const uint64_t m2 = f32x2(to_out, to_out);
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
             const int g = first + i * step;
@@ -557,9 +561,7 @@ __global__ void __launch_bounds__(BLOCK, ring_blocks(NG, BLOCK, WARP)) block_nor
             float2 y[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                uint64_t v = mul2(z[i][e], m2);
-                if constexpr (OUT == kOutE4m3) v = mul2(v, k2);
-                y[e] = unpack2(v);
+                y[e] = unpack2(mul2(z[i][e], m2));
             }
             if constexpr (OUT == kOutBf16) {
                 *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at) =

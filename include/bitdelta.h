@@ -474,17 +474,17 @@ bd_status bd_kv_read(const bd_kv_pages* cache, const int32_t* page_table, int64_
  *     chunks; in the one for few rows (decode steps: up to 16 for each kv head
  *     of a sequence) to fp16, of 11 bits, but where one of 32 keys' products is
  *     too small for fp16's range all of theirs are rounded to bf16, of 8.
- *   - over a 4-bit cache, in the kernel for few rows: probability times the
- *     scale of its key's group, to fp16, over a power of two near the largest
- *     product of a probability of the row with a scale or lowest value (2^-25 of
- *     it still has all 11 bits, less than 2^-36 counts as 0); lowest values
- *     multiply fp32 probabilities.  In the kernel for chunks: probabilities to
- *     bf16, and v (code * scale + low) to bf16.
+ *   - over a 4-bit cache, to fp16, in the kernel for few rows: probability
+ *     times the scale of its key's group (lowest values multiply fp32
+ *     probabilities); in the one for chunks: probability, and v (code * scale +
+ *     low).  Each over a power of two near the largest product of a probability of
+ *     the row with a size (scale or lowest value) of v: 2^-25 of it still has all
+ *     11 bits, less than 2^-36 counts as 0.
  * Int8 codes enter the tensor cores exactly (K's in fp16 with q, whose rows are
  * scaled by a power of two so that bf16's 8 bits fit), and their scales
  * multiply the fp32 scores and probabilities.  4-bit codes of K enter exactly
  * too, with scales and lowest values in fp32 terms; in chunks, what lies 2^-27
- * and more below the largest element of its key may be lost.
+ * and more below the largest element of its key (or value) may be lost.
  * Cached values up to 2^80 in magnitude give the formula's result; beyond that
  * a product may overflow, and a result below 2^-125 may come out as 0.  Results do not depend on timing (no atomics).  A
  * page outside [0, n_pages), a length outside
