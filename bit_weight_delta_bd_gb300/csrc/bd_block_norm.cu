@@ -347,6 +347,10 @@ __device__ __forceinline__ uint64_t pair(uint32_t w)
 // row; with two the next row would have to be there before the one after it is
 // asked for (4096 x 8192 gated e4m3: 59.5 us with one meeting, 57.5 with two; bf16
 // with one gate and three stages 51.7 and 54.0).
+// Gates that tokens share come through the ring as well: read where they are used,
+// which leaves room for a third stage, 20011 rows of 1000 take 47.5 us for 35.8 (on
+// their way early, with the gains: 42.6).  Seven, six or five warps of a block in
+// place of eight, with a longer ring each: 37.1, 40.1 and 44.8.
 constexpr int kRingMaxStages = 8;
 constexpr int kRingWarps = 8;  // rows of a block where a row is a warp's
 
