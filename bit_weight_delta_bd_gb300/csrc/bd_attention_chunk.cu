@@ -59,8 +59,8 @@
 // scales and lowest values, and the fourth warpgroup forms tiles of fp16 numbers,
 // two warps K's and two V's (by four warps one tile after the other, what a tile
 // waits for is waited for twice as often: 1140 us for 1066, 4096 tokens over 8192
-// keys; a warp takes one group at a time, since with two or four in flight its
-// reads and writes get into the products' way: 1079 and 1167).
+// keys; a warp's loop has one group in it, with two or four 1079 and 1167: the
+// instructions of all the kernel's loops together are many).
 //   K is kept exact, since its rounding would show in the scores (by 2^-12 of the
 // sum of their products' magnitudes, where fp32 sums leave 2^-20: the
 // log-sum-exp of a row that sees few keys was off by 1e-4 to 1e-3).  A key is
@@ -83,7 +83,7 @@
 // one, which a causal row may not even see, flush the others).  Within a key or a
 // value, what lies 2^-27 below its largest element may lose bits.
 // A chunk of 4096 tokens over 8192 keys, 64/8 heads, takes 1066 us (bf16 of the
-// same values 773, int8 1110), 4096 over 8192 with heads of 64 999 (718, 1119).
+// same values 765, int8 1112), 4096 over 8192 with heads of 64 982 (718, 1118).
 // What the conversion adds to a kernel that the softmax bounds: without it 1009
 // and 935.
 #include <cuda_fp16.h>
@@ -511,8 +511,11 @@ __device__ __forceinline__ uint4 centred4(uint32_t w, __half2 scale)
 
 // The size of a key or value: of its groups' 16 scale and |lowest value| the
 // largest, as the bits of a bf16 number whose exponent e bounds its elements by
-// 2^(e + 2).  One that is not finite, or below 2^-98 (a vector of zeros has scales
-// of 2^-104), has no say: 0.
+// 2^(e + 2).  From kNotFinite on there is something that is not finite among them;
+// a size below 2^-98 (a vector of zeros has scales of 2^-104) has no say: 0.
+constexpr uint32_t kNotFinite = 0x7F80u;
+__device__ __forceinline__ uint32_t size_of(uint32_t w) { return max((w & 0xFFFFu) + (4u << 7), w >> 16); }
+
 template <int PAIRS>
 __device__ __forceinline__ uint32_t pairs_size(const uint8_t* pairs, int key)
 {
@@ -524,9 +527,21 @@ __device__ __forceinline__ uint32_t pairs_size(const uint8_t* pairs, int key)
         const uint2 w = *reinterpret_cast<const uint2*>(pairs + key * 8);
         most = __vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu);
     }
-    const uint32_t size = max((most & 0xFFFFu) + (4u << 7), most >> 16);
-    constexpr uint32_t kFrom = (127 - 98) << 7;
-    return size - kFrom < 0x7F80u - kFrom ? size : 0u;
+    const uint32_t size = size_of(most);
+    return size >= (127 - 98) << 7 ? size : 0u;
+}
+
+// The same of the groups that are finite.
+template <int PAIRS>
+__device__ __forceinline__ uint32_t finite_size(const uint8_t* pairs, int key)
+{
+    uint32_t size = 0;
+#pragma unroll 1
+    for (int g = 0; g < PAIRS; ++g) {
+        const uint32_t one = size_of(*reinterpret_cast<const uint32_t*>(pairs + (key * PAIRS + g) * 4) & 0x7FFF7FFFu);
+        if (one < kNotFinite) size = max(size, one);
+    }
+    return size >= (127 - 98) << 7 ? size : 0u;
 }
 
 // What converted values of a size with exponent e are multiplied by is 2^(kTopExp
@@ -971,7 +986,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
                     far_v = ks[2] == 0.0f;
                     cs = far_v ? 1.0f : fmaxf(back == 0.0f ? c : c * back, 1e-30f);
                 }
-                if (INT4 && (back == 0.0f || far_v)) {
+                if (INT4 && __builtin_expect(back == 0.0f || far_v, 0)) {
                     // keys or values far apart (rare, and a pass of its own through tensor memory, so that the usual one
                     // has no second form): each key's factor; with the values', the scores are in units of log2
                     const float c = fabsf(a.scale) * kLog2e * unit;
@@ -1040,7 +1055,10 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
                 const float mu = INT4 ? fmaf(mt, cs, v_exp) : mt;
                 // the first step sets the maximum; later it moves when it has grown by kLag
                 const bool grow = mu > m && (mu - m) * cm > S::kLag;
-                if (__any_sync(0xffffffffu, grow || (INT4 && far_v))) {
+                // (the kernel is larger than the cache for its instructions: what is rare lies out of the way, 284 -> 276 us
+                // for the mixed chunks with 4 bits)
+                const bool any = __any_sync(0xffffffffu, grow || (INT4 && far_v));
+                if (INT4 ? __builtin_expect(any, 0) : any) {
                     const float f = !grow ? 1.0f : m == -INFINITY ? 0.0f : ex2((m - mu) * cm);
                     if (grow) m = mu;
                     l *= f;
@@ -1385,26 +1403,27 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
                     if (!(ok = warp_wait(&sh.abort, &sh.raw_full[raw], raw_phase))) break;
                     // the sizes of the tile's keys (values), by each of the two warps for itself, four keys a lane (by a
                     // warp that has no other work, which is late then, the chunk of 4096 over 8192 keys takes 100 us more)
-                    uint32_t size[4], most = 0, least = 0xFFFFu;
+                    uint32_t most = 0, least = 0xFFFFu;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int key = 32 * k + lane;
-                        size[k] = key < valid ? pairs_size<DIM / 32>(pairs, key) : 0u;
-                        most = max(most, size[k]);
-                        least = min(least, size[k] ? size[k] : 0xFFFFu);
+                        const uint32_t size = key < valid ? pairs_size<DIM / 32>(pairs, key) : 0u;
+                        most = max(most, size);
+                        least = min(least, size ? size : 0xFFFFu);
                     }
                     most = __reduce_max_sync(0xffffffffu, most);
                     least = __reduce_min_sync(0xffffffffu, least);
                     const int from = is_v ? kLeastV : kLeastK;
-                    const bool far = most != 0 && (least >> 7) + kFar < (most >> 7);
+                    const bool far = most >= kNotFinite || (most != 0 && (least >> 7) + kFar < (most >> 7));
                     const int e = size_exp(most, from);
                     // The factors' slot has been read when it is written again, four tiles later: the place that the
                     // tile's K goes to held K of at most three tiles before it (or a later V), which has been multiplied,
                     // after P of the tile before that one.
                     if (!(ok = warp_wait(&sh.abort, &sh.empty[k_place()], (is_v && buf == 0 ? phase : phase ^ 1)))) break;
-                    if (far) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) by_key[32 * k + lane] = static_cast<float>(size_exp(size[k], from));
+                    if (__builtin_expect(far, 0)) {  // (what is not finite says nothing of the others)
+#pragma unroll 1
+                        for (int key = lane; key < kTile; key += 32)
+                            by_key[key] = static_cast<float>(size_exp(key < valid ? finite_size<DIM / 32>(pairs, key) : 0u, from));
                     }
                     // what takes K's factor back (0: by key); V's exponent, which P gets, and what takes it out of the sum
                     // of P (0: by key)

@@ -82,6 +82,84 @@ def test_small_probabilities(dev, n_new, gap):  # noqa: F811
     within(out, want[0], bound + ref.half_ulp_bf16(want[0].abs() + bound), "attention")
 
 
+# ------------------------------------------------------------------------------- sizes far apart
+
+SIZES = [  # of token j's key and value, and the scale
+    (lambda j: 2.0 ** (20 * (j % 3) - 20), lambda j: 1.0, 0.02),
+    (lambda j: 1.0, lambda j: 2.0 ** (20 * (j % 3) - 20), 0.1),
+    (lambda j: 2.0 ** (-30 if j % 5 else 0), lambda j: 2.0 ** (30 if j % 7 else -40), 0.1),
+    (lambda j: 1.0, lambda j: 2.0 ** (60 if 100 <= j < 110 else -60), 0.1),  # a tile of each kind
+    (lambda j: 1.0, lambda j: 2.0 ** (-60 if j < 128 else 60 if j < 256 else 0), 0.1)]
+
+
+@pytest.mark.parametrize("sizes", range(len(SIZES)))
+@pytest.mark.parametrize("n_new,kv_len,n_q,n_kv,dim,page", [
+    ([1, 2], [300, 129], 8, 2, 64, 16), ([300], [333], 8, 2, 128, 16), ([40, 130], [300, 200], 4, 2, 64, 64),
+    ([20, 5], [400, 77], 4, 2, 128, 32)])
+def test_magnitudes_in_every_kernel(dev, n_new, kv_len, n_q, n_kv, dim, page, sizes):  # noqa: F811
+    """Few rows, pairs, single blocks: keys and values of neighbouring tokens, and of tiles, far apart.  (fp16's bits
+    reach 2^-25 below a row's largest product; the bound is 8 bits of all products together.)"""
+    key_of, value_of, scale = SIZES[sizes]
+    c = att.scaled_cache(n_new, kv_len, n_kv, dim, page, 7, key_of, value_of)
+    att.run_attention(dev, n_new, kv_len, n_q, n_kv, dim, page, seed=7, scale=scale, c=c, coded_rel=ref.U16,
+                      value_rel=2 * ref.U16)
+
+
+@pytest.mark.parametrize("what", [2.0 ** 40, 2.0 ** 80, -2.0 ** 80])
+@pytest.mark.parametrize("n_new,n_q,dim", [(2, 8, 128), (40, 8, 128), (300, 8, 128), (40, 4, 64)])
+def test_hidden_values_of_any_size(dev, n_new, n_q, dim, what):  # noqa: F811
+    """Values that a causal row does not see, however large, leave it what it was to the bounds of its own."""
+    length = n_new + 30
+    c = ref4.paged([n_new], [length], 2, dim, 16, 3)
+    pg, at = c["table"][0, (length - 1) // 16].long(), (length - 1) % 16
+    c["vs"][pg, :, at, :, 1] = what  # the last token's, which its own rows alone see
+    c["vals"]["v"][0][-1] = ref4.values(c["v"][pg, :, at], c["vs"][pg, :, at])
+    att.run_attention(dev, [n_new], [length], n_q, 2, dim, 16, seed=3, c=c, coded_rel=ref.U16, value_rel=2 * ref.U16)
+
+
+@pytest.mark.parametrize("what", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("part", [0, 1])
+@pytest.mark.parametrize("n_new,max_new,dim", [([1, 1], 1, 64), ([40, 1], 40, 64), ([300, 2], 300, 128), ([30, 1], 30, 128)])
+def test_values_that_are_not_finite_stay_in_their_group(dev, n_new, max_new, dim, part, what):  # noqa: F811
+    """A scale or lowest value of a seen value that is not finite reaches the dims of its group, of the rows that see
+    it; the key's other groups, larger than every other token's, are what they were."""
+    lens = [n + 90 for n in n_new]
+    c = ref4.paged(n_new, lens, 2, dim, 16, 3)
+    pg, at = c["table"][0, 10 // 16].long(), 10 % 16  # key 10, before every new token
+    c["vs"][pg, 1, at, :, 1] = 100.0
+    c["vals"]["v"][0][10] = ref4.values(c["v"][pg, :, at], c["vs"][pg, :, at])
+    base, q, _, _, off, ln = att.run_attention(dev, n_new, lens, 4, 2, dim, 16, seed=3, c=c, max_new=max_new,
+                                               coded_rel=ref4.U11, value_rel=2 * ref.U16)
+    c["vs"][pg, 1, at, 1, part] = what
+    cache, table = cache_on(c, dev)
+    out = torch.empty_like(base)
+    ws = bd.new_workspace(bd.bd_attention_workspace_size(sum(n_new), 2, 4, 2, dim), dev)
+    bd.bd_attention(q, off, cache, table, ln, dim ** -0.5, max_new, out, ws)
+    hit = torch.zeros_like(base, dtype=torch.bool)
+    hit[: n_new[0], 2:, 32:64] = True
+    assert not out[hit].isfinite().any()
+    # (another factor may have been taken for the tile, or reference for the row: a rounding's width apart)
+    near = (out[~hit].float() - base[~hit].float()).abs()
+    assert bool((near <= 2.0 ** -7 * base[~hit].float().abs() + 2.0 ** -9).all())
+
+
+# ------------------------------------------------------------------------------- the ends of the sizes
+
+def test_a_hint_of_no_new_tokens(dev):  # noqa: F811
+    att.run_attention(dev, [1, 40], [300, 200], 8, 2, 128, 16, seed=5, max_new=0, coded_rel=ref4.U11, value_rel=2 * ref.U16)
+
+
+def test_as_many_heads_as_there_may_be(dev):  # noqa: F811
+    """1024 kv heads: written, read back, attended to by few rows and by a chunk."""
+    for T in (1, 40):
+        run, need, (_, _, qo, out, ko, vo) = layer(dev, T, [T], [T + 3], 2048, 1024, 64, 16)
+        ws = bd.new_workspace(need, dev)
+        run(ws)
+        assert bd.bd_check_async(ws) == bd.BD_OK
+        want = ref.attention(qo[:, ::194].cpu(), [0, T], [ko[:, ::97].cpu()], [vo[:, ::97].cpu()], [T + 3], 0.125, True)[0]
+        assert float((out[:, ::194].double().cpu() - want).norm() / want.norm()) <= 0.02
+
+
 # ------------------------------------------------------------------------------- past 32 bits
 
 def test_cache_past_32_bits(dev):  # noqa: F811
