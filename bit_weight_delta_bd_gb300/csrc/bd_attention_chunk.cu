@@ -83,7 +83,7 @@
 // one, which a causal row may not even see, flush the others).  Within a key or a
 // value, what lies 2^-27 below its largest element may lose bits.
 // A chunk of 4096 tokens over 8192 keys, 64/8 heads, takes 1066 us (bf16 of the
-// same values 765, int8 1112), 4096 over 8192 with heads of 64 982 (718, 1118).
+// same values 765, int8 1112), 4096 over 8192 with heads of 64 975 (718, 1118).
 // What the conversion adds to a kernel that the softmax bounds: without it 1009
 // and 935.
 #include <cuda_fp16.h>
@@ -578,15 +578,13 @@ __device__ __forceinline__ void convert_v4(const uint8_t* src, const uint8_t* pa
         const uint4 c = *reinterpret_cast<const uint4*>(src + swizzled_codes<DIM / 2>(key, g));
         const uint32_t pair = *reinterpret_cast<const uint32_t*>(pairs + (key * PAIRS + first + g) * 4);
         const float fk = f != 0.0f ? f : exp2_int(kTopExp - static_cast<int>(by_key[key]));
-        const __half2 scale = __float2half2_rn(__uint_as_float(pair << 16) * fk);
-        const __half2 low = __float2half2_rn(__uint_as_float(pair & 0xFFFF0000u) * fk);
+        __half2 scale = __float2half2_rn(__uint_as_float(pair << 16) * fk);
+        __half2 low = __float2half2_rn(__uint_as_float(pair & 0xFFFF0000u) * fk);
+        if (key >= valid) scale = low = __float2half2_rn(0.0f);
         const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint4 v = values4(w[j], scale, low);
-            if (key >= valid) v = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(half + key * 128 + (((4 * (g & 1) + j) ^ (key & 7)) << 4)) = v;
-        }
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(half + key * 128 + (((4 * (g & 1) + j) ^ (key & 7)) << 4)) = values4(w[j], scale, low);
     }
 }
 
