@@ -410,11 +410,10 @@ def bd_block_norm(x, residual, gain, eps, out, ws, residual_out=None, post_gain=
         V = len(gain_list)
         if post_gain is not None and len(post_gain_list) != V:
             raise ValueError("gain_list and post_gain_list differ in length")
-        table = _row_ptrs(gain_list, d, "gain", dev)
-        tab = table.buffer_info()[0] if V else None
-        if post_gain is not None:
-            post_table = _row_ptrs(post_gain_list, d, "post_gain", dev)
-            post_tab = post_table.buffer_info()[0] if V else None
+        table = _row_ptrs(gain_list if post_gain is None else [*gain_list, *post_gain_list], d, "gain", dev)
+        if V:
+            tab = table.buffer_info()[0]
+            post_tab = None if post_gain is None else tab + 8 * V
     out_dtype = _OUT_DTYPES.get(out.dtype)
     if out_dtype is None:
         raise ValueError(f"out has dtype {out.dtype}, expected bfloat16, float32 or float8_e4m3fn")

@@ -154,7 +154,7 @@ struct ChunkShared {
     uint64_t full[kMaxBufs], empty[kMaxBufs];    // bf16 tiles (full: of both CTAs, in the even one)
     uint64_t landed[kMaxBufs];                   // this CTA's part of them (pairs; int8: the odd one's)
     uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];     // tiles of codes
-    uint64_t sc_full[kMaxScales], sc_empty[kMaxScales];  // scales
+    uint64_t sc_full[kMaxScales], sc_empty[kMaxScales];  // scales (4 bits: the factors of V)
     uint64_t q_full[2], o_full[2];
     uint64_t s_full[2][2], p_full[2][2], pv_done[2];  // by query tile (and place)
     uint64_t done;

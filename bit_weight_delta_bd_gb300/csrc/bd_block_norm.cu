@@ -607,7 +607,7 @@ cudaError_t launch_ring(const BlockNormArgs& a, int threads, int sm_count, cudaS
     const int per_sm = 2048 / threads < by_registers ? 2048 / threads : by_registers;
     const int rows = WARP ? kRingWarps : 1;
     const size_t stage = static_cast<size_t>(p.row_bytes) * (a.gate && a.gate_rows > 1 ? 3 : 2) * rows;
-    const size_t room = (228u * 1024u) / per_sm - 3072u;
+    const size_t room = (228u * 1024u) / per_sm - 3u * 1024u;
     p.stages = static_cast<int>(room / stage);
     if (p.stages > kRingMaxStages) p.stages = kRingMaxStages;
     if (p.stages < 2) return cudaErrorInvalidConfiguration;  // (rows that long do not come here)
