@@ -69,9 +69,9 @@ def run_attention(dev, n_new, kv_len, n_q, n_kv, dim, page, causal=True, seed=0,
     assert bd.bd_check_async(ws) == bd.BD_OK
     want = ref4.attention(q, q_off, c, scale, causal)
     few = most * (n_q // n_kv) <= 16
-    # few rows: probability times scale enters its product in fp16; chunks: probabilities and V's values in bf16
+    # few rows: probability times scale enters its product in fp16; chunks: probabilities and V's values in fp16
     b_out, b_lse = ref4.bounds(want, dim, max(kv_len + [1]), (ref4.U11 if few else 0.0) if coded_rel is None else coded_rel,
-                               (0.0 if few else 2 * ref.U16) if value_rel is None else value_rel)
+                               (0.0 if few else 2 * ref4.U11) if value_rel is None else value_rel)
     within(out, want[0], b_out, "attention")
     assert torch.equal(lse.cpu() == -math.inf, want[1] == -math.inf)
     fin = want[1] > -math.inf
