@@ -1004,18 +1004,30 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
                 // values may amount to.  It lags: it moves when that passes 2^15, which after the first keys is rare, so
                 // that the lanes need not tell one another their scores
                 const uint8_t* v_pairs = pairs + (S::kTile + slice + g) * S::kPairBytes;  // keys 16 b + 8 j + g from here on
-                float size[2][2];  // at or above scale and lowest value of this lane's group, and 2^-65
+                // A key's size: at or above the scale and the lowest value of each of its groups, and 2^-65.  A row's
+                // probabilities multiply the scales of all groups, so all have a say: a lane looks at one key of the
+                // slice, and the lanes tell one another.  (32 decode steps up to 8193 keys 62.7 us; 61.1 where a lane
+                // looks at one group of its own keys, which leaves its rows' products with the others unwatched: they
+                // pass fp16's range.)  bf16's bits are in the order of the magnitudes; what is not finite counts as
+                // infinite, so that its key is looked at again below.
+                constexpr uint32_t kLeastSize = (127 - 65) << 7, kInf = 0x7F80u;
+                const uint8_t* my_pairs = pairs + (S::kTile + slice + lane) * S::kPairBytes;
+                float size[2][2];
+                {
+                    uint32_t w[kGroups];
+                    load_pairs<kGroups>(my_pairs, w);
+                    uint32_t most = w[0] & 0x7FFF7FFFu;
+#pragma unroll
+                    for (int k = 1; k < kGroups; ++k) most = __vmaxu2(most, w[k] & 0x7FFF7FFFu);
+                    const float mine =
+                        __uint_as_float(min(max(max(most & 0xFFFFu, most >> 16), kLeastSize), kInf) << 16);
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) size[b][j] = __shfl_sync(0xffffffffu, mine, 16 * b + 8 * j + g);
+                }
                 float p[NT][2][4];
                 bool grow = false;
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint32_t w = *reinterpret_cast<const uint32_t*>(v_pairs + (16 * b + 8 * j) * S::kPairBytes +
-                                                                              4 * (q4 & (kGroups - 1)));
-                        // (the scale's bits under the lowest value's add little)
-                        size[b][j] = max3(2.7e-20f, fabsf(pair_scale(w)), fabsf(__uint_as_float(w)));
-                    }
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -1032,21 +1044,19 @@ __global__ void __launch_bounds__(kMmaThreads, mma_blocks_per_sm(8 * NT, DIM, KI
                     }
                 if (__any_sync(0xffffffffu, grow)) {
                     // (values that are not finite say nothing of the others of their key: those are looked at here)
+                    uint32_t w[kGroups], big = kLeastSize;
+                    load_pairs<kGroups>(my_pairs, w);
+#pragma unroll
+                    for (int k = 0; k < kGroups; ++k) {
+                        const uint32_t x = w[k] & 0x7FFFu, y = w[k] >> 16 & 0x7FFFu;
+                        if (x < kInf) big = max(big, x);
+                        if (y < kInf) big = max(big, y);
+                    }
+                    const float mine = log2f(__uint_as_float(big << 16));
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            float big = 2.7e-20f;
-                            uint32_t w[kGroups];
-                            load_pairs<kGroups>(v_pairs + (16 * b + 8 * j) * S::kPairBytes, w);
-#pragma unroll
-                            for (int k = 0; k < kGroups; ++k) {
-                                const float x = fabsf(pair_scale(w[k])), y = fabsf(__uint_as_float(w[k]));
-                                if (x < INFINITY) big = fmaxf(big, x);
-                                if (y < INFINITY) big = fmaxf(big, y);
-                            }
-                            size[b][j] = log2f(big);
-                        }
+                        for (int j = 0; j < 2; ++j) size[b][j] = __shfl_sync(0xffffffffu, mine, 16 * b + 8 * j + g);
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll

@@ -1,0 +1,161 @@
+"""Attention over a 4-bit cache whose values differ in size from group to group
+of one token, while scores climb along the cache (GPU): a row of the query, alone
+among its kv head's, meets keys that lie above all before them, and one group of
+32 elements outweighs the others, or is nothing.  Every row and every group has
+its turn: the pairs of sequence and kv head take them one after the other.
+
+Bounds, beside those of int4_oracle.py (roundings to 11 bits).  Few rows: a
+product of probability and scale is rounded to a multiple of 2^-24 where the
+row's largest product with a scale or lowest value is 2^11 or more: off by 2^-36
+of that at most, 15 times for the code.  Chunks: probabilities likewise, times
+values of up to 4 sizes; scales, lowest values and values over the size's power
+of two, times 2^13, are rounded to multiples of 2^-24, 17 / 2 of them off at most,
+2^-33.9 of the size.  Both are less than 2^-33 of the largest probability times
+the largest size, max(16 scale, |lowest value|), for each key."""
+import math
+
+import pytest
+import torch
+
+import int4_oracle as ref4
+import test_int4_attention as att
+from bit_weight_delta_bd_gb300 import bitdelta as bd
+from test_int4_attention import cache_on, dev, gen, within  # noqa: F401  (dev is a fixture)
+from test_int4_paths import SIZES
+
+pytestmark = pytest.mark.gpu
+
+
+def refresh(c):
+    """The values that the cache's codes and pairs stand for, after they were changed."""
+    page, c["steps"] = c["k"].shape[2], []
+    for s, length in enumerate(c["kv_len"]):
+        at = torch.arange(length)
+        pg, off = c["table"][s].long()[at // page], at % page
+        for name in "kv":
+            pair = c[name + "s"][pg, :, off]
+            c["vals"][name][s] = ref4.values(c[name][pg, :, off], pair)
+            if name == "k":
+                p = pair.double().abs()
+                c["steps"].append((15 * p[..., 0] + p[..., 1]).repeat_interleave(32, -1))
+
+
+def climb(c, q, q_off, scale, keys, first=0):
+    """Puts keys along a row's query into the cache: pair i of (sequence, kv head) takes row i + first; keys[j] lies so
+    much above what the others reach.  Returns the row's number past each turn of the rows, by pair."""
+    n_kv, page = c["k"].shape[1:3]
+    group = q.shape[1] // n_kv
+    turns = {}
+    for s, length in enumerate(c["kv_len"]):
+        rows = (q_off[s + 1] - q_off[s]) * group
+        for h in range(n_kv):
+            i = s * n_kv + h + first
+            r = i % rows if rows else 0
+            turns[s, h] = i // rows if rows else 0
+            for j, above in keys.items():
+                if not rows or j >= length - (q_off[s + 1] - q_off[s]):
+                    continue
+                x = q[q_off[s] + r // group, h * group + r % group].float()
+                byte, pair = ref4.codes(x * ((3.5 + above) / (abs(scale) * float(x @ x))))
+                pg, at = c["table"][s, j // page].long(), j % page
+                c["k"][pg, h, at], c["ks"][pg, h, at] = byte, pair
+    return turns
+
+
+def attend(dev, c, q, n_new, scale, max_new=None):  # noqa: F811
+    """Runs the call and holds it to the bounds of the module's head."""
+    lens, (T, n_q, dim) = c["kv_len"], q.shape
+    cache, table = cache_on(c, dev)
+    q_off = [0]
+    for n in n_new:
+        q_off.append(q_off[-1] + n)
+    out, lse = torch.empty(T, n_q, dim, device=dev, dtype=torch.bfloat16), torch.empty(T, n_q, device=dev)
+    ws = bd.new_workspace(bd.bd_attention_workspace_size(T, len(lens), n_q, cache.n_kv, dim), dev)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)  # noqa: E731
+    most = max(n_new) if max_new is None else max_new
+    bd.bd_attention(q.to(dev), i32(q_off), cache, table, i32(lens), scale, most, out, ws, lse=lse)
+    assert bd.bd_check_async(ws) == bd.BD_OK
+    want = ref4.attention(q, q_off, c, scale, True)
+    few = most * (n_q // cache.n_kv) <= 16
+    mixed = not few and min(n_new) * (n_q // cache.n_kv) <= 16  # either kernel may take its sequences
+    b_out, b_lse = ref4.bounds(want, dim, max(lens), ref4.U11 if few or mixed else 0.0, 0.0 if few else 2 * ref4.U11)
+    for s, length in enumerate(lens):
+        rows = slice(q_off[s], q_off[s + 1])
+        if not length or q_off[s] == q_off[s + 1]:
+            continue
+        at = torch.arange(length)
+        pair = c["vs"][c["table"][s].long()[at // c["v"].shape[2]], :, at % c["v"].shape[2]].double().abs()
+        size = torch.maximum(16 * pair[..., 0], pair[..., 1]).amax(-1)  # [len][n_kv]
+        k = c["vals"]["k"][s].double().repeat_interleave(n_q // cache.n_kv, 1)
+        z = torch.einsum("thd,jhd->thj", q[rows].double(), k) * scale
+        see = length - (q_off[s + 1] - q_off[s]) + torch.arange(q_off[s + 1] - q_off[s])
+        z = z.masked_fill(at[None, None] > see[:, None, None], -math.inf)
+        p = torch.exp(z - want[1][rows][..., None]).nan_to_num(0.0)  # (a row that sees no key)
+        big = (p * size.T.repeat_interleave(n_q // cache.n_kv, 0)[None]).amax(-1)
+        if not few:  # a tile's values share their factor
+            big = p.amax(-1) * size.amax(0).repeat_interleave(n_q // cache.n_kv)[None]
+        b_out[rows] += (1 + 2.0 ** -7) * length * 2.0 ** -33 * big[..., None]
+    within(out, want[0], b_out, "attention")
+    assert torch.equal(lse.cpu() == -math.inf, want[1] == -math.inf)
+    fin = want[1] > -math.inf
+    within(lse.cpu()[fin], want[1][fin], b_lse[fin], "log-sum-exp")
+
+
+# what the group whose turn it is is times, and what the others are; the lowest values as they are or 0
+KINDS = [(2.0, 1.0, True), (2.0, 1.0, False), (8.0, 1.0, False), (16.0, 1.0, True), (2.0 ** 7, 1.0, True),
+         (2.0 ** 7, 1.0, False), (2.0 ** 12, 1.0, True), (2.0 ** 20, 1.0, False), (0.0, 1.0, True), (1.0, 0.0, True),
+         (1.0, 0.0, False), (2.0 ** -20, 1.0, True)]
+# keys that lie above the rest, and by how much (natural units): for the first of a block's four warps that takes
+# them, past its first 32 keys, for other blocks of a cluster, and past 1024 keys of a dealt cache
+KEYS = {40: 5.0, 100: 2.0, 129: 3.6, 135: 9.0, 170: 5.5, 200: 4.0, 230: 12.0, 300: 6.0, 390: 4.5, 500: 8.0, 650: 10.0,
+        777: 3.9, 1100: 5.0, 1290: 7.0, 1700: 11.0, 1950: 12.0} | {2100 + 139 * i: 4.0 + i % 9 for i in range(24)}
+FORMS = [
+    ([1] * 4, [333, 700, 1300, 2000], 4, 4, 64, 16), ([1] * 4, [333, 700, 1300, 2000], 4, 4, 128, 64),  # 1 row, clusters
+    ([3, 1, 3], [2000, 260, 900], 4, 4, 128, 16), ([1] * 3, [2000, 260, 900], 12, 4, 64, 32),  # 3 rows
+    ([1] * 4, [333, 700, 1300, 2000], 64, 8, 128, 16), ([1] * 4, [150, 300, 5000, 600], 64, 8, 128, 128),  # 8 rows
+    ([1] * 4, [150, 300, 5000, 600], 32, 4, 64, 16),
+    ([2] * 4, [2000, 140, 300, 1000], 64, 8, 128, 16), ([4, 2, 4], [2000, 300, 900], 16, 4, 64, 32),  # 16 rows
+    ([1] * 4, [5000, 300, 900, 2000], 64, 4, 128, 32)]
+DEALT = [  # several tiles to a block
+    ([1] * 4, [4400, 3000, 4100, 2500], 32, 16, 128, 64), ([1] * 4, [4400, 3000, 4100, 2500], 16, 16, 64, 16),
+    ([4] * 4, [4400, 3000, 4100, 2500], 64, 16, 64, 128)]
+CHUNKS = [
+    ([20, 40], [400, 1300], 8, 2, 64, 16), ([20, 33], [700, 1300], 4, 2, 128, 32), ([300], [1300], 8, 4, 128, 16),
+    ([300, 1, 1, 40, 1], [700, 1500, 300, 777, 900], 16, 2, 128, 16), ([1, 200, 1, 1], [2000, 700, 300, 500], 8, 2, 64, 64)]
+LONG = [  # several tiles to a block, and the single tokens' dealt so
+    ([40] * 6, [1500, 1400, 1600, 1700, 900, 1100], 8, 8, 64, 16), ([40] * 6, [1500, 1400, 1600, 1700, 900, 1100], 8, 8, 128, 64),
+    ([270] * 3, [1500, 1700, 900], 8, 8, 128, 32),
+    ([150, 1, 1, 1], [1700, 4400, 3000, 4100], 32, 16, 128, 16), ([150, 1, 1, 1], [1700, 4400, 3000, 4100], 16, 16, 64, 32)]
+
+
+@pytest.mark.parametrize("n_new,kv_len,n_q,n_kv,dim,page,kind", [
+    (*form, kind) for i, form in enumerate(FORMS + DEALT + CHUNKS + LONG) for kind in range(i % 2, len(KINDS), 2)])
+def test_groups_apart_while_scores_climb(dev, n_new, kv_len, n_q, n_kv, dim, page, kind):  # noqa: F811
+    times, others, lows = KINDS[kind]
+    c = ref4.paged(n_new, kv_len, n_kv, dim, page, 31 + kind)
+    q = torch.randn(sum(n_new), n_q, dim, generator=gen(kind)).to(torch.bfloat16)
+    q_off = [sum(n_new[:s]) for s in range(len(n_new) + 1)]
+    scale = dim ** -0.5 * (-1 if kind % 5 == 4 else 1)
+    turns = climb(c, q if scale > 0 else -q, q_off, scale, KEYS, first=kind)
+    for (s, h), turn in turns.items():
+        pg = c["table"][s, : -(-kv_len[s] // page)].long()
+        f = torch.full((dim // 32, 1), others)
+        f[(turn + kind) % (dim // 32)] = times
+        c["vs"][pg, h] = (c["vs"][pg, h].float() * f).to(torch.bfloat16)
+    if not lows:
+        c["vs"][..., 1] = 0.0  # (values that are all of one sign)
+        for s, length in enumerate(kv_len):  # past the lengths NaN again
+            if length % page:
+                c["vs"][c["table"][s, length // page].long(), :, length % page:] = math.nan
+    refresh(c)
+    attend(dev, c, q, n_new, scale)
+
+
+@pytest.mark.parametrize("sizes", range(len(SIZES)))
+@pytest.mark.parametrize("n_new,kv_len,n_q,n_kv,dim,page", DEALT + LONG)
+def test_sizes_apart_from_tile_to_tile(dev, n_new, kv_len, n_q, n_kv, dim, page, sizes):  # noqa: F811
+    """Keys and values of neighbouring tokens, and of tiles, far apart, where a block takes several tiles."""
+    key_of, value_of, scale = SIZES[sizes]
+    c = att.scaled_cache(n_new, kv_len, n_kv, dim, page, 7, key_of, value_of)
+    q = torch.randn(sum(n_new), n_q, dim, generator=gen(sizes)).to(torch.bfloat16)
+    attend(dev, c, q, n_new, scale)
