@@ -553,9 +553,12 @@ constexpr int kLeastV = -66;  // smaller sizes count as this: the sum of the pro
 
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((127 + e) << 23); }
 
-__device__ __forceinline__ int size_exp(uint32_t size, int from)
+// The exponent that a size is taken for.  Nothing (a size of 0) has no size to leave room for: values of nothing count as
+// the smallest, so that the row's reference does not follow them; keys of nothing are 0 over any factor.
+__device__ __forceinline__ int size_exp(uint32_t size, bool is_v)
 {
-    return size ? min(max(static_cast<int>(size >> 7) - 127, from), 100) : 0;
+    if (!size) return is_v ? kLeastV : 0;
+    return min(max(static_cast<int>(size >> 7) - 127, is_v ? kLeastV : kLeastK), 100);
 }
 
 // A tile of V's 4-bit codes with their scales and lowest values as a tile of fp16
@@ -1411,9 +1414,8 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
                     }
                     most = __reduce_max_sync(0xffffffffu, most);
                     least = __reduce_min_sync(0xffffffffu, least);
-                    const int from = is_v ? kLeastV : kLeastK;
                     const bool far = most >= kNotFinite || (most != 0 && (least >> 7) + kFar < (most >> 7));
-                    const int e = size_exp(most, from);
+                    const int e = size_exp(most, is_v);
                     // The factors' slot has been read when it is written again, four tiles later: the place that the
                     // tile's K goes to held K of at most three tiles before it (or a later V), which has been multiplied,
                     // after P of the tile before that one.
@@ -1421,7 +1423,7 @@ __global__ void __launch_bounds__(ChunkShape<DIM, KIND, PAIR>::kThreads, 1)
                     if (__builtin_expect(far, 0)) {  // (what is not finite says nothing of the others)
 #pragma unroll 1
                         for (int key = lane; key < kTile; key += 32)
-                            by_key[key] = static_cast<float>(size_exp(key < valid ? finite_size<DIM / 32>(pairs, key) : 0u, from));
+                            by_key[key] = static_cast<float>(size_exp(key < valid ? finite_size<DIM / 32>(pairs, key) : 0u, is_v));
                     }
                     // what takes K's factor back (0: by key); V's exponent, which P gets, and what takes it out of the sum
                     // of P (0: by key)

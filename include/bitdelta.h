@@ -478,8 +478,10 @@ bd_status bd_kv_read(const bd_kv_pages* cache, const int32_t* page_table, int64_
  *     times the scale of its key's group (lowest values multiply fp32
  *     probabilities); in the one for chunks: probability, and v (code * scale +
  *     low).  Each over a power of two near the largest product of a probability of
- *     the row with a size (scale or lowest value) of v: 2^-25 of it still has all
- *     11 bits, less than 2^-36 counts as 0.
+ *     the row with the size of its key's v, in chunks of all v of a tile of 128
+ *     keys unless they lie more than 2^16 apart: 2^-25 of it still has all 11 bits,
+ *     less than 2^-36 counts as 0.  The size is the largest of the groups' scales
+ *     and lowest values, finite ones, and 2^-65 at least.
  * Int8 codes enter the tensor cores exactly (K's in fp16 with q, whose rows are
  * scaled by a power of two so that bf16's 8 bits fit), and their scales
  * multiply the fp32 scores and probabilities.  4-bit codes of K enter exactly

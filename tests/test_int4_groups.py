@@ -159,3 +159,31 @@ def test_sizes_apart_from_tile_to_tile(dev, n_new, kv_len, n_q, n_kv, dim, page,
     c = att.scaled_cache(n_new, kv_len, n_kv, dim, page, 7, key_of, value_of)
     q = torch.randn(sum(n_new), n_q, dim, generator=gen(sizes)).to(torch.bfloat16)
     attend(dev, c, q, n_new, scale)
+
+
+# ------------------------------------------------------------------------------- values of nothing
+
+@pytest.mark.parametrize("zero", ["tile", "tail", "key", "far"])
+@pytest.mark.parametrize("written", [True, False])
+@pytest.mark.parametrize("n_new,kv_len,n_q,n_kv,dim,page", [
+    ([1, 2], [300, 400], 8, 2, 128, 16), *DEALT[:1], *LONG[:3]])
+def test_zeros_among_small_values(dev, n_new, kv_len, n_q, n_kv, dim, page, zero, written):  # noqa: F811
+    """Values of 0 say nothing of the size of the others, whatever their probability: a tile of them, single ones, and
+    single ones among values far apart; as bd_rope_append writes them (a scale of 2^-104), and with scales of 0."""
+    c = ref4.paged(n_new, kv_len, n_kv, dim, page, 17)
+    q = torch.randn(sum(n_new), n_q, dim, generator=gen(4)).to(torch.bfloat16)
+    tiny = float((torch.tensor(1e-30) / torch.tensor(15.0)).to(torch.bfloat16))
+    for s, length in enumerate(kv_len):
+        at = torch.arange(length)
+        pg, off = c["table"][s].long()[at // page], at % page
+        hit = {"tile": at // 128 % 3 == 1, "tail": at >= length // 256 * 128, "key": at % 5 == 2, "far": at % 3 == 2}[zero]
+        f = torch.full((length,), 2.0 ** -40)
+        if zero == "far":
+            f[at % 3 == 1] = 2.0 ** -60
+        pair = c["vs"][pg, :, off].float() * f[:, None, None, None]
+        pair[hit] = torch.tensor([tiny if written else 0.0, 0.0])
+        c["vs"][pg, :, off] = pair.to(torch.bfloat16)
+        if written:
+            c["v"][pg[hit], :, off[hit]] = 0
+    refresh(c)
+    attend(dev, c, q, n_new, dim ** -0.5)
