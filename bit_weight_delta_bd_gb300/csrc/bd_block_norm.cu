@@ -549,11 +549,18 @@ __global__ void __launch_bounds__(BLOCK, ring_blocks(NG, BLOCK, WARP)) block_nor
             amax = max_nan(both.z * mult, 1e-30f);
             if (first == 0) a.scale[t] = amax / 448.0f;
         }
-        // 8 bits: y 448 / max |y| in one factor.  (A row whose largest |y| counts as 1e-30 may have one past fp32's range.)
+        // 8 bits: y 448 / max |y| in one factor; in two for a row so small that the one leaves fp32's range.
         float to_out = mult;
         if constexpr (OUT == kOutE4m3) {
             to_out = amax > 1e-30f ? 448.0f / both.z : mult * (448.0f / amax);
-            if (to_out == INFINITY) to_out = 3e38f;
+            if (__builtin_expect(to_out == INFINITY, 0)) {
+                const uint64_t y2 = f32x2(mult, mult);
+#pragma unroll
+                for (int i = 0; i < NG; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[i][e] = mul2(z[i][e], y2);
+                to_out = 448.0f / amax;
+            }
         }
         const uint64_t m2 = f32x2(to_out, to_out);
 #pragma unroll
