@@ -397,7 +397,8 @@ __global__ void __launch_bounds__(BLOCK, ring_blocks(NG, BLOCK, WARP)) block_nor
     // by turns: a warp may still read the last row's; and the one of a meeting that the other lies between
     __shared__ float4 red[3][32];
     __shared__ uint64_t full_all[kRows][kRingMaxStages];
-    __shared__ int given_up;
+    __shared__ volatile int given_up;
+    __shared__ int64_t unfilled[kRows];  // given up: the first row that was not asked for any more
     const BlockNormArgs& a = p.a;
     const int which = WARP ? threadIdx.x >> 5 : 0;
     const int first = WARP ? threadIdx.x & 31 : threadIdx.x, step = WARP ? 32 : blockDim.x;
@@ -412,6 +413,7 @@ __global__ void __launch_bounds__(BLOCK, ring_blocks(NG, BLOCK, WARP)) block_nor
     grid_launch_dependents();
     if (first == 0) {
         for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
+        unfilled[which] = a.T;
         if (which == 0) given_up = 0;
         fence_mbarrier_init();
     }
@@ -428,9 +430,14 @@ __global__ void __launch_bounds__(BLOCK, ring_blocks(NG, BLOCK, WARP)) block_nor
         }
         return i;
     };
-    // by the row's first thread: row t into stage s
+    // by the row's first thread: row t into stage s.  Not once a wait was given up, which this thread knows of before it
+    // gets to a stage whose copies may still be on their way.
     const auto fill = [&](int64_t t, int s, int64_t gate_at) {
         if (t >= a.T) return;
+        if (given_up) {
+            if (t < unfilled[which]) unfilled[which] = t;
+            return;
+        }
         uint8_t* dst = ring + static_cast<size_t>(s) * stage_bytes;
         mbar_arrive_expect_tx(&full[s], stage_bytes);
         bulk_g2s(dst, a.x + t * a.d, p.row_bytes, &full[s]);
@@ -600,8 +607,12 @@ __global__ void __launch_bounds__(BLOCK, ring_blocks(NG, BLOCK, WARP)) block_nor
             phase ^= 1;
         }
     }
-    // given up: leave only when the copies in flight have landed
-    if (given_up && first < p.stages) mbar_wait_bounded(&full[first], first < stage ? phase : phase ^ 1);
+    // given up: leave only when the copies in flight have landed, each stage's last ones
+    __syncthreads();
+    if (given_up && first < p.stages && t0 < a.T) {
+        const int64_t rows = (unfilled[which] - t0 + rows_step - 1) / rows_step;  // that were, in the order of the stages
+        if (rows > first) mbar_wait_bounded(&full[first], (rows - first - 1) / p.stages & 1);
+    }
 }
 
 template <int NG, int BLOCK, bool WARP>
