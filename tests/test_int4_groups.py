@@ -62,10 +62,11 @@ def climb(c, q, q_off, scale, keys, first=0):
     return turns
 
 
-def attend(dev, c, q, n_new, scale, max_new=None):  # noqa: F811
-    """Runs the call and holds it to the bounds of the module's head."""
+def attend(dev, c, q, n_new, scale, max_new=None, given=None, hit=None):  # noqa: F811
+    """Runs the call and holds it to the bounds of the module's head; with another cache than the definition's, but for
+    the elements that it may hit, which it has to make infinite or NaN."""
     lens, (T, n_q, dim) = c["kv_len"], q.shape
-    cache, table = cache_on(c, dev)
+    cache, table = cache_on(given or c, dev)
     q_off = [0]
     for n in n_new:
         q_off.append(q_off[-1] + n)
@@ -95,7 +96,11 @@ def attend(dev, c, q, n_new, scale, max_new=None):  # noqa: F811
         if not few:  # a tile's values share their factor
             big = p.amax(-1) * size.amax(0).repeat_interleave(n_q // cache.n_kv)[None]
         b_out[rows] += (1 + 2.0 ** -7) * length * 2.0 ** -33 * big[..., None]
-    within(out, want[0], b_out, "attention")
+    if hit is None:
+        within(out, want[0], b_out, "attention")
+    else:
+        assert not out.cpu()[hit].isfinite().any()
+        within(out.cpu()[~hit], want[0][~hit], b_out[~hit], "attention")
     assert torch.equal(lse.cpu() == -math.inf, want[1] == -math.inf)
     fin = want[1] > -math.inf
     within(lse.cpu()[fin], want[1][fin], b_lse[fin], "log-sum-exp")
@@ -149,6 +154,34 @@ def test_groups_apart_while_scores_climb(dev, n_new, kv_len, n_q, n_kv, dim, pag
                 c["vs"][c["table"][s, length // page].long(), :, length % page:] = math.nan
     refresh(c)
     attend(dev, c, q, n_new, scale)
+
+
+@pytest.mark.parametrize("part,what", [(0, math.nan), (0, math.inf), (1, math.inf), (1, math.nan)])
+@pytest.mark.parametrize("n_new,kv_len,n_q,n_kv,dim,page", [FORMS[4], FORMS[6], FORMS[7], *DEALT[:2], CHUNKS[0], *LONG[:3]])
+def test_a_group_that_is_not_finite_hides_no_other(dev, n_new, kv_len, n_q, n_kv, dim, page, part, what):  # noqa: F811
+    """A key that lies above those before it, with a group that is not finite and another that is larger than the rest:
+    all dims but the first group's are what they were."""
+    c = ref4.paged(n_new, kv_len, n_kv, dim, page, 8)
+    q = torch.randn(sum(n_new), n_q, dim, generator=gen(3)).to(torch.bfloat16)
+    q_off = [sum(n_new[:s]) for s in range(len(n_new) + 1)]
+    climb(c, q, q_off, dim ** -0.5, {200: 6.0, 850: 6.0})
+    given, hit = dict(c, vs=None), torch.zeros(q.shape, dtype=torch.bool)
+    bad = []
+    for s, length in enumerate(kv_len):
+        for h in range(n_kv):
+            for j in (200, 850):
+                if j < length - n_new[s]:
+                    group = (s + h + j // 200) % (dim // 32)
+                    pg, at = c["table"][s, j // page].long(), j % page
+                    c["vs"][pg, h, at, (group + 1) % (dim // 32)] *= 2.0 ** 7
+                    bad.append((pg, h, at, group))
+                    heads = slice(h * (n_q // n_kv), (h + 1) * (n_q // n_kv))
+                    hit[q_off[s]: q_off[s + 1], heads, 32 * group: 32 * group + 32] = True
+    refresh(c)
+    given["vs"] = c["vs"].clone()
+    for pg, h, at, group in bad:
+        given["vs"][pg, h, at, group, part] = what
+    attend(dev, c, q, n_new, dim ** -0.5, given=given, hit=hit)
 
 
 @pytest.mark.parametrize("sizes", range(len(SIZES)))
