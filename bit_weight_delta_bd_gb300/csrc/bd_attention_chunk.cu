@@ -26,9 +26,10 @@
 // Sequences of up to 256 rows would fill a pair's first query tile at most,
 // which takes as long as both: 8 sequences of 4 tokens over 4000 int8 keys take
 // 45 us by single CTAs and 68 by pairs.  With head_dim 64 half of V's dims
-// would leave 64-byte rows: single CTAs, 717 us for bf16 and 1122 for int8,
-// which by their number should be the exponentials' time (as many as with
-// head_dim 128, for half the products; no measurement sets them apart).
+// would leave 64-byte rows: single CTAs, 719 us for bf16 and 1122 for int8.
+// The softmax bounds bf16: as many scores as with head_dim 128 for half the
+// products, and without their maxima, factors, exponentials and sums it would
+// take 531; with a multiply-add in each exponential's place 657.
 //
 // The running maximum that P is formed with lags behind the true one by at
 // most 2^8 (a row's sums are rescaled in tensor memory only when its maximum
@@ -82,10 +83,12 @@
 // softmax goes through the scores once more (such a tile is not to let a large
 // one, which a causal row may not even see, flush the others).  Within a key or a
 // value, what lies 2^-27 below its largest element may lose bits.
-// A chunk of 4096 tokens over 8192 keys, 64/8 heads, takes 1066 us (bf16 of the
-// same values 765, int8 1112), 4096 over 8192 with heads of 64 975 (718, 1118).
-// What the conversion adds to a kernel that the softmax bounds: without it 1009
-// and 935.
+// A chunk of 4096 tokens over 8192 keys, 64/8 heads, takes 1063 us (bf16 of the
+// same values 765, int8 1112), 4096 over 8192 with heads of 64 972 (719, 1118).
+// What bounds it is the instructions of softmax and conversion together: without
+// the conversion 1009 and 935; without maxima, factors, exponentials and sums of
+// the scores 940 and 838.  The unit of the exponentials does not: with a
+// multiply-add in each one's place 1033 and 979.
 #include <cuda_fp16.h>
 
 #include <type_traits>

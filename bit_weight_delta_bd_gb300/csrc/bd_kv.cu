@@ -11,9 +11,11 @@
 // 4-bit codes.  Per (token, kv head, group of 32 elements): low = bf16(min x),
 // scale = bf16(max(max x - min x, 1e-30) / 15), code = round-half-even((x -
 // low) / scale) within 0 .. 15, formed in the same way.  The codes are found
-// for the rounded scale and lowest value, so that their 8 bits cost next to
-// nothing: the largest element lies within 15.06 steps, and the lowest is off
-// by no more than a bf16 cache would have it.
+// for the rounded scale and lowest value: an element is off by half a step, or
+// at the ends of the group by what the rounding of the two leaves past the first
+// or last step, up to 2^-8 of the group's range and of |low|.  Where |low| is 2^8
+// times the range and more (a group in 100.2 .. 100.3) that says more than the
+// codes do, and the group is held about as a bf16 cache would hold it.
 #include "bd_device.cuh"
 
 namespace bd {
