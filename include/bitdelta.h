@@ -487,7 +487,8 @@ bd_status bd_kv_read(const bd_kv_pages* cache, const int32_t* page_table, int64_
  * multiply the fp32 scores and probabilities.  4-bit codes of K enter exactly
  * too, with scales and lowest values in fp32 terms; in chunks, what lies 2^-27
  * and more below the largest element of its key (or value) may be lost.
- * Cached values up to 2^80 in magnitude give the formula's result; beyond that
+ * Cached values up to 2^80 in magnitude give the formula's result (over a 4-bit
+ * cache where scores, scale * q . k, are up to 2^20 in magnitude); beyond that
  * a product may overflow, and a result below 2^-125 may come out as 0.  Results do not depend on timing (no atomics).  A
  * page outside [0, n_pages), a length outside
  * [0, max_pages * page_size] or offsets out of order set BD_ERR_BAD_INDEX:

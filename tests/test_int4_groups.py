@@ -7,11 +7,13 @@ its turn: the pairs of sequence and kv head take them one after the other.
 Bounds, beside those of int4_oracle.py (roundings to 11 bits).  Few rows: a
 product of probability and scale is rounded to a multiple of 2^-24 where the
 row's largest product with a scale or lowest value is 2^11 or more: off by 2^-36
-of that at most, 15 times for the code.  Chunks: probabilities likewise, times
-values of up to 4 sizes; scales, lowest values and values over the size's power
-of two, times 2^13, are rounded to multiples of 2^-24, 17 / 2 of them off at most,
-2^-33.9 of the size.  Both are less than 2^-33 of the largest probability times
-the largest size, max(16 scale, |lowest value|), for each key."""
+of that at most, 15 times for the code, 15/16 2^-32.  Chunks: a probability is
+off by 2^-36 of the largest times its tile's power of two likewise, times values
+below 4 of those, and values over it times 2^13 by 15 roundings of the scale, one
+of the lowest value and one of the sum to multiples of 2^-24, 17 2^-38; together
+33 2^-38.  So each key adds 2^-32 at most of the largest probability times the
+largest size, max(16 scale, |lowest value|).
+"""
 import math
 
 import pytest
@@ -20,6 +22,7 @@ import torch
 import int4_oracle as ref4
 import test_int4_attention as att
 from bit_weight_delta_bd_gb300 import bitdelta as bd
+from layer_oracle import half_ulp_bf16
 from test_int4_attention import cache_on, dev, gen, within  # noqa: F401  (dev is a fixture)
 from test_int4_paths import SIZES
 
@@ -95,7 +98,7 @@ def attend(dev, c, q, n_new, scale, max_new=None, given=None, hit=None):  # noqa
         big = (p * size.T.repeat_interleave(n_q // cache.n_kv, 0)[None]).amax(-1)
         if not few:  # a tile's values share their factor
             big = p.amax(-1) * size.amax(0).repeat_interleave(n_q // cache.n_kv)[None]
-        b_out[rows] += (1 + 2.0 ** -7) * length * 2.0 ** -33 * big[..., None]
+        b_out[rows] += (1 + 2.0 ** -7) * length * 2.0 ** -32 * big[..., None]
     if hit is None:
         within(out, want[0], b_out, "attention")
     else:
@@ -220,3 +223,46 @@ def test_zeros_among_small_values(dev, n_new, kv_len, n_q, n_kv, dim, page, zero
             c["v"][pg[hit], :, off[hit]] = 0
     refresh(c)
     attend(dev, c, q, n_new, dim ** -0.5)
+
+
+# ------------------------------------------------------------------------------- large scores
+
+@pytest.mark.parametrize("score", [2.0 ** 20, -2.0 ** 20, 2.0 ** 19.7, -2.0 ** 17.3])
+@pytest.mark.parametrize("n_new,kv_len,n_q,n_kv,dim,page", [FORMS[0], FORMS[4], FORMS[7], *DEALT[:2], CHUNKS[0], *LONG])
+def test_scores_of_a_million(dev, n_new, kv_len, n_q, n_kv, dim, page, score):  # noqa: F811
+    """Keys that are all alike, with scores of up to 2^20 in magnitude: every row is the mean of the values that it sees,
+    whose groups differ in size.  (All keys have the same score, whatever its rounding.)"""
+    c = ref4.paged(n_new, kv_len, n_kv, dim, page, 5)
+    q = torch.zeros(sum(n_new), n_q, dim, dtype=torch.bfloat16)
+    byte, pair = ref4.codes(torch.randn(n_kv, dim, generator=gen(2)))
+    c["k"][:], c["ks"][:] = byte[None, :, None], pair[None, :, None]
+    key = ref4.values(byte, pair).repeat_interleave(n_q // n_kv, 0)
+    q[:] = (score * key / (0.25 * key.pow(2).sum(-1, keepdim=True))).to(torch.bfloat16)
+    for s, length in enumerate(kv_len):
+        pg = c["table"][s, : -(-length // page)].long()
+        f = 2.0 ** torch.randint(-8, 9, (n_kv, 1, dim // 32, 1), generator=gen(s)).float()
+        c["vs"][pg] = (c["vs"][pg].float() * f).to(torch.bfloat16)
+    refresh(c)
+    cache, table = cache_on(c, dev)
+    q_off = [sum(n_new[:s]) for s in range(len(n_new) + 1)]
+    out, lse = torch.empty(q.shape, device=dev, dtype=torch.bfloat16), torch.empty(q.shape[:2], device=dev)
+    ws = bd.new_workspace(bd.bd_attention_workspace_size(q.shape[0], len(kv_len), n_q, n_kv, dim), dev)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)  # noqa: E731
+    bd.bd_attention(q.to(dev), i32(q_off), cache, table, i32(kv_len), 0.25, max(n_new), out, ws, lse=lse)
+    assert bd.bd_check_async(ws) == bd.BD_OK
+    z = (q.double() * key[None]).sum(-1) * 0.25
+    zmag = (q.double().abs() * key.abs()[None]).sum(-1) * 0.25
+    for s, length in enumerate(kv_len):
+        at = torch.arange(length)
+        pair = c["vs"][c["table"][s].long()[at // page], :, at % page].double()
+        sizes = (15 * pair[..., 0].abs()).repeat_interleave(32, -1), pair[..., 1].abs().repeat_interleave(32, -1)
+        v = c["vals"]["v"][s].double()
+        seen = length - n_new[s] + 1 + torch.arange(n_new[s])
+        mean = [(x.cumsum(0)[seen - 1] / seen[:, None, None]).repeat_interleave(n_q // n_kv, 1) for x in (v, *sizes)]
+        rows = slice(q_off[s], q_off[s + 1])
+        # roundings of probabilities times scales, or of probabilities and values; fp32 sums; the largest size's 2^-32
+        bound = (mean[1] + mean[2]) * (2 * ref4.U11 + (length + 64) * 2.0 ** -21)
+        bound = bound + 2.0 ** -32 * torch.maximum(16 * pair[..., 0].abs(), pair[..., 1].abs()).max()
+        within(out[rows], mean[0], bound + half_ulp_bf16(mean[0].abs() + bound), "attention")
+        want = z[rows] + seen.log()[:, None]
+        within(lse[rows], want, zmag[rows] * (dim + 8) * 2.0 ** -22 + (length + 64) * 2.0 ** -22, "log-sum-exp")
