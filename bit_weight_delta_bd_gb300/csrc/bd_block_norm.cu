@@ -16,6 +16,7 @@
 #include <cuda_fp8.h>
 
 #include <atomic>
+#include <cmath>
 
 #include "bd_device.cuh"
 #include "bd_tma.h"
@@ -670,7 +671,10 @@ cudaError_t launch_block_norm(const BlockNormArgs& a, int sm_count, cudaStream_t
     };
     // Few rows: as many threads on a row as it has groups, for its latency.
     // Many: a warp for short rows, else two groups a thread.
-    const bool few = a.T <= 2 * sm_count;
+    // The ring's kernel has block_scale and the first norm's factor, 2^-64 .. 2^74, in one number: not where that may
+    // leave fp32's range (scales past 2^30 and 2^-30, far from those in use).
+    const float bs = fabsf(a.block_scale);
+    const bool few = a.T <= 2 * sm_count || (bs != 0.0f && (bs < 0x1p-30f || bs > 0x1p30f));
     if (!few && groups <= 32) return launch_ring<1, 32 * kRingWarps, true>(a, 32 * kRingWarps, sm_count, stream);
     if (!few && groups <= 64) return launch_ring<2, 32 * kRingWarps, true>(a, 32 * kRingWarps, sm_count, stream);
     if (!few && groups <= 128) return launch_ring<4, 32 * kRingWarps, true>(a, 32 * kRingWarps, sm_count, stream);

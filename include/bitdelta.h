@@ -337,6 +337,8 @@ bd_status bd_rms_norm(const uint16_t* x, const uint16_t* residual, int64_t T, in
  *   residual_out, out, out_dtype, scale, d, eps, V and ids out of range as in
  *                 bd_rms_norm; residual_out may be the residual's own buffer
  *                 (or x's)
+ * Sums of squares, and an element's products with its gate and gains in any
+ * order, have to lie in fp32's range (as normal numbers, to keep their bits).
  * Matrices, gains and gates 16-byte aligned; out may not overlap an input.
  * ------------------------------------------------------------------------ */
 size_t bd_block_norm_workspace_size(int64_t T, int64_t d);

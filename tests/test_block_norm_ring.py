@@ -140,6 +140,29 @@ def test_e4m3_of_tiny_rows(dev, T, d, small, gain_size, eps):  # noqa: F811
            half_step * (1 + 2.0 ** -10) + z * 3 * rel + (1 + z / 448) * step / s[:, None], "codes")
 
 
+@pytest.mark.parametrize("T,d", [(300, 1000), (700, 256), (700, 1000), (400, 8192), (400, 16384)])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("x_size,post_size,r_size,block_scale,residual_scale", [
+    (2.0 ** -58, 2.0 ** -22, 1.0, 2.0 ** 72, 2.0 ** 50),  # block_scale over x's root mean square is past fp32's range
+    (2.0 ** 50, 2.0 ** 30, 2.0 ** -20, -2.0 ** -85, 2.0 ** -35),  # and here below its normal numbers
+    (2.0 ** -58, 1.0, 1.0, 2.0 ** 40, 2.0 ** 40), (2.0 ** 50, 1.0, 1.0, 2.0 ** -50, 2.0 ** -50)])
+def test_block_scales_of_any_size(dev, T, d, gated, x_size, post_size, r_size, block_scale, residual_scale):  # noqa: F811
+    """Wherever the formula's own factors, and the squares that it sums, are in fp32's range, so is the result."""
+    g = gen(T + d)
+    x, r, post, gate = ((n * torch.randn(*m, generator=g)).to(torch.bfloat16)
+                        for n, m in ((x_size, (T, d)), (r_size, (T, d)), (post_size, (d,)), (1.0, (T, d))))
+    gain = (1 + 0.2 * torch.randn(d, generator=g)).to(torch.bfloat16)
+    out, ho = torch.empty(T, d, device=dev), torch.empty(T, d, device=dev, dtype=torch.bfloat16)
+    ws = bd.new_workspace(256, dev)
+    bd.bd_block_norm(x.to(dev), r.to(dev), gain.to(dev), 0.0, out, ws, residual_out=ho, post_gain=post.to(dev),
+                     gate=gate.to(dev) if gated else None, block_scale=block_scale, residual_scale=residual_scale)
+    assert bd.bd_check_async(ws) == bd.BD_OK
+    h, y, size = definition(x, r, post.expand(T, d), gate if gated else None, gain.expand(T, d), block_scale, residual_scale, 0.0)
+    dh, dy = tolerance(h, y, size, gain.expand(T, d), 0.0)
+    within(ho, h, dh + ref.half_ulp_bf16(h.abs() + dh), "residual")
+    within(out, y, dy, "norm")
+
+
 @pytest.mark.parametrize("T,d", SHAPES + [(33, 8192), (2, 40000)])
 def test_elements_as_rms_norm(dev, T, d):  # noqa: F811
     """Without gate, scales and norm after the block each element is bd_rms_norm's with a residual but for the order of
